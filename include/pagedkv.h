@@ -109,6 +109,9 @@ typedef enum pa_dtype {
                                    from the unit's, or whose block table differs from the
                                    unit's first member's over a shared partition */
 
+#define PA_DEV_BAD_POSITION 128u /* a position outside [0, max_position) of the rotation table
+                                   (the token is skipped) */
+
 /* Supported shapes: head_size in {64, 128, 256}; block_size in [1, 1024];
  * partition_size a positive multiple of 32 (512 on the pages). */
 
@@ -139,6 +142,56 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_cache
                                int head_size, int block_size, int64_t num_blocks,
                                pa_dtype in_dtype, pa_dtype cache_dtype, float k_scale,
                                float v_scale, uint32_t* dev_status, void* stream);
+
+/*
+ * pa_rope_and_cache -- the KV write with the position rotation, and optionally
+ * a norm of each query and key head, applied on the way. The pages start at
+ * rotated keys; this call takes the projection's output instead. For every
+ * token t and head row x of `query` and `key`:
+ *   norm      y = x * (mean(x^2) + eps)^(-1/2) * weight, the mean over the
+ *             head_size components, if q_weight (k_weight) is given; else y = x.
+ *   rotation  pair i < rotary_dim / 2 -- components (i, i + rotary_dim / 2), or
+ *             (2 i, 2 i + 1) with adjacent_pairs -- becomes
+ *             (a cos - b sin, b cos + a sin), with cos = cos_sin[pos][i],
+ *             sin = cos_sin[pos][rotary_dim / 2 + i], pos = positions[axis][t],
+ *             axis = freq_axes[i]. Components from rotary_dim on stay as they are.
+ * The query goes to query_out, the key to its slot of k_cache; the value goes
+ * to v_cache as pa_reshape_and_cache stores it. Norm and rotation are computed
+ * in float32 (the sum of squares included) and rounded once: to in_dtype, or
+ * to E4M3 as y / k_scale.
+ *
+ *  query_out      [num_tokens][num_q_heads][head_size], type in_dtype; may be
+ *                 `query` itself where that is contiguous.
+ *  query, key,
+ *  value          per token the [heads][head_size] rows, contiguous; tokens are
+ *                 query_stride, key_stride, value_stride elements apart (multiples
+ *                 of 16 bytes), so the three may be views of one projection output.
+ *  cos_sin        [max_position][rotary_dim] float32: rotary_dim / 2 cosines, then
+ *                 as many sines. rotary_dim: a multiple of 16 up to head_size.
+ *  positions      [num_axes][num_tokens] int64, 1 <= num_axes <= PA_MAX_ROPE_AXES.
+ *                 One outside [0, max_position) sets PA_DEV_BAD_POSITION; the
+ *                 token is skipped (query_out and the caches keep their contents).
+ *  freq_axes      HOST memory, rotary_dim / 2 entries below num_axes, read
+ *                 during the call; ignored (may be NULL) for one axis.
+ *  q_weight,
+ *  k_weight       [head_size] float32, or NULL: no norm. eps: finite, >= 0.
+ *  slot_mapping   as in pa_reshape_and_cache; a token with a negative slot (or
+ *                 one outside the pool, PA_DEV_BAD_SLOT) stores nothing, its query
+ *                 is still written.
+ * in_dtype F32, F16 or BF16; cache_dtype the same, or PA_FP8_E4M3. head_size
+ * 64, 128 or 256; block_size at most 1024. num_tokens == 0 launches nothing.
+ */
+#define PA_MAX_ROPE_AXES 4
+pa_status pa_rope_and_cache(void* query_out, const void* query, int64_t query_stride,
+                            const void* key, int64_t key_stride, const void* value,
+                            int64_t value_stride, void* k_cache, void* v_cache,
+                            const float* cos_sin, int64_t max_position, int rotary_dim,
+                            const int64_t* positions, int num_axes, const uint8_t* freq_axes,
+                            int adjacent_pairs, const float* q_weight, const float* k_weight,
+                            float eps, const int64_t* slot_mapping, int64_t num_tokens,
+                            int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                            int64_t num_blocks, pa_dtype in_dtype, pa_dtype cache_dtype,
+                            float k_scale, float v_scale, uint32_t* dev_status, void* stream);
 
 /*
  * pa_decode -- single-pass decode (PagedAttention "V1" on the pages: one
@@ -466,6 +519,77 @@ pa_status pa_paged_prefill(void* out, const void* query, const int32_t* query_st
                            int64_t num_blocks, int max_context_len, float scale,
                            pa_dtype q_dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
                            const int32_t* seq_order, uint32_t* dev_status, void* stream);
+
+/*
+ * Block-sparse decode. Over a long context most of the decode's reads are keys
+ * with negligible weight. pa_sparse_decode reads, for each (sequence, KV head),
+ * only num_select blocks of the context, chosen by an upper bound of their
+ * logits that is computed from a summary of each block's keys:
+ *     score(s, h, b) = max over the group's query heads g of
+ *                      sum_d max(q_gd lo_bd, q_gd hi_bd),
+ * where lo and hi are the minimum and maximum of component d over the block's
+ * keys (pa_key_bounds keeps them). The pages read whole contexts; this form is
+ * this library's.
+ *
+ * pa_key_bounds -- recompute the bounds of every cache block that holds one of
+ * its sequence's new tokens; call it after each KV write.
+ *  k_bounds       [num_blocks][num_kv_heads][2][head_size] (minimum, maximum),
+ *                 type bounds_dtype: the cache type, or F16 / BF16 (the query's
+ *                 type) for an E4M3 cache, in units of the codes (not scaled).
+ *                 Every element is exact. A NaN key gives NaN bounds.
+ *  new_tokens     [num_seqs] int32: the last new_tokens[s] positions below
+ *                 context_lens[s] are new, 0 <= new_tokens[s] <= max_new_tokens and
+ *                 <= context_lens[s] (else PA_DEV_BAD_LEN, and the sequence is
+ *                 skipped). NULL: one each (none where the context is empty), and
+ *                 max_new_tokens must be 1. max_new_tokens sizes the grid.
+ *  Bounds cover the block's tokens below context_lens[s]; bounds of other blocks
+ *  are left as they are. If several sequences' new tokens touch one physical
+ *  block, its bounds are those of one of them.
+ */
+pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* new_tokens, int max_new_tokens, int num_seqs,
+                        int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                        int max_context_len, pa_dtype cache_dtype, pa_dtype bounds_dtype,
+                        uint32_t* dev_status, void* stream);
+
+/*
+ * pa_sparse_decode -- select blocks, then decode over them. With n =
+ * ceil(L / block_size) blocks in a context: n <= num_select takes all of them
+ * (the plain decode); otherwise blocks 0 .. first_blocks - 1, the newest
+ * recent_blocks, and of the others the num_select - first_blocks -
+ * recent_blocks of largest score, ties to the lowest index. The order is that
+ * of the scores computed exactly (in binary64), so it does not depend on how
+ * the work is split; a NaN score counts as +infinity. The output is
+ * softmax(scale * q K^T) V over the selected blocks' tokens below L.
+ *
+ *  k_bounds       [num_blocks][num_kv_heads][2][head_size], of the query's type;
+ *                 read only for blocks that are scored (never for the newest
+ *                 recent_blocks, nor where a context fits num_select blocks).
+ *  num_select     blocks per (sequence, KV head), >= first_blocks + recent_blocks;
+ *                 first_blocks >= 0, recent_blocks >= 1. scale must be > 0.
+ *  selected       NULL, or [num_seqs][num_kv_heads][num_select] int32: the logical
+ *                 blocks taken, ascending, padded with -1.
+ *  workspace      256-byte aligned, pa_sparse_decode_workspace_bytes(...) bytes
+ *                 (0 for invalid sizes); nothing in it outlives the call's kernels.
+ *                 Calls that overlap on the GPU need workspaces of their own.
+ * Several query tokens of one sequence (draft tokens, a chunk) go as that many
+ * rows: each with the sequence's table and the length it sees, so that each
+ * query selects its own blocks. Other arguments, shapes, types and device
+ * checks as pa_decode; num_blocks * num_kv_heads must be below 2^31.
+ */
+size_t pa_sparse_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_size, int block_size, int max_context_len,
+                                        int num_select);
+pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, const void* v_cache,
+                           const void* k_bounds, const int32_t* block_tables,
+                           int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                           int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                           int64_t num_blocks, int max_context_len, float scale, int num_select,
+                           int first_blocks, int recent_blocks, int32_t* selected,
+                           pa_dtype q_dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
+                           void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                           void* stream);
 
 /* ------------------------------------------------------------------------
  * Block management: the host-side allocator and the copy-on-write copy.

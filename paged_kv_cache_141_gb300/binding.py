@@ -33,6 +33,7 @@ PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = range(4)
 DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT, DEV_SLOT_MISMATCH = 1, 2, 4, 8, 16
 DEV_BAD_ORDER = 32
 DEV_BAD_PREFIX = 64
+DEV_BAD_POSITION = 128
 
 DEFAULT_PARTITION_SIZE = 512
 
@@ -91,6 +92,14 @@ def lib() -> ctypes.CDLL:
                                        I, F, F, P, P, P]
         L.pa_paged_prefill_kernel.argtypes = [I, I, I, I, I, I64, I, I]
         L.pa_paged_prefill_kernel.restype = I
+        L.pa_rope_and_cache.argtypes = [P, P, I64, P, I64, P, I64, P, P, P, I64, I, P, I,
+                                        ctypes.c_char_p, I, P, P, F, P, I64, I, I, I, I, I64, I, I,
+                                        F, F, P, P]
+        L.pa_key_bounds.argtypes = [P, P, P, I, P, P, I, I, I, I, I, I64, I, I, I, P, P]
+        L.pa_sparse_decode_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+        L.pa_sparse_decode_workspace_bytes.restype = S
+        L.pa_sparse_decode.argtypes = [P, P, P, P, P, P, I, P, I, I, I, I, I, I64, I, F, I, I, I, P,
+                                       I, I, F, F, P, S, P, P]
         L.pa_copy_blocks.argtypes = [P, P, P, I64, I, I, I, I64, I, P, P]
         L.pa_selftest_wait.argtypes = [I, P, P]
         L.pa_allocator_create.argtypes = [I64, I, I]
@@ -124,6 +133,7 @@ def lib() -> ctypes.CDLL:
                      "pa_write_decode_partitioned", "pa_write_decode_partitions",
                      "pa_decode_choose", "pa_decode_partition_size", "pa_version",
                      "pa_shared_prefix_plan", "pa_write_decode_shared_prefix",
+                     "pa_rope_and_cache", "pa_key_bounds", "pa_sparse_decode",
                      "pa_copy_blocks", "pa_selftest_wait", "pa_allocator_allocate", "pa_allocator_fork",
                      "pa_allocator_free", "pa_allocator_append_slot"):
             getattr(L, name).restype = ctypes.c_int
@@ -450,6 +460,157 @@ def write_decode_shared_prefix(out, query, k_cache, v_cache, block_tables, conte
         int(unit_parts.numel()), int(max_unit_parts), partition_size, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)),
         "pa_write_decode_shared_prefix")
+
+
+# ------------------------------------------------- append with rotation, block-sparse decode
+
+MAX_ROPE_AXES = 4
+
+
+def _on_device(stream, first, *others):
+    """The stream for a call whose tensors must share one device: the given
+    one, or that device's current stream (whichever device is current)."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must live on one device")
+    if stream is None:
+        return torch.cuda.current_stream(first.device).cuda_stream
+    return _stream(stream)
+
+
+def _token_rows(t, heads, head_size, what):
+    """Pointer and token stride of [T, heads, head_size] rows whose last two
+    dimensions are contiguous (a view of a wider projection output is fine)."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
+        raise ValueError(f"{what} must be [num_tokens, {heads}, {head_size}]")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_size):
+        raise ValueError(f"{what}: each token's [heads, head_size] rows must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_size
+
+
+def rope_sections(sections) -> bytes:
+    """freq_axes of consecutive sections: sections[a] frequencies follow axis a."""
+    return bytes(a for a, n in enumerate(sections) for _ in range(n))
+
+
+def rope_and_cache(query_out, query, key, value, k_cache, v_cache, cos_sin, positions,
+                   slot_mapping, q_weight=None, k_weight=None, eps=1e-6, freq_axes=None,
+                   adjacent_pairs=False, k_scale=1.0, v_scale=1.0, dev_status=None,
+                   stream=None) -> None:
+    """The KV write with norms and position rotation on the way: query
+    [T, Hq, d] goes (normed by q_weight, rotated) to query_out, key [T, Hkv, d]
+    (normed by k_weight, rotated) and value to the caches at slot_mapping.
+    cos_sin: float32 [max_position, rotary_dim], cosines then sines.
+    positions: int64 [T], or [axes, T] with freq_axes naming the axis of each of
+    the rotary_dim / 2 frequencies (see rope_sections). q_weight, k_weight:
+    float32 [d] or None (no norm). adjacent_pairs: rotate components (2i, 2i+1)
+    instead of (i, i + rotary_dim / 2). query, key and value may be views with
+    any token stride; query_out may be query."""
+    T, Hq, D = query.shape
+    nb, Hkv, B, D2 = k_cache.shape
+    if v_cache.shape != k_cache.shape or D2 != D:
+        raise ValueError("inconsistent query/cache shapes")
+    if key.dtype != query.dtype or value.dtype != query.dtype or query_out.dtype != query.dtype:
+        raise ValueError("query, key, value and query_out must share one dtype")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must share one dtype")
+    if query_out.shape != query.shape or key.shape[0] != T or value.shape[0] != T:
+        raise ValueError("query_out, key and value must have the query's tokens")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dtype != torch.int64 or positions.dim() > 2 or positions.shape[-1] != T or axes < 1:
+        raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.numel() != D):
+            raise ValueError("norm weights must be float32 [head_size]")
+    fa = None
+    if axes > 1:
+        if freq_axes is None or len(freq_axes) != cos_sin.shape[1] // 2:
+            raise ValueError("several axes need freq_axes, one axis for each of rotary_dim / 2 frequencies")
+        fa = bytes(freq_axes)
+    q, qs = _token_rows(query, Hq, D, "query")
+    k, ks = _token_rows(key, Hkv, D, "key")
+    v, vs = _token_rows(value, Hkv, D, "value")
+    st = _on_device(stream, query, query_out, key, value, k_cache, v_cache, cos_sin, positions,
+                    slot_mapping, q_weight, k_weight, dev_status)
+    with torch.cuda.device(query.device):
+        status = lib().pa_rope_and_cache(
+            _ptr(query_out), q, qs, k, ks, v, vs, _ptr(k_cache), _ptr(v_cache), _ptr(cos_sin),
+            cos_sin.shape[0], cos_sin.shape[1], _ptr(positions), axes, fa, int(bool(adjacent_pairs)),
+            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(slot_mapping), T, Hq, Hkv, D, B, nb,
+            _dtype(query), _dtype(k_cache), float(k_scale), float(v_scale), _ptr(dev_status), st)
+    _check(status, "pa_rope_and_cache")
+
+
+def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, new_tokens=None,
+               max_new_tokens=1, dev_status=None, stream=None) -> None:
+    """Recompute k_bounds [num_blocks, Hkv, 2, d] (minimum, maximum of each
+    block's keys) for the blocks that hold the last new_tokens[s] (int32 [S];
+    None: one) positions of each context."""
+    nb, Hkv, B, D = k_cache.shape
+    S = context_lens.numel()
+    if k_bounds.shape != (nb, Hkv, 2, D):
+        raise ValueError("k_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    if new_tokens is not None and (new_tokens.dtype != torch.int32 or new_tokens.numel() != S):
+        raise ValueError("new_tokens must be int32 [num_seqs]")
+    st = _on_device(stream, k_cache, k_bounds, block_tables, context_lens, new_tokens, dev_status)
+    with torch.cuda.device(k_cache.device):
+        status = lib().pa_key_bounds(
+            _ptr(k_bounds), _ptr(k_cache), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), _ptr(new_tokens), int(max_new_tokens), S, Hkv, D, B, nb,
+            int(max_context_len), _dtype(k_cache), _dtype(k_bounds), _ptr(dev_status), st)
+    _check(status, "pa_key_bounds")
+
+
+def sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                           max_context_len, num_select) -> int:
+    return int(lib().pa_sparse_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                      head_size, block_size,
+                                                      int(max_context_len), int(num_select)))
+
+
+def alloc_sparse_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                           max_context_len, num_select, device=None) -> torch.Tensor:
+    n = sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                               max_context_len, num_select)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def sparse_decode(out, query, k_cache, v_cache, k_bounds, block_tables, context_lens,
+                  max_context_len, scale, num_select, workspace, first_blocks=1, recent_blocks=1,
+                  selected=None, k_scale=1.0, v_scale=1.0, dev_status=None, stream=None) -> None:
+    """Decode over num_select blocks of each context per KV head: the first
+    first_blocks, the newest recent_blocks and those whose k_bounds allow the
+    largest logits. selected (int32 [S, Hkv, num_select], optional) receives
+    the logical blocks taken, ascending, -1 padded."""
+    S, Hq, D, nb, Hkv, B, mb = _decode_dims(query, k_cache, block_tables, context_lens)
+    if out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("out must have the query's shape and dtype")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    if k_bounds.shape != (nb, Hkv, 2, D) or k_bounds.dtype != query.dtype:
+        raise ValueError("k_bounds must be [num_blocks, num_kv_heads, 2, head_size] of the query's dtype")
+    if selected is not None and (selected.dtype != torch.int32 or selected.shape != (S, Hkv, num_select)):
+        raise ValueError("selected must be int32 [num_seqs, num_kv_heads, num_select]")
+    st = _on_device(stream, query, out, k_cache, v_cache, k_bounds, block_tables, context_lens,
+                    selected, workspace, dev_status)
+    with torch.cuda.device(query.device):
+        status = lib().pa_sparse_decode(
+            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_bounds),
+            _ptr(block_tables), mb, _ptr(context_lens), S, Hq, Hkv, D, B, nb, int(max_context_len),
+            float(scale), int(num_select), int(first_blocks), int(recent_blocks), _ptr(selected),
+            _dtype(query), _dtype(k_cache), float(k_scale), float(v_scale), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(dev_status), st)
+    _check(status, "pa_sparse_decode")
 
 
 STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024

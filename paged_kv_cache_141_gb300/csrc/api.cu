@@ -324,6 +324,71 @@ long long decode_len_cap(int max_context_len, int max_blocks_per_seq, int block_
     return tab < max_context_len ? tab : (long long)max_context_len;
 }
 
+// --- the block-sparse decode: its rows are one-head sequences over slabs
+
+struct SparsePlan {
+    int max_ctx_blocks;           // blocks of the longest context
+    int table_width;              // slabs per row at most
+    int max_tokens;               // tokens per row at most
+    int chunk_seqs;               // sequences per decode launch (its grid holds 65535 rows)
+    int partition_size;
+    bool split;
+    size_t scores, slab_tables, slab_lens, partials, total;   // workspace offsets
+};
+
+// Partitions of the selected tokens: 512, halved (down to 128) while the
+// launch has fewer than two waves of work units at three CTAs per SM, as few
+// rows leave SMs idle; one pass where a row is one partition or the rows alone
+// fill eight waves (the rule of pa_decode_choose). 152 SMs, not the device's
+// count: the workspace must not depend on the current device.
+SparsePlan sparse_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
+                       int block_size, int max_context_len, int num_select) {
+    SparsePlan l;
+    l.max_ctx_blocks = (max_context_len + block_size - 1) / block_size;
+    l.table_width = num_select < l.max_ctx_blocks ? num_select : l.max_ctx_blocks;
+    if (l.table_width < 1) l.table_width = 1;
+    const long long tokens = (long long)l.table_width * block_size;
+    l.max_tokens = tokens < max_context_len ? (int)tokens : max_context_len;
+    const long long rows = (long long)num_seqs * num_kv_heads;
+    l.chunk_seqs = 65535 / num_kv_heads;
+    if (l.chunk_seqs < 1) l.chunk_seqs = 1;
+    if (num_seqs < l.chunk_seqs) l.chunk_seqs = num_seqs;
+    const long long slots = 3 * 152;
+    l.partition_size = 512;
+    while (l.partition_size > 128 &&
+           rows * max_partitions(l.max_tokens, l.partition_size) < 2 * slots)
+        l.partition_size /= 2;
+    const int parts = max_partitions(l.max_tokens, l.partition_size);
+    l.split = parts > 1 && !(rows >= 8 * slots && parts <= 2);
+    l.scores = 0;
+    l.slab_tables = align256((size_t)rows * l.max_ctx_blocks * sizeof(double));
+    l.slab_lens = l.slab_tables + align256((size_t)rows * l.table_width * sizeof(int32_t));
+    l.partials = l.slab_lens + align256((size_t)rows * sizeof(int32_t));
+    // Partials for any smaller batch or context too (whose partitions may be
+    // shorter), so that a workspace made for the largest serves them all: a
+    // halved partition size means fewer than 2 slots partitions before, so at
+    // most 4 slots after.
+    const long long lrows = (long long)l.chunk_seqs * num_kv_heads;
+    const long long most = lrows * max_partitions(l.max_tokens, 128);
+    long long parts_total = lrows * max_partitions(l.max_tokens, 512);
+    const long long halved = most < 4 * slots ? most : 4 * slots;
+    if (parts_total < halved) parts_total = halved;
+    parts_total *= num_q_heads / num_kv_heads;
+    l.total = l.partials + align256((size_t)parts_total * head_size * sizeof(float)) +
+              2 * align256((size_t)parts_total * sizeof(float));
+    return l;
+}
+
+bool sparse_sizes_ok(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
+                     int block_size, int max_context_len, int num_select) {
+    return num_seqs >= 0 && num_q_heads > 0 && num_kv_heads > 0 &&
+           num_q_heads % num_kv_heads == 0 && head_size > 0 && block_size > 0 &&
+           max_context_len >= 0 && num_select > 0;
+}
+
+// Lengths round up to whole blocks in 32-bit arithmetic.
+constexpr int kMaxSparseContext = 0x7fffffff - 1024;
+
 }  // namespace
 
 extern "C" {
@@ -727,6 +792,215 @@ int pa_paged_prefill_kernel(int max_queries_per_seq, int num_q_heads, int num_kv
         return -1;
     return prefill_kernel(q_dtype, cache_dtype, head_size, block_size, num_q_heads / num_kv_heads,
                           num_blocks, num_kv_heads, max_queries_per_seq, true);
+}
+
+pa_status pa_rope_and_cache(void* query_out, const void* query, int64_t query_stride,
+                            const void* key, int64_t key_stride, const void* value,
+                            int64_t value_stride, void* k_cache, void* v_cache,
+                            const float* cos_sin, int64_t max_position, int rotary_dim,
+                            const int64_t* positions, int num_axes, const uint8_t* freq_axes,
+                            int adjacent_pairs, const float* q_weight, const float* k_weight,
+                            float eps, const int64_t* slot_mapping, int64_t num_tokens,
+                            int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                            int64_t num_blocks, pa_dtype in_dtype, pa_dtype cache_dtype,
+                            float k_scale, float v_scale, uint32_t* dev_status, void* stream) {
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+        block_size <= 0 || num_blocks < 0 || max_position < 0 || rotary_dim <= 0 ||
+        rotary_dim > head_size || num_axes < 1 || (adjacent_pairs != 0 && adjacent_pairs != 1))
+        return PA_ERR_INVALID_ARG;
+    if ((int)in_dtype < 0 || (int)in_dtype > 3 || (int)cache_dtype < 0 || (int)cache_dtype > 3)
+        return PA_ERR_INVALID_ARG;
+    if (!is_compute_type(in_dtype)) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype != in_dtype && cache_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (cache_dtype == PA_FP8_E4M3 &&
+        (!isfinite(k_scale) || !isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f))
+        return PA_ERR_INVALID_ARG;
+    if ((q_weight || k_weight) && !(isfinite(eps) && eps >= 0.f)) return PA_ERR_INVALID_ARG;
+    if (!supported_head_size(head_size) || block_size > 1024 || rotary_dim % 16 != 0 ||
+        num_axes > PA_MAX_ROPE_AXES || num_q_heads > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    RopeParams p{};
+    if (num_axes > 1) {
+        if (!freq_axes) return PA_ERR_INVALID_ARG;
+        for (int i = 0; i < rotary_dim / 2; ++i) {
+            if (freq_axes[i] >= num_axes) return PA_ERR_INVALID_ARG;
+            p.freq_axes[i / 16] |= (uint32_t)freq_axes[i] << (2 * (i % 16));
+        }
+    }
+    // rows move as 16-byte vectors: every token's row must start on one
+    const int per16 = 16 / elem_bytes(in_dtype);
+    if (query_stride % per16 != 0 || key_stride % per16 != 0 || value_stride % per16 != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!query_out || !query || !key || !value || !k_cache || !v_cache || !cos_sin || !positions ||
+        !slot_mapping)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(query_out, query, key, value) || !aligned16(k_cache, v_cache, cos_sin) ||
+        !aligned16(q_weight, k_weight) || !aligned(positions, 8) || !aligned(slot_mapping, 8))
+        return PA_ERR_INVALID_ARG;
+    p.query_out = query_out;
+    p.query = query;
+    p.key = key;
+    p.value = value;
+    p.query_stride = query_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.cos_sin = cos_sin;
+    p.positions = positions;
+    p.slots = slot_mapping;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.status = dev_status;
+    p.total_tokens = num_tokens;
+    p.max_position = max_position;
+    p.num_blocks = num_blocks;
+    p.num_axes = num_axes;
+    p.rotary_dim = rotary_dim;
+    p.adjacent_pairs = adjacent_pairs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.eps = eps;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    return from_cuda(launch_rope_and_cache(p, head_size, in_dtype, cache_dtype,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* new_tokens, int max_new_tokens, int num_seqs,
+                        int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                        int max_context_len, pa_dtype cache_dtype, pa_dtype bounds_dtype,
+                        uint32_t* dev_status, void* stream) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0 ||
+        max_blocks_per_seq < 0 || max_context_len < 0 || max_new_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!new_tokens && max_new_tokens != 1) return PA_ERR_INVALID_ARG;
+    if ((int)cache_dtype < 0 || (int)cache_dtype > 3 || (int)bounds_dtype < 0 || (int)bounds_dtype > 3)
+        return PA_ERR_INVALID_ARG;
+    if (!supported_pair(bounds_dtype, cache_dtype) || !supported_head_size(head_size) ||
+        block_size > 1024 || max_context_len > kMaxSparseContext)
+        return PA_ERR_UNSUPPORTED;
+    if (max_new_tokens > max_context_len) max_new_tokens = max_context_len;
+    const int64_t touched = max_new_tokens == 0 ? 0 : ((int64_t)max_new_tokens + block_size - 2) / block_size + 1;
+    if ((int64_t)num_seqs * num_kv_heads > (1ll << 32) / (touched + 1)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || touched == 0) return PA_OK;
+    if (!k_bounds || !k_cache || !block_tables || !context_lens || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_bounds, k_cache) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(new_tokens, 4))
+        return PA_ERR_INVALID_ARG;
+    BoundsParams p{};
+    p.k_bounds = k_bounds;
+    p.k_cache = k_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.new_tokens = new_tokens;
+    p.status = dev_status;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.max_context_len = max_context_len;
+    p.max_new_tokens = max_new_tokens;
+    p.touched = (int)touched;
+    return from_cuda(launch_key_bounds(p, head_size, cache_dtype, bounds_dtype,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_sparse_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                        int head_size, int block_size, int max_context_len,
+                                        int num_select) {
+    if (!sparse_sizes_ok(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                         max_context_len, num_select) ||
+        block_size > 1024 || max_context_len > kMaxSparseContext || num_seqs > 65535 ||
+        num_kv_heads > 65535)
+        return 0;
+    return sparse_plan(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                       max_context_len, num_select).total;
+}
+
+pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, const void* v_cache,
+                           const void* k_bounds, const int32_t* block_tables,
+                           int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                           int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                           int64_t num_blocks, int max_context_len, float scale, int num_select,
+                           int first_blocks, int recent_blocks, int32_t* selected,
+                           pa_dtype q_dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
+                           void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                           void* stream) {
+    DecodeParams p;
+    pa_status st = check_decode(query, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                context_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                block_size, num_blocks, max_context_len, scale, q_dtype,
+                                cache_dtype, k_scale, v_scale, dev_status, p);
+    if (st != PA_OK) return st;
+    if (!(scale > 0.f) || num_select < 1 || first_blocks < 0 || recent_blocks < 1 ||
+        first_blocks > num_select || recent_blocks > num_select - first_blocks)
+        return PA_ERR_INVALID_ARG;
+    // slab ids are 32-bit, and rows index a one-dimensional grid
+    if (max_context_len > kMaxSparseContext || num_blocks > 0x7fffffffll / num_kv_heads ||
+        (long long)num_seqs * num_kv_heads > 0x7fffffffll)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !k_bounds || !aligned16(out, k_bounds) || !aligned(selected, 4))
+        return PA_ERR_INVALID_ARG;
+    const SparsePlan l = sparse_plan(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                                     max_context_len, num_select);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total) return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    SelectParams sp{};
+    sp.query = query;
+    sp.k_bounds = k_bounds;
+    sp.block_tables = block_tables;
+    sp.context_lens = context_lens;
+    sp.scores = reinterpret_cast<double*>(w + l.scores);
+    sp.slab_tables = reinterpret_cast<int32_t*>(w + l.slab_tables);
+    sp.slab_lens = reinterpret_cast<int32_t*>(w + l.slab_lens);
+    sp.selected = selected;
+    sp.status = dev_status;
+    sp.num_blocks = num_blocks;
+    sp.max_blocks = max_blocks_per_seq;
+    sp.num_seqs = num_seqs;
+    sp.num_q_heads = num_q_heads;
+    sp.num_kv_heads = num_kv_heads;
+    sp.group = p.group;
+    sp.block_size = block_size;
+    sp.max_context_len = max_context_len;
+    sp.max_ctx_blocks = l.max_ctx_blocks;
+    sp.table_width = l.table_width;
+    sp.num_select = num_select;
+    sp.first_blocks = first_blocks;
+    sp.recent_blocks = recent_blocks;
+    const cudaError_t e = launch_select_blocks(sp, head_size, q_dtype, cs);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    const size_t seq_bytes = (size_t)num_q_heads * head_size * elem_bytes(q_dtype);
+    for (int s0 = 0; s0 < num_seqs; s0 += l.chunk_seqs) {
+        const int rows = (num_seqs - s0 < l.chunk_seqs ? num_seqs - s0 : l.chunk_seqs) * num_kv_heads;
+        const size_t row0 = (size_t)s0 * num_kv_heads;
+        const void* q = static_cast<const uint8_t*>(query) + s0 * seq_bytes;
+        void* o = static_cast<uint8_t*>(out) + s0 * seq_bytes;
+        const int32_t* tables = sp.slab_tables + row0 * l.table_width;
+        if (l.split)
+            st = pa_decode_partitioned(o, q, k_cache, v_cache, tables, l.table_width,
+                                       sp.slab_lens + row0, rows, p.group, 1, head_size, block_size,
+                                       num_blocks * num_kv_heads, l.max_tokens, scale, q_dtype,
+                                       cache_dtype, k_scale, v_scale, l.partition_size,
+                                       w + l.partials, workspace_bytes - l.partials, dev_status,
+                                       stream);
+        else
+            st = pa_decode(o, q, k_cache, v_cache, tables, l.table_width, sp.slab_lens + row0, rows,
+                           p.group, 1, head_size, block_size, num_blocks * num_kv_heads,
+                           l.max_tokens, scale, q_dtype, cache_dtype, k_scale, v_scale, dev_status,
+                           stream);
+        if (st != PA_OK) return st;
+    }
+    return PA_OK;
 }
 
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_pairs,

@@ -142,6 +142,96 @@ cudaError_t launch_prefill_tc_bf16(const PrefillParams& p, int head_size, cudaSt
 cudaError_t launch_prefill_tc_f16_e4m3(const PrefillParams& p, int head_size, cudaStream_t stream);
 cudaError_t launch_prefill_tc_bf16_e4m3(const PrefillParams& p, int head_size, cudaStream_t stream);
 
+// The KV append with norms and rotation (rope_and_cache.cu).
+struct RopeParams {
+    void* query_out;              // [T, Hq, D]
+    const void* query;            // rows of Hq * D elements, query_stride apart
+    const void* key;
+    const void* value;
+    int64_t query_stride;         // elements between tokens
+    int64_t key_stride;
+    int64_t value_stride;
+    void* k_cache;                // [num_blocks, Hkv, B, D]
+    void* v_cache;
+    const float* cos_sin;         // [max_position, rotary_dim]: cosines, then sines
+    const int64_t* positions;     // [num_axes, T]
+    const int64_t* slots;         // [T]
+    const float* q_weight;        // [D] or null
+    const float* k_weight;
+    uint32_t* status;             // may be null
+    int64_t total_tokens;         // T
+    int64_t first_token;          // of this launch
+    int64_t max_position;
+    int64_t num_blocks;
+    int num_tokens;               // of this launch
+    int num_axes;                 // 1..4
+    int rotary_dim;
+    int adjacent_pairs;           // pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
+    int num_q_heads;
+    int num_kv_heads;
+    int block_size;
+    int groups;                   // row groups per token
+    float eps;
+    float k_scale;
+    float v_scale;
+    uint32_t freq_axes[8];        // two bits per frequency
+};
+
+cudaError_t launch_rope_and_cache(const RopeParams& p, int head_size, pa_dtype in_dtype,
+                                  pa_dtype cache_dtype, cudaStream_t stream);
+
+// Per-block key bounds (key_bounds.cu).
+struct BoundsParams {
+    void* k_bounds;               // [num_blocks, Hkv, 2, D]: minimum, maximum
+    const void* k_cache;          // [num_blocks, Hkv, B, D]
+    const int32_t* block_tables;  // [S, max_blocks]
+    const int32_t* context_lens;  // [S]
+    const int32_t* new_tokens;    // [S], or null: one each
+    uint32_t* status;             // may be null
+    int64_t num_blocks;
+    int max_blocks;
+    int num_seqs;
+    int num_kv_heads;
+    int block_size;
+    int max_context_len;
+    int max_new_tokens;
+    int touched;                  // blocks that max_new_tokens tokens can touch
+};
+
+cudaError_t launch_key_bounds(const BoundsParams& p, int head_size, pa_dtype cache_dtype,
+                              pa_dtype bounds_dtype, cudaStream_t stream);
+
+// Block scores and selection of the block-sparse decode (sparse_select.cu).
+// A slab is one (block, KV head) pair of the cache, block * Hkv + head; the
+// selection of (sequence s, KV head h) is row s * Hkv + h of slab_tables.
+struct SelectParams {
+    const void* query;            // [S, Hq, D]
+    const void* k_bounds;         // [num_blocks, Hkv, 2, D], the query's type
+    const int32_t* block_tables;  // [S, max_blocks]
+    const int32_t* context_lens;  // [S]
+    double* scores;               // [S * Hkv, max_ctx_blocks]
+    int32_t* slab_tables;         // [S * Hkv, table_width]
+    int32_t* slab_lens;           // [S * Hkv] tokens of the selection
+    int32_t* selected;            // [S, Hkv, num_select] logical blocks, -1 padded; may be null
+    uint32_t* status;             // may be null
+    int64_t num_blocks;
+    int max_blocks;
+    int num_seqs;
+    int num_q_heads;
+    int num_kv_heads;
+    int group;
+    int block_size;
+    int max_context_len;
+    int max_ctx_blocks;           // ceil(max_context_len / block_size)
+    int table_width;              // min(num_select, max_ctx_blocks)
+    int num_select;
+    int first_blocks;
+    int recent_blocks;
+};
+
+cudaError_t launch_select_blocks(const SelectParams& p, int head_size, pa_dtype q_dtype,
+                                 cudaStream_t stream);
+
 // len_cap: context lengths above it are clamped to it (and flagged
 // PA_DEV_BAD_LEN), the clamp the partition kernel applied, so that only
 // partitions it wrote are merged.

@@ -1,0 +1,379 @@
+"""key_bounds and sparse_decode on the GPU against plain forms in 64 bits.
+
+Bounds and selections are compared for equality. The output's tolerance,
+derived: the decode rounds it once (half a step of its type, relative); its
+softmax weights carry ex2.approx's 2^-22, the binary32 sums and scores (about
+2^-17 relative here: |scale q k| stays below 2^5 and is accumulated over at
+most 256 products) and their cut to 16-bit terms (2^-16 for two terms of a
+16-bit cache, 2^-11 for the one binary16 term of an E4M3 cache), each against
+sum_i p_i |v_i|, twice (numerator and sum): 2^-13 and 2^-9 of that sum, and
+2^-15 for binary32, cover them.
+"""
+import pytest
+import torch
+
+from paged_kv_cache_141_gb300 import binding as pk
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+WEIGHTS = {"f32": 2.0 ** -15, "f16": 2.0 ** -13, "bf16": 2.0 ** -13, "e4m3": 2.0 ** -9}
+
+
+class Pool:
+    def __init__(self, lens, Hq=8, Hkv=2, D=128, B=16, dtype="bf16", e4m3=False, seed=0, max_blocks=None):
+        g = torch.Generator().manual_seed(seed)
+        self.S, self.Hq, self.Hkv, self.D, self.B, self.e4m3, self.dtype = len(lens), Hq, Hkv, D, B, e4m3, dtype
+        self.dt = TYPES[dtype]
+        n = [-(-L // B) for L in lens]
+        self.max_blocks = max_blocks or max(1, max(n))
+        self.num_blocks = sum(n) + 3
+        perm = torch.randperm(self.num_blocks - 1, generator=g) + 1          # block 0: NaN, in the padding
+        self.tables = torch.zeros((self.S, self.max_blocks), dtype=torch.int32)
+        at = 0
+        for s, k in enumerate(n):
+            self.tables[s, :k] = perm[at:at + k].int()
+            at += k
+        self.lens, self.max_len = lens, max(lens)
+        shape = (self.num_blocks, Hkv, B, D)
+        caches = []
+        for _ in range(2):
+            x = torch.randn(shape, generator=g) * (1 + (torch.rand(D, generator=g) < 0.1).float())
+            x = (x * 40).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else x.to(self.dt)
+            nan = 0x7F if e4m3 else float("nan")
+            x[0] = nan
+            for s, L in enumerate(lens):
+                if L % B:
+                    x[self.tables[s, L // B], :, L % B:] = nan
+            caches.append(x.cuda())
+        self.kc, self.vc = caches
+        self.ks, self.vs = (0.021, 0.027) if e4m3 else (1.0, 1.0)
+        self.query = torch.randn((self.S, Hq, D), generator=g).to(self.dt).cuda()
+        self.tables = self.tables.cuda()
+        self.context = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.bounds = torch.full((self.num_blocks, Hkv, 2, D), float("nan"), dtype=self.dt, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.scale = D ** -0.5
+
+    def keys(self, cache):
+        return (cache.view(torch.float8_e4m3fn) if self.e4m3 else cache).double()
+
+    def want_bounds(self, s, j):
+        """Bounds of logical block j of sequence s: [Hkv, 2, D]."""
+        k = self.keys(self.kc[self.tables[s, j]])[:, :min(self.B, self.lens[s] - j * self.B)]
+        return torch.stack((k.amin(1), k.amax(1)), 1)
+
+    def fill_bounds(self):
+        pk.key_bounds(self.bounds, self.kc, self.tables, self.context, self.max_len, new_tokens=self.context,
+                      max_new_tokens=self.max_len, dev_status=self.status)
+
+    def decode(self, K, first=1, recent=1, ws=None, **kw):
+        out = torch.full_like(self.query, 7.5)
+        sel = torch.full((self.S, self.Hkv, K), 99, dtype=torch.int32, device="cuda")
+        ws = ws if ws is not None else pk.alloc_sparse_workspace(self.S, self.Hq, self.Hkv, self.D, self.B,
+                                                                 self.max_len, K)
+        pk.sparse_decode(out, self.query, self.kc, self.vc, self.bounds, self.tables, self.context, self.max_len,
+                         self.scale, K, ws, first, recent, selected=sel, k_scale=self.ks, v_scale=self.vs,
+                         dev_status=self.status, **kw)
+        torch.cuda.synchronize()
+        return out, sel
+
+    def want_selected(self, s, h, K, first, recent):
+        L, B, G = self.lens[s], self.B, self.Hq // self.Hkv
+        n = -(-L // B)
+        if n <= K:
+            return list(range(n))
+        q = self.query[s, h * G:(h + 1) * G].double()
+        bnd = self.bounds[self.tables[s, :n].long(), h].double()             # [n, 2, D]
+        t = torch.where(q[:, None] < 0, q[:, None] * bnd[None, :, 0], q[:, None] * bnd[None, :, 1])
+        score = t.sum(-1)
+        score = torch.where(score.isnan(), float("inf"), score).amax(0).tolist()
+        rest = sorted(range(first, n - recent), key=lambda b: (-score[b], b))
+        return sorted(list(range(first)) + rest[:K - first - recent] + list(range(n - recent, n)))
+
+    def check(self, out, sel, K, first=1, recent=1):
+        G = self.Hq // self.Hkv
+        sel, got = sel.cpu().tolist(), out.double()
+        for s, L in enumerate(self.lens):
+            for h in range(self.Hkv):
+                want = self.want_selected(s, h, K, first, recent)
+                assert sel[s][h] == want + [-1] * (K - len(want)), (s, h)
+                rows = got[s, h * G:(h + 1) * G]
+                if L == 0:
+                    assert bool((rows == 0).all())
+                    continue
+                tok = torch.tensor([b * self.B + i for b in want for i in range(self.B) if b * self.B + i < L])
+                blk = self.tables[s].long()[(tok // self.B).cuda()]
+                k, v = (self.keys(c)[blk, h, (tok % self.B).cuda()] for c in (self.kc, self.vc))
+                p = torch.softmax(self.query[s, h * G:(h + 1) * G].double() @ k.t() * (self.scale * self.ks), -1)
+                ref, mass = p @ v * self.vs, p @ v.abs() * self.vs
+                tol = torch.finfo(self.dt).eps / 2 * ref.abs() + WEIGHTS["e4m3" if self.e4m3 else self.dtype] * mass
+                err = (rows - ref).abs()
+                assert bool((err <= tol).all()), (s, h, float((err - tol).max()))
+
+
+# ------------------------------------------------------------------ bounds
+
+@pytest.mark.parametrize("dtype,e4m3", [("f32", False), ("f16", False), ("bf16", False), ("f16", True), ("bf16", True)])
+@pytest.mark.parametrize("D,B", [(64, 16), (128, 16), (256, 16), (128, 1), (64, 7), (128, 48), (256, 1024)])
+def test_bounds_of_new_tokens(dtype, e4m3, D, B):
+    lens = [1, B, B + 1, 3 * B - 1, 0, 5 * B + B // 2, 4 * B]
+    new = [1, B, 1, 2 * B, 0, B + B // 2 + 1, 0]
+    p = Pool(lens, D=D, B=B, dtype=dtype, e4m3=e4m3, seed=B)
+    before = torch.full_like(p.bounds, 3.5)
+    p.bounds.copy_(before)
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, p.max_len, torch.tensor(new, dtype=torch.int32, device="cuda"),
+                  max(new), dev_status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    want = before.double()
+    for s, (L, m) in enumerate(zip(lens, new)):
+        for j in range((L - m) // B, -(-L // B)) if m else ():
+            want[p.tables[s, j].long()] = p.want_bounds(s, j)
+    assert torch.equal(p.bounds.double(), want)
+
+
+def test_bounds_default_is_the_newest_block():
+    p = Pool([16, 17, 1, 40, 0])
+    before = p.bounds.clone()
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, p.max_len, dev_status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    touched = torch.zeros(p.num_blocks, dtype=torch.bool)
+    for s, j in ((0, 0), (1, 1), (2, 0), (3, 2)):
+        blk = int(p.tables[s, j])
+        touched[blk] = True
+        assert torch.equal(p.bounds[blk].double(), p.want_bounds(s, j))
+    assert bool(p.bounds[~touched].isnan().all()) and bool(before.isnan().all())
+
+
+def test_bounds_nan_and_infinite_keys():
+    p = Pool([48], dtype="f16")
+    b = p.tables[0].tolist()
+    p.kc[b[0], 0, 3, 5] = float("nan")
+    p.kc[b[1], 1, 2, 7] = float("inf")
+    p.kc[b[2], 1, 2, 9] = float("-inf")
+    p.fill_bounds()
+    torch.cuda.synchronize()
+    got = p.bounds.double()
+    nan = torch.zeros_like(got[b[0], 0], dtype=torch.bool)
+    nan[:, 5] = True
+    assert torch.equal(got[b[0], 0].isnan(), nan)
+    assert got[b[1], 1, 1, 7] == float("inf") and got[b[2], 1, 0, 9] == float("-inf")
+    for j in range(3):
+        want = p.want_bounds(0, j)
+        assert torch.equal(torch.nan_to_num(got[b[j]], 1e9), torch.nan_to_num(want, 1e9))
+
+
+def test_bounds_bad_data_is_flagged_and_skipped():
+    p = Pool([32, 32, 32, 32])
+    p.tables[0, 1] = p.num_blocks
+    p.tables[1, 1] = -7
+    new = torch.tensor([1, 1, 33, -1], dtype=torch.int32, device="cuda")
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, 32, new, 40, dev_status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == pk.DEV_BAD_BLOCK_ID | pk.DEV_BAD_LEN
+    assert bool(p.bounds.isnan().all())
+    p.status.zero_()
+    p.context[2], p.context[3] = -5, 1000
+    pk.key_bounds(p.bounds, p.kc, p.tables[2:].contiguous(), p.context[2:].contiguous(), 32, dev_status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == pk.DEV_BAD_LEN and bool(p.bounds.isnan().all())
+
+
+# ------------------------------------------------------------------ sparse decode
+
+@pytest.mark.parametrize("dtype,e4m3", [("f32", False), ("f16", False), ("bf16", False), ("f16", True), ("bf16", True)])
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(8, 2, 128, 16), (4, 4, 64, 16), (6, 2, 256, 16), (16, 1, 128, 32),
+                                        (8, 2, 64, 5), (5, 1, 128, 8), (64, 2, 128, 16)])
+def test_types_and_heads(dtype, e4m3, Hq, Hkv, D, B):
+    lens = [B * 40 + 3, 1, B * 12, 0, B * 25 + 1, B * 11 - 1, B * 13]
+    p = Pool(lens, Hq, Hkv, D, B, dtype, e4m3, seed=D + B)
+    p.fill_bounds()
+    out, sel = p.decode(12, 1, 2)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, 12, 1, 2)
+
+
+@pytest.mark.parametrize("K,first,recent", [(1, 0, 1), (2, 1, 1), (3, 0, 3), (5, 0, 1), (40, 2, 3), (200, 1, 1),
+                                            (1000, 7, 9)])
+def test_selection_sizes(K, first, recent):
+    p = Pool([16 * 300 + 5, 16 * 41, 16 * 200 - 3, 700], seed=K)
+    p.fill_bounds()
+    out, sel = p.decode(K, first, recent)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, K, first, recent)
+
+
+@pytest.mark.parametrize("lens,K", [([30000], 64), ([40001, 3, 9000], 100), ([131072], 33)])
+def test_long_contexts(lens, K):
+    p = Pool(lens, 8, 2, seed=1)
+    p.fill_bounds()
+    out, sel = p.decode(K, 1, 2)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, K, 1, 2)
+
+
+def test_many_sequences():
+    lens = [(37 * i) % 900 for i in range(300)]
+    p = Pool(lens, 8, 2, 64, seed=3)
+    p.fill_bounds()
+    out, sel = p.decode(10, 1, 1)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, 10)
+
+
+def test_all_blocks_equals_the_dense_decode_of_a_head():
+    # every block selected: the plain decode's result, up to rounding order
+    p = Pool([1000, 513, 16], seed=6)
+    p.fill_bounds()
+    out, sel = p.decode(63)
+    dense = torch.empty_like(out)
+    pk.decode(dense, p.query, p.kc, p.vc, p.tables, p.context, p.max_len, p.scale)
+    torch.cuda.synchronize()
+    assert bool(((out.float() - dense.float()).abs() <= 2.0 ** -7 * dense.float().abs() + 2.0 ** -11).all())
+    p.check(out, sel, 63)
+
+
+def test_ties_go_to_the_lowest_block():
+    for e4m3 in (False, True):
+        p = Pool([16 * 100, 16 * 77 + 1], seed=8, e4m3=e4m3)
+        for s in range(2):                                   # keys alike in all blocks, then a few better ones
+            blk = p.tables[s, :p.lens[s] // 16].long()
+            p.kc[blk] = p.kc[blk[0]].clone()
+        p.fill_bounds()
+        out, sel = p.decode(9, 0, 1)
+        assert sel[0, 0].tolist() == list(range(8)) + [99] and sel[1, 1].tolist() == list(range(8)) + [77]
+        p.check(out, sel, 9, 0, 1)
+    p = Pool([16 * 300], seed=8)
+    p.query.zero_()                                          # all scores zero
+    p.fill_bounds()
+    out, sel = p.decode(50, 2, 3)
+    p.check(out, sel, 50, 2, 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_scores_that_binary32_cannot_tell_apart(dtype):
+    # a large common part and differences far below its binary32 step decide the order
+    p = Pool([16 * 64], Hq=2, Hkv=2, D=64, dtype=dtype, seed=9)
+    p.fill_bounds()
+    p.query.fill_(0)
+    p.query[..., 0], p.query[..., 1] = 256.0, 2.0 ** -9
+    blk = p.tables[0].long()
+    p.bounds.zero_()
+    p.bounds[blk, :, 1, 0] = 1.0
+    p.bounds[blk, :, 1, 0] += torch.where(torch.arange(64, device="cuda") % 7 == 3, 2.0 ** -7, 0.0).to(p.dt)[:, None]
+    order = torch.randperm(64, generator=torch.Generator().manual_seed(1)).cuda()
+    p.bounds[blk, :, 1, 1] = (order[:, None] * 2.0 ** -8).to(p.dt)            # exact in every type
+    out, sel = p.decode(20, 0, 1)
+    p.check(out, sel, 20, 0, 1)
+
+
+def test_infinite_and_nan_bounds_come_first():
+    p = Pool([16 * 60], dtype="f16", seed=10)
+    p.fill_bounds()
+    blk = p.tables[0].long()
+    p.bounds[blk[40], 0, 1] = float("inf")
+    p.bounds[blk[41], 0] = float("nan")
+    p.bounds[blk[42], 1] = float("-inf")
+    p.query[0, 0, 3] = 0.0
+    out, sel = p.decode(5, 1, 1)
+    assert sel[0, 0].tolist() == p.want_selected(0, 0, 5, 1, 1) and {40, 41} <= set(sel[0, 0].tolist())
+    assert sel[0, 1].tolist() == p.want_selected(0, 1, 5, 1, 1)
+    p.query[0, 5] = float("nan")                             # every score of head 1 is NaN: the lowest blocks
+    out, sel = p.decode(5, 1, 1)
+    assert sel[0, 1].tolist() == [0, 1, 2, 3, 59]
+
+
+def test_bad_table_entries_and_lengths_are_flagged():
+    p = Pool([16 * 50, 16 * 50, 100])
+    p.fill_bounds()
+    p.tables[0, 0] = p.num_blocks + 3                        # always selected: the decode meets it
+    p.tables[1, 20] = -1                                     # scored: skipped unless nothing else is left
+    out, sel = p.decode(8, 1, 1)
+    assert int(p.status.item()) == pk.DEV_BAD_BLOCK_ID
+    assert 20 not in sel[1, 0].tolist()
+    p.status.zero_()
+    p.context[2] = -3
+    p.decode(8, 1, 1)
+    assert int(p.status.item()) & pk.DEV_BAD_LEN
+
+
+def test_padded_batch_workspace_reuse_and_graph():
+    p = Pool([16 * 90 + 1, 0, 16 * 33, 0], seed=12)
+    p.fill_bounds()
+    ws = pk.alloc_sparse_workspace(p.S, p.Hq, p.Hkv, p.D, p.B, p.max_len, 16)
+    ws.fill_(0xFF)
+    out, sel = p.decode(16, 1, 2, ws)
+    p.check(out, sel, 16, 1, 2)
+    again, sel2 = p.decode(16, 1, 2, ws)
+    assert torch.equal(out, again) and torch.equal(sel, sel2)
+    # captured, with the lengths changed before the replay
+    side, o2, s2 = torch.cuda.Stream(), torch.empty_like(out), torch.empty_like(sel)
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            pk.sparse_decode(o2, p.query, p.kc, p.vc, p.bounds, p.tables, p.context, p.max_len, p.scale, 16, ws, 1, 2,
+                             selected=s2, dev_status=p.status)
+        graph.replay()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, o2) and torch.equal(sel, s2)
+    p.lens = [16 * 70, 0, 16 * 20 + 0, 0]
+    p.context.copy_(torch.tensor(p.lens, dtype=torch.int32))
+    with torch.cuda.stream(side):
+        graph.replay()
+    torch.cuda.synchronize()
+    p.check(o2, s2, 16, 1, 2)
+
+
+def test_two_calls_at_once_on_two_streams():
+    a, b = Pool([16 * 200, 777], seed=13), Pool([16 * 150 + 9, 3001], seed=14)
+    a.fill_bounds()
+    b.fill_bounds()
+    torch.cuda.synchronize()
+    want = [x.decode(11)[0].clone() for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.empty_like(w) for w in want]
+    ws = [pk.alloc_sparse_workspace(x.S, x.Hq, x.Hkv, x.D, x.B, x.max_len, 11) for x in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, o, w, st in zip((a, b), got, ws, streams):
+            pk.sparse_decode(o, x.query, x.kc, x.vc, x.bounds, x.tables, x.context, x.max_len, x.scale, 11, w,
+                             stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_draft_tokens_as_rows():
+    # four query tokens of one sequence: the table repeated, each with the length it sees
+    p = Pool([16 * 80 + 2], seed=15)
+    p.fill_bounds()
+    rows = Pool([16 * 80 + 2 - 3 + i for i in range(4)], seed=15, max_blocks=81)
+    rows.kc, rows.vc, rows.bounds, rows.num_blocks = p.kc, p.vc, p.bounds, p.num_blocks
+    rows.tables = p.tables.expand(4, -1).contiguous()
+    out, sel = rows.decode(10, 1, 2)
+    assert int(rows.status.item()) == 0
+    rows.check(out, sel, 10, 1, 2)
+
+
+def test_wrong_arguments():
+    p = Pool([100])
+    ws = pk.alloc_sparse_workspace(1, 8, 2, 128, 16, 100, 4)
+    call = lambda **kw: pk.sparse_decode(**{**dict(                                       # noqa: E731
+        out=p.query.clone(), query=p.query, k_cache=p.kc, v_cache=p.vc, k_bounds=p.bounds, block_tables=p.tables,
+        context_lens=p.context, max_context_len=100, scale=0.1, num_select=4, workspace=ws), **kw})
+    for kw in (dict(num_select=0), dict(first_blocks=-1), dict(recent_blocks=0), dict(first_blocks=3, recent_blocks=2),
+               dict(scale=0.0), dict(scale=-1.0), dict(workspace=ws[:128]), dict(workspace=ws[1:])):
+        with pytest.raises(pk.PagedKVError):
+            call(**kw)
+    for kw in (dict(k_bounds=p.bounds.float()), dict(k_bounds=p.bounds[:1]), dict(out=p.query.float()),
+               dict(selected=torch.zeros(1, 2, 5, dtype=torch.int32, device="cuda")),
+               dict(selected=torch.zeros(1, 2, 4, device="cuda")), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(ValueError):
+        pk.key_bounds(p.bounds[:, :1], p.kc, p.tables, p.context, 100)
+    with pytest.raises(pk.PagedKVError):                     # max_new_tokens without new_tokens
+        pk.key_bounds(p.bounds, p.kc, p.tables, p.context, 100, max_new_tokens=2)
+    torch.cuda.synchronize()

@@ -333,7 +333,7 @@ struct SparsePlan {
     int chunk_seqs;               // sequences per decode launch (its grid holds 65535 rows)
     int partition_size;
     bool split;
-    size_t scores, slab_tables, slab_lens, partials, total;   // workspace offsets
+    size_t scores, exact_keys, slab_tables, slab_lens, partials, total;   // workspace offsets
 };
 
 // Partitions of the selected tokens: 512, halved (down to 128) while the
@@ -361,7 +361,8 @@ SparsePlan sparse_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
     const int parts = max_partitions(l.max_tokens, l.partition_size);
     l.split = parts > 1 && !(rows >= 8 * slots && parts <= 2);
     l.scores = 0;
-    l.slab_tables = align256((size_t)rows * l.max_ctx_blocks * sizeof(double));
+    l.exact_keys = align256((size_t)rows * l.max_ctx_blocks * sizeof(float));
+    l.slab_tables = l.exact_keys + align256((size_t)rows * l.max_ctx_blocks * sizeof(uint64_t));
     l.slab_lens = l.slab_tables + align256((size_t)rows * l.table_width * sizeof(int32_t));
     l.partials = l.slab_lens + align256((size_t)rows * sizeof(int32_t));
     // Partials for any smaller batch or context too (whose partitions may be
@@ -942,8 +943,9 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
     if (!(scale > 0.f) || num_select < 1 || first_blocks < 0 || recent_blocks < 1 ||
         first_blocks > num_select || recent_blocks > num_select - first_blocks)
         return PA_ERR_INVALID_ARG;
-    // slab ids are 32-bit, and rows index a one-dimensional grid
-    if (max_context_len > kMaxSparseContext || num_blocks > 0x7fffffffll / num_kv_heads ||
+    // slab ids are 32-bit, rows index a one-dimensional grid, and the group's
+    // queries are staged in shared memory
+    if (p.group > 128 || max_context_len > kMaxSparseContext || num_blocks > 0x7fffffffll / num_kv_heads ||
         (long long)num_seqs * num_kv_heads > 0x7fffffffll)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
@@ -959,7 +961,8 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
     sp.k_bounds = k_bounds;
     sp.block_tables = block_tables;
     sp.context_lens = context_lens;
-    sp.scores = reinterpret_cast<double*>(w + l.scores);
+    sp.scores = reinterpret_cast<float*>(w + l.scores);
+    sp.exact_keys = reinterpret_cast<uint64_t*>(w + l.exact_keys);
     sp.slab_tables = reinterpret_cast<int32_t*>(w + l.slab_tables);
     sp.slab_lens = reinterpret_cast<int32_t*>(w + l.slab_lens);
     sp.selected = selected;

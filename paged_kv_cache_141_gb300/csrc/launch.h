@@ -209,7 +209,8 @@ struct SelectParams {
     const void* k_bounds;         // [num_blocks, Hkv, 2, D], the query's type
     const int32_t* block_tables;  // [S, max_blocks]
     const int32_t* context_lens;  // [S]
-    double* scores;               // [S * Hkv, max_ctx_blocks]
+    float* scores;                // [S * Hkv, max_ctx_blocks]: where they exceed shared memory
+    uint64_t* exact_keys;         // [S * Hkv, max_ctx_blocks]: many undecided blocks
     int32_t* slab_tables;         // [S * Hkv, table_width]
     int32_t* slab_lens;           // [S * Hkv] tokens of the selection
     int32_t* selected;            // [S, Hkv, num_select] logical blocks, -1 padded; may be null
@@ -227,6 +228,8 @@ struct SelectParams {
     int num_select;
     int first_blocks;
     int recent_blocks;
+    int side_bytes;               // set by the launcher: shared memory of the query's sides,
+    int keys_in_smem;             // and whether the scores are kept there
 };
 
 cudaError_t launch_select_blocks(const SelectParams& p, int head_size, pa_dtype q_dtype,

@@ -16,9 +16,12 @@
 //    16 blocks x 2 D by 2 D x 8 heads. The products are exact in binary32; the
 //    sums are taken to err by at most kScoreEps times sum |q_d bound_d|, which
 //    a second product of the magnitudes gives.
-//  - the threshold among those scores. Blocks whose distance to the other side
-//    of it exceeds both errors are settled; the rest (usually none) are scored
-//    again in binary64 and ranked.
+//  - the threshold among those scores, from a histogram over their range.
+//    Blocks whose distance to the other side of the threshold exceeds both
+//    errors are settled; the rest (usually none) are scored again in binary64
+//    and ranked. Where the histogram's bin at the threshold holds too many
+//    blocks (equal scores) or a score is not finite, a search over the key
+//    bits takes its place.
 // A cluster of CTAs takes one (sequence, KV head): all score, into the first
 // CTA's shared memory, and the first one selects. Reading the bounds once
 // (2 D elements per block) bounds the kernel for batches, the latency of the
@@ -41,13 +44,19 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kRankList = 256;          // ambiguous blocks ranked in shared memory
+constexpr int kRankList = kSelThreads;  // blocks ranked in shared memory, one per thread
+constexpr int kBins = 4 * kSelThreads;  // of the score histogram
 // Keys of up to this many blocks are kept in shared memory (two CTAs per SM);
 // longer contexts' in the workspace.
 constexpr int kSmemKeys = 24 * 1024;
-// |approximate - exact score| <= kScoreEps * sum_d |q_d bound_d|: 2 D <= 512
-// terms, each addition off by at most 2^-23 of the sum of magnitudes.
-constexpr float kScoreEps = 6.2e-5f;    // > 2^-14
+// |approximate - exact score| <= kScoreEps * sum_d |q_d bound_d|. An MMA adds 16
+// exact products to its accumulator; taking each of the 17 terms to lose up to
+// 2^-23 of the largest, a chain of four MMAs errs by at most 4 * 17 * 2^-23 of
+// its own terms' magnitudes, and so do all chains together (chains are joined
+// in binary32, eight additions at most). That is below 2^-16.8; 2^-16 leaves a
+// factor of 1.7. Binary32 queries (a sum of 8 + 5 terms a lane and across) are
+// well inside it.
+constexpr float kScoreEps = 1.0f / 65536;
 
 // The sequence's length as the decode takes it (clamped to what the table and
 // the bound allow).
@@ -113,12 +122,59 @@ __device__ double exact_score(const SelectParams& p, int s, int h, int64_t blk, 
     return best;
 }
 
+// Sixteen blocks' bounds rows, four 64-byte steps (a quarter: 128 elements) at
+// a time: this lane's 16-byte chunks of blocks g and g + 8.
+struct Quarter {
+    uint4 x[4], y[4];
+    template <typename T>
+    __device__ __forceinline__ void load(const T* x_row, const T* y_row) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = __ldg(reinterpret_cast<const uint4*>(x_row + 32 * j));
+            y[j] = __ldg(reinterpret_cast<const uint4*>(y_row + 32 * j));
+        }
+    }
+};
+
+// Adds a quarter's products with the query sides (this lane's chunks, 32 lanes
+// apart) to the scores c and magnitudes m: lane (g, t4) holds blocks g and
+// g + 8, heads 2 t4 and 2 t4 + 1. A lane's eight consecutive elements stand
+// for k = 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of two MMAs, in the bounds and the
+// sides alike, so both are loaded as 16-byte vectors.
+template <typename T>
+__device__ __forceinline__ void add_quarter(const Quarter& b, const uint4* sides, float (&c)[4],
+                                            float (&m)[4]) {
+    using Ops = MmaOps<T>;
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 q = sides[32 * j];
+        const uint32_t a0[4] = {b.x[j].x, b.y[j].x, b.x[j].y, b.y[j].y};
+        const uint32_t a1[4] = {b.x[j].z, b.y[j].z, b.x[j].w, b.y[j].w};
+        Ops::mma(c0, a0, q.x, q.y);
+        Ops::mma(c1, a1, q.z, q.w);
+        const uint32_t b0[4] = {a0[0] & kAbs, a0[1] & kAbs, a0[2] & kAbs, a0[3] & kAbs};
+        const uint32_t b1[4] = {a1[0] & kAbs, a1[1] & kAbs, a1[2] & kAbs, a1[3] & kAbs};
+        Ops::mma(m, b0, q.x & kAbs, q.y & kAbs);
+        Ops::mma(m, b1, q.z & kAbs, q.w & kAbs);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += c0[i] + c1[i];
+}
+
 struct SelShared {
-    float err[kMaxCluster];             // per CTA: the largest sum of magnitudes
+    float err[kMaxCluster];             // per CTA: the largest sum of magnitudes,
+    float lowest[kMaxCluster];          // and the range of its finite scores
+    float highest[kMaxCluster];
+    int bins[kBins];
+    int bin;                            // the threshold's, and the candidates above it
+    int above;
     int part[2][kSelWarps];             // count(): per-warp sums, double-buffered
-    float fpart[2][kSelWarps];
+    float fpart[3][kSelWarps];
     int list_n;
     int list[kRankList];
+    float list_score[kRankList];
     uint64_t list_key[kRankList];
 };
 
@@ -155,10 +211,148 @@ __device__ __forceinline__ K kth_largest(SelShared& sh, int n, int want, int& tu
     return prefix;
 }
 
+// The score that ordered() puts below every value: a block not taken.
+__device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu); }
+
+// The taken candidates, where a histogram of the approximate scores over their
+// range leaves few blocks near the threshold: thr such that they are those of
+// ordered(keys[i]) >= thr (undecided blocks' keys are replaced). False: not
+// decided here, and keys are as they were.
 template <typename T, int D>
+__device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, float* keys, int nc,
+                                       int want, float mag, int C, int s, int h,
+                                       const int32_t* table, uint32_t& thr) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float lowest = sh.lowest[0], highest = sh.highest[0];
+    for (int r = 1; r < C; ++r) {
+        lowest = fminf(lowest, sh.lowest[r]);
+        highest = fmaxf(highest, sh.highest[r]);
+    }
+    // err2: both errors, and the rounding of k +- err2 below (2^-24 of k <= mag)
+    const float err2 = mag * (2.f * kScoreEps * 1.01f);
+    const float scale = (float)(kBins - 1) / (highest - lowest);
+    if (!(isfinite(mag) && highest > lowest && isfinite(scale))) return false;
+    // non-decreasing in k; blocks the table does not name score -infinity: bin 0
+    auto bin_of = [&](float k) {
+        const int b = __float2int_rz((k - lowest) * scale);
+        return b < 0 ? 0 : (b >= kBins ? kBins - 1 : b);
+    };
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.bins[i] = 0;
+    if (threadIdx.x == 0) sh.list_n = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nc; i += kSelThreads) atomicAdd(&sh.bins[bin_of(keys[i])], 1);
+    __syncthreads();
+    // the bin where the count from the top reaches want: thread t has the four
+    // bins below kBins - 4 t
+    {
+        const int top = kBins - 1 - 4 * (int)threadIdx.x;
+        int c[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += c[j] = sh.bins[top - j];
+        int run = sum;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, m);
+            if (lane >= m) run += v;
+        }
+        if (lane == 31) sh.part[0][warp] = run;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) run += sh.part[0][w];
+        int before = run - sum;
+        if (before < want && run >= want) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < want && before + c[j] >= want) {
+                    sh.bin = top - j;
+                    sh.above = before;
+                }
+                before += c[j];
+            }
+        }
+    }
+    __syncthreads();
+    // Every block that can change sides is within err2 of the threshold's bin.
+    const int bin = sh.bin;
+    int below_bin_near = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+        const float k = keys[i];
+        if (bin_of(k + err2) >= bin && bin_of(k - err2) <= bin) {
+            const int at = atomicAdd(&sh.list_n, 1);
+            if (at < kRankList) {
+                sh.list[at] = i;
+                sh.list_score[at] = k;
+            }
+            below_bin_near += bin_of(k) > bin;                 // counted above, but not settled
+        }
+    }
+    __syncthreads();
+    const int m = sh.list_n;
+    if (m > kRankList) return false;
+    int turn = 0;
+    const int left = want - (sh.above - cta_sum(sh, below_bin_near, turn));   // the list's places
+    // rank by approximate score (the list's order varies, the ranks do not)
+    const int e = threadIdx.x;
+    const bool mine = e < m;
+    const float k = mine ? sh.list_score[e] : 0.f;
+    const int i = mine ? sh.list[e] : 0;
+    int before = 0;
+    if (mine)
+        for (int o = 0; o < m; ++o)
+            before += sh.list_score[o] > k || (sh.list_score[o] == k && sh.list[o] < i);
+    const bool in = mine && before < left;
+    float a = in ? k : INFINITY, b = mine && !in ? k : -INFINITY;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+    }
+    if (lane == 0) {
+        sh.fpart[0][warp] = a;
+        sh.fpart[1][warp] = b;
+    }
+    __syncthreads();
+    for (int w = 0; w < kSelWarps; ++w) {
+        a = fminf(a, sh.fpart[0][w]);
+        b = fmaxf(b, sh.fpart[1][w]);
+    }
+    bool take = in;
+    if (a - b <= err2) {
+        // the blocks within err2 of the other side, in binary64
+        const bool open = mine && (in ? k <= b + err2 : k >= a - err2);
+        if (mine) sh.list_key[e] = open ? 1 : 0;
+        __syncthreads();
+        for (int o = warp; o < m; o += kSelWarps) {
+            if (sh.list_key[o] == 0) continue;
+            const uint64_t x = ordered64(exact_score<T, D>(p, s, h, table[sh.list[o]], lane));
+            if (lane == 0) sh.list_key[o] = x;                 // above 0, the settled ones' mark
+        }
+        __syncthreads();
+        if (open) {
+            int places = left, ahead = 0;
+            const uint64_t x = sh.list_key[e];
+            for (int o = 0; o < m; ++o) {
+                const uint64_t y = sh.list_key[o];
+                if (y == 0) places -= sh.list_score[o] >= a;   // settled inside
+                else ahead += y > x || (y == x && sh.list[o] < i);
+            }
+            take = ahead < places;
+        }
+    }
+    __syncthreads();
+    if (mine) keys[i] = take ? INFINITY : out_key();
+    thr = ordered(a);
+    __syncthreads();
+    return true;
+}
+
+// kOneTile: groups of at most eight heads, one MMA tile.
+template <typename T, int D, bool kOneTile>
 __global__ void __launch_bounds__(kSelThreads, 2)
 select_blocks_kernel(const __grid_constant__ SelectParams p) {
     constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
+    constexpr int NQ = STEPS / 4;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -178,17 +372,17 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
     const int want = p.num_select - p.first_blocks - p.recent_blocks;
     const int lo = p.first_blocks;
     const int nc = all ? 0 : n - p.recent_blocks - lo;         // candidates lo .. lo + nc - 1
+    const bool scored = nc > 0 && want > 0;
 
     uint4* sides = reinterpret_cast<uint4*>(dyn);              // [n-tile][step][lane]
-    const int ntiles = (p.group + 7) / 8;
     float* keys = p.keys_in_smem ? reinterpret_cast<float*>(dyn + p.side_bytes)
                                  : p.scores + (size_t)row * p.max_ctx_blocks;
 
-    if (nc > 0 && want > 0) {
+    if (scored) {
         // ------------------------------------------------ approximate scores
         cluster.sync();                                        // the first CTA runs: its memory may be written
         float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(keys, 0) : keys;
-        float worst = 0.f;
+        float worst = 0.f, lowest = INFINITY, highest = -INFINITY;
         if constexpr (std::is_same<T, float>::value) {
             constexpr int E = D / 32;
             for (int i = rank * kSelWarps + warp; i < nc; i += C * kSelWarps) {
@@ -218,11 +412,13 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
                         best = fmaxf(best, sum);
                         worst = max_nan(worst, mag);
                     }
+                    lowest = fminf(lowest, best);
+                    highest = fmaxf(highest, best);
                 }
                 if (lane == 0) out_keys[i] = best;
             }
         } else {
-            using Ops = MmaOps<T>;
+            const int ntiles = (p.group + 7) / 8;
             for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += kSelThreads) {
                 const int l = i & 31, j = (i >> 5) % STEPS, nt = i / (32 * STEPS);
                 const int g = nt * 8 + (l >> 2);
@@ -241,71 +437,119 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
             __syncthreads();
             const int g = lane >> 2, t4 = lane & 3;
             const int tiles = (nc + 15) / 16;
-            for (int tile = rank * kSelWarps + warp; tile < tiles; tile += C * kSelWarps) {
-                // this lane's rows: blocks g and g + 8 of the tile
-                const T* src[2];
-                bool there[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = tile * 16 + g + 8 * r;
-                    const int64_t blk = table[lo + (i < nc ? i : nc - 1)];
-                    there[r] = blk >= 0 && blk < p.num_blocks;
-                    src[r] = static_cast<const T*>(p.k_bounds) +
-                             ((size_t)(there[r] ? blk : 0) * p.num_kv_heads + h) * 2 * D + 8 * t4;
-                }
-                float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
-                for (int nt = 0; nt < ntiles; ++nt) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j0 = 0; j0 < STEPS; j0 += 4) {
-                        constexpr int U = 4;
-                        uint4 x[U], y[U];
-#pragma unroll
-                        for (int j = 0; j < U; ++j) {
-                            x[j] = __ldg(reinterpret_cast<const uint4*>(src[0] + 32 * (j0 + j)));
-                            y[j] = __ldg(reinterpret_cast<const uint4*>(src[1] + 32 * (j0 + j)));
-                        }
-#pragma unroll
-                        for (int j = 0; j < U; ++j) {
-                            const uint4 q = sides[(nt * STEPS + j0 + j) * 32 + lane];
-                            constexpr uint32_t kAbs = 0x7fff7fffu;
-                            const uint32_t a0[4] = {x[j].x, y[j].x, x[j].y, y[j].y};
-                            const uint32_t a1[4] = {x[j].z, y[j].z, x[j].w, y[j].w};
-                            Ops::mma(c, a0, q.x, q.y);
-                            Ops::mma(c, a1, q.z, q.w);
-                            const uint32_t b0[4] = {x[j].x & kAbs, y[j].x & kAbs, x[j].y & kAbs, y[j].y & kAbs};
-                            const uint32_t b1[4] = {x[j].z & kAbs, y[j].z & kAbs, x[j].w & kAbs, y[j].w & kAbs};
-                            Ops::mma(m, b0, q.x & kAbs, q.y & kAbs);
-                            Ops::mma(m, b1, q.z & kAbs, q.w & kAbs);
-                        }
-                    }
-                    // this lane: heads 2 t4 and 2 t4 + 1 of blocks g and g + 8
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (nt * 8 + 2 * t4 + e < p.group) {
-                                best[r] = fmaxf(best[r], c[2 * r + e]);
-                                mag[r] = max_nan(mag[r], m[2 * r + e]);
-                            }
-                }
+            const int stride = C * kSelWarps;
+            // this lane's two blocks of a tile, and their bounds rows (block 0's
+            // where the table names none)
+            auto block_of = [&](int tile, int r) {
+                const int i = tile * 16 + g + 8 * r;
+                return table[lo + (i < nc ? i : nc - 1)];
+            };
+            auto there = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
+            auto row_of = [&](int blk) {
+                return static_cast<const T*>(p.k_bounds) +
+                       ((size_t)(there(blk) ? blk : 0) * p.num_kv_heads + h) * 2 * D + 8 * t4;
+            };
+            auto finish = [&](int tile, const int (&blk)[2], float (&best)[2], float (&mag)[2]) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
                     best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
                     const int i = tile * 16 + g + 8 * r;
-                    if (there[r]) worst = max_nan(worst, mag[r]);
-                    if (t4 == 0 && i < nc) out_keys[i] = there[r] ? best[r] : -INFINITY;
+                    const bool ok = there(blk[r]);
+                    if (ok) {
+                        worst = max_nan(worst, mag[r]);
+                        lowest = fminf(lowest, best[r]);
+                        highest = fmaxf(highest, best[r]);
+                    }
+                    if (t4 == 0 && i < nc) out_keys[i] = ok ? best[r] : -INFINITY;
+                }
+            };
+            // maxima over the heads of one MMA tile
+            auto over_heads = [&](int nt, const float (&c)[4], const float (&m)[4], float (&best)[2], float (&mag)[2]) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (nt * 8 + 2 * t4 + e < p.group) {
+                            best[r] = fmaxf(best[r], c[2 * r + e]);
+                            mag[r] = max_nan(mag[r], m[2 * r + e]);
+                        }
+            };
+            int tile = rank * kSelWarps + warp;
+            if constexpr (kOneTile) {
+                // the next quarter's loads are in flight while one is multiplied
+                Quarter buf[2];
+                int blk[2];
+                const T *x = nullptr, *y = nullptr;
+                if (tile < tiles) {
+                    blk[0] = block_of(tile, 0);
+                    blk[1] = block_of(tile, 1);
+                    x = row_of(blk[0]);
+                    y = row_of(blk[1]);
+                    buf[0].load(x, y);
+                }
+                for (; tile < tiles; tile += stride) {
+                    const int next = tile + stride < tiles ? tile + stride : tile;
+                    const int nblk[2] = {block_of(next, 0), block_of(next, 1)};
+                    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (q + 1 < NQ) {
+                            buf[(q + 1) & 1].load(x + 128 * (q + 1), y + 128 * (q + 1));
+                        } else {
+                            x = row_of(nblk[0]);
+                            y = row_of(nblk[1]);
+                            if (next != tile) buf[(q + 1) & 1].load(x, y);
+                        }
+                        add_quarter<T>(buf[q & 1], sides + 128 * q + lane, c, m);
+                    }
+                    if (NQ == 1) buf[0] = buf[1];
+                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                    over_heads(0, c, m, best, mag);
+                    finish(tile, blk, best, mag);
+                    blk[0] = nblk[0];
+                    blk[1] = nblk[1];
+                }
+            } else {
+                for (; tile < tiles; tile += stride) {
+                    const int blk[2] = {block_of(tile, 0), block_of(tile, 1)};
+                    const T *x = row_of(blk[0]), *y = row_of(blk[1]);
+                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                    for (int nt = 0; nt < ntiles; ++nt) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            Quarter b;
+                            b.load(x + 128 * q, y + 128 * q);
+                            add_quarter<T>(b, sides + (nt * STEPS + 4 * q) * 32 + lane, c, m);
+                        }
+                        over_heads(nt, c, m, best, mag);
+                    }
+                    finish(tile, blk, best, mag);
                 }
             }
         }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
-        if (lane == 0) sh.fpart[0][warp] = worst;
+        for (int m = 16; m > 0; m >>= 1) {
+            worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
+            lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, m));
+            highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, m));
+        }
+        if (lane == 0) {
+            sh.fpart[0][warp] = worst;
+            sh.fpart[1][warp] = lowest;
+            sh.fpart[2][warp] = highest;
+        }
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kSelWarps; ++w) worst = max_nan(worst, sh.fpart[0][w]);
+            for (int w = 1; w < kSelWarps; ++w) {
+                worst = max_nan(worst, sh.fpart[0][w]);
+                lowest = fminf(lowest, sh.fpart[1][w]);
+                highest = fmaxf(highest, sh.fpart[2][w]);
+            }
             *cluster.map_shared_rank(&sh.err[rank], 0) = worst;
+            *cluster.map_shared_rank(&sh.lowest[rank], 0) = lowest;
+            *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
         }
     }
     cluster.sync();
@@ -313,10 +557,14 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
 
     int turn = 0;
     uint32_t thr = 0;                                          // taken candidates: ordered(key) >= thr
-    if (nc > 0 && want > 0) {
-        float mag = 0.f;
+    bool done = !scored;
+    float mag = 0.f;
+    if (scored) {
         for (int r = 0; r < C; ++r) mag = max_nan(mag, sh.err[r]);
-        const double err2 = 2.0 * (double)kScoreEps * (double)mag;
+        done = threshold_by_histogram<T, D>(p, sh, keys, nc, want, mag, C, s, h, table + lo, thr);
+    }
+    if (!done) {
+        const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
         const bool finite = isfinite(mag);
         // Settled blocks: those that beat (or lose to) every block on the other
         // side of the threshold by more than both errors. in_above: taken for
@@ -350,7 +598,7 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
             in_above = (double)b + err2;
             out_below = (double)a - err2;
         }
-        const float kOut = __uint_as_float(0xffffffffu);       // ordered() puts it below every value
+        const float kOut = out_key();
         auto settled = [&](float k) { return finite && ((double)k > in_above || (double)k < out_below); };
         // count the certain ones and the unsettled
         int in = 0, open = 0;
@@ -479,19 +727,28 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
 template <typename T, int D>
 cudaError_t launch_select(SelectParams p, cudaStream_t stream) {
     const int rows = p.num_seqs * p.num_kv_heads;
-    // CTAs per row: enough for two on each of 152 SMs, each with a tile of 16
-    // blocks per warp or more
+    // CTAs per row: while all fit on 152 SMs, two each, and every warp keeps a
+    // tile of 16 blocks or more. For many rows one CTA each wins, as their
+    // selections overlap other rows' scoring (512 rows of up to 2048 blocks:
+    // steps of 133, 141, 159 and 205 us with 1, 2, 4 and 8; 8 rows of 8192:
+    // 111, 72, 53, 43 and 39 us with 1, 2, 4, 8 and 16).
     int C = 1;
-    while (C < 8 && rows * C < 304 && p.max_ctx_blocks >= 2 * C * kSelWarps * 16) C *= 2;
+    while (C < kMaxCluster && rows <= 152 / C && p.max_ctx_blocks >= 2 * C * kSelWarps * 16) C *= 2;
     const int ntiles = (p.group + 7) / 8;
     p.side_bytes = std::is_same<T, float>::value ? 0 : ntiles * (2 * D / 32) * 512;
     const bool scored = p.max_ctx_blocks > p.num_select;
     p.keys_in_smem = p.max_ctx_blocks <= kSmemKeys && p.side_bytes <= 96 * 1024;
     if (p.side_bytes > 200 * 1024) return cudaErrorInvalidValue;
     const int smem = scored ? p.side_bytes + (p.keys_in_smem ? p.max_ctx_blocks * 4 : 0) : 0;
-    auto kernel = select_blocks_kernel<T, D>;
+    // one MMA tile of heads, or (binary32 has no tiles) any number
+    auto kernel = std::is_same<T, float>::value || p.group <= 8 ? select_blocks_kernel<T, D, true>
+                                                                : select_blocks_kernel<T, D, false>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 200 * 1024);
     if (e != cudaSuccess) return e;
+    if (C > 8) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows * C);
     cfg.blockDim = dim3(kSelThreads);

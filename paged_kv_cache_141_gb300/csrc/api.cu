@@ -980,6 +980,16 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
     sp.num_select = num_select;
     sp.first_blocks = first_blocks;
     sp.recent_blocks = recent_blocks;
+    if (sparse_fused(q_dtype, p.group, head_size, block_size, l.table_width)) {
+        SparseParams f{};
+        f.sel = sp;
+        f.out = out;
+        f.k_cache = k_cache;
+        f.v_cache = v_cache;
+        f.q_mul = p.q_mul;
+        f.v_mul = p.v_mul;
+        return from_cuda(launch_sparse_decode(f, head_size, q_dtype, cache_dtype, cs));
+    }
     const cudaError_t e = launch_select_blocks(sp, head_size, q_dtype, cs);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     const size_t seq_bytes = (size_t)num_q_heads * head_size * elem_bytes(q_dtype);

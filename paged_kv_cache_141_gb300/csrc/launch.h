@@ -201,7 +201,7 @@ struct BoundsParams {
 cudaError_t launch_key_bounds(const BoundsParams& p, int head_size, pa_dtype cache_dtype,
                               pa_dtype bounds_dtype, cudaStream_t stream);
 
-// Block scores and selection of the block-sparse decode (sparse_select.cu).
+// Block scores and selection of the block-sparse decode (sparse_select.cuh).
 // A slab is one (block, KV head) pair of the cache, block * Hkv + head; the
 // selection of (sequence s, KV head h) is row s * Hkv + h of slab_tables.
 struct SelectParams {
@@ -231,6 +231,21 @@ struct SelectParams {
     int side_bytes;               // set by the launcher: shared memory of the query's sides,
     int keys_in_smem;             // and whether the scores are kept there
 };
+
+// The fused block-sparse decode (sparse_decode.cu).
+struct SparseParams {
+    SelectParams sel;             // slab_tables, slab_lens unused
+    void* out;                    // [S, Hq, D]
+    const void* k_cache;
+    const void* v_cache;
+    float q_mul;                  // scale * log2(e) * (E4M3 cache ? k_scale : 1)
+    float v_mul;                  // E4M3 cache ? v_scale : 1
+    int list_bytes;               // set by the launcher
+};
+
+bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width);
+cudaError_t launch_sparse_decode(const SparseParams& sp, int head_size, pa_dtype q_dtype,
+                                 pa_dtype cache_dtype, cudaStream_t stream);
 
 cudaError_t launch_select_blocks(const SelectParams& p, int head_size, pa_dtype q_dtype,
                                  cudaStream_t stream);

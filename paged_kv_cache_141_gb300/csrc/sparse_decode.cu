@@ -1,0 +1,446 @@
+// sparse_decode.cu -- the block-sparse decode in one kernel: a cluster of CTAs
+// takes one (sequence, KV head), scores its blocks and selects (see
+// sparse_select.cuh), and then attends to the selection:
+//     out_h = sum_i softmax_i(scale q_h . k_i) v_i   over the selected tokens.
+// While one row's first CTA selects, other rows' CTAs on the SM score or
+// attend, so the memory system has work throughout; nothing goes through
+// memory between the two parts, and few rows pay one launch.
+//
+// Attention: each warp takes every 8 C-th tile of 16 tokens (a block, or a part
+// of one). Both products run on warp-level MMAs, straight from global memory
+// to registers, as no element is used twice but by the group's heads:
+//   S (16 tokens x 8 heads) = K (16 x D) . Q^T, a lane's 16-byte chunk of a key
+//     row standing for k = 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of two steps;
+//   O^T (D x 8 heads) += V^T (D x 16 tokens) . P^T: a lane loads the 16-byte
+//     chunks of the four tokens it holds as k (2 t4, 2 t4 + 1, 2 t4 + 8,
+//     2 t4 + 9) and pairs them component by component with byte permutes; the
+//     components of a chunk are spread over the tiles' rows g and g + 8.
+// The next tile's keys are loaded while this tile's softmax and P.V run, its
+// values while the next scores run. The softmax reference moves only when a
+// score passes it by 2^8 (weights up to 256 are as good as those up to 1), so
+// most tiles need no maximum across lanes. Weights are two 16-bit terms (16
+// significant bits; one binary16 term for E4M3 values, 2^-11, inside the codes'
+// own 2^-4), and the sums use exactly the weights that the products use. E4M3 codes
+// widen to binary16 times 2^-8 in integer operations; a 16-bit query meets
+// them scaled by a power of two to at most 2 in magnitude, exact but for
+// components more than 2^14 below the head's largest. Partial results are joined in
+// shared memory across the warps, and through the cluster's across CTAs.
+#include "sparse_select.cuh"
+
+namespace pagedkv {
+
+namespace {
+
+// A tile's keys of tokens g and g + 8 (this lane's chunks), and values of
+// tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9.
+template <typename CT, int D>
+struct Tile16 {                                     // 16-bit caches
+    static constexpr int KJ = D / 32, VU = D / 64;
+    uint4 x[KJ], y[KJ];
+    uint4 v[4][VU];
+};
+
+template <int D>
+struct Tile16<e4m3_t, D> {
+    static constexpr int KJ = D / 64;
+    using VWord = typename std::conditional<D == 128, uint4, uint2>::type;   // D / 8 codes
+    uint4 x[KJ], y[KJ];
+    VWord v[4];
+};
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
+
+// Codes in bytes 0 and 2 (even) or 1 and 3 (odd) of w as a binary16 pair of
+// their values times 2^-8 (see e4m3x2_to_f16x2_scaled).
+__device__ __forceinline__ uint32_t widen_even(uint32_t w) {
+    const uint32_t x = (w << 7) & 0x7f807f80u;
+    return x + (x & 0x40004000u);
+}
+__device__ __forceinline__ uint32_t widen_odd(uint32_t w) {
+    const uint32_t x = (w >> 1) & 0x7f807f80u;
+    return x + (x & 0x40004000u);
+}
+
+struct Joined {                                     // one CTA's result, read by the cluster
+    float m[8], l[8];
+};
+
+template <typename QT, typename CT, int D>
+__global__ void __launch_bounds__(kSelThreads, 2)
+sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
+    constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
+    using MT = typename MathType<CT>::T;            // the MMAs' type
+    using Ops = MmaOps<MT>;
+    using Tile = Tile16<CT, D>;
+    constexpr int MD = D / 16;                      // O^T row tiles
+    const SelectParams& p = sp.sel;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ SelShared sh;
+    __shared__ Joined joined;
+    __shared__ float wm[kSelWarps][8], wl[kSelWarps][8], q_unit[8];
+    int32_t* list = reinterpret_cast<int32_t*>(dyn);                   // the row's slabs
+    uint4* qf = reinterpret_cast<uint4*>(dyn + sp.list_bytes);         // query fragments: D * 16 bytes
+    uint8_t* work = dyn + sp.list_bytes + 16 * D;                      // selection, then the warps' O
+    cg::cluster_group cluster = cg::this_cluster();
+    const SelRow rw(p, cluster, work);
+    const int C = rw.C;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int G = p.group, B = p.block_size;
+    QT* out = static_cast<QT*>(sp.out) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
+
+    // query fragments: head g's elements as the keys' chunks hold them
+    const QT* query = static_cast<const QT*>(p.query) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
+    if constexpr (!kFp8) {
+        for (int i = threadIdx.x; i < D; i += kSelThreads) {           // [step][lane], 32 elements a step
+            const int hd = (i & 31) >> 2, e = 32 * (i >> 5) + 8 * (i & 3);
+            qf[i] = hd < G ? *reinterpret_cast<const uint4*>(query + hd * D + e) : make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        // per head: a power of two that brings the largest magnitude into [1, 2)
+        if (warp < 8) {
+            float mx = 0.f;
+            if (warp < G)
+                for (int e = lane; e < D; e += 32) mx = fmaxf(mx, fabsf(to_float(query[warp * D + e])));
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+            // 2^exponent, kept to the range whose reciprocal is a normal number
+            const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
+            if (lane == 0) q_unit[warp] = mx > 0.f && mx < INFINITY ? __uint_as_float(e << 23) : 1.f;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kSelThreads) {           // [step][lane][2], 64 elements a step
+            const int part = i & 1, l = (i >> 1) & 31;
+            const int hd = l >> 2, e = 64 * (i >> 6) + 16 * (l & 3) + 8 * part;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (hd < G) {
+                float x[8];
+                RowLoader<QT, 8>::load(query + hd * D + e, x);
+                const float r = 1.f / q_unit[hd];                      // exact
+                // a word of codes (4) meets elements (0, 2) and (1, 3)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    w[2 * k] = Ops::pack(x[4 * k] * r, x[4 * k + 2] * r);
+                    w[2 * k + 1] = Ops::pack(x[4 * k + 1] * r, x[4 * k + 3] * r);
+                }
+            }
+            qf[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+
+    // ------------------------------------------------------------ selection
+    const uint32_t thr = score_and_decide<QT, D, true>(p, sh, cluster, rw);
+    int32_t* selected = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
+    const int total = rw.n < p.num_select ? rw.n : p.num_select;
+    if (rw.rank == 0 || rw.all) {                   // with every block taken each CTA lists them itself
+        for_taken(p, sh, rw, thr, [&](int at, int b) { list[at] = b; });
+        __syncthreads();
+        for (int i = threadIdx.x; i < total; i += kSelThreads) {
+            const int b = list[i];
+            const int slab = slab_of(p, rw, b);
+            if (rw.rank == 0) {
+                if (selected) selected[i] = b;
+                if (slab < 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+            }
+            list[i] = slab;
+        }
+        if (rw.rank == 0 && selected)
+            for (int i = total + threadIdx.x; i < p.num_select; i += kSelThreads) selected[i] = -1;
+    }
+    if (C > 1 && !rw.all) {
+        cluster.sync();
+        if (rw.rank != 0) {
+            const int32_t* first = cluster.map_shared_rank(list, 0);
+            for (int i = threadIdx.x; i < total; i += kSelThreads) list[i] = first[i];
+        }
+    }
+    __syncthreads();
+
+    // ------------------------------------------------------------ attention
+    const int len = total * B - (rw.n * B - rw.L);  // the selection's tokens
+    const int tiles = (len + 15) / 16;
+    const int per_block = B / 16;                   // B is a multiple of 16
+    float acc[MD][4];
+#pragma unroll
+    for (int i = 0; i < MD; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    const float unit0 = kFp8 && 2 * t4 < G ? q_unit[2 * t4] : 1.f;
+    const float unit1 = kFp8 && 2 * t4 + 1 < G ? q_unit[2 * t4 + 1] : 1.f;
+    const float q_mul[2] = {sp.q_mul * unit0, sp.q_mul * unit1};
+
+    Tile tl;
+    constexpr int kRowBytes = D * (int)sizeof(CT);
+    // byte offset of a tile's first token in the caches; -1: no such block
+    auto tile_at = [&](int tile) -> int64_t {
+        const int j = per_block == 1 ? tile : tile / per_block;
+        const int slab = list[j];
+        return slab < 0 ? -1 : ((int64_t)slab * B + (tile - j * per_block) * 16) * kRowBytes;
+    };
+    auto load_keys = [&](int64_t at) {
+        const uint8_t* k = static_cast<const uint8_t*>(sp.k_cache) + (at < 0 ? 0 : at) + g * kRowBytes + 16 * t4;
+#pragma unroll
+        for (int j = 0; j < Tile::KJ; ++j) {
+            tl.x[j] = __ldg(reinterpret_cast<const uint4*>(k + 64 * j));
+            tl.y[j] = __ldg(reinterpret_cast<const uint4*>(k + 8 * kRowBytes + 64 * j));
+        }
+    };
+    // rows from nvalid on are zeroed: their weights are 0, and 0 x NaN is not
+    auto load_values = [&](int64_t at, int nvalid) {
+        const uint8_t* v = static_cast<const uint8_t*>(sp.v_cache) + (at < 0 ? 0 : at);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tok = 2 * t4 + (r & 1) + 8 * (r >> 1);
+            const uint8_t* row = v + tok * kRowBytes;
+            const bool there = tok < nvalid;
+            if constexpr (kFp8) {
+                typename Tile::VWord w{};
+                if (there) w = __ldg(reinterpret_cast<const typename Tile::VWord*>(row + g * (D / 8)));
+                tl.v[r] = w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < Tile::VU; ++u) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (there) w = __ldg(reinterpret_cast<const uint4*>(row + 128 * u + 16 * g));
+                    tl.v[r][u] = w;
+                }
+            }
+        }
+    };
+    const int stride = C * kSelWarps;
+    int tile = rw.rank * kSelWarps + warp;
+    int64_t at = -1;
+    int nvalid = 0;
+    auto valid_of = [&](int64_t a, int tile) { return a < 0 ? 0 : min(16, len - tile * 16); };
+    if (tile < tiles) {
+        at = tile_at(tile);
+        nvalid = valid_of(at, tile);
+        load_keys(at);
+        load_values(at, nvalid);
+    }
+    while (tile < tiles) {
+        // ---- scores: tokens g, g + 8 x heads 2 t4, 2 t4 + 1
+        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kFp8) {
+#pragma unroll
+            for (int j = 0; j < Tile::KJ; ++j)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint4 q = qf[(j * 32 + lane) * 2 + part];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t wx = word_of(tl.x[j], 2 * part + k), wy = word_of(tl.y[j], 2 * part + k);
+                        const uint32_t a[4] = {widen_even(wx), widen_even(wy), widen_odd(wx), widen_odd(wy)};
+                        Ops::mma(sc, a, k ? q.z : q.x, k ? q.w : q.y);
+                    }
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < Tile::KJ; ++j) {
+                const uint4 q = qf[j * 32 + lane];
+                const uint32_t a0[4] = {tl.x[j].x, tl.y[j].x, tl.x[j].y, tl.y[j].y};
+                const uint32_t a1[4] = {tl.x[j].z, tl.y[j].z, tl.x[j].w, tl.y[j].w};
+                Ops::mma(sc, a0, q.x, q.y);
+                Ops::mma(sc, a1, q.z, q.w);
+            }
+        }
+        const int next = tile + stride;
+        const int64_t next_at = next < tiles ? tile_at(next) : -1;
+        if (next < tiles) load_keys(next_at);
+
+        // ---- softmax weights
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = sc[i] * q_mul[i & 1];
+            sc[i] = g + 8 * (i >> 1) < nvalid ? v : -INFINITY;         // select, never multiply
+            over |= sc[i] > m_ref[i & 1] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+            float alpha[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = fmaxf(sc[j], sc[j + 2]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float m_new = fmaxf(m_ref[j], mx);
+                alpha[j] = m_new == -INFINITY ? 1.f : (m_ref[j] == -INFINITY ? 0.f : fast_exp2(m_ref[j] - m_new));
+                m_ref[j] = m_new;
+                l_run[j] *= alpha[j];
+            }
+#pragma unroll
+            for (int i = 0; i < MD; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] *= alpha[j & 1];
+        }
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float w0 = sc[2 * r] == -INFINITY ? 0.f : fast_exp2(sc[2 * r] - m_ref[0]);
+            const float w1 = sc[2 * r + 1] == -INFINITY ? 0.f : fast_exp2(sc[2 * r + 1] - m_ref[1]);
+            const uint32_t h = Ops::pack(w0, w1);
+            const float2 hf = Ops::unpack(h);
+            if constexpr (kFp8) {
+                l_run[0] += hf.x;
+                l_run[1] += hf.y;
+            } else {
+                const uint32_t l = Ops::pack(w0 - hf.x, w1 - hf.y);
+                const float2 lf = Ops::unpack(l);
+                l_run[0] += hf.x + lf.x;
+                l_run[1] += hf.y + lf.y;
+                lo[r] = movmatrix_trans(l);
+            }
+            hi[r] = movmatrix_trans(h);
+        }
+
+        // ---- O^T += V^T P^T
+        if constexpr (kFp8) {
+#pragma unroll
+            for (int i = 0; i < MD; ++i) {
+                // codes 2 i and 2 i + 1 of each token's chunk: rows g and g + 8
+                const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
+                const uint32_t v01 = __byte_perm(word_of(tl.v[0], i / 2), word_of(tl.v[1], i / 2), sel);
+                const uint32_t v23 = __byte_perm(word_of(tl.v[2], i / 2), word_of(tl.v[3], i / 2), sel);
+                const uint32_t a[4] = {widen_even(v01), widen_odd(v01), widen_even(v23), widen_odd(v23)};
+                Ops::mma(acc[i], a, hi[0], hi[1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MD; ++i) {
+                const int u = i / 4, w = i % 4;
+                const uint32_t v0 = word_of(tl.v[0][u], w), v1 = word_of(tl.v[1][u], w);
+                const uint32_t v2 = word_of(tl.v[2][u], w), v3 = word_of(tl.v[3][u], w);
+                const uint32_t a[4] = {__byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632),
+                                       __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632)};
+                Ops::mma(acc[i], a, hi[0], hi[1]);
+                Ops::mma(acc[i], a, lo[0], lo[1]);
+            }
+        }
+        tile = next;
+        if (tile < tiles) {
+            at = next_at;
+            nvalid = valid_of(at, tile);
+            load_values(at, nvalid);
+        }
+    }
+
+    // ------------------------------------------------------------ join the warps
+    // O of a warp: [head][D + 4] (the padding spreads the heads over the banks)
+    constexpr int kPitch = D + 4;
+    float* wo = reinterpret_cast<float*>(work);
+    __syncthreads();                                // the selection's use of this memory is over
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], m);
+        const int hd = 2 * t4 + j;
+        if (g == 0) {
+            wm[warp][hd] = m_ref[j];
+            wl[warp][hd] = l_run[j];
+        }
+        float* o = wo + (warp * 8 + hd) * kPitch;
+#pragma unroll
+        for (int i = 0; i < MD; ++i) {
+            const int d = kFp8 ? (D / 8) * g + 2 * i : 64 * (i / 4) + 8 * g + 2 * (i % 4);
+            *reinterpret_cast<float2*>(o + d) = make_float2(acc[i][j], acc[i][2 + j]);
+        }
+    }
+    __syncthreads();
+    // elements d, d + 1 of head hd: the sum over the warps, relative to the CTA's maximum
+    const float* jo_base = wo;
+    for (int e = threadIdx.x; e < G * (D / 2); e += kSelThreads) {
+        const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) M = fmaxf(M, wm[w][hd]);
+        float l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) {
+            const float f = wm[w][hd] == -INFINITY ? 0.f : fast_exp2(wm[w][hd] - M);
+            const float2 o = *reinterpret_cast<const float2*>(jo_base + (w * 8 + hd) * kPitch + d);
+            l += f * wl[w][hd];
+            o0 += f * o.x;
+            o1 += f * o.y;
+        }
+        if (C == 1) {
+            const float r = l > 0.f || l != l ? sp.v_mul / l : 0.f;    // no tokens: zero; NaN stays
+            out[hd * D + d] = from_float<QT>(o0 * r);
+            out[hd * D + d + 1] = from_float<QT>(o1 * r);
+        } else {
+            // into warp 0's place, which only this thread reads for these elements
+            *reinterpret_cast<float2*>(wo + hd * kPitch + d) = make_float2(o0, o1);
+            if (d == 0) {
+                joined.m[hd] = M;
+                joined.l[hd] = l;
+            }
+        }
+    }
+    if (C == 1) return;
+    cluster.sync();
+    // ------------------------------------------------------------ join the CTAs
+    for (int e = rw.rank * kSelThreads + threadIdx.x; e < G * (D / 2); e += C * kSelThreads) {
+        const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
+        float M = -INFINITY;
+        for (int r = 0; r < C; ++r) M = fmaxf(M, cluster.map_shared_rank(&joined, r)->m[hd]);
+        float l = 0.f, o0 = 0.f, o1 = 0.f;
+        for (int r = 0; r < C; ++r) {
+            const Joined* jr = cluster.map_shared_rank(&joined, r);
+            const float2 o = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + hd * kPitch + d, r));
+            const float f = jr->m[hd] == -INFINITY ? 0.f : fast_exp2(jr->m[hd] - M);
+            l += f * jr->l[hd];
+            o0 += f * o.x;
+            o1 += f * o.y;
+        }
+        const float r = l > 0.f || l != l ? sp.v_mul / l : 0.f;
+        out[hd * D + d] = from_float<QT>(o0 * r);
+        out[hd * D + d + 1] = from_float<QT>(o1 * r);
+    }
+    cluster.sync();                                 // no CTA leaves while its memory is read
+}
+
+template <typename QT, typename CT, int D>
+cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
+    const int rows = sp.sel.num_seqs * sp.sel.num_kv_heads;
+    const int C = select_cluster(rows, sp.sel.max_ctx_blocks);
+    const int select = select_smem<QT, D>(sp.sel);
+    const int join = kSelWarps * 8 * (D + 4) * (int)sizeof(float);
+    sp.list_bytes = (sp.sel.table_width * 4 + 15) / 16 * 16;
+    const int smem = sp.list_bytes + 16 * D + (select > join ? select : join);
+    constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
+    if (kFp8) {
+        sp.q_mul *= 256.f;                          // codes are widened times 2^-8
+        sp.v_mul *= 256.f;
+    }
+    return launch_cluster(sparse_decode_kernel<QT, CT, D>, sp, rows * C, C, smem, stream);
+}
+
+template <typename QT, typename CT>
+cudaError_t launch_sparse_d(const SparseParams& sp, int head_size, cudaStream_t stream) {
+    return head_size == 64 ? launch_sparse<QT, CT, 64>(sp, stream) : launch_sparse<QT, CT, 128>(sp, stream);
+}
+
+}  // namespace
+
+// Shapes of the fused kernel: 16-bit query, one MMA tile of heads, whole
+// 16-token tiles per block, head sizes whose accumulators leave registers for
+// loads in flight (256 does not), and a selection that fits shared memory.
+bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width) {
+    return (q_dtype == PA_F16 || q_dtype == PA_BF16) && group <= 8 && head_size <= 128 &&
+           block_size % 16 == 0 && table_width <= 8192;
+}
+
+cudaError_t launch_sparse_decode(const SparseParams& sp, int head_size, pa_dtype q_dtype,
+                                 pa_dtype cache_dtype, cudaStream_t stream) {
+    if (cache_dtype == PA_FP8_E4M3)
+        return q_dtype == PA_F16 ? launch_sparse_d<__half, e4m3_t>(sp, head_size, stream)
+                                 : launch_sparse_d<__nv_bfloat16, e4m3_t>(sp, head_size, stream);
+    return q_dtype == PA_F16 ? launch_sparse_d<__half, __half>(sp, head_size, stream)
+                             : launch_sparse_d<__nv_bfloat16, __nv_bfloat16>(sp, head_size, stream);
+}
+
+}  // namespace pagedkv

@@ -1,0 +1,804 @@
+// sparse_select.cuh -- which blocks a block-sparse decode reads. For a sequence
+// of n blocks and each KV head h,
+//     score(b) = max over the group's query heads g of
+//                sum_d max(q_gd lo_bd, q_gd hi_bd),
+// the largest value q_g . k can take for keys within block b's bounds. The
+// first `first_blocks` and the newest `recent_blocks` blocks are always taken;
+// of the others the num_select - first - recent of largest score (ties: the
+// lowest index; a NaN score counts as +infinity, so that a NaN key is read and
+// shows, as it would in the dense decode). n <= num_select: every block.
+//
+// The result is defined by the exact order of the scores. Almost every block's
+// place is clear at far lower precision, so there are two steps:
+//  - approximate scores on warp-level MMAs. max(q lo, q hi) = min(q,0) lo +
+//    max(q,0) hi, so a block's scores for all heads are one product of its
+//    bounds, read as one row of 2 D elements, with the query's two sides:
+//    16 blocks x 2 D by 2 D x 8 heads. The products are exact in binary32; the
+//    sums are taken to err by at most kScoreEps times sum |q_d bound_d|, which
+//    a second product of the magnitudes gives.
+//  - the threshold among those scores, from a histogram over their range.
+//    Blocks whose distance to the other side of the threshold exceeds both
+//    errors are settled; the rest (usually none) are scored again in binary64
+//    and ranked. Where the histogram's bin at the threshold holds too many
+//    blocks (equal scores) or a score is not finite, a search over the key
+//    bits takes its place.
+// A cluster of CTAs takes one (sequence, KV head): all score, into the first
+// CTA's shared memory, and the first one selects. Reading the bounds once
+// (2 D elements per block) bounds the kernel for batches, the latency of the
+// score-search-emit chain for few rows.
+//
+// Shared by the fused kernel (sparse_decode.cu) and the selection kernel whose
+// slab tables the paged decode reads (sparse_select.cu).
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "decode_mma.cuh"
+#include "launch.h"
+
+namespace pagedkv {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kRankList = kSelThreads;  // blocks ranked in shared memory, one per thread
+constexpr int kBins = 4 * kSelThreads;  // of the score histogram
+// Keys of up to this many blocks are kept in shared memory (two CTAs per SM);
+// longer contexts' in the workspace.
+constexpr int kSmemKeys = 24 * 1024;
+// |approximate - exact score| <= kScoreEps * sum_d |q_d bound_d|. An MMA adds 16
+// exact products to its accumulator; taking each of the 17 terms to lose up to
+// 2^-23 of the largest, a chain of four MMAs errs by at most 4 * 17 * 2^-23 of
+// its own terms' magnitudes, and so do all chains together (chains are joined
+// in binary32, eight additions at most). That is below 2^-16.8; 2^-16 leaves a
+// factor of 1.7. Binary32 queries (a sum of 8 + 5 terms a lane and across) are
+// well inside it.
+constexpr float kScoreEps = 1.0f / 65536;
+
+// The sequence's length as the decode takes it (clamped to what the table and
+// the bound allow).
+__device__ __forceinline__ int clamped_len(const SelectParams& p, int s, bool& bad) {
+    const int L = p.context_lens[s];
+    const int64_t tab = (int64_t)p.max_blocks * p.block_size;
+    const int cap = tab < p.max_context_len ? (int)tab : p.max_context_len;
+    bad = L < 0 || L > cap;
+    return L < 0 ? 0 : (L > cap ? cap : L);
+}
+
+__device__ __forceinline__ uint32_t ordered(float x) {        // the order of the values
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);   // -0 and 0 are one value
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t ordered64(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
+    return u >> 63 ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The two sides of eight query elements: min(x, 0) or max(x, 0), NaN kept.
+template <typename T>
+__device__ __forceinline__ uint32_t side2(uint32_t w, bool positive) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 x = *reinterpret_cast<const __half2*>(&w);
+        const __half2 z = __float2half2_rn(0.f);
+        const __half2 y = positive ? __hmax2_nan(x, z) : __hmin2_nan(x, z);
+        return *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w);
+        const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+        const __nv_bfloat162 y = positive ? __hmax2_nan(x, z) : __hmin2_nan(x, z);
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
+// A block's score for one head of the group in binary64, by one warp, as an
+// ordered key (NaN as +infinity).
+template <typename T, int D>
+__device__ uint64_t exact_head_score(const SelectParams& p, int s, int h, int g, int64_t blk, int lane) {
+    constexpr int E = D / 32;
+    if (blk < 0 || blk >= p.num_blocks) return ordered64(-INFINITY);
+    const T* bounds = static_cast<const T*>(p.k_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
+    float lo[E], hi[E], q[E];
+    RowLoader<T, E>::load(bounds, lo);
+    RowLoader<T, E>::load(bounds + D, hi);
+    RowLoader<T, E>::load(static_cast<const T*>(p.query) +
+                          ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) sum += (double)q[i] * (double)(q[i] < 0.f ? lo[i] : hi[i]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    return ordered64(isnan(sum) ? INFINITY : sum);
+}
+
+// The same over all heads of the group.
+template <typename T, int D>
+__device__ uint64_t exact_score(const SelectParams& p, int s, int h, int64_t blk, int lane) {
+    uint64_t best = 0;
+    for (int g = 0; g < p.group; ++g) {
+        const uint64_t x = exact_head_score<T, D>(p, s, h, g, blk, lane);
+        best = x > best ? x : best;
+    }
+    return best;
+}
+
+// Sixteen blocks' bounds rows, four 64-byte steps (a quarter: 128 elements) at
+// a time: this lane's 16-byte chunks of blocks g and g + 8.
+struct Quarter {
+    uint4 x[4], y[4];
+    template <typename T>
+    __device__ __forceinline__ void load(const T* x_row, const T* y_row) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = __ldg(reinterpret_cast<const uint4*>(x_row + 32 * j));
+            y[j] = __ldg(reinterpret_cast<const uint4*>(y_row + 32 * j));
+        }
+    }
+};
+
+// Adds a quarter's products with the query sides (this lane's chunks, 32 lanes
+// apart) to the scores c and magnitudes m: lane (g, t4) holds blocks g and
+// g + 8, heads 2 t4 and 2 t4 + 1. A lane's eight consecutive elements stand
+// for k = 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of two MMAs, in the bounds and the
+// sides alike, so both are loaded as 16-byte vectors.
+template <typename T>
+__device__ __forceinline__ void add_quarter(const Quarter& b, const uint4* sides, float (&c)[4],
+                                            float (&m)[4]) {
+    using Ops = MmaOps<T>;
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 q = sides[32 * j];
+        const uint32_t a0[4] = {b.x[j].x, b.y[j].x, b.x[j].y, b.y[j].y};
+        const uint32_t a1[4] = {b.x[j].z, b.y[j].z, b.x[j].w, b.y[j].w};
+        Ops::mma(c0, a0, q.x, q.y);
+        Ops::mma(c1, a1, q.z, q.w);
+        const uint32_t b0[4] = {a0[0] & kAbs, a0[1] & kAbs, a0[2] & kAbs, a0[3] & kAbs};
+        const uint32_t b1[4] = {a1[0] & kAbs, a1[1] & kAbs, a1[2] & kAbs, a1[3] & kAbs};
+        Ops::mma(m, b0, q.x & kAbs, q.y & kAbs);
+        Ops::mma(m, b1, q.z & kAbs, q.w & kAbs);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += c0[i] + c1[i];
+}
+
+struct SelShared {
+    float err[kMaxCluster];             // per CTA: the largest sum of magnitudes,
+    float lowest[kMaxCluster];          // and the range of its finite scores
+    float highest[kMaxCluster];
+    int bins[kBins];
+    int bin;                            // the threshold's, and the candidates above it
+    int above;
+    int part[2][kSelWarps];             // count(): per-warp sums, double-buffered
+    float fpart[3][kSelWarps];
+    int list_n;
+    int list[kRankList];
+    float list_score[kRankList];
+    uint64_t list_key[kRankList];
+};
+
+// Sum over the CTA; one barrier (`turn` alternates the buffer).
+__device__ __forceinline__ int cta_sum(SelShared& sh, int x, int& turn) {
+    const int w = __reduce_add_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0) sh.part[turn][threadIdx.x >> 5] = w;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int y = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? sh.part[turn][lane] : 0);
+    turn ^= 1;
+    return y;
+}
+
+// The largest P with count(key >= P) >= want over the candidates that `key`
+// gives (i strided over the threads; skip(i) leaves one out). exact: whether
+// count(key >= P) == want.
+template <typename K, typename Key, typename Skip>
+__device__ __forceinline__ K kth_largest(SelShared& sh, int n, int want, int& turn, bool& exact,
+                                         Key key, Skip skip) {
+    K prefix = 0;
+    exact = false;
+    for (int bit = (int)sizeof(K) * 8 - 1; bit >= 0; --bit) {
+        const K cand = prefix | ((K)1 << bit);
+        int c = 0;
+        for (int i = threadIdx.x; i < n; i += kSelThreads) c += !skip(i) && key(i) >= cand;
+        const int total = cta_sum(sh, c, turn);
+        if (total >= want) prefix = cand;
+        if (total == want) {
+            exact = true;
+            break;
+        }
+    }
+    return prefix;
+}
+
+// The score that ordered() puts below every value: a block not taken.
+__device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu); }
+
+// The taken candidates, where a histogram of the approximate scores over their
+// range leaves few blocks near the threshold: thr such that they are those of
+// ordered(keys[i]) >= thr (undecided blocks' keys are replaced). False: not
+// decided here, and keys are as they were.
+template <typename T, int D>
+__device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, float* keys, int nc,
+                                       int want, float mag, int C, int s, int h,
+                                       const int32_t* table, uint32_t& thr) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float lowest = sh.lowest[0], highest = sh.highest[0];
+    for (int r = 1; r < C; ++r) {
+        lowest = fminf(lowest, sh.lowest[r]);
+        highest = fmaxf(highest, sh.highest[r]);
+    }
+    // err2: both errors, and the rounding of k +- err2 below (2^-24 of k <= mag)
+    const float err2 = mag * (2.f * kScoreEps * 1.01f);
+    const float scale = (float)(kBins - 1) / (highest - lowest);
+    if (!(isfinite(mag) && highest > lowest && isfinite(scale))) return false;
+    // non-decreasing in k; blocks the table does not name score -infinity: bin 0
+    auto bin_of = [&](float k) {
+        const int b = __float2int_rz((k - lowest) * scale);
+        return b < 0 ? 0 : (b >= kBins ? kBins - 1 : b);
+    };
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.bins[i] = 0;
+    if (threadIdx.x == 0) sh.list_n = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nc; i += kSelThreads) atomicAdd(&sh.bins[bin_of(keys[i])], 1);
+    __syncthreads();
+    // the bin where the count from the top reaches want: thread t has the four
+    // bins below kBins - 4 t
+    {
+        const int top = kBins - 1 - 4 * (int)threadIdx.x;
+        int c[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += c[j] = sh.bins[top - j];
+        int run = sum;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, m);
+            if (lane >= m) run += v;
+        }
+        if (lane == 31) sh.part[0][warp] = run;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) run += sh.part[0][w];
+        int before = run - sum;
+        if (before < want && run >= want) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < want && before + c[j] >= want) {
+                    sh.bin = top - j;
+                    sh.above = before;
+                }
+                before += c[j];
+            }
+        }
+    }
+    __syncthreads();
+    // Every block that can change sides is within err2 of the threshold's bin.
+    const int bin = sh.bin;
+    int below_bin_near = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+        const float k = keys[i];
+        if (bin_of(k + err2) >= bin && bin_of(k - err2) <= bin) {
+            const int at = atomicAdd(&sh.list_n, 1);
+            if (at < kRankList) {
+                sh.list[at] = i;
+                sh.list_score[at] = k;
+            }
+            below_bin_near += bin_of(k) > bin;                 // counted above, but not settled
+        }
+    }
+    __syncthreads();
+    const int m = sh.list_n;
+    if (m > kRankList) return false;
+    int turn = 0;
+    const int left = want - (sh.above - cta_sum(sh, below_bin_near, turn));   // the list's places
+    // rank by approximate score (the list's order varies, the ranks do not)
+    const int e = threadIdx.x;
+    const bool mine = e < m;
+    const float k = mine ? sh.list_score[e] : 0.f;
+    const int i = mine ? sh.list[e] : 0;
+    int before = 0;
+    if (mine)
+        for (int o = 0; o < m; ++o)
+            before += sh.list_score[o] > k || (sh.list_score[o] == k && sh.list[o] < i);
+    const bool in = mine && before < left;
+    float a = in ? k : INFINITY, b = mine && !in ? k : -INFINITY;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
+    }
+    if (lane == 0) {
+        sh.fpart[0][warp] = a;
+        sh.fpart[1][warp] = b;
+    }
+    __syncthreads();
+    for (int w = 0; w < kSelWarps; ++w) {
+        a = fminf(a, sh.fpart[0][w]);
+        b = fmaxf(b, sh.fpart[1][w]);
+    }
+    bool take = in;
+    if (a - b <= err2) {
+        // the blocks within err2 of the other side, in binary64
+        const bool open = mine && (in ? k <= b + err2 : k >= a - err2);
+        if (mine) sh.list_key[e] = open ? 1 : 0;               // below every key of a score
+        __syncthreads();
+        for (int w = warp; w < m * p.group; w += kSelWarps) {  // a warp per (block, head)
+            const int o = w / p.group;
+            if (sh.list_key[o] == 0) continue;
+            const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
+            if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
+        }
+        __syncthreads();
+        if (open) {
+            int places = left, ahead = 0;
+            const uint64_t x = sh.list_key[e];
+            for (int o = 0; o < m; ++o) {
+                const uint64_t y = sh.list_key[o];
+                if (y == 0) places -= sh.list_score[o] >= a;   // settled inside
+                else ahead += y > x || (y == x && sh.list[o] < i);
+            }
+            take = ahead < places;
+        }
+    }
+    __syncthreads();
+    if (mine) keys[i] = take ? INFINITY : out_key();
+    thr = ordered(a);
+    __syncthreads();
+    return true;
+}
+
+// One (sequence, KV head) of the batch, as every CTA of its cluster sees it.
+struct SelRow {
+    int row, s, h;                      // row = s * num_kv_heads + h
+    int L, n;                           // tokens, blocks
+    int C, rank;                        // CTAs of the cluster, this one's
+    int lo, nc, want;                   // candidates lo .. lo + nc - 1, and how many are taken
+    bool all, scored;
+    const int32_t* table;
+    uint4* sides;                       // [n-tile][step][lane]
+    float* keys;                        // the candidates' scores (of the first CTA, or in memory)
+
+    __device__ __forceinline__ SelRow(const SelectParams& p, cg::cluster_group& cluster, uint8_t* smem) {
+        C = (int)cluster.num_blocks();
+        rank = (int)cluster.block_rank();
+        row = blockIdx.x / C;
+        s = row / p.num_kv_heads;
+        h = row - s * p.num_kv_heads;
+        bool bad;
+        L = clamped_len(p, s, bad);
+        if (bad && h == 0 && rank == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_LEN);
+        n = (L + p.block_size - 1) / p.block_size;
+        table = p.block_tables + (size_t)s * p.max_blocks;
+        all = n <= p.num_select;
+        want = p.num_select - p.first_blocks - p.recent_blocks;
+        lo = p.first_blocks;
+        nc = all ? 0 : n - p.recent_blocks - lo;
+        scored = nc > 0 && want > 0;
+        sides = reinterpret_cast<uint4*>(smem);
+        keys = p.keys_in_smem ? reinterpret_cast<float*>(smem + p.side_bytes)
+                              : p.scores + (size_t)row * p.max_ctx_blocks;
+    }
+};
+
+// Scores the candidates (all CTAs of the cluster) and finds the threshold (the
+// first): there, and only there, candidate i is taken if ordered(keys[i]) is
+// at least the result. All CTAs meet at two cluster barriers if row.scored,
+// else at none. kOneTile: groups of at most eight heads, one MMA tile.
+template <typename T, int D, bool kOneTile>
+__device__ uint32_t score_and_decide(const SelectParams& p, SelShared& sh, cg::cluster_group& cluster,
+                                     const SelRow& rw) {
+    if (!rw.scored) return 0;
+    constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
+    constexpr int NQ = STEPS / 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int C = rw.C, rank = rw.rank, row = rw.row, s = rw.s, h = rw.h;
+    const int nc = rw.nc, want = rw.want, lo = rw.lo;
+    const int32_t* table = rw.table;
+    uint4* sides = rw.sides;
+    float* keys = rw.keys;
+    {
+        // ------------------------------------------------ approximate scores
+        cluster.sync();                                        // the first CTA runs: its memory may be written
+        float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(keys, 0) : keys;
+        float worst = 0.f, lowest = INFINITY, highest = -INFINITY;
+        if constexpr (std::is_same<T, float>::value) {
+            constexpr int E = D / 32;
+            for (int i = rank * kSelWarps + warp; i < nc; i += C * kSelWarps) {
+                const int64_t blk = table[lo + i];
+                float best = -INFINITY;
+                if (blk >= 0 && blk < p.num_blocks) {
+                    const float* bounds = static_cast<const float*>(p.k_bounds) +
+                                          ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
+                    float bl[E], bh[E], q[E];
+                    RowLoader<float, E>::load(bounds, bl);
+                    RowLoader<float, E>::load(bounds + D, bh);
+                    for (int g = 0; g < p.group; ++g) {
+                        RowLoader<float, E>::load(static_cast<const float*>(p.query) +
+                                                  ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
+                        float sum = 0.f, mag = 0.f;
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            const float t = q[j] * (q[j] < 0.f ? bl[j] : bh[j]);
+                            sum += t;
+                            mag += fabsf(t);
+                        }
+#pragma unroll
+                        for (int m = 16; m > 0; m >>= 1) {
+                            sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                            mag += __shfl_xor_sync(0xffffffffu, mag, m);
+                        }
+                        best = fmaxf(best, sum);
+                        worst = max_nan(worst, mag);
+                    }
+                    lowest = fminf(lowest, best);
+                    highest = fmaxf(highest, best);
+                }
+                if (lane == 0) out_keys[i] = best;
+            }
+        } else {
+            const int ntiles = (p.group + 7) / 8;
+            for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += kSelThreads) {
+                const int l = i & 31, j = (i >> 5) % STEPS, nt = i / (32 * STEPS);
+                const int g = nt * 8 + (l >> 2);
+                const int e = 32 * j + 8 * (l & 3);
+                const bool positive = e >= D;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (g < p.group) {
+                    w = *reinterpret_cast<const uint4*>(
+                        static_cast<const T*>(p.query) +
+                        ((size_t)s * p.num_q_heads + h * p.group + g) * D + (positive ? e - D : e));
+                    w = make_uint4(side2<T>(w.x, positive), side2<T>(w.y, positive),
+                                   side2<T>(w.z, positive), side2<T>(w.w, positive));
+                }
+                sides[i] = w;
+            }
+            __syncthreads();
+            const int g = lane >> 2, t4 = lane & 3;
+            const int tiles = (nc + 15) / 16;
+            const int stride = C * kSelWarps;
+            // this lane's two blocks of a tile, and their bounds rows (block 0's
+            // where the table names none)
+            auto block_of = [&](int tile, int r) {
+                const int i = tile * 16 + g + 8 * r;
+                return table[lo + (i < nc ? i : nc - 1)];
+            };
+            auto there = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
+            auto row_of = [&](int blk) {
+                return static_cast<const T*>(p.k_bounds) +
+                       ((size_t)(there(blk) ? blk : 0) * p.num_kv_heads + h) * 2 * D + 8 * t4;
+            };
+            auto finish = [&](int tile, const int (&blk)[2], float (&best)[2], float (&mag)[2]) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+                    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+                    const int i = tile * 16 + g + 8 * r;
+                    const bool ok = there(blk[r]);
+                    if (ok) {
+                        worst = max_nan(worst, mag[r]);
+                        lowest = fminf(lowest, best[r]);
+                        highest = fmaxf(highest, best[r]);
+                    }
+                    if (t4 == 0 && i < nc) out_keys[i] = ok ? best[r] : -INFINITY;
+                }
+            };
+            // maxima over the heads of one MMA tile
+            auto over_heads = [&](int nt, const float (&c)[4], const float (&m)[4], float (&best)[2], float (&mag)[2]) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (nt * 8 + 2 * t4 + e < p.group) {
+                            best[r] = fmaxf(best[r], c[2 * r + e]);
+                            mag[r] = max_nan(mag[r], m[2 * r + e]);
+                        }
+            };
+            int tile = rank * kSelWarps + warp;
+            if constexpr (kOneTile) {
+                // the next quarter's loads are in flight while one is multiplied
+                Quarter buf[2];
+                int blk[2];
+                const T *x = nullptr, *y = nullptr;
+                if (tile < tiles) {
+                    blk[0] = block_of(tile, 0);
+                    blk[1] = block_of(tile, 1);
+                    x = row_of(blk[0]);
+                    y = row_of(blk[1]);
+                    buf[0].load(x, y);
+                }
+                for (; tile < tiles; tile += stride) {
+                    const int next = tile + stride < tiles ? tile + stride : tile;
+                    const int nblk[2] = {block_of(next, 0), block_of(next, 1)};
+                    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (q + 1 < NQ) {
+                            buf[(q + 1) & 1].load(x + 128 * (q + 1), y + 128 * (q + 1));
+                        } else {
+                            x = row_of(nblk[0]);
+                            y = row_of(nblk[1]);
+                            if (next != tile) buf[(q + 1) & 1].load(x, y);
+                        }
+                        add_quarter<T>(buf[q & 1], sides + 128 * q + lane, c, m);
+                    }
+                    if (NQ == 1) buf[0] = buf[1];
+                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                    over_heads(0, c, m, best, mag);
+                    finish(tile, blk, best, mag);
+                    blk[0] = nblk[0];
+                    blk[1] = nblk[1];
+                }
+            } else {
+                for (; tile < tiles; tile += stride) {
+                    const int blk[2] = {block_of(tile, 0), block_of(tile, 1)};
+                    const T *x = row_of(blk[0]), *y = row_of(blk[1]);
+                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                    for (int nt = 0; nt < ntiles; ++nt) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            Quarter b;
+                            b.load(x + 128 * q, y + 128 * q);
+                            add_quarter<T>(b, sides + (nt * STEPS + 4 * q) * 32 + lane, c, m);
+                        }
+                        over_heads(nt, c, m, best, mag);
+                    }
+                    finish(tile, blk, best, mag);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
+            lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, m));
+            highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, m));
+        }
+        if (lane == 0) {
+            sh.fpart[0][warp] = worst;
+            sh.fpart[1][warp] = lowest;
+            sh.fpart[2][warp] = highest;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kSelWarps; ++w) {
+                worst = max_nan(worst, sh.fpart[0][w]);
+                lowest = fminf(lowest, sh.fpart[1][w]);
+                highest = fmaxf(highest, sh.fpart[2][w]);
+            }
+            *cluster.map_shared_rank(&sh.err[rank], 0) = worst;
+            *cluster.map_shared_rank(&sh.lowest[rank], 0) = lowest;
+            *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
+        }
+    }
+    cluster.sync();
+    if (rank != 0) return 0;
+
+    int turn = 0;
+    uint32_t thr = 0;                                          // taken candidates: ordered(key) >= thr
+    float mag = 0.f;
+    for (int r = 0; r < C; ++r) mag = max_nan(mag, sh.err[r]);
+    if (!threshold_by_histogram<T, D>(p, sh, keys, nc, want, mag, C, s, h, table + lo, thr)) {
+        const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
+        const bool finite = isfinite(mag);
+        // Settled blocks: those that beat (or lose to) every block on the other
+        // side of the threshold by more than both errors. in_above: taken for
+        // certain above it; out_below: left out for certain below it.
+        double in_above = INFINITY, out_below = -INFINITY;
+        if (finite) {
+            bool exact;
+            thr = kth_largest<uint32_t>(sh, nc, want, turn, exact, [&](int i) { return ordered(keys[i]); },
+                                        [](int) { return false; });
+            float a = INFINITY, b = -INFINITY;                 // the smallest taken, the largest left out
+            for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+                const float k = keys[i];
+                if (ordered(k) >= thr) a = fminf(a, k);
+                else b = fmaxf(b, k);
+            }
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) {
+                a = fminf(a, __shfl_xor_sync(0xffffffffu, a, m));
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, m));
+            }
+            if (lane == 0) {
+                sh.fpart[0][warp] = a;
+                sh.fpart[1][warp] = b;
+            }
+            __syncthreads();
+            for (int w = 0; w < kSelWarps; ++w) {
+                a = fminf(a, sh.fpart[0][w]);
+                b = fmaxf(b, sh.fpart[1][w]);
+            }
+            if (!exact) b = a;                                 // equal keys across the threshold
+            in_above = (double)b + err2;
+            out_below = (double)a - err2;
+        }
+        const float kOut = out_key();
+        auto settled = [&](float k) { return finite && ((double)k > in_above || (double)k < out_below); };
+        // count the certain ones and the unsettled
+        int in = 0, open = 0;
+        for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+            const float k = keys[i];
+            if (!settled(k)) ++open;
+            else in += (double)k > in_above;
+        }
+        in = cta_sum(sh, in, turn);
+        open = cta_sum(sh, open, turn);
+        const int left = want - in;                            // places for the unsettled
+        if (!finite) thr = ordered(INFINITY);
+        if (left < open) {
+            // ------------------------------------------- exact scores of the unsettled
+            const bool small = open <= kRankList;
+            if (threadIdx.x == 0) sh.list_n = 0;
+            __syncthreads();
+            uint64_t* exact_keys = p.exact_keys + (size_t)row * p.max_ctx_blocks;
+            for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
+                const bool mine = i0 + lane < nc && !settled(keys[i0 + lane]);
+                uint32_t votes = __ballot_sync(0xffffffffu, mine);
+                while (votes) {
+                    const int i = i0 + __ffs(votes) - 1;
+                    votes &= votes - 1;
+                    const uint64_t k = exact_score<T, D>(p, s, h, table[lo + i], lane);
+                    if (lane == 0) {
+                        if (small) {
+                            const int at = atomicAdd(&sh.list_n, 1);
+                            sh.list[at] = i;
+                            sh.list_key[at] = k;
+                        } else {
+                            exact_keys[i] = k;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            if (small) {
+                // the list's order varies, the ranks do not: (key, index) differ in every pair
+                const int e = threadIdx.x;
+                if (e < open) {
+                    const uint64_t k = sh.list_key[e];
+                    const int i = sh.list[e];
+                    int before = 0;
+                    for (int o = 0; o < open; ++o)
+                        before += sh.list_key[o] > k || (sh.list_key[o] == k && sh.list[o] < i);
+                    keys[i] = before < left ? INFINITY : kOut;
+                }
+            } else if (left > 0) {
+                bool exact;
+                const uint64_t t = kth_largest<uint64_t>(
+                    sh, nc, left, turn, exact, [&](int i) { return exact_keys[i]; },
+                    [&](int i) { return settled(keys[i]); });
+                int above = 0;
+                for (int i = threadIdx.x; i < nc; i += kSelThreads)
+                    above += !settled(keys[i]) && exact_keys[i] > t;
+                above = cta_sum(sh, above, turn);
+                int ties = exact ? 0x7fffffff : left - above;  // places for keys equal to t, lowest first
+                for (int i0 = 0; i0 < nc; i0 += kSelThreads) {
+                    const int i = i0 + threadIdx.x;
+                    const bool mine = i < nc && !settled(keys[i]);
+                    const uint64_t k = mine ? exact_keys[i] : 0;
+                    const bool tie = mine && k == t;
+                    const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+                    if (lane == 0) sh.part[turn][warp] = __popc(votes);
+                    __syncthreads();
+                    int at = __popc(votes & ((1u << lane) - 1)), total = 0;
+                    for (int w = 0; w < kSelWarps; ++w) {
+                        if (w < warp) at += sh.part[turn][w];
+                        total += sh.part[turn][w];
+                    }
+                    turn ^= 1;
+                    if (mine) keys[i] = k > t || (tie && at < ties) ? INFINITY : kOut;
+                    if (!exact) ties -= total < ties ? total : ties;
+                }
+            } else {
+                for (int i = threadIdx.x; i < nc; i += kSelThreads)
+                    if (!settled(keys[i])) keys[i] = kOut;
+            }
+            __syncthreads();
+        } else {
+            // every unsettled block is taken: they are the candidates from out_below on
+            for (int i = threadIdx.x; i < nc; i += kSelThreads)
+                if (!settled(keys[i])) keys[i] = INFINITY;
+            __syncthreads();
+        }
+    }
+    return thr;
+}
+
+// Calls put(position, block) for every block the row takes, positions in block
+// order (the first CTA, after score_and_decide). Returns their number.
+template <typename Put>
+__device__ __forceinline__ int for_taken(const SelectParams& p, SelShared& sh, const SelRow& rw,
+                                         uint32_t thr, Put put) {
+    if (rw.all) {
+        for (int b = threadIdx.x; b < rw.n; b += kSelThreads) put(b, b);
+        return rw.n;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = rw.n;
+    auto taken = [&](int b) {
+        if (b < rw.lo || b >= rw.lo + rw.nc) return true;
+        return rw.want > 0 && ordered(rw.keys[b - rw.lo]) >= thr;
+    };
+    __syncthreads();
+    const int span = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;   // blocks per warp
+    const int b_lo = warp * span, b_hi = min(b_lo + span, n);
+    int mine = 0;
+    for (int b = b_lo + lane; b < b_hi; b += 32) mine += taken(b);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) sh.part[0][warp] = mine;
+    __syncthreads();
+    int at = 0, total = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+        if (w < warp) at += sh.part[0][w];
+        total += sh.part[0][w];
+    }
+    for (int b0 = b_lo; b0 < b_hi; b0 += 32) {
+        const int b = b0 + lane;
+        const bool take = b < b_hi && taken(b);
+        const uint32_t votes = __ballot_sync(0xffffffffu, take);
+        const int to = at + __popc(votes & ((1u << lane) - 1));
+        if (take && to < p.table_width) put(to, b);
+        at += __popc(votes);
+    }
+    return total;                                              // num_select
+}
+
+// The slab of a row's block, or -1 where the table names none.
+__device__ __forceinline__ int32_t slab_of(const SelectParams& p, const SelRow& rw, int block) {
+    const int64_t blk = rw.table[block];
+    return blk >= 0 && blk < p.num_blocks ? (int32_t)(blk * p.num_kv_heads + rw.h) : -1;
+}
+
+// ---------------------------------------------------------------- host side
+
+// CTAs per row.
+inline int select_cluster(int rows, int max_ctx_blocks) {
+    // CTAs per row: while all fit on 152 SMs, two each, and every warp keeps a
+    // tile of 16 blocks or more. For many rows one CTA each wins, as their
+    // selections overlap other rows' scoring (512 rows of up to 2048 blocks:
+    // steps of 133, 141, 159 and 205 us with 1, 2, 4 and 8; 8 rows of 8192:
+    // 111, 72, 53, 43 and 39 us with 1, 2, 4, 8 and 16).
+    int C = 1;
+    while (C < kMaxCluster && rows <= 152 / C && max_ctx_blocks >= 2 * C * kSelWarps * 16) C *= 2;
+    return C;
+}
+
+// Sets the launch's shared-memory fields; returns the bytes of sides and keys.
+template <typename T, int D>
+int select_smem(SelectParams& p) {
+    const int ntiles = (p.group + 7) / 8;
+    p.side_bytes = std::is_same<T, float>::value ? 0 : ntiles * (2 * D / 32) * 512;
+    p.keys_in_smem = p.max_ctx_blocks <= kSmemKeys && p.side_bytes <= 96 * 1024;
+    if (p.max_ctx_blocks <= p.num_select) return 0;            // nothing is scored
+    return p.side_bytes + (p.keys_in_smem ? p.max_ctx_blocks * 4 : 0);
+}
+
+template <typename Kernel, typename Params>
+cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster, int smem,
+                           cudaStream_t stream) {
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 200 * 1024);
+    if (e != cudaSuccess) return e;
+    if (cluster > 8) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace pagedkv

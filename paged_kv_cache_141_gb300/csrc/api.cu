@@ -389,6 +389,8 @@ bool sparse_sizes_ok(int num_seqs, int num_q_heads, int num_kv_heads, int head_s
 
 // Lengths round up to whole blocks in 32-bit arithmetic.
 constexpr int kMaxSparseContext = 0x7fffffff - 1024;
+// The selection holds a bit per block of a context in shared memory.
+constexpr int kMaxSparseBlocks = 1 << 19;
 
 }  // namespace
 
@@ -953,6 +955,7 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
         return PA_ERR_INVALID_ARG;
     const SparsePlan l = sparse_plan(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
                                      max_context_len, num_select);
+    if (l.max_ctx_blocks > kMaxSparseBlocks) return PA_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total) return PA_ERR_WORKSPACE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);

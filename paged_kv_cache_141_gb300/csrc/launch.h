@@ -229,6 +229,7 @@ struct SelectParams {
     int first_blocks;
     int recent_blocks;
     int side_bytes;               // set by the launcher: shared memory of the query's sides,
+    int taken_bytes;              // of the candidates' bits,
     int keys_in_smem;             // and whether the scores are kept there
 };
 

@@ -92,55 +92,57 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     const int G = p.group, B = p.block_size;
     QT* out = static_cast<QT*>(sp.out) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
 
-    // query fragments: head g's elements as the keys' chunks hold them
-    const QT* query = static_cast<const QT*>(p.query) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
-    if constexpr (!kFp8) {
-        for (int i = threadIdx.x; i < D; i += kSelThreads) {           // [step][lane], 32 elements a step
-            const int hd = (i & 31) >> 2, e = 32 * (i >> 5) + 8 * (i & 3);
-            qf[i] = hd < G ? *reinterpret_cast<const uint4*>(query + hd * D + e) : make_uint4(0, 0, 0, 0);
-        }
-    } else {
-        // per head: a power of two that brings the largest magnitude into [1, 2)
-        if (warp < 8) {
-            float mx = 0.f;
-            if (warp < G)
-                for (int e = lane; e < D; e += 32) mx = fmaxf(mx, fabsf(to_float(query[warp * D + e])));
+    for (int i = threadIdx.x; i < p.table_width; i += kSelThreads) list[i] = -1;
+    // The query in two forms, from one load: its sides for the scores, and the
+    // fragments for S (head g's elements as the keys' chunks hold them). A
+    // thread has eight elements, a head D / 8 neighbouring threads.
+    if (threadIdx.x < D) {
+        constexpr int N = D / 8;
+        const int hd = threadIdx.x / N, c = threadIdx.x % N;   // chunk of elements 8 c ..
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (hd < G)
+            w = *reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) +
+                                                ((size_t)rw.s * p.num_q_heads + rw.h * G + hd) * D + 8 * c);
+        const int l = 4 * hd + (c & 3);                        // the lane, in step c / 4
+        if (rw.scored) {
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-            // 2^exponent, kept to the range whose reciprocal is a normal number
-            const uint32_t e = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
-            if (lane == 0) q_unit[warp] = mx > 0.f && mx < INFINITY ? __uint_as_float(e << 23) : 1.f;
+            for (int side = 0; side < 2; ++side)
+                rw.sides[(side * (D / 32) + c / 4) * 32 + l] =
+                    make_uint4(side2<QT>(w.x, side), side2<QT>(w.y, side), side2<QT>(w.z, side), side2<QT>(w.w, side));
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < D; i += kSelThreads) {           // [step][lane][2], 64 elements a step
-            const int part = i & 1, l = (i >> 1) & 31;
-            const int hd = l >> 2, e = 64 * (i >> 6) + 16 * (l & 3) + 8 * part;
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (hd < G) {
-                float x[8];
-                RowLoader<QT, 8>::load(query + hd * D + e, x);
-                const float r = 1.f / q_unit[hd];                      // exact
-                // a word of codes (4) meets elements (0, 2) and (1, 3)
+        if constexpr (!kFp8) {
+            qf[(c / 4) * 32 + l] = w;
+        } else {
+            float x[8], mx = 0.f;
+            widen16<QT>(w, x);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    w[2 * k] = Ops::pack(x[4 * k] * r, x[4 * k + 2] * r);
-                    w[2 * k + 1] = Ops::pack(x[4 * k + 1] * r, x[4 * k + 3] * r);
-                }
-            }
-            qf[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
+#pragma unroll
+            for (int m = N / 2; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+            // a power of two that brings the largest magnitude into [1, 2),
+            // kept to the range whose reciprocal is a normal number
+            const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
+            const float unit = mx > 0.f && mx < INFINITY ? __uint_as_float(ex << 23) : 1.f;
+            if (c == 0) q_unit[hd] = unit;
+            const float r = 1.f / unit;                        // exact
+            // 64 elements a step, 16 a lane: this chunk is half c & 1 of lane
+            // c / 2 & 3; a word of codes (4) meets elements (0, 2) and (1, 3)
+            qf[((c / 8) * 32 + 4 * hd + (c / 2 & 3)) * 2 + (c & 1)] =
+                make_uint4(Ops::pack(x[0] * r, x[2] * r), Ops::pack(x[1] * r, x[3] * r),
+                           Ops::pack(x[4] * r, x[6] * r), Ops::pack(x[5] * r, x[7] * r));
         }
     }
 
     // ------------------------------------------------------------ selection
-    const uint32_t thr = score_and_decide<QT, D, true>(p, sh, cluster, rw);
+    score_and_take<QT, D, true>(p, sh, cluster, rw);
     int32_t* selected = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
     const int total = rw.n < p.num_select ? rw.n : p.num_select;
     if (rw.rank == 0 || rw.all) {                   // with every block taken each CTA lists them itself
-        for_taken(p, sh, rw, thr, [&](int at, int b) { list[at] = b; });
+        for_taken(sh, rw, [&](int at, int b) { list[at] = b; });
         __syncthreads();
         for (int i = threadIdx.x; i < total; i += kSelThreads) {
             const int b = list[i];
-            const int slab = slab_of(p, rw, b);
+            const int slab = b < 0 ? -1 : slab_of(p, rw, b);
             if (rw.rank == 0) {
                 if (selected) selected[i] = b;
                 if (slab < 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);

@@ -16,11 +16,13 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
     __shared__ SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const SelRow rw(p, cluster, dyn);
-    const uint32_t thr = score_and_decide<T, D, kOneTile>(p, sh, cluster, rw);
+    if (!std::is_same<T, float>::value && rw.scored) stage_sides<T, D>(p, rw);
+    score_and_take<T, D, kOneTile>(p, sh, cluster, rw);
     if (rw.rank != 0) return;
     int32_t* slabs = p.slab_tables + (size_t)rw.row * p.table_width;
     int32_t* out = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
-    const int total = for_taken(p, sh, rw, thr, [&](int at, int b) {
+    const int total = rw.n < p.num_select ? rw.n : p.num_select;
+    for_taken(sh, rw, [&](int at, int b) {
         slabs[at] = slab_of(p, rw, b);
         if (out) out[at] = b;
     });
@@ -35,7 +37,6 @@ cudaError_t launch_select(SelectParams p, cudaStream_t stream) {
     const int rows = p.num_seqs * p.num_kv_heads;
     const int C = select_cluster(rows, p.max_ctx_blocks);
     const int smem = select_smem<T, D>(p);
-    if (p.side_bytes > 200 * 1024) return cudaErrorInvalidValue;
     // one MMA tile of heads, or (binary32 has no tiles) any number
     auto kernel = std::is_same<T, float>::value || p.group <= 8 ? select_blocks_kernel<T, D, true>
                                                                 : select_blocks_kernel<T, D, false>;

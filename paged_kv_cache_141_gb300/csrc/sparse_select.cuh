@@ -75,6 +75,9 @@ __device__ __forceinline__ uint64_t ordered64(double x) {
     const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
     return u >> 63 ? ~u : u | (1ull << 63);
 }
+__device__ __forceinline__ double value64(uint64_t key) {      // ordered64's inverse
+    return __longlong_as_double((long long)(key >> 63 ? key ^ (1ull << 63) : ~key));
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -126,6 +129,39 @@ __device__ uint64_t exact_score(const SelectParams& p, int s, int h, int64_t blk
         best = x > best ? x : best;
     }
     return best;
+}
+
+// A block's score for one head to about 2^-44 of its terms' magnitudes, by one
+// warp, for 16-bit types: their products are exact in binary32, and the sum is
+// kept as a pair (Knuth's two-sum, errors collected), far cheaper here than
+// binary64. Not for magnitudes whose products could under- or overflow.
+template <typename T, int D>
+__device__ double close_head_score(const SelectParams& p, int s, int h, int g, int64_t blk, int lane) {
+    constexpr int E = D / 32;
+    if (blk < 0 || blk >= p.num_blocks) return -INFINITY;
+    const T* bounds = static_cast<const T*>(p.k_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
+    float lo[E], hi[E], q[E];
+    RowLoader<T, E>::load(bounds, lo);
+    RowLoader<T, E>::load(bounds + D, hi);
+    RowLoader<T, E>::load(static_cast<const T*>(p.query) +
+                          ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
+    float sum = 0.f, err = 0.f;
+    auto add = [&](float x) {
+        const float t = __fadd_rn(sum, x);
+        const float z = __fsub_rn(t, sum);
+        err = __fadd_rn(err, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, z)), __fsub_rn(x, z)));
+        sum = t;
+    };
+#pragma unroll
+    for (int i = 0; i < E; ++i) add(__fmul_rn(q[i], q[i] < 0.f ? lo[i] : hi[i]));
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, sum, m);
+        const float e2 = __shfl_xor_sync(0xffffffffu, err, m);
+        add(s2);
+        err = __fadd_rn(err, e2);
+    }
+    return (double)sum + (double)err;
 }
 
 // Sixteen blocks' bounds rows, four 64-byte steps (a quarter: 128 elements) at
@@ -195,6 +231,21 @@ __device__ __forceinline__ int cta_sum(SelShared& sh, int x, int& turn) {
     return y;
 }
 
+__device__ __forceinline__ float warp_min(float x) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+
+__device__ __forceinline__ float cta_min(SelShared& sh, float x) {
+    x = warp_min(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.fpart[0][threadIdx.x >> 5] = x;
+    __syncthreads();
+    for (int w = 0; w < kSelWarps; ++w) x = fminf(x, sh.fpart[0][w]);
+    return x;
+}
+
 // The largest P with count(key >= P) >= want over the candidates that `key`
 // gives (i strided over the threads; skip(i) leaves one out). exact: whether
 // count(key >= P) == want.
@@ -220,24 +271,23 @@ __device__ __forceinline__ K kth_largest(SelShared& sh, int n, int want, int& tu
 // The score that ordered() puts below every value: a block not taken.
 __device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu); }
 
-// The taken candidates, where a histogram of the approximate scores over their
-// range leaves few blocks near the threshold: thr such that they are those of
-// ordered(keys[i]) >= thr (undecided blocks' keys are replaced). False: not
-// decided here, and keys are as they were.
+// Marks the taken candidates in `taken` (a bit each, in words) where a histogram
+// of the approximate scores over their range leaves few blocks near the
+// threshold. False: not decided here.
 template <typename T, int D>
-__device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, float* keys, int nc,
-                                       int want, float mag, int C, int s, int h,
-                                       const int32_t* table, uint32_t& thr) {
+__device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const float* keys,
+                                  uint32_t* taken, int nc, int want, float mag, int C, int s, int h,
+                                  const int32_t* table) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float lowest = sh.lowest[0], highest = sh.highest[0];
     for (int r = 1; r < C; ++r) {
         lowest = fminf(lowest, sh.lowest[r]);
         highest = fmaxf(highest, sh.highest[r]);
     }
-    // err2: both errors, and the rounding of k +- err2 below (2^-24 of k <= mag)
-    const float err2 = mag * (2.f * kScoreEps * 1.01f);
-    const float scale = (float)(kBins - 1) / (highest - lowest);
+    const float range = highest - lowest;
+    const float scale = (float)(kBins - 1) / range;
     if (!(isfinite(mag) && highest > lowest && isfinite(scale))) return false;
+    const float err2 = mag * (2.f * kScoreEps * 1.01f);        // both errors
     // non-decreasing in k; blocks the table does not name score -infinity: bin 0
     auto bin_of = [&](float k) {
         const int b = __float2int_rz((k - lowest) * scale);
@@ -246,7 +296,7 @@ __device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, flo
     for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.bins[i] = 0;
     if (threadIdx.x == 0) sh.list_n = 0;
     __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x; i < nc; i += kSelThreads) atomicAdd(&sh.bins[bin_of(keys[i])], 1);
     __syncthreads();
     // the bin where the count from the top reaches want: thread t has the four
@@ -278,26 +328,32 @@ __device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, flo
         }
     }
     __syncthreads();
-    // Every block that can change sides is within err2 of the threshold's bin.
+    // Every block that can change sides is within err2 of that bin's range of
+    // scores (to the rounding of bin_of and of the range's ends). Above: taken.
     const int bin = sh.bin;
-    int below_bin_near = 0;
+    const float slack = err2 + range * 0x1p-20f + (fabsf(lowest) + fabsf(highest)) * 0x1p-21f;
+    const float from = bin == 0 ? -INFINITY : lowest + (float)bin / scale - slack;
+    const float to = lowest + (float)(bin + 1) / scale + slack;
+    int near_above = 0;                                        // counted above the bin, but not settled
 #pragma unroll 4
-    for (int i = threadIdx.x; i < nc; i += kSelThreads) {
-        const float k = keys[i];
-        if (bin_of(k + err2) >= bin && bin_of(k - err2) <= bin) {
+    for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
+        const int i = i0 + lane;
+        const float k = i < nc ? keys[i] : out_key();          // (NaN: in neither)
+        const uint32_t word = __ballot_sync(0xffffffffu, k > to);
+        if (lane == 0) taken[i0 >> 5] = word;
+        if (k >= from && k <= to) {
             const int at = atomicAdd(&sh.list_n, 1);
             if (at < kRankList) {
                 sh.list[at] = i;
                 sh.list_score[at] = k;
             }
-            below_bin_near += bin_of(k) > bin;                 // counted above, but not settled
+            near_above += bin_of(k) > bin;
         }
     }
-    __syncthreads();
+    int turn = 0;
+    const int left = want - (sh.above - cta_sum(sh, near_above, turn));       // the list's places
     const int m = sh.list_n;
     if (m > kRankList) return false;
-    int turn = 0;
-    const int left = want - (sh.above - cta_sum(sh, below_bin_near, turn));   // the list's places
     // rank by approximate score (the list's order varies, the ranks do not)
     const int e = threadIdx.x;
     const bool mine = e < m;
@@ -307,49 +363,83 @@ __device__ bool threshold_by_histogram(const SelectParams& p, SelShared& sh, flo
     if (mine)
         for (int o = 0; o < m; ++o)
             before += sh.list_score[o] > k || (sh.list_score[o] == k && sh.list[o] < i);
-    const bool in = mine && before < left;
-    float a = in ? k : INFINITY, b = mine && !in ? k : -INFINITY;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
-        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-    }
-    if (lane == 0) {
-        sh.fpart[0][warp] = a;
-        sh.fpart[1][warp] = b;
-    }
-    __syncthreads();
-    for (int w = 0; w < kSelWarps; ++w) {
-        a = fminf(a, sh.fpart[0][w]);
-        b = fmaxf(b, sh.fpart[1][w]);
-    }
-    bool take = in;
-    if (a - b <= err2) {
-        // the blocks within err2 of the other side, in binary64
-        const bool open = mine && (in ? k <= b + err2 : k >= a - err2);
-        if (mine) sh.list_key[e] = open ? 1 : 0;               // below every key of a score
-        __syncthreads();
-        for (int w = warp; w < m * p.group; w += kSelWarps) {  // a warp per (block, head)
-            const int o = w / p.group;
-            if (sh.list_key[o] == 0) continue;
-            const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
-            if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
-        }
-        __syncthreads();
-        if (open) {
-            int places = left, ahead = 0;
-            const uint64_t x = sh.list_key[e];
-            for (int o = 0; o < m; ++o) {
-                const uint64_t y = sh.list_key[o];
-                if (y == 0) places -= sh.list_score[o] >= a;   // settled inside
-                else ahead += y > x || (y == x && sh.list[o] < i);
+    bool take = mine && before < left;
+    // the smallest taken and the largest left out of a set of scores in the list
+    auto border = [&](float x, float& a, float& b) {
+        a = take ? x : INFINITY;
+        b = mine && !take ? x : -INFINITY;
+        if (m > 32) {
+            a = cta_min(sh, a);
+            b = -cta_min(sh, -b);
+        } else {                                               // the list is in warp 0
+            a = warp_min(a);
+            b = -warp_min(-b);
+            if (threadIdx.x == 0) {
+                sh.fpart[0][0] = a;
+                sh.fpart[1][0] = b;
             }
-            take = ahead < places;
+            __syncthreads();
+            a = sh.fpart[0][0];
+            b = sh.fpart[1][0];
+        }
+    };
+    float a, b;
+    border(k, a, b);
+    if (a - b <= err2) {
+        // the blocks within err2 of the other side: a closer score, and where
+        // that leaves a doubt, binary64
+        const bool inside = take;
+        const bool open = mine && (take ? k <= b + err2 : k >= a - err2);
+        const int inner = cta_sum(sh, mine && !open && inside, turn);         // settled inside
+        bool decided = false;
+        if constexpr (!std::is_same<T, float>::value) {
+            if (mag > 0x1p-90f && mag < 0x1p120f) {
+                if (mine) sh.list_key[e] = open ? 1 : 0;       // below every key of a score
+                __syncthreads();
+                for (int w = warp; w < m * p.group; w += kSelWarps) {         // a warp per (block, head)
+                    const int o = w / p.group;
+                    if (sh.list_key[o] == 0) continue;
+                    const uint64_t x = ordered64(close_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane));
+                    if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
+                }
+                __syncthreads();
+                const uint64_t x = mine ? sh.list_key[e] : 0;
+                int ahead = inner, nearby = 0;
+                if (open) {
+                    const double mine_d = value64(x), margin = (double)mag * 0x1p-40;
+                    for (int o = 0; o < m; ++o) {
+                        const uint64_t y = sh.list_key[o];
+                        ahead += y > x || (y == x && y != 0 && sh.list[o] < i);
+                        if (o != e && y != 0) nearby += fabs(value64(y) - mine_d) <= margin;
+                    }
+                    take = ahead < left;
+                }
+                decided = cta_sum(sh, nearby, turn) == 0;
+            }
+        }
+        if (!decided) {
+            take = inside;
+            if (mine) sh.list_key[e] = open ? 1 : 0;
+            __syncthreads();
+            for (int w = warp; w < m * p.group; w += kSelWarps) {
+                const int o = w / p.group;
+                if (sh.list_key[o] == 0) continue;
+                const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
+                if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
+            }
+            __syncthreads();
+            if (open) {
+                int ahead = inner;
+                const uint64_t x = sh.list_key[e];
+                for (int o = 0; o < m; ++o) {
+                    const uint64_t y = sh.list_key[o];
+                    ahead += y > x || (y == x && sh.list[o] < i);
+                }
+                take = ahead < left;
+            }
         }
     }
-    __syncthreads();
-    if (mine) keys[i] = take ? INFINITY : out_key();
-    thr = ordered(a);
+    if (take) atomicOr(&taken[i >> 5], 1u << (i & 31));
     __syncthreads();
     return true;
 }
@@ -364,6 +454,7 @@ struct SelRow {
     const int32_t* table;
     uint4* sides;                       // [n-tile][step][lane]
     float* keys;                        // the candidates' scores (of the first CTA, or in memory)
+    uint32_t* taken;                    // a bit per candidate (the first CTA's)
 
     __device__ __forceinline__ SelRow(const SelectParams& p, cg::cluster_group& cluster, uint8_t* smem) {
         C = (int)cluster.num_blocks();
@@ -382,30 +473,61 @@ struct SelRow {
         nc = all ? 0 : n - p.recent_blocks - lo;
         scored = nc > 0 && want > 0;
         sides = reinterpret_cast<uint4*>(smem);
-        keys = p.keys_in_smem ? reinterpret_cast<float*>(smem + p.side_bytes)
+        taken = reinterpret_cast<uint32_t*>(smem + p.side_bytes);
+        keys = p.keys_in_smem ? reinterpret_cast<float*>(smem + p.side_bytes + p.taken_bytes)
                               : p.scores + (size_t)row * p.max_ctx_blocks;
     }
 };
 
-// Scores the candidates (all CTAs of the cluster) and finds the threshold (the
-// first): there, and only there, candidate i is taken if ordered(keys[i]) is
-// at least the result. All CTAs meet at two cluster barriers if row.scored,
-// else at none. kOneTile: groups of at most eight heads, one MMA tile.
+// Barrier over the cluster (over the CTA where it is one).
+__device__ __forceinline__ void cluster_barrier(cg::cluster_group& cluster, int C) {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+}
+
+// The query's two sides as the MMAs' second operand, [n-tile][step][lane]:
+// lane (g, t4) of step j has head g's elements 32 j + 8 t4 .. of (min(q, 0),
+// max(q, 0)). Followed by a barrier before their use.
+template <typename T, int D>
+__device__ void stage_sides(const SelectParams& p, const SelRow& rw) {
+    constexpr int STEPS = 2 * D / 32;
+    const int ntiles = (p.group + 7) / 8;
+    for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += kSelThreads) {
+        const int l = i & 31, j = (i >> 5) % STEPS, nt = i / (32 * STEPS);
+        const int g = nt * 8 + (l >> 2);
+        const int e = 32 * j + 8 * (l & 3);
+        const bool positive = e >= D;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (g < p.group) {
+            w = *reinterpret_cast<const uint4*>(
+                static_cast<const T*>(p.query) +
+                ((size_t)rw.s * p.num_q_heads + rw.h * p.group + g) * D + (positive ? e - D : e));
+            w = make_uint4(side2<T>(w.x, positive), side2<T>(w.y, positive),
+                           side2<T>(w.z, positive), side2<T>(w.w, positive));
+        }
+        rw.sides[i] = w;
+    }
+}
+
+// Scores the candidates (all CTAs of the cluster) and marks the taken ones (the
+// first CTA, in rw.taken). All CTAs meet at two cluster barriers if rw.scored,
+// else at none; the sides have been staged. kOneTile: groups of at most eight
+// heads, one MMA tile.
 template <typename T, int D, bool kOneTile>
-__device__ uint32_t score_and_decide(const SelectParams& p, SelShared& sh, cg::cluster_group& cluster,
-                                     const SelRow& rw) {
-    if (!rw.scored) return 0;
+__device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster_group& cluster,
+                               const SelRow& rw) {
+    if (!rw.scored) return;
     constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
     constexpr int NQ = STEPS / 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = rw.C, rank = rw.rank, row = rw.row, s = rw.s, h = rw.h;
     const int nc = rw.nc, want = rw.want, lo = rw.lo;
     const int32_t* table = rw.table;
-    uint4* sides = rw.sides;
+    const uint4* sides = rw.sides;
     float* keys = rw.keys;
     {
         // ------------------------------------------------ approximate scores
-        cluster.sync();                                        // the first CTA runs: its memory may be written
+        cluster_barrier(cluster, C);                           // the sides; the first CTA runs: its memory may be written
         float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(keys, 0) : keys;
         float worst = 0.f, lowest = INFINITY, highest = -INFINITY;
         if constexpr (std::is_same<T, float>::value) {
@@ -444,22 +566,6 @@ __device__ uint32_t score_and_decide(const SelectParams& p, SelShared& sh, cg::c
             }
         } else {
             const int ntiles = (p.group + 7) / 8;
-            for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += kSelThreads) {
-                const int l = i & 31, j = (i >> 5) % STEPS, nt = i / (32 * STEPS);
-                const int g = nt * 8 + (l >> 2);
-                const int e = 32 * j + 8 * (l & 3);
-                const bool positive = e >= D;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (g < p.group) {
-                    w = *reinterpret_cast<const uint4*>(
-                        static_cast<const T*>(p.query) +
-                        ((size_t)s * p.num_q_heads + h * p.group + g) * D + (positive ? e - D : e));
-                    w = make_uint4(side2<T>(w.x, positive), side2<T>(w.y, positive),
-                                   side2<T>(w.z, positive), side2<T>(w.w, positive));
-                }
-                sides[i] = w;
-            }
-            __syncthreads();
             const int g = lane >> 2, t4 = lane & 3;
             const int tiles = (nc + 15) / 16;
             const int stride = C * kSelWarps;
@@ -577,14 +683,15 @@ __device__ uint32_t score_and_decide(const SelectParams& p, SelShared& sh, cg::c
             *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
         }
     }
-    cluster.sync();
-    if (rank != 0) return 0;
+    cluster_barrier(cluster, C);
+    if (rank != 0) return;
 
-    int turn = 0;
-    uint32_t thr = 0;                                          // taken candidates: ordered(key) >= thr
     float mag = 0.f;
     for (int r = 0; r < C; ++r) mag = max_nan(mag, sh.err[r]);
-    if (!threshold_by_histogram<T, D>(p, sh, keys, nc, want, mag, C, s, h, table + lo, thr)) {
+    if (take_by_histogram<T, D>(p, sh, keys, rw.taken, nc, want, mag, C, s, h, table + lo)) return;
+    {
+        int turn = 0;
+        uint32_t thr = 0;                                      // taken candidates: ordered(key) >= thr
         const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
         const bool finite = isfinite(mag);
         // Settled blocks: those that beat (or lose to) every block on the other
@@ -706,47 +813,46 @@ __device__ uint32_t score_and_decide(const SelectParams& p, SelShared& sh, cg::c
                 if (!settled(keys[i])) keys[i] = INFINITY;
             __syncthreads();
         }
+        for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
+            const uint32_t word = __ballot_sync(0xffffffffu, i0 + lane < nc && ordered(keys[i0 + lane]) >= thr);
+            if (lane == 0) rw.taken[i0 >> 5] = word;
+        }
+        __syncthreads();
     }
-    return thr;
 }
 
 // Calls put(position, block) for every block the row takes, positions in block
-// order (the first CTA, after score_and_decide). Returns their number.
+// order (the first CTA, after score_and_take; any CTA where rw.all).
 template <typename Put>
-__device__ __forceinline__ int for_taken(const SelectParams& p, SelShared& sh, const SelRow& rw,
-                                         uint32_t thr, Put put) {
+__device__ __forceinline__ void for_taken(SelShared& sh, const SelRow& rw, Put put) {
     if (rw.all) {
         for (int b = threadIdx.x; b < rw.n; b += kSelThreads) put(b, b);
-        return rw.n;
+        return;
     }
+    for (int b = threadIdx.x; b < rw.lo; b += kSelThreads) put(b, b);
+    const int recent = rw.n - rw.lo - rw.nc;
+    for (int i = threadIdx.x; i < recent; i += kSelThreads) put(rw.lo + rw.want + i, rw.lo + rw.nc + i);
+    if (!rw.scored) return;
+    // each thread has consecutive words of the candidates' bits
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = rw.n;
-    auto taken = [&](int b) {
-        if (b < rw.lo || b >= rw.lo + rw.nc) return true;
-        return rw.want > 0 && ordered(rw.keys[b - rw.lo]) >= thr;
-    };
-    __syncthreads();
-    const int span = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;   // blocks per warp
-    const int b_lo = warp * span, b_hi = min(b_lo + span, n);
+    const int words = (rw.nc + 31) / 32, per = (words + kSelThreads - 1) / kSelThreads;
+    const int w0 = threadIdx.x * per, w1 = min(w0 + per, words);
     int mine = 0;
-    for (int b = b_lo + lane; b < b_hi; b += 32) mine += taken(b);
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) sh.part[0][warp] = mine;
+    for (int w = w0; w < w1; ++w) mine += __popc(rw.taken[w]);
+    int run = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, m);
+        if (lane >= m) run += v;
+    }
     __syncthreads();
-    int at = 0, total = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-        if (w < warp) at += sh.part[0][w];
-        total += sh.part[0][w];
-    }
-    for (int b0 = b_lo; b0 < b_hi; b0 += 32) {
-        const int b = b0 + lane;
-        const bool take = b < b_hi && taken(b);
-        const uint32_t votes = __ballot_sync(0xffffffffu, take);
-        const int to = at + __popc(votes & ((1u << lane) - 1));
-        if (take && to < p.table_width) put(to, b);
-        at += __popc(votes);
-    }
-    return total;                                              // num_select
+    if (lane == 31) sh.part[0][warp] = run;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) run += sh.part[0][w];
+    int at = rw.lo + run - mine;
+    for (int w = w0; w < w1; ++w)
+        for (uint32_t word = rw.taken[w]; word && at < rw.lo + rw.want; word &= word - 1)
+            put(at++, rw.lo + 32 * w + __ffs(word) - 1);
 }
 
 // The slab of a row's block, or -1 where the table names none.
@@ -774,9 +880,10 @@ template <typename T, int D>
 int select_smem(SelectParams& p) {
     const int ntiles = (p.group + 7) / 8;
     p.side_bytes = std::is_same<T, float>::value ? 0 : ntiles * (2 * D / 32) * 512;
-    p.keys_in_smem = p.max_ctx_blocks <= kSmemKeys && p.side_bytes <= 96 * 1024;
+    p.keys_in_smem = p.max_ctx_blocks <= kSmemKeys && p.side_bytes <= 64 * 1024;
+    p.taken_bytes = (p.max_ctx_blocks + 127) / 128 * 16;
     if (p.max_ctx_blocks <= p.num_select) return 0;            // nothing is scored
-    return p.side_bytes + (p.keys_in_smem ? p.max_ctx_blocks * 4 : 0);
+    return p.side_bytes + p.taken_bytes + (p.keys_in_smem ? p.max_ctx_blocks * 4 : 0);
 }
 
 template <typename Kernel, typename Params>

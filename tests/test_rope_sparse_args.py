@@ -88,7 +88,8 @@ def test_sparse_invalid(pk, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(D=96), dict(B=1025), dict(nb=2 ** 31), dict(nb=2 ** 28), dict(ct=1),
-                                dict(maxlen=2 ** 31 - 1), dict(S=70000), dict(Hq=129, Hkv=1)])
+                                dict(maxlen=2 ** 31 - 1), dict(S=70000), dict(Hq=129, Hkv=1),
+                                dict(maxlen=2 ** 19 + 1, B=1)])
 def test_sparse_unsupported(pk, kw):
     assert sparse(pk, **kw) == pk.PA_ERR_UNSUPPORTED
 

@@ -6,7 +6,7 @@
 // attend, so the memory system has work throughout; nothing goes through
 // memory between the two parts, and few rows pay one launch.
 //
-// Attention: each warp takes every 8 C-th tile of 16 tokens (a block, or a part
+// Attention: each warp of the cluster in turn takes a tile of 16 tokens (a block, or a part
 // of one). Both products run on warp-level MMAs, straight from global memory
 // to registers, as no element is used twice but by the group's heads:
 //   S (16 tokens x 8 heads) = K (16 x D) . Q^T, a lane's 16-byte chunk of a key
@@ -68,19 +68,20 @@ struct Joined {                                     // one CTA's result, read by
     float m[8], l[8];
 };
 
-template <typename QT, typename CT, int D>
-__global__ void __launch_bounds__(kSelThreads, 2)
+template <typename QT, typename CT, int D, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT)
 sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
     using MT = typename MathType<CT>::T;            // the MMAs' type
     using Ops = MmaOps<MT>;
     using Tile = Tile16<CT, D>;
     constexpr int MD = D / 16;                      // O^T row tiles
+    constexpr int NW = NT / 32;
     const SelectParams& p = sp.sel;
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ SelShared sh;
+    __shared__ SelShared<NT> sh;
     __shared__ Joined joined;
-    __shared__ float wm[kSelWarps][8], wl[kSelWarps][8], q_unit[8];
+    __shared__ float wm[NW][8], wl[NW][8], q_unit[8];
     int32_t* list = reinterpret_cast<int32_t*>(dyn);                   // the row's slabs
     uint4* qf = reinterpret_cast<uint4*>(dyn + sp.list_bytes);         // query fragments: D * 16 bytes
     uint8_t* work = dyn + sp.list_bytes + 16 * D;                      // selection, then the warps' O
@@ -92,7 +93,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     const int G = p.group, B = p.block_size;
     QT* out = static_cast<QT*>(sp.out) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
 
-    for (int i = threadIdx.x; i < p.table_width; i += kSelThreads) list[i] = -1;
+    for (int i = threadIdx.x; i < p.table_width; i += NT) list[i] = -1;
     // The query in two forms, from one load: its sides for the scores, and the
     // fragments for S (head g's elements as the keys' chunks hold them). A
     // thread has eight elements, a head D / 8 neighbouring threads.
@@ -134,13 +135,13 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     }
 
     // ------------------------------------------------------------ selection
-    score_and_take<QT, D, true>(p, sh, cluster, rw);
+    score_and_take<QT, D, true, NT>(p, sh, cluster, rw);
     int32_t* selected = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
     const int total = rw.n < p.num_select ? rw.n : p.num_select;
     if (rw.rank == 0 || rw.all) {                   // with every block taken each CTA lists them itself
         for_taken(sh, rw, [&](int at, int b) { list[at] = b; });
         __syncthreads();
-        for (int i = threadIdx.x; i < total; i += kSelThreads) {
+        for (int i = threadIdx.x; i < total; i += NT) {
             const int b = list[i];
             const int slab = b < 0 ? -1 : slab_of(p, rw, b);
             if (rw.rank == 0) {
@@ -150,13 +151,13 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
             list[i] = slab;
         }
         if (rw.rank == 0 && selected)
-            for (int i = total + threadIdx.x; i < p.num_select; i += kSelThreads) selected[i] = -1;
+            for (int i = total + threadIdx.x; i < p.num_select; i += NT) selected[i] = -1;
     }
     if (C > 1 && !rw.all) {
         cluster.sync();
         if (rw.rank != 0) {
             const int32_t* first = cluster.map_shared_rank(list, 0);
-            for (int i = threadIdx.x; i < total; i += kSelThreads) list[i] = first[i];
+            for (int i = threadIdx.x; i < total; i += NT) list[i] = first[i];
         }
     }
     __syncthreads();
@@ -213,8 +214,8 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
             }
         }
     };
-    const int stride = C * kSelWarps;
-    int tile = rw.rank * kSelWarps + warp;
+    const int stride = C * NW;
+    int tile = rw.rank * NW + warp;
     int64_t at = -1;
     int nvalid = 0;
     auto valid_of = [&](int64_t a, int tile) { return a < 0 ? 0 : min(16, len - tile * 16); };
@@ -355,14 +356,14 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     __syncthreads();
     // elements d, d + 1 of head hd: the sum over the warps, relative to the CTA's maximum
     const float* jo_base = wo;
-    for (int e = threadIdx.x; e < G * (D / 2); e += kSelThreads) {
+    for (int e = threadIdx.x; e < G * (D / 2); e += NT) {
         const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) M = fmaxf(M, wm[w][hd]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w][hd]);
         float l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = wm[w][hd] == -INFINITY ? 0.f : fast_exp2(wm[w][hd] - M);
             const float2 o = *reinterpret_cast<const float2*>(jo_base + (w * 8 + hd) * kPitch + d);
             l += f * wl[w][hd];
@@ -385,11 +386,13 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     if (C == 1) return;
     cluster.sync();
     // ------------------------------------------------------------ join the CTAs
-    for (int e = rw.rank * kSelThreads + threadIdx.x; e < G * (D / 2); e += C * kSelThreads) {
+    for (int e = rw.rank * NT + threadIdx.x; e < G * (D / 2); e += C * NT) {
         const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
         float M = -INFINITY;
+#pragma unroll 4
         for (int r = 0; r < C; ++r) M = fmaxf(M, cluster.map_shared_rank(&joined, r)->m[hd]);
         float l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 4
         for (int r = 0; r < C; ++r) {
             const Joined* jr = cluster.map_shared_rank(&joined, r);
             const float2 o = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + hd * kPitch + d, r));
@@ -409,8 +412,12 @@ template <typename QT, typename CT, int D>
 cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
     const int rows = sp.sel.num_seqs * sp.sel.num_kv_heads;
     const int C = select_cluster(rows, sp.sel.max_ctx_blocks);
+    // an SM for every CTA: 16 warps each, else two CTAs of 8. (A cluster of 16
+    // takes 16 SMs of one GPC then, and only some GPCs have them free: 8
+    // clusters ran in two waves, 47 us against 30 with 8 warps.)
+    const bool wide = C < 16 && rows * C <= 152;
     const int select = select_smem<QT, D>(sp.sel);
-    const int join = kSelWarps * 8 * (D + 4) * (int)sizeof(float);
+    const int join = (wide ? 16 : 8) * 8 * (D + 4) * (int)sizeof(float);
     sp.list_bytes = (sp.sel.table_width * 4 + 15) / 16 * 16;
     const int smem = sp.list_bytes + 16 * D + (select > join ? select : join);
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
@@ -418,7 +425,9 @@ cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
         sp.q_mul *= 256.f;                          // codes are widened times 2^-8
         sp.v_mul *= 256.f;
     }
-    return launch_cluster(sparse_decode_kernel<QT, CT, D>, sp, rows * C, C, smem, stream);
+    if (wide)
+        return launch_cluster(sparse_decode_kernel<QT, CT, D, 512>, sp, rows * C, C, 512, smem, stream);
+    return launch_cluster(sparse_decode_kernel<QT, CT, D, 256>, sp, rows * C, C, 256, smem, stream);
 }
 
 template <typename QT, typename CT>

@@ -9,15 +9,17 @@ namespace pagedkv {
 
 namespace {
 
+constexpr int NT = 256;
+
 template <typename T, int D, bool kOneTile>
-__global__ void __launch_bounds__(kSelThreads, 2)
+__global__ void __launch_bounds__(NT, 2)
 select_blocks_kernel(const __grid_constant__ SelectParams p) {
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ SelShared sh;
+    __shared__ SelShared<NT> sh;
     cg::cluster_group cluster = cg::this_cluster();
     const SelRow rw(p, cluster, dyn);
-    if (!std::is_same<T, float>::value && rw.scored) stage_sides<T, D>(p, rw);
-    score_and_take<T, D, kOneTile>(p, sh, cluster, rw);
+    if (!std::is_same<T, float>::value && rw.scored) stage_sides<T, D, NT>(p, rw);
+    score_and_take<T, D, kOneTile, NT>(p, sh, cluster, rw);
     if (rw.rank != 0) return;
     int32_t* slabs = p.slab_tables + (size_t)rw.row * p.table_width;
     int32_t* out = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
@@ -29,7 +31,7 @@ select_blocks_kernel(const __grid_constant__ SelectParams p) {
     if (threadIdx.x == 0)
         p.slab_lens[rw.row] = total * p.block_size - (rw.n * p.block_size - rw.L);
     if (out)
-        for (int i = total + threadIdx.x; i < p.num_select; i += kSelThreads) out[i] = -1;
+        for (int i = total + threadIdx.x; i < p.num_select; i += NT) out[i] = -1;
 }
 
 template <typename T, int D>
@@ -40,7 +42,7 @@ cudaError_t launch_select(SelectParams p, cudaStream_t stream) {
     // one MMA tile of heads, or (binary32 has no tiles) any number
     auto kernel = std::is_same<T, float>::value || p.group <= 8 ? select_blocks_kernel<T, D, true>
                                                                 : select_blocks_kernel<T, D, false>;
-    return launch_cluster(kernel, p, rows * C, C, smem, stream);
+    return launch_cluster(kernel, p, rows * C, C, NT, smem, stream);
 }
 
 template <typename T>

@@ -40,11 +40,7 @@ namespace pagedkv {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kRankList = kSelThreads;  // blocks ranked in shared memory, one per thread
-constexpr int kBins = 4 * kSelThreads;  // of the score histogram
 // Keys of up to this many blocks are kept in shared memory (two CTAs per SM);
 // longer contexts' in the workspace.
 constexpr int kSmemKeys = 24 * 1024;
@@ -205,15 +201,19 @@ __device__ __forceinline__ void add_quarter(const Quarter& b, const uint4* sides
     for (int i = 0; i < 4; ++i) c[i] += c0[i] + c1[i];
 }
 
+template <int NT>
 struct SelShared {
+    static constexpr int kWarps = NT / 32;
+    static constexpr int kRankList = NT;    // blocks ranked here, one per thread
+    static constexpr int kBins = 4 * NT;    // of the score histogram
     float err[kMaxCluster];             // per CTA: the largest sum of magnitudes,
     float lowest[kMaxCluster];          // and the range of its finite scores
     float highest[kMaxCluster];
     int bins[kBins];
     int bin;                            // the threshold's, and the candidates above it
     int above;
-    int part[2][kSelWarps];             // count(): per-warp sums, double-buffered
-    float fpart[3][kSelWarps];
+    int part[2][kWarps];             // count(): per-warp sums, double-buffered
+    float fpart[3][kWarps];
     int list_n;
     int list[kRankList];
     float list_score[kRankList];
@@ -221,12 +221,13 @@ struct SelShared {
 };
 
 // Sum over the CTA; one barrier (`turn` alternates the buffer).
-__device__ __forceinline__ int cta_sum(SelShared& sh, int x, int& turn) {
+template <int NT>
+__device__ __forceinline__ int cta_sum(SelShared<NT>& sh, int x, int& turn) {
     const int w = __reduce_add_sync(0xffffffffu, x);
     if ((threadIdx.x & 31) == 0) sh.part[turn][threadIdx.x >> 5] = w;
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int y = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? sh.part[turn][lane] : 0);
+    const int y = __reduce_add_sync(0xffffffffu, lane < (NT / 32) ? sh.part[turn][lane] : 0);
     turn ^= 1;
     return y;
 }
@@ -237,27 +238,28 @@ __device__ __forceinline__ float warp_min(float x) {
     return x;
 }
 
-__device__ __forceinline__ float cta_min(SelShared& sh, float x) {
+template <int NT>
+__device__ __forceinline__ float cta_min(SelShared<NT>& sh, float x) {
     x = warp_min(x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.fpart[0][threadIdx.x >> 5] = x;
     __syncthreads();
-    for (int w = 0; w < kSelWarps; ++w) x = fminf(x, sh.fpart[0][w]);
+    for (int w = 0; w < (NT / 32); ++w) x = fminf(x, sh.fpart[0][w]);
     return x;
 }
 
 // The largest P with count(key >= P) >= want over the candidates that `key`
 // gives (i strided over the threads; skip(i) leaves one out). exact: whether
 // count(key >= P) == want.
-template <typename K, typename Key, typename Skip>
-__device__ __forceinline__ K kth_largest(SelShared& sh, int n, int want, int& turn, bool& exact,
+template <typename K, int NT, typename Key, typename Skip>
+__device__ __forceinline__ K kth_largest(SelShared<NT>& sh, int n, int want, int& turn, bool& exact,
                                          Key key, Skip skip) {
     K prefix = 0;
     exact = false;
     for (int bit = (int)sizeof(K) * 8 - 1; bit >= 0; --bit) {
         const K cand = prefix | ((K)1 << bit);
         int c = 0;
-        for (int i = threadIdx.x; i < n; i += kSelThreads) c += !skip(i) && key(i) >= cand;
+        for (int i = threadIdx.x; i < n; i += NT) c += !skip(i) && key(i) >= cand;
         const int total = cta_sum(sh, c, turn);
         if (total >= want) prefix = cand;
         if (total == want) {
@@ -274,8 +276,8 @@ __device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu)
 // Marks the taken candidates in `taken` (a bit each, in words) where a histogram
 // of the approximate scores over their range leaves few blocks near the
 // threshold. False: not decided here.
-template <typename T, int D>
-__device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const float* keys,
+template <typename T, int D, int NT>
+__device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, const float* keys,
                                   uint32_t* taken, int nc, int want, float mag, int C, int s, int h,
                                   const int32_t* table) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -285,24 +287,32 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const fl
         highest = fmaxf(highest, sh.highest[r]);
     }
     const float range = highest - lowest;
-    const float scale = (float)(kBins - 1) / range;
+    const float scale = (float)(SelShared<NT>::kBins - 1) / range;
     if (!(isfinite(mag) && highest > lowest && isfinite(scale))) return false;
     const float err2 = mag * (2.f * kScoreEps * 1.01f);        // both errors
     // non-decreasing in k; blocks the table does not name score -infinity: bin 0
     auto bin_of = [&](float k) {
         const int b = __float2int_rz((k - lowest) * scale);
-        return b < 0 ? 0 : (b >= kBins ? kBins - 1 : b);
+        return b < 0 ? 0 : (b >= SelShared<NT>::kBins ? SelShared<NT>::kBins - 1 : b);
     };
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.bins[i] = 0;
+    for (int i = threadIdx.x; i < SelShared<NT>::kBins; i += NT) sh.bins[i] = 0;
     if (threadIdx.x == 0) sh.list_n = 0;
     __syncthreads();
-#pragma unroll 8
-    for (int i = threadIdx.x; i < nc; i += kSelThreads) atomicAdd(&sh.bins[bin_of(keys[i])], 1);
+    // both passes read eight keys a thread before they use one
+    constexpr int kBatch = 8;
+    for (int i0 = threadIdx.x; i0 < nc; i0 += kBatch * NT) {
+        float k[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * NT < nc ? keys[i0 + j * NT] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (i0 + j * NT < nc) atomicAdd(&sh.bins[bin_of(k[j])], 1);
+    }
     __syncthreads();
     // the bin where the count from the top reaches want: thread t has the four
-    // bins below kBins - 4 t
+    // bins below SelShared<NT>::kBins - 4 t
     {
-        const int top = kBins - 1 - 4 * (int)threadIdx.x;
+        const int top = SelShared<NT>::kBins - 1 - 4 * (int)threadIdx.x;
         int c[4], sum = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum += c[j] = sh.bins[top - j];
@@ -335,25 +345,31 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const fl
     const float from = bin == 0 ? -INFINITY : lowest + (float)bin / scale - slack;
     const float to = lowest + (float)(bin + 1) / scale + slack;
     int near_above = 0;                                        // counted above the bin, but not settled
-#pragma unroll 4
-    for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
-        const int i = i0 + lane;
-        const float k = i < nc ? keys[i] : out_key();          // (NaN: in neither)
-        const uint32_t word = __ballot_sync(0xffffffffu, k > to);
-        if (lane == 0) taken[i0 >> 5] = word;
-        if (k >= from && k <= to) {
-            const int at = atomicAdd(&sh.list_n, 1);
-            if (at < kRankList) {
-                sh.list[at] = i;
-                sh.list_score[at] = k;
+    for (int i0 = warp * 32; i0 < nc; i0 += kBatch * NT) {
+        float k[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * NT + lane;
+            k[j] = i < nc ? keys[i] : out_key();               // (NaN: in neither)
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint32_t word = __ballot_sync(0xffffffffu, k[j] > to);
+            if (lane == 0 && i0 + j * NT < nc) taken[(i0 + j * NT) >> 5] = word;
+            if (k[j] >= from && k[j] <= to) {
+                const int at = atomicAdd(&sh.list_n, 1);
+                if (at < SelShared<NT>::kRankList) {
+                    sh.list[at] = i0 + j * NT + lane;
+                    sh.list_score[at] = k[j];
+                }
+                near_above += bin_of(k[j]) > bin;
             }
-            near_above += bin_of(k) > bin;
         }
     }
     int turn = 0;
     const int left = want - (sh.above - cta_sum(sh, near_above, turn));       // the list's places
     const int m = sh.list_n;
-    if (m > kRankList) return false;
+    if (m > SelShared<NT>::kRankList) return false;
     // rank by approximate score (the list's order varies, the ranks do not)
     const int e = threadIdx.x;
     const bool mine = e < m;
@@ -396,7 +412,7 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const fl
             if (mag > 0x1p-90f && mag < 0x1p120f) {
                 if (mine) sh.list_key[e] = open ? 1 : 0;       // below every key of a score
                 __syncthreads();
-                for (int w = warp; w < m * p.group; w += kSelWarps) {         // a warp per (block, head)
+                for (int w = warp; w < m * p.group; w += (NT / 32)) {         // a warp per (block, head)
                     const int o = w / p.group;
                     if (sh.list_key[o] == 0) continue;
                     const uint64_t x = ordered64(close_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane));
@@ -421,7 +437,7 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared& sh, const fl
             take = inside;
             if (mine) sh.list_key[e] = open ? 1 : 0;
             __syncthreads();
-            for (int w = warp; w < m * p.group; w += kSelWarps) {
+            for (int w = warp; w < m * p.group; w += (NT / 32)) {
                 const int o = w / p.group;
                 if (sh.list_key[o] == 0) continue;
                 const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
@@ -488,11 +504,11 @@ __device__ __forceinline__ void cluster_barrier(cg::cluster_group& cluster, int 
 // The query's two sides as the MMAs' second operand, [n-tile][step][lane]:
 // lane (g, t4) of step j has head g's elements 32 j + 8 t4 .. of (min(q, 0),
 // max(q, 0)). Followed by a barrier before their use.
-template <typename T, int D>
+template <typename T, int D, int NT>
 __device__ void stage_sides(const SelectParams& p, const SelRow& rw) {
     constexpr int STEPS = 2 * D / 32;
     const int ntiles = (p.group + 7) / 8;
-    for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += kSelThreads) {
+    for (int i = threadIdx.x; i < ntiles * STEPS * 32; i += NT) {
         const int l = i & 31, j = (i >> 5) % STEPS, nt = i / (32 * STEPS);
         const int g = nt * 8 + (l >> 2);
         const int e = 32 * j + 8 * (l & 3);
@@ -513,8 +529,8 @@ __device__ void stage_sides(const SelectParams& p, const SelRow& rw) {
 // first CTA, in rw.taken). All CTAs meet at two cluster barriers if rw.scored,
 // else at none; the sides have been staged. kOneTile: groups of at most eight
 // heads, one MMA tile.
-template <typename T, int D, bool kOneTile>
-__device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster_group& cluster,
+template <typename T, int D, bool kOneTile, int NT>
+__device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::cluster_group& cluster,
                                const SelRow& rw) {
     if (!rw.scored) return;
     constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
@@ -532,7 +548,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
         float worst = 0.f, lowest = INFINITY, highest = -INFINITY;
         if constexpr (std::is_same<T, float>::value) {
             constexpr int E = D / 32;
-            for (int i = rank * kSelWarps + warp; i < nc; i += C * kSelWarps) {
+            for (int i = rank * (NT / 32) + warp; i < nc; i += C * (NT / 32)) {
                 const int64_t blk = table[lo + i];
                 float best = -INFINITY;
                 if (blk >= 0 && blk < p.num_blocks) {
@@ -568,7 +584,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
             const int ntiles = (p.group + 7) / 8;
             const int g = lane >> 2, t4 = lane & 3;
             const int tiles = (nc + 15) / 16;
-            const int stride = C * kSelWarps;
+            const int stride = C * (NT / 32);
             // this lane's two blocks of a tile, and their bounds rows (block 0's
             // where the table names none)
             auto block_of = [&](int tile, int r) {
@@ -606,22 +622,26 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                             mag[r] = max_nan(mag[r], m[2 * r + e]);
                         }
             };
-            int tile = rank * kSelWarps + warp;
+            int tile = rank * (NT / 32) + warp;
             if constexpr (kOneTile) {
                 // the next quarter's loads are in flight while one is multiplied
                 Quarter buf[2];
-                int blk[2];
+                int blk[2], nblk[2];                            // this tile's blocks, the next one's
                 const T *x = nullptr, *y = nullptr;
+                auto after = [&](int t) { return t + stride < tiles ? t + stride : t; };
                 if (tile < tiles) {
-                    blk[0] = block_of(tile, 0);
-                    blk[1] = block_of(tile, 1);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        blk[r] = block_of(tile, r);
+                        nblk[r] = block_of(after(tile), r);
+                    }
                     x = row_of(blk[0]);
                     y = row_of(blk[1]);
                     buf[0].load(x, y);
                 }
                 for (; tile < tiles; tile += stride) {
-                    const int next = tile + stride < tiles ? tile + stride : tile;
-                    const int nblk[2] = {block_of(next, 0), block_of(next, 1)};
+                    const int next = after(tile);
+                    const int fblk[2] = {block_of(after(next), 0), block_of(after(next), 1)};
                     float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
@@ -638,8 +658,11 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                     float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
                     over_heads(0, c, m, best, mag);
                     finish(tile, blk, best, mag);
-                    blk[0] = nblk[0];
-                    blk[1] = nblk[1];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        blk[r] = nblk[r];
+                        nblk[r] = fblk[r];
+                    }
                 }
             } else {
                 for (; tile < tiles; tile += stride) {
@@ -673,7 +696,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
         }
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kSelWarps; ++w) {
+            for (int w = 1; w < (NT / 32); ++w) {
                 worst = max_nan(worst, sh.fpart[0][w]);
                 lowest = fminf(lowest, sh.fpart[1][w]);
                 highest = fmaxf(highest, sh.fpart[2][w]);
@@ -688,7 +711,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
 
     float mag = 0.f;
     for (int r = 0; r < C; ++r) mag = max_nan(mag, sh.err[r]);
-    if (take_by_histogram<T, D>(p, sh, keys, rw.taken, nc, want, mag, C, s, h, table + lo)) return;
+    if (take_by_histogram<T, D, NT>(p, sh, keys, rw.taken, nc, want, mag, C, s, h, table + lo)) return;
     {
         int turn = 0;
         uint32_t thr = 0;                                      // taken candidates: ordered(key) >= thr
@@ -700,10 +723,10 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
         double in_above = INFINITY, out_below = -INFINITY;
         if (finite) {
             bool exact;
-            thr = kth_largest<uint32_t>(sh, nc, want, turn, exact, [&](int i) { return ordered(keys[i]); },
+            thr = kth_largest<uint32_t, NT>(sh, nc, want, turn, exact, [&](int i) { return ordered(keys[i]); },
                                         [](int) { return false; });
             float a = INFINITY, b = -INFINITY;                 // the smallest taken, the largest left out
-            for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+            for (int i = threadIdx.x; i < nc; i += NT) {
                 const float k = keys[i];
                 if (ordered(k) >= thr) a = fminf(a, k);
                 else b = fmaxf(b, k);
@@ -718,7 +741,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                 sh.fpart[1][warp] = b;
             }
             __syncthreads();
-            for (int w = 0; w < kSelWarps; ++w) {
+            for (int w = 0; w < (NT / 32); ++w) {
                 a = fminf(a, sh.fpart[0][w]);
                 b = fmaxf(b, sh.fpart[1][w]);
             }
@@ -730,7 +753,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
         auto settled = [&](float k) { return finite && ((double)k > in_above || (double)k < out_below); };
         // count the certain ones and the unsettled
         int in = 0, open = 0;
-        for (int i = threadIdx.x; i < nc; i += kSelThreads) {
+        for (int i = threadIdx.x; i < nc; i += NT) {
             const float k = keys[i];
             if (!settled(k)) ++open;
             else in += (double)k > in_above;
@@ -741,11 +764,11 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
         if (!finite) thr = ordered(INFINITY);
         if (left < open) {
             // ------------------------------------------- exact scores of the unsettled
-            const bool small = open <= kRankList;
+            const bool small = open <= SelShared<NT>::kRankList;
             if (threadIdx.x == 0) sh.list_n = 0;
             __syncthreads();
             uint64_t* exact_keys = p.exact_keys + (size_t)row * p.max_ctx_blocks;
-            for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
+            for (int i0 = warp * 32; i0 < nc; i0 += NT) {
                 const bool mine = i0 + lane < nc && !settled(keys[i0 + lane]);
                 uint32_t votes = __ballot_sync(0xffffffffu, mine);
                 while (votes) {
@@ -777,15 +800,15 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                 }
             } else if (left > 0) {
                 bool exact;
-                const uint64_t t = kth_largest<uint64_t>(
+                const uint64_t t = kth_largest<uint64_t, NT>(
                     sh, nc, left, turn, exact, [&](int i) { return exact_keys[i]; },
                     [&](int i) { return settled(keys[i]); });
                 int above = 0;
-                for (int i = threadIdx.x; i < nc; i += kSelThreads)
+                for (int i = threadIdx.x; i < nc; i += NT)
                     above += !settled(keys[i]) && exact_keys[i] > t;
                 above = cta_sum(sh, above, turn);
                 int ties = exact ? 0x7fffffff : left - above;  // places for keys equal to t, lowest first
-                for (int i0 = 0; i0 < nc; i0 += kSelThreads) {
+                for (int i0 = 0; i0 < nc; i0 += NT) {
                     const int i = i0 + threadIdx.x;
                     const bool mine = i < nc && !settled(keys[i]);
                     const uint64_t k = mine ? exact_keys[i] : 0;
@@ -794,7 +817,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                     if (lane == 0) sh.part[turn][warp] = __popc(votes);
                     __syncthreads();
                     int at = __popc(votes & ((1u << lane) - 1)), total = 0;
-                    for (int w = 0; w < kSelWarps; ++w) {
+                    for (int w = 0; w < (NT / 32); ++w) {
                         if (w < warp) at += sh.part[turn][w];
                         total += sh.part[turn][w];
                     }
@@ -803,17 +826,17 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
                     if (!exact) ties -= total < ties ? total : ties;
                 }
             } else {
-                for (int i = threadIdx.x; i < nc; i += kSelThreads)
+                for (int i = threadIdx.x; i < nc; i += NT)
                     if (!settled(keys[i])) keys[i] = kOut;
             }
             __syncthreads();
         } else {
             // every unsettled block is taken: they are the candidates from out_below on
-            for (int i = threadIdx.x; i < nc; i += kSelThreads)
+            for (int i = threadIdx.x; i < nc; i += NT)
                 if (!settled(keys[i])) keys[i] = INFINITY;
             __syncthreads();
         }
-        for (int i0 = warp * 32; i0 < nc; i0 += kSelThreads) {
+        for (int i0 = warp * 32; i0 < nc; i0 += NT) {
             const uint32_t word = __ballot_sync(0xffffffffu, i0 + lane < nc && ordered(keys[i0 + lane]) >= thr);
             if (lane == 0) rw.taken[i0 >> 5] = word;
         }
@@ -823,19 +846,19 @@ __device__ void score_and_take(const SelectParams& p, SelShared& sh, cg::cluster
 
 // Calls put(position, block) for every block the row takes, positions in block
 // order (the first CTA, after score_and_take; any CTA where rw.all).
-template <typename Put>
-__device__ __forceinline__ void for_taken(SelShared& sh, const SelRow& rw, Put put) {
+template <int NT, typename Put>
+__device__ __forceinline__ void for_taken(SelShared<NT>& sh, const SelRow& rw, Put put) {
     if (rw.all) {
-        for (int b = threadIdx.x; b < rw.n; b += kSelThreads) put(b, b);
+        for (int b = threadIdx.x; b < rw.n; b += NT) put(b, b);
         return;
     }
-    for (int b = threadIdx.x; b < rw.lo; b += kSelThreads) put(b, b);
+    for (int b = threadIdx.x; b < rw.lo; b += NT) put(b, b);
     const int recent = rw.n - rw.lo - rw.nc;
-    for (int i = threadIdx.x; i < recent; i += kSelThreads) put(rw.lo + rw.want + i, rw.lo + rw.nc + i);
+    for (int i = threadIdx.x; i < recent; i += NT) put(rw.lo + rw.want + i, rw.lo + rw.nc + i);
     if (!rw.scored) return;
     // each thread has consecutive words of the candidates' bits
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int words = (rw.nc + 31) / 32, per = (words + kSelThreads - 1) / kSelThreads;
+    const int words = (rw.nc + 31) / 32, per = (words + NT - 1) / NT;
     const int w0 = threadIdx.x * per, w1 = min(w0 + per, words);
     int mine = 0;
     for (int w = w0; w < w1; ++w) mine += __popc(rw.taken[w]);
@@ -863,15 +886,13 @@ __device__ __forceinline__ int32_t slab_of(const SelectParams& p, const SelRow& 
 
 // ---------------------------------------------------------------- host side
 
-// CTAs per row.
+// CTAs per row: as many
+// as fit on 152 SMs with a tile of 16 blocks or more for every warp. For many
+// rows one CTA each wins, two on an SM: their selections overlap other rows'
+// scoring.
 inline int select_cluster(int rows, int max_ctx_blocks) {
-    // CTAs per row: while all fit on 152 SMs, two each, and every warp keeps a
-    // tile of 16 blocks or more. For many rows one CTA each wins, as their
-    // selections overlap other rows' scoring (512 rows of up to 2048 blocks:
-    // steps of 133, 141, 159 and 205 us with 1, 2, 4 and 8; 8 rows of 8192:
-    // 111, 72, 53, 43 and 39 us with 1, 2, 4, 8 and 16).
     int C = 1;
-    while (C < kMaxCluster && rows <= 152 / C && max_ctx_blocks >= 2 * C * kSelWarps * 16) C *= 2;
+    while (C < kMaxCluster && rows <= 152 / (2 * C) && max_ctx_blocks >= 2 * C * 256) C *= 2;
     return C;
 }
 
@@ -887,7 +908,7 @@ int select_smem(SelectParams& p) {
 }
 
 template <typename Kernel, typename Params>
-cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster, int smem,
+cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster, int threads, int smem,
                            cudaStream_t stream) {
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 200 * 1024);
     if (e != cudaSuccess) return e;
@@ -897,7 +918,7 @@ cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

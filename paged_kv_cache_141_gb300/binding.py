@@ -56,6 +56,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libpagedkv.so and declare its signatures (once)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -150,11 +152,15 @@ def _check(status: int, what: str) -> None:
         raise PagedKVError(what, status)
 
 
-def _dtype(t: torch.Tensor) -> int:
+def _dtype_code(dtype: torch.dtype) -> int:
     try:
-        return _DTYPES[t.dtype]
+        return _DTYPES[dtype]
     except KeyError:
-        raise TypeError(f"unsupported tensor dtype {t.dtype}") from None
+        raise TypeError(f"unsupported tensor dtype {dtype}") from None
+
+
+def _dtype(t: torch.Tensor) -> int:
+    return _dtype_code(t.dtype)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -467,27 +473,51 @@ def write_decode_shared_prefix(out, query, k_cache, v_cache, block_tables, conte
 MAX_ROPE_AXES = 4
 
 
-def _on_device(stream, first, *others):
-    """The stream for a call whose tensors must share one device: the given
-    one, or that device's current stream (whichever device is current)."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must live on one device")
+def _pointers(first, *tensors):
+    """Device index of `first` and the data pointers of all tensors (None for
+    None), which must be contiguous and on that device."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("tensor must live on a CUDA device")
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError("all tensors must live on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        out.append(t.data_ptr())
+    return dev, out
+
+
+def _call(fn, dev, stream, *args) -> int:
+    """fn(*args, stream) with device `dev` current; stream None: that device's
+    current stream. (The raw getters: a stream object and a device context cost
+    several microseconds each, as much as the launch.)"""
     if stream is None:
-        return torch.cuda.current_stream(first.device).cuda_stream
-    return _stream(stream)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
 
 
-def _token_rows(t, heads, head_size, what):
+def _token_rows(t, dev, tokens, heads, head_size, what):
     """Pointer and token stride of [T, heads, head_size] rows whose last two
     dimensions are contiguous (a view of a wider projection output is fine)."""
-    if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
-        raise ValueError(f"{what} must be [num_tokens, {heads}, {head_size}]")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_size):
+    if t.get_device() != dev:
+        raise ValueError("all tensors must live on one CUDA device")
+    T, h, d = t.shape
+    st, sh, sd = t.stride()
+    if T != tokens or h != heads or d != head_size:
+        raise ValueError(f"{what} must be [{tokens}, {heads}, {head_size}]")
+    if sd != 1 or (sh != d and h > 1):
         raise ValueError(f"{what}: each token's [heads, head_size] rows must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_size
+    return t.data_ptr(), st if T > 1 else h * d
 
 
 def rope_sections(sections) -> bytes:
@@ -508,43 +538,46 @@ def rope_and_cache(query_out, query, key, value, k_cache, v_cache, cos_sin, posi
     float32 [d] or None (no norm). adjacent_pairs: rotate components (2i, 2i+1)
     instead of (i, i + rotary_dim / 2). query, key and value may be views with
     any token stride; query_out may be query."""
-    T, Hq, D = query.shape
-    nb, Hkv, B, D2 = k_cache.shape
-    if v_cache.shape != k_cache.shape or D2 != D:
+    shape, dtype = query.shape, query.dtype
+    T, Hq, D = shape
+    nb, Hkv, B, D2 = cache_shape = k_cache.shape
+    if v_cache.shape != cache_shape or D2 != D:
         raise ValueError("inconsistent query/cache shapes")
-    if key.dtype != query.dtype or value.dtype != query.dtype or query_out.dtype != query.dtype:
+    if key.dtype != dtype or value.dtype != dtype or query_out.dtype != dtype:
         raise ValueError("query, key, value and query_out must share one dtype")
-    if v_cache.dtype != k_cache.dtype:
+    cache_dtype = k_cache.dtype
+    if v_cache.dtype != cache_dtype:
         raise ValueError("k_cache and v_cache must share one dtype")
-    if query_out.shape != query.shape or key.shape[0] != T or value.shape[0] != T:
-        raise ValueError("query_out, key and value must have the query's tokens")
+    if query_out.shape != shape:
+        raise ValueError("query_out must have the query's shape")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dtype != torch.int64 or positions.dim() > 2 or positions.shape[-1] != T or axes < 1:
+    max_position, rotary_dim = cos_sin.shape
+    pos_shape = positions.shape
+    axes = 1 if len(pos_shape) == 1 else pos_shape[0]
+    if positions.dtype != torch.int64 or len(pos_shape) > 2 or pos_shape[-1] != T or axes < 1:
         raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [num_tokens]")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != D):
-            raise ValueError("norm weights must be float32 [head_size]")
+    if q_weight is not None and (q_weight.dtype != torch.float32 or q_weight.numel() != D):
+        raise ValueError("norm weights must be float32 [head_size]")
+    if k_weight is not None and (k_weight.dtype != torch.float32 or k_weight.numel() != D):
+        raise ValueError("norm weights must be float32 [head_size]")
     fa = None
     if axes > 1:
-        if freq_axes is None or len(freq_axes) != cos_sin.shape[1] // 2:
+        if freq_axes is None or len(freq_axes) != rotary_dim // 2:
             raise ValueError("several axes need freq_axes, one axis for each of rotary_dim / 2 frequencies")
         fa = bytes(freq_axes)
-    q, qs = _token_rows(query, Hq, D, "query")
-    k, ks = _token_rows(key, Hkv, D, "key")
-    v, vs = _token_rows(value, Hkv, D, "value")
-    st = _on_device(stream, query, query_out, key, value, k_cache, v_cache, cos_sin, positions,
-                    slot_mapping, q_weight, k_weight, dev_status)
-    with torch.cuda.device(query.device):
-        status = lib().pa_rope_and_cache(
-            _ptr(query_out), q, qs, k, ks, v, vs, _ptr(k_cache), _ptr(v_cache), _ptr(cos_sin),
-            cos_sin.shape[0], cos_sin.shape[1], _ptr(positions), axes, fa, int(bool(adjacent_pairs)),
-            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(slot_mapping), T, Hq, Hkv, D, B, nb,
-            _dtype(query), _dtype(k_cache), float(k_scale), float(v_scale), _ptr(dev_status), st)
-    _check(status, "pa_rope_and_cache")
+    dev, (qo, kc, vc, cs, ps, sm, qw, kw, ds) = _pointers(
+        query, query_out, k_cache, v_cache, cos_sin, positions, slot_mapping, q_weight, k_weight,
+        dev_status)
+    q, q_stride = _token_rows(query, dev, T, Hq, D, "query")
+    k, k_stride = _token_rows(key, dev, T, Hkv, D, "key")
+    v, v_stride = _token_rows(value, dev, T, Hkv, D, "value")
+    _check(_call(lib().pa_rope_and_cache, dev, stream, qo, q, q_stride, k, k_stride, v, v_stride,
+                 kc, vc, cs, max_position, rotary_dim, ps, axes, fa, bool(adjacent_pairs), qw, kw,
+                 eps, sm, T, Hq, Hkv, D, B, nb, _dtype_code(dtype), _dtype_code(cache_dtype),
+                 k_scale, v_scale, ds), "pa_rope_and_cache")
 
 
 def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, new_tokens=None,
@@ -562,13 +595,11 @@ def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, n
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
     if new_tokens is not None and (new_tokens.dtype != torch.int32 or new_tokens.numel() != S):
         raise ValueError("new_tokens must be int32 [num_seqs]")
-    st = _on_device(stream, k_cache, k_bounds, block_tables, context_lens, new_tokens, dev_status)
-    with torch.cuda.device(k_cache.device):
-        status = lib().pa_key_bounds(
-            _ptr(k_bounds), _ptr(k_cache), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), _ptr(new_tokens), int(max_new_tokens), S, Hkv, D, B, nb,
-            int(max_context_len), _dtype(k_cache), _dtype(k_bounds), _ptr(dev_status), st)
-    _check(status, "pa_key_bounds")
+    dev, (kb, kc, bt, cl, nt, ds) = _pointers(k_cache, k_bounds, k_cache, block_tables,
+                                              context_lens, new_tokens, dev_status)
+    _check(_call(lib().pa_key_bounds, dev, stream, kb, kc, bt, block_tables.shape[1], cl, nt,
+                 max_new_tokens, S, Hkv, D, B, nb, max_context_len, _dtype_code(k_cache.dtype),
+                 _dtype_code(k_bounds.dtype), ds), "pa_key_bounds")
 
 
 def sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
@@ -601,16 +632,13 @@ def sparse_decode(out, query, k_cache, v_cache, k_bounds, block_tables, context_
         raise ValueError("k_bounds must be [num_blocks, num_kv_heads, 2, head_size] of the query's dtype")
     if selected is not None and (selected.dtype != torch.int32 or selected.shape != (S, Hkv, num_select)):
         raise ValueError("selected must be int32 [num_seqs, num_kv_heads, num_select]")
-    st = _on_device(stream, query, out, k_cache, v_cache, k_bounds, block_tables, context_lens,
-                    selected, workspace, dev_status)
-    with torch.cuda.device(query.device):
-        status = lib().pa_sparse_decode(
-            _ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache), _ptr(k_bounds),
-            _ptr(block_tables), mb, _ptr(context_lens), S, Hq, Hkv, D, B, nb, int(max_context_len),
-            float(scale), int(num_select), int(first_blocks), int(recent_blocks), _ptr(selected),
-            _dtype(query), _dtype(k_cache), float(k_scale), float(v_scale), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(dev_status), st)
-    _check(status, "pa_sparse_decode")
+    dev, (o, q, kc, vc, kb, bt, cl, sel, ws, ds) = _pointers(
+        query, out, query, k_cache, v_cache, k_bounds, block_tables, context_lens, selected,
+        workspace, dev_status)
+    _check(_call(lib().pa_sparse_decode, dev, stream, o, q, kc, vc, kb, bt, mb, cl, S, Hq, Hkv, D,
+                 B, nb, max_context_len, scale, num_select, first_blocks, recent_blocks, sel,
+                 _dtype_code(query.dtype), _dtype_code(k_cache.dtype), k_scale, v_scale, ws,
+                 workspace.numel() * workspace.element_size(), ds), "pa_sparse_decode")
 
 
 STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024

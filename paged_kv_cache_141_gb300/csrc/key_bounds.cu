@@ -6,12 +6,14 @@
 // (whole blocks: no state carries over from earlier calls, and a repeated or
 // replayed call gives the same bounds).
 //
-// One warp per (sequence, touched block, KV head): D / 8 lanes hold a token's
-// row, eight elements each, and the warp's 256 / D lane groups take
-// alternate tokens. Comparisons are exact, so the order of tokens does not
-// matter; a NaN key makes both of its component's bounds NaN. E4M3 codes
-// widen exactly to binary16 and from there to bfloat16. Bound by reading the
-// keys once (bandwidth), or by launch and load latency for a decode step.
+// One warp per (sequence, touched block, KV head). A row's lanes hold 16 bytes
+// each (32 for binary32) and the warp's lane groups take alternate tokens, four
+// loads of each in flight; the comparisons run on packed 16-bit pairs, E4M3
+// codes widened to binary16 (exactly). Across the groups, one half of the warp
+// reduces the minima and the other the maxima. Comparisons are exact, so the
+// order of tokens does not matter; a NaN key makes both of its component's
+// bounds NaN. Bound by reading the keys once (bandwidth), or by launch and load
+// latency for a decode step.
 #include "device_common.cuh"
 #include "launch.h"
 
@@ -32,37 +34,133 @@ __device__ __forceinline__ float nan_max(float a, float b) {
     return r;
 }
 
-template <typename CT, typename BT, int D>
-__global__ void __launch_bounds__(kBoundsThreads)
-key_bounds_kernel(const __grid_constant__ BoundsParams p) {
-    constexpr int LANES = D / 8;               // lanes per token row
-    constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
-    const int lane = threadIdx.x & 31;
+// This warp's block: the slab (block * Hkv + head) and the tokens it holds, 0
+// where there is nothing to do.
+__device__ __forceinline__ int bounds_unit(const BoundsParams& p, int lane, size_t& slab) {
     const int64_t unit = ((int64_t)blockIdx.x * kBoundsThreads + threadIdx.x) >> 5;
     const int64_t sj = unit / p.num_kv_heads;
     const int h = (int)(unit - sj * p.num_kv_heads);
     const int s = (int)(sj / p.touched);
-    if (s >= p.num_seqs) return;
+    if (s >= p.num_seqs) return 0;
     const int B = p.block_size;
     const int L = p.context_lens[s];
     const int n = p.new_tokens ? p.new_tokens[s] : (L > 0 ? 1 : 0);
     const int64_t tab = (int64_t)p.max_blocks * B;
     if (L < 0 || L > p.max_context_len || L > tab || n < 0 || n > L || n > p.max_new_tokens) {
         if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_LEN);
-        return;
+        return 0;
     }
-    if (n == 0) return;
-    const int j = (L - n) / B + (int)(sj - (int64_t)s * p.touched);
-    if ((int64_t)j * B >= L) return;
+    if (n == 0) return 0;
+    const int64_t j = (L - n) / B + (sj - (int64_t)s * p.touched);
+    if (j * B >= L) return 0;
     const int64_t blk = p.block_tables[(size_t)s * p.max_blocks + j];
     if (blk < 0 || blk >= p.num_blocks) {
         if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
-        return;
+        return 0;
     }
-    const int tokens = min(B, L - j * B);
+    slab = (size_t)blk * p.num_kv_heads + h;
+    return min(B, L - (int)j * B);
+}
+
+// Packed pairs of a 16-bit type: the cache's own, or binary16 for E4M3 codes.
+template <typename CT> struct Pairs { using T2 = __half2; };
+template <> struct Pairs<__nv_bfloat16> { using T2 = __nv_bfloat162; };
+
+template <typename CT, typename BT, int D>
+__global__ void __launch_bounds__(kBoundsThreads)
+key_bounds_kernel(const __grid_constant__ BoundsParams p) {
+    constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
+    using T2 = typename Pairs<CT>::T2;
+    constexpr int E = 16 / (int)sizeof(CT);    // elements per lane
+    constexpr int W = E / 2;                   // pairs per lane
+    constexpr int LANES = D / E;               // lanes per token row
+    constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
+    constexpr int kBatch = 4;
+    const int lane = threadIdx.x & 31;
+    size_t slab = 0;
+    const int tokens = bounds_unit(p, lane, slab);
+    if (tokens == 0) return;
+    const int c = (lane & (LANES - 1)) * E;
+    const CT* keys = static_cast<const CT*>(p.k_cache) + slab * p.block_size * D + c;
+    auto as2 = [](uint32_t w) { return *reinterpret_cast<T2*>(&w); };
+    auto bits = [](T2 x) { return *reinterpret_cast<uint32_t*>(&x); };
+    T2 lo[W], hi[W];
+    const int r0 = lane / LANES;
+    // a lane group without a token of its own starts from the first token too
+    for (int r = 0; r < tokens; r += kBatch * ROWS) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int t = r + k * ROWS + r0;
+            x[k] = *reinterpret_cast<const uint4*>(keys + (size_t)(t < tokens ? t : 0) * D);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                T2 v;
+                if constexpr (kFp8) {
+                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                        static_cast<__nv_fp8x2_storage_t>(ws[i / 2] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3);
+                    v = *reinterpret_cast<const T2*>(&h);
+                } else {
+                    v = as2(ws[i]);
+                }
+                lo[i] = r == 0 && k == 0 ? v : __hmin2_nan(lo[i], v);
+                hi[i] = r == 0 && k == 0 ? v : __hmax2_nan(hi[i], v);
+            }
+        }
+    }
+    auto store = [&](BT* out, const T2 (&v)[W]) {
+        uint32_t w[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (kFp8 && std::is_same<BT, __nv_bfloat16>::value) {
+                const __nv_bfloat162 b = __float22bfloat162_rn(__half22float2(v[i]));      // exact
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                w[i] = bits(v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+            *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    };
+    BT* out = static_cast<BT*>(p.k_bounds) + slab * 2 * D + c;
+    if constexpr (ROWS == 1) {
+        store(out, lo);
+        store(out + D, hi);
+    } else {
+        // lanes 0-15 go on with the minima, 16-31 with the maxima
+        const bool upper = lane >= 16;
+        T2 v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const T2 o = as2(__shfl_xor_sync(0xffffffffu, bits(upper ? lo[i] : hi[i]), 16));
+            v[i] = upper ? __hmax2_nan(hi[i], o) : __hmin2_nan(lo[i], o);
+#pragma unroll
+            for (int m = 8; m >= LANES; m >>= 1) {
+                const T2 y = as2(__shfl_xor_sync(0xffffffffu, bits(v[i]), m));
+                v[i] = upper ? __hmax2_nan(v[i], y) : __hmin2_nan(v[i], y);
+            }
+        }
+        if ((lane & 15) < LANES) store(out + (upper ? D : 0), v);
+    }
+}
+
+// Binary32 caches: eight elements per lane.
+template <int D>
+__global__ void __launch_bounds__(kBoundsThreads)
+key_bounds_f32_kernel(const __grid_constant__ BoundsParams p) {
+    constexpr int LANES = D / 8;               // lanes per token row
+    constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
+    const int lane = threadIdx.x & 31;
+    size_t slab = 0;
+    const int tokens = bounds_unit(p, lane, slab);
+    if (tokens == 0) return;
     const int c = (lane & (LANES - 1)) * 8;
-    const size_t slab = (size_t)blk * p.num_kv_heads + h;
-    const CT* keys = static_cast<const CT*>(p.k_cache) + slab * B * D + c;
+    const float* keys = static_cast<const float*>(p.k_cache) + slab * p.block_size * D + c;
     float lo[8], hi[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -72,7 +170,7 @@ key_bounds_kernel(const __grid_constant__ BoundsParams p) {
 #pragma unroll 4
     for (int r = lane / LANES; r < tokens; r += ROWS) {
         float x[8];
-        RowLoader<CT, 8>::load(keys + (size_t)r * D, x);
+        RowLoader<float, 8>::load(keys + (size_t)r * D, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             lo[i] = nan_min(lo[i], x[i]);
@@ -87,14 +185,12 @@ key_bounds_kernel(const __grid_constant__ BoundsParams p) {
             hi[i] = nan_max(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], m));
         }
     }
-    // the values are the cache's own, so the conversions below are exact
-    if (lane < 2 * LANES || ROWS == 1) {
-        BT* out = static_cast<BT*>(p.k_bounds) + slab * 2 * D + c;
+    if (lane < LANES) {
+        float* out = static_cast<float*>(p.k_bounds) + slab * 2 * D + c;
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            if (ROWS > 1 && side != lane / LANES) continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) out[side * D + i] = from_float<BT>(side ? hi[i] : lo[i]);
+        for (int i = 0; i < 8; i += 4) {
+            *reinterpret_cast<float4*>(out + i) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+            *reinterpret_cast<float4*>(out + D + i) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
         }
     }
 }
@@ -104,10 +200,19 @@ cudaError_t launch_bounds(const BoundsParams& p, int head_size, cudaStream_t str
     const int64_t units = (int64_t)p.num_seqs * p.touched * p.num_kv_heads;
     const int64_t grid = (units * 32 + kBoundsThreads - 1) / kBoundsThreads;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    switch (head_size) {
-    case 64: key_bounds_kernel<CT, BT, 64><<<(unsigned)grid, kBoundsThreads, 0, stream>>>(p); break;
-    case 128: key_bounds_kernel<CT, BT, 128><<<(unsigned)grid, kBoundsThreads, 0, stream>>>(p); break;
-    default: key_bounds_kernel<CT, BT, 256><<<(unsigned)grid, kBoundsThreads, 0, stream>>>(p); break;
+    auto launch = [&](auto kernel) { kernel<<<(unsigned)grid, kBoundsThreads, 0, stream>>>(p); };
+    if constexpr (std::is_same<CT, float>::value) {
+        switch (head_size) {
+        case 64: launch(key_bounds_f32_kernel<64>); break;
+        case 128: launch(key_bounds_f32_kernel<128>); break;
+        default: launch(key_bounds_f32_kernel<256>); break;
+        }
+    } else {
+        switch (head_size) {
+        case 64: launch(key_bounds_kernel<CT, BT, 64>); break;
+        case 128: launch(key_bounds_kernel<CT, BT, 128>); break;
+        default: launch(key_bounds_kernel<CT, BT, 256>); break;
+        }
     }
     return cudaGetLastError();
 }

@@ -160,17 +160,14 @@ struct RopeParams {
     const float* k_weight;
     uint32_t* status;             // may be null
     int64_t total_tokens;         // T
-    int64_t first_token;          // of this launch
     int64_t max_position;
     int64_t num_blocks;
-    int num_tokens;               // of this launch
     int num_axes;                 // 1..4
     int rotary_dim;
     int adjacent_pairs;           // pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
     int num_q_heads;
     int num_kv_heads;
     int block_size;
-    int groups;                   // row groups per token
     float eps;
     float k_scale;
     float v_scale;

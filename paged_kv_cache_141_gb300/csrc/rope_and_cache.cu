@@ -27,6 +27,10 @@ namespace pagedkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// The prompt kernel from four token-warps per SM on (152 SMs): one prompt of 400
+// tokens takes 4.8 us with a row per 8 lanes and 6.2 with a token per warp (32/8
+// heads, bf16), 1000 tokens 8.3 and 6.2, 1373 tokens 13.1 and 9.0.
+constexpr int64_t kPromptTokens = 152 * 4;
 
 // Eight consecutive elements of type T as 16-byte words.
 template <typename T>
@@ -87,191 +91,288 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* dst, const float (&x)[8], f
     *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
 }
 
-// One head row per D / 16 lanes; a row group takes every `groups`-th of its
-// token's Hq + 2 Hkv rows (queries, keys, values), up to kRows of them, with
-// all their loads issued before the first is used.
-template <typename T, bool kE4M3, int D, int kRows>
+// A lane's place in its head row: chunks a and b (eight elements each), and the
+// cosines and sines of its eight pairs.
+template <typename T, int D>
+struct Turn {
+    static constexpr int LANES = D / 16;
+    int a_off, b_off;
+    bool rotates, adjacent;
+    uint32_t mask;                                             // the row's lanes
+    float cs[8], sn[8];
+
+    __device__ __forceinline__ Turn(const RopeParams& p, int lane) {
+        const int c = lane & (LANES - 1);
+        rotates = 16 * c < p.rotary_dim;
+        adjacent = p.adjacent_pairs;
+        a_off = 16 * c;
+        b_off = 16 * c + 8;
+        if (!adjacent && rotates) {
+            a_off = 8 * c;
+            b_off = (p.rotary_dim >> 1) + 8 * c;
+        }
+        mask = (uint32_t)((1ull << LANES) - 1) << (lane & ~(LANES - 1));
+    }
+
+    // The token's positions into angles; false: one lies outside the table.
+    __device__ __forceinline__ bool load(const RopeParams& p, int64_t t, int lane) {
+        const int c = lane & (LANES - 1);
+        const int half = p.rotary_dim >> 1;
+        int64_t pos[4];
+        bool ok = true;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            pos[a] = p.positions[(a < p.num_axes ? a : 0) * p.total_tokens + t];
+            ok = ok && pos[a] >= 0 && pos[a] < p.max_position;
+        }
+        if (!ok) return false;
+        if (!rotates) return true;
+        const uint32_t axes = p.num_axes == 1 ? 0 : (p.freq_axes[c >> 1] >> (16 * (c & 1))) & 0xffffu;
+        auto row_of = [&](uint32_t a) {                        // table row of axis a, at this lane's frequencies
+            return p.cos_sin + (a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]) * p.rotary_dim + 8 * c;
+        };
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const uint32_t four = (axes >> (2 * j)) & 0xffu;
+            if (four == (four & 3) * 0x55u) {                  // the four frequencies follow one axis
+                const float* row = row_of(four & 3) + j;
+                const float4 x = *reinterpret_cast<const float4*>(row);
+                const float4 y = *reinterpret_cast<const float4*>(row + half);
+                cs[j] = x.x; cs[j + 1] = x.y; cs[j + 2] = x.z; cs[j + 3] = x.w;
+                sn[j] = y.x; sn[j + 1] = y.y; sn[j + 2] = y.z; sn[j + 3] = y.w;
+            } else {
+#pragma unroll
+                for (int k = j; k < j + 4; ++k) {
+                    const float* row = row_of((axes >> (2 * k)) & 3) + k;
+                    cs[k] = row[0];
+                    sn[k] = row[half];
+                }
+            }
+        }
+        return true;
+    }
+
+    __device__ __forceinline__ void norm(float (&a)[8], float (&b)[8], const float (&wa)[8],
+                                         const float (&wb)[8], float eps) const {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+#pragma unroll
+        for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
+        const float r = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[j] *= r * wa[j];
+            b[j] *= r * wb[j];
+        }
+    }
+
+    __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8]) const {
+        if (!rotates) return;
+        if (adjacent) {
+            // a and b are 16 neighbouring components: pairs (2j, 2j + 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float u = a[2 * j], v = a[2 * j + 1], y = b[2 * j], z = b[2 * j + 1];
+                a[2 * j] = u * cs[j] - v * sn[j];
+                a[2 * j + 1] = v * cs[j] + u * sn[j];
+                b[2 * j] = y * cs[j + 4] - z * sn[j + 4];
+                b[2 * j + 1] = z * cs[j + 4] + y * sn[j + 4];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = a[j], v = b[j];
+                a[j] = u * cs[j] - v * sn[j];
+                b[j] = v * cs[j] + u * sn[j];
+            }
+        }
+    }
+};
+
+// The slot's row under KV head 0 (rows are D elements), or -1: nothing stored.
+__device__ __forceinline__ int64_t cache_row(const RopeParams& p, int64_t slot) {
+    if (slot < 0 || slot >= p.num_blocks * p.block_size) return -1;
+    const int64_t blk = slot / p.block_size;
+    return blk * p.num_kv_heads * p.block_size + (slot - blk * p.block_size);
+}
+
+__device__ __forceinline__ void flag_token(const RopeParams& p, bool ok, int64_t slot, int64_t row) {
+    if (!p.status) return;
+    if (!ok) atomicOr(p.status, PA_DEV_BAD_POSITION);
+    if (slot >= 0 && row < 0) atomicOr(p.status, PA_DEV_BAD_SLOT);
+}
+
+// Decode steps: one head row per D / 16 lanes and nothing more, so that all of
+// a step's latencies overlap.
+template <typename T, bool kE4M3, int D>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     constexpr int LANES = D / 16;
     const int lane = threadIdx.x & 31;
     const uint32_t g = (blockIdx.x * (uint32_t)kRopeThreads + threadIdx.x) / LANES;
-    const int c = lane & (LANES - 1);
-    const uint32_t tl = g / (uint32_t)p.groups;
-    if (tl >= (uint32_t)p.num_tokens) return;
-    const int64_t t = p.first_token + tl;
-    const int h0 = (int)(g - tl * (uint32_t)p.groups);
-    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, H = Hq + 2 * Hkv;
-    const int half = p.rotary_dim >> 1;
-    const bool rotates = 16 * c < p.rotary_dim;
-    // element offsets of the lane's two chunks in a head row
-    int a_off = 16 * c, b_off = 16 * c + 8;
-    if (!p.adjacent_pairs && rotates) {
-        a_off = 8 * c;
-        b_off = half + 8 * c;
+    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
+    const uint32_t H = Hq + 2 * Hkv;
+    const uint32_t tl = g / H;
+    if (tl >= (uint32_t)p.total_tokens) return;
+    const int64_t t = tl;
+    const int h = (int)(g - tl * H);
+    const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
+    Turn<T, D> turn(p, lane);
+    const T* src;
+    if (is_q) src = static_cast<const T*>(p.query) + t * p.query_stride + (int64_t)h * D;
+    else if (!is_v) src = static_cast<const T*>(p.key) + t * p.key_stride + (int64_t)(h - Hq) * D;
+    else src = static_cast<const T*>(p.value) + t * p.value_stride + (int64_t)(h - Hq - Hkv) * D;
+    Chunk<T> xa, xb;
+    xa.load(src + turn.a_off);
+    xb.load(src + turn.b_off);
+    const float* w = is_v ? nullptr : (is_q ? p.q_weight : p.k_weight);
+    float wa[8], wb[8];
+    if (w) {
+        RowLoader<float, 8>::load(w + turn.a_off, wa);
+        RowLoader<float, 8>::load(w + turn.b_off, wb);
     }
-
-    Chunk<T> xa[kRows], xb[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int h = h0 + i * p.groups;
-        if (h < H) {
-            const T* src;
-            if (h < Hq) src = static_cast<const T*>(p.query) + t * p.query_stride + (int64_t)h * D;
-            else if (h < Hq + Hkv) src = static_cast<const T*>(p.key) + t * p.key_stride + (int64_t)(h - Hq) * D;
-            else src = static_cast<const T*>(p.value) + t * p.value_stride + (int64_t)(h - Hq - Hkv) * D;
-            xa[i].load(src + a_off);
-            xb[i].load(src + b_off);
-        }
-    }
-
     const int64_t slot = p.slots[t];
-    int64_t pos[4];
-    bool ok = true;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        pos[a] = p.positions[(a < p.num_axes ? a : 0) * p.total_tokens + t];
-        ok = ok && pos[a] >= 0 && pos[a] < p.max_position;
+    const bool ok = turn.load(p, t, lane);
+    const int64_t row0 = cache_row(p, slot);
+    if (h == 0 && (lane & (LANES - 1)) == 0) flag_token(p, ok, slot, row0);
+    if (!ok || (!is_q && row0 < 0)) return;                    // the token, or its store, is skipped
+    const size_t dst = is_q ? (size_t)(t * Hq + h) * D
+                            : (size_t)(row0 + (int64_t)(h - Hq - (is_v ? Hkv : 0)) * p.block_size) * D;
+    if (is_v && !kE4M3) {
+        xa.store(static_cast<T*>(p.v_cache) + dst + turn.a_off);
+        xb.store(static_cast<T*>(p.v_cache) + dst + turn.b_off);
+        return;
     }
-    const bool stores = slot >= 0 && slot < p.num_blocks * p.block_size;
-    if (h0 == 0 && c == 0 && p.status) {
-        if (!ok) atomicOr(p.status, PA_DEV_BAD_POSITION);
-        if (slot >= 0 && !stores) atomicOr(p.status, PA_DEV_BAD_SLOT);
-    }
-    if (!ok) return;                                          // the whole token is skipped
-
-    float cs[8], sn[8];
-    if (rotates) {
-        const uint32_t axes = p.num_axes == 1 ? 0 : (p.freq_axes[c >> 1] >> (16 * (c & 1))) & 0xffffu;
-        const uint32_t a0 = axes & 3;
-        if (axes == a0 * 0x5555u) {                           // the eight frequencies follow one axis
-            const int64_t q = a0 == 0 ? pos[0] : a0 == 1 ? pos[1] : a0 == 2 ? pos[2] : pos[3];
-            const float* row = p.cos_sin + q * p.rotary_dim + 8 * c;
-            RowLoader<float, 8>::load(row, cs);
-            RowLoader<float, 8>::load(row + half, sn);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t a = (axes >> (2 * j)) & 3;
-                const int64_t q = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-                const float* row = p.cos_sin + q * p.rotary_dim + 8 * c + j;
-                cs[j] = row[0];
-                sn[j] = row[half];
-            }
-        }
+    float a[8], b[8];
+    xa.widen(a);
+    xb.widen(b);
+    if (w) turn.norm(a, b, wa, wb, p.eps);
+    if (!is_v) turn.rotate(a, b);
+    if (!is_q && kE4M3) {
+        uint8_t* y = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + dst;
+        store8_e4m3(y + turn.a_off, a, is_v ? p.v_scale : p.k_scale);
+        store8_e4m3(y + turn.b_off, b, is_v ? p.v_scale : p.k_scale);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) { cs[j] = 1.f; sn[j] = 0.f; }
-    }
-    size_t cache_row = 0;                                     // row of the token's slot under KV head 0
-    if (stores) {
-        const int64_t blk = slot / p.block_size;
-        cache_row = (size_t)blk * Hkv * p.block_size + (size_t)(slot - blk * p.block_size);
-    }
-    const uint32_t mask = (uint32_t)((1ull << LANES) - 1) << (lane & ~(LANES - 1));
-
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int h = h0 + i * p.groups;
-        if (h >= H) break;
-        const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-        if (!is_q && !stores) continue;
-        const size_t dst = is_q ? (size_t)(t * Hq + h) * D
-                                : (cache_row + (size_t)(h - Hq - (is_v ? Hkv : 0)) * p.block_size) * D;
-        if (is_v) {
-            if constexpr (kE4M3) {
-                float x[8];
-                uint8_t* v = static_cast<uint8_t*>(p.v_cache) + dst;
-                xa[i].widen(x);
-                store8_e4m3(v + a_off, x, p.v_scale);
-                xb[i].widen(x);
-                store8_e4m3(v + b_off, x, p.v_scale);
-            } else {
-                T* v = static_cast<T*>(p.v_cache) + dst;
-                xa[i].store(v + a_off);
-                xb[i].store(v + b_off);
-            }
-            continue;
-        }
-        float a[8], b[8];
-        xa[i].widen(a);
-        xb[i].widen(b);
-        const float* w = is_q ? p.q_weight : p.k_weight;
-        if (w) {
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
-#pragma unroll
-            for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
-            const float r = rsqrtf(ss * (1.f / D) + p.eps);
-            float wa[8], wb[8];
-            RowLoader<float, 8>::load(w + a_off, wa);
-            RowLoader<float, 8>::load(w + b_off, wb);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[j] *= r * wa[j];
-                b[j] *= r * wb[j];
-            }
-        }
-        if (rotates) {
-            if (p.adjacent_pairs) {
-                // a and b are 16 neighbouring components: pairs (2j, 2j + 1)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float u = a[2 * j], v = a[2 * j + 1], y = b[2 * j], z = b[2 * j + 1];
-                    a[2 * j] = u * cs[j] - v * sn[j];
-                    a[2 * j + 1] = v * cs[j] + u * sn[j];
-                    b[2 * j] = y * cs[j + 4] - z * sn[j + 4];
-                    b[2 * j + 1] = z * cs[j + 4] + y * sn[j + 4];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = a[j], v = b[j];
-                    a[j] = u * cs[j] - v * sn[j];
-                    b[j] = v * cs[j] + u * sn[j];
-                }
-            }
-        }
-        if (!is_q && kE4M3) {
-            uint8_t* k = static_cast<uint8_t*>(p.k_cache) + dst;
-            store8_e4m3(k + a_off, a, p.k_scale);
-            store8_e4m3(k + b_off, b, p.k_scale);
-        } else {
-            T* y = (is_q ? static_cast<T*>(p.query_out) : static_cast<T*>(p.k_cache)) + dst;
-            xa[i].round_from(a);
-            xb[i].round_from(b);
-            xa[i].store(y + a_off);
-            xb[i].store(y + b_off);
-        }
+        T* y = static_cast<T*>(is_q ? p.query_out : p.k_cache) + dst;
+        xa.round_from(a);
+        xb.round_from(b);
+        xa.store(y + turn.a_off);
+        xb.store(y + turn.b_off);
     }
 }
 
+// Prompts: one warp per token, so that its angles and the weights are loaded
+// once for all its heads (several warps per token, each loading them, measured
+// slower at every length: 8000 tokens 38.7, 38.7, 44.8 and 66.3 us with 1, 2, 4
+// and 8). The warp's 512 / D row groups take alternate heads, kRows of them with
+// all loads issued before the first is used; the first ones of the queries are on
+// their way while the token's position becomes angles.
 template <typename T, bool kE4M3, int D, int kRows>
-cudaError_t launch_rows(RopeParams p, cudaStream_t stream) {
-    constexpr int kPerCta = kRopeThreads / (D / 16);
-    p.groups = (p.num_q_heads + 2 * p.num_kv_heads + kRows - 1) / kRows;
-    // token ranges whose thread indices stay below 2^31
-    int64_t step = (1ll << 30) / ((int64_t)p.groups * (D / 16));
-    if (step < 1) step = 1;
-    for (int64_t t0 = 0; t0 < p.total_tokens; t0 += step) {
-        const int64_t n = p.total_tokens - t0 < step ? p.total_tokens - t0 : step;
-        p.first_token = t0;
-        p.num_tokens = (int)n;
-        const int64_t grid = (n * p.groups + kPerCta - 1) / kPerCta;
-        rope_and_cache_kernel<T, kE4M3, D, kRows><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+__global__ void __launch_bounds__(kRopeThreads, 2)
+rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int LANES = D / 16;
+    const int lane = threadIdx.x & 31;
+    constexpr int GROUPS = 32 / LANES;
+    const int grp = lane / LANES;
+    const int64_t t = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+    if (t >= p.total_tokens) return;
+    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, B = p.block_size;
+    Turn<T, D> turn(p, lane);
+    Chunk<T> xa[kRows], xb[kRows];
+    auto load = [&](const T* src, int h0, int heads) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int h = h0 + i * GROUPS;
+            if (h < heads) {
+                xa[i].load(src + (int64_t)h * D + turn.a_off);
+                xb[i].load(src + (int64_t)h * D + turn.b_off);
+            }
+        }
+    };
+    const T* query = static_cast<const T*>(p.query) + t * p.query_stride;
+    load(query, grp, Hq);
+    const int64_t slot = p.slots[t];
+    const bool ok = turn.load(p, t, lane);
+    const int64_t row0 = cache_row(p, slot);
+    if (lane == 0) flag_token(p, ok, slot, row0);
+    if (!ok) return;
+
+    // one kind of rows: `heads` of them from src, row h to dst + h * step
+    auto rows = [&](auto kind, const T* src, void* dst, int heads, size_t step, const float* w, float scale) {
+        constexpr int kKind = decltype(kind)::value;           // 0 queries, 1 keys, 2 values
+        constexpr bool kCodes = kE4M3 && kKind != 0;
+        float wa[8], wb[8];
+        if (kKind != 2 && w) {
+            RowLoader<float, 8>::load(w + turn.a_off, wa);
+            RowLoader<float, 8>::load(w + turn.b_off, wb);
+        }
+        for (int h0 = grp; h0 < heads; h0 += kRows * GROUPS) {
+            if (kKind != 0 || h0 != grp) load(src, h0, heads);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int h = h0 + i * GROUPS;
+                if (h >= heads) break;
+                if (kKind == 2 && !kCodes) {
+                    T* y = static_cast<T*>(dst) + h * step;
+                    xa[i].store(y + turn.a_off);
+                    xb[i].store(y + turn.b_off);
+                    continue;
+                }
+                float a[8], b[8];
+                xa[i].widen(a);
+                xb[i].widen(b);
+                if (kKind != 2) {
+                    if (w) turn.norm(a, b, wa, wb, p.eps);
+                    turn.rotate(a, b);
+                }
+                if constexpr (kCodes) {
+                    uint8_t* y = static_cast<uint8_t*>(dst) + h * step;
+                    store8_e4m3(y + turn.a_off, a, scale);
+                    store8_e4m3(y + turn.b_off, b, scale);
+                } else {
+                    T* y = static_cast<T*>(dst) + h * step;
+                    xa[i].round_from(a);
+                    xb[i].round_from(b);
+                    xa[i].store(y + turn.a_off);
+                    xb[i].store(y + turn.b_off);
+                }
+            }
+        }
+    };
+    rows(std::integral_constant<int, 0>{}, query,
+         static_cast<T*>(p.query_out) + (size_t)t * Hq * D, Hq, D, p.q_weight, 1.f);
+    if (row0 < 0) return;
+    constexpr int kCell = kE4M3 ? 1 : (int)sizeof(T);
+    const size_t step = (size_t)B * D;
+    rows(std::integral_constant<int, 1>{}, static_cast<const T*>(p.key) + t * p.key_stride,
+         static_cast<uint8_t*>(p.k_cache) + (size_t)row0 * D * kCell, Hkv, step, p.k_weight, p.k_scale);
+    rows(std::integral_constant<int, 2>{}, static_cast<const T*>(p.value) + t * p.value_stride,
+         static_cast<uint8_t*>(p.v_cache) + (size_t)row0 * D * kCell, Hkv, step, nullptr, p.v_scale);
+}
+
+template <typename T, bool kE4M3, int D>
+cudaError_t launch_head_size(RopeParams p, cudaStream_t stream) {
+    const int64_t H = p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
+    constexpr int LANES = D / 16;
+    if (p.total_tokens > kPromptTokens) {
+        constexpr int kRows = sizeof(T) == 4 ? 2 : 4;
+        const int64_t grid = (p.total_tokens * 32 + kRopeThreads - 1) / kRopeThreads;
+        if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+        rope_and_cache_prompt_kernel<T, kE4M3, D, kRows><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
+    } else {
+        const int64_t grid = (p.total_tokens * H * LANES + kRopeThreads - 1) / kRopeThreads;
+        rope_and_cache_kernel<T, kE4M3, D><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
     }
-    return cudaSuccess;
+    return cudaGetLastError();
 }
 
 template <typename T, bool kE4M3>
 cudaError_t launch_rope(const RopeParams& p, int head_size, cudaStream_t stream) {
     switch (head_size) {
-    case 64: return launch_rows<T, kE4M3, 64, 1>(p, stream);
-    case 128: return launch_rows<T, kE4M3, 128, 1>(p, stream);
-    default: return launch_rows<T, kE4M3, 256, 1>(p, stream);
+    case 64: return launch_head_size<T, kE4M3, 64>(p, stream);
+    case 128: return launch_head_size<T, kE4M3, 128>(p, stream);
+    default: return launch_head_size<T, kE4M3, 256>(p, stream);
     }
 }
 

@@ -34,14 +34,14 @@ __device__ __forceinline__ float nan_max(float a, float b) {
     return r;
 }
 
-// This warp's block: the slab (block * Hkv + head) and the tokens it holds, 0
-// where there is nothing to do.
-__device__ __forceinline__ int bounds_unit(const BoundsParams& p, int lane, size_t& slab) {
-    const int64_t unit = ((int64_t)blockIdx.x * kBoundsThreads + threadIdx.x) >> 5;
-    const int64_t sj = unit / p.num_kv_heads;
-    const int h = (int)(unit - sj * p.num_kv_heads);
-    const int s = (int)(sj / p.touched);
-    if (s >= p.num_seqs) return 0;
+// This warp's block of sequence s (grid x: touched blocks and heads, y:
+// sequences): the slab (block * Hkv + head) and the tokens it holds, 0 where
+// there is nothing to do.
+__device__ __forceinline__ int bounds_unit(const BoundsParams& p, int s, int lane, size_t& slab) {
+    const uint32_t unit = (blockIdx.x * kBoundsThreads + threadIdx.x) >> 5;
+    const uint32_t nth = unit / (uint32_t)p.num_kv_heads;     // of the touched blocks
+    const int h = (int)(unit - nth * p.num_kv_heads);
+    if (nth >= (uint32_t)p.touched) return 0;
     const int B = p.block_size;
     const int L = p.context_lens[s];
     const int n = p.new_tokens ? p.new_tokens[s] : (L > 0 ? 1 : 0);
@@ -51,15 +51,15 @@ __device__ __forceinline__ int bounds_unit(const BoundsParams& p, int lane, size
         return 0;
     }
     if (n == 0) return 0;
-    const int64_t j = (L - n) / B + (sj - (int64_t)s * p.touched);
-    if (j * B >= L) return 0;
+    const int j = (L - n) / B + (int)nth;                     // below 2^31: touched blocks end by L + B
+    if ((int64_t)j * B >= L) return 0;
     const int64_t blk = p.block_tables[(size_t)s * p.max_blocks + j];
     if (blk < 0 || blk >= p.num_blocks) {
         if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
         return 0;
     }
     slab = (size_t)blk * p.num_kv_heads + h;
-    return min(B, L - (int)j * B);
+    return min(B, L - j * B);
 }
 
 // Packed pairs of a 16-bit type: the cache's own, or binary16 for E4M3 codes.
@@ -77,75 +77,77 @@ key_bounds_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
     constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31;
-    size_t slab = 0;
-    const int tokens = bounds_unit(p, lane, slab);
-    if (tokens == 0) return;
-    const int c = (lane & (LANES - 1)) * E;
-    const CT* keys = static_cast<const CT*>(p.k_cache) + slab * p.block_size * D + c;
-    auto as2 = [](uint32_t w) { return *reinterpret_cast<T2*>(&w); };
-    auto bits = [](T2 x) { return *reinterpret_cast<uint32_t*>(&x); };
-    T2 lo[W], hi[W];
-    const int r0 = lane / LANES;
-    // a lane group without a token of its own starts from the first token too
-    for (int r = 0; r < tokens; r += kBatch * ROWS) {
-        uint4 x[kBatch];
+    for (int s = blockIdx.y; s < p.num_seqs; s += gridDim.y) {
+        size_t slab = 0;
+        const int tokens = bounds_unit(p, s, lane, slab);
+        if (tokens == 0) continue;
+        const int c = (lane & (LANES - 1)) * E;
+        const CT* keys = static_cast<const CT*>(p.k_cache) + slab * p.block_size * D + c;
+        auto as2 = [](uint32_t w) { return *reinterpret_cast<T2*>(&w); };
+        auto bits = [](T2 x) { return *reinterpret_cast<uint32_t*>(&x); };
+        T2 lo[W], hi[W];
+        const int r0 = lane / LANES;
+        // a lane group without a token of its own starts from the first token too
+        for (int r = 0; r < tokens; r += kBatch * ROWS) {
+            uint4 x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int t = r + k * ROWS + r0;
-            x[k] = *reinterpret_cast<const uint4*>(keys + (size_t)(t < tokens ? t : 0) * D);
+            for (int k = 0; k < kBatch; ++k) {
+                const int t = r + k * ROWS + r0;
+                x[k] = *reinterpret_cast<const uint4*>(keys + (t < tokens ? t : 0) * D);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    T2 v;
+                    if constexpr (kFp8) {
+                        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                            static_cast<__nv_fp8x2_storage_t>(ws[i / 2] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3);
+                        v = *reinterpret_cast<const T2*>(&h);
+                    } else {
+                        v = as2(ws[i]);
+                    }
+                    lo[i] = r == 0 && k == 0 ? v : __hmin2_nan(lo[i], v);
+                    hi[i] = r == 0 && k == 0 ? v : __hmax2_nan(hi[i], v);
+                }
+            }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const uint32_t ws[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        auto store = [&](BT* out, const T2 (&v)[W]) {
+            uint32_t w[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                T2 v;
-                if constexpr (kFp8) {
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                        static_cast<__nv_fp8x2_storage_t>(ws[i / 2] >> (16 * (i & 1)) & 0xffffu), __NV_E4M3);
-                    v = *reinterpret_cast<const T2*>(&h);
+                if constexpr (kFp8 && std::is_same<BT, __nv_bfloat16>::value) {
+                    const __nv_bfloat162 b = __float22bfloat162_rn(__half22float2(v[i]));      // exact
+                    w[i] = *reinterpret_cast<const uint32_t*>(&b);
                 } else {
-                    v = as2(ws[i]);
+                    w[i] = bits(v[i]);
                 }
-                lo[i] = r == 0 && k == 0 ? v : __hmin2_nan(lo[i], v);
-                hi[i] = r == 0 && k == 0 ? v : __hmax2_nan(hi[i], v);
             }
-        }
-    }
-    auto store = [&](BT* out, const T2 (&v)[W]) {
-        uint32_t w[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if constexpr (kFp8 && std::is_same<BT, __nv_bfloat16>::value) {
-                const __nv_bfloat162 b = __float22bfloat162_rn(__half22float2(v[i]));      // exact
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-                w[i] = bits(v[i]);
+            for (int i = 0; i < W; i += 4)
+                *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        };
+        BT* out = static_cast<BT*>(p.k_bounds) + slab * 2 * D + c;
+        if constexpr (ROWS == 1) {
+            store(out, lo);
+            store(out + D, hi);
+        } else {
+            // lanes 0-15 go on with the minima, 16-31 with the maxima
+            const bool upper = lane >= 16;
+            T2 v[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const T2 o = as2(__shfl_xor_sync(0xffffffffu, bits(upper ? lo[i] : hi[i]), 16));
+                v[i] = upper ? __hmax2_nan(hi[i], o) : __hmin2_nan(lo[i], o);
+#pragma unroll
+                for (int m = 8; m >= LANES; m >>= 1) {
+                    const T2 y = as2(__shfl_xor_sync(0xffffffffu, bits(v[i]), m));
+                    v[i] = upper ? __hmax2_nan(v[i], y) : __hmin2_nan(v[i], y);
+                }
             }
+            if ((lane & 15) < LANES) store(out + (upper ? D : 0), v);
         }
-#pragma unroll
-        for (int i = 0; i < W; i += 4)
-            *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    };
-    BT* out = static_cast<BT*>(p.k_bounds) + slab * 2 * D + c;
-    if constexpr (ROWS == 1) {
-        store(out, lo);
-        store(out + D, hi);
-    } else {
-        // lanes 0-15 go on with the minima, 16-31 with the maxima
-        const bool upper = lane >= 16;
-        T2 v[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const T2 o = as2(__shfl_xor_sync(0xffffffffu, bits(upper ? lo[i] : hi[i]), 16));
-            v[i] = upper ? __hmax2_nan(hi[i], o) : __hmin2_nan(lo[i], o);
-#pragma unroll
-            for (int m = 8; m >= LANES; m >>= 1) {
-                const T2 y = as2(__shfl_xor_sync(0xffffffffu, bits(v[i]), m));
-                v[i] = upper ? __hmax2_nan(v[i], y) : __hmin2_nan(v[i], y);
-            }
-        }
-        if ((lane & 15) < LANES) store(out + (upper ? D : 0), v);
     }
 }
 
@@ -156,51 +158,54 @@ key_bounds_f32_kernel(const __grid_constant__ BoundsParams p) {
     constexpr int LANES = D / 8;               // lanes per token row
     constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
     const int lane = threadIdx.x & 31;
-    size_t slab = 0;
-    const int tokens = bounds_unit(p, lane, slab);
-    if (tokens == 0) return;
-    const int c = (lane & (LANES - 1)) * 8;
-    const float* keys = static_cast<const float*>(p.k_cache) + slab * p.block_size * D + c;
-    float lo[8], hi[8];
+    for (int s = blockIdx.y; s < p.num_seqs; s += gridDim.y) {
+        size_t slab = 0;
+        const int tokens = bounds_unit(p, s, lane, slab);
+        if (tokens == 0) continue;
+        const int c = (lane & (LANES - 1)) * 8;
+        const float* keys = static_cast<const float*>(p.k_cache) + slab * p.block_size * D + c;
+        float lo[8], hi[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo[i] = __int_as_float(0x7f800000);
-        hi[i] = __int_as_float(0xff800000);
-    }
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __int_as_float(0x7f800000);
+            hi[i] = __int_as_float(0xff800000);
+        }
 #pragma unroll 4
-    for (int r = lane / LANES; r < tokens; r += ROWS) {
-        float x[8];
-        RowLoader<float, 8>::load(keys + (size_t)r * D, x);
+        for (int r = lane / LANES; r < tokens; r += ROWS) {
+            float x[8];
+            RowLoader<float, 8>::load(keys + (size_t)r * D, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo[i] = nan_min(lo[i], x[i]);
-            hi[i] = nan_max(hi[i], x[i]);
+            for (int i = 0; i < 8; ++i) {
+                lo[i] = nan_min(lo[i], x[i]);
+                hi[i] = nan_max(hi[i], x[i]);
+            }
         }
-    }
 #pragma unroll
-    for (int m = LANES; m < 32; m <<= 1) {
+        for (int m = LANES; m < 32; m <<= 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo[i] = nan_min(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], m));
-            hi[i] = nan_max(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], m));
+            for (int i = 0; i < 8; ++i) {
+                lo[i] = nan_min(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], m));
+                hi[i] = nan_max(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], m));
+            }
         }
-    }
-    if (lane < LANES) {
-        float* out = static_cast<float*>(p.k_bounds) + slab * 2 * D + c;
+        if (lane < LANES) {
+            float* out = static_cast<float*>(p.k_bounds) + slab * 2 * D + c;
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            *reinterpret_cast<float4*>(out + i) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
-            *reinterpret_cast<float4*>(out + D + i) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+            for (int i = 0; i < 8; i += 4) {
+                *reinterpret_cast<float4*>(out + i) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+                *reinterpret_cast<float4*>(out + D + i) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+            }
         }
     }
 }
 
 template <typename CT, typename BT>
 cudaError_t launch_bounds(const BoundsParams& p, int head_size, cudaStream_t stream) {
-    const int64_t units = (int64_t)p.num_seqs * p.touched * p.num_kv_heads;
-    const int64_t grid = (units * 32 + kBoundsThreads - 1) / kBoundsThreads;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    auto launch = [&](auto kernel) { kernel<<<(unsigned)grid, kBoundsThreads, 0, stream>>>(p); };
+    const int64_t units = (int64_t)p.touched * p.num_kv_heads;
+    const int64_t gx = (units * 32 + kBoundsThreads - 1) / kBoundsThreads;
+    if (gx > 0x3ffffff) return cudaErrorInvalidConfiguration;  // thread indices stay below 2^32
+    const dim3 grid((unsigned)gx, p.num_seqs < 65535 ? p.num_seqs : 65535);
+    auto launch = [&](auto kernel) { kernel<<<grid, kBoundsThreads, 0, stream>>>(p); };
     if constexpr (std::is_same<CT, float>::value) {
         switch (head_size) {
         case 64: launch(key_bounds_f32_kernel<64>); break;

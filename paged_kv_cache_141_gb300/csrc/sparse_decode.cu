@@ -135,6 +135,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     }
 
     // ------------------------------------------------------------ selection
+    if (!rw.scored) __syncthreads();                // else at the scoring's first barrier
     score_and_take<QT, D, true, NT>(p, sh, cluster, rw);
     int32_t* selected = p.selected ? p.selected + (size_t)rw.row * p.num_select : nullptr;
     const int total = rw.n < p.num_select ? rw.n : p.num_select;

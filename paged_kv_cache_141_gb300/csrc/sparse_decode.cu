@@ -74,6 +74,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
     using MT = typename MathType<CT>::T;            // the MMAs' type
     using Ops = MmaOps<MT>;
+    using OutOps = MmaOps<QT>;
     using Tile = Tile16<CT, D>;
     constexpr int MD = D / 16;                      // O^T row tiles
     constexpr int NW = NT / 32;
@@ -81,16 +82,24 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ SelShared<NT> sh;
     __shared__ Joined joined;
-    __shared__ float wm[NW][8], wl[NW][8], q_unit[8];
+    __shared__ float wm[NW][8], wl[NW][8], wf[NW][8], q_unit[8];
     int32_t* list = reinterpret_cast<int32_t*>(dyn);                   // the row's slabs
     uint4* qf = reinterpret_cast<uint4*>(dyn + sp.list_bytes);         // query fragments: D * 16 bytes
     uint8_t* work = dyn + sp.list_bytes + 16 * D;                      // selection, then the warps' O
     cg::cluster_group cluster = cg::this_cluster();
+    const int G = p.group, B = p.block_size;
+    // this thread's eight query elements, before anything waits for the length
+    constexpr int kChunks = D / 8;                  // chunks of a head
+    const int q_head = threadIdx.x / kChunks, q_chunk = threadIdx.x % kChunks;
+    uint4 q_words = make_uint4(0, 0, 0, 0);
+    if (q_head < G) {                               // rows of a sequence's heads are contiguous
+        const size_t row = blockIdx.x / cluster.num_blocks();
+        q_words = __ldg(reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) + (row * G + q_head) * D + 8 * q_chunk));
+    }
     const SelRow rw(p, cluster, work);
     const int C = rw.C;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t4 = lane & 3;
-    const int G = p.group, B = p.block_size;
     QT* out = static_cast<QT*>(sp.out) + ((size_t)rw.s * p.num_q_heads + rw.h * G) * D;
 
     for (int i = threadIdx.x; i < p.table_width; i += NT) list[i] = -1;
@@ -98,12 +107,9 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     // fragments for S (head g's elements as the keys' chunks hold them). A
     // thread has eight elements, a head D / 8 neighbouring threads.
     if (threadIdx.x < D) {
-        constexpr int N = D / 8;
-        const int hd = threadIdx.x / N, c = threadIdx.x % N;   // chunk of elements 8 c ..
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (hd < G)
-            w = *reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) +
-                                                ((size_t)rw.s * p.num_q_heads + rw.h * G + hd) * D + 8 * c);
+        constexpr int N = kChunks;
+        const int hd = q_head, c = q_chunk;
+        const uint4 w = q_words;
         const int l = 4 * hd + (c & 3);                        // the lane, in step c / 4
         if (rw.scored) {
 #pragma unroll
@@ -355,33 +361,41 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
         }
     }
     __syncthreads();
-    // elements d, d + 1 of head hd: the sum over the warps, relative to the CTA's maximum
-    const float* jo_base = wo;
-    for (int e = threadIdx.x; e < G * (D / 2); e += NT) {
-        const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
-        float M = -INFINITY;
+    // each warp's factor relative to the CTA's maximum (a single CTA: over the sum)
+    if (threadIdx.x < NW * 8) {
+        const int w = threadIdx.x >> 3, hd = threadIdx.x & 7;
+        float M = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w][hd]);
-        float l = 0.f, o0 = 0.f, o1 = 0.f;
+        for (int v = 0; v < NW; ++v) M = fmaxf(M, wm[v][hd]);
+#pragma unroll
+        for (int v = 0; v < NW; ++v) l += wm[v][hd] == -INFINITY ? 0.f : fast_exp2(wm[v][hd] - M) * wl[v][hd];
+        float f = wm[w][hd] == -INFINITY ? 0.f : fast_exp2(wm[w][hd] - M);
+        if (C == 1) f *= l > 0.f || l != l ? sp.v_mul / l : 0.f;       // no tokens: zero; NaN stays
+        wf[w][hd] = f;
+        if (w == 0) {
+            joined.m[hd] = M;
+            joined.l[hd] = l;
+        }
+    }
+    __syncthreads();
+    // four elements of a head a thread
+    for (int e = threadIdx.x; e < G * (D / 4); e += NT) {
+        const int hd = e / (D / 4), d = 4 * (e - hd * (D / 4));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = wm[w][hd] == -INFINITY ? 0.f : fast_exp2(wm[w][hd] - M);
-            const float2 o = *reinterpret_cast<const float2*>(jo_base + (w * 8 + hd) * kPitch + d);
-            l += f * wl[w][hd];
-            o0 += f * o.x;
-            o1 += f * o.y;
+            const float f = wf[w][hd];
+            const float4 x = *reinterpret_cast<const float4*>(wo + (w * 8 + hd) * kPitch + d);
+            o.x += f * x.x;
+            o.y += f * x.y;
+            o.z += f * x.z;
+            o.w += f * x.w;
         }
         if (C == 1) {
-            const float r = l > 0.f || l != l ? sp.v_mul / l : 0.f;    // no tokens: zero; NaN stays
-            out[hd * D + d] = from_float<QT>(o0 * r);
-            out[hd * D + d + 1] = from_float<QT>(o1 * r);
+            *reinterpret_cast<uint2*>(out + hd * D + d) = make_uint2(OutOps::pack(o.x, o.y), OutOps::pack(o.z, o.w));
         } else {
             // into warp 0's place, which only this thread reads for these elements
-            *reinterpret_cast<float2*>(wo + hd * kPitch + d) = make_float2(o0, o1);
-            if (d == 0) {
-                joined.m[hd] = M;
-                joined.l[hd] = l;
-            }
+            *reinterpret_cast<float4*>(wo + hd * kPitch + d) = o;
         }
     }
     if (C == 1) return;

@@ -471,6 +471,7 @@ struct SelRow {
     uint4* sides;                       // [n-tile][step][lane]
     float* keys;                        // the candidates' scores (of the first CTA, or in memory)
     uint32_t* taken;                    // a bit per candidate (the first CTA's)
+    int ahead[2];                       // the blocks of this lane's rows of its first tile
 
     __device__ __forceinline__ SelRow(const SelectParams& p, cg::cluster_group& cluster, uint8_t* smem) {
         C = (int)cluster.num_blocks();
@@ -478,14 +479,21 @@ struct SelRow {
         row = blockIdx.x / C;
         s = row / p.num_kv_heads;
         h = row - s * p.num_kv_heads;
+        table = p.block_tables + (size_t)s * p.max_blocks;
+        lo = p.first_blocks;
+        // the first table entries, on their way while the length is
+        const int tile = (rank * blockDim.x + threadIdx.x) >> 5;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t i = (int64_t)lo + tile * 16 + ((threadIdx.x & 31) >> 2) + 8 * r;
+            ahead[r] = table[i < p.max_blocks ? i : p.max_blocks - 1];
+        }
         bool bad;
         L = clamped_len(p, s, bad);
         if (bad && h == 0 && rank == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_LEN);
         n = (L + p.block_size - 1) / p.block_size;
-        table = p.block_tables + (size_t)s * p.max_blocks;
         all = n <= p.num_select;
         want = p.num_select - p.first_blocks - p.recent_blocks;
-        lo = p.first_blocks;
         nc = all ? 0 : n - p.recent_blocks - lo;
         scored = nc > 0 && want > 0;
         sides = reinterpret_cast<uint4*>(smem);
@@ -603,7 +611,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
                     best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
                     const int i = tile * 16 + g + 8 * r;
                     const bool ok = there(blk[r]);
-                    if (ok) {
+                    if (ok && i < nc) {
                         worst = max_nan(worst, mag[r]);
                         lowest = fminf(lowest, best[r]);
                         highest = fmaxf(highest, best[r]);
@@ -632,7 +640,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
                 if (tile < tiles) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        blk[r] = block_of(tile, r);
+                        blk[r] = rw.ahead[r];                  // (past nc: any block, its score unused)
                         nblk[r] = block_of(after(tile), r);
                     }
                     x = row_of(blk[0]);

@@ -127,10 +127,12 @@ __device__ uint64_t exact_score(const SelectParams& p, int s, int h, int64_t blk
     return best;
 }
 
-// A block's score for one head to about 2^-44 of its terms' magnitudes, by one
-// warp, for 16-bit types: their products are exact in binary32, and the sum is
-// kept as a pair (Knuth's two-sum, errors collected), far cheaper here than
-// binary64. Not for magnitudes whose products could under- or overflow.
+// A block's score for one head to 2^-40 of its terms' magnitudes T, by one warp,
+// for 16-bit types: their products are exact in binary32, and the sum is kept as
+// a pair (Knuth's two-sum, errors collected), far cheaper here than binary64.
+// The collected errors are at most (8 + 5) 2^-24 T, and collecting them rounds at
+// most 18 times by 2^-24 of that: 2^-40.1 T. Not for magnitudes whose products
+// could under- or overflow.
 template <typename T, int D>
 __device__ double close_head_score(const SelectParams& p, int s, int h, int g, int64_t blk, int lane) {
     constexpr int E = D / 32;
@@ -422,7 +424,7 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
                 const uint64_t x = mine ? sh.list_key[e] : 0;
                 int ahead = inner, nearby = 0;
                 if (open) {
-                    const double mine_d = value64(x), margin = (double)mag * 0x1p-40;
+                    const double mine_d = value64(x), margin = (double)mag * 0x1p-38;
                     for (int o = 0; o < m; ++o) {
                         const uint64_t y = sh.list_key[o];
                         ahead += y > x || (y == x && y != 0 && sh.list[o] < i);

@@ -214,6 +214,49 @@ def test_long_contexts(lens, K):
     p.check(out, sel, K, 1, 2)
 
 
+@pytest.mark.parametrize("dtype,e4m3", [("f16", False), ("bf16", True), ("f32", False)])
+def test_long_contexts_of_other_types(dtype, e4m3):
+    p = Pool([33333, 20001], 8, 2, dtype=dtype, e4m3=e4m3, seed=2)
+    p.fill_bounds()
+    out, sel = p.decode(70, 2, 1)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, 70, 2, 1)
+
+
+@pytest.mark.parametrize("L,B,K,first", [(400003, 16, 40, 1), (30001, 1, 50, 0), (12000, 1, 9000, 3), (150000, 8, 33, 2)])
+def test_more_blocks_than_shared_memory_keeps(L, B, K, first):
+    p = Pool([L, 17 * B], 4, 1, 64, B, seed=4)
+    p.fill_bounds()
+    out, sel = p.decode(K, first, 2)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, K, first, 2)
+
+
+@pytest.mark.parametrize("group", [1, 3, 8, 9, 64, 128])
+def test_every_group_size(group):
+    p = Pool([16 * 60 + 1, 16 * 300], group * 2, 2, 64, seed=group)
+    p.fill_bounds()
+    out, sel = p.decode(20)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, 20)
+
+
+def test_close_scores_in_a_crowd():
+    # many blocks whose scores differ by less than the approximate scores' error, ties among them
+    p = Pool([16 * 700], Hq=4, Hkv=1, D=128, seed=5)
+    p.fill_bounds()
+    blk = p.tables[0].long()
+    base = p.bounds[blk[0]].clone()
+    g = torch.Generator().manual_seed(7)
+    step = torch.randint(0, 40, (700,), generator=g).cuda()
+    p.bounds[blk] = base
+    p.bounds[blk, 0, 1, 17] = (2.0 ** -6 * (1 + step * 2.0 ** -7)).to(p.dt)          # the only difference
+    p.query[..., 17] = 2.0 ** -8
+    for K in (30, 200, 500):
+        out, sel = p.decode(K, 1, 1)
+        p.check(out, sel, K, 1, 1)
+
+
 def test_many_sequences():
     lens = [(37 * i) % 900 for i in range(300)]
     p = Pool(lens, 8, 2, 64, seed=3)

@@ -559,7 +559,7 @@ pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* bloc
  * (the plain decode); otherwise blocks 0 .. first_blocks - 1, the newest
  * recent_blocks, and of the others the num_select - first_blocks -
  * recent_blocks of largest score, ties to the lowest index. The order is that
- * of the scores computed exactly (in binary64), so it does not depend on how
+ * of the exact scores (held in binary64 at least), so it does not depend on how
  * the work is split; a NaN score counts as +infinity. The output is
  * softmax(scale * q K^T) V over the selected blocks' tokens below L.
  *

@@ -18,8 +18,8 @@
 //    a second product of the magnitudes gives.
 //  - the threshold among those scores, from a histogram over their range.
 //    Blocks whose distance to the other side of the threshold exceeds both
-//    errors are settled; the rest (usually none) are scored again in binary64
-//    and ranked. Where the histogram's bin at the threshold holds too many
+//    errors are settled; the rest (usually none) are scored again exactly and
+//    ranked. Where the histogram's bin at the threshold holds too many
 //    blocks (equal scores) or a score is not finite, a search over the key
 //    bits takes its place.
 // A cluster of CTAs takes one (sequence, KV head): all score, into the first
@@ -71,9 +71,6 @@ __device__ __forceinline__ uint64_t ordered64(double x) {
     const uint64_t u = (uint64_t)__double_as_longlong(x == 0.0 ? 0.0 : x);
     return u >> 63 ? ~u : u | (1ull << 63);
 }
-__device__ __forceinline__ double value64(uint64_t key) {      // ordered64's inverse
-    return __longlong_as_double((long long)(key >> 63 ? key ^ (1ull << 63) : ~key));
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -96,8 +93,12 @@ __device__ __forceinline__ uint32_t side2(uint32_t w, bool positive) {
     }
 }
 
-// A block's score for one head of the group in binary64, by one warp, as an
-// ordered key (NaN as +infinity).
+// A block's score for one head of the group, by one warp, as an ordered key (NaN
+// as +infinity): the exact sum where a pair of binary32 numbers holds it, else
+// the sum in binary64. Products of 16-bit types are exact in binary32, and the
+// pair (Knuth's two-sum, for the sum and for its collected errors) says by
+// itself whether anything was lost; with 48 bits that is rare, and binary64
+// runs at a small fraction of binary32's rate on this GPU.
 template <typename T, int D>
 __device__ uint64_t exact_head_score(const SelectParams& p, int s, int h, int g, int64_t blk, int lane) {
     constexpr int E = D / 32;
@@ -108,6 +109,33 @@ __device__ uint64_t exact_head_score(const SelectParams& p, int s, int h, int g,
     RowLoader<T, E>::load(bounds + D, hi);
     RowLoader<T, E>::load(static_cast<const T*>(p.query) +
                           ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
+    if constexpr (!std::is_same<T, float>::value) {
+        float sum = 0.f, err = 0.f;
+        bool lost = false;
+        // a + b = t + two_sum's result, exactly
+        auto two_sum = [](float a, float b, float& t) {
+            t = __fadd_rn(a, b);
+            const float z = __fsub_rn(t, a);
+            return __fadd_rn(__fsub_rn(a, __fsub_rn(t, z)), __fsub_rn(b, z));
+        };
+        auto collect = [&](float e) { lost |= two_sum(err, e, err) != 0.f; };
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float b = q[i] < 0.f ? lo[i] : hi[i];
+            const float x = __fmul_rn(q[i], b);
+            lost |= !(fabsf(x) > 0x1p-100f && fabsf(x) < INFINITY) && q[i] != 0.f && b != 0.f;   // may be inexact
+            collect(two_sum(sum, x, sum));
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            const float s2 = __shfl_xor_sync(0xffffffffu, sum, m);
+            const float e2 = __shfl_xor_sync(0xffffffffu, err, m);
+            collect(two_sum(sum, s2, sum));
+            collect(e2);
+        }
+        // (an infinity or a NaN anywhere leaves NaN errors: lost)
+        if (!__any_sync(0xffffffffu, lost)) return ordered64((double)sum + (double)err);
+    }
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < E; ++i) sum += (double)q[i] * (double)(q[i] < 0.f ? lo[i] : hi[i]);
@@ -125,41 +153,6 @@ __device__ uint64_t exact_score(const SelectParams& p, int s, int h, int64_t blk
         best = x > best ? x : best;
     }
     return best;
-}
-
-// A block's score for one head to 2^-40 of its terms' magnitudes T, by one warp,
-// for 16-bit types: their products are exact in binary32, and the sum is kept as
-// a pair (Knuth's two-sum, errors collected), far cheaper here than binary64.
-// The collected errors are at most (8 + 5) 2^-24 T, and collecting them rounds at
-// most 18 times by 2^-24 of that: 2^-40.1 T. Not for magnitudes whose products
-// could under- or overflow.
-template <typename T, int D>
-__device__ double close_head_score(const SelectParams& p, int s, int h, int g, int64_t blk, int lane) {
-    constexpr int E = D / 32;
-    if (blk < 0 || blk >= p.num_blocks) return -INFINITY;
-    const T* bounds = static_cast<const T*>(p.k_bounds) + ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
-    float lo[E], hi[E], q[E];
-    RowLoader<T, E>::load(bounds, lo);
-    RowLoader<T, E>::load(bounds + D, hi);
-    RowLoader<T, E>::load(static_cast<const T*>(p.query) +
-                          ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
-    float sum = 0.f, err = 0.f;
-    auto add = [&](float x) {
-        const float t = __fadd_rn(sum, x);
-        const float z = __fsub_rn(t, sum);
-        err = __fadd_rn(err, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, z)), __fsub_rn(x, z)));
-        sum = t;
-    };
-#pragma unroll
-    for (int i = 0; i < E; ++i) add(__fmul_rn(q[i], q[i] < 0.f ? lo[i] : hi[i]));
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        const float s2 = __shfl_xor_sync(0xffffffffu, sum, m);
-        const float e2 = __shfl_xor_sync(0xffffffffu, err, m);
-        add(s2);
-        err = __fadd_rn(err, e2);
-    }
-    return (double)sum + (double)err;
 }
 
 // Sixteen blocks' bounds rows, four 64-byte steps (a quarter: 128 elements) at
@@ -216,6 +209,7 @@ struct SelShared {
     int above;
     int part[2][kWarps];             // count(): per-warp sums, double-buffered
     float fpart[3][kWarps];
+    uint64_t bits_all[kWarps], bits_any[kWarps];
     int list_n;
     int list[kRankList];
     float list_score[kRankList];
@@ -256,9 +250,29 @@ __device__ __forceinline__ float cta_min(SelShared<NT>& sh, float x) {
 template <typename K, int NT, typename Key, typename Skip>
 __device__ __forceinline__ K kth_largest(SelShared<NT>& sh, int n, int want, int& turn, bool& exact,
                                          Key key, Skip skip) {
-    K prefix = 0;
     exact = false;
-    for (int bit = (int)sizeof(K) * 8 - 1; bit >= 0; --bit) {
+    // the bits that all keys share need no search
+    K common = ~(K)0, any = 0;
+    for (int i = threadIdx.x; i < n; i += NT)
+        if (!skip(i)) {
+            common &= key(i);
+            any |= key(i);
+        }
+    uint64_t c64 = common, a64 = any;
+    c64 = (uint64_t)__reduce_and_sync(0xffffffffu, (uint32_t)(c64 >> 32)) << 32 | __reduce_and_sync(0xffffffffu, (uint32_t)c64);
+    a64 = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(a64 >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)a64);
+    if ((threadIdx.x & 31) == 0) {
+        sh.bits_all[threadIdx.x >> 5] = c64;
+        sh.bits_any[threadIdx.x >> 5] = a64;
+    }
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) {
+        c64 &= sh.bits_all[w];
+        a64 |= sh.bits_any[w];
+    }
+    const int top = 63 - __clzll((long long)(c64 ^ a64));      // -1: one value
+    K prefix = (K)(top < 0 ? c64 : c64 >> top >> 1 << top << 1);
+    for (int bit = top; bit >= 0; --bit) {
         const K cand = prefix | ((K)1 << bit);
         int c = 0;
         for (int i = threadIdx.x; i < n; i += NT) c += !skip(i) && key(i) >= cand;
@@ -404,57 +418,25 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
     float a, b;
     border(k, a, b);
     if (a - b <= err2) {
-        // the blocks within err2 of the other side: a closer score, and where
-        // that leaves a doubt, binary64
-        const bool inside = take;
+        // the blocks within err2 of the other side, by their exact scores
         const bool open = mine && (take ? k <= b + err2 : k >= a - err2);
-        const int inner = cta_sum(sh, mine && !open && inside, turn);         // settled inside
-        bool decided = false;
-        if constexpr (!std::is_same<T, float>::value) {
-            if (mag > 0x1p-90f && mag < 0x1p120f) {
-                if (mine) sh.list_key[e] = open ? 1 : 0;       // below every key of a score
-                __syncthreads();
-                for (int w = warp; w < m * p.group; w += (NT / 32)) {         // a warp per (block, head)
-                    const int o = w / p.group;
-                    if (sh.list_key[o] == 0) continue;
-                    const uint64_t x = ordered64(close_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane));
-                    if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
-                }
-                __syncthreads();
-                const uint64_t x = mine ? sh.list_key[e] : 0;
-                int ahead = inner, nearby = 0;
-                if (open) {
-                    const double mine_d = value64(x), margin = (double)mag * 0x1p-38;
-                    for (int o = 0; o < m; ++o) {
-                        const uint64_t y = sh.list_key[o];
-                        ahead += y > x || (y == x && y != 0 && sh.list[o] < i);
-                        if (o != e && y != 0) nearby += fabs(value64(y) - mine_d) <= margin;
-                    }
-                    take = ahead < left;
-                }
-                decided = cta_sum(sh, nearby, turn) == 0;
-            }
+        int ahead = cta_sum(sh, mine && !open && take, turn);  // settled inside
+        if (mine) sh.list_key[e] = open ? 1 : 0;               // below every key of a score
+        __syncthreads();
+        for (int w = warp; w < m * p.group; w += (NT / 32)) {  // a warp per (block, head)
+            const int o = w / p.group;
+            if (sh.list_key[o] == 0) continue;
+            const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
+            if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
         }
-        if (!decided) {
-            take = inside;
-            if (mine) sh.list_key[e] = open ? 1 : 0;
-            __syncthreads();
-            for (int w = warp; w < m * p.group; w += (NT / 32)) {
-                const int o = w / p.group;
-                if (sh.list_key[o] == 0) continue;
-                const uint64_t x = exact_head_score<T, D>(p, s, h, w - o * p.group, table[sh.list[o]], lane);
-                if (lane == 0) atomicMax(reinterpret_cast<unsigned long long*>(&sh.list_key[o]), (unsigned long long)x);
+        __syncthreads();
+        if (open) {
+            const uint64_t x = sh.list_key[e];
+            for (int o = 0; o < m; ++o) {
+                const uint64_t y = sh.list_key[o];
+                ahead += y > x || (y == x && sh.list[o] < i);
             }
-            __syncthreads();
-            if (open) {
-                int ahead = inner;
-                const uint64_t x = sh.list_key[e];
-                for (int o = 0; o < m; ++o) {
-                    const uint64_t y = sh.list_key[o];
-                    ahead += y > x || (y == x && sh.list[o] < i);
-                }
-                take = ahead < left;
-            }
+            take = ahead < left;
         }
     }
     if (take) atomicOr(&taken[i >> 5], 1u << (i & 31));
@@ -774,11 +756,15 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
         if (!finite) thr = ordered(INFINITY);
         if (left < open) {
             // ------------------------------------------- exact scores of the unsettled
-            const bool small = open <= SelShared<NT>::kRankList;
+            // (A zero query, say of a padding row, makes every score 0, exactly.)
+            const bool zeros = mag == 0.f;
+            const bool small = open <= SelShared<NT>::kRankList && !zeros;
             if (threadIdx.x == 0) sh.list_n = 0;
             __syncthreads();
             uint64_t* exact_keys = p.exact_keys + (size_t)row * p.max_ctx_blocks;
-            for (int i0 = warp * 32; i0 < nc; i0 += NT) {
+            if (zeros)
+                for (int i = threadIdx.x; i < nc; i += NT) exact_keys[i] = ordered64(keys[i]);
+            for (int i0 = zeros ? nc : warp * 32; i0 < nc; i0 += NT) {
                 const bool mine = i0 + lane < nc && !settled(keys[i0 + lane]);
                 uint32_t votes = __ballot_sync(0xffffffffu, mine);
                 while (votes) {

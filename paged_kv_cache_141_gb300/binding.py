@@ -4,7 +4,9 @@ Argument marshalling only: every function passes tensor data pointers, sizes
 and the current CUDA stream to the library, and raises PagedKVError when the
 library returns a non-zero status. All computation happens in the library's
 CUDA kernels. If the library has not been built, loading fails with an error;
-there is no fallback path.
+there is no fallback path. The calls go through ctypes, but for the rotating
+append, the key bounds and the block-sparse decode, whose arguments a small C++
+module marshals (pysrc/marshal.cpp).
 
 Tensors are CUDA tensors, contiguous, in the library's layouts:
   query/out        [num_seqs, num_q_heads, head_size]   float32/float16/bfloat16
@@ -152,15 +154,11 @@ def _check(status: int, what: str) -> None:
         raise PagedKVError(what, status)
 
 
-def _dtype_code(dtype: torch.dtype) -> int:
-    try:
-        return _DTYPES[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported tensor dtype {dtype}") from None
-
-
 def _dtype(t: torch.Tensor) -> int:
-    return _dtype_code(t.dtype)
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported tensor dtype {t.dtype}") from None
 
 
 def _ptr(t: torch.Tensor | None):
@@ -473,51 +471,25 @@ def write_decode_shared_prefix(out, query, k_cache, v_cache, block_tables, conte
 MAX_ROPE_AXES = 4
 
 
-def _pointers(first, *tensors):
-    """Device index of `first` and the data pointers of all tensors (None for
-    None), which must be contiguous and on that device."""
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("tensor must live on a CUDA device")
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError("all tensors must live on one CUDA device")
-        if not t.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-        out.append(t.data_ptr())
-    return dev, out
+_marshal = None
 
 
-def _call(fn, dev, stream, *args) -> int:
-    """fn(*args, stream) with device `dev` current; stream None: that device's
-    current stream. (The raw getters: a stream object and a device context cost
-    several microseconds each, as much as the launch.)"""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        return fn(*args, stream)
-    with torch.cuda.device(dev):
-        return fn(*args, stream)
-
-
-def _token_rows(t, dev, tokens, heads, head_size, what):
-    """Pointer and token stride of [T, heads, head_size] rows whose last two
-    dimensions are contiguous (a view of a wider projection output is fine)."""
-    if t.get_device() != dev:
-        raise ValueError("all tensors must live on one CUDA device")
-    T, h, d = t.shape
-    st, sh, sd = t.stride()
-    if T != tokens or h != heads or d != head_size:
-        raise ValueError(f"{what} must be [{tokens}, {heads}, {head_size}]")
-    if sd != 1 or (sh != d and h > 1):
-        raise ValueError(f"{what}: each token's [heads, head_size] rows must be contiguous")
-    return t.data_ptr(), st if T > 1 else h * d
+def _native():
+    """The marshalling module of the calls below (pysrc/marshal.cpp)."""
+    global _marshal
+    if _marshal is None:
+        L = lib()
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("the binding's _marshal module is missing or of another PyTorch: build it "
+                               "first (python -m paged_kv_cache_141_gb300.build)") from e
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+        C = torch._C
+        module.bind(address(L.pa_rope_and_cache), address(L.pa_key_bounds), address(L.pa_sparse_decode),
+                    C._cuda_getCurrentRawStream, C._cuda_getDevice, C._cuda_exchangeDevice)
+        _marshal = module
+    return _marshal
 
 
 def rope_sections(sections) -> bytes:
@@ -538,46 +510,10 @@ def rope_and_cache(query_out, query, key, value, k_cache, v_cache, cos_sin, posi
     float32 [d] or None (no norm). adjacent_pairs: rotate components (2i, 2i+1)
     instead of (i, i + rotary_dim / 2). query, key and value may be views with
     any token stride; query_out may be query."""
-    shape, dtype = query.shape, query.dtype
-    T, Hq, D = shape
-    nb, Hkv, B, D2 = cache_shape = k_cache.shape
-    if v_cache.shape != cache_shape or D2 != D:
-        raise ValueError("inconsistent query/cache shapes")
-    if key.dtype != dtype or value.dtype != dtype or query_out.dtype != dtype:
-        raise ValueError("query, key, value and query_out must share one dtype")
-    cache_dtype = k_cache.dtype
-    if v_cache.dtype != cache_dtype:
-        raise ValueError("k_cache and v_cache must share one dtype")
-    if query_out.shape != shape:
-        raise ValueError("query_out must have the query's shape")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
-    max_position, rotary_dim = cos_sin.shape
-    pos_shape = positions.shape
-    axes = 1 if len(pos_shape) == 1 else pos_shape[0]
-    if positions.dtype != torch.int64 or len(pos_shape) > 2 or pos_shape[-1] != T or axes < 1:
-        raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
-        raise ValueError("slot_mapping must be int64 [num_tokens]")
-    if q_weight is not None and (q_weight.dtype != torch.float32 or q_weight.numel() != D):
-        raise ValueError("norm weights must be float32 [head_size]")
-    if k_weight is not None and (k_weight.dtype != torch.float32 or k_weight.numel() != D):
-        raise ValueError("norm weights must be float32 [head_size]")
-    fa = None
-    if axes > 1:
-        if freq_axes is None or len(freq_axes) != rotary_dim // 2:
-            raise ValueError("several axes need freq_axes, one axis for each of rotary_dim / 2 frequencies")
-        fa = bytes(freq_axes)
-    dev, (qo, kc, vc, cs, ps, sm, qw, kw, ds) = _pointers(
-        query, query_out, k_cache, v_cache, cos_sin, positions, slot_mapping, q_weight, k_weight,
-        dev_status)
-    q, q_stride = _token_rows(query, dev, T, Hq, D, "query")
-    k, k_stride = _token_rows(key, dev, T, Hkv, D, "key")
-    v, v_stride = _token_rows(value, dev, T, Hkv, D, "value")
-    _check(_call(lib().pa_rope_and_cache, dev, stream, qo, q, q_stride, k, k_stride, v, v_stride,
-                 kc, vc, cs, max_position, rotary_dim, ps, axes, fa, bool(adjacent_pairs), qw, kw,
-                 eps, sm, T, Hq, Hkv, D, B, nb, _dtype_code(dtype), _dtype_code(cache_dtype),
-                 k_scale, v_scale, ds), "pa_rope_and_cache")
+    _check((_marshal or _native()).rope_and_cache(
+        query_out, query, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping, q_weight,
+        k_weight, eps, freq_axes, adjacent_pairs, k_scale, v_scale, dev_status, stream),
+        "pa_rope_and_cache")
 
 
 def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, new_tokens=None,
@@ -585,21 +521,9 @@ def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, n
     """Recompute k_bounds [num_blocks, Hkv, 2, d] (minimum, maximum of each
     block's keys) for the blocks that hold the last new_tokens[s] (int32 [S];
     None: one) positions of each context."""
-    nb, Hkv, B, D = k_cache.shape
-    S = context_lens.numel()
-    if k_bounds.shape != (nb, Hkv, 2, D):
-        raise ValueError("k_bounds must be [num_blocks, num_kv_heads, 2, head_size]")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    if new_tokens is not None and (new_tokens.dtype != torch.int32 or new_tokens.numel() != S):
-        raise ValueError("new_tokens must be int32 [num_seqs]")
-    dev, (kb, kc, bt, cl, nt, ds) = _pointers(k_cache, k_bounds, k_cache, block_tables,
-                                              context_lens, new_tokens, dev_status)
-    _check(_call(lib().pa_key_bounds, dev, stream, kb, kc, bt, block_tables.shape[1], cl, nt,
-                 max_new_tokens, S, Hkv, D, B, nb, max_context_len, _dtype_code(k_cache.dtype),
-                 _dtype_code(k_bounds.dtype), ds), "pa_key_bounds")
+    _check((_marshal or _native()).key_bounds(
+        k_bounds, k_cache, block_tables, context_lens, max_context_len, new_tokens, max_new_tokens,
+        dev_status, stream), "pa_key_bounds")
 
 
 def sparse_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
@@ -623,22 +547,10 @@ def sparse_decode(out, query, k_cache, v_cache, k_bounds, block_tables, context_
     first_blocks, the newest recent_blocks and those whose k_bounds allow the
     largest logits. selected (int32 [S, Hkv, num_select], optional) receives
     the logical blocks taken, ascending, -1 padded."""
-    S, Hq, D, nb, Hkv, B, mb = _decode_dims(query, k_cache, block_tables, context_lens)
-    if out.shape != query.shape or out.dtype != query.dtype:
-        raise ValueError("out must have the query's shape and dtype")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must have one shape and dtype")
-    if k_bounds.shape != (nb, Hkv, 2, D) or k_bounds.dtype != query.dtype:
-        raise ValueError("k_bounds must be [num_blocks, num_kv_heads, 2, head_size] of the query's dtype")
-    if selected is not None and (selected.dtype != torch.int32 or selected.shape != (S, Hkv, num_select)):
-        raise ValueError("selected must be int32 [num_seqs, num_kv_heads, num_select]")
-    dev, (o, q, kc, vc, kb, bt, cl, sel, ws, ds) = _pointers(
-        query, out, query, k_cache, v_cache, k_bounds, block_tables, context_lens, selected,
-        workspace, dev_status)
-    _check(_call(lib().pa_sparse_decode, dev, stream, o, q, kc, vc, kb, bt, mb, cl, S, Hq, Hkv, D,
-                 B, nb, max_context_len, scale, num_select, first_blocks, recent_blocks, sel,
-                 _dtype_code(query.dtype), _dtype_code(k_cache.dtype), k_scale, v_scale, ws,
-                 workspace.numel() * workspace.element_size(), ds), "pa_sparse_decode")
+    _check((_marshal or _native()).sparse_decode(
+        out, query, k_cache, v_cache, k_bounds, block_tables, context_lens, max_context_len, scale,
+        num_select, workspace, first_blocks, recent_blocks, selected, k_scale, v_scale, dev_status,
+        stream), "pa_sparse_decode")
 
 
 STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024

@@ -1,9 +1,11 @@
-"""Build libpagedkv.so in-tree with nvcc for sm_103a (GB300).
+"""Build libpagedkv.so in-tree with nvcc for sm_103a (GB300), and with g++ the
+binding's marshalling module _marshal.so.
 
 Each CUDA translation unit compiles in its own nvcc process, in parallel;
 the objects link into one shared library next to this file. The CUDA runtime
 is linked statically, so the library loads without a GPU (the driver is only
-opened by the first CUDA call).
+opened by the first CUDA call). _marshal.so is compiled against the installed
+PyTorch's headers (and again when its version changes).
 
     python -m paged_kv_cache_141_gb300.build [--force] [-v]
 """
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+MARSHAL_SRC = os.path.join(PKG, "pysrc", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -51,8 +55,46 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """The marshalling module, against this interpreter's and PyTorch's headers."""
+    import sysconfig
+
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    stamp, made_for = os.path.join(BUILD, "marshal.torch"), f"{torch.__version__} {sysconfig.get_platform()}"
+    try:
+        with open(stamp) as f:
+            same = f.read() == made_for
+    except OSError:
+        same = False
+    if not force and same and not _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "pagedkv.h")]):
+        return MARSHAL
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    part = os.path.join(BUILD, "_marshal.so")          # moved into place when whole
+    cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I" + INCLUDE,
+           "-isystem", os.path.join(root, "include"), "-I" + sysconfig.get_path("include"), MARSHAL_SRC,
+           "-o", part, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + libs]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(MARSHAL_SRC)}:\n{proc.stderr}")
+    os.replace(part, MARSHAL)
+    with open(stamp, "w") as f:
+        f.write(made_for)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(1) as side:
+        marshal = side.submit(build_marshal, force)
+        lib = _build_library(force, verbose)
+        marshal.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     headers = _headers()
     jobs = []
     for src in sources():

@@ -283,6 +283,36 @@ inline cudaError_t ensure_smem_attribute(const void* key, int bytes) {
     return e;
 }
 
+// Programmatic dependent launch, for kernels launched by launch_overlapped: the
+// kernel may start while the one before it in the stream still runs, and every
+// thread first waits here until that one has completed and its writes are
+// visible -- unconditionally, before any access to memory and any return, so
+// that the chain of a stream's kernels holds. Then it lets the next one start:
+// launch and scheduling latency, several microseconds for the small kernels of
+// a decode step, overlap the running kernel.
+__device__ __forceinline__ void begin_overlapped() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename Params>
+cudaError_t launch_overlapped(void (*kernel)(Params), const Params& p, dim3 grid, int threads,
+                              int smem, cudaStream_t stream, int cluster = 1) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;   // log2(e)
 constexpr float kLn2 = 0.6931471805599453f;     // ln(2)
 

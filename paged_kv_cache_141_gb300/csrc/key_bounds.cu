@@ -69,6 +69,7 @@ template <> struct Pairs<__nv_bfloat16> { using T2 = __nv_bfloat162; };
 template <typename CT, typename BT, int D>
 __global__ void __launch_bounds__(kBoundsThreads)
 key_bounds_kernel(const __grid_constant__ BoundsParams p) {
+    begin_overlapped();
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
     using T2 = typename Pairs<CT>::T2;
     constexpr int E = 16 / (int)sizeof(CT);    // elements per lane
@@ -155,6 +156,7 @@ key_bounds_kernel(const __grid_constant__ BoundsParams p) {
 template <int D>
 __global__ void __launch_bounds__(kBoundsThreads)
 key_bounds_f32_kernel(const __grid_constant__ BoundsParams p) {
+    begin_overlapped();
     constexpr int LANES = D / 8;               // lanes per token row
     constexpr int ROWS = 32 / LANES;           // token rows per step of the warp
     const int lane = threadIdx.x & 31;
@@ -205,21 +207,22 @@ cudaError_t launch_bounds(const BoundsParams& p, int head_size, cudaStream_t str
     const int64_t gx = (units * 32 + kBoundsThreads - 1) / kBoundsThreads;
     if (gx > 0x3ffffff) return cudaErrorInvalidConfiguration;  // thread indices stay below 2^32
     const dim3 grid((unsigned)gx, p.num_seqs < 65535 ? p.num_seqs : 65535);
-    auto launch = [&](auto kernel) { kernel<<<grid, kBoundsThreads, 0, stream>>>(p); };
+    auto launch = [&](void (*kernel)(BoundsParams)) {
+        return launch_overlapped(kernel, p, grid, kBoundsThreads, 0, stream);
+    };
     if constexpr (std::is_same<CT, float>::value) {
         switch (head_size) {
-        case 64: launch(key_bounds_f32_kernel<64>); break;
-        case 128: launch(key_bounds_f32_kernel<128>); break;
-        default: launch(key_bounds_f32_kernel<256>); break;
+        case 64: return launch(key_bounds_f32_kernel<64>);
+        case 128: return launch(key_bounds_f32_kernel<128>);
+        default: return launch(key_bounds_f32_kernel<256>);
         }
     } else {
         switch (head_size) {
-        case 64: launch(key_bounds_kernel<CT, BT, 64>); break;
-        case 128: launch(key_bounds_kernel<CT, BT, 128>); break;
-        default: launch(key_bounds_kernel<CT, BT, 256>); break;
+        case 64: return launch(key_bounds_kernel<CT, BT, 64>);
+        case 128: return launch(key_bounds_kernel<CT, BT, 128>);
+        default: return launch(key_bounds_kernel<CT, BT, 256>);
         }
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

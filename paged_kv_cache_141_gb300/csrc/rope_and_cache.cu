@@ -208,6 +208,7 @@ __device__ __forceinline__ void flag_token(const RopeParams& p, bool ok, int64_t
 template <typename T, bool kE4M3, int D>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
+    begin_overlapped();
     constexpr int LANES = D / 16;
     const int lane = threadIdx.x & 31;
     const uint32_t g = (blockIdx.x * (uint32_t)kRopeThreads + threadIdx.x) / LANES;
@@ -271,6 +272,7 @@ rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
 template <typename T, bool kE4M3, int D, int kRows>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
+    begin_overlapped();
     constexpr int LANES = D / 16;
     const int lane = threadIdx.x & 31;
     constexpr int GROUPS = 32 / LANES;
@@ -352,19 +354,18 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
 }
 
 template <typename T, bool kE4M3, int D>
-cudaError_t launch_head_size(RopeParams p, cudaStream_t stream) {
+cudaError_t launch_head_size(const RopeParams& p, cudaStream_t stream) {
     const int64_t H = p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
     constexpr int LANES = D / 16;
     if (p.total_tokens > kPromptTokens) {
         constexpr int kRows = sizeof(T) == 4 ? 2 : 4;
         const int64_t grid = (p.total_tokens * 32 + kRopeThreads - 1) / kRopeThreads;
         if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-        rope_and_cache_prompt_kernel<T, kE4M3, D, kRows><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
-    } else {
-        const int64_t grid = (p.total_tokens * H * LANES + kRopeThreads - 1) / kRopeThreads;
-        rope_and_cache_kernel<T, kE4M3, D><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
+        return launch_overlapped(rope_and_cache_prompt_kernel<T, kE4M3, D, kRows>, p, dim3((unsigned)grid),
+                                 kRopeThreads, 0, stream);
     }
-    return cudaGetLastError();
+    const int64_t grid = (p.total_tokens * H * LANES + kRopeThreads - 1) / kRopeThreads;
+    return launch_overlapped(rope_and_cache_kernel<T, kE4M3, D>, p, dim3((unsigned)grid), kRopeThreads, 0, stream);
 }
 
 template <typename T, bool kE4M3>

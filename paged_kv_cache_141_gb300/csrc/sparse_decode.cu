@@ -71,6 +71,7 @@ struct Joined {                                     // one CTA's result, read by
 template <typename QT, typename CT, int D, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT)
 sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
+    begin_overlapped();
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
     using MT = typename MathType<CT>::T;            // the MMAs' type
     using Ops = MmaOps<MT>;

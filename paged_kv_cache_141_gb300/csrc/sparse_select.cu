@@ -14,6 +14,7 @@ constexpr int NT = 256;
 template <typename T, int D, bool kOneTile>
 __global__ void __launch_bounds__(NT, 2)
 select_blocks_kernel(const __grid_constant__ SelectParams p) {
+    begin_overlapped();
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ SelShared<NT> sh;
     cg::cluster_group cluster = cg::this_cluster();

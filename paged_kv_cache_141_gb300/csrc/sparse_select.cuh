@@ -903,8 +903,8 @@ int select_smem(SelectParams& p) {
     return p.side_bytes + p.taken_bytes + (p.keys_in_smem ? p.max_ctx_blocks * 4 : 0);
 }
 
-template <typename Kernel, typename Params>
-cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster, int threads, int smem,
+template <typename Params>
+cudaError_t launch_cluster(void (*kernel)(Params), const Params& p, int grid, int cluster, int threads, int smem,
                            cudaStream_t stream) {
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 200 * 1024);
     if (e != cudaSuccess) return e;
@@ -912,17 +912,7 @@ cudaError_t launch_cluster(Kernel kernel, const Params& p, int grid, int cluster
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return launch_overlapped(kernel, p, dim3(grid), threads, smem, stream, cluster);
 }
 
 }  // namespace pagedkv

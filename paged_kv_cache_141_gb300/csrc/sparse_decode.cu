@@ -84,6 +84,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     __shared__ SelShared<NT> sh;
     __shared__ Joined joined;
     __shared__ float wm[NW][8], wl[NW][8], wf[NW][8], q_unit[8];
+    __shared__ float sh_m[8 * kMaxCluster], sh_l[8 * kMaxCluster];
     int32_t* list = reinterpret_cast<int32_t*>(dyn);                   // the row's slabs
     uint4* qf = reinterpret_cast<uint4*>(dyn + sp.list_bytes);         // query fragments: D * 16 bytes
     uint8_t* work = dyn + sp.list_bytes + 16 * D;                      // selection, then the warps' O
@@ -161,14 +162,10 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
         if (rw.rank == 0 && selected)
             for (int i = total + threadIdx.x; i < p.num_select; i += NT) selected[i] = -1;
     }
-    if (C > 1 && !rw.all) {
-        cluster.sync();
-        if (rw.rank != 0) {
-            const int32_t* first = cluster.map_shared_rank(list, 0);
-            for (int i = threadIdx.x; i < total; i += NT) list[i] = first[i];
-        }
-    }
-    __syncthreads();
+    // (the others read the first one's list in place)
+    if (C > 1 && !rw.all) cluster.sync();
+    else __syncthreads();
+    const int32_t* slabs = C > 1 && !rw.all ? cluster.map_shared_rank(list, 0) : list;
 
     // ------------------------------------------------------------ attention
     const int len = total * B - (rw.n * B - rw.L);  // the selection's tokens
@@ -189,7 +186,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     // byte offset of a tile's first token in the caches; -1: no such block
     auto tile_at = [&](int tile) -> int64_t {
         const int j = per_block == 1 ? tile : tile / per_block;
-        const int slab = list[j];
+        const int slab = slabs[j];
         return slab < 0 ? -1 : ((int64_t)slab * B + (tile - j * per_block) * 16) * kRowBytes;
     };
     auto load_keys = [&](int64_t at) {
@@ -402,24 +399,39 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     if (C == 1) return;
     cluster.sync();
     // ------------------------------------------------------------ join the CTAs
-    for (int e = rw.rank * NT + threadIdx.x; e < G * (D / 2); e += C * NT) {
-        const int hd = e / (D / 2), d = 2 * (e - hd * (D / 2));
-        float M = -INFINITY;
-#pragma unroll 4
-        for (int r = 0; r < C; ++r) M = fmaxf(M, cluster.map_shared_rank(&joined, r)->m[hd]);
-        float l = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll 4
+    // each CTA's factor relative to the row's maximum, over the sum
+    if (threadIdx.x < 8 * C) {
+        const Joined* jr = cluster.map_shared_rank(&joined, threadIdx.x >> 3);
+        sh_m[threadIdx.x] = jr->m[threadIdx.x & 7];
+        sh_l[threadIdx.x] = jr->l[threadIdx.x & 7];
+    }
+    __syncthreads();
+    float f = 0.f;
+    if (threadIdx.x < 8 * C) {
+        const int hd = threadIdx.x & 7;
+        float M = -INFINITY, l = 0.f;
+        for (int r = 0; r < C; ++r) M = fmaxf(M, sh_m[8 * r + hd]);
+        for (int r = 0; r < C; ++r)
+            l += sh_m[8 * r + hd] == -INFINITY ? 0.f : fast_exp2(sh_m[8 * r + hd] - M) * sh_l[8 * r + hd];
+        f = sh_m[threadIdx.x] == -INFINITY ? 0.f : fast_exp2(sh_m[threadIdx.x] - M);
+        f *= l > 0.f || l != l ? sp.v_mul / l : 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 * C) sh_m[threadIdx.x] = f;
+    __syncthreads();
+    for (int e = rw.rank + C * threadIdx.x; e < G * (D / 4); e += C * NT) {
+        const int hd = e / (D / 4), d = 4 * (e - hd * (D / 4));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int r = 0; r < C; ++r) {
-            const Joined* jr = cluster.map_shared_rank(&joined, r);
-            const float2 o = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + hd * kPitch + d, r));
-            const float f = jr->m[hd] == -INFINITY ? 0.f : fast_exp2(jr->m[hd] - M);
-            l += f * jr->l[hd];
-            o0 += f * o.x;
-            o1 += f * o.y;
+            const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(wo + hd * kPitch + d, r));
+            const float w = sh_m[8 * r + hd];
+            o.x += w * x.x;
+            o.y += w * x.y;
+            o.z += w * x.z;
+            o.w += w * x.w;
         }
-        const float r = l > 0.f || l != l ? sp.v_mul / l : 0.f;
-        out[hd * D + d] = from_float<QT>(o0 * r);
-        out[hd * D + d + 1] = from_float<QT>(o1 * r);
+        *reinterpret_cast<uint2*>(out + hd * D + d) = make_uint2(OutOps::pack(o.x, o.y), OutOps::pack(o.z, o.w));
     }
     cluster.sync();                                 // no CTA leaves while its memory is read
 }

@@ -204,11 +204,12 @@ struct SelShared {
     float err[kMaxCluster];             // per CTA: the largest sum of magnitudes,
     float lowest[kMaxCluster];          // and the range of its finite scores
     float highest[kMaxCluster];
+    float sum[kMaxCluster];             // of its finite scores
     int bins[kBins];
     int bin;                            // the threshold's, and the candidates above it
     int above;
     int part[2][kWarps];             // count(): per-warp sums, double-buffered
-    float fpart[3][kWarps];
+    float fpart[4][kWarps];
     uint64_t bits_all[kWarps], bits_any[kWarps];
     int list_n;
     int list[kRankList];
@@ -297,37 +298,49 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
                                   uint32_t* taken, int nc, int want, float mag, int C, int s, int h,
                                   const int32_t* table) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float lowest = sh.lowest[0], highest = sh.highest[0];
-    for (int r = 1; r < C; ++r) {
-        lowest = fminf(lowest, sh.lowest[r]);
-        highest = fmaxf(highest, sh.highest[r]);
+    float lowest = INFINITY, highest = -INFINITY, mean = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {                    // (unrolled: loads in flight together)
+        lowest = fminf(lowest, r < C ? sh.lowest[r] : INFINITY);
+        highest = fmaxf(highest, r < C ? sh.highest[r] : -INFINITY);
+        mean += r < C ? sh.sum[r] : 0.f;
     }
-    const float range = highest - lowest;
-    const float scale = (float)(SelShared<NT>::kBins - 1) / range;
-    if (!(isfinite(mag) && highest > lowest && isfinite(scale))) return false;
+    mean = __fdividef(mean, (float)nc);                        // only places the cut
     const float err2 = mag * (2.f * kScoreEps * 1.01f);        // both errors
-    // non-decreasing in k; blocks the table does not name score -infinity: bin 0
+    constexpr int kBatch = 8;                                  // keys read before one is used
+    // Where few are taken, first only the scores a quarter of the way from the
+    // mean to the highest: shared-memory atomics are what the pass costs.
+    float cut = want < nc / 16 && isfinite(mean) ? mean + 0.25f * (highest - mean) : -INFINITY;
+    float bottom, range, scale;
+    // non-decreasing in k; what lies below the range goes to bin 0
     auto bin_of = [&](float k) {
-        const int b = __float2int_rz((k - lowest) * scale);
+        const int b = __float2int_rz((k - bottom) * scale);
         return b < 0 ? 0 : (b >= SelShared<NT>::kBins ? SelShared<NT>::kBins - 1 : b);
     };
-    for (int i = threadIdx.x; i < SelShared<NT>::kBins; i += NT) sh.bins[i] = 0;
-    if (threadIdx.x == 0) sh.list_n = 0;
-    __syncthreads();
-    // both passes read eight keys a thread before they use one
-    constexpr int kBatch = 8;
-    for (int i0 = threadIdx.x; i0 < nc; i0 += kBatch * NT) {
-        float k[kBatch];
+    for (;;) {
+        bottom = fmaxf(cut, lowest);
+        range = highest - bottom;
+        scale = (float)(SelShared<NT>::kBins - 1) / range;
+        if (!(isfinite(mag) && highest > bottom && isfinite(scale))) return false;
+        for (int i = threadIdx.x; i < SelShared<NT>::kBins; i += NT) sh.bins[i] = 0;
+        if (threadIdx.x == 0) {
+            sh.list_n = 0;
+            sh.bin = -1;
+        }
+        __syncthreads();
+        for (int i0 = threadIdx.x; i0 < nc; i0 += kBatch * NT) {
+            float k[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * NT < nc ? keys[i0 + j * NT] : 0.f;
+            for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * NT < nc ? keys[i0 + j * NT] : out_key();
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (i0 + j * NT < nc) atomicAdd(&sh.bins[bin_of(k[j])], 1);
-    }
-    __syncthreads();
-    // the bin where the count from the top reaches want: thread t has the four
-    // bins below SelShared<NT>::kBins - 4 t
-    {
+            for (int j = 0; j < kBatch; ++j) {
+                const int b = bin_of(k[j]);
+                if (k[j] >= cut) atomicAdd(&sh.bins[b], 1);    // (not the NaN)
+            }
+        }
+        __syncthreads();
+        // the bin where the count from the top reaches want: thread t has the
+        // four bins below kBins - 4 t
         const int top = SelShared<NT>::kBins - 1 - 4 * (int)threadIdx.x;
         int c[4], sum = 0;
 #pragma unroll
@@ -352,14 +365,17 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
                 before += c[j];
             }
         }
+        __syncthreads();
+        if (sh.bin >= 0) break;
+        cut = -INFINITY;                                       // too few above the cut
+        __syncthreads();
     }
-    __syncthreads();
     // Every block that can change sides is within err2 of that bin's range of
     // scores (to the rounding of bin_of and of the range's ends). Above: taken.
     const int bin = sh.bin;
-    const float slack = err2 + range * 0x1p-20f + (fabsf(lowest) + fabsf(highest)) * 0x1p-21f;
-    const float from = bin == 0 ? -INFINITY : lowest + (float)bin / scale - slack;
-    const float to = lowest + (float)(bin + 1) / scale + slack;
+    const float slack = err2 + range * 0x1p-20f + (fabsf(bottom) + fabsf(highest)) * 0x1p-21f;
+    const float from = bin == 0 && cut == -INFINITY ? -INFINITY : bottom + (float)bin / scale - slack;
+    const float to = bottom + (float)(bin + 1) / scale + slack;
     int near_above = 0;                                        // counted above the bin, but not settled
     for (int i0 = warp * 32; i0 < nc; i0 += kBatch * NT) {
         float k[kBatch];
@@ -368,18 +384,25 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
             const int i = i0 + j * NT + lane;
             k[j] = i < nc ? keys[i] : out_key();               // (NaN: in neither)
         }
+        uint32_t word = 0, near = 0;                           // lane j: the words of keys j
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const uint32_t word = __ballot_sync(0xffffffffu, k[j] > to);
-            if (lane == 0 && i0 + j * NT < nc) taken[(i0 + j * NT) >> 5] = word;
-            if (k[j] >= from && k[j] <= to) {
-                const int at = atomicAdd(&sh.list_n, 1);
-                if (at < SelShared<NT>::kRankList) {
-                    sh.list[at] = i0 + j * NT + lane;
-                    sh.list_score[at] = k[j];
-                }
-                near_above += bin_of(k[j]) > bin;
+            const uint32_t w = __ballot_sync(0xffffffffu, k[j] > to);
+            if (lane == j) word = w;
+            near |= (uint32_t)(k[j] >= from && k[j] <= to) << j;
+        }
+        if (lane < kBatch && i0 + lane * NT < nc) taken[(i0 + lane * NT) >> 5] = word;
+        while (near) {
+            const int j = __ffs(near) - 1;
+            near &= near - 1;
+            const int i = i0 + j * NT + lane;
+            const float x = keys[i];
+            const int at = atomicAdd(&sh.list_n, 1);
+            if (at < SelShared<NT>::kRankList) {
+                sh.list[at] = i;
+                sh.list_score[at] = x;
             }
+            near_above += bin_of(x) > bin;
         }
     }
     int turn = 0;
@@ -537,7 +560,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
         // ------------------------------------------------ approximate scores
         cluster_barrier(cluster, C);                           // the sides; the first CTA runs: its memory may be written
         float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(keys, 0) : keys;
-        float worst = 0.f, lowest = INFINITY, highest = -INFINITY;
+        float worst = 0.f, lowest = INFINITY, highest = -INFINITY, total = 0.f;
         if constexpr (std::is_same<T, float>::value) {
             constexpr int E = D / 32;
             for (int i = rank * (NT / 32) + warp; i < nc; i += C * (NT / 32)) {
@@ -569,6 +592,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
                     }
                     lowest = fminf(lowest, best);
                     highest = fmaxf(highest, best);
+                    if (lane == 0) total += best;
                 }
                 if (lane == 0) out_keys[i] = best;
             }
@@ -599,6 +623,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
                         worst = max_nan(worst, mag[r]);
                         lowest = fminf(lowest, best[r]);
                         highest = fmaxf(highest, best[r]);
+                        if (t4 == 0) total += best[r];
                     }
                     if (t4 == 0 && i < nc) out_keys[i] = ok ? best[r] : -INFINITY;
                 }
@@ -680,11 +705,13 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
             worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
             lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, m));
             highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, m));
+            total += __shfl_xor_sync(0xffffffffu, total, m);
         }
         if (lane == 0) {
             sh.fpart[0][warp] = worst;
             sh.fpart[1][warp] = lowest;
             sh.fpart[2][warp] = highest;
+            sh.fpart[3][warp] = total;
         }
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -692,17 +719,20 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
                 worst = max_nan(worst, sh.fpart[0][w]);
                 lowest = fminf(lowest, sh.fpart[1][w]);
                 highest = fmaxf(highest, sh.fpart[2][w]);
+                total += sh.fpart[3][w];
             }
             *cluster.map_shared_rank(&sh.err[rank], 0) = worst;
             *cluster.map_shared_rank(&sh.lowest[rank], 0) = lowest;
             *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
+            *cluster.map_shared_rank(&sh.sum[rank], 0) = total;
         }
     }
     cluster_barrier(cluster, C);
     if (rank != 0) return;
 
     float mag = 0.f;
-    for (int r = 0; r < C; ++r) mag = max_nan(mag, sh.err[r]);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) mag = max_nan(mag, r < C ? sh.err[r] : 0.f);
     if (take_by_histogram<T, D, NT>(p, sh, keys, rw.taken, nc, want, mag, C, s, h, table + lo)) return;
     {
         int turn = 0;

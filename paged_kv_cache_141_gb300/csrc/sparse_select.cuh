@@ -77,7 +77,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// The two sides of eight query elements: min(x, 0) or max(x, 0), NaN kept.
+// The two sides of a pair of query elements: min(x, 0) or max(x, 0), NaN kept;
+// bfloat16 ones times 2^40, so that products of bfloat16's small numbers stay
+// above binary32's smallest (binary16's do).
 template <typename T>
 __device__ __forceinline__ uint32_t side2(uint32_t w, bool positive) {
     if constexpr (std::is_same<T, __half>::value) {
@@ -88,7 +90,8 @@ __device__ __forceinline__ uint32_t side2(uint32_t w, bool positive) {
     } else {
         const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w);
         const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
-        const __nv_bfloat162 y = positive ? __hmax2_nan(x, z) : __hmin2_nan(x, z);
+        const __nv_bfloat162 y = __hmul2(positive ? __hmax2_nan(x, z) : __hmin2_nan(x, z),
+                                         __float2bfloat162_rn(0x1p40f));
         return *reinterpret_cast<const uint32_t*>(&y);
     }
 }
@@ -287,6 +290,12 @@ __device__ __forceinline__ K kth_largest(SelShared<NT>& sh, int n, int want, int
     return prefix;
 }
 
+// Whether approximate scores with terms of up to mag may be relied on: far above
+// what an underflow could drop, or all zero.
+__device__ __forceinline__ bool reliable(float mag) {
+    return isfinite(mag) && (mag == 0.f || mag >= 0x1p-100f);
+}
+
 // The score that ordered() puts below every value: a block not taken.
 __device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu); }
 
@@ -321,7 +330,7 @@ __device__ bool take_by_histogram(const SelectParams& p, SelShared<NT>& sh, cons
         bottom = fmaxf(cut, lowest);
         range = highest - bottom;
         scale = (float)(SelShared<NT>::kBins - 1) / range;
-        if (!(isfinite(mag) && highest > bottom && isfinite(scale))) return false;
+        if (!(reliable(mag) && highest > bottom && isfinite(scale))) return false;
         for (int i = threadIdx.x; i < SelShared<NT>::kBins; i += NT) sh.bins[i] = 0;
         if (threadIdx.x == 0) {
             sh.list_n = 0;
@@ -738,7 +747,7 @@ __device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::clu
         int turn = 0;
         uint32_t thr = 0;                                      // taken candidates: ordered(key) >= thr
         const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
-        const bool finite = isfinite(mag);
+        const bool finite = reliable(mag);
         // Settled blocks: those that beat (or lose to) every block on the other
         // side of the threshold by more than both errors. in_above: taken for
         // certain above it; out_below: left out for certain below it.

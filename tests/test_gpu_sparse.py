@@ -312,6 +312,19 @@ def test_scores_that_binary32_cannot_tell_apart(dtype):
     p.check(out, sel, 20, 0, 1)
 
 
+@pytest.mark.parametrize("dtype,size", [("bf16", 2.0 ** -66), ("bf16", 2.0 ** -80), ("bf16", 2.0 ** 63), ("bf16", 2.0 ** 90),
+                                        ("f32", 2.0 ** -60), ("f32", 2.0 ** -70), ("f16", 2.0 ** -12)])
+def test_very_small_and_large_magnitudes(dtype, size):
+    # the squares of these pass binary32's range at either end
+    p = Pool([16 * 120], dtype=dtype, seed=11)
+    p.fill_bounds()
+    p.bounds.copy_((p.bounds.double().nan_to_num(0) * size).to(p.dt))
+    p.query.copy_((p.query.double() * size).to(p.dt))
+    sel = p.decode(15, 1, 1)[1]
+    for h in range(2):
+        assert sel[0, h].tolist() == p.want_selected(0, h, 15, 1, 1)
+
+
 def test_infinite_and_nan_bounds_come_first():
     p = Pool([16 * 60], dtype="f16", seed=10)
     p.fill_bounds()

@@ -577,7 +577,7 @@ pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* bloc
  * rows: each with the sequence's table and the length it sees, so that each
  * query selects its own blocks. Other arguments, shapes, types and device
  * checks as pa_decode; a group of at most 128 heads, at most 2^19 blocks to a
- * context, and num_blocks * num_kv_heads below 2^31.
+ * context, num_blocks at least 1, and num_blocks * num_kv_heads below 2^31.
  */
 size_t pa_sparse_decode_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                         int head_size, int block_size, int max_context_len,

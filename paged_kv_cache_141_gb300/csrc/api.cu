@@ -951,7 +951,7 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
         (long long)num_seqs * num_kv_heads > 0x7fffffffll)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
-    if (!out || !k_bounds || !aligned16(out, k_bounds) || !aligned(selected, 4))
+    if (!out || !k_bounds || num_blocks < 1 || !aligned16(out, k_bounds) || !aligned(selected, 4))
         return PA_ERR_INVALID_ARG;
     const SparsePlan l = sparse_plan(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
                                      max_context_len, num_select);

@@ -82,7 +82,7 @@ def sparse(pk, **kw):
                                 dict(first=3, recent=2), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1, K=2 ** 31 - 1),
                                 dict(scale=0.0), dict(scale=-0.5), dict(scale=float("nan")), dict(out=None),
                                 dict(kb=None), dict(kb=ODD), dict(sel=ctypes.c_void_p(257)), dict(q=None),
-                                dict(bt=None), dict(ct=3, ks=-1.0)])
+                                dict(bt=None), dict(ct=3, ks=-1.0), dict(nb=0)])
 def test_sparse_invalid(pk, kw):
     assert sparse(pk, **kw) == pk.PA_ERR_INVALID_ARG
 
@@ -118,3 +118,28 @@ def test_sparse_workspace(pk):
 
 def test_rope_sections(pk):
     assert pk.rope_sections((2, 1, 3)) == b"\0\0\1\2\2\2"
+
+
+def test_binding_checks_before_the_library(pk):
+    """The marshalling module's own refusals: host tensors, wrong objects and types."""
+    import torch
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    kv = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    cs = torch.zeros(8, 64)
+    i64 = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA device"):
+        pk.rope_and_cache(q, q, kv, kv, cache, cache, cs, i64, i64)
+    with pytest.raises(TypeError, match="query must be a tensor"):
+        pk.rope_and_cache(q, [1], kv, kv, cache, cache, cs, i64, i64)
+    with pytest.raises(TypeError):
+        pk.rope_and_cache(q, q)
+    bounds = torch.zeros(4, 2, 2, 64, dtype=torch.bfloat16)
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        pk.key_bounds(bounds, cache, torch.zeros(2, 3, dtype=torch.int32), i32, 16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        pk.sparse_decode(q, q, cache, cache, bounds, torch.zeros(2, 3, dtype=torch.int32), i32, 16, 0.1, 4,
+                         torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="workspace must be a tensor"):
+        pk.sparse_decode(q, q, cache, cache, bounds, i32, i32, 16, 0.1, 4, None)

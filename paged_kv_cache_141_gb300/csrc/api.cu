@@ -380,6 +380,15 @@ SparsePlan sparse_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
     return l;
 }
 
+// Shapes of the fused kernel: 16-bit query, one MMA tile of heads, whole
+// 16-token tiles per block, head sizes whose accumulators leave registers for
+// loads in flight (256 does not), and a selection that fits shared memory.
+// Others select into a table of slabs that the paged decode reads.
+bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width) {
+    return (q_dtype == PA_F16 || q_dtype == PA_BF16) && group <= 8 && head_size <= 128 &&
+           block_size % 16 == 0 && table_width <= 8192;
+}
+
 bool sparse_sizes_ok(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
                      int block_size, int max_context_len, int num_select) {
     return num_seqs >= 0 && num_q_heads > 0 && num_kv_heads > 0 &&
@@ -991,7 +1000,11 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
         f.v_cache = v_cache;
         f.q_mul = p.q_mul;
         f.v_mul = p.v_mul;
-        return from_cuda(launch_sparse_decode(f, head_size, q_dtype, cache_dtype, cs));
+        if (cache_dtype == PA_FP8_E4M3)
+            return from_cuda(q_dtype == PA_F16 ? launch_sparse_decode_f16_e4m3(f, head_size, cs)
+                                               : launch_sparse_decode_bf16_e4m3(f, head_size, cs));
+        return from_cuda(q_dtype == PA_F16 ? launch_sparse_decode_f16(f, head_size, cs)
+                                           : launch_sparse_decode_bf16(f, head_size, cs));
     }
     const cudaError_t e = launch_select_blocks(sp, head_size, q_dtype, cs);
     if (e != cudaSuccess) return PA_ERR_CUDA;

@@ -230,7 +230,7 @@ struct SelectParams {
     int keys_in_smem;             // and whether the scores are kept there
 };
 
-// The fused block-sparse decode (sparse_decode.cu).
+// The fused block-sparse decode (sparse_decode.cuh).
 struct SparseParams {
     SelectParams sel;             // slab_tables, slab_lens unused
     void* out;                    // [S, Hq, D]
@@ -241,9 +241,10 @@ struct SparseParams {
     int list_bytes;               // set by the launcher
 };
 
-bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width);
-cudaError_t launch_sparse_decode(const SparseParams& sp, int head_size, pa_dtype q_dtype,
-                                 pa_dtype cache_dtype, cudaStream_t stream);
+cudaError_t launch_sparse_decode_f16(const SparseParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_sparse_decode_bf16(const SparseParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_sparse_decode_f16_e4m3(const SparseParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_sparse_decode_bf16_e4m3(const SparseParams& p, int head_size, cudaStream_t stream);
 
 cudaError_t launch_select_blocks(const SelectParams& p, int head_size, pa_dtype q_dtype,
                                  cudaStream_t stream);

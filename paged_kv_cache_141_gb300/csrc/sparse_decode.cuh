@@ -1,4 +1,4 @@
-// sparse_decode.cu -- the block-sparse decode in one kernel: a cluster of CTAs
+// sparse_decode.cuh -- the block-sparse decode in one kernel: a cluster of CTAs
 // takes one (sequence, KV head), scores its blocks and selects (see
 // sparse_select.cuh), and then attends to the selection:
 //     out_h = sum_i softmax_i(scale q_h . k_i) v_i   over the selected tokens.
@@ -25,11 +25,11 @@
 // them scaled by a power of two to at most 2 in magnitude, exact but for
 // components more than 2^14 below the head's largest. Partial results are joined in
 // shared memory across the warps, and through the cluster's across CTAs.
+#pragma once
+
 #include "sparse_select.cuh"
 
 namespace pagedkv {
-
-namespace {
 
 // A tile's keys of tokens g and g + 8 (this lane's chunks), and values of
 // tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9.
@@ -440,10 +440,8 @@ template <typename QT, typename CT, int D>
 cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
     const int rows = sp.sel.num_seqs * sp.sel.num_kv_heads;
     const int C = select_cluster(rows, sp.sel.max_ctx_blocks);
-    // an SM for every CTA: 16 warps each, else two CTAs of 8. (A cluster of 16
-    // takes 16 SMs of one GPC then, and only some GPCs have them free: 8
-    // clusters ran in two waves, 47 us against 30 with 8 warps.)
-    const bool wide = C < 16 && rows * C <= 152;
+    // an SM for every CTA: 16 warps each, else two CTAs of 8 an SM
+    const bool wide = rows * C <= 152;
     const int select = select_smem<QT, D>(sp.sel);
     const int join = (wide ? 16 : 8) * 8 * (D + 4) * (int)sizeof(float);
     sp.list_bytes = (sp.sel.table_width * 4 + 15) / 16 * 16;
@@ -453,33 +451,14 @@ cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
         sp.q_mul *= 256.f;                          // codes are widened times 2^-8
         sp.v_mul *= 256.f;
     }
-    if (wide)
-        return launch_cluster(sparse_decode_kernel<QT, CT, D, 512>, sp, rows * C, C, 512, smem, stream);
+    if (wide) return launch_cluster(sparse_decode_kernel<QT, CT, D, 512>, sp, rows * C, C, 512, smem, stream);
     return launch_cluster(sparse_decode_kernel<QT, CT, D, 256>, sp, rows * C, C, 256, smem, stream);
 }
 
+// Head size 64 or 128 (sparse_fused).
 template <typename QT, typename CT>
-cudaError_t launch_sparse_d(const SparseParams& sp, int head_size, cudaStream_t stream) {
+cudaError_t launch_sparse_types(const SparseParams& sp, int head_size, cudaStream_t stream) {
     return head_size == 64 ? launch_sparse<QT, CT, 64>(sp, stream) : launch_sparse<QT, CT, 128>(sp, stream);
-}
-
-}  // namespace
-
-// Shapes of the fused kernel: 16-bit query, one MMA tile of heads, whole
-// 16-token tiles per block, head sizes whose accumulators leave registers for
-// loads in flight (256 does not), and a selection that fits shared memory.
-bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width) {
-    return (q_dtype == PA_F16 || q_dtype == PA_BF16) && group <= 8 && head_size <= 128 &&
-           block_size % 16 == 0 && table_width <= 8192;
-}
-
-cudaError_t launch_sparse_decode(const SparseParams& sp, int head_size, pa_dtype q_dtype,
-                                 pa_dtype cache_dtype, cudaStream_t stream) {
-    if (cache_dtype == PA_FP8_E4M3)
-        return q_dtype == PA_F16 ? launch_sparse_d<__half, e4m3_t>(sp, head_size, stream)
-                                 : launch_sparse_d<__nv_bfloat16, e4m3_t>(sp, head_size, stream);
-    return q_dtype == PA_F16 ? launch_sparse_d<__half, __half>(sp, head_size, stream)
-                             : launch_sparse_d<__nv_bfloat16, __nv_bfloat16>(sp, head_size, stream);
 }
 
 }  // namespace pagedkv

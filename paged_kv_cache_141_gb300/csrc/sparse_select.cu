@@ -2,7 +2,7 @@
 // slabs (block * Hkv + head) in ascending block order, so that only its last
 // block, the newest, can be partial: the paged decode reads it as a block
 // table of S * Hkv one-head sequences. For the shapes that the fused kernel
-// (sparse_decode.cu) does not take.
+// (sparse_decode.cuh) does not take.
 #include "sparse_select.cuh"
 
 namespace pagedkv {

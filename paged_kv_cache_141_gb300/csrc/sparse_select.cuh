@@ -27,7 +27,7 @@
 // (2 D elements per block) bounds the kernel for batches, the latency of the
 // score-search-emit chain for few rows.
 //
-// Shared by the fused kernel (sparse_decode.cu) and the selection kernel whose
+// Shared by the fused kernel (sparse_decode.cuh) and the selection kernel whose
 // slab tables the paged decode reads (sparse_select.cu).
 #pragma once
 
@@ -40,7 +40,7 @@ namespace pagedkv {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;         // the portable size
 // Keys of up to this many blocks are kept in shared memory (two CTAs per SM);
 // longer contexts' in the workspace.
 constexpr int kSmemKeys = 24 * 1024;
@@ -921,10 +921,11 @@ __device__ __forceinline__ int32_t slab_of(const SelectParams& p, const SelRow& 
 
 // ---------------------------------------------------------------- host side
 
-// CTAs per row: as many
-// as fit on 152 SMs with a tile of 16 blocks or more for every warp. For many
-// rows one CTA each wins, two on an SM: their selections overlap other rows'
-// scoring.
+// CTAs per row: as many as fit on 152 SMs with a tile of 16 blocks or more for
+// every warp. For many rows one CTA each wins, two on an SM: their selections
+// overlap other rows' scoring. (8 rows of 8192 blocks: steps of 30.6, 26.8 and
+// 26.3 us with 7, 8 and 12 CTAs of 16 warps; 14 and more no longer have 8
+// clusters placed at once: 46 us.)
 inline int select_cluster(int rows, int max_ctx_blocks) {
     int C = 1;
     while (C < kMaxCluster && rows <= 152 / (2 * C) && max_ctx_blocks >= 2 * C * 256) C *= 2;
@@ -947,10 +948,6 @@ cudaError_t launch_cluster(void (*kernel)(Params), const Params& p, int grid, in
                            cudaStream_t stream) {
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 200 * 1024);
     if (e != cudaSuccess) return e;
-    if (cluster > 8) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     return launch_overlapped(kernel, p, dim3(grid), threads, smem, stream, cluster);
 }
 

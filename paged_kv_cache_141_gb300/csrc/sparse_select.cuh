@@ -549,334 +549,349 @@ __device__ void stage_sides(const SelectParams& p, const SelRow& rw) {
     }
 }
 
+// Approximate scores of the candidates (all CTAs of the cluster) into the first
+// CTA's keys, and what it needs to know of them (err, lowest, highest, sum).
+template <typename T, int D, bool kOneTile, int NT>
+__device__ __forceinline__ void score_candidates(const SelectParams& p, SelShared<NT>& sh,
+                                                 cg::cluster_group& cluster, const SelRow& rw) {
+    constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
+    constexpr int NQ = STEPS / 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int C = rw.C, rank = rw.rank, s = rw.s, h = rw.h, nc = rw.nc, lo = rw.lo;
+    const int32_t* table = rw.table;
+    const uint4* sides = rw.sides;
+    float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(rw.keys, 0) : rw.keys;
+    float worst = 0.f, lowest = INFINITY, highest = -INFINITY, total = 0.f;
+    if constexpr (std::is_same<T, float>::value) {
+        constexpr int E = D / 32;
+        for (int i = rank * (NT / 32) + warp; i < nc; i += C * (NT / 32)) {
+            const int64_t blk = table[lo + i];
+            float best = -INFINITY;
+            if (blk >= 0 && blk < p.num_blocks) {
+                const float* bounds = static_cast<const float*>(p.k_bounds) +
+                                      ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
+                float bl[E], bh[E], q[E];
+                RowLoader<float, E>::load(bounds, bl);
+                RowLoader<float, E>::load(bounds + D, bh);
+                for (int g = 0; g < p.group; ++g) {
+                    RowLoader<float, E>::load(static_cast<const float*>(p.query) +
+                                              ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
+                    float sum = 0.f, mag = 0.f;
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const float t = q[j] * (q[j] < 0.f ? bl[j] : bh[j]);
+                        sum += t;
+                        mag += fabsf(t);
+                    }
+#pragma unroll
+                    for (int m = 16; m > 0; m >>= 1) {
+                        sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                        mag += __shfl_xor_sync(0xffffffffu, mag, m);
+                    }
+                    best = fmaxf(best, sum);
+                    worst = max_nan(worst, mag);
+                }
+                lowest = fminf(lowest, best);
+                highest = fmaxf(highest, best);
+                if (lane == 0) total += best;
+            }
+            if (lane == 0) out_keys[i] = best;
+        }
+    } else {
+        const int ntiles = (p.group + 7) / 8;
+        const int g = lane >> 2, t4 = lane & 3;
+        const int tiles = (nc + 15) / 16;
+        const int stride = C * (NT / 32);
+        // this lane's two blocks of a tile, and their bounds rows (block 0's
+        // where the table names none)
+        auto block_of = [&](int tile, int r) {
+            const int i = tile * 16 + g + 8 * r;
+            return table[lo + (i < nc ? i : nc - 1)];
+        };
+        auto there = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
+        auto row_of = [&](int blk) {
+            return static_cast<const T*>(p.k_bounds) +
+                   ((size_t)(there(blk) ? blk : 0) * p.num_kv_heads + h) * 2 * D + 8 * t4;
+        };
+        auto finish = [&](int tile, const int (&blk)[2], float (&best)[2], float (&mag)[2]) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+                best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+                const int i = tile * 16 + g + 8 * r;
+                const bool ok = there(blk[r]);
+                if (ok && i < nc) {
+                    worst = max_nan(worst, mag[r]);
+                    lowest = fminf(lowest, best[r]);
+                    highest = fmaxf(highest, best[r]);
+                    if (t4 == 0) total += best[r];
+                }
+                if (t4 == 0 && i < nc) out_keys[i] = ok ? best[r] : -INFINITY;
+            }
+        };
+        // maxima over the heads of one MMA tile
+        auto over_heads = [&](int nt, const float (&c)[4], const float (&m)[4], float (&best)[2], float (&mag)[2]) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (nt * 8 + 2 * t4 + e < p.group) {
+                        best[r] = fmaxf(best[r], c[2 * r + e]);
+                        mag[r] = max_nan(mag[r], m[2 * r + e]);
+                    }
+        };
+        int tile = rank * (NT / 32) + warp;
+        if constexpr (kOneTile) {
+            // the next quarter's loads are in flight while one is multiplied
+            Quarter buf[2];
+            int blk[2], nblk[2];                            // this tile's blocks, the next one's
+            const T *x = nullptr, *y = nullptr;
+            auto after = [&](int t) { return t + stride < tiles ? t + stride : t; };
+            if (tile < tiles) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    blk[r] = rw.ahead[r];                  // (past nc: any block, its score unused)
+                    nblk[r] = block_of(after(tile), r);
+                }
+                x = row_of(blk[0]);
+                y = row_of(blk[1]);
+                buf[0].load(x, y);
+            }
+            for (; tile < tiles; tile += stride) {
+                const int next = after(tile);
+                const int fblk[2] = {block_of(after(next), 0), block_of(after(next), 1)};
+                float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    if (q + 1 < NQ) {
+                        buf[(q + 1) & 1].load(x + 128 * (q + 1), y + 128 * (q + 1));
+                    } else {
+                        x = row_of(nblk[0]);
+                        y = row_of(nblk[1]);
+                        if (next != tile) buf[(q + 1) & 1].load(x, y);
+                    }
+                    add_quarter<T>(buf[q & 1], sides + 128 * q + lane, c, m);
+                }
+                if (NQ == 1) buf[0] = buf[1];
+                float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                over_heads(0, c, m, best, mag);
+                finish(tile, blk, best, mag);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    blk[r] = nblk[r];
+                    nblk[r] = fblk[r];
+                }
+            }
+        } else {
+            for (; tile < tiles; tile += stride) {
+                const int blk[2] = {block_of(tile, 0), block_of(tile, 1)};
+                const T *x = row_of(blk[0]), *y = row_of(blk[1]);
+                float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
+                for (int nt = 0; nt < ntiles; ++nt) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        Quarter b;
+                        b.load(x + 128 * q, y + 128 * q);
+                        add_quarter<T>(b, sides + (nt * STEPS + 4 * q) * 32 + lane, c, m);
+                    }
+                    over_heads(nt, c, m, best, mag);
+                }
+                finish(tile, blk, best, mag);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
+        lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, m));
+        highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, m));
+        total += __shfl_xor_sync(0xffffffffu, total, m);
+    }
+    if (lane == 0) {
+        sh.fpart[0][warp] = worst;
+        sh.fpart[1][warp] = lowest;
+        sh.fpart[2][warp] = highest;
+        sh.fpart[3][warp] = total;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < (NT / 32); ++w) {
+            worst = max_nan(worst, sh.fpart[0][w]);
+            lowest = fminf(lowest, sh.fpart[1][w]);
+            highest = fmaxf(highest, sh.fpart[2][w]);
+            total += sh.fpart[3][w];
+        }
+        *cluster.map_shared_rank(&sh.err[rank], 0) = worst;
+        *cluster.map_shared_rank(&sh.lowest[rank], 0) = lowest;
+        *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
+        *cluster.map_shared_rank(&sh.sum[rank], 0) = total;
+    }
+}
+
+// Marks the taken candidates where the histogram does not decide: a search over
+// the bits of the approximate scores, exact scores of all that it leaves
+// unsettled (every block where magnitudes are not reliable), and if those are
+// many a search over the exact scores' bits.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void take_by_search(const SelectParams& p, SelShared<NT>& sh, const SelRow& rw,
+                                            float mag) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = rw.row, s = rw.s, h = rw.h, nc = rw.nc, want = rw.want, lo = rw.lo;
+    const int32_t* table = rw.table;
+    float* keys = rw.keys;
+    int turn = 0;
+    uint32_t thr = 0;                                      // taken candidates: ordered(key) >= thr
+    const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
+    const bool finite = reliable(mag);
+    // Settled blocks: those that beat (or lose to) every block on the other
+    // side of the threshold by more than both errors. in_above: taken for
+    // certain above it; out_below: left out for certain below it.
+    double in_above = INFINITY, out_below = -INFINITY;
+    if (finite) {
+        bool exact;
+        thr = kth_largest<uint32_t, NT>(sh, nc, want, turn, exact, [&](int i) { return ordered(keys[i]); },
+                                    [](int) { return false; });
+        float a = INFINITY, b = -INFINITY;                 // the smallest taken, the largest left out
+        for (int i = threadIdx.x; i < nc; i += NT) {
+            const float k = keys[i];
+            if (ordered(k) >= thr) a = fminf(a, k);
+            else b = fmaxf(b, k);
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            a = fminf(a, __shfl_xor_sync(0xffffffffu, a, m));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, m));
+        }
+        if (lane == 0) {
+            sh.fpart[0][warp] = a;
+            sh.fpart[1][warp] = b;
+        }
+        __syncthreads();
+        for (int w = 0; w < (NT / 32); ++w) {
+            a = fminf(a, sh.fpart[0][w]);
+            b = fmaxf(b, sh.fpart[1][w]);
+        }
+        if (!exact) b = a;                                 // equal keys across the threshold
+        in_above = (double)b + err2;
+        out_below = (double)a - err2;
+    }
+    const float kOut = out_key();
+    auto settled = [&](float k) { return finite && ((double)k > in_above || (double)k < out_below); };
+    // count the certain ones and the unsettled
+    int in = 0, open = 0;
+    for (int i = threadIdx.x; i < nc; i += NT) {
+        const float k = keys[i];
+        if (!settled(k)) ++open;
+        else in += (double)k > in_above;
+    }
+    in = cta_sum(sh, in, turn);
+    open = cta_sum(sh, open, turn);
+    const int left = want - in;                            // places for the unsettled
+    if (!finite) thr = ordered(INFINITY);
+    if (left < open) {
+        // ------------------------------------------- exact scores of the unsettled
+        // (A zero query, say of a padding row, makes every score 0, exactly.)
+        const bool zeros = mag == 0.f;
+        const bool small = open <= SelShared<NT>::kRankList && !zeros;
+        if (threadIdx.x == 0) sh.list_n = 0;
+        __syncthreads();
+        uint64_t* exact_keys = p.exact_keys + (size_t)row * p.max_ctx_blocks;
+        if (zeros)
+            for (int i = threadIdx.x; i < nc; i += NT) exact_keys[i] = ordered64(keys[i]);
+        for (int i0 = zeros ? nc : warp * 32; i0 < nc; i0 += NT) {
+            const bool mine = i0 + lane < nc && !settled(keys[i0 + lane]);
+            uint32_t votes = __ballot_sync(0xffffffffu, mine);
+            while (votes) {
+                const int i = i0 + __ffs(votes) - 1;
+                votes &= votes - 1;
+                const uint64_t k = exact_score<T, D>(p, s, h, table[lo + i], lane);
+                if (lane == 0) {
+                    if (small) {
+                        const int at = atomicAdd(&sh.list_n, 1);
+                        sh.list[at] = i;
+                        sh.list_key[at] = k;
+                    } else {
+                        exact_keys[i] = k;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (small) {
+            // the list's order varies, the ranks do not: (key, index) differ in every pair
+            const int e = threadIdx.x;
+            if (e < open) {
+                const uint64_t k = sh.list_key[e];
+                const int i = sh.list[e];
+                int before = 0;
+                for (int o = 0; o < open; ++o)
+                    before += sh.list_key[o] > k || (sh.list_key[o] == k && sh.list[o] < i);
+                keys[i] = before < left ? INFINITY : kOut;
+            }
+        } else if (left > 0) {
+            bool exact;
+            const uint64_t t = kth_largest<uint64_t, NT>(
+                sh, nc, left, turn, exact, [&](int i) { return exact_keys[i]; },
+                [&](int i) { return settled(keys[i]); });
+            int above = 0;
+            for (int i = threadIdx.x; i < nc; i += NT)
+                above += !settled(keys[i]) && exact_keys[i] > t;
+            above = cta_sum(sh, above, turn);
+            int ties = exact ? 0x7fffffff : left - above;  // places for keys equal to t, lowest first
+            for (int i0 = 0; i0 < nc; i0 += NT) {
+                const int i = i0 + threadIdx.x;
+                const bool mine = i < nc && !settled(keys[i]);
+                const uint64_t k = mine ? exact_keys[i] : 0;
+                const bool tie = mine && k == t;
+                const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+                if (lane == 0) sh.part[turn][warp] = __popc(votes);
+                __syncthreads();
+                int at = __popc(votes & ((1u << lane) - 1)), total = 0;
+                for (int w = 0; w < (NT / 32); ++w) {
+                    if (w < warp) at += sh.part[turn][w];
+                    total += sh.part[turn][w];
+                }
+                turn ^= 1;
+                if (mine) keys[i] = k > t || (tie && at < ties) ? INFINITY : kOut;
+                if (!exact) ties -= total < ties ? total : ties;
+            }
+        } else {
+            for (int i = threadIdx.x; i < nc; i += NT)
+                if (!settled(keys[i])) keys[i] = kOut;
+        }
+        __syncthreads();
+    } else {
+        // every unsettled block is taken: they are the candidates from out_below on
+        for (int i = threadIdx.x; i < nc; i += NT)
+            if (!settled(keys[i])) keys[i] = INFINITY;
+        __syncthreads();
+    }
+    for (int i0 = warp * 32; i0 < nc; i0 += NT) {
+        const uint32_t word = __ballot_sync(0xffffffffu, i0 + lane < nc && ordered(keys[i0 + lane]) >= thr);
+        if (lane == 0) rw.taken[i0 >> 5] = word;
+    }
+    __syncthreads();
+}
+
 // Scores the candidates (all CTAs of the cluster) and marks the taken ones (the
 // first CTA, in rw.taken). All CTAs meet at two cluster barriers if rw.scored,
 // else at none; the sides have been staged. kOneTile: groups of at most eight
 // heads, one MMA tile.
 template <typename T, int D, bool kOneTile, int NT>
-__device__ void score_and_take(const SelectParams& p, SelShared<NT>& sh, cg::cluster_group& cluster,
-                               const SelRow& rw) {
+__device__ __forceinline__ void score_and_take(const SelectParams& p, SelShared<NT>& sh,
+                                               cg::cluster_group& cluster, const SelRow& rw) {
     if (!rw.scored) return;
-    constexpr int STEPS = 2 * D / 32;                          // 64-byte steps of a bounds row (16-bit types)
-    constexpr int NQ = STEPS / 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int C = rw.C, rank = rw.rank, row = rw.row, s = rw.s, h = rw.h;
-    const int nc = rw.nc, want = rw.want, lo = rw.lo;
-    const int32_t* table = rw.table;
-    const uint4* sides = rw.sides;
-    float* keys = rw.keys;
-    {
-        // ------------------------------------------------ approximate scores
-        cluster_barrier(cluster, C);                           // the sides; the first CTA runs: its memory may be written
-        float* out_keys = p.keys_in_smem ? cluster.map_shared_rank(keys, 0) : keys;
-        float worst = 0.f, lowest = INFINITY, highest = -INFINITY, total = 0.f;
-        if constexpr (std::is_same<T, float>::value) {
-            constexpr int E = D / 32;
-            for (int i = rank * (NT / 32) + warp; i < nc; i += C * (NT / 32)) {
-                const int64_t blk = table[lo + i];
-                float best = -INFINITY;
-                if (blk >= 0 && blk < p.num_blocks) {
-                    const float* bounds = static_cast<const float*>(p.k_bounds) +
-                                          ((size_t)blk * p.num_kv_heads + h) * 2 * D + lane * E;
-                    float bl[E], bh[E], q[E];
-                    RowLoader<float, E>::load(bounds, bl);
-                    RowLoader<float, E>::load(bounds + D, bh);
-                    for (int g = 0; g < p.group; ++g) {
-                        RowLoader<float, E>::load(static_cast<const float*>(p.query) +
-                                                  ((size_t)s * p.num_q_heads + h * p.group + g) * D + lane * E, q);
-                        float sum = 0.f, mag = 0.f;
-#pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            const float t = q[j] * (q[j] < 0.f ? bl[j] : bh[j]);
-                            sum += t;
-                            mag += fabsf(t);
-                        }
-#pragma unroll
-                        for (int m = 16; m > 0; m >>= 1) {
-                            sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                            mag += __shfl_xor_sync(0xffffffffu, mag, m);
-                        }
-                        best = fmaxf(best, sum);
-                        worst = max_nan(worst, mag);
-                    }
-                    lowest = fminf(lowest, best);
-                    highest = fmaxf(highest, best);
-                    if (lane == 0) total += best;
-                }
-                if (lane == 0) out_keys[i] = best;
-            }
-        } else {
-            const int ntiles = (p.group + 7) / 8;
-            const int g = lane >> 2, t4 = lane & 3;
-            const int tiles = (nc + 15) / 16;
-            const int stride = C * (NT / 32);
-            // this lane's two blocks of a tile, and their bounds rows (block 0's
-            // where the table names none)
-            auto block_of = [&](int tile, int r) {
-                const int i = tile * 16 + g + 8 * r;
-                return table[lo + (i < nc ? i : nc - 1)];
-            };
-            auto there = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
-            auto row_of = [&](int blk) {
-                return static_cast<const T*>(p.k_bounds) +
-                       ((size_t)(there(blk) ? blk : 0) * p.num_kv_heads + h) * 2 * D + 8 * t4;
-            };
-            auto finish = [&](int tile, const int (&blk)[2], float (&best)[2], float (&mag)[2]) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
-                    best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-                    const int i = tile * 16 + g + 8 * r;
-                    const bool ok = there(blk[r]);
-                    if (ok && i < nc) {
-                        worst = max_nan(worst, mag[r]);
-                        lowest = fminf(lowest, best[r]);
-                        highest = fmaxf(highest, best[r]);
-                        if (t4 == 0) total += best[r];
-                    }
-                    if (t4 == 0 && i < nc) out_keys[i] = ok ? best[r] : -INFINITY;
-                }
-            };
-            // maxima over the heads of one MMA tile
-            auto over_heads = [&](int nt, const float (&c)[4], const float (&m)[4], float (&best)[2], float (&mag)[2]) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (nt * 8 + 2 * t4 + e < p.group) {
-                            best[r] = fmaxf(best[r], c[2 * r + e]);
-                            mag[r] = max_nan(mag[r], m[2 * r + e]);
-                        }
-            };
-            int tile = rank * (NT / 32) + warp;
-            if constexpr (kOneTile) {
-                // the next quarter's loads are in flight while one is multiplied
-                Quarter buf[2];
-                int blk[2], nblk[2];                            // this tile's blocks, the next one's
-                const T *x = nullptr, *y = nullptr;
-                auto after = [&](int t) { return t + stride < tiles ? t + stride : t; };
-                if (tile < tiles) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        blk[r] = rw.ahead[r];                  // (past nc: any block, its score unused)
-                        nblk[r] = block_of(after(tile), r);
-                    }
-                    x = row_of(blk[0]);
-                    y = row_of(blk[1]);
-                    buf[0].load(x, y);
-                }
-                for (; tile < tiles; tile += stride) {
-                    const int next = after(tile);
-                    const int fblk[2] = {block_of(after(next), 0), block_of(after(next), 1)};
-                    float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        if (q + 1 < NQ) {
-                            buf[(q + 1) & 1].load(x + 128 * (q + 1), y + 128 * (q + 1));
-                        } else {
-                            x = row_of(nblk[0]);
-                            y = row_of(nblk[1]);
-                            if (next != tile) buf[(q + 1) & 1].load(x, y);
-                        }
-                        add_quarter<T>(buf[q & 1], sides + 128 * q + lane, c, m);
-                    }
-                    if (NQ == 1) buf[0] = buf[1];
-                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
-                    over_heads(0, c, m, best, mag);
-                    finish(tile, blk, best, mag);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        blk[r] = nblk[r];
-                        nblk[r] = fblk[r];
-                    }
-                }
-            } else {
-                for (; tile < tiles; tile += stride) {
-                    const int blk[2] = {block_of(tile, 0), block_of(tile, 1)};
-                    const T *x = row_of(blk[0]), *y = row_of(blk[1]);
-                    float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
-                    for (int nt = 0; nt < ntiles; ++nt) {
-                        float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            Quarter b;
-                            b.load(x + 128 * q, y + 128 * q);
-                            add_quarter<T>(b, sides + (nt * STEPS + 4 * q) * 32 + lane, c, m);
-                        }
-                        over_heads(nt, c, m, best, mag);
-                    }
-                    finish(tile, blk, best, mag);
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) {
-            worst = max_nan(worst, __shfl_xor_sync(0xffffffffu, worst, m));
-            lowest = fminf(lowest, __shfl_xor_sync(0xffffffffu, lowest, m));
-            highest = fmaxf(highest, __shfl_xor_sync(0xffffffffu, highest, m));
-            total += __shfl_xor_sync(0xffffffffu, total, m);
-        }
-        if (lane == 0) {
-            sh.fpart[0][warp] = worst;
-            sh.fpart[1][warp] = lowest;
-            sh.fpart[2][warp] = highest;
-            sh.fpart[3][warp] = total;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < (NT / 32); ++w) {
-                worst = max_nan(worst, sh.fpart[0][w]);
-                lowest = fminf(lowest, sh.fpart[1][w]);
-                highest = fmaxf(highest, sh.fpart[2][w]);
-                total += sh.fpart[3][w];
-            }
-            *cluster.map_shared_rank(&sh.err[rank], 0) = worst;
-            *cluster.map_shared_rank(&sh.lowest[rank], 0) = lowest;
-            *cluster.map_shared_rank(&sh.highest[rank], 0) = highest;
-            *cluster.map_shared_rank(&sh.sum[rank], 0) = total;
-        }
-    }
-    cluster_barrier(cluster, C);
-    if (rank != 0) return;
-
+    cluster_barrier(cluster, rw.C);                            // the sides; the first CTA runs: its memory may be written
+    score_candidates<T, D, kOneTile, NT>(p, sh, cluster, rw);
+    cluster_barrier(cluster, rw.C);
+    if (rw.rank != 0) return;
     float mag = 0.f;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) mag = max_nan(mag, r < C ? sh.err[r] : 0.f);
-    if (take_by_histogram<T, D, NT>(p, sh, keys, rw.taken, nc, want, mag, C, s, h, table + lo)) return;
-    {
-        int turn = 0;
-        uint32_t thr = 0;                                      // taken candidates: ordered(key) >= thr
-        const double err2 = 2.0 * (double)kScoreEps * (double)mag * 1.001;
-        const bool finite = reliable(mag);
-        // Settled blocks: those that beat (or lose to) every block on the other
-        // side of the threshold by more than both errors. in_above: taken for
-        // certain above it; out_below: left out for certain below it.
-        double in_above = INFINITY, out_below = -INFINITY;
-        if (finite) {
-            bool exact;
-            thr = kth_largest<uint32_t, NT>(sh, nc, want, turn, exact, [&](int i) { return ordered(keys[i]); },
-                                        [](int) { return false; });
-            float a = INFINITY, b = -INFINITY;                 // the smallest taken, the largest left out
-            for (int i = threadIdx.x; i < nc; i += NT) {
-                const float k = keys[i];
-                if (ordered(k) >= thr) a = fminf(a, k);
-                else b = fmaxf(b, k);
-            }
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) {
-                a = fminf(a, __shfl_xor_sync(0xffffffffu, a, m));
-                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, m));
-            }
-            if (lane == 0) {
-                sh.fpart[0][warp] = a;
-                sh.fpart[1][warp] = b;
-            }
-            __syncthreads();
-            for (int w = 0; w < (NT / 32); ++w) {
-                a = fminf(a, sh.fpart[0][w]);
-                b = fmaxf(b, sh.fpart[1][w]);
-            }
-            if (!exact) b = a;                                 // equal keys across the threshold
-            in_above = (double)b + err2;
-            out_below = (double)a - err2;
-        }
-        const float kOut = out_key();
-        auto settled = [&](float k) { return finite && ((double)k > in_above || (double)k < out_below); };
-        // count the certain ones and the unsettled
-        int in = 0, open = 0;
-        for (int i = threadIdx.x; i < nc; i += NT) {
-            const float k = keys[i];
-            if (!settled(k)) ++open;
-            else in += (double)k > in_above;
-        }
-        in = cta_sum(sh, in, turn);
-        open = cta_sum(sh, open, turn);
-        const int left = want - in;                            // places for the unsettled
-        if (!finite) thr = ordered(INFINITY);
-        if (left < open) {
-            // ------------------------------------------- exact scores of the unsettled
-            // (A zero query, say of a padding row, makes every score 0, exactly.)
-            const bool zeros = mag == 0.f;
-            const bool small = open <= SelShared<NT>::kRankList && !zeros;
-            if (threadIdx.x == 0) sh.list_n = 0;
-            __syncthreads();
-            uint64_t* exact_keys = p.exact_keys + (size_t)row * p.max_ctx_blocks;
-            if (zeros)
-                for (int i = threadIdx.x; i < nc; i += NT) exact_keys[i] = ordered64(keys[i]);
-            for (int i0 = zeros ? nc : warp * 32; i0 < nc; i0 += NT) {
-                const bool mine = i0 + lane < nc && !settled(keys[i0 + lane]);
-                uint32_t votes = __ballot_sync(0xffffffffu, mine);
-                while (votes) {
-                    const int i = i0 + __ffs(votes) - 1;
-                    votes &= votes - 1;
-                    const uint64_t k = exact_score<T, D>(p, s, h, table[lo + i], lane);
-                    if (lane == 0) {
-                        if (small) {
-                            const int at = atomicAdd(&sh.list_n, 1);
-                            sh.list[at] = i;
-                            sh.list_key[at] = k;
-                        } else {
-                            exact_keys[i] = k;
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-            if (small) {
-                // the list's order varies, the ranks do not: (key, index) differ in every pair
-                const int e = threadIdx.x;
-                if (e < open) {
-                    const uint64_t k = sh.list_key[e];
-                    const int i = sh.list[e];
-                    int before = 0;
-                    for (int o = 0; o < open; ++o)
-                        before += sh.list_key[o] > k || (sh.list_key[o] == k && sh.list[o] < i);
-                    keys[i] = before < left ? INFINITY : kOut;
-                }
-            } else if (left > 0) {
-                bool exact;
-                const uint64_t t = kth_largest<uint64_t, NT>(
-                    sh, nc, left, turn, exact, [&](int i) { return exact_keys[i]; },
-                    [&](int i) { return settled(keys[i]); });
-                int above = 0;
-                for (int i = threadIdx.x; i < nc; i += NT)
-                    above += !settled(keys[i]) && exact_keys[i] > t;
-                above = cta_sum(sh, above, turn);
-                int ties = exact ? 0x7fffffff : left - above;  // places for keys equal to t, lowest first
-                for (int i0 = 0; i0 < nc; i0 += NT) {
-                    const int i = i0 + threadIdx.x;
-                    const bool mine = i < nc && !settled(keys[i]);
-                    const uint64_t k = mine ? exact_keys[i] : 0;
-                    const bool tie = mine && k == t;
-                    const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-                    if (lane == 0) sh.part[turn][warp] = __popc(votes);
-                    __syncthreads();
-                    int at = __popc(votes & ((1u << lane) - 1)), total = 0;
-                    for (int w = 0; w < (NT / 32); ++w) {
-                        if (w < warp) at += sh.part[turn][w];
-                        total += sh.part[turn][w];
-                    }
-                    turn ^= 1;
-                    if (mine) keys[i] = k > t || (tie && at < ties) ? INFINITY : kOut;
-                    if (!exact) ties -= total < ties ? total : ties;
-                }
-            } else {
-                for (int i = threadIdx.x; i < nc; i += NT)
-                    if (!settled(keys[i])) keys[i] = kOut;
-            }
-            __syncthreads();
-        } else {
-            // every unsettled block is taken: they are the candidates from out_below on
-            for (int i = threadIdx.x; i < nc; i += NT)
-                if (!settled(keys[i])) keys[i] = INFINITY;
-            __syncthreads();
-        }
-        for (int i0 = warp * 32; i0 < nc; i0 += NT) {
-            const uint32_t word = __ballot_sync(0xffffffffu, i0 + lane < nc && ordered(keys[i0 + lane]) >= thr);
-            if (lane == 0) rw.taken[i0 >> 5] = word;
-        }
-        __syncthreads();
-    }
+    for (int r = 0; r < kMaxCluster; ++r) mag = max_nan(mag, r < rw.C ? sh.err[r] : 0.f);
+    if (!take_by_histogram<T, D, NT>(p, sh, rw.keys, rw.taken, rw.nc, rw.want, mag, rw.C, rw.s, rw.h,
+                                     rw.table + rw.lo))
+        take_by_search<T, D, NT>(p, sh, rw, mag);
 }
 
 // Calls put(position, block) for every block the row takes, positions in block

@@ -381,12 +381,11 @@ SparsePlan sparse_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head
 }
 
 // Shapes of the fused kernel: 16-bit query, one MMA tile of heads, whole
-// 16-token tiles per block, head sizes whose accumulators leave registers for
-// loads in flight (256 does not), and a selection that fits shared memory.
-// Others select into a table of slabs that the paged decode reads.
-bool sparse_fused(pa_dtype q_dtype, int group, int head_size, int block_size, int table_width) {
-    return (q_dtype == PA_F16 || q_dtype == PA_BF16) && group <= 8 && head_size <= 128 &&
-           block_size % 16 == 0 && table_width <= 8192;
+// 16-token tiles per block, and a selection that fits shared memory. Others
+// select into a table of slabs that the paged decode reads.
+bool sparse_fused(pa_dtype q_dtype, int group, int block_size, int table_width) {
+    return (q_dtype == PA_F16 || q_dtype == PA_BF16) && group <= 8 && block_size % 16 == 0 &&
+           table_width <= 8192;
 }
 
 bool sparse_sizes_ok(int num_seqs, int num_q_heads, int num_kv_heads, int head_size,
@@ -992,7 +991,7 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
     sp.num_select = num_select;
     sp.first_blocks = first_blocks;
     sp.recent_blocks = recent_blocks;
-    if (sparse_fused(q_dtype, p.group, head_size, block_size, l.table_width)) {
+    if (sparse_fused(q_dtype, p.group, block_size, l.table_width)) {
         SparseParams f{};
         f.sel = sp;
         f.out = out;

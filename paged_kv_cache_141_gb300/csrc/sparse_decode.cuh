@@ -42,16 +42,14 @@ struct Tile16 {                                     // 16-bit caches
 
 template <int D>
 struct Tile16<e4m3_t, D> {
-    static constexpr int KJ = D / 64;
-    using VWord = typename std::conditional<D == 128, uint4, uint2>::type;   // D / 8 codes
+    static constexpr int KJ = D / 64, VW = D / 32;  // D / 8 codes a lane and token
     uint4 x[KJ], y[KJ];
-    VWord v[4];
+    uint32_t v[4][VW];
 };
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
-__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
 
 // Codes in bytes 0 and 2 (even) or 1 and 3 (odd) of w as a binary16 pair of
 // their values times 2^-8 (see e4m3x2_to_f16x2_scaled).
@@ -69,7 +67,7 @@ struct Joined {                                     // one CTA's result, read by
 };
 
 template <typename QT, typename CT, int D, int NT>
-__global__ void __launch_bounds__(NT, 512 / NT)
+__global__ void __launch_bounds__(NT, D == 256 ? 1 : 512 / NT)
 sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     begin_overlapped();
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
@@ -206,9 +204,22 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
             const uint8_t* row = v + tok * kRowBytes;
             const bool there = tok < nvalid;
             if constexpr (kFp8) {
-                typename Tile::VWord w{};
-                if (there) w = __ldg(reinterpret_cast<const typename Tile::VWord*>(row + g * (D / 8)));
-                tl.v[r] = w;
+                const uint8_t* codes = row + g * (D / 8);
+                if constexpr (D == 64) {
+                    const uint2 w = there ? __ldg(reinterpret_cast<const uint2*>(codes)) : make_uint2(0, 0);
+                    tl.v[r][0] = w.x;
+                    tl.v[r][1] = w.y;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < Tile::VW; u += 4) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (there) w = __ldg(reinterpret_cast<const uint4*>(codes + 4 * u));
+                        tl.v[r][u] = w.x;
+                        tl.v[r][u + 1] = w.y;
+                        tl.v[r][u + 2] = w.z;
+                        tl.v[r][u + 3] = w.w;
+                    }
+                }
             } else {
 #pragma unroll
                 for (int u = 0; u < Tile::VU; ++u) {
@@ -312,8 +323,8 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
             for (int i = 0; i < MD; ++i) {
                 // codes 2 i and 2 i + 1 of each token's chunk: rows g and g + 8
                 const uint32_t sel = i & 1 ? 0x7632 : 0x5410;
-                const uint32_t v01 = __byte_perm(word_of(tl.v[0], i / 2), word_of(tl.v[1], i / 2), sel);
-                const uint32_t v23 = __byte_perm(word_of(tl.v[2], i / 2), word_of(tl.v[3], i / 2), sel);
+                const uint32_t v01 = __byte_perm(tl.v[0][i / 2], tl.v[1][i / 2], sel);
+                const uint32_t v23 = __byte_perm(tl.v[2][i / 2], tl.v[3][i / 2], sel);
                 const uint32_t a[4] = {widen_even(v01), widen_odd(v01), widen_even(v23), widen_odd(v23)};
                 Ops::mma(acc[i], a, hi[0], hi[1]);
             }
@@ -439,9 +450,15 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
 template <typename QT, typename CT, int D>
 cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
     const int rows = sp.sel.num_seqs * sp.sel.num_kv_heads;
-    const int C = select_cluster(rows, sp.sel.max_ctx_blocks);
-    // an SM for every CTA: 16 warps each, else two CTAs of 8 an SM
-    const bool wide = rows * C <= 152;
+    int C = select_cluster(rows, sp.sel.max_ctx_blocks);
+    // An SM for every CTA: 16 warps each, else two CTAs of 8 an SM (head size
+    // 256: a tile's fragments take the registers of one CTA of 8 warps). Not
+    // every GPC has 16 SMs for two clusters of 8 that fill theirs: of 16 clusters
+    // one waits for a second wave (2 contexts of 131072: 49 us, 33 us with 8
+    // warps; head size 256 in clusters of 8 and 4: 53 and 41 us).
+    const bool placed = rows * C <= (C == kMaxCluster ? 112 : 152);
+    const bool wide = D < 256 && placed;
+    if (D == 256 && !placed && C > 1) C /= 2;
     const int select = select_smem<QT, D>(sp.sel);
     const int join = (wide ? 16 : 8) * 8 * (D + 4) * (int)sizeof(float);
     sp.list_bytes = (sp.sel.table_width * 4 + 15) / 16 * 16;
@@ -451,14 +468,19 @@ cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
         sp.q_mul *= 256.f;                          // codes are widened times 2^-8
         sp.v_mul *= 256.f;
     }
-    if (wide) return launch_cluster(sparse_decode_kernel<QT, CT, D, 512>, sp, rows * C, C, 512, smem, stream);
+    if constexpr (D < 256) {
+        if (wide) return launch_cluster(sparse_decode_kernel<QT, CT, D, 512>, sp, rows * C, C, 512, smem, stream);
+    }
     return launch_cluster(sparse_decode_kernel<QT, CT, D, 256>, sp, rows * C, C, 256, smem, stream);
 }
 
-// Head size 64 or 128 (sparse_fused).
 template <typename QT, typename CT>
 cudaError_t launch_sparse_types(const SparseParams& sp, int head_size, cudaStream_t stream) {
-    return head_size == 64 ? launch_sparse<QT, CT, 64>(sp, stream) : launch_sparse<QT, CT, 128>(sp, stream);
+    switch (head_size) {
+    case 64: return launch_sparse<QT, CT, 64>(sp, stream);
+    case 128: return launch_sparse<QT, CT, 128>(sp, stream);
+    default: return launch_sparse<QT, CT, 256>(sp, stream);
+    }
 }
 
 }  // namespace pagedkv

@@ -938,9 +938,8 @@ __device__ __forceinline__ int32_t slab_of(const SelectParams& p, const SelRow& 
 
 // CTAs per row: as many as fit on 152 SMs with a tile of 16 blocks or more for
 // every warp. For many rows one CTA each wins, two on an SM: their selections
-// overlap other rows' scoring. (8 rows of 8192 blocks: steps of 30.6, 26.8 and
-// 26.3 us with 7, 8 and 12 CTAs of 16 warps; 14 and more no longer have 8
-// clusters placed at once: 46 us.)
+// overlap other rows' scoring. (8 rows of 8192 blocks: 69, 44, 31 and 25 us with
+// 1, 2, 4 and 8 CTAs of 16 warps; 112 rows of 1170: 34, 51 and 77 with 1, 2, 4.)
 inline int select_cluster(int rows, int max_ctx_blocks) {
     int C = 1;
     while (C < kMaxCluster && rows <= 152 / (2 * C) && max_ctx_blocks >= 2 * C * 256) C *= 2;

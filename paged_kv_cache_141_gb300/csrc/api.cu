@@ -876,6 +876,8 @@ pa_status pa_rope_and_cache(void* query_out, const void* query, int64_t query_st
     p.eps = eps;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.k_inv = isnormal(1.f / k_scale) && isnormal(k_scale) ? 1.f / k_scale : 0.f;
+    p.v_inv = isnormal(1.f / v_scale) && isnormal(v_scale) ? 1.f / v_scale : 0.f;
     return from_cuda(launch_rope_and_cache(p, head_size, in_dtype, cache_dtype,
                                            static_cast<cudaStream_t>(stream)));
 }

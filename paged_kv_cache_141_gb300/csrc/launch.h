@@ -171,6 +171,8 @@ struct RopeParams {
     float eps;
     float k_scale;
     float v_scale;
+    float k_inv;                  // 1 / scale, or 0 where that is no normal number
+    float v_inv;
     uint32_t freq_axes[8];        // two bits per frequency
 };
 

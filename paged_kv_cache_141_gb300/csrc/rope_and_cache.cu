@@ -78,13 +78,31 @@ struct Chunk {
     }
 };
 
-// Eight binary32 values as E4M3 codes of x / scale (the KV write's conversion).
-__device__ __forceinline__ void store8_e4m3(uint8_t* dst, const float (&x)[8], float scale) {
+// Eight binary32 values as E4M3 codes of x / scale, the KV write's conversion: an
+// IEEE division, then round to nearest even with saturation. The division is
+// most of a row's arithmetic, and the code rarely needs it: x * inv (inv =
+// 1 / scale, rounded; both roundings move the quotient by less than 2 units in
+// its last place) gives the same code unless the quotient lies that close to a
+// midpoint of two codes, whose low 20 mantissa bits are 0x80000. Those, and
+// quotients below E4M3's normal range (other midpoints), are divided; inv = 0
+// (a scale whose reciprocal is out of range) divides all.
+__device__ __forceinline__ void store8_e4m3(uint8_t* dst, const float (&x)[8], float scale, float inv) {
+    float q[8];
+    bool divide = inv == 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = __fmul_rn(x[i], inv);
+        const uint32_t u = __float_as_uint(q[i]) & 0x7fffffffu;
+        divide |= (u & 0xfffffu) - 0x7fffcu <= 8u || (u < 0x3c800000u && u != 0u);         // 2^-6
+    }
+    if (divide) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
+    }
     uint32_t packed[2];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const float2 q = make_float2(__fdiv_rn(x[i], scale), __fdiv_rn(x[i + 1], scale));
-        const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q[i], q[i + 1]), __NV_SATFINITE, __NV_E4M3);
         if ((i & 2) == 0) packed[i / 4] = two;
         else packed[i / 4] |= two << 16;
     }
@@ -252,8 +270,9 @@ rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     if (!is_v) turn.rotate(a, b);
     if (!is_q && kE4M3) {
         uint8_t* y = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + dst;
-        store8_e4m3(y + turn.a_off, a, is_v ? p.v_scale : p.k_scale);
-        store8_e4m3(y + turn.b_off, b, is_v ? p.v_scale : p.k_scale);
+        const float scale = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv : p.k_inv;
+        store8_e4m3(y + turn.a_off, a, scale, inv);
+        store8_e4m3(y + turn.b_off, b, scale, inv);
     } else {
         T* y = static_cast<T*>(is_q ? p.query_out : p.k_cache) + dst;
         xa.round_from(a);
@@ -301,7 +320,8 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     if (!ok) return;
 
     // one kind of rows: `heads` of them from src, row h to dst + h * step
-    auto rows = [&](auto kind, const T* src, void* dst, int heads, size_t step, const float* w, float scale) {
+    auto rows = [&](auto kind, const T* src, void* dst, int heads, size_t step, const float* w, float scale,
+                    float inv) {
         constexpr int kKind = decltype(kind)::value;           // 0 queries, 1 keys, 2 values
         constexpr bool kCodes = kE4M3 && kKind != 0;
         float wa[8], wb[8];
@@ -330,8 +350,8 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
                 }
                 if constexpr (kCodes) {
                     uint8_t* y = static_cast<uint8_t*>(dst) + h * step;
-                    store8_e4m3(y + turn.a_off, a, scale);
-                    store8_e4m3(y + turn.b_off, b, scale);
+                    store8_e4m3(y + turn.a_off, a, scale, inv);
+                    store8_e4m3(y + turn.b_off, b, scale, inv);
                 } else {
                     T* y = static_cast<T*>(dst) + h * step;
                     xa[i].round_from(a);
@@ -343,14 +363,16 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
         }
     };
     rows(std::integral_constant<int, 0>{}, query,
-         static_cast<T*>(p.query_out) + (size_t)t * Hq * D, Hq, D, p.q_weight, 1.f);
+         static_cast<T*>(p.query_out) + (size_t)t * Hq * D, Hq, D, p.q_weight, 1.f, 1.f);
     if (row0 < 0) return;
     constexpr int kCell = kE4M3 ? 1 : (int)sizeof(T);
     const size_t step = (size_t)B * D;
     rows(std::integral_constant<int, 1>{}, static_cast<const T*>(p.key) + t * p.key_stride,
-         static_cast<uint8_t*>(p.k_cache) + (size_t)row0 * D * kCell, Hkv, step, p.k_weight, p.k_scale);
+         static_cast<uint8_t*>(p.k_cache) + (size_t)row0 * D * kCell, Hkv, step, p.k_weight, p.k_scale,
+         p.k_inv);
     rows(std::integral_constant<int, 2>{}, static_cast<const T*>(p.value) + t * p.value_stride,
-         static_cast<uint8_t*>(p.v_cache) + (size_t)row0 * D * kCell, Hkv, step, nullptr, p.v_scale);
+         static_cast<uint8_t*>(p.v_cache) + (size_t)row0 * D * kCell, Hkv, step, nullptr, p.v_scale,
+         p.v_inv);
 }
 
 template <typename T, bool kE4M3, int D>

@@ -157,6 +157,34 @@ def test_block_sizes(B):
     s.check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [0.011, 1.0, 1 / 3, 3e-5, 1e-39, 2e38, 448.0])
+def test_e4m3_values_are_the_quotients_codes(dtype, scale):
+    """Every stored value has the code of the IEEE quotient: random ones, midpoints of two codes and
+    their neighbours, quotients below the normal range, beyond the largest, and special values."""
+    T, Hkv, D = 1500, 2, 64
+    s = Step(T, 2, Hkv, D, dtype=dtype, e4m3=True, fused=False)
+    g = torch.Generator().manual_seed(1)
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mid = (codes[:-1] + codes[1:]) / 2
+    v = torch.randn((T, Hkv, D), generator=g).double() * 40
+    pick = torch.randint(0, 126, (T, Hkv, D), generator=g)
+    near = mid[pick] * (1 + torch.randint(-3, 4, (T, Hkv, D), generator=g) * 2.0 ** -23)
+    v = torch.where(torch.rand((T, Hkv, D), generator=g) < 0.5, near, v)
+    v[:, 0, 0] = torch.where(torch.arange(T) % 2 == 0, 0.0, -0.0)
+    v[:, 0, 1:6] = torch.tensor([float("inf"), float("-inf"), float("nan"), 1e4, 2.0 ** -11])
+    s.v = (v * scale).to(s.dt).cuda()
+    s.slots = torch.arange(T, device="cuda")
+    s.ks = s.vs = scale
+    assert s.run() == 0
+    want = (s.v.float() / torch.tensor(scale, dtype=torch.float32, device="cuda"))
+    nan = want.isnan()
+    want = want.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    got = s.vc.transpose(1, 2).reshape(-1, Hkv, D)[:T]
+    assert torch.equal(got[~nan], want[~nan])
+    assert bool(((got[nan] & 0x7F) == 0x7F).all())
+
+
 def test_only_one_norm_and_large_prompt():
     s = Step(5000, 16, 4, 128, norm=True, dtype="f16")
     s.kw = None

@@ -286,8 +286,9 @@ rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
 // once for all its heads (several warps per token, each loading them, measured
 // slower at every length: 8000 tokens 38.7, 38.7, 44.8 and 66.3 us with 1, 2, 4
 // and 8). The warp's 512 / D row groups take alternate heads, kRows of them with
-// all loads issued before the first is used; the first ones of the queries are on
-// their way while the token's position becomes angles.
+// all loads issued before the first is used (keys and values together); the
+// first ones of the queries are on their way while the token's position becomes
+// angles.
 template <typename T, bool kE4M3, int D, int kRows>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
@@ -301,78 +302,102 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, B = p.block_size;
     Turn<T, D> turn(p, lane);
     Chunk<T> xa[kRows], xb[kRows];
-    auto load = [&](const T* src, int h0, int heads) {
+    // rows h0, h0 + GROUPS, ... of the token: of its queries, or of its keys (the
+    // first Hkv) and values
+    const T* query = static_cast<const T*>(p.query) + t * p.query_stride;
+    const T* key = static_cast<const T*>(p.key) + t * p.key_stride;
+    const T* value = static_cast<const T*>(p.value) + t * p.value_stride;
+    auto load_queries = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int h = h0 + i * GROUPS;
-            if (h < heads) {
-                xa[i].load(src + (int64_t)h * D + turn.a_off);
-                xb[i].load(src + (int64_t)h * D + turn.b_off);
+            if (h < Hq) {
+                xa[i].load(query + h * D + turn.a_off);
+                xb[i].load(query + h * D + turn.b_off);
             }
         }
     };
-    const T* query = static_cast<const T*>(p.query) + t * p.query_stride;
-    load(query, grp, Hq);
+    auto load_keys_values = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int h = h0 + i * GROUPS;
+            if (h < 2 * Hkv) {
+                const T* src = h < Hkv ? key + h * D : value + (h - Hkv) * D;
+                xa[i].load(src + turn.a_off);
+                xb[i].load(src + turn.b_off);
+            }
+        }
+    };
+    load_queries(grp);
     const int64_t slot = p.slots[t];
     const bool ok = turn.load(p, t, lane);
     const int64_t row0 = cache_row(p, slot);
     if (lane == 0) flag_token(p, ok, slot, row0);
     if (!ok) return;
 
-    // one kind of rows: `heads` of them from src, row h to dst + h * step
-    auto rows = [&](auto kind, const T* src, void* dst, int heads, size_t step, const float* w, float scale,
-                    float inv) {
-        constexpr int kKind = decltype(kind)::value;           // 0 queries, 1 keys, 2 values
-        constexpr bool kCodes = kE4M3 && kKind != 0;
-        float wa[8], wb[8];
-        if (kKind != 2 && w) {
+    float wa[8], wb[8];
+    auto load_weights = [&](const float* w) {
+        if (w) {
             RowLoader<float, 8>::load(w + turn.a_off, wa);
             RowLoader<float, 8>::load(w + turn.b_off, wb);
         }
-        for (int h0 = grp; h0 < heads; h0 += kRows * GROUPS) {
-            if (kKind != 0 || h0 != grp) load(src, h0, heads);
+    };
+    load_weights(p.q_weight);
+    T* q_out = static_cast<T*>(p.query_out) + (size_t)t * Hq * D;
+    for (int h0 = grp; h0 < Hq; h0 += kRows * GROUPS) {
+        if (h0 != grp) load_queries(h0);
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int h = h0 + i * GROUPS;
-                if (h >= heads) break;
-                if (kKind == 2 && !kCodes) {
-                    T* y = static_cast<T*>(dst) + h * step;
-                    xa[i].store(y + turn.a_off);
-                    xb[i].store(y + turn.b_off);
-                    continue;
-                }
-                float a[8], b[8];
+        for (int i = 0; i < kRows; ++i) {
+            const int h = h0 + i * GROUPS;
+            if (h >= Hq) break;
+            float a[8], b[8];
+            xa[i].widen(a);
+            xb[i].widen(b);
+            if (p.q_weight) turn.norm(a, b, wa, wb, p.eps);
+            turn.rotate(a, b);
+            xa[i].round_from(a);
+            xb[i].round_from(b);
+            xa[i].store(q_out + h * D + turn.a_off);
+            xb[i].store(q_out + h * D + turn.b_off);
+        }
+    }
+    if (row0 < 0) return;
+    load_weights(p.k_weight);
+    const size_t cell0 = (size_t)row0 * D, step = (size_t)B * D;           // elements of the caches
+    for (int h0 = grp; h0 < 2 * Hkv; h0 += kRows * GROUPS) {
+        load_keys_values(h0);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int h = h0 + i * GROUPS;
+            if (h >= 2 * Hkv) break;
+            const bool is_v = h >= Hkv;
+            const size_t dst = cell0 + (is_v ? h - Hkv : h) * step;
+            void* cache = is_v ? p.v_cache : p.k_cache;
+            float a[8], b[8];
+            if (kE4M3 || !is_v) {
                 xa[i].widen(a);
                 xb[i].widen(b);
-                if (kKind != 2) {
-                    if (w) turn.norm(a, b, wa, wb, p.eps);
-                    turn.rotate(a, b);
-                }
-                if constexpr (kCodes) {
-                    uint8_t* y = static_cast<uint8_t*>(dst) + h * step;
-                    store8_e4m3(y + turn.a_off, a, scale, inv);
-                    store8_e4m3(y + turn.b_off, b, scale, inv);
-                } else {
-                    T* y = static_cast<T*>(dst) + h * step;
+            }
+            if (!is_v) {
+                if (p.k_weight) turn.norm(a, b, wa, wb, p.eps);
+                turn.rotate(a, b);
+            }
+            if constexpr (kE4M3) {
+                uint8_t* y = static_cast<uint8_t*>(cache) + dst;
+                const float scale = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv : p.k_inv;
+                store8_e4m3(y + turn.a_off, a, scale, inv);
+                store8_e4m3(y + turn.b_off, b, scale, inv);
+            } else {
+                if (!is_v) {
                     xa[i].round_from(a);
                     xb[i].round_from(b);
-                    xa[i].store(y + turn.a_off);
-                    xb[i].store(y + turn.b_off);
                 }
+                T* y = static_cast<T*>(cache) + dst;
+                xa[i].store(y + turn.a_off);
+                xb[i].store(y + turn.b_off);
             }
         }
-    };
-    rows(std::integral_constant<int, 0>{}, query,
-         static_cast<T*>(p.query_out) + (size_t)t * Hq * D, Hq, D, p.q_weight, 1.f, 1.f);
-    if (row0 < 0) return;
-    constexpr int kCell = kE4M3 ? 1 : (int)sizeof(T);
-    const size_t step = (size_t)B * D;
-    rows(std::integral_constant<int, 1>{}, static_cast<const T*>(p.key) + t * p.key_stride,
-         static_cast<uint8_t*>(p.k_cache) + (size_t)row0 * D * kCell, Hkv, step, p.k_weight, p.k_scale,
-         p.k_inv);
-    rows(std::integral_constant<int, 2>{}, static_cast<const T*>(p.value) + t * p.value_stride,
-         static_cast<uint8_t*>(p.v_cache) + (size_t)row0 * D * kCell, Hkv, step, nullptr, p.v_scale,
-         p.v_inv);
+    }
 }
 
 template <typename T, bool kE4M3, int D>

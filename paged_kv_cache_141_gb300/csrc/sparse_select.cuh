@@ -642,45 +642,50 @@ __device__ __forceinline__ void score_candidates(const SelectParams& p, SelShare
         };
         int tile = rank * (NT / 32) + warp;
         if constexpr (kOneTile) {
-            // the next quarter's loads are in flight while one is multiplied
+            // Two quarters' loads are always in flight: a buffer is refilled as
+            // soon as it is multiplied. Block ids come two tiles ahead.
             Quarter buf[2];
-            int blk[2], nblk[2];                            // this tile's blocks, the next one's
-            const T *x = nullptr, *y = nullptr;
             auto after = [&](int t) { return t + stride < tiles ? t + stride : t; };
+            int blk[2], next_blk[2];                           // this tile's blocks, the next one's
             if (tile < tiles) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    blk[r] = rw.ahead[r];                  // (past nc: any block, its score unused)
-                    nblk[r] = block_of(after(tile), r);
+                    blk[r] = rw.ahead[r];                      // (past nc: any block, its score unused)
+                    next_blk[r] = block_of(after(tile), r);
                 }
-                x = row_of(blk[0]);
-                y = row_of(blk[1]);
+                const T *x = row_of(blk[0]), *y = row_of(blk[1]);
                 buf[0].load(x, y);
+                if (NQ > 1) buf[1].load(x + 128, y + 128);
+                else buf[1].load(row_of(next_blk[0]), row_of(next_blk[1]));
             }
-            for (; tile < tiles; tile += stride) {
-                const int next = after(tile);
-                const int fblk[2] = {block_of(after(next), 0), block_of(after(next), 1)};
+            // one tile from buffers b0 (and b1), which it refills
+            auto step = [&](Quarter& b0, Quarter& b1) {
+                const int next = after(tile), far = after(next);
+                const int far_blk[2] = {block_of(far, 0), block_of(far, 1)};
+                const T *x = row_of(blk[0]), *y = row_of(blk[1]);
                 float c[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    if (q + 1 < NQ) {
-                        buf[(q + 1) & 1].load(x + 128 * (q + 1), y + 128 * (q + 1));
-                    } else {
-                        x = row_of(nblk[0]);
-                        y = row_of(nblk[1]);
-                        if (next != tile) buf[(q + 1) & 1].load(x, y);
-                    }
-                    add_quarter<T>(buf[q & 1], sides + 128 * q + lane, c, m);
+                    Quarter& b = q & 1 ? b1 : b0;
+                    add_quarter<T>(b, sides + 128 * q + lane, c, m);
+                    if (q + 2 < NQ) b.load(x + 128 * (q + 2), y + 128 * (q + 2));
+                    else if (NQ > 1 && next != tile)
+                        b.load(row_of(next_blk[0]) + 128 * (q + 2 - NQ), row_of(next_blk[1]) + 128 * (q + 2 - NQ));
+                    else if (NQ == 1 && far != next) b.load(row_of(far_blk[0]), row_of(far_blk[1]));
                 }
-                if (NQ == 1) buf[0] = buf[1];
                 float best[2] = {-INFINITY, -INFINITY}, mag[2] = {0.f, 0.f};
                 over_heads(0, c, m, best, mag);
                 finish(tile, blk, best, mag);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    blk[r] = nblk[r];
-                    nblk[r] = fblk[r];
+                    blk[r] = next_blk[r];
+                    next_blk[r] = far_blk[r];
                 }
+                tile += stride;
+            };
+            while (tile < tiles) {
+                step(buf[0], buf[1]);
+                if (NQ == 1 && tile < tiles) step(buf[1], buf[0]);
             }
         } else {
             for (; tile < tiles; tile += stride) {

@@ -171,6 +171,7 @@ struct RopeParams {
     float eps;
     float k_scale;
     float v_scale;
+    int group_shift;              // set by the launcher: log2 of a token's row groups
     float k_inv;                  // 1 / scale, or 0 where that is no normal number
     float v_inv;
     uint32_t freq_axes[8];        // two bits per frequency

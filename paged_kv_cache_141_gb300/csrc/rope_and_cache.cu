@@ -27,10 +27,10 @@ namespace pagedkv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-// The prompt kernel from four token-warps per SM on (152 SMs): one prompt of 400
-// tokens takes 4.8 us with a row per 8 lanes and 6.2 with a token per warp (32/8
-// heads, bf16), 1000 tokens 8.3 and 6.2, 1373 tokens 13.1 and 9.0.
-constexpr int64_t kPromptTokens = 152 * 4;
+constexpr int kSms = 152;
+// Warps that an SM holds of each kernel: of the one with a row per lane group,
+// and of the one that walks a token's rows, which keeps more in registers.
+constexpr int64_t kRowWarps = 24, kTokenWarps = 16;
 
 // Eight consecutive elements of type T as 16-byte words.
 template <typename T>
@@ -282,27 +282,26 @@ rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     }
 }
 
-// Prompts: one warp per token, so that its angles and the weights are loaded
-// once for all its heads (several warps per token, each loading them, measured
-// slower at every length: 8000 tokens 38.7, 38.7, 44.8 and 66.3 us with 1, 2, 4
-// and 8). The warp's 512 / D row groups take alternate heads, kRows of them with
-// all loads issued before the first is used (keys and values together); the
-// first ones of the queries are on their way while the token's position becomes
-// angles.
+// Prompts: a token has 2^group_shift row groups of D / 16 lanes. They take its
+// heads in turn, kRows of them with all loads issued before the first is used
+// (keys and values together); the first ones of the queries are on their way
+// while the token's position becomes angles, which with the weights are loaded
+// once for all the rows that a group takes.
 template <typename T, bool kE4M3, int D, int kRows>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     begin_overlapped();
     constexpr int LANES = D / 16;
     const int lane = threadIdx.x & 31;
-    constexpr int GROUPS = 32 / LANES;
-    const int grp = lane / LANES;
-    const int64_t t = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+    const int groups = 1 << p.group_shift;
+    const int64_t g = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) / LANES;
+    const int64_t t = g >> p.group_shift;
+    const int grp = (int)g & (groups - 1);
     if (t >= p.total_tokens) return;
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, B = p.block_size;
     Turn<T, D> turn(p, lane);
     Chunk<T> xa[kRows], xb[kRows];
-    // rows h0, h0 + GROUPS, ... of the token: of its queries, or of its keys (the
+    // rows h0, h0 + groups, ... of the token: of its queries, or of its keys (the
     // first Hkv) and values
     const T* query = static_cast<const T*>(p.query) + t * p.query_stride;
     const T* key = static_cast<const T*>(p.key) + t * p.key_stride;
@@ -310,7 +309,7 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     auto load_queries = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int h = h0 + i * GROUPS;
+            const int h = h0 + i * groups;
             if (h < Hq) {
                 xa[i].load(query + h * D + turn.a_off);
                 xb[i].load(query + h * D + turn.b_off);
@@ -320,7 +319,7 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     auto load_keys_values = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int h = h0 + i * GROUPS;
+            const int h = h0 + i * groups;
             if (h < 2 * Hkv) {
                 const T* src = h < Hkv ? key + h * D : value + (h - Hkv) * D;
                 xa[i].load(src + turn.a_off);
@@ -332,7 +331,7 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     const int64_t slot = p.slots[t];
     const bool ok = turn.load(p, t, lane);
     const int64_t row0 = cache_row(p, slot);
-    if (lane == 0) flag_token(p, ok, slot, row0);
+    if (grp == 0 && (lane & (LANES - 1)) == 0) flag_token(p, ok, slot, row0);
     if (!ok) return;
 
     float wa[8], wb[8];
@@ -344,11 +343,11 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     };
     load_weights(p.q_weight);
     T* q_out = static_cast<T*>(p.query_out) + (size_t)t * Hq * D;
-    for (int h0 = grp; h0 < Hq; h0 += kRows * GROUPS) {
+    for (int h0 = grp; h0 < Hq; h0 += kRows * groups) {
         if (h0 != grp) load_queries(h0);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int h = h0 + i * GROUPS;
+            const int h = h0 + i * groups;
             if (h >= Hq) break;
             float a[8], b[8];
             xa[i].widen(a);
@@ -364,11 +363,11 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     if (row0 < 0) return;
     load_weights(p.k_weight);
     const size_t cell0 = (size_t)row0 * D, step = (size_t)B * D;           // elements of the caches
-    for (int h0 = grp; h0 < 2 * Hkv; h0 += kRows * GROUPS) {
+    for (int h0 = grp; h0 < 2 * Hkv; h0 += kRows * groups) {
         load_keys_values(h0);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int h = h0 + i * GROUPS;
+            const int h = h0 + i * groups;
             if (h >= 2 * Hkv) break;
             const bool is_v = h >= Hkv;
             const size_t dst = cell0 + (is_v ? h - Hkv : h) * step;
@@ -400,19 +399,49 @@ rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {
     }
 }
 
+// The row groups of a token that make the call shortest: its time goes as the
+// waves of warps on the device times the batches of kRows rows that each warp
+// walks through, so few tokens want many groups and many tokens the count that
+// divides both evenly; of equals the fewest, which load the angles least often.
+// Measured with 1, 2, 4 and 8 groups (bf16, 32/8 heads of 128 with norms): 700
+// tokens 19.5, 11.0, 6.9, 4.6 us, 3000 tokens 26.6, 18.5, 19.0 us, 32032 tokens
+// 134, 129, 133 us; with 8/1 heads 32032 tokens take 31, 36 and 50 us.
+inline int row_group_shift(const RopeParams& p, int lanes, int rows) {
+    int best_shift = 0;
+    int64_t best = INT64_MAX;
+    for (int shift = 0; shift <= 5; ++shift) {
+        const int64_t warps = ((p.total_tokens << shift) * lanes + 31) / 32;
+        const int64_t waves = (warps + kSms * kTokenWarps - 1) / (kSms * kTokenWarps);
+        const int64_t taken = (int64_t)rows << shift;
+        const int64_t batches = (p.num_q_heads + taken - 1) / taken + (2 * (int64_t)p.num_kv_heads + taken - 1) / taken;
+        if (waves * batches < best) {
+            best = waves * batches;
+            best_shift = shift;
+        }
+    }
+    return best_shift;
+}
+
 template <typename T, bool kE4M3, int D>
 cudaError_t launch_head_size(const RopeParams& p, cudaStream_t stream) {
     const int64_t H = p.num_q_heads + 2 * (int64_t)p.num_kv_heads;
     constexpr int LANES = D / 16;
-    if (p.total_tokens > kPromptTokens) {
-        constexpr int kRows = sizeof(T) == 4 ? 2 : 4;
-        const int64_t grid = (p.total_tokens * 32 + kRopeThreads - 1) / kRopeThreads;
-        if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-        return launch_overlapped(rope_and_cache_prompt_kernel<T, kE4M3, D, kRows>, p, dim3((unsigned)grid),
-                                 kRopeThreads, 0, stream);
+    // A row per lane group while all of them are resident at once: 300 tokens of
+    // 48 rows of 128 with norms take 3.6 us so and 3.9 in row groups, 600 tokens
+    // 5.9 and 4.5 (MHA without norms: 128 tokens of 96 rows 3.2 and 3.2, 300 5.0
+    // and 3.9).
+    if (p.total_tokens * H * LANES <= kSms * kRowWarps * 32) {
+        const int64_t grid = (p.total_tokens * H * LANES + kRopeThreads - 1) / kRopeThreads;
+        return launch_overlapped(rope_and_cache_kernel<T, kE4M3, D>, p, dim3((unsigned)grid), kRopeThreads, 0,
+                                 stream);
     }
-    const int64_t grid = (p.total_tokens * H * LANES + kRopeThreads - 1) / kRopeThreads;
-    return launch_overlapped(rope_and_cache_kernel<T, kE4M3, D>, p, dim3((unsigned)grid), kRopeThreads, 0, stream);
+    constexpr int kRows = sizeof(T) == 4 ? 2 : 4;
+    RopeParams q = p;
+    q.group_shift = row_group_shift(p, LANES, kRows);
+    const int64_t grid = ((p.total_tokens << q.group_shift) * LANES + kRopeThreads - 1) / kRopeThreads;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(rope_and_cache_prompt_kernel<T, kE4M3, D, kRows>, q, dim3((unsigned)grid),
+                             kRopeThreads, 0, stream);
 }
 
 template <typename T, bool kE4M3>

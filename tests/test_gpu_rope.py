@@ -124,6 +124,15 @@ def test_heads_and_tokens(T, Hq, Hkv):
     s.check()
 
 
+@pytest.mark.parametrize("T,Hq,Hkv", [(130, 64, 64), (305, 32, 8), (601, 32, 8), (1401, 32, 8), (3001, 16, 4),
+                                      (9001, 7, 1)])
+@pytest.mark.parametrize("D,dtype,e4m3", [(64, "bf16", False), (128, "f16", True), (256, "f32", False)])
+def test_tokens_of_one_to_many_row_groups(T, Hq, Hkv, D, dtype, e4m3):
+    s = Step(T, Hq, Hkv, D, dtype=dtype, e4m3=e4m3, norm=True, seed=T + D)
+    assert s.run() == 0
+    s.check()
+
+
 @pytest.mark.parametrize("dtype,e4m3", [("f32", False), ("f16", False), ("bf16", False), ("f32", True), ("f16", True),
                                         ("bf16", True)])
 @pytest.mark.parametrize("D,R", [(64, 64), (64, 16), (128, 128), (128, 96), (256, 256), (256, 64)])

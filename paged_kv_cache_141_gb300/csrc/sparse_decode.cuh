@@ -447,10 +447,33 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     cluster.sync();                                 // no CTA leaves while its memory is read
 }
 
+// CTAs per row: as many as find room, for contexts long enough to score together
+// or where a single CTA's warps would each attend to more than three tiles of 16
+// tokens; what a cluster costs is about 3 us. Up to 152 CTAs have an SM each; 256
+// of clusters of 8 share them in pairs. Measured with 1, 2, 4 and 8 CTAs (bf16,
+// head size 128, block size 16): 8 rows of 8192 blocks 69, 44, 31, 25 us (the
+// selection alone); 8 rows of 170 blocks with 117 selected 26, 22, 19, 17, with
+// 64 selected 19, 18, 17, 17, with 32 selected 15, 17, 17, 17; 32 rows of 500
+// blocks with 64 selected 22, 21, 19, 17; 64 rows of it 25, 23, 22, 34; 104 rows
+// 26, 28, 40, 50.
+template <int D>
+int decode_cluster(int rows, int max_ctx_blocks, int num_select, int block_size) {
+    constexpr int kWarps = D < 256 ? 16 : 8;
+    const int64_t tiles = (int64_t)(num_select < max_ctx_blocks ? num_select : max_ctx_blocks) * (block_size / 16);
+    if (max_ctx_blocks < 512 && tiles <= 3 * kWarps) return 1;
+    constexpr int kMost[] = {76, 38, D < 256 ? 32 : 14};       // rows for 2, 4 and 8
+    int C = 1;
+    for (int most : kMost) {
+        if (rows > most) break;
+        C *= 2;
+    }
+    return C;
+}
+
 template <typename QT, typename CT, int D>
 cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
     const int rows = sp.sel.num_seqs * sp.sel.num_kv_heads;
-    int C = select_cluster(rows, sp.sel.max_ctx_blocks);
+    const int C = decode_cluster<D>(rows, sp.sel.max_ctx_blocks, sp.sel.num_select, sp.sel.block_size);
     // An SM for every CTA: 16 warps each, else two CTAs of 8 an SM (head size
     // 256: a tile's fragments take the registers of one CTA of 8 warps). Not
     // every GPC has 16 SMs for two clusters of 8 that fill theirs: of 16 clusters
@@ -458,7 +481,6 @@ cudaError_t launch_sparse(SparseParams sp, cudaStream_t stream) {
     // warps; head size 256 in clusters of 8 and 4: 53 and 41 us).
     const bool placed = rows * C <= (C == kMaxCluster ? 112 : 152);
     const bool wide = D < 256 && placed;
-    if (D == 256 && !placed && C > 1) C /= 2;
     const int select = select_smem<QT, D>(sp.sel);
     const int join = (wide ? 16 : 8) * 8 * (D + 4) * (int)sizeof(float);
     sp.list_bytes = (sp.sel.table_width * 4 + 15) / 16 * 16;

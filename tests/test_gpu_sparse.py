@@ -241,6 +241,18 @@ def test_every_group_size(group):
     p.check(out, sel, 20)
 
 
+@pytest.mark.parametrize("lens,K", [([1500, 30, 900, 0], 70), ([64 * 16 + 3], 60), ([49 * 16, 1, 48 * 16], 100),
+                                    ([300] * 20 + [2000], 90), ([900] * 37, 50)])
+@pytest.mark.parametrize("D,e4m3", [(128, False), (64, True), (256, False)])
+def test_short_contexts_shared_by_a_cluster(lens, K, D, e4m3):
+    # few blocks to score, many to attend to: some CTAs of a cluster have neither
+    p = Pool(lens, 8, 2, D, e4m3=e4m3, seed=K)
+    p.fill_bounds()
+    out, sel = p.decode(K, 1, 2)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, K, 1, 2)
+
+
 def test_close_scores_in_a_crowd():
     # many blocks whose scores differ by less than the approximate scores' error, ties among them
     p = Pool([16 * 700], Hq=4, Hkv=1, D=128, seed=5)

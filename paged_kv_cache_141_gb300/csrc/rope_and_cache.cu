@@ -222,7 +222,8 @@ __device__ __forceinline__ void flag_token(const RopeParams& p, bool ok, int64_t
 }
 
 // Decode steps: one head row per D / 16 lanes and nothing more, so that all of
-// a step's latencies overlap.
+// a step's latencies overlap. Measured: 1 token 2.6 us, 256 tokens of 32/8 heads
+// of 128 3.2 us (in a graph): launch and four loads that depend on each other.
 template <typename T, bool kE4M3, int D>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
@@ -286,7 +287,10 @@ rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
 // heads in turn, kRows of them with all loads issued before the first is used
 // (keys and values together); the first ones of the queries are on their way
 // while the token's position becomes angles, which with the weights are loaded
-// once for all the rows that a group takes.
+// once for all the rows that a group takes. Measured: 16 x 512 tokens of 32/32
+// heads of 128, fp16, 63 us, 6.4 TB/s: bound by memory. 32 x 1001 tokens of 32/8
+// heads with norms, bf16, 129 us, 6.2 TB/s: 16 warps per SM (two CTAs of up to 128
+// registers a thread) just do not cover the latency.
 template <typename T, bool kE4M3, int D, int kRows>
 __global__ void __launch_bounds__(kRopeThreads, 2)
 rope_and_cache_prompt_kernel(const __grid_constant__ RopeParams p) {

@@ -25,6 +25,14 @@
 // them scaled by a power of two to at most 2 in magnitude, exact but for
 // components more than 2^14 below the head's largest. Partial results are joined in
 // shared memory across the warps, and through the cluster's across CTAs.
+//
+// Measured (32/8 heads of 128, block size 16): 64 bf16 contexts of 8k to 32k
+// tokens with 64 blocks selected 114 us, 5.3 TB/s of bounds, keys and values,
+// where bare gathers of such chunks reach 5.2 (512 bytes) to 5.9 (4 KB) TB/s: bound
+// by them. One context of 131072 with 128 selected 27 us: bound by the latencies
+// of score, select, attend and the cluster's barriers in a row. E4M3 (64/8 heads,
+// 128 contexts of 100 to 8k, 96 selected) 117 to 122 us, 4.6 TB/s: bound by issue
+// (widening the codes) and the selection.
 #pragma once
 
 #include "sparse_select.cuh"

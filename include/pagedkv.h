@@ -113,7 +113,12 @@ typedef enum pa_dtype {
                                    (the token is skipped) */
 
 /* Supported shapes: head_size in {64, 128, 256}; block_size in [1, 1024];
- * partition_size a positive multiple of 32 (512 on the pages). */
+ * partition_size a positive multiple of 32 (512 on the pages).
+ *
+ * A NaN key or value is stored in an E4M3 cache as a NaN code (0x7f, 0xff).
+ * pa_sparse_decode and the kernels on the CUDA cores read it as NaN; the
+ * tensor-core kernels of the whole-context decode and of the multi-query
+ * attention may read it as +-480 (their widening is integer arithmetic). */
 
 /*
  * pa_reshape_and_cache -- the KV write (TGI deep-dive sec. 4.1, the write
@@ -561,7 +566,8 @@ pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* bloc
  * recent_blocks of largest score, ties to the lowest index. The order is that
  * of the exact scores (held in binary64 at least), so it does not depend on how
  * the work is split; a NaN score counts as +infinity. The output is
- * softmax(scale * q K^T) V over the selected blocks' tokens below L.
+ * softmax(scale * q K^T) V over the selected blocks' tokens below L; a NaN among
+ * those (a NaN code of an E4M3 cache too) shows in it.
  *
  *  k_bounds       [num_blocks][num_kv_heads][2][head_size], of the query's type;
  *                 read only for blocks that are scored (never for the newest

@@ -1009,26 +1009,33 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
     }
     const cudaError_t e = launch_select_blocks(sp, head_size, q_dtype, cs);
     if (e != cudaSuccess) return PA_ERR_CUDA;
+    // the paged decode of one-head sequences over slabs; E4M3's NaN codes stay NaN
     const size_t seq_bytes = (size_t)num_q_heads * head_size * elem_bytes(q_dtype);
     for (int s0 = 0; s0 < num_seqs; s0 += l.chunk_seqs) {
         const int rows = (num_seqs - s0 < l.chunk_seqs ? num_seqs - s0 : l.chunk_seqs) * num_kv_heads;
         const size_t row0 = (size_t)s0 * num_kv_heads;
-        const void* q = static_cast<const uint8_t*>(query) + s0 * seq_bytes;
         void* o = static_cast<uint8_t*>(out) + s0 * seq_bytes;
-        const int32_t* tables = sp.slab_tables + row0 * l.table_width;
-        if (l.split)
-            st = pa_decode_partitioned(o, q, k_cache, v_cache, tables, l.table_width,
-                                       sp.slab_lens + row0, rows, p.group, 1, head_size, block_size,
-                                       num_blocks * num_kv_heads, l.max_tokens, scale, q_dtype,
-                                       cache_dtype, k_scale, v_scale, l.partition_size,
-                                       w + l.partials, workspace_bytes - l.partials, dev_status,
-                                       stream);
-        else
-            st = pa_decode(o, q, k_cache, v_cache, tables, l.table_width, sp.slab_lens + row0, rows,
-                           p.group, 1, head_size, block_size, num_blocks * num_kv_heads,
-                           l.max_tokens, scale, q_dtype, cache_dtype, k_scale, v_scale, dev_status,
-                           stream);
+        const int32_t* lens = sp.slab_lens + row0;
+        DecodeParams d;
+        st = check_decode(static_cast<const uint8_t*>(query) + s0 * seq_bytes, k_cache, v_cache,
+                          sp.slab_tables + row0 * l.table_width, l.table_width, lens, rows, p.group,
+                          1, head_size, block_size, num_blocks * num_kv_heads, l.max_tokens, scale,
+                          q_dtype, cache_dtype, k_scale, v_scale, dev_status, d);
         if (st != PA_OK) return st;
+        d.nan_codes = true;
+        d.out = o;
+        if (l.split &&
+            (st = bind_workspace(d, rows, p.group, head_size, l.max_tokens, l.partition_size,
+                                 w + l.partials, workspace_bytes - l.partials)) != PA_OK)
+            return st;
+        if (run_decode_kernel(d, head_size, q_dtype, cache_dtype, l.split, cs) != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (l.split &&
+            (st = merge_checked(o, d.tmp_out, d.max_logits, d.exp_sums, lens, rows, p.group,
+                                head_size, l.partition_size, d.max_parts,
+                                decode_len_cap(l.max_tokens, l.table_width, block_size), q_dtype,
+                                dev_status, stream)) != PA_OK)
+            return st;
     }
     return PA_OK;
 }

@@ -17,7 +17,8 @@
 //     (E4M3 caches: binary16 weights as one term, 11 bits, far below the
 //     codes' own error).
 // E4M3 caches are widened to binary16 in registers by integer operations
-// (e4m3x2_to_f16x2_scaled) and multiplied on binary16 MMAs. (Warp-level MMAs
+// (e4m3x2_to_f16x2_scaled; for the block-sparse decode by conversions, which
+// keep NaN) and multiplied on binary16 MMAs. (Warp-level MMAs
 // with E4M3 operands were measured to cost as many instructions as this
 // widening on this GPU, with the query and weights cut to two E4M3 terms.)
 // Heads beyond the group (up to the MMA's 8 columns) carry zero queries and
@@ -134,11 +135,21 @@ template <> struct MathType<e4m3_t> { using T = __half; };
 // exponent field (bias 7) and 3 mantissa bits moved up 7 places are a binary16
 // exponent (bias 15) and mantissa of the value times 2^-8 (a subnormal code
 // gives the binary16 subnormal of that value), and the sign, moved to bit 14,
-// is carried into bit 15 by adding it to itself. The saturating write never
-// stores the NaN codes 0x7f / 0xff.
+// is carried into bit 15 by adding it to itself. The NaN codes 0x7f / 0xff,
+// which the write stores for a NaN, are read as +-480.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_scaled(uint32_t t) {
     const uint32_t x = t << 7;
     return x + (x & 0x40004000u);
+}
+
+// Two E4M3 codes, in bytes 0 and 1 of w, to the binary16 pair of their values,
+// NaN codes to NaN, by the conversion instruction. (The decode of whole contexts
+// takes the integer operations above: with conversions 64 contexts of 4096
+// tokens took 126 us for 124 with 32/8 heads of 128, 32 of 32/32 heads 228 for
+// 218. The block-sparse decode keeps NaN.)
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
 // CTAs per SM the registers must allow: 4 at head size <= 128 (shared memory
@@ -159,8 +170,9 @@ constexpr int mma_threads() {
 // (2 t4 and 2 t4 + 1), and the work on one 32-token stage of K and V.
 // kOneTermP: the weights as one 16-bit term (E4M3 values, widened in
 // registers or staged as binary16 tiles); otherwise high part + residual.
+// kNan: E4M3's NaN codes are read as NaN.
 template <typename QT, typename CT, int D, int GS,
-          bool kOneTermP = std::is_same<CT, e4m3_t>::value>
+          bool kOneTermP = std::is_same<CT, e4m3_t>::value, bool kNan = false>
 struct MmaWarp {
     using S = TmaShape<CT, D>;
     using MT = typename MathType<CT>::T;
@@ -196,8 +208,8 @@ struct MmaWarp {
                 qb[ks][1] = *reinterpret_cast<const uint32_t*>(qp + g * D + 16 * ks + 2 * t4 + 8);
             }
         }
-        // the widened E4M3 codes are their values times 2^-8
-        qk_mul = kFp8 ? q_mul * 256.f : q_mul;
+        // the widened E4M3 codes are their values times 2^-8 (the converted ones their values)
+        qk_mul = kFp8 && !kNan ? q_mul * 256.f : q_mul;
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -256,11 +268,19 @@ struct MmaWarp {
                     ldmatrix_x4(x, rbase + (c >> 3) * S::kSpanTileBytes + (((c & 7) ^ (row & 7)) << 4));
 #pragma unroll
                     for (int h2 = 0; h2 < 2; ++h2) {
-                        const uint32_t a[4] = {
-                            e4m3x2_to_f16x2_scaled(__byte_perm(x[2 * h2], 0u, 0x4140)),
-                            e4m3x2_to_f16x2_scaled(__byte_perm(x[2 * h2 + 1], 0u, 0x4140)),
-                            e4m3x2_to_f16x2_scaled(__byte_perm(x[2 * h2], 0u, 0x4342)),
-                            e4m3x2_to_f16x2_scaled(__byte_perm(x[2 * h2 + 1], 0u, 0x4342))};
+                        const uint32_t x0 = x[2 * h2], x1 = x[2 * h2 + 1];
+                        uint32_t a[4];
+                        if constexpr (kNan) {
+                            a[0] = e4m3x2_to_f16x2(x0);
+                            a[1] = e4m3x2_to_f16x2(x1);
+                            a[2] = e4m3x2_to_f16x2(x0 >> 16);
+                            a[3] = e4m3x2_to_f16x2(x1 >> 16);
+                        } else {
+                            a[0] = e4m3x2_to_f16x2_scaled(__byte_perm(x0, 0u, 0x4140));
+                            a[1] = e4m3x2_to_f16x2_scaled(__byte_perm(x1, 0u, 0x4140));
+                            a[2] = e4m3x2_to_f16x2_scaled(__byte_perm(x0, 0u, 0x4342));
+                            a[3] = e4m3x2_to_f16x2_scaled(__byte_perm(x1, 0u, 0x4342));
+                        }
                         Ops::mma(sc[mt], a, qb[2 * kp + h2][0], qb[2 * kp + h2][1]);
                     }
                 }
@@ -356,10 +376,19 @@ struct MmaWarp {
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt) {
                     const uint32_t lo = y[2 * kt], hi = y[2 * kt + 1];
-                    const uint32_t a[4] = {e4m3x2_to_f16x2_scaled(__byte_perm(lo, 0u, 0x4240)),
-                                           e4m3x2_to_f16x2_scaled(__byte_perm(lo, 0u, 0x4341)),
-                                           e4m3x2_to_f16x2_scaled(__byte_perm(hi, 0u, 0x4240)),
-                                           e4m3x2_to_f16x2_scaled(__byte_perm(hi, 0u, 0x4341))};
+                    uint32_t a[4];
+                    if constexpr (kNan) {
+                        const uint32_t l = __byte_perm(lo, 0u, 0x3120), h = __byte_perm(hi, 0u, 0x3120);
+                        a[0] = e4m3x2_to_f16x2(l);
+                        a[1] = e4m3x2_to_f16x2(l >> 16);
+                        a[2] = e4m3x2_to_f16x2(h);
+                        a[3] = e4m3x2_to_f16x2(h >> 16);
+                    } else {
+                        a[0] = e4m3x2_to_f16x2_scaled(__byte_perm(lo, 0u, 0x4240));
+                        a[1] = e4m3x2_to_f16x2_scaled(__byte_perm(lo, 0u, 0x4341));
+                        a[2] = e4m3x2_to_f16x2_scaled(__byte_perm(hi, 0u, 0x4240));
+                        a[3] = e4m3x2_to_f16x2_scaled(__byte_perm(hi, 0u, 0x4341));
+                    }
                     Ops::mma(acc[md], a, bh[kt][0], bh[kt][1]);
                 }
             }
@@ -647,8 +676,9 @@ __device__ __forceinline__ void shared_unit_cta(const TmaDecodeParams& tp, uint8
 
 // kShared: a split launch with shared-prefix units (grid z: units, then
 // sequences); a separate instantiation, so that the plain kernels carry
-// neither the unit path nor the skip test.
-template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false>
+// neither the unit path nor the skip test. kNan: E4M3 caches whose NaN codes
+// are read as NaN.
+template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false, bool kNan = false>
 __global__ void __launch_bounds__(mma_threads<CT, D>(), mma_min_blocks<CT, D>())
 paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
     using S = TmaShape<CT, D>;
@@ -800,7 +830,7 @@ paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
     }
 
     // ---------------------------------------------------------------- consumers
-    MmaWarp<QT, CT, D, GS> cw;
+    MmaWarp<QT, CT, D, GS, kFp8, kNan> cw;
     cw.load_query(reinterpret_cast<const QT*>(p.query) + ((size_t)s * p.num_q_heads + hq0) * D,
                   p.q_mul, lane);
 
@@ -877,7 +907,7 @@ paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
             W = fmaf(f, cl[w * 8 + h], W);
             O = fmaf(f, co[(w * 8 + h) * D + e], O);
         }
-        const float val = __fdiv_rn(O, W) * (kFp8 ? p.v_mul * 256.f : p.v_mul);
+        const float val = __fdiv_rn(O, W) * (kFp8 && !kNan ? p.v_mul * 256.f : p.v_mul);
         const int hq = hq0 + h;
         if constexpr (kSplit) {
             const size_t row = ((size_t)s * p.num_q_heads + hq) * p.max_parts + blockIdx.x;
@@ -893,10 +923,10 @@ paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
     }
 }
 
-template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false>
+template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false, bool kNan = false>
 cudaError_t launch_mma_variant(const TmaDecodeParams& tp, cudaStream_t stream) {
     using Smem = MmaSmem<CT, D>;
-    auto kern = paged_decode_mma_kernel<QT, CT, D, GS, kSplit, kShared>;
+    auto kern = paged_decode_mma_kernel<QT, CT, D, GS, kSplit, kShared, kNan>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kern), Smem::kAlloc);
     if (e != cudaSuccess) return e;
     const DecodeParams& p = tp.p;
@@ -910,6 +940,11 @@ template <typename QT, typename CT, int D>
 cudaError_t launch_mma_d(const TmaDecodeParams& tp, int gs, bool split, cudaStream_t stream) {
 #define PA_MMA_CASE(G)                                                        \
     case G:                                                                   \
+        if constexpr (std::is_same<CT, e4m3_t>::value) {                      \
+            if (tp.p.nan_codes)                                               \
+                return split ? launch_mma_variant<QT, CT, D, G, true, false, true>(tp, stream)   \
+                             : launch_mma_variant<QT, CT, D, G, false, false, true>(tp, stream); \
+        }                                                                     \
         if (split && tp.p.num_units > 0)                                      \
             return launch_mma_variant<QT, CT, D, G, true, true>(tp, stream);  \
         return split ? launch_mma_variant<QT, CT, D, G, true>(tp, stream)     \

@@ -59,6 +59,7 @@ struct DecodeParams {
     const int32_t* unit_seqs;     // [num_units, 4]
     const int32_t* unit_parts;    // [num_units]
     int num_units;
+    bool nan_codes;               // E4M3's NaN codes are read as NaN by the tensor cores too
 };
 
 // Generic CUDA-core decode; one launcher per (query type, cache type).

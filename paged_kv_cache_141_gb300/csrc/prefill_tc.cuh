@@ -306,8 +306,8 @@ __device__ __forceinline__ void fence_async_smem() {
 // binary16 exponent (bias 15) and mantissa of the same value times 2^-8, an
 // E4M3 subnormal becomes the binary16 subnormal of that value, and the sign
 // (moved to bit 14) is carried into bit 15 by adding it to itself. The 2^8 is
-// folded into the score and output scales. (Codes 0x7f/0xff, NaN, are never
-// stored by the saturating write.)
+// folded into the score and output scales. (Codes 0x7f/0xff, which the write
+// stores for a NaN, are read as +-480.)
 __device__ __forceinline__ uint32_t e4m3x2_spread_to_f16x2_scaled(uint32_t t) {
     const uint32_t x = t << 7;
     return x + (x & 0x40004000u);

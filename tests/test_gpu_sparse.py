@@ -445,3 +445,40 @@ def test_wrong_arguments():
     with pytest.raises(pk.PagedKVError):                     # max_new_tokens without new_tokens
         pk.key_bounds(p.bounds, p.kc, p.tables, p.context, 100, max_new_tokens=2)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(8, 2, 128, 16), (32, 2, 128, 16), (8, 2, 128, 8), (4, 4, 256, 16), (16, 1, 256, 16),
+                                        (6, 2, 64, 16), (32, 2, 64, 16), (6, 2, 128, 7)])
+@pytest.mark.parametrize("K,first", [(70, 1), (7, 0)])
+def test_nan_codes_of_an_e4m3_pool_show(dtype, Hq, Hkv, D, B, K, first):
+    """A NaN code in a selected token: a key's makes its head's rows NaN, a value's its component; all else keeps
+    the tolerances. (The codes behind a context's end are NaN throughout.)"""
+    lens = [1, B, 20 * B + 3, 60 * B, 33 * B + 1]
+    G = Hq // Hkv
+    for code in (0x7F, 0xFF):
+        for cache in ("key", "value"):
+            p = Pool(lens, Hq, Hkv, D, B, dtype, True, seed=B + D)
+            bad = [(0, 0, 0, 3), (2, 20 * B + 2, 0, D - 1), (3, 0, Hkv - 1, 17), (4, 33 * B, Hkv - 1, D // 2)]
+            for s, t, h, d in bad:                       # the first and the newest block: selected (a NaN key always is)
+                if first or cache == "key" or t >= p.B * (-(-lens[s] // p.B) - 1):
+                    (p.kc if cache == "key" else p.vc)[p.tables[s, t // B].long(), h, t % B, d] = code
+            p.fill_bounds()
+            out, sel = p.decode(K, first)
+            want = torch.zeros(out.shape, dtype=torch.bool)
+            for s, t, h, d in bad:
+                if (p.kc if cache == "key" else p.vc)[p.tables[s, t // B].long(), h, t % B, d].item() == code:
+                    want[s, h * G:(h + 1) * G, slice(None) if cache == "key" else d] = True
+            assert torch.equal(out.isnan().cpu(), want), (code, cache)
+            for s, L in enumerate(lens):
+                for h in range(Hkv):
+                    blocks = [b for b in sel[s, h].tolist() if b >= 0]
+                    assert blocks == p.want_selected(s, h, K, first, 1)
+                    tok = torch.tensor([b * B + i for b in blocks for i in range(B) if b * B + i < L])
+                    blk = p.tables[s].long()[(tok // B).cuda()]
+                    k, v = (p.keys(c)[blk, h, (tok % B).cuda()] for c in (p.kc, p.vc))
+                    w = torch.softmax(p.query[s, h * G:(h + 1) * G].double() @ k.t() * (p.scale * p.ks), -1)
+                    ref, mass = w @ v * p.vs, w @ v.abs() * p.vs
+                    tol = torch.finfo(p.dt).eps / 2 * ref.abs() + WEIGHTS["e4m3"] * mass
+                    got = out[s, h * G:(h + 1) * G].double()
+                    assert bool((((got - ref).abs() <= tol) | (got.isnan() & ref.isnan())).all())

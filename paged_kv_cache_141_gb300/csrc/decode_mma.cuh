@@ -15,7 +15,7 @@
 //     accumulators with movmatrix. P is split into a 16-bit high part and a
 //     16-bit residual, two MMAs, so the weights keep ~16 significant bits
 //     (E4M3 caches: binary16 weights as one term, 11 bits, far below the
-//     codes' own error).
+//     codes' own error; two for the block-sparse decode).
 // E4M3 caches are widened to binary16 in registers by integer operations
 // (e4m3x2_to_f16x2_scaled; for the block-sparse decode by conversions, which
 // keep NaN) and multiplied on binary16 MMAs. (Warp-level MMAs
@@ -390,6 +390,7 @@ struct MmaWarp {
                         a[3] = e4m3x2_to_f16x2_scaled(__byte_perm(hi, 0u, 0x4341));
                     }
                     Ops::mma(acc[md], a, bh[kt][0], bh[kt][1]);
+                    if constexpr (!kOneTermP) Ops::mma(acc[md], a, bl[kt][0], bl[kt][1]);
                 }
             }
         } else {
@@ -677,7 +678,7 @@ __device__ __forceinline__ void shared_unit_cta(const TmaDecodeParams& tp, uint8
 // kShared: a split launch with shared-prefix units (grid z: units, then
 // sequences); a separate instantiation, so that the plain kernels carry
 // neither the unit path nor the skip test. kNan: E4M3 caches whose NaN codes
-// are read as NaN.
+// are read as NaN, with the weights in two terms.
 template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false, bool kNan = false>
 __global__ void __launch_bounds__(mma_threads<CT, D>(), mma_min_blocks<CT, D>())
 paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
@@ -830,7 +831,7 @@ paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {
     }
 
     // ---------------------------------------------------------------- consumers
-    MmaWarp<QT, CT, D, GS, kFp8, kNan> cw;
+    MmaWarp<QT, CT, D, GS, kFp8 && !kNan, kNan> cw;
     cw.load_query(reinterpret_cast<const QT*>(p.query) + ((size_t)s * p.num_q_heads + hq0) * D,
                   p.q_mul, lane);
 

@@ -18,12 +18,15 @@
 // The next tile's keys are loaded while this tile's softmax and P.V run, its
 // values while the next scores run. The softmax reference moves only when a
 // score passes it by 2^8 (weights up to 256 are as good as those up to 1), so
-// most tiles need no maximum across lanes. Weights are two 16-bit terms (16
-// significant bits; one binary16 term for E4M3 values, 2^-11, inside the codes'
-// own 2^-4), and the sums use exactly the weights that the products use. E4M3 codes
+// most tiles need no maximum across lanes. Weights are sums of 16-bit terms, each
+// with its own MMA: three of bfloat16, all 24 bits, or two of binary16, 22 bits
+// (times 2^7, so that what binary16 cannot hold is below 2^-31 of the reference's
+// weight). The sums use exactly the weights that the products use. Fewer terms
+// would be a little faster on E4M3 caches (one: 120 us for 123 on the batch below)
+// and no faster on 16-bit ones, which the loads bound. E4M3 codes
 // convert to binary16, NaN codes to NaN: a NaN key or value shows in the output
 // (the integer widening of the dense decode, which reads those as +-480, took 117 us
-// for 120 on the E4M3 batch below). A 16-bit query meets them scaled by a power of two to at most 2 in magnitude, exact but for
+// for 120). A 16-bit query meets them scaled by a power of two to at most 2 in magnitude, exact but for
 // components more than 2^14 below the head's largest. Partial results are joined in
 // shared memory across the warps, and through the cluster's across CTAs.
 //
@@ -70,6 +73,9 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     begin_overlapped();
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
     using MT = typename MathType<CT>::T;            // the MMAs' type
+    // weights: bfloat16 terms of 8 bits, or binary16 ones of 11, those times 2^7
+    constexpr bool kThreeTerms = std::is_same<MT, __nv_bfloat16>::value;
+    constexpr float kUp = kThreeTerms ? 0.f : 7.f;
     using Ops = MmaOps<MT>;
     using OutOps = MmaOps<QT>;
     using Tile = Tile16<CT, D>;
@@ -296,24 +302,21 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] *= alpha[j & 1];
         }
-        uint32_t hi[2], lo[2];
+        const float ref[2] = {m_ref[0] - kUp, m_ref[1] - kUp};
+        uint32_t hi[2], lo[2], low[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const float w0 = sc[2 * r] == -INFINITY ? 0.f : fast_exp2(sc[2 * r] - m_ref[0]);
-            const float w1 = sc[2 * r + 1] == -INFINITY ? 0.f : fast_exp2(sc[2 * r + 1] - m_ref[1]);
+            const float w0 = sc[2 * r] == -INFINITY ? 0.f : fast_exp2(sc[2 * r] - ref[0]);
+            const float w1 = sc[2 * r + 1] == -INFINITY ? 0.f : fast_exp2(sc[2 * r + 1] - ref[1]);
             const uint32_t h = Ops::pack(w0, w1);
             const float2 hf = Ops::unpack(h);
-            if constexpr (kFp8) {
-                l_run[0] += hf.x;
-                l_run[1] += hf.y;
-            } else {
-                const uint32_t l = Ops::pack(w0 - hf.x, w1 - hf.y);
-                const float2 lf = Ops::unpack(l);
-                l_run[0] += hf.x + lf.x;
-                l_run[1] += hf.y + lf.y;
-                lo[r] = movmatrix_trans(l);
-            }
+            const uint32_t l = Ops::pack(w0 - hf.x, w1 - hf.y);
+            const float2 lf = Ops::unpack(l);
+            if constexpr (kThreeTerms) low[r] = movmatrix_trans(Ops::pack(w0 - hf.x - lf.x, w1 - hf.y - lf.y));
+            l_run[0] += kThreeTerms ? w0 : hf.x + lf.x;
+            l_run[1] += kThreeTerms ? w1 : hf.y + lf.y;
             hi[r] = movmatrix_trans(h);
+            lo[r] = movmatrix_trans(l);
         }
 
         // ---- O^T += V^T P^T
@@ -327,6 +330,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
                 const uint32_t a[4] = {e4m3x2_to_f16x2(v01), e4m3x2_to_f16x2(v01 >> 16), e4m3x2_to_f16x2(v23),
                                        e4m3x2_to_f16x2(v23 >> 16)};
                 Ops::mma(acc[i], a, hi[0], hi[1]);
+                Ops::mma(acc[i], a, lo[0], lo[1]);
             }
         } else {
 #pragma unroll
@@ -338,6 +342,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
                                        __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632)};
                 Ops::mma(acc[i], a, hi[0], hi[1]);
                 Ops::mma(acc[i], a, lo[0], lo[1]);
+                if constexpr (kThreeTerms) Ops::mma(acc[i], a, low[0], low[1]);
             }
         }
         tile = next;

@@ -482,3 +482,45 @@ def test_nan_codes_of_an_e4m3_pool_show(dtype, Hq, Hkv, D, B, K, first):
                     tol = torch.finfo(p.dt).eps / 2 * ref.abs() + WEIGHTS["e4m3"] * mass
                     got = out[s, h * G:(h + 1) * G].double()
                     assert bool((((got - ref).abs() <= tol) | (got.isnan() & ref.isnan())).all())
+
+
+@pytest.mark.parametrize("dtype,e4m3,Hq", [("bf16", False, 8), ("f16", False, 8), ("bf16", True, 8), ("f16", True, 8),
+                                           ("f16", False, 32), ("bf16", True, 32), ("f16", True, 32)])
+def test_weights_keep_their_bits(dtype, e4m3, Hq):
+    """Values that cancel against the exact weights (64 contexts of one block; each head in a share of the
+    components), so that the output's rounding is negligible and what is left is the weights' error. Tolerance,
+    against sum_i p_i |v_i|: one component of the query is not zero and |scale q k log2 e| <= 2, so a weight errs by
+    ex2.approx's 2^-22 and by the rounding of its argument, below 8 with the reference's shift: 2^-22 ln 2; the
+    products' sum loses up to 17 2^-23 of its largest term, about a sixth of the whole: 2^-21.5. Together 2^-20.2."""
+    S, Hkv, D, B = 64, 2, 128, 16
+    G = Hq // Hkv
+    p = Pool([B] * S, Hq, Hkv, D, B, dtype, e4m3, seed=5)
+    g = torch.Generator().manual_seed(6)
+    cast = (lambda x: (x.clamp(-448, 448)).to(torch.float8_e4m3fn)) if e4m3 else (lambda x: x.to(p.dt))
+    back = lambda x: x.view(torch.uint8) if e4m3 else x
+    p.ks, p.vs, p.scale = (2.0 ** -6, 0.027, 1.0) if e4m3 else (1.0, 1.0, 1.0)
+    k = cast(torch.rand((S, Hkv, B), generator=g) * (1.38 / p.ks))
+    q = (0.7 + 0.3 * torch.rand((S, Hkv, G), generator=g)).to(p.dt)
+    w = torch.softmax((q.double().unsqueeze(-1) * k.double().unsqueeze(2)) * p.ks, -1)          # [S, Hkv, G, B]
+    head = torch.arange(D) * G // D
+    w = w[:, :, head].transpose(2, 3)                                                         # [S, Hkv, B, D]
+    v = torch.zeros((S, Hkv, B, D), dtype=torch.float64)
+    left = torch.zeros((S, Hkv, D), dtype=torch.float64)
+    top = 200.0 if e4m3 else 1.0
+    for t in range(B):
+        new = top * torch.randn((S, Hkv, D), generator=g).double() if t < 4 else -left / w[:, :, t]
+        v[:, :, t] = cast(new.float()).double()
+        left += w[:, :, t] * v[:, :, t]
+    blocks = p.tables[:, 0].long()
+    p.kc.zero_(), p.query.zero_()
+    p.kc[blocks, :, :, 0] = back(k).cuda()
+    p.vc[blocks] = back(cast(v.float())).cuda()
+    p.query.view(S, Hkv, G, D)[..., 0] = q.cuda()
+    p.fill_bounds()
+    out, _ = p.decode(4)
+    got = out.view(S, Hkv, G, D).gather(2, head.view(1, 1, 1, D).expand(S, Hkv, 1, D).cuda()).squeeze(2).double().cpu()
+    mass = (w * v.abs()).sum(2) * p.vs
+    ref = left * p.vs
+    tol = torch.finfo(p.dt).eps / 2 * ref.abs() + 2.0 ** -20 * mass + (2.0 ** -25 if dtype == "f16" else 0.0)
+    assert float((ref.abs() / mass).max()) < 2.0 ** -9
+    assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / mass).max())

@@ -291,9 +291,17 @@ __device__ __forceinline__ K kth_largest(SelShared<NT>& sh, int n, int want, int
 }
 
 // Whether approximate scores with terms of up to mag may be relied on: far above
-// what an underflow could drop, or all zero.
-__device__ __forceinline__ bool reliable(float mag) {
-    return isfinite(mag) && (mag == 0.f || mag >= 0x1p-100f);
+// what an underflow could drop. (A sum of 0 says nothing: all products may have
+// underflowed.)
+__device__ __forceinline__ bool reliable(float mag) { return isfinite(mag) && mag >= 0x1p-100f; }
+
+// Whether all query elements of the row's group are zero (all threads, for all).
+template <typename T, int D, int NT>
+__device__ bool zero_query(const SelectParams& p, int s, int h) {
+    const T* q = static_cast<const T*>(p.query) + ((size_t)s * p.num_q_heads + h * p.group) * D;
+    bool any = false;
+    for (int i = threadIdx.x; i < p.group * D; i += NT) any |= to_float(q[i]) != 0.f;
+    return !__syncthreads_or(any);
 }
 
 // The score that ordered() puts below every value: a block not taken.
@@ -797,7 +805,7 @@ __device__ __forceinline__ void take_by_search(const SelectParams& p, SelShared<
     if (left < open) {
         // ------------------------------------------- exact scores of the unsettled
         // (A zero query, say of a padding row, makes every score 0, exactly.)
-        const bool zeros = mag == 0.f;
+        const bool zeros = mag == 0.f && zero_query<T, D, NT>(p, s, h);
         const bool small = open <= SelShared<NT>::kRankList && !zeros;
         if (threadIdx.x == 0) sh.list_n = 0;
         __syncthreads();

@@ -524,3 +524,22 @@ def test_weights_keep_their_bits(dtype, e4m3, Hq):
     tol = torch.finfo(p.dt).eps / 2 * ref.abs() + 2.0 ** -20 * mass + (2.0 ** -25 if dtype == "f16" else 0.0)
     assert float((ref.abs() / mass).max()) < 2.0 ** -9
     assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / mass).max())
+
+
+@pytest.mark.parametrize("dtype,Hq,B,size", [("bf16", 8, 16, 2.0 ** -96), ("bf16", 8, 16, 2.0 ** -120), ("bf16", 32, 16, 2.0 ** -110),
+                                             ("bf16", 8, 5, 2.0 ** -110), ("f32", 8, 16, 2.0 ** -80), ("f32", 8, 16, 2.0 ** -140),
+                                             ("f32", 32, 16, 2.0 ** -100)])
+def test_products_that_all_underflow(dtype, Hq, B, size):
+    """Query and bounds whose products pass below binary32's range (bfloat16's range too, with 2^40 to spare): the
+    order is that of the exact scores all the same. One sequence each with a zero query, and with zero keys."""
+    p = Pool([B * 120, B * 97 + 1, B * 50], Hq, 2, 128, B, dtype, seed=13)
+    p.fill_bounds()
+    p.bounds.copy_((p.bounds.double().nan_to_num(0) * size).to(p.dt))
+    p.query.copy_((p.query.double() * size).to(p.dt))
+    assert bool((p.query != 0).any()) and bool((p.bounds != 0).any())
+    p.query[1] = 0
+    p.bounds[p.tables[2].long()] = 0
+    sel = p.decode(15, 1, 1)[1]
+    for s in range(3):
+        for h in range(2):
+            assert sel[s, h].tolist() == p.want_selected(s, h, 15, 1, 1), (s, h)

@@ -543,3 +543,67 @@ def test_products_that_all_underflow(dtype, Hq, B, size):
     for s in range(3):
         for h in range(2):
             assert sel[s, h].tolist() == p.want_selected(s, h, 15, 1, 1), (s, h)
+
+
+def spread(shape, g, bits):
+    """Signed magnitudes log-uniform over 2^-bits .. 2^bits."""
+    x = torch.exp2((2 * torch.rand(shape, generator=g, device="cuda") - 1) * bits)
+    return torch.where(torch.rand(shape, generator=g, device="cuda") < 0.5, -x, x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 12), (128, 8), (128, 16), (256, 4), (256, 9)])
+@pytest.mark.parametrize("values", ["normal", "spread", "one sign", "cancelling"])
+def test_approximate_scores_err_less_than_the_selection_takes_them_to(dtype, D, G, values):
+    """A context of more blocks than shared memory keeps scores for leaves its approximate scores at the start of the
+    workspace (bfloat16's times 2^40): each within 2^-16 of the sum of its terms' magnitudes, as the selection
+    assumes (a quarter of it here: the margin)."""
+    n, B, dt = 25000, 1, TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(D + G)
+    query = torch.randn((1, G, D), generator=g, device="cuda")
+    bounds = torch.randn((n, 1, 2, D), generator=g, device="cuda")
+    if values == "spread":
+        query, bounds = spread(query.shape, g, 4), spread(bounds.shape, g, 8)
+    elif values == "one sign":
+        query, bounds = 1 + torch.rand(query.shape, generator=g, device="cuda"), 1 + torch.rand(bounds.shape, generator=g, device="cuda")
+    elif values == "cancelling":                       # the second half of the components takes the first half's sum back
+        query[..., D // 2:] = -query[..., :D // 2]
+        half = torch.randn((n, 1, 1, D // 2), generator=g, device="cuda").to(dt).float()
+        bounds = torch.cat((half, half), -1).expand(n, 1, 2, D).contiguous()
+        bounds[:, :, :, -1] += torch.rand((n, 1, 1), generator=g, device="cuda") * 4    # (so that the best ones are clear)
+    query, bounds = query.to(dt), bounds.to(dt)
+    lo, hi = torch.minimum(bounds[:, :, 0], bounds[:, :, 1]), torch.maximum(bounds[:, :, 0], bounds[:, :, 1])
+    bounds = torch.stack((lo, hi), 2)
+    cache = torch.zeros((n, 1, B, D), device="cuda", dtype=dt)
+    table = torch.arange(n, device="cuda", dtype=torch.int32).view(1, n)
+    context = torch.full((1,), n * B, device="cuda", dtype=torch.int32)
+    ws = pk.alloc_sparse_workspace(1, G, 1, D, B, n * B, 50)
+    out = torch.empty_like(query)
+    pk.sparse_decode(out, query, cache, cache, bounds, table, context, n * B, 1.0, 50, ws, 0, 1)
+    got = ws[:4 * (n - 1)].view(torch.float32).double() * (2.0 ** -40 if dtype == "bf16" else 1.0)
+    q, b = query[0].double(), bounds[:n - 1, 0].double()                       # [G, D], [n, 2, D]
+    neg, pos = q.clamp(max=0), q.clamp(min=0)
+    want = (neg @ b[:, 0].t() + pos @ b[:, 1].t()).amax(0)
+    mag = (neg.abs() @ b[:, 0].abs().t() + pos @ b[:, 1].abs().t()).amax(0)
+    taken = torch.isinf(got) | torch.isnan(got)                                # marked by the search, where that was needed
+    assert int(taken.sum()) < n // 2
+    worst = float(((got - want).abs() / mag)[~taken].max())
+    assert worst <= 2.0 ** -18, worst
+
+
+def test_subnormal_bounds_and_query_elements_count():
+    """bfloat16 bounds, and query elements, below its normal range decide where others are level."""
+    for swap in (False, True):
+        p = Pool([16 * 200], 8, 2, 128, 16, seed=17)
+        p.bounds.zero_()
+        p.query.zero_()
+        tiny = (torch.arange(p.num_blocks, device="cuda") * 37 % 113 + 1).double() * 2.0 ** -133
+        p.query[..., 0], p.query[..., 1] = 2.0 ** 100, 2.0 ** -20
+        p.bounds[:, :, :, 0] = tiny.to(p.dt).view(-1, 1, 1)
+        p.bounds[:, :, :, 1] = 2.0 ** -30
+        if swap:
+            p.query[..., 0] = 2.0 ** -132
+            p.bounds[:, :, :, 0] = (tiny * 2.0 ** 233).to(p.dt).view(-1, 1, 1)
+        sel = p.decode(15, 1, 1)[1]
+        for h in range(2):
+            assert sel[0, h].tolist() == p.want_selected(0, h, 15, 1, 1)

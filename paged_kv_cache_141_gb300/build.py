@@ -1,11 +1,12 @@
 """Build libpagedkv.so in-tree with nvcc for sm_103a (GB300), and with g++ the
-binding's marshalling module _marshal.so.
+binding's marshalling module _marshal.
 
 Each CUDA translation unit compiles in its own nvcc process, in parallel;
 the objects link into one shared library next to this file. The CUDA runtime
 is linked statically, so the library loads without a GPU (the driver is only
-opened by the first CUDA call). _marshal.so is compiled against the installed
-PyTorch's headers (and again when its version changes).
+opened by the first CUDA call). _marshal is compiled against this interpreter's
+and the installed PyTorch's headers, under the interpreter's own suffix (no other
+one imports it), and again when the PyTorch changes.
 
     python -m paged_kv_cache_141_gb300.build [--force] [-v]
 """
@@ -15,6 +16,7 @@ import argparse
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 MARSHAL_SRC = os.path.join(PKG, "pysrc", "marshal.cpp")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -57,11 +59,10 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 def build_marshal(force: bool = False) -> str:
     """The marshalling module, against this interpreter's and PyTorch's headers."""
-    import sysconfig
-
     import torch
     os.makedirs(BUILD, exist_ok=True)
-    stamp, made_for = os.path.join(BUILD, "marshal.torch"), f"{torch.__version__} {sysconfig.get_platform()}"
+    stamp = os.path.join(BUILD, os.path.basename(MARSHAL) + ".for")
+    made_for = f"{sysconfig.get_config_var('SOABI')} {torch.__version__} {os.path.dirname(torch.__file__)}"
     try:
         with open(stamp) as f:
             same = f.read() == made_for
@@ -71,7 +72,7 @@ def build_marshal(force: bool = False) -> str:
         return MARSHAL
     root = os.path.dirname(torch.__file__)
     libs = os.path.join(root, "lib")
-    part = os.path.join(BUILD, "_marshal.so")          # moved into place when whole
+    part = os.path.join(BUILD, f"_marshal.{os.getpid()}.so")    # moved into place when whole
     cmd = ["g++", "-O2", "-shared", "-fPIC", "-std=c++17", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I" + INCLUDE,
            "-isystem", os.path.join(root, "include"), "-I" + sysconfig.get_path("include"), MARSHAL_SRC,
@@ -82,6 +83,9 @@ def build_marshal(force: bool = False) -> str:
     os.replace(part, MARSHAL)
     with open(stamp, "w") as f:
         f.write(made_for)
+    untagged = os.path.join(PKG, "_marshal.so")        # of an earlier build: any interpreter would import it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     return MARSHAL
 
 

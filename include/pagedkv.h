@@ -548,8 +548,12 @@ pa_status pa_paged_prefill(void* out, const void* query, const int32_t* query_st
  *                 skipped). NULL: one each (none where the context is empty), and
  *                 max_new_tokens must be 1. max_new_tokens sizes the grid.
  *  Bounds cover the block's tokens below context_lens[s]; bounds of other blocks
- *  are left as they are. If several sequences' new tokens touch one physical
- *  block, its bounds are those of one of them.
+ *  are left as they are. Name each physical block by one sequence, the longest
+ *  that holds it: where several sequences' new tokens touch a block, every
+ *  element of its bounds is that of one of them, minima and maxima perhaps of
+ *  different ones -- the same for all that see the same tokens of the block, but
+ *  no bound for the others. (The rows that pa_sparse_decode takes for several query
+ *  tokens of a sequence are one sequence here, with the last row's length.)
  */
 pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* block_tables,
                         int max_blocks_per_seq, const int32_t* context_lens,

@@ -520,7 +520,9 @@ def key_bounds(k_bounds, k_cache, block_tables, context_lens, max_context_len, n
                max_new_tokens=1, dev_status=None, stream=None) -> None:
     """Recompute k_bounds [num_blocks, Hkv, 2, d] (minimum, maximum of each
     block's keys) for the blocks that hold the last new_tokens[s] (int32 [S];
-    None: one) positions of each context."""
+    None: one) positions of each context. Name a physical block by one sequence
+    only, the longest that holds it (several query tokens of a sequence, rows of
+    sparse_decode, are one sequence here)."""
     _check((_marshal or _native()).key_bounds(
         k_bounds, k_cache, block_tables, context_lens, max_context_len, new_tokens, max_new_tokens,
         dev_status, stream), "pa_key_bounds")

@@ -607,3 +607,27 @@ def test_subnormal_bounds_and_query_elements_count():
         sel = p.decode(15, 1, 1)[1]
         for h in range(2):
             assert sel[0, h].tolist() == p.want_selected(0, h, 15, 1, 1)
+
+
+@pytest.mark.parametrize("dtype,e4m3", [("bf16", False), ("f32", False), ("f16", True)])
+def test_bounds_of_a_block_that_several_sequences_name(dtype, e4m3):
+    """Sequences that see the same tokens of a block give its bounds; of those that see different ones, every
+    element is that of one of them. The longest alone (rows of one sequence's query tokens) gives the longest's."""
+    p = Pool([16 * 40 + 9], dtype=dtype, e4m3=e4m3, seed=21)
+    L = p.lens[0]
+    newest = p.tables[0, L // 16].long()
+    full = torch.stack([p.want_bounds(0, j) for j in range(L // 16)])
+    ends = []
+    for m in (3, 6, 9):
+        k = p.keys(p.kc[newest])[:, :m]
+        ends.append(torch.stack((k.amin(1), k.amax(1)), 1))
+    lens = [L - 6, L, L - 3, L] * 16
+    rows = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pk.key_bounds(p.bounds, p.kc, p.tables.expand(64, -1).contiguous(), rows, L, rows, L, dev_status=p.status)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0
+    assert torch.equal(p.bounds[p.tables[0, :L // 16].long()].double(), full)
+    got = p.bounds[newest].double()
+    assert bool(torch.stack([got == e for e in ends]).any(0).all())
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, L, dev_status=p.status)
+    assert torch.equal(p.bounds[newest].double(), ends[2])

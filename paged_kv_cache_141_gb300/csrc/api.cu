@@ -899,7 +899,7 @@ pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* bloc
         return PA_ERR_UNSUPPORTED;
     if (max_new_tokens > max_context_len) max_new_tokens = max_context_len;
     const int64_t touched = max_new_tokens == 0 ? 0 : ((int64_t)max_new_tokens + block_size - 2) / block_size + 1;
-    if (touched * num_kv_heads > (1ll << 27)) return PA_ERR_UNSUPPORTED;     // the grid's x
+    if (touched * num_kv_heads > kMaxBoundsUnits) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || touched == 0) return PA_OK;
     if (!k_bounds || !k_cache || !block_tables || !context_lens || max_blocks_per_seq == 0)
         return PA_ERR_INVALID_ARG;

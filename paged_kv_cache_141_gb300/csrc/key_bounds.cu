@@ -204,9 +204,8 @@ key_bounds_f32_kernel(const __grid_constant__ BoundsParams p) {
 
 template <typename CT, typename BT>
 cudaError_t launch_bounds(const BoundsParams& p, int head_size, cudaStream_t stream) {
-    const int64_t units = (int64_t)p.touched * p.num_kv_heads;
+    const int64_t units = (int64_t)p.touched * p.num_kv_heads;         // kMaxBoundsUnits at most
     const int64_t gx = (units * 32 + kBoundsThreads - 1) / kBoundsThreads;
-    if (gx > 0x3ffffff) return cudaErrorInvalidConfiguration;  // thread indices stay below 2^32
     const dim3 grid((unsigned)gx, p.num_seqs < 65535 ? p.num_seqs : 65535);
     auto launch = [&](void (*kernel)(BoundsParams)) {
         return launch_overlapped(kernel, p, grid, kBoundsThreads, 0, stream);

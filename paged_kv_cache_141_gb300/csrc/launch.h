@@ -199,6 +199,9 @@ struct BoundsParams {
     int touched;                  // blocks that max_new_tokens tokens can touch
 };
 
+// A warp each in the grid's x, whose thread indices are 32-bit.
+constexpr int64_t kMaxBoundsUnits = 1ll << 27;    // touched blocks x KV heads
+
 cudaError_t launch_key_bounds(const BoundsParams& p, int head_size, pa_dtype cache_dtype,
                               pa_dtype bounds_dtype, cudaStream_t stream);
 

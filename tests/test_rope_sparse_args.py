@@ -143,3 +143,11 @@ def test_binding_checks_before_the_library(pk):
                          torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(TypeError, match="workspace must be a tensor"):
         pk.sparse_decode(q, q, cache, cache, bounds, i32, i32, 16, 0.1, 4, None)
+
+
+def test_bounds_of_more_warps_than_indices(pk):
+    """Touched blocks times KV heads beyond 2^27 (a warp each) are refused: 32-bit thread indices would wrap."""
+    assert bounds(pk, new=OK, maxnew=2 ** 24 + 1, maxlen=2 ** 30, B=1, Hkv=8) == pk.PA_ERR_UNSUPPORTED
+    assert bounds(pk, new=OK, maxnew=2 ** 30, maxlen=2 ** 30, B=16, Hkv=8) == pk.PA_ERR_UNSUPPORTED
+    # at most the context: a larger bound on the new tokens is no reason
+    assert bounds(pk, S=0, new=OK, maxnew=2 ** 30, maxlen=2 ** 20) == pk.PA_OK

@@ -620,6 +620,9 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
  * "Sharing KV Cache-COW"). A pair naming a block outside [0, num_blocks) is
  * skipped and sets PA_DEV_BAD_BLOCK_ID. Pairs must not write the same dst, or
  * read a block another pair writes, in one call (they run concurrently).
+ * Key bounds are not copied: where the block-sparse decode is used, call
+ * pa_key_bounds with new_tokens reaching back to the first copied block (the
+ * newest block, which the next append writes to, is recomputed anyway).
  */
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_pairs,
                          int64_t num_pairs, int num_kv_heads, int head_size, int block_size,

@@ -620,7 +620,8 @@ def version() -> int:
 
 def copy_blocks(k_cache, v_cache, block_pairs, dev_status=None, stream=None) -> None:
     """Copy whole blocks for each (src, dst) row of block_pairs ([n, 2] int64,
-    on the device): the copy of copy-on-write."""
+    on the device): the copy of copy-on-write. Their key bounds are recomputed by
+    key_bounds, with new_tokens reaching back to the first copied block."""
     nb, H, B, D = k_cache.shape
     if block_pairs.dtype != torch.int64 or block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("block_pairs must be int64 [n, 2]")

@@ -164,3 +164,38 @@ def test_caches_past_32_bit_offsets():
     assert int(status.item()) == 0
     small.check(o, sel, 8)
     assert torch.equal(small.vc.transpose(1, 2).reshape(-1, Hkv, D)[:T], v)
+
+
+@pytest.mark.parametrize("dtype,e4m3", [("bf16", False), ("bf16", True)])
+def test_copied_blocks(dtype, e4m3):
+    """Blocks moved to other ids, then bounds from the first of them on: the context decodes as it did. A fork whose
+    newest block is copied and appended to needs that block's bounds alone."""
+    p = Pool([16 * 60 + 5], dtype=dtype, e4m3=e4m3, seed=23)
+    L = p.lens[0]
+    kc, vc = (torch.cat((c, torch.full_like(c[:10], 0x7F if e4m3 else float("nan")))) for c in (p.kc, p.vc))
+    p.bounds = torch.cat((p.bounds, torch.full_like(p.bounds[:10], 100.0)))       # (of a block's earlier owner)
+    p.kc, p.vc, p.num_blocks = kc, vc, p.num_blocks + 10
+    p.fill_bounds()
+    out, sel = p.decode(20)
+    table = p.tables.clone()
+    moved = list(range(30, 38))
+    fresh = torch.arange(p.num_blocks - 10, p.num_blocks - 2)
+    pairs = torch.stack((table[0, moved].cpu().long(), fresh), 1).cuda()
+    pk.copy_blocks(p.kc, p.vc, pairs, dev_status=p.status)
+    p.tables[0, moved] = fresh.int().cuda()
+    back = torch.tensor([L - 30 * 16], dtype=torch.int32, device="cuda")
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, L, back, L, dev_status=p.status)
+    again, same = p.decode(20)
+    assert torch.equal(out, again) and torch.equal(sel, same) and int(p.status.item()) == 0
+    # the fork: a copy of the newest block, one more token (in both caches the first token's rows)
+    last = L // 16
+    fork = p.num_blocks - 1
+    pk.copy_blocks(p.kc, p.vc, torch.tensor([[int(p.tables[0, last]), fork]], device="cuda"), dev_status=p.status)
+    p.tables[0, last] = fork
+    for c in (p.kc, p.vc):
+        c[fork, :, L % 16] = c[p.tables[0, 0].long(), :, 0]
+    p.lens, p.max_len, p.context = [L + 1], L + 1, p.context + 1
+    pk.key_bounds(p.bounds, p.kc, p.tables, p.context, L + 1, dev_status=p.status)
+    out, sel = p.decode(20)
+    assert int(p.status.item()) == 0
+    p.check(out, sel, 20)

@@ -289,7 +289,10 @@ inline cudaError_t ensure_smem_attribute(const void* key, int bytes) {
 // visible -- unconditionally, before any access to memory and any return, so
 // that the chain of a stream's kernels holds. Then it lets the next one start:
 // launch and scheduling latency, several microseconds for the small kernels of
-// a decode step, overlap the running kernel.
+// a decode step, overlap the running kernel. (The grid's life overlaps the writes
+// of the one before it, so these kernels read by plain loads, not by the read-only
+// path, whose data must not change while the kernel is alive. 64 sparse contexts of
+// 8k-32k: 113.2 us so, 112.7 otherwise.)
 __device__ __forceinline__ void begin_overlapped() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -98,7 +98,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
     uint4 q_words = make_uint4(0, 0, 0, 0);
     if (q_head < G) {                               // rows of a sequence's heads are contiguous
         const size_t row = blockIdx.x / cluster.num_blocks();
-        q_words = __ldg(reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) + (row * G + q_head) * D + 8 * q_chunk));
+        q_words = *reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) + (row * G + q_head) * D + 8 * q_chunk);
     }
     const SelRow rw(p, cluster, work);
     const int C = rw.C;
@@ -195,8 +195,8 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
         const uint8_t* k = static_cast<const uint8_t*>(sp.k_cache) + (at < 0 ? 0 : at) + g * kRowBytes + 16 * t4;
 #pragma unroll
         for (int j = 0; j < Tile::KJ; ++j) {
-            tl.x[j] = __ldg(reinterpret_cast<const uint4*>(k + 64 * j));
-            tl.y[j] = __ldg(reinterpret_cast<const uint4*>(k + 8 * kRowBytes + 64 * j));
+            tl.x[j] = *reinterpret_cast<const uint4*>(k + 64 * j);
+            tl.y[j] = *reinterpret_cast<const uint4*>(k + 8 * kRowBytes + 64 * j);
         }
     };
     // rows from nvalid on are zeroed: their weights are 0, and 0 x NaN is not
@@ -210,14 +210,14 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
             if constexpr (kFp8) {
                 const uint8_t* codes = row + g * (D / 8);
                 if constexpr (D == 64) {
-                    const uint2 w = there ? __ldg(reinterpret_cast<const uint2*>(codes)) : make_uint2(0, 0);
+                    const uint2 w = there ? *reinterpret_cast<const uint2*>(codes) : make_uint2(0, 0);
                     tl.v[r][0] = w.x;
                     tl.v[r][1] = w.y;
                 } else {
 #pragma unroll
                     for (int u = 0; u < Tile::VW; u += 4) {
                         uint4 w = make_uint4(0, 0, 0, 0);
-                        if (there) w = __ldg(reinterpret_cast<const uint4*>(codes + 4 * u));
+                        if (there) w = *reinterpret_cast<const uint4*>(codes + 4 * u);
                         tl.v[r][u] = w.x;
                         tl.v[r][u + 1] = w.y;
                         tl.v[r][u + 2] = w.z;
@@ -228,7 +228,7 @@ sparse_decode_kernel(const __grid_constant__ SparseParams sp) {
 #pragma unroll
                 for (int u = 0; u < Tile::VU; ++u) {
                     uint4 w = make_uint4(0, 0, 0, 0);
-                    if (there) w = __ldg(reinterpret_cast<const uint4*>(row + 128 * u + 16 * g));
+                    if (there) w = *reinterpret_cast<const uint4*>(row + 128 * u + 16 * g);
                     tl.v[r][u] = w;
                 }
             }

@@ -169,8 +169,8 @@ struct Quarter {
     __device__ __forceinline__ void load(const T* x_row, const T* y_row) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x[j] = __ldg(reinterpret_cast<const uint4*>(x_row + 32 * j));
-            y[j] = __ldg(reinterpret_cast<const uint4*>(y_row + 32 * j));
+            x[j] = *reinterpret_cast<const uint4*>(x_row + 32 * j);
+            y[j] = *reinterpret_cast<const uint4*>(y_row + 32 * j);
         }
     }
 };

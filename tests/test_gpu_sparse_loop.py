@@ -199,3 +199,45 @@ def test_copied_blocks(dtype, e4m3):
     out, sel = p.decode(20)
     assert int(p.status.item()) == 0
     p.check(out, sel, 20)
+
+
+def test_steps_without_a_wait_equal_steps_with_one():
+    """Append, bounds and sparse decode back to back on one stream: each kernel starts while the one before it runs,
+    and reads what that one writes (query, caches, bounds). Bit for bit the results of the same calls one at a time."""
+    S, Hq, Hkv, D, B, steps = 24, 32, 8, 128, 16, 40
+    g = torch.Generator().manual_seed(31)
+    lens = torch.randint(200, 900, (S,), generator=g)
+    width = (900 + steps) // B + 1
+    tables = (torch.randperm(S * width, generator=g) + 1).view(S, width).int().cuda()
+    shape = (S * width + 1, Hkv, B, D)
+    kc0, vc0 = (torch.randn(shape, generator=g).bfloat16().cuda() for _ in range(2))
+    qkv = torch.randn((steps, S, Hq + 2 * Hkv, D), generator=g).bfloat16().cuda()
+    angle = torch.rand((1024, D // 2), generator=g) * 6.28
+    cos_sin = torch.cat((angle.cos(), angle.sin()), 1).cuda()
+    at = [(lens + i) for i in range(steps)]
+    slots = [(tables.cpu().gather(1, (a // B).view(-1, 1)).view(-1).long() * B + a % B).cuda() for a in at]
+    positions, context = [a.cuda() for a in at], [(a + 1).int().cuda() for a in at]
+    max_len = int(lens.max()) + steps
+    results = []
+    for wait in (True, False):
+        kc, vc = kc0.clone(), vc0.clone()
+        bounds = torch.full((shape[0], Hkv, 2, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        pk.key_bounds(bounds, kc, tables, lens.int().cuda(), max_len, lens.int().cuda(), max_len)
+        q, outs = torch.empty((S, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((steps, S, Hq, D), dtype=torch.bfloat16, device="cuda")
+        ws = pk.alloc_sparse_workspace(S, Hq, Hkv, D, B, max_len, 12)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            x = qkv[i]
+            pk.rope_and_cache(q, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], kc, vc, cos_sin, positions[i], slots[i])
+            if wait:
+                torch.cuda.synchronize()
+            pk.key_bounds(bounds, kc, tables, context[i], max_len)
+            if wait:
+                torch.cuda.synchronize()
+            pk.sparse_decode(outs[i], q, kc, vc, bounds, tables, context[i], max_len, D ** -0.5, 12, ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append((outs, kc, vc, bounds[tables.flatten().long()]))
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

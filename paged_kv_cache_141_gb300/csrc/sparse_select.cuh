@@ -307,6 +307,34 @@ __device__ bool zero_query(const SelectParams& p, int s, int h) {
     return !__syncthreads_or(any);
 }
 
+// Whether all bounds of the candidates are zero (all threads, for all).
+template <typename T, int D, int NT>
+__device__ bool zero_bounds(const SelectParams& p, int h, const int32_t* table, int nc) {
+    constexpr int W = 2 * D * (int)sizeof(T) / 16;             // 16-byte words of a block's row
+    constexpr uint32_t kAbs = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+    constexpr int kBatch = 8;                                  // blocks read before one is looked at
+    const int lane = threadIdx.x & 31;
+    bool any = false;
+    for (int i0 = threadIdx.x >> 5; i0 < nc && !any; i0 += kBatch * (NT / 32)) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * (NT / 32);
+            const int64_t blk = i < nc ? table[i] : -1;
+            if (blk < 0 || blk >= p.num_blocks) continue;
+            const uint4* row = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_bounds) +
+                                                              ((size_t)blk * p.num_kv_heads + h) * 2 * D);
+#pragma unroll
+            for (int c = lane; c < W; c += 32) {
+                const uint4 w = row[c];
+                bits |= w.x | w.y | w.z | w.w;
+            }
+        }
+        any = __any_sync(0xffffffffu, (bits & kAbs) != 0);
+    }
+    return !__syncthreads_or(any);
+}
+
 // The score that ordered() puts below every value: a block not taken.
 __device__ __forceinline__ float out_key() { return __uint_as_float(0xffffffffu); }
 
@@ -807,8 +835,9 @@ __device__ __forceinline__ void take_by_search(const SelectParams& p, SelShared<
     if (!finite) thr = ordered(INFINITY);
     if (left < open) {
         // ------------------------------------------- exact scores of the unsettled
-        // (A zero query, say of a padding row, makes every score 0, exactly.)
-        const bool zeros = mag == 0.f && zero_query<T, D, NT>(p, s, h);
+        // (A zero query, say of a padding row, or a pool of zeros makes every score
+        // 0, exactly.)
+        const bool zeros = mag == 0.f && (zero_query<T, D, NT>(p, s, h) || zero_bounds<T, D, NT>(p, h, table + lo, nc));
         const bool small = open <= SelShared<NT>::kRankList && !zeros;
         if (threadIdx.x == 0) sh.list_n = 0;
         __syncthreads();
@@ -952,10 +981,13 @@ __device__ __forceinline__ int32_t slab_of(const SelectParams& p, const SelRow& 
 
 // ---------------------------------------------------------------- host side
 
-// CTAs per row: as many as fit on 152 SMs with a tile of 16 blocks or more for
-// every warp. For many rows one CTA each wins, two on an SM: their selections
-// overlap other rows' scoring. (8 rows of 8192 blocks: 69, 44, 31 and 25 us with
-// 1, 2, 4 and 8 CTAs of 16 warps; 112 rows of 1170: 34, 51 and 77 with 1, 2, 4.)
+// CTAs of 8 warps per row for the selection alone (the fused kernel has a rule of
+// its own): as many as fit on 152 SMs with a tile of 16 blocks or more for every
+// warp. For many rows one CTA each wins, two on an SM: their selections overlap
+// other rows' scoring. Whole calls of groups of 16 heads of 128, bf16, with 1, 2, 4
+// and 8 CTAs: 8 rows of 8192 blocks 235, 137, 83 and 56 us; 32 rows of 1024 blocks
+// 56, 46, 40 and 40, of 500 blocks 42, 38, 36 and 38; 112 rows of 1170 blocks 80, 79,
+// 87 and 99. Binary32, 8 rows of 8192: 766, 446, 237 and 132.
 inline int select_cluster(int rows, int max_ctx_blocks) {
     int C = 1;
     while (C < kMaxCluster && rows <= 152 / (2 * C) && max_ctx_blocks >= 2 * C * 256) C *= 2;

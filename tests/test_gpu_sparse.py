@@ -531,16 +531,19 @@ def test_weights_keep_their_bits(dtype, e4m3, Hq):
                                              ("f32", 32, 16, 2.0 ** -100)])
 def test_products_that_all_underflow(dtype, Hq, B, size):
     """Query and bounds whose products pass below binary32's range (bfloat16's range too, with 2^40 to spare): the
-    order is that of the exact scores all the same. One sequence each with a zero query, and with zero keys."""
-    p = Pool([B * 120, B * 97 + 1, B * 50], Hq, 2, 128, B, dtype, seed=13)
+    order is that of the exact scores all the same. One sequence each with a zero query, and with zero keys (but for
+    one that is not, in the last)."""
+    p = Pool([B * 120, B * 97 + 1, B * 50, B * 600], Hq, 2, 128, B, dtype, seed=13)
     p.fill_bounds()
     p.bounds.copy_((p.bounds.double().nan_to_num(0) * size).to(p.dt))
     p.query.copy_((p.query.double() * size).to(p.dt))
     assert bool((p.query != 0).any()) and bool((p.bounds != 0).any())
     p.query[1] = 0
-    p.bounds[p.tables[2].long()] = 0
+    p.bounds[p.tables[2, :50].long()] = 0
+    p.bounds[p.tables[3].long()] = 0
+    p.bounds[p.tables[3, 571].long(), :, 1, 77] = size
     sel = p.decode(15, 1, 1)[1]
-    for s in range(3):
+    for s in range(4):
         for h in range(2):
             assert sel[s, h].tolist() == p.want_selected(s, h, 15, 1, 1), (s, h)
 

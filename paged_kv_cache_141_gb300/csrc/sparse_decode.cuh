@@ -23,20 +23,20 @@
 // (times 2^7, so that what binary16 cannot hold is below 2^-31 of the reference's
 // weight). The sums use exactly the weights that the products use. Fewer terms
 // would be a little faster on E4M3 caches (one: 120 us for 123 on the batch below)
-// and no faster on 16-bit ones, which the loads bound. E4M3 codes
-// convert to binary16, NaN codes to NaN: a NaN key or value shows in the output
-// (the integer widening of the dense decode, which reads those as +-480, took 117 us
-// for 120). A 16-bit query meets them scaled by a power of two to at most 2 in magnitude, exact but for
-// components more than 2^14 below the head's largest. Partial results are joined in
-// shared memory across the warps, and through the cluster's across CTAs.
+// and no faster on 16-bit ones, which the loads bound. E4M3 codes convert to
+// binary16, NaN codes to NaN: a NaN key or value shows in the output (the integer
+// widening of the dense decode, which reads those as +-480, took 117 us for 120). A
+// 16-bit query meets them scaled by a power of two to at most 2 in magnitude, exact
+// but for components more than 2^14 below the head's largest. Partial results are
+// joined in shared memory across the warps, and through the cluster's across CTAs.
 //
-// Measured (32/8 heads of 128, block size 16): 64 bf16 contexts of 8k to 32k
-// tokens with 64 blocks selected 114 us, 5.3 TB/s of bounds, keys and values,
+// Measured in a graph (32/8 heads of 128, block size 16): 64 bf16 contexts of 8k to
+// 32k tokens with 64 blocks selected 113 us, 5.4 TB/s of bounds, keys and values,
 // where bare gathers of such chunks reach 5.2 (512 bytes) to 5.9 (4 KB) TB/s: bound
 // by them. One context of 131072 with 128 selected 27 us: bound by the latencies
 // of score, select, attend and the cluster's barriers in a row. E4M3 (64/8 heads,
-// 128 contexts of 100 to 8k, 96 selected) 117 to 122 us, 4.6 TB/s: bound by issue
-// (widening the codes) and the selection.
+// 128 contexts of 100 to 8k, 96 selected) 124 us, 4.4 TB/s: bound by latency at 16
+// warps per SM (loads, the conversions' chain, the selection's barriers).
 #pragma once
 
 #include "sparse_select.cuh"

@@ -572,13 +572,13 @@ pa_status pa_key_bounds(void* k_bounds, const void* k_cache, const int32_t* bloc
  * the work is split; a NaN score counts as +infinity. The output is
  * softmax(scale * q K^T) V over the selected blocks' tokens below L; a NaN among
  * those (a NaN code of an E4M3 cache too) shows in it. Scores, softmax statistics
- * and sums are held in binary32. The weights meet the values in at least 22
- * significant bits for F16 and E4M3 caches and 24 for BF16 (16 where the paged
- * decode reads the selection of a BF16 cache: groups above 8 heads, block sizes
- * not a multiple of 16, selections above 8192 blocks). E4M3 caches meet the query
- * in binary16: under a power of two of its own for each head (exact but for
- * components more than 2^14 below the head's largest), in those other shapes as
- * it is (a component beyond +-65504 becomes infinite).
+ * and sums are held in binary32. A weight meets the values to within 2^-22 of
+ * itself or 2^-24 of the largest (F16 and E4M3 caches), or 2^-24 of itself (BF16;
+ * 2^-16 where the paged decode reads the selection: groups above 8 heads, block
+ * sizes not a multiple of 16, selections above 8192 blocks). E4M3 caches meet the
+ * query in binary16 under a power of two for each head, exact but for components
+ * more than 2^14 below the head's largest (where the paged decode reads head size
+ * 64, odd groups or other block sizes than 8, 16 and multiples of 32: in binary32).
  *
  *  k_bounds       [num_blocks][num_kv_heads][2][head_size], of the query's type;
  *                 read only for blocks that are scored (never for the newest

@@ -170,7 +170,7 @@ constexpr int mma_threads() {
 // (2 t4 and 2 t4 + 1), and the work on one 32-token stage of K and V.
 // kOneTermP: the weights as one 16-bit term (E4M3 values, widened in
 // registers or staged as binary16 tiles); otherwise high part + residual.
-// kNan: E4M3's NaN codes are read as NaN.
+// kNan: E4M3's NaN codes are read as NaN, and the query meets them scaled.
 template <typename QT, typename CT, int D, int GS,
           bool kOneTermP = std::is_same<CT, e4m3_t>::value, bool kNan = false>
 struct MmaWarp {
@@ -185,6 +185,7 @@ struct MmaWarp {
     // permutation of the reduction, applied to K and Q alike).
     uint32_t qb[KS][2];
     float qk_mul;                               // scale * log2(e) (E4M3: k_scale and 2^8 too)
+    float head_mul[2];                          // kNan: times the units of heads 2 t4, 2 t4 + 1
     float acc[KS][4];                           // O^T fragments: rows d, columns heads
     float m_run[2];                             // heads 2*t4 and 2*t4+1
     float l_run[2];                             // this lane's share of the sums
@@ -194,6 +195,23 @@ struct MmaWarp {
     __device__ __forceinline__ void load_query(const QT* __restrict__ qp, float q_mul, int lane) {
         const int g = lane >> 2;
         const int t4 = lane & 3;
+        float r = 1.f;
+        if constexpr (kNan) {
+            // each head under a power of two that brings its largest magnitude
+            // into [1, 2), kept to the range whose reciprocal is a normal number
+            float mx = 0.f;
+            if (g < GS) {
+#pragma unroll
+                for (int i = 0; i < 4 * KS; ++i) mx = fmaxf(mx, fabsf(to_float(qp[g * D + 4 * i + t4])));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
+            const float unit = mx > 0.f && mx < INFINITY ? __uint_as_float(ex << 23) : 1.f;
+            r = 1.f / unit;                                    // exact
+            head_mul[0] = q_mul * __shfl_sync(0xffffffffu, unit, 8 * t4);
+            head_mul[1] = q_mul * __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             if (g >= GS) {
@@ -201,15 +219,15 @@ struct MmaWarp {
                 qb[ks][1] = 0u;
             } else if constexpr (kFp8) {
                 const QT* q4 = qp + g * D + 16 * ks + 4 * t4;
-                qb[ks][0] = Ops::pack(to_float(q4[0]), to_float(q4[1]));
-                qb[ks][1] = Ops::pack(to_float(q4[2]), to_float(q4[3]));
+                qb[ks][0] = Ops::pack(to_float(q4[0]) * r, to_float(q4[1]) * r);
+                qb[ks][1] = Ops::pack(to_float(q4[2]) * r, to_float(q4[3]) * r);
             } else {
                 qb[ks][0] = *reinterpret_cast<const uint32_t*>(qp + g * D + 16 * ks + 2 * t4);
                 qb[ks][1] = *reinterpret_cast<const uint32_t*>(qp + g * D + 16 * ks + 2 * t4 + 8);
             }
         }
-        // the widened E4M3 codes are their values times 2^-8 (the converted ones their values)
-        qk_mul = kFp8 && !kNan ? q_mul * 256.f : q_mul;
+        // the widened E4M3 codes are their values times 2^-8
+        qk_mul = kFp8 ? q_mul * 256.f : q_mul;
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -306,7 +324,7 @@ struct MmaWarp {
 #pragma unroll
                 for (int hr = 0; hr < 2; ++hr) {
                     const int tok = 16 * mt + g + 8 * hr;
-                    float v = sc[mt][2 * hr + j] * qk_mul;
+                    float v = sc[mt][2 * hr + j] * (kNan ? head_mul[j] : qk_mul);
                     v = tok < nvalid ? v : -INFINITY;          // select, never multiply
                     sc[mt][2 * hr + j] = v;
                     mx = fmaxf(mx, v);
@@ -678,7 +696,7 @@ __device__ __forceinline__ void shared_unit_cta(const TmaDecodeParams& tp, uint8
 // kShared: a split launch with shared-prefix units (grid z: units, then
 // sequences); a separate instantiation, so that the plain kernels carry
 // neither the unit path nor the skip test. kNan: E4M3 caches whose NaN codes
-// are read as NaN, with the weights in two terms.
+// are read as NaN, with the weights in two terms and the query scaled.
 template <typename QT, typename CT, int D, int GS, bool kSplit, bool kShared = false, bool kNan = false>
 __global__ void __launch_bounds__(mma_threads<CT, D>(), mma_min_blocks<CT, D>())
 paged_decode_mma_kernel(const __grid_constant__ TmaDecodeParams tp) {

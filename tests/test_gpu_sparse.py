@@ -634,3 +634,19 @@ def test_bounds_of_a_block_that_several_sequences_name(dtype, e4m3):
     assert bool(torch.stack([got == e for e in ends]).any(0).all())
     pk.key_bounds(p.bounds, p.kc, p.tables, p.context, L, dev_status=p.status)
     assert torch.equal(p.bounds[newest].double(), ends[2])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(8, 2, 128, 16), (32, 2, 128, 16), (16, 1, 256, 16), (8, 2, 128, 8), (32, 2, 64, 16)])
+@pytest.mark.parametrize("sizes", [(2.0 ** 20, 2.0 ** 30), (2.0 ** -30, 2.0 ** -18), (2.0 ** 40, 2.0 ** -40)])
+def test_e4m3_pools_with_queries_beyond_binary16(Hq, Hkv, D, B, sizes):
+    """bfloat16 queries far above and below binary16's range, heads of one group of different size: the scores have
+    the precision of ordinary ones (each head's scale brings them to the same logits as size 1 would)."""
+    lens = [1, 300, 40 * B]
+    for size in sizes:
+        p = Pool(lens, Hq, Hkv, D, B, "bf16", True, seed=41)
+        p.query.copy_((p.query.double() * size).to(p.dt))
+        p.query[:, ::2] /= 4.0
+        p.scale /= size
+        p.fill_bounds()
+        out, sel = p.decode(20)
+        p.check(out, sel, 20)

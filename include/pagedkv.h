@@ -91,7 +91,8 @@ typedef enum pa_dtype {
     PA_F32 = 0,               /* IEEE binary32 */
     PA_F16 = 1,               /* IEEE binary16 */
     PA_BF16 = 2,              /* bfloat16 */
-    PA_FP8_E4M3 = 3           /* OCP E4M3 (bias 7, max 448, no infinities) */
+    PA_FP8_E4M3 = 3,          /* OCP E4M3 (bias 7, max 448, no infinities) */
+    PA_INT8 = 4               /* 8-bit integer codes, of block-scaled caches alone */
 } pa_dtype;
 
 /* Bits a kernel ORs into *dev_status. */
@@ -111,6 +112,10 @@ typedef enum pa_dtype {
 
 #define PA_DEV_BAD_POSITION 128u /* a position outside [0, max_position) of the rotation table
                                    (the token is skipped) */
+#define PA_DEV_NO_BLOCKS   256u /* pa_extend_tables: too few free blocks for a request (it
+                                   gets no token) */
+#define PA_DEV_BAD_TOKEN   512u /* a drafted token outside the vocabulary (it counts as rejected) */
+#define PA_DEV_BAD_PROB   1024u /* probabilities with no positive, finite sum: no token is drawn */
 
 /* Supported shapes: head_size in {64, 128, 256}; block_size in [1, 1024];
  * partition_size a positive multiple of 32 (512 on the pages).
@@ -608,6 +613,172 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
                            pa_dtype q_dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
                            void* workspace, size_t workspace_bytes, uint32_t* dev_status,
                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * A step that does not wait for the host: block tables on the device, a cache of
+ * 8-bit codes with a scale for each (block, KV head), and the verification of
+ * drafted tokens. In a speculative step: pa_extend_tables makes room for every
+ * request's tokens, pa_scaled_append writes their keys and values,
+ * pa_scaled_attention attends to them, pa_verify_drafts accepts drafts and counts
+ * the rejected ones, pa_trim_tables takes those out again. All can be captured in a
+ * CUDA graph; none needs a length on the host beyond its bounds. The pages build
+ * tables on the host and quantise with one scale per tensor; these are this
+ * library's.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pa_extend_tables -- new_tokens[s] tokens more for every request: the blocks they
+ * need, from a stack of free ones, and their slots and positions.
+ *
+ *  block_tables   [num_seqs][max_blocks_per_seq] int32; entries from
+ *                 ceil(context_lens[s] / block_size) on are written.
+ *  context_lens,
+ *  new_tokens     [num_seqs] int32.
+ *  free_blocks    [free_capacity] int32, a stack whose first *num_free entries are
+ *                 free. Blocks are taken from its top, requests in their order.
+ *  slot_mapping   [max_tokens] int64: the new tokens' slots, those of request s at
+ *                 query_start[s]; -1 (padding) behind the last.
+ *  positions      [max_tokens] int64, or NULL; 0 behind the last.
+ *  query_start    [num_seqs + 1] int32: sums of the tokens served.
+ *  new_lens       [num_seqs] int32: context_lens plus the tokens served; may be
+ *                 context_lens itself.
+ *  new_num_free   [1] int32; may be num_free itself.
+ *  Served in order: a request whose blocks are not all there after those of the
+ *  requests before it gets no token (PA_DEV_NO_BLOCKS), nor does any later one that
+ *  needs a block. A count below zero, one that does not fit the table, or one whose
+ *  slots (with those asked for before it) pass max_tokens gets none either
+ *  (PA_DEV_BAD_LEN). A *num_free outside [0, free_capacity] is brought into it
+ *  (PA_DEV_BAD_BLOCK_ID). At most 16384 requests.
+ */
+pa_status pa_extend_tables(int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* new_tokens, int num_seqs,
+                           const int32_t* free_blocks, const int32_t* num_free,
+                           int64_t free_capacity, int block_size, int64_t* slot_mapping,
+                           int64_t* positions, int64_t max_tokens, int32_t* query_start,
+                           int32_t* new_lens, int32_t* new_num_free, uint32_t* dev_status,
+                           void* stream);
+
+/*
+ * pa_trim_tables -- the newest drop_tokens[s] tokens of every request are dropped
+ * (rejected drafts; all of them where a request has ended), and the blocks that fall
+ * empty go back on the stack, in the reverse of the order in which pa_extend_tables
+ * takes them: extending again by as many gives the same blocks.
+ *
+ *  shared_blocks  [num_seqs] int32, or NULL: leading blocks of each table that never
+ *                 go to the stack (a prefix that other requests hold too).
+ *  A count outside [0, context_lens[s]] drops nothing (PA_DEV_BAD_LEN). If the stack
+ *  cannot hold all blocks, nothing is dropped (PA_DEV_BAD_BLOCK_ID). The tables keep
+ *  their entries. Other arguments as above.
+ */
+pa_status pa_trim_tables(const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* drop_tokens, int num_seqs,
+                         int32_t* free_blocks, const int32_t* num_free, int64_t free_capacity,
+                         int block_size, const int32_t* shared_blocks, int32_t* new_lens,
+                         int32_t* new_num_free, uint32_t* dev_status, void* stream);
+
+/*
+ * pa_scaled_append -- the KV write into a block-scaled cache. The newest tokens of
+ * each sequence are quantised under their blocks' scales; no calibration is needed.
+ *
+ *  key, value     rows of [num_kv_heads][head_size] elements (F32, F16 or BF16),
+ *                 contiguous, tokens key_stride / value_stride elements apart
+ *                 (multiples of 16 bytes). Row query_start[s] + i is position
+ *                 context_lens[s] - n_s + i of sequence s, n_s = query_start[s + 1] -
+ *                 query_start[s] <= max_new_tokens. query_start NULL: row s is the
+ *                 newest token of sequence s (none where its length is 0),
+ *                 max_new_tokens 1, num_tokens = num_seqs.
+ *  k_cache,
+ *  v_cache        [num_blocks][num_kv_heads][block_size][head_size] codes, cache_dtype
+ *                 PA_FP8_E4M3 or PA_INT8.
+ *  k_scales,
+ *  v_scales       [num_blocks][num_kv_heads] float32: an element is code * scale.
+ *  For each block and head that receives tokens, with m their largest magnitude:
+ *    fresh  = m / 127 (PA_INT8), or the least power of two with m <= 448 fresh
+ *             (PA_FP8_E4M3); never below 2^-96;
+ *    scale' = max(scale, fresh) where the block holds older tokens of the sequence,
+ *             else fresh (what an earlier request left there does not count);
+ *    codes  = x / scale' to nearest even, in [-127, 127] or as E4M3; older codes c
+ *             become c (scale / scale') to nearest even where the scale has grown.
+ *  A NaN or an infinity makes the block's scale NaN, and with it whatever is read
+ *  through it, until the block starts anew. Two sequences that write to one block
+ *  race, as do the rows that pass num_tokens (PA_DEV_BAD_LEN, skipped).
+ *  Blocks copied by pa_copy_blocks need their scales copied too.
+ */
+pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* value,
+                           int64_t value_stride, void* k_cache, void* v_cache, float* k_scales,
+                           float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* query_start,
+                           int64_t num_tokens, int max_new_tokens, int num_seqs, int num_kv_heads,
+                           int head_size, int block_size, int64_t num_blocks, pa_dtype in_dtype,
+                           pa_dtype cache_dtype, uint32_t* dev_status, void* stream);
+
+/*
+ * pa_scaled_attention -- causal attention over a block-scaled cache: for the Q_s =
+ * query_start[s + 1] - query_start[s] query tokens of sequence s, its last Q_s
+ * positions (their keys and values already written), token i attends to positions
+ * 0 .. context_lens[s] - Q_s + i. query_start NULL: one query token each (the
+ * decode; a context of length 0 gives zeros).
+ *
+ *  out, query     [num_queries][num_q_heads][head_size], F16 or BF16; rows behind
+ *                 the last sequence's are left as they are.
+ *  k_cache, v_cache, k_scales, v_scales  as pa_scaled_append leaves them; any finite
+ *                 scale >= 0 is read as it is.
+ *  max_queries_per_seq  an upper bound of Q_s; 0 <= Q_s <= it and Q_s <=
+ *                 context_lens[s] (else PA_DEV_BAD_LEN and the sequence is skipped).
+ *  workspace      256-byte aligned, pa_scaled_attention_workspace_bytes(...) of these
+ *                 sizes (NULL where that is 0); nothing in it outlives the call's
+ *                 kernels. Calls that overlap on the GPU need workspaces of their own.
+ *  Codes past a context's end are not read. An E4M3 NaN code within it is read as
+ *  +-480 (pa_scaled_append writes none but under a NaN scale).
+ *  Scores, softmax statistics and sums are binary32. The query meets the codes exactly
+ *  but for components more than 2^14 below a row's largest; a weight meets them to
+ *  within 2^-11 of itself or 2^-25 of the largest. Block sizes up to 1024, head sizes
+ *  64, 128 and 256, any group.
+ */
+size_t pa_scaled_attention_workspace_bytes(int num_seqs, int num_queries, int num_q_heads,
+                                           int num_kv_heads, int head_size,
+                                           int max_queries_per_seq, int max_context_len);
+pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
+                              const void* v_cache, const float* k_scales, const float* v_scales,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, const int32_t* query_start,
+                              int num_queries, int max_queries_per_seq, int num_seqs,
+                              int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                              int64_t num_blocks, int max_context_len, float scale,
+                              pa_dtype q_dtype, pa_dtype cache_dtype, void* workspace,
+                              size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * pa_verify_drafts -- which drafted tokens the target accepts, and the token after
+ * them, from given random numbers. Request s has rows query_start[s] ..
+ * query_start[s + 1] - 1 of target_probs, one more than it has drafts: row i is the
+ * target's distribution of the token after i drafts.
+ *
+ *  draft i is accepted while u_i q_i(x_i) < p_i(x_i) for it and all before it (in
+ *  binary64). With a accepted, the next token is drawn from w = max(p_a - q_a, 0)
+ *  where a draft was rejected (from p_a if that is zero throughout), or from p_a
+ *  after the last: the first j with w_0 + .. + w_j > u W, W the sum of all.
+ *
+ *  out_tokens     [num_seqs][max_drafts + 1] int64: the accepted drafts, the drawn
+ *                 token, -1 behind it (all -1 for a request without rows).
+ *  accepted       [num_seqs] int32; rejected (or NULL): the drafts that were not.
+ *  target_probs   [num_rows] rows of vocab float32, target_stride elements apart.
+ *  draft_probs    [num_seqs][max_drafts] such rows, draft_stride apart, or NULL: the
+ *                 drafts were not sampled (q is 1 for the token, 0 for others).
+ *  draft_tokens   [num_seqs][max_drafts] int64; entries behind a request's drafts
+ *                 are not read.
+ *  uniforms       [num_seqs][max_drafts + 1] float32 in [0, 1): u_i of the drafts, and
+ *                 last in the row the one that draws.
+ *  Rows need not sum to 1. Sums are kept to 2^-44 of themselves. More
+ *  rows than max_drafts + 1, or outside [0, num_rows): PA_DEV_BAD_LEN, as without
+ *  rows. vocab up to 2^22.
+ */
+pa_status pa_verify_drafts(int64_t* out_tokens, int32_t* accepted, int32_t* rejected,
+                           const float* target_probs, int64_t target_stride, int64_t num_rows,
+                           const float* draft_probs, int64_t draft_stride,
+                           const int64_t* draft_tokens, const float* uniforms,
+                           const int32_t* query_start, int num_seqs, int max_drafts, int vocab,
+                           uint32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------
  * Block management: the host-side allocator and the copy-on-write copy.

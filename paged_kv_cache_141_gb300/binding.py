@@ -5,14 +5,17 @@ and the current CUDA stream to the library, and raises PagedKVError when the
 library returns a non-zero status. All computation happens in the library's
 CUDA kernels. If the library has not been built, loading fails with an error;
 there is no fallback path. The calls go through ctypes, but for the rotating
-append, the key bounds and the block-sparse decode, whose arguments a small C++
-module marshals (pysrc/marshal.cpp).
+append, the key bounds, the block-sparse decode and the calls of a step that does
+not wait for the host, whose arguments a small C++ module marshals
+(pysrc/marshal.cpp).
 
 Tensors are CUDA tensors, contiguous, in the library's layouts:
   query/out        [num_seqs, num_q_heads, head_size]   float32/float16/bfloat16
   key/value        [num_tokens, num_kv_heads, head_size]
   k_cache/v_cache  [num_blocks, num_kv_heads, block_size, head_size]
-                   (E4M3 caches as torch.uint8 or torch.float8_e4m3fn)
+                   (E4M3 caches as torch.uint8 or torch.float8_e4m3fn; integer codes of
+                   block-scaled caches as torch.int8)
+  k_scales/v_scales [num_blocks, num_kv_heads] float32, of block-scaled caches
   block_tables     [num_seqs, max_blocks] int32
   context_lens     [num_seqs] int32
   slot_mapping     [num_tokens] int64
@@ -31,11 +34,12 @@ _lock = threading.Lock()
 _lib = None
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_NO_BLOCKS = range(6)
-PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = range(4)
+PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT8 = range(5)
 DEV_BAD_BLOCK_ID, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT, DEV_SLOT_MISMATCH = 1, 2, 4, 8, 16
 DEV_BAD_ORDER = 32
 DEV_BAD_PREFIX = 64
 DEV_BAD_POSITION = 128
+DEV_NO_BLOCKS, DEV_BAD_TOKEN, DEV_BAD_PROB = 256, 512, 1024
 
 DEFAULT_PARTITION_SIZE = 512
 
@@ -104,6 +108,15 @@ def lib() -> ctypes.CDLL:
         L.pa_sparse_decode_workspace_bytes.restype = S
         L.pa_sparse_decode.argtypes = [P, P, P, P, P, P, I, P, I, I, I, I, I, I64, I, F, I, I, I, P,
                                        I, I, F, F, P, S, P, P]
+        L.pa_extend_tables.argtypes = [P, I, P, P, I, P, P, I64, I, P, P, I64, P, P, P, P, P]
+        L.pa_trim_tables.argtypes = [P, I, P, P, I, P, P, I64, I, P, P, P, P, P]
+        L.pa_scaled_append.argtypes = [P, I64, P, I64, P, P, P, P, P, I, P, P, I64, I, I, I, I, I,
+                                       I64, I, I, P, P]
+        L.pa_scaled_attention_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+        L.pa_scaled_attention_workspace_bytes.restype = S
+        L.pa_scaled_attention.argtypes = [P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I64, I,
+                                          F, I, I, P, S, P, P]
+        L.pa_verify_drafts.argtypes = [P, P, P, P, I64, I64, P, I64, P, P, P, I, I, I, P, P]
         L.pa_copy_blocks.argtypes = [P, P, P, I64, I, I, I, I64, I, P, P]
         L.pa_selftest_wait.argtypes = [I, P, P]
         L.pa_allocator_create.argtypes = [I64, I, I]
@@ -138,6 +151,8 @@ def lib() -> ctypes.CDLL:
                      "pa_decode_choose", "pa_decode_partition_size", "pa_version",
                      "pa_shared_prefix_plan", "pa_write_decode_shared_prefix",
                      "pa_rope_and_cache", "pa_key_bounds", "pa_sparse_decode",
+                     "pa_extend_tables", "pa_trim_tables", "pa_scaled_append",
+                     "pa_scaled_attention", "pa_verify_drafts",
                      "pa_copy_blocks", "pa_selftest_wait", "pa_allocator_allocate", "pa_allocator_fork",
                      "pa_allocator_free", "pa_allocator_append_slot"):
             getattr(L, name).restype = ctypes.c_int
@@ -488,6 +503,8 @@ def _native():
         C = torch._C
         module.bind(address(L.pa_rope_and_cache), address(L.pa_key_bounds), address(L.pa_sparse_decode),
                     C._cuda_getCurrentRawStream, C._cuda_getDevice, C._cuda_exchangeDevice)
+        module.bind_step(address(L.pa_extend_tables), address(L.pa_trim_tables), address(L.pa_scaled_append),
+                         address(L.pa_scaled_attention), address(L.pa_verify_drafts))
         _marshal = module
     return _marshal
 
@@ -553,6 +570,88 @@ def sparse_decode(out, query, k_cache, v_cache, k_bounds, block_tables, context_
         out, query, k_cache, v_cache, k_bounds, block_tables, context_lens, max_context_len, scale,
         num_select, workspace, first_blocks, recent_blocks, selected, k_scale, v_scale, dev_status,
         stream), "pa_sparse_decode")
+
+
+# ------------------------------------------------- a step that does not wait for the host
+
+def extend_tables(block_tables, context_lens, new_tokens, free_blocks, num_free, slot_mapping,
+                  query_start, block_size, positions=None, new_lens=None, new_num_free=None,
+                  dev_status=None, stream=None) -> None:
+    """new_tokens[s] (int32 [S]) tokens more for every request, on the device: the
+    blocks they need are taken from the top of free_blocks (int32, the first
+    num_free[0] entries are free) into block_tables; slot_mapping and positions
+    (int64 [max_tokens]) receive the new tokens' slots (-1 behind the last) and
+    positions, query_start (int32 [S + 1]) where each request's begin. Lengths and
+    the free count are updated in place, or go to new_lens and new_num_free. A
+    request that the stack cannot serve gets no token (DEV_NO_BLOCKS)."""
+    _check((_marshal or _native()).extend_tables(
+        block_tables, context_lens, new_tokens, free_blocks, num_free, slot_mapping, query_start,
+        block_size, positions, new_lens, new_num_free, dev_status, stream), "pa_extend_tables")
+
+
+def trim_tables(block_tables, context_lens, drop_tokens, free_blocks, num_free, block_size,
+                shared_blocks=None, new_lens=None, new_num_free=None, dev_status=None,
+                stream=None) -> None:
+    """Drop the newest drop_tokens[s] (int32 [S]) tokens of every request and put
+    the blocks that fall empty back on the stack of free ones (but for the first
+    shared_blocks[s]). Lengths and the free count as in extend_tables."""
+    _check((_marshal or _native()).trim_tables(
+        block_tables, context_lens, drop_tokens, free_blocks, num_free, block_size, shared_blocks,
+        new_lens, new_num_free, dev_status, stream), "pa_trim_tables")
+
+
+def scaled_append(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                  max_new_tokens=1, query_start=None, dev_status=None, stream=None) -> None:
+    """The KV write into a cache of 8-bit codes (E4M3, or torch.int8) with a scale
+    for each (block, KV head), float32 [num_blocks, Hkv]: the newest tokens of each
+    context, rows query_start[s].. of key/value [T, Hkv, d] (None: row s, one token
+    each). A scale follows its block's largest magnitude; where it grows, the
+    block's older codes are rounded anew. key and value may be views with any token
+    stride."""
+    _check((_marshal or _native()).scaled_append(
+        key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_new_tokens,
+        query_start, dev_status, stream), "pa_scaled_append")
+
+
+def scaled_workspace_bytes(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
+                           max_queries_per_seq, max_context_len) -> int:
+    return int(lib().pa_scaled_attention_workspace_bytes(
+        num_seqs, num_queries, num_q_heads, num_kv_heads, head_size, int(max_queries_per_seq),
+        int(max_context_len)))
+
+
+def alloc_scaled_workspace(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
+                           max_queries_per_seq, max_context_len, device=None) -> torch.Tensor:
+    n = scaled_workspace_bytes(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
+                               max_queries_per_seq, max_context_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def scaled_attention(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                     max_context_len, scale, workspace, query_start=None, max_queries_per_seq=1,
+                     dev_status=None, stream=None) -> None:
+    """Causal attention over a block-scaled cache into `out` ([T, Hq, d] like
+    `query`): the tokens of sequence s, rows query_start[s]..query_start[s+1]-1, are
+    the last positions of its context. query_start None: one query token each (the
+    decode; an empty context gives zeros). workspace: alloc_scaled_workspace of the
+    same sizes, one for each call in flight."""
+    _check((_marshal or _native()).scaled_attention(
+        out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len,
+        scale, workspace, query_start, max_queries_per_seq, dev_status, stream), "pa_scaled_attention")
+
+
+def verify_drafts(out_tokens, accepted, target_probs, draft_tokens, uniforms, query_start,
+                  draft_probs=None, rejected=None, dev_status=None, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities and draw the token
+    after them, from given random numbers. target_probs float32 [T, V]: rows
+    query_start[s].. of request s, one more than it has drafts; draft_tokens int64
+    [S, K], draft_probs float32 [S, K, V] (None: drafts that were not sampled);
+    uniforms float32 [S, K + 1], one for each draft and the last for the draw.
+    out_tokens int64 [S, K + 1]: accepted drafts, the drawn token, -1; accepted and
+    rejected (optional) int32 [S]."""
+    _check((_marshal or _native()).verify_drafts(
+        out_tokens, accepted, target_probs, draft_tokens, uniforms, query_start, draft_probs,
+        rejected, dev_status, stream), "pa_verify_drafts")
 
 
 STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024
@@ -622,6 +721,8 @@ def copy_blocks(k_cache, v_cache, block_pairs, dev_status=None, stream=None) -> 
     """Copy whole blocks for each (src, dst) row of block_pairs ([n, 2] int64,
     on the device): the copy of copy-on-write. Their key bounds are recomputed by
     key_bounds, with new_tokens reaching back to the first copied block."""
+    if k_cache.dtype == torch.int8:                     # codes: the copy is one of bytes
+        k_cache, v_cache = k_cache.view(torch.uint8), v_cache.view(torch.uint8)
     nb, H, B, D = k_cache.shape
     if block_pairs.dtype != torch.int64 or block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("block_pairs must be int64 [n, 2]")

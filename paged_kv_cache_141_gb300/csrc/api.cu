@@ -91,6 +91,73 @@ Layout workspace_layout(int num_seqs, int num_q_heads, int head_size, int max_co
     return l;
 }
 
+// Caches of 8-bit codes with a scale for each block and KV head.
+bool is_scaled_type(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_INT8; }
+
+constexpr int kMaxScaledContext = 1 << 30;    // positions plus a partition stay in 32 bits
+
+struct ScaledPlan {
+    int tile_rows, row_tiles, partition_size, max_parts;
+    size_t max_logits, exp_sums, total;       // the partials' start at 0; total 0: none
+};
+
+// The split of a call's work: the query rows of a CTA (the smallest n-tiles that hold a
+// sequence's; 32 at most, 16 at head size 256, whose accumulators fill the registers), and
+// partitions of the context where the sequences, heads and row tiles alone do not give
+// every SM some four CTAs.
+ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_kv_heads,
+                       int head_size, int max_queries, int max_context_len) {
+    ScaledPlan l{};
+    const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
+    l.tile_rows = rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32);
+    const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
+    l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);
+    const int64_t units = (int64_t)num_seqs * num_kv_heads * tiles;
+    const int64_t want = 8 * 152;
+    int64_t parts = (want + units - 1) / units;
+    int64_t size = (max_context_len + parts - 1) / parts;
+    if (tiles == 1 && size > 4096) size = 4096;             // one sequence's length does not hold up the rest
+    size = size < 256 ? 256 : (size + 127) / 128 * 128;
+    l.partition_size = (int)size;
+    parts = (max_context_len + size - 1) / size;
+    l.max_parts = parts < 1 ? 1 : (int)parts;
+    if (l.max_parts > 1) {
+        const size_t n = (size_t)num_queries * num_q_heads * l.max_parts;
+        l.max_logits = align256(n * head_size * sizeof(float));
+        l.exp_sums = l.max_logits + align256(n * sizeof(float));
+        l.total = l.exp_sums + align256(n * sizeof(float));
+    }
+    return l;
+}
+
+// What the calls on block tables share.
+pa_status check_tables(TablesParams& p, const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* counts, int num_seqs,
+                       const int32_t* free_blocks, const int32_t* num_free, int64_t free_capacity,
+                       int block_size, int32_t* new_lens, int32_t* new_num_free, uint32_t* dev_status) {
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || block_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > kMaxTableSeqs || block_size > 1024 || free_capacity > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (!num_free || !new_num_free || (free_capacity > 0 && !free_blocks)) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!context_lens || !counts || !new_lens || (max_blocks_per_seq > 0 && !block_tables)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(counts, 4) || !aligned(free_blocks, 4) ||
+        !aligned(num_free, 4) || !aligned(new_lens, 4) || !aligned(new_num_free, 4))
+        return PA_ERR_INVALID_ARG;
+    p.context_lens = context_lens;
+    p.new_tokens = counts;
+    p.free_blocks = free_blocks;
+    p.num_free = num_free;
+    p.new_lens = new_lens;
+    p.new_num_free = new_num_free;
+    p.status = dev_status;
+    p.free_capacity = free_capacity;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.block_size = block_size;
+    return PA_OK;
+}
+
 pa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
 // Shared validation of the decode arguments. Fills `p` on success.
@@ -1038,6 +1105,218 @@ pa_status pa_sparse_decode(void* out, const void* query, const void* k_cache, co
             return st;
     }
     return PA_OK;
+}
+
+pa_status pa_extend_tables(int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* new_tokens, int num_seqs,
+                           const int32_t* free_blocks, const int32_t* num_free,
+                           int64_t free_capacity, int block_size, int64_t* slot_mapping,
+                           int64_t* positions, int64_t max_tokens, int32_t* query_start,
+                           int32_t* new_lens, int32_t* new_num_free, uint32_t* dev_status,
+                           void* stream) {
+    TablesParams p{};
+    const pa_status st = check_tables(p, block_tables, max_blocks_per_seq, context_lens, new_tokens,
+                                      num_seqs, free_blocks, num_free, free_capacity, block_size,
+                                      new_lens, new_num_free, dev_status);
+    if (st != PA_OK) return st;
+    if (max_tokens < 0 || !query_start || (max_tokens > 0 && !slot_mapping)) return PA_ERR_INVALID_ARG;
+    if (!aligned(query_start, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 8)) return PA_ERR_INVALID_ARG;
+    if (max_tokens > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    p.block_tables = block_tables;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.max_tokens = max_tokens;
+    p.query_start = query_start;
+    return from_cuda(launch_tables(p, true, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_trim_tables(const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* drop_tokens, int num_seqs,
+                         int32_t* free_blocks, const int32_t* num_free, int64_t free_capacity,
+                         int block_size, const int32_t* shared_blocks, int32_t* new_lens,
+                         int32_t* new_num_free, uint32_t* dev_status, void* stream) {
+    TablesParams p{};
+    const pa_status st = check_tables(p, block_tables, max_blocks_per_seq, context_lens, drop_tokens,
+                                      num_seqs, free_blocks, num_free, free_capacity, block_size,
+                                      new_lens, new_num_free, dev_status);
+    if (st != PA_OK) return st;
+    if (!aligned(shared_blocks, 4)) return PA_ERR_INVALID_ARG;
+    p.block_tables = const_cast<int32_t*>(block_tables);           // read only
+    p.shared_blocks = shared_blocks;
+    p.stack = free_blocks;
+    return from_cuda(launch_tables(p, false, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* value,
+                           int64_t value_stride, void* k_cache, void* v_cache, float* k_scales,
+                           float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, const int32_t* query_start,
+                           int64_t num_tokens, int max_new_tokens, int num_seqs, int num_kv_heads,
+                           int head_size, int block_size, int64_t num_blocks, pa_dtype in_dtype,
+                           pa_dtype cache_dtype, uint32_t* dev_status, void* stream) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0 ||
+        max_blocks_per_seq < 0 || num_tokens < 0 || max_new_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!query_start && (max_new_tokens != 1 || num_tokens != num_seqs)) return PA_ERR_INVALID_ARG;
+    if ((int)in_dtype < 0 || (int)in_dtype > 4 || (int)cache_dtype < 0 || (int)cache_dtype > 4)
+        return PA_ERR_INVALID_ARG;
+    if (!is_compute_type(in_dtype) || !is_scaled_type(cache_dtype) || !supported_head_size(head_size) ||
+        block_size > 1024 || num_seqs > 65535)
+        return PA_ERR_UNSUPPORTED;
+    const int64_t row = (int64_t)num_kv_heads * head_size, in = elem_bytes(in_dtype);
+    if (num_tokens > 1 && (key_stride < row || value_stride < row)) return PA_ERR_INVALID_ARG;
+    if (key_stride * in % 16 != 0 || value_stride * in % 16 != 0) return PA_ERR_INVALID_ARG;
+    if (max_new_tokens > num_tokens) max_new_tokens = (int)num_tokens;
+    const int64_t touched = max_new_tokens == 0 ? 0 : ((int64_t)max_new_tokens + block_size - 2) / block_size + 1;
+    if (touched * 2 * num_kv_heads > kMaxBoundsUnits) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || touched == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens ||
+        max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(key, value, k_cache, v_cache) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    ScaledAppendParams p{};
+    p.key = key;
+    p.value = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.status = dev_status;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.num_blocks = num_blocks;
+    p.num_tokens = num_tokens;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.max_new_tokens = max_new_tokens;
+    p.touched = (int)touched;
+    return from_cuda(launch_scaled_append(p, head_size, in_dtype, cache_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_scaled_attention_workspace_bytes(int num_seqs, int num_queries, int num_q_heads,
+                                           int num_kv_heads, int head_size,
+                                           int max_queries_per_seq, int max_context_len) {
+    if (num_seqs <= 0 || num_queries <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || !supported_head_size(head_size) ||
+        max_queries_per_seq <= 0 || max_context_len <= 0 || max_context_len > kMaxScaledContext)
+        return 0;
+    return scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
+                       max_queries_per_seq, max_context_len).total;
+}
+
+pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
+                              const void* v_cache, const float* k_scales, const float* v_scales,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, const int32_t* query_start,
+                              int num_queries, int max_queries_per_seq, int num_seqs,
+                              int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                              int64_t num_blocks, int max_context_len, float scale,
+                              pa_dtype q_dtype, pa_dtype cache_dtype, void* workspace,
+                              size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+    if (num_seqs < 0 || num_queries < 0 || max_queries_per_seq < 0 || num_q_heads <= 0 ||
+        num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0 ||
+        max_blocks_per_seq < 0 || max_context_len < 0 || num_q_heads % num_kv_heads != 0)
+        return PA_ERR_INVALID_ARG;
+    if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+    if (!query_start && (max_queries_per_seq != 1 || num_queries != num_seqs)) return PA_ERR_INVALID_ARG;
+    if ((int)q_dtype < 0 || (int)q_dtype > 4 || (int)cache_dtype < 0 || (int)cache_dtype > 4)
+        return PA_ERR_INVALID_ARG;
+    if (!(q_dtype == PA_F16 || q_dtype == PA_BF16) || !is_scaled_type(cache_dtype) ||
+        !supported_head_size(head_size) || block_size > 1024 || num_seqs > 65535 ||
+        max_context_len > kMaxScaledContext)
+        return PA_ERR_UNSUPPORTED;
+    if (num_queries == 0) return PA_OK;
+    if (num_seqs == 0 || max_queries_per_seq == 0) return PA_ERR_INVALID_ARG;
+    if (!out || !query || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables ||
+        !context_lens || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out, query, k_cache, v_cache) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    if (max_queries_per_seq > num_queries) max_queries_per_seq = num_queries;
+    const ScaledPlan l = scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
+                                     max_queries_per_seq, max_context_len);
+    if ((int64_t)num_kv_heads * l.row_tiles > 65535 || max_queries_per_seq > 65535) return PA_ERR_UNSUPPORTED;
+    if (l.total > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total)) return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    ScaledAttnParams p{};
+    p.out = out;
+    p.query = query;
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    if (l.total > 0) {
+        p.tmp_out = reinterpret_cast<float*>(w);
+        p.max_logits = reinterpret_cast<float*>(w + l.max_logits);
+        p.exp_sums = reinterpret_cast<float*>(w + l.exp_sums);
+    }
+    p.status = dev_status;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_queries = num_queries;
+    p.max_queries = max_queries_per_seq;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.max_context_len = max_context_len;
+    p.partition_size = l.partition_size;
+    p.max_parts = l.max_parts;
+    p.tile_rows = l.tile_rows;
+    p.row_tiles = l.row_tiles;
+    p.q_mul = scale * 1.4426950408889634f;
+    p.bf16 = q_dtype == PA_BF16;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return from_cuda(cache_dtype == PA_INT8 ? launch_scaled_attention_int8(p, head_size, cs)
+                                            : launch_scaled_attention_e4m3(p, head_size, cs));
+}
+
+pa_status pa_verify_drafts(int64_t* out_tokens, int32_t* accepted, int32_t* rejected,
+                           const float* target_probs, int64_t target_stride, int64_t num_rows,
+                           const float* draft_probs, int64_t draft_stride,
+                           const int64_t* draft_tokens, const float* uniforms,
+                           const int32_t* query_start, int num_seqs, int max_drafts, int vocab,
+                           uint32_t* dev_status, void* stream) {
+    if (num_seqs < 0 || max_drafts < 0 || vocab <= 0 || num_rows < 0 || target_stride < vocab ||
+        (draft_probs && max_drafts > 0 && draft_stride < vocab))
+        return PA_ERR_INVALID_ARG;
+    if (vocab > kMaxVerifyVocab || num_seqs > 65535 || max_drafts > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!out_tokens || !accepted || !uniforms || !query_start || (num_rows > 0 && !target_probs) ||
+        (max_drafts > 0 && !draft_tokens))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(out_tokens, 8) || !aligned(draft_tokens, 8) || !aligned(accepted, 4) || !aligned(rejected, 4) ||
+        !aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(uniforms, 4) || !aligned(query_start, 4))
+        return PA_ERR_INVALID_ARG;
+    VerifyParams p{};
+    p.out_tokens = out_tokens;
+    p.accepted = accepted;
+    p.rejected = rejected;
+    p.target_probs = target_probs;
+    p.draft_probs = draft_probs;
+    p.draft_tokens = draft_tokens;
+    p.uniforms = uniforms;
+    p.query_start = query_start;
+    p.status = dev_status;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.num_rows = num_rows;
+    p.num_seqs = num_seqs;
+    p.max_drafts = max_drafts;
+    p.vocab = vocab;
+    return from_cuda(launch_verify_drafts(p, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* block_pairs,

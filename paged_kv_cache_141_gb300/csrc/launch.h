@@ -278,4 +278,115 @@ cudaError_t launch_reshape_and_cache(const void* key, const void* value, void* k
                                      float k_scale, float v_scale, uint32_t* status,
                                      cudaStream_t stream);
 
+// Block tables and slot maps from request lengths (step_tables.cu). The sums over the
+// requests stand in shared memory, 12 bytes each.
+constexpr int kMaxTableSeqs = 16384;
+struct TablesParams {
+    int32_t* block_tables;        // [S, max_blocks]; trim reads it
+    const int32_t* context_lens;  // [S]
+    const int32_t* new_tokens;    // [S]; trim: dropped tokens
+    const int32_t* shared_blocks; // trim: [S] leading blocks that stay out of the stack; may be null
+    const int32_t* free_blocks;   // [free_capacity]
+    int32_t* stack;               // the same, for trim
+    const int32_t* num_free;      // [1]
+    int64_t* slot_mapping;        // [max_tokens]
+    int64_t* positions;           // [max_tokens]; may be null
+    int32_t* query_start;         // [S + 1]
+    int32_t* new_lens;            // [S]
+    int32_t* new_num_free;        // [1]
+    uint32_t* status;             // may be null
+    int64_t free_capacity;
+    int64_t max_tokens;
+    int max_blocks;
+    int num_seqs;
+    int block_size;
+};
+
+cudaError_t launch_tables(const TablesParams& p, bool extend, cudaStream_t stream);
+
+// The KV write into block-scaled codes (scaled_append.cu).
+struct ScaledAppendParams {
+    const void* key;              // [num_tokens][Hkv][D], rows key_stride apart
+    const void* value;
+    void* k_cache;                // [num_blocks, Hkv, B, D] codes
+    void* v_cache;
+    float* k_scales;              // [num_blocks, Hkv]
+    float* v_scales;
+    const int32_t* block_tables;  // [S, max_blocks]
+    const int32_t* context_lens;  // [S]
+    const int32_t* query_start;   // [S + 1]; null: one token each
+    uint32_t* status;             // may be null
+    int64_t key_stride;           // elements between tokens
+    int64_t value_stride;
+    int64_t num_blocks;
+    int64_t num_tokens;
+    int max_blocks;
+    int num_seqs;
+    int num_kv_heads;
+    int block_size;
+    int max_new_tokens;
+    int touched;                  // blocks that max_new_tokens can touch
+};
+
+cudaError_t launch_scaled_append(const ScaledAppendParams& p, int head_size, pa_dtype in_dtype,
+                                 pa_dtype cache_dtype, cudaStream_t stream);
+
+// Attention over block-scaled codes (scaled_attention.cuh).
+struct ScaledAttnParams {
+    void* out;                    // [num_queries, Hq, D]
+    const void* query;
+    const uint8_t* k_cache;       // [num_blocks, Hkv, B, D] codes
+    const uint8_t* v_cache;
+    const float* k_scales;        // [num_blocks, Hkv]
+    const float* v_scales;
+    const int32_t* block_tables;  // [S, max_blocks]
+    const int32_t* context_lens;  // [S]
+    const int32_t* query_start;   // [S + 1]; null: one query each
+    float* tmp_out;               // several partitions: [num_queries, Hq, max_parts, D]
+    float* max_logits;            // [num_queries, Hq, max_parts], base 2
+    float* exp_sums;
+    uint32_t* status;             // may be null
+    int64_t num_blocks;
+    int max_blocks;
+    int num_seqs;
+    int num_queries;
+    int max_queries;              // most query tokens of a sequence
+    int num_q_heads;
+    int num_kv_heads;
+    int group;
+    int block_size;
+    int max_context_len;
+    int partition_size;           // a multiple of 32
+    int max_parts;
+    int tile_rows;                // query rows of a CTA: 8, 16 or 32
+    int row_tiles;                // CTAs that share a sequence's rows
+    float q_mul;                  // scale * log2(e)
+    int bf16;                     // the query's and the output's type; else binary16
+};
+
+cudaError_t launch_scaled_attention_int8(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_scaled_attention_e4m3(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+
+// Draft verification (verify_drafts.cu).
+constexpr int kMaxVerifyVocab = 1 << 22;      // the tiles' sums in shared memory
+struct VerifyParams {
+    int64_t* out_tokens;          // [S, max_drafts + 1]
+    int32_t* accepted;            // [S]
+    int32_t* rejected;            // [S]; may be null
+    const float* target_probs;    // [num_rows] rows of `vocab`, target_stride apart
+    const float* draft_probs;     // [S * max_drafts] rows; may be null
+    const int64_t* draft_tokens;  // [S, max_drafts]
+    const float* uniforms;        // [S, max_drafts + 1]
+    const int32_t* query_start;   // [S + 1]
+    uint32_t* status;             // may be null
+    int64_t target_stride;
+    int64_t draft_stride;
+    int64_t num_rows;
+    int num_seqs;
+    int max_drafts;
+    int vocab;
+};
+
+cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream);
+
 }  // namespace pagedkv

@@ -1,0 +1,256 @@
+// verify_drafts.cu -- verification of drafted tokens against the target's
+// probabilities, by given random numbers. Draft i of a request, token x_i drawn
+// with probability q_i(x_i), is accepted while
+//     u_i q_i(x_i) < p_i(x_i)
+// holds for it and for all before it (the products in binary64, where they are
+// exact). After a accepted drafts one more token is drawn: from the part of p_a
+// that lies beyond q_a, w_j = max(p_a(j) - q_a(j), 0), where a draft was
+// rejected (w = p_a where nothing lies beyond), or from w = p_a after the last
+// draft; this makes the tokens' distribution the target's. The drawn token is the
+// first j with w_0 + .. + w_j > u W, W the sum of all.
+//
+// The accept tests read one value of each row; the work is one row of p and of q
+// for each request, read once: HBM-bound for a batch, latency for one request. A
+// cluster of CTAs takes a request, each CTA a contiguous section of the row in
+// tiles of 512, a warp a tile, whose sum stays in shared memory. The CTAs trade their
+// totals, the one whose section holds u W finds the tile among its sums, and one warp
+// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-44: a lane's 16
+// values as a pair of binary32 numbers, lanes and tiles in binary64 (whose units would
+// take five times as long as the reads for every value). With 100,000 borders between
+// tokens, sums to 2^-30 alone would draw another token in one request of 5,000.
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+#include "launch.h"
+
+namespace pagedkv {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyTile = 512;
+constexpr int kVerifyPer = kVerifyTile / 32;       // of a tile, a lane's values
+constexpr int kVerifyCluster = 8;
+
+// Row weights: p alone, p beyond q, or p without one token.
+struct Weights {
+    const float* p;
+    const float* q;                                // may be null
+    int64_t without;                               // -1: none
+};
+
+// This lane's values of the tile at `at`: elements 32 i + lane, i < 16; zeros past the row.
+__device__ __forceinline__ void load_tile(const Weights& w, int64_t at, int64_t V, int lane, float (&a)[kVerifyPer],
+                                          float (&b)[kVerifyPer]) {
+#pragma unroll
+    for (int i = 0; i < kVerifyPer; ++i) {
+        const int64_t j = at + 32 * i + lane;
+        a[i] = j < V && j != w.without ? w.p[j] : 0.f;
+        b[i] = w.q && j < V ? w.q[j] : 0.f;
+    }
+}
+
+// Their sum, max(a - b, 0) each, as a pair of binary32 numbers: the differences and the
+// sums keep their rounding errors, so that the pair is within 2^-44 of the sum. A NaN stays.
+__device__ __forceinline__ double lane_sum(const float (&a)[kVerifyPer], const float (&b)[kVerifyPer]) {
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVerifyPer; ++i) {
+        float d = a[i] - b[i];
+        float e = (a[i] - d) - b[i];                               // exact for a >= b >= 0
+        if (d <= 0.f) d = e = 0.f;
+        const float s = hi + d, t = s - hi;
+        lo += ((hi - (s - t)) + (d - t)) + e;
+        hi = s;
+    }
+    return (double)hi + (double)lo;
+}
+
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
+__global__ void __launch_bounds__(kVerifyThreads)
+verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
+    begin_overlapped();
+    extern __shared__ double tile_sums[];
+    __shared__ int s_accepted;
+    __shared__ double s_part[kVerifyWarps];
+    __shared__ double s_totals[kVerifyCluster];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int s = blockIdx.x / ranks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = p.max_drafts;
+    const int64_t V = p.vocab;
+    int64_t* out = p.out_tokens + (size_t)s * (K + 1);
+    const int64_t row0 = p.query_start[s], rows = p.query_start[s + 1] - row0;
+    const bool bad = rows < 0 || rows > K + 1 || row0 < 0 || row0 + rows > p.num_rows;
+    if (bad || rows == 0) {                        // every CTA of the cluster alike
+        if (rank == 0) {
+            for (int i = threadIdx.x; i <= K; i += kVerifyThreads) out[i] = -1;
+            if (threadIdx.x == 0) {
+                p.accepted[s] = 0;
+                if (p.rejected) p.rejected[s] = 0;
+                if (bad && p.status) atomicOr(p.status, PA_DEV_BAD_LEN);
+            }
+        }
+        return;
+    }
+    const int n = (int)rows - 1;
+    if (warp == 0) {
+        int a = n;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            bool fine = true;
+            if (i < n) {
+                const int64_t x = p.draft_tokens[(size_t)s * K + i];
+                if (x < 0 || x >= V) {
+                    fine = false;
+                    if (rank == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_TOKEN);
+                } else {
+                    const double q = p.draft_probs ? p.draft_probs[((size_t)s * K + i) * p.draft_stride + x] : 1.f;
+                    const double t = p.target_probs[(row0 + i) * p.target_stride + x];
+                    fine = (double)p.uniforms[(size_t)s * (K + 1) + i] * q < t;
+                }
+            }
+            const uint32_t no = __ballot_sync(0xffffffffu, !fine);
+            if (no) {
+                a = i0 + __ffs(no) - 1;
+                break;
+            }
+        }
+        if (lane == 0) s_accepted = a;
+    }
+    __syncthreads();
+    const int a = s_accepted;
+    Weights w{p.target_probs + (row0 + a) * p.target_stride, nullptr, -1};
+    if (a < n) {
+        if (p.draft_probs) w.q = p.draft_probs + ((size_t)s * K + a) * p.draft_stride;
+        else w.without = p.draft_tokens[(size_t)s * K + a];
+    }
+    auto started = cluster.barrier_arrive();       // every CTA of the cluster runs before its memory is written
+    bool first_pass = true;
+    const int tiles = (int)((V + kVerifyTile - 1) / kVerifyTile);
+    const int per = (tiles + ranks - 1) / ranks;
+    const int first = min(tiles, rank * per), mine = min(tiles, first + per) - first;
+    const double u = p.uniforms[(size_t)s * (K + 1) + K];
+    for (;;) {
+        double sum = 0;
+        for (int t = warp; t < mine; t += kVerifyWarps) {
+            float a[kVerifyPer], b[kVerifyPer];
+            load_tile(w, (int64_t)(first + t) * kVerifyTile, V, lane, a, b);
+            const double total = warp_sum(lane_sum(a, b));
+            if (lane == 0) tile_sums[t] = total;
+            sum += total;
+        }
+        if (lane == 0) s_part[warp] = sum;
+        if (first_pass) cluster.barrier_wait(std::move(started));
+        first_pass = false;
+        __syncthreads();
+        if (threadIdx.x < ranks) {
+            double c = 0;
+            for (int i = 0; i < kVerifyWarps; ++i) c += s_part[i];
+            cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = c;
+        }
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
+        double before = 0, total = 0;
+        for (int r = 0; r < ranks; ++r) {
+            if (r < rank) before += s_totals[r];
+            total += s_totals[r];
+        }
+        // nothing beyond q: from p itself (every CTA of the cluster alike)
+        if (total == 0 && (w.q || w.without >= 0)) {
+            w.q = nullptr;
+            w.without = -1;
+            if (ranks > 1) cluster.sync();         // the totals have been read
+            else __syncthreads();
+            continue;
+        }
+        const bool drawable = total > 0 && total < (double)INFINITY;
+        const double goal = u * total;
+        if (rank == 0 && threadIdx.x < 32) {
+            for (int i = lane; i <= K; i += 32)
+                if (i != a || !drawable) out[i] = i < a ? p.draft_tokens[(size_t)s * K + i] : -1;
+            if (lane == 0) {
+                p.accepted[s] = a;
+                if (p.rejected) p.rejected[s] = n - a;
+                if (!drawable && p.status) atomicOr(p.status, PA_DEV_BAD_PROB);
+            }
+        }
+        // the section of the goal: the last one with any weight that starts at or below it
+        int holder = -1;
+        double start = 0;
+        for (int r = 0; r < ranks; ++r) {
+            if (s_totals[r] > 0 && (holder < 0 || start <= goal)) holder = r;
+            start += s_totals[r];
+        }
+        if (!drawable || holder != rank || warp != 0) return;
+        // its tile, alike
+        int tile = -1;
+        double run = before, base = before;
+        for (int t0 = 0; t0 < mine; t0 += 32) {
+            const double v = t0 + lane < mine ? tile_sums[t0 + lane] : 0;
+            double up = v;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(0xffffffffu, up, m);
+                if (lane >= m) up += o;
+            }
+            const uint32_t here = __ballot_sync(0xffffffffu, v > 0 && run + (up - v) <= goal);
+            const uint32_t any = __ballot_sync(0xffffffffu, v > 0);
+            const int at = here ? 31 - __clz(here) : (tile < 0 && any ? __ffs(any) - 1 : -1);
+            if (at >= 0) {
+                tile = t0 + at;
+                base = run + __shfl_sync(0xffffffffu, up - v, at);
+            }
+            run += __shfl_sync(0xffffffffu, up, 31);
+        }
+        // and the token: the first whose sum passes the goal, or the tile's last with any weight
+        float x[kVerifyPer], y[kVerifyPer];
+        const int64_t at = (int64_t)(first + tile) * kVerifyTile;
+        load_tile(w, at, V, lane, x, y);
+        int64_t token = -1;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kVerifyPer; ++i) {
+            const double own = x[i] > y[i] ? (double)x[i] - (double)y[i] : 0;
+            double up = own;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(0xffffffffu, up, m);
+                if (lane >= m) up += o;
+            }
+            if (!found) {
+                const uint32_t past = __ballot_sync(0xffffffffu, own > 0 && base + up > goal);
+                const uint32_t any = __ballot_sync(0xffffffffu, own > 0);
+                if (past) token = at + 32 * i + __ffs(past) - 1;
+                else if (any) token = at + 32 * i + 31 - __clz(any);
+                found = past != 0;
+            }
+            base += __shfl_sync(0xffffffffu, up, 31);
+        }
+        if (lane == 0) out[a] = token;
+        return;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
+    const int tiles = (int)((p.vocab + kVerifyTile - 1) / kVerifyTile);
+    int cluster = 1;
+    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster < 304 && tiles > cluster * kVerifyWarps) cluster *= 2;
+    const int smem = (tiles + cluster - 1) / cluster * (int)sizeof(double);
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(verify_drafts_kernel), smem);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(verify_drafts_kernel, p, dim3(p.num_seqs * cluster), kVerifyThreads, smem, stream, cluster);
+}
+
+}  // namespace pagedkv

@@ -1,5 +1,6 @@
 // marshal.cpp -- the binding's argument marshalling for the calls of every
-// decode step (rope_and_cache, key_bounds, sparse_decode), as a Python module
+// decode step (rope_and_cache, key_bounds, sparse_decode; extend_tables, trim_tables,
+// scaled_append, scaled_attention, verify_drafts), as a Python module
 // against PyTorch's C++ headers. The checks and conversions are those a Python
 // function would make; read from the tensors directly they take a fraction of a
 // microsecond where attribute by attribute they took eight, several times the
@@ -25,6 +26,11 @@ struct PythonProblem {};                           // the Python error is set
 decltype(&pa_rope_and_cache) rope_fn = nullptr;
 decltype(&pa_key_bounds) bounds_fn = nullptr;
 decltype(&pa_sparse_decode) sparse_fn = nullptr;
+decltype(&pa_extend_tables) extend_fn = nullptr;
+decltype(&pa_trim_tables) trim_fn = nullptr;
+decltype(&pa_scaled_append) append_fn = nullptr;
+decltype(&pa_scaled_attention) attention_fn = nullptr;
+decltype(&pa_verify_drafts) verify_fn = nullptr;
 PyObject *stream_of = nullptr, *current_device = nullptr, *exchange_device = nullptr;
 
 [[noreturn]] void bad(const std::string& what) { throw std::invalid_argument(what); }
@@ -330,7 +336,232 @@ PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// The addresses of the three entry points, and PyTorch's raw getters: the
+// ---- a step that does not wait for the host
+
+const at::Tensor& ints(PyObject* o, const char* name, int64_t n) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != at::kInt || t.numel() != n) bad(std::string(name) + " must be int32 [" + std::to_string(n) + "]");
+    return t;
+}
+int32_t* int_data(PyObject* o, int dev, const char* name, int64_t n) {
+    ints(o, name, n);
+    return static_cast<int32_t*>(data(o, dev, name));
+}
+int32_t* int_data_or_null(PyObject* o, int dev, const char* name, int64_t n) {
+    return o == Py_None ? nullptr : int_data(o, dev, name, n);
+}
+int32_t* table_data(PyObject* o, int dev, int64_t S, int& max_blocks) {
+    const at::Tensor& t = tensor(o, "block_tables");
+    if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != S) bad("block_tables must be int32 [num_seqs, max_blocks]");
+    max_blocks = small_size(t.size(1));
+    return static_cast<int32_t*>(data(o, dev, "block_tables"));
+}
+int64_t* long_data(PyObject* o, int dev, const char* name) {
+    if (tensor(o, name).scalar_type() != at::kLong) bad(std::string(name) + " must be int64");
+    return static_cast<int64_t*>(data(o, dev, name));
+}
+
+// block_tables, context_lens, new_tokens, free_blocks, num_free, slot_mapping, query_start, block_size,
+// positions, new_lens, new_num_free, dev_status, stream
+PyObject* extend_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 13)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &cl = tensor(a[1], "context_lens"), &stack = tensor(a[3], "free_blocks"),
+                         &slots = tensor(a[5], "slot_mapping");
+        const int dev = index_of(cl);
+        const int S = small_size(cl.numel());
+        int mb;
+        int32_t* bt = table_data(a[0], dev, S, mb);
+        int32_t *len = int_data(a[1], dev, "context_lens", S), *more = int_data(a[2], dev, "new_tokens", S);
+        int32_t *sp = int_data(a[3], dev, "free_blocks", stack.numel()), *nf = int_data(a[4], dev, "num_free", 1);
+        int64_t* slp = long_data(a[5], dev, "slot_mapping");
+        int32_t* qs = int_data(a[6], dev, "query_start", (int64_t)S + 1);
+        int64_t* pos = a[8] == Py_None ? nullptr : long_data(a[8], dev, "positions");
+        const int64_t cap = stack.numel(), T = slots.numel();
+        if (pos && tensor(a[8], "positions").numel() != T) bad("positions must have slot_mapping's size");
+        int32_t *nl = a[9] == Py_None ? len : int_data(a[9], dev, "new_lens", S),
+                *nn = a[10] == Py_None ? nf : int_data(a[10], dev, "new_num_free", 1);
+        const int B = small(a[7]);
+        uint32_t* status = static_cast<uint32_t*>(data_or_null(a[11], dev, "dev_status"));
+        void* stream = stream_handle(a[12], dev);
+        return run(dev, [&] {
+            return extend_fn(bt, mb, len, more, S, sp, nf, cap, B, slp, pos, T, qs, nl, nn, status, stream);
+        });
+    });
+}
+
+// block_tables, context_lens, drop_tokens, free_blocks, num_free, block_size, shared_blocks, new_lens,
+// new_num_free, dev_status, stream
+PyObject* trim_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 11)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &cl = tensor(a[1], "context_lens"), &stack = tensor(a[3], "free_blocks");
+        const int dev = index_of(cl);
+        const int S = small_size(cl.numel());
+        int mb;
+        const int32_t* bt = table_data(a[0], dev, S, mb);
+        int32_t *len = int_data(a[1], dev, "context_lens", S), *drop = int_data(a[2], dev, "drop_tokens", S);
+        int32_t *sp = int_data(a[3], dev, "free_blocks", stack.numel()), *nf = int_data(a[4], dev, "num_free", 1);
+        const int32_t* shared = int_data_or_null(a[6], dev, "shared_blocks", S);
+        const int64_t cap = stack.numel();
+        int32_t *nl = a[7] == Py_None ? len : int_data(a[7], dev, "new_lens", S),
+                *nn = a[8] == Py_None ? nf : int_data(a[8], dev, "new_num_free", 1);
+        const int B = small(a[5]);
+        uint32_t* status = static_cast<uint32_t*>(data_or_null(a[9], dev, "dev_status"));
+        void* stream = stream_handle(a[10], dev);
+        return run(dev, [&] { return trim_fn(bt, mb, len, drop, S, sp, nf, cap, B, shared, nl, nn, status, stream); });
+    });
+}
+
+pa_dtype scaled_code(const at::Tensor& t) { return t.scalar_type() == at::kChar ? PA_INT8 : code_of(t); }
+
+// Caches of codes and their scales, as they lie.
+struct ScaledPool : Pool {
+    void *k, *v;
+    float *k_scales, *v_scales;
+    pa_dtype type;
+};
+ScaledPool scaled_pool(PyObject* const* a, int dev) {              // k_cache, v_cache, k_scales, v_scales
+    const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache"), &ks = tensor(a[2], "k_scales"),
+                     &vs = tensor(a[3], "v_scales");
+    ScaledPool p;
+    static_cast<Pool&>(p) = pool_of(kc);
+    if (!vc.sizes().equals(kc.sizes()) || vc.scalar_type() != kc.scalar_type())
+        bad("k_cache and v_cache must have one shape and dtype");
+    for (const at::Tensor* t : {&ks, &vs})
+        if (t->scalar_type() != at::kFloat || t->dim() != 2 || t->size(0) != p.blocks || t->size(1) != p.heads)
+            bad("k_scales and v_scales must be float32 [num_blocks, num_kv_heads]");
+    p.k = data(a[0], dev, "k_cache");
+    p.v = data(a[1], dev, "v_cache");
+    p.k_scales = static_cast<float*>(data(a[2], dev, "k_scales"));
+    p.v_scales = static_cast<float*>(data(a[3], dev, "v_scales"));
+    p.type = scaled_code(kc);
+    return p;
+}
+
+// key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_new_tokens, query_start,
+// dev_status, stream
+PyObject* scaled_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 12)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &k = tensor(a[0], "key"), &v = tensor(a[1], "value"), &cl = tensor(a[7], "context_lens");
+        const int dev = index_of(k);
+        const ScaledPool p = scaled_pool(a + 2, dev);
+        if (k.dim() != 3) bad("key must be [num_tokens, num_kv_heads, head_size]");
+        if (v.scalar_type() != k.scalar_type()) bad("key and value must share one dtype");
+        const int64_t T = k.size(0);
+        int64_t kst, vst;
+        const void *kp = token_rows(k, dev, T, p.heads, p.head, "key", kst),
+                   *vp = token_rows(v, dev, T, p.heads, p.head, "value", vst);
+        const int S = small_size(cl.numel());
+        int mb;
+        const int32_t* bt = table_data(a[6], dev, S, mb);
+        const int32_t* len = int_data(a[7], dev, "context_lens", S);
+        const int32_t* qs = int_data_or_null(a[9], dev, "query_start", (int64_t)S + 1);
+        const int most = small(a[8]);
+        uint32_t* status = static_cast<uint32_t*>(data_or_null(a[10], dev, "dev_status"));
+        const pa_dtype in = code_of(k);
+        void* stream = stream_handle(a[11], dev);
+        return run(dev, [&] {
+            return append_fn(kp, kst, vp, vst, p.k, p.v, p.k_scales, p.v_scales, bt, mb, len, qs, T, most, S, p.heads,
+                             p.head, p.block, p.blocks, in, p.type, status, stream);
+        });
+    });
+}
+
+// out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len, scale,
+// workspace, query_start, max_queries_per_seq, dev_status, stream
+PyObject* scaled_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 15)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &out = tensor(a[0], "out"), &q = tensor(a[1], "query"), &cl = tensor(a[7], "context_lens");
+        const int dev = index_of(q);
+        const ScaledPool p = scaled_pool(a + 2, dev);
+        if (q.dim() != 3 || q.size(2) != p.head) bad("query must be [num_queries, num_q_heads, head_size] of the cache's head size");
+        if (!out.sizes().equals(q.sizes()) || out.scalar_type() != q.scalar_type())
+            bad("out must have the query's shape and dtype");
+        const int T = small_size(q.size(0)), Hq = small_size(q.size(1)), S = small_size(cl.numel());
+        void* op = data(a[0], dev, "out");
+        const void* qp = data(a[1], dev, "query");
+        int mb;
+        const int32_t* bt = table_data(a[6], dev, S, mb);
+        const int32_t* len = int_data(a[7], dev, "context_lens", S);
+        const int32_t* qs = int_data_or_null(a[11], dev, "query_start", (int64_t)S + 1);
+        void* wsp = data_or_null(a[10], dev, "workspace");
+        const size_t ws_bytes = wsp ? tensor(a[10], "workspace").nbytes() : 0;
+        const int max_len = small(a[8]), most = small(a[12]);
+        const float scale = number(a[9]);
+        uint32_t* status = static_cast<uint32_t*>(data_or_null(a[13], dev, "dev_status"));
+        const pa_dtype qt = code_of(q);
+        void* stream = stream_handle(a[14], dev);
+        return run(dev, [&] {
+            return attention_fn(op, qp, p.k, p.v, p.k_scales, p.v_scales, bt, mb, len, qs, T, most, S, Hq, p.heads, p.head,
+                                p.block, p.blocks, max_len, scale, qt, p.type, wsp, ws_bytes, status, stream);
+        });
+    });
+}
+
+// Rows of a vocabulary, the last dimension contiguous and the others evenly spaced.
+const float* prob_rows(PyObject* o, int dev, const char* name, int64_t& rows, int64_t& vocab, int64_t& stride) {
+    const at::Tensor& t = tensor(o, name);
+    if (!t.is_cuda() || t.get_device() != dev) bad("all tensors must live on one CUDA device");
+    if (t.scalar_type() != at::kFloat || t.dim() < 2) bad(std::string(name) + " must be float32 rows of the vocabulary");
+    const int64_t d = t.dim();
+    vocab = t.size(d - 1);
+    rows = t.numel() == 0 ? 0 : t.numel() / vocab;
+    stride = t.size(d - 2) > 1 ? t.stride(d - 2) : (d == 3 && t.size(0) > 1 ? t.stride(0) : vocab);
+    if ((vocab > 1 && t.stride(d - 1) != 1) || (d == 3 && t.size(0) > 1 && t.stride(0) != t.size(1) * stride) || d > 3)
+        bad(std::string(name) + ": rows must be contiguous and evenly spaced");
+    return t.const_data_ptr<float>();
+}
+
+// out_tokens, accepted, target_probs, draft_tokens, uniforms, query_start, draft_probs, rejected, dev_status, stream
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 10)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &ot = tensor(a[0], "out_tokens"), &dt = tensor(a[3], "draft_tokens"), &u = tensor(a[4], "uniforms");
+        const int dev = index_of(tensor(a[2], "target_probs"));
+        if (dt.dim() != 2) bad("draft_tokens must be int64 [num_seqs, max_drafts]");
+        const int S = small_size(dt.size(0)), K = small_size(dt.size(1));
+        if (ot.dim() != 2 || ot.size(0) != S || ot.size(1) != (int64_t)K + 1) bad("out_tokens must be int64 [num_seqs, max_drafts + 1]");
+        if (u.scalar_type() != at::kFloat || u.dim() != 2 || u.size(0) != S || u.size(1) != (int64_t)K + 1)
+            bad("uniforms must be float32 [num_seqs, max_drafts + 1]");
+        int64_t rows, V, stride, drows, dV, dstride = 0;
+        const float* tp = prob_rows(a[2], dev, "target_probs", rows, V, stride);
+        const float* dp = nullptr;
+        if (a[6] != Py_None) {
+            dp = prob_rows(a[6], dev, "draft_probs", drows, dV, dstride);
+            if (dV != V || drows != (int64_t)S * K) bad("draft_probs must be [num_seqs, max_drafts] rows of the target's vocabulary");
+            if (drows <= 1) dstride = V;
+        }
+        if (rows <= 1) stride = V;
+        int64_t *otp = long_data(a[0], dev, "out_tokens"), *dtp = long_data(a[3], dev, "draft_tokens");
+        const float* up = static_cast<const float*>(data(a[4], dev, "uniforms"));
+        int32_t* acc = int_data(a[1], dev, "accepted", S);
+        const int32_t* qs = int_data(a[5], dev, "query_start", (int64_t)S + 1);
+        int32_t* rej = int_data_or_null(a[7], dev, "rejected", S);
+        const int vocab = small_size(V);
+        uint32_t* status = static_cast<uint32_t*>(data_or_null(a[8], dev, "dev_status"));
+        void* stream = stream_handle(a[9], dev);
+        return run(dev, [&] {
+            return verify_fn(otp, acc, rej, tp, stride, rows, dp, dstride, dtp, up, qs, S, K, vocab, status, stream);
+        });
+    });
+}
+
+// The addresses of the five entry points above.
+PyObject* bind_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (wrong_count(n, 5)) return nullptr;
+    extend_fn = reinterpret_cast<decltype(extend_fn)>(PyLong_AsVoidPtr(a[0]));
+    trim_fn = reinterpret_cast<decltype(trim_fn)>(PyLong_AsVoidPtr(a[1]));
+    append_fn = reinterpret_cast<decltype(append_fn)>(PyLong_AsVoidPtr(a[2]));
+    attention_fn = reinterpret_cast<decltype(attention_fn)>(PyLong_AsVoidPtr(a[3]));
+    verify_fn = reinterpret_cast<decltype(verify_fn)>(PyLong_AsVoidPtr(a[4]));
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+}
+
+// The addresses of the first three entry points, and PyTorch's raw getters: the
 // current stream of a device, the current device, and its exchange.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (wrong_count(n, 6)) return nullptr;
@@ -346,7 +577,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define PA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(bind), PA_METHOD(rope_and_cache), PA_METHOD(key_bounds),
-                         PA_METHOD(sparse_decode), {nullptr, nullptr, 0, nullptr}};
+                         PA_METHOD(sparse_decode), PA_METHOD(extend_tables), PA_METHOD(trim_tables),
+                         PA_METHOD(scaled_append), PA_METHOD(scaled_attention), PA_METHOD(verify_drafts),
+                         PA_METHOD(bind_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

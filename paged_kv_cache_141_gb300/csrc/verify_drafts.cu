@@ -14,9 +14,9 @@
 // cluster of CTAs takes a request, each CTA a contiguous section of the row in
 // tiles of 512, a warp a tile, whose sum stays in shared memory. The CTAs trade their
 // totals, the one whose section holds u W finds the tile among its sums, and one warp
-// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-44: a lane's 16
-// values as a pair of binary32 numbers, lanes and tiles in binary64 (whose units would
-// take five times as long as the reads for every value). With 100,000 borders between
+// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-44, as pairs of
+// binary32 numbers (binary64 units would take five times as long as the reads; binary64
+// across the lanes alone took 85 us where this takes 63 for 256 requests of 128,256 tokens). With 100,000 borders between
 // tokens, sums to 2^-30 alone would draw another token in one request of 5,000.
 #include <cooperative_groups.h>
 
@@ -29,7 +29,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyTile = 512;
 constexpr int kVerifyPer = kVerifyTile / 32;       // of a tile, a lane's values
@@ -53,34 +53,38 @@ __device__ __forceinline__ void load_tile(const Weights& w, int64_t at, int64_t 
     }
 }
 
-// Their sum, max(a - b, 0) each, as a pair of binary32 numbers: the differences and the
-// sums keep their rounding errors, so that the pair is within 2^-44 of the sum. A NaN stays.
-__device__ __forceinline__ double lane_sum(const float (&a)[kVerifyPer], const float (&b)[kVerifyPer]) {
-    float hi = 0.f, lo = 0.f;
+// A sum as an unevaluated pair of binary32 numbers.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair add(Pair x, Pair y) {
+    const float s = x.hi + y.hi, t = s - x.hi;
+    return {s, (x.lo + y.lo) + ((x.hi - (s - t)) + (y.hi - t))};
+}
+__device__ __forceinline__ double value(Pair x) { return (double)x.hi + (double)x.lo; }
+
+// The sum of max(a - b, 0) over the warp's values; the differences keep their rounding
+// errors, as the sums do. A NaN stays.
+__device__ __forceinline__ Pair tile_sum(const float (&a)[kVerifyPer], const float (&b)[kVerifyPer]) {
+    Pair x{0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kVerifyPer; ++i) {
         float d = a[i] - b[i];
         float e = (a[i] - d) - b[i];                               // exact for a >= b >= 0
         if (d <= 0.f) d = e = 0.f;
-        const float s = hi + d, t = s - hi;
-        lo += ((hi - (s - t)) + (d - t)) + e;
-        hi = s;
+        x = add(x, {d, e});
     }
-    return (double)hi + (double)lo;
-}
-
-__device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
-    for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    for (int m = 16; m; m >>= 1) x = add(x, {__shfl_xor_sync(0xffffffffu, x.hi, m), __shfl_xor_sync(0xffffffffu, x.lo, m)});
     return x;
 }
 
 __global__ void __launch_bounds__(kVerifyThreads)
 verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     begin_overlapped();
-    extern __shared__ double tile_sums[];
+    extern __shared__ Pair tile_sums[];
     __shared__ int s_accepted;
-    __shared__ double s_part[kVerifyWarps];
+    __shared__ Pair s_part[kVerifyWarps];
     __shared__ double s_totals[kVerifyCluster];
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -89,6 +93,10 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const int K = p.max_drafts;
     const int64_t V = p.vocab;
     int64_t* out = p.out_tokens + (size_t)s * (K + 1);
+    // the first drafts, next to the rows' starts
+    const int64_t token0 = warp == 0 && lane < K ? p.draft_tokens[(size_t)s * K + lane] : -1;
+    const float u0 = warp == 0 && lane < K ? p.uniforms[(size_t)s * (K + 1) + lane] : 0.f;
+    const double u = p.uniforms[(size_t)s * (K + 1) + K];
     const int64_t row0 = p.query_start[s], rows = p.query_start[s + 1] - row0;
     const bool bad = rows < 0 || rows > K + 1 || row0 < 0 || row0 + rows > p.num_rows;
     if (bad || rows == 0) {                        // every CTA of the cluster alike
@@ -109,14 +117,15 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
             const int i = i0 + lane;
             bool fine = true;
             if (i < n) {
-                const int64_t x = p.draft_tokens[(size_t)s * K + i];
+                const int64_t x = i0 ? p.draft_tokens[(size_t)s * K + i] : token0;
+                const double ui = i0 ? p.uniforms[(size_t)s * (K + 1) + i] : u0;
                 if (x < 0 || x >= V) {
                     fine = false;
                     if (rank == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_TOKEN);
                 } else {
                     const double q = p.draft_probs ? p.draft_probs[((size_t)s * K + i) * p.draft_stride + x] : 1.f;
                     const double t = p.target_probs[(row0 + i) * p.target_stride + x];
-                    fine = (double)p.uniforms[(size_t)s * (K + 1) + i] * q < t;
+                    fine = ui * q < t;
                 }
             }
             const uint32_t no = __ballot_sync(0xffffffffu, !fine);
@@ -139,24 +148,24 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const int tiles = (int)((V + kVerifyTile - 1) / kVerifyTile);
     const int per = (tiles + ranks - 1) / ranks;
     const int first = min(tiles, rank * per), mine = min(tiles, first + per) - first;
-    const double u = p.uniforms[(size_t)s * (K + 1) + K];
     for (;;) {
-        double sum = 0;
+        Pair sum{0.f, 0.f};
         for (int t = warp; t < mine; t += kVerifyWarps) {
             float a[kVerifyPer], b[kVerifyPer];
             load_tile(w, (int64_t)(first + t) * kVerifyTile, V, lane, a, b);
-            const double total = warp_sum(lane_sum(a, b));
+            const Pair total = tile_sum(a, b);
             if (lane == 0) tile_sums[t] = total;
-            sum += total;
+            sum = add(sum, total);
         }
         if (lane == 0) s_part[warp] = sum;
         if (first_pass) cluster.barrier_wait(std::move(started));
         first_pass = false;
         __syncthreads();
         if (threadIdx.x < ranks) {
-            double c = 0;
-            for (int i = 0; i < kVerifyWarps; ++i) c += s_part[i];
-            cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = c;
+            Pair c = s_part[0];
+#pragma unroll
+            for (int i = 1; i < kVerifyWarps; ++i) c = add(c, s_part[i]);
+            cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = value(c);
         }
         if (ranks > 1) cluster.sync();
         else __syncthreads();
@@ -196,7 +205,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
         int tile = -1;
         double run = before, base = before;
         for (int t0 = 0; t0 < mine; t0 += 32) {
-            const double v = t0 + lane < mine ? tile_sums[t0 + lane] : 0;
+            const double v = t0 + lane < mine ? value(tile_sums[t0 + lane]) : 0;
             double up = v;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -212,31 +221,33 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
             }
             run += __shfl_sync(0xffffffffu, up, 31);
         }
-        // and the token: the first whose sum passes the goal, or the tile's last with any weight
-        float x[kVerifyPer], y[kVerifyPer];
-        const int64_t at = (int64_t)(first + tile) * kVerifyTile;
-        load_tile(w, at, V, lane, x, y);
-        int64_t token = -1;
-        bool found = false;
+        // and the token: the first whose sum passes the goal, or the tile's last with any
+        // weight. A lane takes 16 neighbours.
+        const int64_t at = (int64_t)(first + tile) * kVerifyTile + lane * kVerifyPer;
+        double own[kVerifyPer], all = 0;
+        int last = -1;
 #pragma unroll
         for (int i = 0; i < kVerifyPer; ++i) {
-            const double own = x[i] > y[i] ? (double)x[i] - (double)y[i] : 0;
-            double up = own;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, up, m);
-                if (lane >= m) up += o;
-            }
-            if (!found) {
-                const uint32_t past = __ballot_sync(0xffffffffu, own > 0 && base + up > goal);
-                const uint32_t any = __ballot_sync(0xffffffffu, own > 0);
-                if (past) token = at + 32 * i + __ffs(past) - 1;
-                else if (any) token = at + 32 * i + 31 - __clz(any);
-                found = past != 0;
-            }
-            base += __shfl_sync(0xffffffffu, up, 31);
+            const float x = at + i < V && at + i != w.without ? w.p[at + i] : 0.f;
+            const float y = w.q && at + i < V ? w.q[at + i] : 0.f;
+            if (x > y) last = i;
+            all += x > y ? (double)x - (double)y : 0;
+            own[i] = all;
         }
-        if (lane == 0) out[a] = token;
+        double up = all;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, up, m);
+            if (lane >= m) up += o;
+        }
+        const double start_of = base + (up - all);
+        int here = kVerifyPer;
+#pragma unroll
+        for (int i = kVerifyPer - 1; i >= 0; --i)
+            if (start_of + own[i] > goal && own[i] > (i ? own[i - 1] : 0)) here = i;
+        const uint32_t past = __ballot_sync(0xffffffffu, here < kVerifyPer), any = __ballot_sync(0xffffffffu, last >= 0);
+        const int who = past ? __ffs(past) - 1 : 31 - __clz(any);
+        if (lane == who) out[a] = at + (past ? here : last);
         return;
     }
 }
@@ -246,8 +257,9 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
 cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
     const int tiles = (int)((p.vocab + kVerifyTile - 1) / kVerifyTile);
     int cluster = 1;
-    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster < 304 && tiles > cluster * kVerifyWarps) cluster *= 2;
-    const int smem = (tiles + cluster - 1) / cluster * (int)sizeof(double);
+    // (some four CTAs fit an SM)
+    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster <= 304 && tiles > cluster * kVerifyWarps) cluster *= 2;
+    const int smem = (tiles + cluster - 1) / cluster * (int)sizeof(Pair);
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(verify_drafts_kernel), smem);
     if (e != cudaSuccess) return e;
     return launch_overlapped(verify_drafts_kernel, p, dim3(p.num_seqs * cluster), kVerifyThreads, smem, stream, cluster);

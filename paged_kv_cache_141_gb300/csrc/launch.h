@@ -300,6 +300,7 @@ struct TablesParams {
     int max_blocks;
     int num_seqs;
     int block_size;
+    int slots_apart;              // set by the launcher: a second kernel makes the slots
 };
 
 cudaError_t launch_tables(const TablesParams& p, bool extend, cudaStream_t stream);
@@ -358,7 +359,7 @@ struct ScaledAttnParams {
     int max_context_len;
     int partition_size;           // a multiple of 32
     int max_parts;
-    int tile_rows;                // query rows of a CTA: 8, 16 or 32
+    int tile_rows;                // query rows of a CTA: 8, 16 or 32; 256: on the tcgen05 tensor cores
     int row_tiles;                // CTAs that share a sequence's rows
     float q_mul;                  // scale * log2(e)
     int bf16;                     // the query's and the output's type; else binary16

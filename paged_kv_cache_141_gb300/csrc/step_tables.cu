@@ -16,7 +16,9 @@
 // outputs may be the inputs' own memory, and then takes its share of the entries
 // and slots, one a thread, found by binary search over the sums. The work is
 // launch latency and two or three dependent loads; sums in a kernel of their own
-// would cost a launch more.
+// would cost a launch more. A prompt step's slots are too many for one cluster's
+// eight SMs (262,144 of them took 23 us): from kSlotsApart on a second kernel
+// fills the whole device with them, from the first one's outputs.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -30,6 +32,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kTablesThreads = 1024;
 constexpr int kTablesCluster = 8;
+constexpr int64_t kSlotsApart = 16384;             // slots from which they have a kernel of their own
 constexpr int64_t kMaxTableTokens = INT32_MAX - 1024;      // lengths round up to blocks in 32 bits
 
 // Sums of a and b over the CTA's threads before this one; totals in ta, tb.
@@ -66,16 +69,15 @@ __device__ __forceinline__ void scan_two(int64_t& a, int64_t& b, int64_t& ta, in
     b = ib - b + (warp ? pb : 0);
 }
 
-// The largest s in [0, n) with first[s] <= x; first[0] <= x.
-__device__ __forceinline__ int owner_of(const int32_t* first, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
+// The largest s in [0, n) with first[s] <= x; first[0] <= x. `top`: the largest power of
+// two below n (0 for n = 1).
+__device__ __forceinline__ int owner_of(const int32_t* first, int n, int top, int x) {
+    int s = 0;
+    for (int step = top; step; step >>= 1)
+        if (s + step < n && first[s + step] <= x) s += step;
+    return s;
 }
+__device__ __forceinline__ int top_step(int n) { return n > 1 ? 1 << (31 - __clz(n - 1)) : 0; }
 
 __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
     if (status) atomicOr(status, bit);
@@ -116,8 +118,7 @@ extend_tables_kernel(const __grid_constant__ TablesParams p) {
                 n = 0;
             }
         }
-        const int64_t held = (L + B - 1) / B;
-        const int64_t need = n ? (L + n + B - 1) / B - held : 0;
+        const int64_t need = n ? (int)(L + n + B - 1) / B - (int)(L + B - 1) / B : 0;
         int64_t a = n, b = need, ta, tb;
         scan_two(a, b, ta, tb, part);
         // a request is served if its blocks and its places in the slot map are there
@@ -128,20 +129,24 @@ extend_tables_kernel(const __grid_constant__ TablesParams p) {
         const int64_t got = blocks && places ? n : 0;
         // the sums over those served: the same ones where all are
         int64_t first = a, served = ta;
-        if (!__syncthreads_and(got == n)) {
+        const bool all = __syncthreads_and(got == n);
+        if (!all) {
             int64_t unused = 0, none;
             first = got;
             scan_two(first, unused, served, none, part);
         }
         // blocks are taken by a leading run of the requests that need any: the sums
         // before a served one count served ones alone
-        int64_t used = got && need ? needed + b + need : 0, most = used;
-#pragma unroll
-        for (int m = 16; m; m >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][0] = most;
-        __syncthreads();
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, part[w][0]);
+        if (all) {
+            if (tb) taken = needed + tb;
+        } else {
+            const int used = got && need ? (int)(needed + b + need) : 0;
+            const int most = __reduce_max_sync(0xffffffffu, used);
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][0] = most;
+            __syncthreads();
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, part[w][0]);
+        }
         if (s < S) {
             len[s] = (int32_t)L;
             tok[s] = (int32_t)(tokens + first);
@@ -166,16 +171,18 @@ extend_tables_kernel(const __grid_constant__ TablesParams p) {
             *p.new_num_free = (int32_t)(F - taken);
         }
     }
-    const int me = rank * blockDim.x + threadIdx.x, all = ranks * blockDim.x;
-    for (int k = me; k < (int)taken; k += all) {
+    const int me = rank * blockDim.x + threadIdx.x, threads = ranks * blockDim.x;
+    const int top = top_step(S);
+    for (int k = me; k < (int)taken; k += threads) {
         // several requests may share a first block where all but the last need none
-        const int s = owner_of(blk, S, k);
+        const int s = owner_of(blk, S, top, k);
         p.block_tables[(size_t)s * p.max_blocks + (len[s] + B - 1) / B + (k - blk[s])] = p.free_blocks[F - 1 - k];
     }
-    for (int64_t t = me; t < T; t += all) {
+    if (p.slots_apart) return;
+    for (int64_t t = me; t < T; t += threads) {
         int64_t slot = -1, pos = 0;
         if (t < total) {
-            const int s = owner_of(tok, S, (int)t);
+            const int s = owner_of(tok, S, top, (int)t);
             const int L = len[s], at = L + ((int)t - tok[s]);
             const int j = at / B, held = (L + B - 1) / B;
             const int64_t id = j < held ? p.block_tables[(size_t)s * p.max_blocks + j]
@@ -186,6 +193,58 @@ extend_tables_kernel(const __grid_constant__ TablesParams p) {
         p.slot_mapping[t] = slot;
         if (p.positions) p.positions[t] = pos;
     }
+}
+
+// The slots and positions of many tokens, from the starts, lengths and tables as extend
+// left them: kSlotsPer neighbours a thread.
+constexpr int kSlotsThreads = 256;
+constexpr int kSlotsPer = 4;
+
+__global__ void __launch_bounds__(kSlotsThreads)
+fill_slots_kernel(const __grid_constant__ TablesParams p) {
+    begin_overlapped();
+    const int S = p.num_seqs, B = p.block_size;
+    const int64_t T = p.max_tokens;
+    const int64_t t0 = ((int64_t)blockIdx.x * kSlotsThreads + threadIdx.x) * kSlotsPer;
+    if (t0 >= T) return;
+    const int total = p.query_start[S];
+    int64_t slot[kSlotsPer], pos[kSlotsPer];
+#pragma unroll
+    for (int i = 0; i < kSlotsPer; ++i) {
+        slot[i] = -1;
+        pos[i] = 0;
+    }
+    if (t0 < total) {
+        int s = owner_of(p.query_start, S, top_step(S), (int)t0);
+        int end = p.query_start[s + 1], ahead = p.new_lens[s] - end;       // a token's position less its row
+        int j = -1;
+        int64_t id = 0;
+#pragma unroll
+        for (int i = 0; i < kSlotsPer; ++i) {
+            const int t = (int)t0 + i;
+            if (t < total) {
+                while (t >= end) {
+                    ++s;
+                    end = p.query_start[s + 1];
+                    ahead = p.new_lens[s] - end;
+                    j = -1;
+                }
+                const int at = t + ahead;
+                if (at / B != j) {
+                    j = at / B;
+                    id = p.block_tables[(size_t)s * p.max_blocks + j];
+                }
+                slot[i] = id * B + (at - j * B);
+                pos[i] = at;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSlotsPer; ++i)
+        if (t0 + i < T) {
+            p.slot_mapping[t0 + i] = slot[i];
+            if (p.positions) p.positions[t0 + i] = pos[i];
+        }
 }
 
 __global__ void __launch_bounds__(kTablesThreads)
@@ -210,13 +269,15 @@ trim_tables_kernel(const __grid_constant__ TablesParams p) {
         if (s < S) {
             L = p.context_lens[s];
             d = p.new_tokens[s];
-            if (L < 0 || L > room || d < 0 || d > L) {
+            if (L < 0 || L > room || L > kMaxTableTokens || d < 0 || d > L) {
                 if (lead) flag(p.status, PA_DEV_BAD_LEN);
                 d = 0;
             }
-            keep = (L - d + B - 1) / B;
-            if (p.shared_blocks) keep = max(keep, (int64_t)p.shared_blocks[s]);
-            count = d ? max((int64_t)0, (L + B - 1) / B - keep) : 0;
+            if (d) {
+                keep = (int)(L - d + B - 1) / B;
+                if (p.shared_blocks) keep = max(keep, (int64_t)p.shared_blocks[s]);
+                count = max((int64_t)0, (int)(L + B - 1) / B - keep);
+            }
         }
         int64_t a = count, unused = 0, ta, tb;
         scan_two(a, unused, ta, tb, part);
@@ -237,24 +298,44 @@ trim_tables_kernel(const __grid_constant__ TablesParams p) {
         if (threadIdx.x == 0) *p.new_num_free = (int32_t)(fits ? F + given : F);
     }
     if (!fits) return;
-    for (int k = rank * blockDim.x + threadIdx.x; k < (int)given; k += ranks * blockDim.x) {
-        const int s = owner_of(blk, S, k);
-        p.stack[F + given - 1 - k] = p.block_tables[(size_t)s * p.max_blocks + from[s] + (k - blk[s])];
+    const int threads = ranks * blockDim.x, top = top_step(S);
+    constexpr int kAtOnce = 4;                     // entries whose loads are in flight together
+    for (int k0 = rank * blockDim.x + threadIdx.x; k0 < (int)given; k0 += kAtOnce * threads) {
+        int32_t id[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int k = k0 + i * threads;
+            if (k < (int)given) {
+                const int s = owner_of(blk, S, top, k);
+                id[i] = p.block_tables[(size_t)s * p.max_blocks + from[s] + (k - blk[s])];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int k = k0 + i * threads;
+            if (k < (int)given) p.stack[F + given - 1 - k] = id[i];
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_tables(const TablesParams& p, bool extend, cudaStream_t stream) {
-    // what there is to write, at the most: a request in four gives all its blocks back at worst
-    const int64_t work = extend ? p.max_tokens : (int64_t)p.num_seqs * p.max_blocks / 4;
+cudaError_t launch_tables(const TablesParams& tables, bool extend, cudaStream_t stream) {
+    TablesParams p = tables;
+    p.slots_apart = extend && p.max_tokens > kSlotsApart;
+    // entries and slots to write, about: a request in four gives all its blocks back at worst
+    const int64_t work = !extend ? (int64_t)p.num_seqs * p.max_blocks / 4
+                                 : (p.slots_apart ? p.max_tokens / p.block_size : p.max_tokens);
     const int threads = p.num_seqs <= 128 && work <= 512 ? 128 : kTablesThreads;
-    const int cluster = work <= 4 * kTablesThreads ? 1 : kTablesCluster;
+    const int cluster = work <= kTablesThreads ? 1 : kTablesCluster;
     auto kernel = extend ? extend_tables_kernel : trim_tables_kernel;
     const int smem = 12 * p.num_seqs;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, p, dim3(cluster), threads, smem, stream, cluster);
+    e = launch_overlapped(kernel, p, dim3(cluster), threads, smem, stream, cluster);
+    if (e != cudaSuccess || !p.slots_apart) return e;
+    const int64_t per = kSlotsThreads * kSlotsPer;
+    return launch_overlapped(fill_slots_kernel, p, dim3((unsigned)((p.max_tokens + per - 1) / per)), kSlotsThreads, 0, stream);
 }
 
 }  // namespace pagedkv

@@ -18,6 +18,7 @@
 // are read once and the codes written once: HBM-bound for prompts, launch and two
 // dependent loads for decode steps.
 #include "device_common.cuh"
+#include "kv_store.cuh"
 #include "launch.h"
 
 namespace pagedkv {
@@ -40,13 +41,52 @@ struct AppendShape {
     static constexpr int E = D / V > 32 ? 2 * V : V;               // elements of a lane
     static constexpr int LANES = D / E;                            // lanes of a row
     static constexpr int ROWS = 32 / LANES;                        // rows at a time
-    static constexpr int kPasses = E * (int)sizeof(QT) > 16 ? 4 : 8;      // of them in registers
+    static constexpr int kPasses = E * (int)sizeof(QT) > 16 ? 8 : (ROWS == 1 ? 16 : 8);   // of them in registers
 };
 
+// A lane's E elements of a row as they lie, and widened.
 template <typename QT, int E>
-__device__ __forceinline__ void load_row(const QT* p, float (&x)[E]) {
-    RowLoader<QT, E>::load(p, x);
-}
+struct RowBits {
+    uint4 w[E * sizeof(QT) / 16];
+    __device__ __forceinline__ void load(const QT* p) {
+#pragma unroll
+        for (int i = 0; i < (int)(E * sizeof(QT) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (int)(E * sizeof(QT) / 16); ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void widen(float (&x)[E]) const {
+        constexpr int V = 16 / (int)sizeof(QT);
+#pragma unroll
+        for (int i = 0; i < E / V; ++i) {
+            float y[V];
+            widen16<QT>(w[i], y);
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[i * V + k] = y[k];
+        }
+    }
+    // The largest magnitude's bits, of `m` too: magnitudes order as integers, infinities
+    // and NaN above all others (16-bit types: two at a time).
+    __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < (int)(E * sizeof(QT) / 16); ++i) {
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                m = sizeof(QT) == 2 ? __vmaxu2(m, v[k] & 0x7fff7fffu) : max(m, v[k] & 0x7fffffffu);
+        }
+        return m;
+    }
+    // That magnitude in binary32, of the whole warp.
+    __device__ __forceinline__ static float magnitude(uint32_t m) {
+        if constexpr (sizeof(QT) == 2) m = max(m & 0xffffu, m >> 16);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if constexpr (std::is_same<QT, float>::value) return __uint_as_float(m);
+        else if constexpr (std::is_same<QT, __half>::value) return __half2float(__ushort_as_half((unsigned short)m));
+        else return __uint_as_float(m << 16);
+    }
+};
 
 template <bool kInt>
 __device__ __forceinline__ float fresh_scale(float most) {
@@ -58,6 +98,14 @@ __device__ __forceinline__ float fresh_scale(float most) {
     return most > 0.f && e > 127 - 96 ? __uint_as_float((uint32_t)e << 23) : kLeastScale;
 }
 
+// x / scale to the nearest integer: by the reciprocal, whose product is within 2^-15 of
+// the quotient (|quotient| <= 127.5), and by a division where that leaves a doubt.
+__device__ __forceinline__ int quotient(float x, float scale, float inv) {
+    float y = x * inv;
+    if (!(fabsf(fabsf(y - rintf(y)) - 0.5f) > 0x1p-14f)) y = __fdiv_rn(x, scale);
+    return min(127, max(-127, __float2int_rn(y)));
+}
+
 // E codes of x / scale, packed in bytes. `inv`: 1 / scale, exact for powers of two.
 template <bool kInt, int E>
 __device__ __forceinline__ void encode(const float (&x)[E], float scale, float inv, uint32_t (&w)[E / 4]) {
@@ -67,8 +115,7 @@ __device__ __forceinline__ void encode(const float (&x)[E], float scale, float i
             uint32_t r = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = min(127, max(-127, __float2int_rn(__fdiv_rn(x[i + j], scale))));
-                r |= (uint32_t)(c & 0xff) << (8 * j);
+                r |= (uint32_t)(quotient(x[i + j], scale, inv) & 0xff) << (8 * j);
             }
             w[i / 4] = r;
         } else {
@@ -138,54 +185,37 @@ scaled_append_kernel(const __grid_constant__ ScaledAppendParams p) {
     const int start = L - (int)n;                                  // the first new position
     const int64_t j = start / B + (int64_t)nth;
     if (j * B >= L) return;
+    // the block's id and its new rows load together
     const int64_t blk = p.block_tables[(size_t)s * p.max_blocks + j];
+    const int base = (int)(j * B);
+    const int lo = max(start - base, 0), hi = min(L - base, B);    // the new rows of the block
+    const int64_t stride = is_v ? p.value_stride : p.key_stride;
+    const QT* src = static_cast<const QT*>(is_v ? p.value : p.key) + (row0 + base - start) * stride + (size_t)h * D;
+    const int r0 = lane / A::LANES, e0 = (lane % A::LANES) * E;
+    RowBits<QT, E> x[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int r = lo + i * ROWS + r0;
+        if (r < hi) x[i].load(src + r * stride + e0);
+        else x[i].clear();
+    }
     if (blk < 0 || blk >= p.num_blocks) {
         if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
         return;
     }
-    const int base = (int)(j * B);
-    const int lo = max(start - base, 0), hi = min(L - base, B);    // the new rows of the block
     const size_t slab = (size_t)blk * p.num_kv_heads + h;
     float* scales = (is_v ? p.v_scales : p.k_scales) + slab;
     const float before = lo > 0 ? *scales : 0.f;
-    const int64_t stride = is_v ? p.value_stride : p.key_stride;
-    const QT* src = static_cast<const QT*>(is_v ? p.value : p.key) + (row0 + base - start) * stride + (size_t)h * D;
     uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slab * B * D;
-    const int r0 = lane / A::LANES, e0 = (lane % A::LANES) * E;
-
-    float x[P][E];
-    float most = 0.f;
-    auto note = [&](const float (&v)[E]) {
+    uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            float m;
-            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(most), "f"(fabsf(v[i])));
-            most = m;
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int r = lo + i * ROWS + r0;
-        if (r < hi) load_row<QT, E>(src + r * stride + e0, x[i]);
-        else {
-#pragma unroll
-            for (int k = 0; k < E; ++k) x[i][k] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) note(x[i]);
+    for (int i = 0; i < P; ++i) bits = x[i].largest(bits);
     for (int r = lo + P * ROWS + r0; r < hi; r += ROWS) {
-        float y[E];
-        load_row<QT, E>(src + r * stride + e0, y);
-        note(y);
+        RowBits<QT, E> y;
+        y.load(src + r * stride + e0);
+        bits = y.largest(bits);
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, most, m);
-        float t;
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(most), "f"(o));
-        most = t;
-    }
+    const float most = RowBits<QT, E>::magnitude(bits);
     float scale = fresh_scale<kInt>(most);
     if (lo > 0) {
         float t;
@@ -200,21 +230,25 @@ scaled_append_kernel(const __grid_constant__ ScaledAppendParams p) {
             }
         }
     }
-    const float inv = kInt ? 0.f : __fdiv_rn(1.f, scale);
+    const float inv = __fdiv_rn(1.f, scale);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int r = lo + i * ROWS + r0;
         if (r < hi) {
+            float v[E];
+            x[i].widen(v);
             uint32_t w[E / 4];
-            encode<kInt, E>(x[i], scale, inv, w);
+            encode<kInt, E>(v, scale, inv, w);
             store_words(dst + (size_t)r * D + e0, w);
         }
     }
     for (int r = lo + P * ROWS + r0; r < hi; r += ROWS) {
-        float y[E];
-        load_row<QT, E>(src + r * stride + e0, y);
+        RowBits<QT, E> y;
+        y.load(src + r * stride + e0);
+        float v[E];
+        y.widen(v);
         uint32_t w[E / 4];
-        encode<kInt, E>(y, scale, inv, w);
+        encode<kInt, E>(v, scale, inv, w);
         store_words(dst + (size_t)r * D + e0, w);
     }
     if (lane == 0) *scales = scale;

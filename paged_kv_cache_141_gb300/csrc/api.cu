@@ -101,23 +101,27 @@ struct ScaledPlan {
     size_t max_logits, exp_sums, total;       // the partials' start at 0; total 0: none
 };
 
-// The split of a call's work: the query rows of a CTA (the smallest n-tiles that hold a
-// sequence's; 32 at most, 16 at head size 256, whose accumulators fill the registers), and
-// partitions of the context where the sequences, heads and row tiles alone do not give
-// every SM some four CTAs.
+// The split of a call's work: the query rows of a CTA, and partitions of the context
+// where the sequences, heads and row tiles alone leave SMs idle. Up to 32 rows of a sequence
+// and KV head: warp-level MMAs, the smallest n-tiles that hold them, some four CTAs for
+// every SM. More, at head size 64 or 128 and blocks of a multiple of 16 tokens: the tcgen05
+// kernel, 256 rows a CTA, one CTA on an SM; else tiles of 32 (16 at head size 256, whose
+// accumulators fill the registers).
 ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_kv_heads,
-                       int head_size, int max_queries, int max_context_len) {
+                       int head_size, int block_size, int max_queries, int max_context_len) {
     ScaledPlan l{};
     const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
-    l.tile_rows = rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32);
+    const bool tc = rows > 32 && head_size <= 128 && block_size % 16 == 0;
+    l.tile_rows = tc ? 256 : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
     l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);
     const int64_t units = (int64_t)num_seqs * num_kv_heads * tiles;
-    const int64_t want = 8 * 152;
+    const int64_t want = tc ? (units >= 152 ? units : 2 * 152) : 8 * 152;
     int64_t parts = (want + units - 1) / units;
     int64_t size = (max_context_len + parts - 1) / parts;
-    if (tiles == 1 && size > 4096) size = 4096;             // one sequence's length does not hold up the rest
-    size = size < 256 ? 256 : (size + 127) / 128 * 128;
+    if (!tc && tiles == 1 && size > 4096) size = 4096;      // one sequence's length does not hold up the rest
+    const int64_t least = tc ? 1024 : 256;
+    size = size < least ? least : (size + 127) / 128 * 128;
     l.partition_size = (int)size;
     parts = (max_context_len + size - 1) / size;
     l.max_parts = parts < 1 ? 1 : (int)parts;
@@ -1207,8 +1211,13 @@ size_t pa_scaled_attention_workspace_bytes(int num_seqs, int num_queries, int nu
         num_q_heads % num_kv_heads != 0 || !supported_head_size(head_size) ||
         max_queries_per_seq <= 0 || max_context_len <= 0 || max_context_len > kMaxScaledContext)
         return 0;
-    return scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
-                       max_queries_per_seq, max_context_len).total;
+    if (max_queries_per_seq > num_queries) max_queries_per_seq = num_queries;
+    // for any block size
+    const size_t even = scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size, 16,
+                                    max_queries_per_seq, max_context_len).total;
+    const size_t odd = scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size, 1,
+                                   max_queries_per_seq, max_context_len).total;
+    return even > odd ? even : odd;
 }
 
 pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
@@ -1242,7 +1251,7 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
         return PA_ERR_INVALID_ARG;
     if (max_queries_per_seq > num_queries) max_queries_per_seq = num_queries;
     const ScaledPlan l = scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
-                                     max_queries_per_seq, max_context_len);
+                                     block_size, max_queries_per_seq, max_context_len);
     if ((int64_t)num_kv_heads * l.row_tiles > 65535 || max_queries_per_seq > 65535) return PA_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total)) return PA_ERR_WORKSPACE;
     uint8_t* w = static_cast<uint8_t*>(workspace);

@@ -530,6 +530,10 @@ scaled_merge_kernel(const __grid_constant__ ScaledAttnParams p) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + 4 * c) = w;
 }
 
+// scaled_prefill.cuh, instantiated in files of its own.
+template <typename CT, int D>
+cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, cudaStream_t stream);
+
 template <typename CT, int D, int NT>
 cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     using S = ScaledShape<D, NT>;
@@ -542,7 +546,10 @@ cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
 template <typename CT, int D>
 cudaError_t launch_scaled_head(const ScaledAttnParams& p, cudaStream_t stream) {
     cudaError_t e;
-    if (p.tile_rows == 8) e = launch_scaled_rows<CT, D, 1>(p, stream);
+    if (p.tile_rows == 256) {
+        if constexpr (D < 256) e = launch_scaled_prefill<CT, D>(p, stream);
+        else return cudaErrorInvalidValue;
+    } else if (p.tile_rows == 8) e = launch_scaled_rows<CT, D, 1>(p, stream);
     else if (p.tile_rows == 16) e = launch_scaled_rows<CT, D, 2>(p, stream);
     else if constexpr (D < 256) e = launch_scaled_rows<CT, D, 4>(p, stream);
     else return cudaErrorInvalidValue;

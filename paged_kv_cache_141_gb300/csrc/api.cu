@@ -97,15 +97,19 @@ bool is_scaled_type(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_INT8; }
 constexpr int kMaxScaledContext = 1 << 30;    // positions plus a partition stay in 32 bits
 
 struct ScaledPlan {
-    int tile_rows, row_tiles, partition_size, max_parts;
-    size_t max_logits, exp_sums, total;       // the partials' start at 0; total 0: none
+    int tile_rows, row_tiles;
+    int workers;                              // warp-level MMAs
+    size_t stages_before;
+    int partition_size, max_parts;            // tcgen05
+    size_t max_logits, exp_sums;
+    size_t total;                             // bytes; the first region starts at 0
 };
 
-// The split of a call's work: the query rows of a CTA, and partitions of the context
-// where the sequences, heads and row tiles alone leave SMs idle. Up to 32 rows of a sequence
-// and KV head: warp-level MMAs, the smallest n-tiles that hold them, some four CTAs for
-// every SM. More, at head size 64 or 128 and blocks of a multiple of 16 tokens: the tcgen05
-// kernel, 256 rows a CTA, one CTA on an SM; else tiles of 32 (16 at head size 256, whose
+// How a call's work is cut. Up to 32 rows of a sequence and KV head: warp-level MMAs, the
+// smallest n-tiles that hold them, one wave of warps for all stages. More, at head size 64
+// or 128 and blocks of a multiple of 16 tokens: the tcgen05 kernel, 256 rows a CTA,
+// one CTA on an SM, and partitions of the context where the sequences, heads and row
+// tiles alone leave SMs idle; else tiles of 32 rows (16 at head size 256, whose
 // accumulators fill the registers).
 ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_kv_heads,
                        int head_size, int block_size, int max_queries, int max_context_len) {
@@ -115,13 +119,19 @@ ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_k
     l.tile_rows = tc ? 256 : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
     l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);
+    if (!tc) {
+        // the CTAs that an SM holds, by their registers and rings
+        const int ctas = head_size == 256 ? 1 : (l.tile_rows == 8 ? 3 : 2);
+        l.workers = 152 * ctas * kScaledWarps;
+        l.stages_before = align256((size_t)l.workers * 2 * l.tile_rows * (head_size + 2) * sizeof(float));
+        l.total = l.stages_before + align256(((size_t)num_seqs + 1) * sizeof(int64_t));
+        l.max_parts = 1;
+        return l;
+    }
     const int64_t units = (int64_t)num_seqs * num_kv_heads * tiles;
-    const int64_t want = tc ? (units >= 152 ? units : 2 * 152) : 8 * 152;
-    int64_t parts = (want + units - 1) / units;
+    int64_t parts = units >= 152 ? 1 : (2 * 152 + units - 1) / units;
     int64_t size = (max_context_len + parts - 1) / parts;
-    if (!tc && tiles == 1 && size > 4096) size = 4096;      // one sequence's length does not hold up the rest
-    const int64_t least = tc ? 1024 : 256;
-    size = size < least ? least : (size + 127) / 128 * 128;
+    size = size < 1024 ? 1024 : (size + 127) / 128 * 128;
     l.partition_size = (int)size;
     parts = (max_context_len + size - 1) / size;
     l.max_parts = parts < 1 ? 1 : (int)parts;
@@ -1209,7 +1219,7 @@ size_t pa_scaled_attention_workspace_bytes(int num_seqs, int num_queries, int nu
                                            int max_queries_per_seq, int max_context_len) {
     if (num_seqs <= 0 || num_queries <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
         num_q_heads % num_kv_heads != 0 || !supported_head_size(head_size) ||
-        max_queries_per_seq <= 0 || max_context_len <= 0 || max_context_len > kMaxScaledContext)
+        max_queries_per_seq <= 0 || max_context_len < 0 || max_context_len > kMaxScaledContext)
         return 0;
     if (max_queries_per_seq > num_queries) max_queries_per_seq = num_queries;
     // for any block size
@@ -1252,7 +1262,7 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     if (max_queries_per_seq > num_queries) max_queries_per_seq = num_queries;
     const ScaledPlan l = scaled_plan(num_seqs, num_queries, num_q_heads, num_kv_heads, head_size,
                                      block_size, max_queries_per_seq, max_context_len);
-    if ((int64_t)num_kv_heads * l.row_tiles > 65535 || max_queries_per_seq > 65535) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_kv_heads * l.row_tiles > (l.workers ? INT32_MAX : 65535) || max_queries_per_seq > 65535) return PA_ERR_UNSUPPORTED;
     if (l.total > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total)) return PA_ERR_WORKSPACE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     ScaledAttnParams p{};
@@ -1265,11 +1275,16 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.query_start = query_start;
-    if (l.total > 0) {
+    if (l.workers > 0) {
+        p.parts = reinterpret_cast<float*>(w);
+        p.stages_before = reinterpret_cast<int64_t*>(w + l.stages_before);
+    } else if (l.total > 0) {
         p.tmp_out = reinterpret_cast<float*>(w);
         p.max_logits = reinterpret_cast<float*>(w + l.max_logits);
         p.exp_sums = reinterpret_cast<float*>(w + l.exp_sums);
     }
+    p.items = l.row_tiles * num_kv_heads;
+    p.workers = l.workers;
     p.status = dev_status;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;

@@ -343,7 +343,11 @@ struct ScaledAttnParams {
     const int32_t* block_tables;  // [S, max_blocks]
     const int32_t* context_lens;  // [S]
     const int32_t* query_start;   // [S + 1]; null: one query each
-    float* tmp_out;               // several partitions: [num_queries, Hq, max_parts, D]
+    // up to 32 rows a tile: warps of one wave share all stages
+    float* parts;                 // [workers][2][tile_rows * (D + 2)]: outputs, maxima (base 2), sums
+    int64_t* stages_before;       // [S + 1]
+    // the tcgen05 kernel, several partitions
+    float* tmp_out;               // [num_queries, Hq, max_parts, D]
     float* max_logits;            // [num_queries, Hq, max_parts], base 2
     float* exp_sums;
     uint32_t* status;             // may be null
@@ -357,13 +361,27 @@ struct ScaledAttnParams {
     int group;
     int block_size;
     int max_context_len;
-    int partition_size;           // a multiple of 32
+    int partition_size;           // a multiple of 128
     int max_parts;
-    int tile_rows;                // query rows of a CTA: 8, 16 or 32; 256: on the tcgen05 tensor cores
-    int row_tiles;                // CTAs that share a sequence's rows
+    int tile_rows;                // query rows at a time: 8, 16 or 32; 256: on the tcgen05 tensor cores
+    int row_tiles;                // such tiles of a sequence and KV head
+    int items;                    // row_tiles * Hkv
+    int workers;                  // warps that share the stages
     float q_mul;                  // scale * log2(e)
     int bf16;                     // the query's and the output's type; else binary16
 };
+
+// Warps of a CTA that share the stages, and how many of those a worker takes: at least
+// kScaledLeast, as a piece costs a start and an end.
+constexpr int kScaledWarps = 4;
+constexpr int kScaledLeast = 4;
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int64_t scaled_piece(int64_t stages, int workers) {
+    const int64_t n = (stages + workers - 1) / workers;
+    return n < kScaledLeast ? kScaledLeast : n;
+}
 
 cudaError_t launch_scaled_attention_int8(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
 cudaError_t launch_scaled_attention_e4m3(const ScaledAttnParams& p, int head_size, cudaStream_t stream);

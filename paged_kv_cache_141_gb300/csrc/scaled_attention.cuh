@@ -4,12 +4,18 @@
 // block that holds position t,
 //     s_t = scale a_t <q, c_t>,   out = sum_t softmax(s)_t b_t c_t.
 //
-// Work unit: (sequence, KV head, 8 NT query rows, partition of the context). Rows
-// are (query token, head of the group) pairs, token-major, so a group's heads and a
-// sequence's drafts read each key once. Four warps of a CTA take the partition's 32-token
-// stages in turn, each with a ring of its own that it fills by 16-byte asynchronous copies
-// (any block size: a lane finds a token's block, the rows' addresses go round by
-// shuffles); no barrier but the warp's own. Per stage:
+// Rows are (query token, head of the group) pairs, token-major, so a group's heads and
+// a sequence's drafts read each key once; an item is a (sequence, KV head, 8 NT rows), and
+// its context is cut into stages of 32 tokens. A stage is small against the latency of
+// memory, and a partition's own start and end (lengths, table, first stage, joining of
+// warps) cost as much as a dozen of them, so nothing starts or ends per partition: the
+// stages of all items lie in one line, and every warp of one wave of CTAs takes an
+// equal piece of it, from the sums of the sequences' stages that each CTA makes for
+// itself. A warp fills a ring of its own by 16-byte asynchronous copies (any block size:
+// a lane finds a token's block, the rows' addresses go round by shuffles), across the
+// borders of items; no barrier but the warp's own. (64 contexts of 512-8192 tokens: @ us,
+// 117 with CTAs of four warps for partitions of 1024-4096 tokens; one of 131072: @, 64.)
+// Per stage:
 //   S (16 tokens x 8 rows) = C_K Q^T on binary16 warp-level MMAs, the codes widened in
 //     registers, exactly: integers by the bits of 1024 + (c + 128), less 1152; E4M3 by
 //     moving the exponent field (values times 2^-8);
@@ -24,8 +30,10 @@
 // scale seen: 2^-14 of the largest weight before its bits thin out, 2^-25 of it before it
 // vanishes.
 //
-// Several partitions: normalised partial outputs with their maximum and sum go to the
-// workspace, and a second kernel merges them (M = max m_p, sum of l_p exp(m_p - M) o_p).
+// An item within one warp's piece is written out by it. Pieces of others go to the
+// workspace, two of a warp's at most (the end of an item that began before its piece, the
+// beginning of one that goes on behind it), and a second kernel joins them
+// (M = max m_w, sum of exp(m_w - M) (o_w, l_w)).
 #pragma once
 
 #include "decode_mma.cuh"
@@ -36,8 +44,6 @@ struct int8_code_t {
     int8_t bits;
 };
 
-constexpr int kScaledWarps = 4;
-constexpr int kScaledThreads = kScaledWarps * 32;
 constexpr int kScaledStage = 32;                   // tokens
 
 template <int D, int NT>
@@ -46,14 +52,10 @@ struct ScaledShape {
     static constexpr int kRows = 8 * NT;
     static constexpr int kTile = kScaledStage * D;                     // bytes of a stage's keys (values)
     static constexpr int kStageBytes = 2 * kTile + 2 * kScaledStage * 4;   // and its scales
-    static constexpr int NST = D == 64 ? 6 : (D == 128 ? 3 : 2);
-    static constexpr int kRing = kScaledWarps * NST * kStageBytes;
-    static constexpr int kOutStride = D + 8;
-    static constexpr int kCombine = kScaledWarps * kRows * (kOutStride + 2) * 4;
-    static constexpr int kQOff = (kRing > kCombine ? kRing : kCombine);
-    static constexpr int kMulOff = kQOff + NT * KS * 256;
-    static constexpr int kBytes = kMulOff + kRows * 4;
+    static constexpr int NST = D == 64 ? 4 : 2;
     static constexpr bool kQReg = NT * KS <= 16;                       // the query's fragments in registers
+    static constexpr int kQBytes = kQReg ? 0 : NT * KS * 256;
+    static constexpr int kWarpBytes = NST * kStageBytes + kQBytes;
 };
 
 // One sequence's part of the call. False: nothing to do (a fault is reported by one thread).
@@ -112,60 +114,196 @@ __device__ __forceinline__ uint32_t biased(uint32_t w) {
     return std::is_same<CT, e4m3_t>::value ? w : w ^ 0x80808080u;
 }
 
+// The query rows of an item as B fragments, each under a power of two, into registers or
+// shared memory; mul: the rows' units (lanes hold rows 2 t4, 2 t4 + 1 of each n-tile).
 template <typename CT, int D, int NT>
-__global__ void __launch_bounds__(kScaledThreads)
+__device__ __forceinline__ void scaled_query(const ScaledAttnParams& p, int q0, int kvh, int row0, int rows, int lane,
+                                             uint2* qr, uint2* qf, float (&mul)[NT][2]) {
+    using S = ScaledShape<D, NT>;
+    using Ops = MmaOps<__half>;
+    const int g = lane >> 2, t4 = lane & 3, G = p.group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g, row = row0 + r;
+        const bool there = r < rows;
+        const size_t at = there ? ((size_t)(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D : 0;
+        uint2 w[S::KS];
+        uint32_t m2 = 0u;                          // 16-bit magnitudes order as integers
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+            w[ks] = make_uint2(0u, 0u);
+            if (there) w[ks] = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.query) + at + 16 * ks + 4 * t4);
+        }
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) m2 = __vmaxu2(m2, __vmaxu2(w[ks].x & 0x7fff7fffu, w[ks].y & 0x7fff7fffu));
+        m2 = max(m2 & 0xffffu, m2 >> 16);
+        m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+        m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+        const float mx = p.bf16 ? __uint_as_float(m2 << 16) : __half2float(__ushort_as_half((unsigned short)m2));
+        // a power of two in the range whose reciprocal is a normal number
+        const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
+        const float unit = mx > 0.f && mx < INFINITY ? __uint_as_float(ex << 23) : 1.f;
+        const float inv = 1.f / unit;                                  // exact
+#pragma unroll
+        for (int ks = 0; ks < S::KS; ++ks) {
+            float2 a, b;
+            if (p.bf16) {
+                a = MmaOps<__nv_bfloat16>::unpack(w[ks].x);
+                b = MmaOps<__nv_bfloat16>::unpack(w[ks].y);
+            } else {
+                a = Ops::unpack(w[ks].x);
+                b = Ops::unpack(w[ks].y);
+            }
+            const uint2 f = make_uint2(Ops::pack(a.x * inv, a.y * inv), Ops::pack(b.x * inv, b.y * inv));
+            if constexpr (S::kQReg) qr[nt * S::KS + ks] = f;
+            else qf[(nt * S::KS + ks) * 32 + lane] = f;
+        }
+        const float u = p.q_mul * unit * (std::is_same<CT, e4m3_t>::value ? 256.f : 1.f);
+        mul[nt][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
+        mul[nt][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
+    }
+}
+
+__device__ __forceinline__ void store_pair(const ScaledAttnParams& p, size_t at, float x, float y) {
+    uint32_t w;
+    if (p.bf16) w = MmaOps<__nv_bfloat16>::pack(x, y);
+    else w = MmaOps<__half>::pack(x, y);
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = w;
+}
+
+// Stages of a sequence's context; 0 where the call has nothing to do for it.
+__device__ __forceinline__ int scaled_stages(const ScaledAttnParams& p, int s, bool report, int& L, int& q0, int& Q) {
+    return scaled_sequence(p, s, report, L, q0, Q) ? (L + kScaledStage - 1) / kScaledStage : 0;
+}
+
+// A place in the line of stages: stage k of item `item` of sequence s.
+struct ScaledPlace {
+    int s, item, k, stages;                        // the sequence's stages
+    int L, q0, Q;
+    __device__ __forceinline__ void next(const ScaledAttnParams& p) {
+        if (++k < stages) return;
+        k = 0;
+        if (++item < p.items) return;
+        item = 0;
+        do {
+            ++s;
+            stages = s < p.num_seqs ? scaled_stages(p, s, false, L, q0, Q) : 0;
+        } while (stages == 0 && s < p.num_seqs);
+    }
+};
+
+template <typename CT, int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, NT == 1 && D < 256 ? 3 : (D < 256 ? 2 : 1))
 scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
     using S = ScaledShape<D, NT>;
     using Ops = MmaOps<__half>;
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
-    constexpr int KS = S::KS, NST = S::NST, W = kScaledWarps;
+    constexpr int KS = S::KS, NST = S::NST;
     constexpr int CPR = D / 16;                    // 16-byte chunks of a row
     constexpr int RPP = 32 / CPR;                  // rows of a copy pass
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_sum[W];
+    __shared__ int64_t s_before[W];                // of each warp's first sequence: stages before it,
+    __shared__ int s_first[W];                     // and which it is
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
     const int mi = lane >> 3, r8 = lane & 7;
-    const int s = blockIdx.z;
-    const int kvh = blockIdx.y / p.row_tiles, tile = blockIdx.y - kvh * p.row_tiles;
     const int G = p.group, B = p.block_size;
-    int L, q0, Q;
-    if (!scaled_sequence(p, s, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0, L, q0, Q)) return;
-    const int row0 = tile * S::kRows, rows = min(S::kRows, Q * G - row0);
-    if (rows <= 0) return;
-    const int first_pos = L - Q;                   // of query token 0
-    const int seen = first_pos + (row0 + rows - 1) / G + 1;            // keys that the tile's last row sees
-    const int T0 = blockIdx.x * p.partition_size;
-    if (T0 >= seen) {
-        if (L == 0 && p.max_parts == 1) {          // an empty context
-            for (int i = threadIdx.x; i < rows * D; i += kScaledThreads) {
-                const size_t o = ((size_t)q0 * p.num_q_heads + kvh * G + row0 + i / D) * D + i % D;
-                if (p.bf16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(0.f);
-                else static_cast<__half*>(p.out)[o] = __float2half_rn(0.f);
+
+    // ------------------------------------------------------------ this warp's piece of the line
+    const int per = (p.num_seqs + W * 32 - 1) / (W * 32);              // sequences a thread
+    const int s_lo = min(p.num_seqs, (int)threadIdx.x * per), s_hi = min(p.num_seqs, s_lo + per);
+    int64_t mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+        int L, q0, Q;
+        const int n = scaled_stages(p, s, blockIdx.x == 0, L, q0, Q);
+        mine += n;
+        if (n == 0 && L == 0 && !p.query_start && s % gridDim.x == blockIdx.x)     // an empty context: zeros
+            for (int i = 0; i < p.num_q_heads * D; i += 2) store_pair(p, (size_t)s * p.num_q_heads * D + i, 0.f, 0.f);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, m);
+        if (lane >= m) upto += o;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w == warp) upto += total;
+        total += s_sum[w];
+    }
+    const int64_t line = total * p.items;
+    const int64_t piece = scaled_piece(line, p.workers);
+    {
+        // the thread whose sequences hold a warp's first stage finds the sequence
+        const int64_t before = upto - mine;
+        for (int w = 0; w < W; ++w) {
+            const int64_t at = (blockIdx.x * W + w) * piece / p.items;
+            if (at >= before && at < upto) {
+                int64_t b = before;
+                int s = s_lo;
+                for (;;) {
+                    int L, q0, Q;
+                    const int n = scaled_stages(p, s, false, L, q0, Q);
+                    if (at < b + n) break;
+                    b += n;
+                    ++s;
+                }
+                s_first[w] = s;
+                s_before[w] = b;
             }
         }
-        return;
+        if (blockIdx.x == 0) {                     // for the kernel that joins the pieces
+            int64_t b = before;
+            for (int s = s_lo; s < s_hi; ++s) {
+                int L, q0, Q;
+                p.stages_before[s] = b;
+                b += scaled_stages(p, s, false, L, q0, Q);
+            }
+            if (threadIdx.x == 0) p.stages_before[p.num_seqs] = total;
+        }
     }
-    const int Tend = min(T0 + p.partition_size, seen);
-    const int n_st = (Tend - T0 + kScaledStage - 1) / kScaledStage;
+    __syncthreads();
+    const int64_t begin = (int64_t)(blockIdx.x * W + warp) * piece;
+    if (begin >= line) return;
+    const int count = (int)(min(begin + piece, line) - begin);
 
-    // ------------------------------------------------------------ this warp's ring
-    uint8_t* ring = smem + warp * NST * S::kStageBytes;
+    ScaledPlace now;
+    now.s = s_first[warp];
+    now.stages = scaled_stages(p, now.s, false, now.L, now.q0, now.Q);
+    {
+        const int64_t in = begin - s_before[warp] * p.items;
+        now.item = (int)(in / now.stages);
+        now.k = (int)(in - (int64_t)now.item * now.stages);
+    }
+
+    // ------------------------------------------------------------ the ring
+    uint8_t* ring = smem + warp * S::kWarpBytes;
+    uint2* qf = reinterpret_cast<uint2*>(ring + NST * S::kStageBytes);
     const uint32_t ring_u32 = smem_u32(ring);
-    const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
     const int cr = lane / CPR, cc = lane % CPR;
-    // the block of this lane's token in stage k, read a stage ahead of its use
-    auto block_of = [&](int k) {
-        const int t = T0 + k * kScaledStage + lane;
-        return k < n_st && t < Tend ? table[t / B] : -1;
+    // the next stage to copy, and the block of this lane's token in it, read a stage ahead
+    ScaledPlace ahead = now;
+    int left = count;                              // stages not yet copied
+    int next_block = -1;
+    auto find = [&] {
+        const int t = ahead.k * kScaledStage + lane;
+        next_block = left > 0 && t < ahead.L ? p.block_tables[(size_t)ahead.s * p.max_blocks + t / B] : -1;
     };
-    int next_block = block_of(warp);
-    auto issue = [&](int k, int slot) {
-        if (k < n_st) {
-            const int t = T0 + k * kScaledStage + lane;
+    find();
+    auto issue = [&](int slot) {
+        if (left > 0) {
+            const int t = ahead.k * kScaledStage + lane;
+            const int kvh = ahead.item / p.row_tiles;
             const int blk = next_block;
-            next_block = block_of(k + W);
-            bool there = t < Tend;
+            bool there = t < ahead.L;
+            --left;
+            ahead.next(p);
+            find();
             if (there && (blk < 0 || blk >= p.num_blocks)) {
                 if (p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
                 there = false;
@@ -188,79 +326,49 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < NST - 1; ++i) issue(warp + i * W, i);
+    for (int i = 0; i < NST - 1; ++i) issue(i);
 
-    // ------------------------------------------------------------ the query, as B fragments
-    uint2* qf = reinterpret_cast<uint2*>(smem + S::kQOff);             // [NT][KS][32]
-    float* mul = reinterpret_cast<float*>(smem + S::kMulOff);          // [rows]
-    for (int nt = warp; nt < NT; nt += W) {
-        const int r = 8 * nt + g;
-        const int row = row0 + r;
-        const bool there = r < rows;
-        const size_t at = there ? ((size_t)(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D : 0;
-        float x[KS][4], mx = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint2 w = make_uint2(0u, 0u);
-            if (there) w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.query) + at + 16 * ks + 4 * t4);
-            float2 a, b;
-            if (p.bf16) {
-                a = MmaOps<__nv_bfloat16>::unpack(w.x);
-                b = MmaOps<__nv_bfloat16>::unpack(w.y);
-            } else {
-                a = Ops::unpack(w.x);
-                b = Ops::unpack(w.y);
-            }
-            x[ks][0] = a.x; x[ks][1] = a.y; x[ks][2] = b.x; x[ks][3] = b.y;
-            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // a power of two in the range whose reciprocal is a normal number
-        const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 252u);
-        const float unit = mx > 0.f && mx < INFINITY ? __uint_as_float(ex << 23) : 1.f;
-        const float inv = 1.f / unit;                                  // exact
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            qf[(nt * KS + ks) * 32 + lane] = make_uint2(Ops::pack(x[ks][0] * inv, x[ks][1] * inv), Ops::pack(x[ks][2] * inv, x[ks][3] * inv));
-        if (t4 == 0) mul[r] = p.q_mul * unit * (kFp8 ? 256.f : 1.f);
-    }
-    __syncthreads();
     uint2 qr[S::kQReg ? NT * KS : 1];
-    if constexpr (S::kQReg) {
-#pragma unroll
-        for (int i = 0; i < NT * KS; ++i) qr[i] = qf[i * 32 + lane];
-    }
     float hm[NT][2], m_ref[NT][2], l_run[NT][2];
-    int lim[NT][2];                                // of the partition's tokens, those that the row sees
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = 8 * nt + 2 * t4 + j;
-            hm[nt][j] = mul[r];
-            lim[nt][j] = r < rows ? first_pos + (row0 + r) / G + 1 - T0 : 0;
-            m_ref[nt][j] = -INFINITY;
-            l_run[nt][j] = 0.f;
-        }
-    const int all_see = first_pos + row0 / G + 1 - T0;                 // tokens below it are seen by every row
+    int lim[NT][2];                                // tokens that the row sees
     float acc[NT][KS][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
-    int e_ref = -120;                              // value scales below 2^(e_ref + 1) fit the weights' range
-
+    int e_ref = 0, all_see = 0, kvh = 0, row0 = 0, rows = 0;
+    bool whole = false;                            // from the item's first stage on
     int slot = 0;
-    for (int k = warp; k < n_st; k += W) {
+    for (int i = 0; i < count; ++i) {
+        if (i == 0 || now.k == 0) {
+            // ---- an item begins
+            kvh = now.item / p.row_tiles;
+            row0 = (now.item - kvh * p.row_tiles) * S::kRows;
+            rows = max(0, min(S::kRows, now.Q * G - row0));
+            whole = now.k == 0;
+            scaled_query<CT, D, NT>(p, now.q0, kvh, row0, rows, lane, qr, qf, hm);
+            const int first_pos = now.L - now.Q;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * nt + 2 * t4 + j;
+                    lim[nt][j] = r < rows ? first_pos + (row0 + r) / G + 1 : 0;
+                    m_ref[nt][j] = -INFINITY;
+                    l_run[nt][j] = 0.f;
+                }
+            all_see = first_pos + row0 / G + 1;    // tokens below it are seen by every row
+            e_ref = -120;                          // value scales below 2^(e_ref + 1) fit the weights' range
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int md = 0; md < KS; ++md)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[nt][md][j] = 0.f;
+        }
         cp_async_wait<NST - 2>();
         __syncwarp();
-        issue(k + (NST - 1) * W, slot == 0 ? NST - 1 : slot - 1);
+        issue(slot == 0 ? NST - 1 : slot - 1);
         const uint8_t* Kst = ring + slot * S::kStageBytes;
         const uint8_t* Vst = Kst + S::kTile;
         const float* scales = reinterpret_cast<const float*>(Kst + 2 * S::kTile);
+        const int key0 = now.k * kScaledStage;
 
         // ---- S = C_K Q^T
         float sc[NT][2][4];
@@ -301,7 +409,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             vb[i] = scales[kScaledStage + g + 8 * i];
         }
         const int vexp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(scales[kScaledStage + lane]) << 1 >> 24)) - 127;
-        const bool masked = (k + 1) * kScaledStage > all_see;
+        const bool masked = key0 + kScaledStage > all_see;
         bool move = vexp > e_ref;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -311,7 +419,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float v = sc[nt][i >> 1][2 * (i & 1) + j] * ka[i] * hm[nt][j];
-                    if (masked && k * kScaledStage + g + 8 * i >= lim[nt][j]) v = -INFINITY;
+                    if (masked && key0 + g + 8 * i >= lim[nt][j]) v = -INFINITY;
                     sc[nt][i >> 1][2 * (i & 1) + j] = v;
                     mx = fmaxf(mx, v);
                 }
@@ -385,76 +493,123 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             }
         }
         slot = slot + 1 == NST ? 0 : slot + 1;
-    }
 
-    // ------------------------------------------------------------ join the four warps
-    cp_async_wait<0>();
-    __syncthreads();                               // the rings are free
-    float* cm = reinterpret_cast<float*>(smem);                        // [W][rows]
-    float* cl = cm + W * S::kRows;                                     // [W][rows]
-    float* co = cl + W * S::kRows;                                     // [W][rows][kOutStride]
-    const float fall = __uint_as_float((uint32_t)(127 + e_ref - 6) << 23) * (kFp8 ? 256.f : 1.f);
+        const bool ends = now.k + 1 == now.stages;
+        if (ends || i + 1 == count) {
+            // ---- the item ends, or the piece does
+            const bool done = whole && ends;
+            const float fall = __uint_as_float((uint32_t)(127 + e_ref - 6) << 23) * (kFp8 ? 256.f : 1.f);
+            // where it began in this piece it is the piece's last, else its first
+            float* part = p.parts + ((size_t)(blockIdx.x * W + warp) * 2 + (whole ? 1 : 0)) * S::kRows * (D + 2);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float l = l_run[nt][j];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            const int r = warp * S::kRows + 8 * nt + 2 * t4 + j;
-            if (g == 0) {
-                cm[r] = m_ref[nt][j];
-                cl[r] = l;
-            }
+                for (int j = 0; j < 2; ++j) {
+                    float l = l_run[nt][j];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    const int r = 8 * nt + 2 * t4 + j;
+                    if (r >= rows) continue;
+                    if (done) {
+                        const int row = row0 + r, token = row / G;
+                        const size_t at = ((size_t)(now.q0 + token) * p.num_q_heads + kvh * G + row - token * G) * D;
+                        const float inv = __fdiv_rn(fall, l);
 #pragma unroll
-            for (int md = 0; md < KS; ++md)
-                *reinterpret_cast<float2*>(co + r * S::kOutStride + 16 * md + 2 * g) =
-                    make_float2(acc[nt][md][j] * fall, acc[nt][md][2 + j] * fall);
+                        for (int md = 0; md < KS; ++md)
+                            store_pair(p, at + 16 * md + 2 * g, acc[nt][md][j] * inv, acc[nt][md][2 + j] * inv);
+                    } else {
+#pragma unroll
+                        for (int md = 0; md < KS; ++md)
+                            *reinterpret_cast<float2*>(part + r * D + 16 * md + 2 * g) = make_float2(acc[nt][md][j] * fall, acc[nt][md][2 + j] * fall);
+                        if (g == 0) {
+                            part[S::kRows * D + r] = m_ref[nt][j];
+                            part[S::kRows * (D + 1) + r] = l;
+                        }
+                    }
+                }
+            __syncwarp();
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kScaledThreads) {
-        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-        const int row = row0 + r, token = row / G, head = kvh * G + row - token * G;
-        if (first_pos + token + 1 <= T0) continue;                     // sees nothing of this partition
+        now.next(p);
+    }
+    cp_async_wait<0>();
+}
+
+// Joins an item's pieces: a CTA for an item (or some of its rows, where there are few
+// items); 16, 32 or 64 threads hold four components each, and the others take pieces in turn.
+constexpr int kScaledMergeThreads = 256;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kScaledMergeThreads)
+scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
+    begin_overlapped();
+    constexpr int ROWS = 8 * NT;
+    constexpr int LANES = D / 4, SLICES = kScaledMergeThreads / LANES;
+    __shared__ float red[kScaledMergeThreads / 32];
+    __shared__ float4 part_o[kScaledMergeThreads];
+    __shared__ float part_l[SLICES];
+    const int s = blockIdx.y, item = blockIdx.x;
+    const int64_t before = p.stages_before[s];
+    const int stages = (int)(p.stages_before[s + 1] - before);
+    if (stages == 0) return;
+    const int64_t piece = scaled_piece(p.stages_before[p.num_seqs] * p.items, p.workers);
+    const int64_t first = before * p.items + (int64_t)item * stages;
+    const int64_t w0 = first / piece, w1 = (first + stages - 1) / piece;
+    if (w0 == w1) return;                          // whole, and written
+    int L, q0, Q;
+    if (!scaled_sequence(p, s, false, L, q0, Q)) return;
+    const int n = (int)(w1 - w0) + 1;
+    const int kvh = item / p.row_tiles, row0 = (item - kvh * p.row_tiles) * ROWS;
+    const int rows = min(ROWS, Q * p.group - row0);
+    // the first piece of the item lies last among its warp's, the others first
+    auto piece_of = [&](int i) { return p.parts + ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS * (D + 2); };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slice = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    for (int r = blockIdx.z; r < rows; r += gridDim.z) {
         float M = -INFINITY;
+        for (int i = threadIdx.x; i < n; i += kScaledMergeThreads) M = fmaxf(M, piece_of(i)[ROWS * D + r]);
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, cm[w * S::kRows + r]);
-        float sum = 0.f;
+        for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+        __syncthreads();                           // the row before has been read
+        if (lane == 0) red[warp] = M;
+        __syncthreads();
+        M = red[0];
+#pragma unroll
+        for (int w = 1; w < kScaledMergeThreads / 32; ++w) M = fmaxf(M, red[w]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float mw = cm[w * S::kRows + r];
-            const float f = mw == -INFINITY ? (cl[w * S::kRows + r] == 0.f ? 0.f : 1.f) : fast_exp2(mw - M);
-            sum = fmaf(f, cl[w * S::kRows + r], sum);
-            const float4 v = *reinterpret_cast<const float4*>(co + (w * S::kRows + r) * S::kOutStride + d);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int i = slice; i < n; i += SLICES) {
+            const float* part = piece_of(i);
+            const float m = part[ROWS * D + r], l = part[ROWS * (D + 1) + r];
+            const float4 v = *reinterpret_cast<const float4*>(part + r * D + 4 * c);
+            const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - M);
+            sum = fmaf(f, l, sum);
             o.x = fmaf(f, v.x, o.x);
             o.y = fmaf(f, v.y, o.y);
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
-        const float inv = __fdiv_rn(1.f, sum);
-        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        const size_t at = (size_t)(q0 + token) * p.num_q_heads + head;
-        if (p.max_parts == 1) {
-            uint2 w;
-            if (p.bf16) w = make_uint2(MmaOps<__nv_bfloat16>::pack(o.x, o.y), MmaOps<__nv_bfloat16>::pack(o.z, o.w));
-            else w = make_uint2(Ops::pack(o.x, o.y), Ops::pack(o.z, o.w));
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + d) = w;
-        } else {
-            const size_t part = at * p.max_parts + blockIdx.x;
-            *reinterpret_cast<float4*>(p.tmp_out + part * D + d) = o;
-            if (d == 0) {
-                p.max_logits[part] = M;
-                p.exp_sums[part] = sum;
+        part_o[threadIdx.x] = o;
+        if (c == 0) part_l[slice] = sum;
+        __syncthreads();
+        if (threadIdx.x < LANES) {
+#pragma unroll
+            for (int i = 1; i < SLICES; ++i) {
+                const float4 v = part_o[i * LANES + c];
+                o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                sum += part_l[i];
             }
+            const float inv = __fdiv_rn(1.f, sum);
+            const int row = row0 + r, token = row / p.group, head = kvh * p.group + row - token * p.group;
+            const size_t at = ((size_t)(q0 + token) * p.num_q_heads + head) * D + 4 * c;
+            store_pair(p, at, o.x * inv, o.y * inv);
+            store_pair(p, at + 2, o.z * inv, o.w * inv);
         }
     }
 }
 
-// The merge of a row's partitions: 32 or 64 threads per (query token, head) hold four
-// components each, eight rows of them a CTA taking partitions in turn.
-constexpr int kScaledMergeThreads = 256;
+// The merge of a row's partitions (scaled_prefill.cuh), by the same threads.
 constexpr int kScaledMergeParts = 512;             // weights at a time
 
 template <int D>
@@ -537,24 +692,28 @@ cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, cudaStream_t stream
 template <typename CT, int D, int NT>
 cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     using S = ScaledShape<D, NT>;
-    auto kernel = scaled_attention_kernel<CT, D, NT>;
-    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), S::kBytes);
+    constexpr int W = kScaledWarps;
+    auto kernel = scaled_attention_kernel<CT, D, NT, W>;
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), W * S::kWarpBytes);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, p, dim3(p.max_parts, p.num_kv_heads * p.row_tiles, p.num_seqs), kScaledThreads, S::kBytes, stream);
+    e = launch_overlapped(kernel, p, dim3(p.workers / W), W * 32, W * S::kWarpBytes, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t all = (int64_t)p.items * p.num_seqs;
+    const int rows = all >= 608 ? 1 : (int)(608 / all < 8 * NT ? 608 / all : 8 * NT);
+    return launch_overlapped(scaled_join_kernel<D, NT>, p, dim3(p.items, p.num_seqs, rows), kScaledMergeThreads, 0, stream);
 }
 
 template <typename CT, int D>
 cudaError_t launch_scaled_head(const ScaledAttnParams& p, cudaStream_t stream) {
-    cudaError_t e;
-    if (p.tile_rows == 256) {
-        if constexpr (D < 256) e = launch_scaled_prefill<CT, D>(p, stream);
-        else return cudaErrorInvalidValue;
-    } else if (p.tile_rows == 8) e = launch_scaled_rows<CT, D, 1>(p, stream);
-    else if (p.tile_rows == 16) e = launch_scaled_rows<CT, D, 2>(p, stream);
-    else if constexpr (D < 256) e = launch_scaled_rows<CT, D, 4>(p, stream);
-    else return cudaErrorInvalidValue;
-    if (e != cudaSuccess || p.max_parts == 1) return e;
-    return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
+    if (p.tile_rows == 8) return launch_scaled_rows<CT, D, 1>(p, stream);
+    if (p.tile_rows == 16) return launch_scaled_rows<CT, D, 2>(p, stream);
+    if constexpr (D < 256) {
+        if (p.tile_rows == 32) return launch_scaled_rows<CT, D, 4>(p, stream);
+        const cudaError_t e = launch_scaled_prefill<CT, D>(p, stream);
+        if (e != cudaSuccess || p.max_parts == 1) return e;
+        return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <typename CT>

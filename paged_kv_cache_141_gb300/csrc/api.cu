@@ -1249,7 +1249,8 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
         return PA_ERR_INVALID_ARG;
     if (!(q_dtype == PA_F16 || q_dtype == PA_BF16) || !is_scaled_type(cache_dtype) ||
         !supported_head_size(head_size) || block_size > 1024 || num_seqs > 65535 ||
-        max_context_len > kMaxScaledContext)
+        max_context_len > kMaxScaledContext ||
+        num_blocks > 0xffffffffll / ((int64_t)num_kv_heads * block_size))      // the pool's rows count in 32 bits
         return PA_ERR_UNSUPPORTED;
     if (num_queries == 0) return PA_OK;
     if (num_seqs == 0 || max_queries_per_seq == 0) return PA_ERR_INVALID_ARG;
@@ -1284,6 +1285,10 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
         p.exp_sums = reinterpret_cast<float*>(w + l.exp_sums);
     }
     p.items = l.row_tiles * num_kv_heads;
+    int log = 0;                                  // 2^log >= block_size
+    while (1 << log < block_size) ++log;
+    p.block_mul = (uint32_t)((1ull << (31 + log)) / block_size + 1);
+    p.block_shift = 31 + log;
     p.workers = l.workers;
     p.status = dev_status;
     p.num_blocks = num_blocks;

@@ -367,6 +367,8 @@ struct ScaledAttnParams {
     int row_tiles;                // such tiles of a sequence and KV head
     int items;                    // row_tiles * Hkv
     int workers;                  // warps that share the stages
+    uint32_t block_mul;           // t / block_size = t * block_mul >> block_shift, t < 2^31
+    int block_shift;
     float q_mul;                  // scale * log2(e)
     int bf16;                     // the query's and the output's type; else binary16
 };

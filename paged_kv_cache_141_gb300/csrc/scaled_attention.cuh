@@ -81,6 +81,9 @@ __device__ __forceinline__ bool scaled_sequence(const ScaledAttnParams& p, int s
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
@@ -96,6 +99,15 @@ template <int D>
 __device__ __forceinline__ int tile_at(int r, int c) {
     if constexpr (D == 64) return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ ((r >> 1) & 7)) << 4);
     else return r * D + ((c >> 3) << 7) + (((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void ldmatrix_x4_at(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans_at(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
 // Two codes of a word to a binary16 pair. The bytes named by sel's digits 0 and 2.
@@ -158,7 +170,8 @@ __device__ __forceinline__ void scaled_query(const ScaledAttnParams& p, int q0, 
             if constexpr (S::kQReg) qr[nt * S::KS + ks] = f;
             else qf[(nt * S::KS + ks) * 32 + lane] = f;
         }
-        const float u = p.q_mul * unit * (std::is_same<CT, e4m3_t>::value ? 256.f : 1.f);
+        // (never zero: that must not meet a masked score)
+        const float u = fmaxf(p.q_mul * unit * (std::is_same<CT, e4m3_t>::value ? 256.f : 1.f), 1.17549435e-38f);
         mul[nt][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
         mul[nt][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
@@ -176,15 +189,17 @@ __device__ __forceinline__ int scaled_stages(const ScaledAttnParams& p, int s, b
     return scaled_sequence(p, s, report, L, q0, Q) ? (L + kScaledStage - 1) / kScaledStage : 0;
 }
 
-// A place in the line of stages: stage k of item `item` of sequence s.
+// A place in the line of stages: stage k of row tile `tile` of KV head kvh of sequence s.
 struct ScaledPlace {
-    int s, item, k, stages;                        // the sequence's stages
+    int s, kvh, tile, k, stages;                   // the sequence's stages
     int L, q0, Q;
     __device__ __forceinline__ void next(const ScaledAttnParams& p) {
         if (++k < stages) return;
         k = 0;
-        if (++item < p.items) return;
-        item = 0;
+        if (++tile < p.row_tiles) return;
+        tile = 0;
+        if (++kvh < p.num_kv_heads) return;
+        kvh = 0;
         do {
             ++s;
             stages = s < p.num_seqs ? scaled_stages(p, s, false, L, q0, Q) : 0;
@@ -277,8 +292,10 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     now.stages = scaled_stages(p, now.s, false, now.L, now.q0, now.Q);
     {
         const int64_t in = begin - s_before[warp] * p.items;
-        now.item = (int)(in / now.stages);
-        now.k = (int)(in - (int64_t)now.item * now.stages);
+        const int item = (int)(in / now.stages);
+        now.k = (int)(in - (int64_t)item * now.stages);
+        now.kvh = item / p.row_tiles;
+        now.tile = item - now.kvh * p.row_tiles;
     }
 
     // ------------------------------------------------------------ the ring
@@ -286,41 +303,52 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     uint2* qf = reinterpret_cast<uint2*>(ring + NST * S::kStageBytes);
     const uint32_t ring_u32 = smem_u32(ring);
     const int cr = lane / CPR, cc = lane % CPR;
-    // the next stage to copy, and the block of this lane's token in it, read a stage ahead
+    const uint8_t* k_from = p.k_cache + cc * 16;
+    const uint8_t* v_from = p.v_cache + cc * 16;
+    // the next stage to copy; the place of this lane's token in it, found a stage ahead
     ScaledPlace ahead = now;
     int left = count;                              // stages not yet copied
-    int next_block = -1;
+    int next_block = -1, next_in = 0;
     auto find = [&] {
         const int t = ahead.k * kScaledStage + lane;
-        next_block = left > 0 && t < ahead.L ? p.block_tables[(size_t)ahead.s * p.max_blocks + t / B] : -1;
+        const int j = (int)((uint64_t)(uint32_t)t * p.block_mul >> p.block_shift);      // t / B
+        next_in = t - j * B;
+        next_block = left > 0 && t < ahead.L ? p.block_tables[(size_t)ahead.s * p.max_blocks + j] : -1;
     };
     find();
     auto issue = [&](int slot) {
         if (left > 0) {
-            const int t = ahead.k * kScaledStage + lane;
-            const int kvh = ahead.item / p.row_tiles;
-            const int blk = next_block;
-            bool there = t < ahead.L;
+            const bool inside = ahead.k * kScaledStage + lane < ahead.L;
+            const bool there = (uint32_t)next_block < (uint32_t)p.num_blocks;
+            if (inside && !there && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+            const uint32_t slab = there ? (uint32_t)next_block * p.num_kv_heads + ahead.kvh : 0u;
+            const uint32_t row = slab * B + next_in;
             --left;
             ahead.next(p);
             find();
-            if (there && (blk < 0 || blk >= p.num_blocks)) {
-                if (p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
-                there = false;
-            }
-            const int64_t slab = there ? (int64_t)blk * p.num_kv_heads + kvh : 0;
-            const int64_t row = there ? slab * B + (t - t / B * B) : -1;
             const uint32_t st = ring_u32 + slot * S::kStageBytes;
             cp_async4(st + 2 * S::kTile + lane * 4, p.k_scales + slab, there);
             cp_async4(st + 2 * S::kTile + (kScaledStage + lane) * 4, p.v_scales + slab, there);
+            const uint32_t all = __ballot_sync(0xffffffffu, there);
+            if (all == 0xffffffffu) {
 #pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-                const int r = i * RPP + cr;
-                const int64_t src = __shfl_sync(0xffffffffu, row, r);
-                const size_t off = (size_t)max(src, (int64_t)0) * D + cc * 16;
-                const uint32_t d = st + tile_at<D>(r, cc);
-                cp_async16(d, p.k_cache + off, src >= 0);
-                cp_async16(d + S::kTile, p.v_cache + off, src >= 0);
+                for (int i = 0; i < CPR; ++i) {
+                    const size_t off = (size_t)__shfl_sync(0xffffffffu, row, i * RPP + cr) * D;
+                    const uint32_t d = st + tile_at<D>(i * RPP + cr, cc);
+                    cp_async16(d, k_from + off);
+                    cp_async16(d + S::kTile, v_from + off);
+                }
+            } else {                               // zeros where there is no token
+#pragma unroll
+                for (int i = 0; i < CPR; ++i) {
+                    const int r = i * RPP + cr;
+                    const bool here = all >> r & 1u;
+                    const uint32_t from = __shfl_sync(0xffffffffu, row, r);
+                    const size_t off = here ? (size_t)from * D : 0;
+                    const uint32_t d = st + tile_at<D>(r, cc);
+                    cp_async16(d, k_from + off, here);
+                    cp_async16(d + S::kTile, v_from + off, here);
+                }
             }
         }
         cp_async_commit();
@@ -338,8 +366,8 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     for (int i = 0; i < count; ++i) {
         if (i == 0 || now.k == 0) {
             // ---- an item begins
-            kvh = now.item / p.row_tiles;
-            row0 = (now.item - kvh * p.row_tiles) * S::kRows;
+            kvh = now.kvh;
+            row0 = now.tile * S::kRows;
             rows = max(0, min(S::kRows, now.Q * G - row0));
             whole = now.k == 0;
             scaled_query<CT, D, NT>(p, now.q0, kvh, row0, rows, lane, qr, qf, hm);
@@ -365,9 +393,8 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
         cp_async_wait<NST - 2>();
         __syncwarp();
         issue(slot == 0 ? NST - 1 : slot - 1);
-        const uint8_t* Kst = ring + slot * S::kStageBytes;
-        const uint8_t* Vst = Kst + S::kTile;
-        const float* scales = reinterpret_cast<const float*>(Kst + 2 * S::kTile);
+        const float* scales = reinterpret_cast<const float*>(ring + slot * S::kStageBytes + 2 * S::kTile);
+        const uint32_t k_at = ring_u32 + slot * S::kStageBytes, v_at = k_at + S::kTile;
         const int key0 = now.k * kScaledStage;
 
         // ---- S = C_K Q^T
@@ -382,7 +409,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
             for (int kp = 0; kp < KS / 2; ++kp) {
                 uint32_t x[4];
-                ldmatrix_x4(x, Kst + tile_at<D>(row, 2 * kp + (mi >> 1)));
+                ldmatrix_x4_at(x, k_at + tile_at<D>(row, 2 * kp + (mi >> 1)));
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                     const uint32_t x0 = biased<CT>(x[2 * h2]), x1 = biased<CT>(x[2 * h2 + 1]);
@@ -409,21 +436,28 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             vb[i] = scales[kScaledStage + g + 8 * i];
         }
         const int vexp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(scales[kScaledStage + lane]) << 1 >> 24)) - 127;
-        const bool masked = key0 + kScaledStage > all_see;
         bool move = vexp > e_ref;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float mx = -INFINITY;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = sc[nt][i >> 1][2 * (i & 1) + j] * ka[i] * hm[nt][j];
-                    if (masked && key0 + g + 8 * i >= lim[nt][j]) v = -INFINITY;
-                    sc[nt][i >> 1][2 * (i & 1) + j] = v;
-                    mx = fmaxf(mx, v);
-                }
-                move |= mx > m_ref[nt][j] + 8.f;
+                for (int j = 0; j < 2; ++j) sc[nt][i >> 1][2 * (i & 1) + j] *= ka[i];
+        if (key0 + kScaledStage > all_see) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (key0 + g + 8 * i >= lim[nt][j]) sc[nt][i >> 1][2 * (i & 1) + j] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mx = fmaxf(fmaxf(sc[nt][0][j], sc[nt][0][2 + j]), fmaxf(sc[nt][1][j], sc[nt][1][2 + j]));
+                move |= mx * hm[nt][j] > m_ref[nt][j] + 8.f;
             }
         if (__any_sync(0xffffffffu, move)) {
             const int e_new = max(e_ref, vexp > e_ref ? vexp + 2 : e_ref);
@@ -438,7 +472,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float m_new = fmaxf(m_ref[nt][j], mx);
+                    const float m_new = fmaxf(m_ref[nt][j], mx * hm[nt][j]);
                     const float al = m_new == -INFINITY || m_ref[nt][j] == -INFINITY ? 1.f : fast_exp2(m_ref[nt][j] - m_new);
                     m_ref[nt][j] = m_new;
                     l_run[nt][j] *= al;
@@ -465,7 +499,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                 const float m = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = fast_exp2(sc[nt][i >> 1][2 * (i & 1) + j] - m);
+                    const float e = fast_exp2(fmaf(sc[nt][i >> 1][2 * (i & 1) + j], hm[nt][j], -m));
                     l_run[nt][j] += e;
                     w[j][i] = e * vb[i];
                 }
@@ -479,7 +513,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
         for (int md = 0; md < KS; ++md) {
             uint32_t y[4];
-            ldmatrix_x4_trans(y, Vst + tile_at<D>(8 * mi + r8, md));
+            ldmatrix_x4_trans_at(y, v_at + tile_at<D>(8 * mi + r8, md));
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt) {
                 const uint32_t lo = biased<CT>(y[2 * kt]), hi = biased<CT>(y[2 * kt + 1]);
@@ -535,24 +569,25 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     cp_async_wait<0>();
 }
 
-// Joins an item's pieces: a CTA for an item (or some of its rows, where there are few
-// items); 16, 32 or 64 threads hold four components each, and the others take pieces in turn.
+// Joins an item's pieces, a CTA for an item (or for some of its rows, where there are few
+// items). Few pieces: a warp a row. Many (a long context alone on the device): all warps a
+// row, and one of them joins their sums.
 constexpr int kScaledMergeThreads = 256;
+constexpr int kScaledFewPieces = 16;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kScaledMergeThreads)
 scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
-    constexpr int ROWS = 8 * NT;
-    constexpr int LANES = D / 4, SLICES = kScaledMergeThreads / LANES;
-    __shared__ float red[kScaledMergeThreads / 32];
-    __shared__ float4 part_o[kScaledMergeThreads];
-    __shared__ float part_l[SLICES];
+    constexpr int ROWS = 8 * NT, W = kScaledMergeThreads / 32;
+    constexpr int E = D / 32;                      // a lane's components, neighbours
+    __shared__ float s_max[W], s_sum[W];
+    __shared__ float s_out[W][D];
     const int s = blockIdx.y, item = blockIdx.x;
-    const int64_t before = p.stages_before[s];
-    const int stages = (int)(p.stages_before[s + 1] - before);
+    const int64_t before = p.stages_before[s], after = p.stages_before[s + 1], total = p.stages_before[p.num_seqs];
+    const int stages = (int)(after - before);
     if (stages == 0) return;
-    const int64_t piece = scaled_piece(p.stages_before[p.num_seqs] * p.items, p.workers);
+    const int64_t piece = scaled_piece(total * p.items, p.workers);
     const int64_t first = before * p.items + (int64_t)item * stages;
     const int64_t w0 = first / piece, w1 = (first + stages - 1) / piece;
     if (w0 == w1) return;                          // whole, and written
@@ -564,47 +599,67 @@ scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
     // the first piece of the item lies last among its warp's, the others first
     auto piece_of = [&](int i) { return p.parts + ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS * (D + 2); };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slice = threadIdx.x / LANES, c = threadIdx.x % LANES;
-    for (int r = blockIdx.z; r < rows; r += gridDim.z) {
-        float M = -INFINITY;
-        for (int i = threadIdx.x; i < n; i += kScaledMergeThreads) M = fmaxf(M, piece_of(i)[ROWS * D + r]);
+    // pieces i0, i0 + step, ..: their maximum, and sums under it
+    auto gather = [&](int r, int i0, int step, float& M, float& sum, float (&o)[E]) {
+        M = -INFINITY;
+        for (int i = i0 + lane * step; i < n; i += 32 * step) M = fmaxf(M, piece_of(i)[ROWS * D + r]);
 #pragma unroll
         for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-        __syncthreads();                           // the row before has been read
-        if (lane == 0) red[warp] = M;
-        __syncthreads();
-        M = red[0];
+        sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < kScaledMergeThreads / 32; ++w) M = fmaxf(M, red[w]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int i = slice; i < n; i += SLICES) {
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 8
+        for (int i = i0; i < n; i += step) {
             const float* part = piece_of(i);
             const float m = part[ROWS * D + r], l = part[ROWS * (D + 1) + r];
-            const float4 v = *reinterpret_cast<const float4*>(part + r * D + 4 * c);
+            float v[E];
+            RowLoader<float, E>::load(part + r * D + lane * E, v);
             const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - M);
             sum = fmaf(f, l, sum);
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
-        }
-        part_o[threadIdx.x] = o;
-        if (c == 0) part_l[slice] = sum;
-        __syncthreads();
-        if (threadIdx.x < LANES) {
 #pragma unroll
-            for (int i = 1; i < SLICES; ++i) {
-                const float4 v = part_o[i * LANES + c];
-                o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-                sum += part_l[i];
+            for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[e], o[e]);
+        }
+    };
+    auto store = [&](int r, float sum, const float (&o)[E]) {
+        const float inv = __fdiv_rn(1.f, sum);
+        const int row = row0 + r, token = row / p.group, head = kvh * p.group + row - token * p.group;
+        const size_t at = ((size_t)(q0 + token) * p.num_q_heads + head) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) store_pair(p, at + e, o[e] * inv, o[e + 1] * inv);
+    };
+    float M, sum, o[E];
+    if (n <= kScaledFewPieces) {
+        for (int r = blockIdx.z * W + warp; r < rows; r += gridDim.z * W) {
+            gather(r, 0, 1, M, sum, o);
+            store(r, sum, o);
+        }
+        return;
+    }
+    for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+        gather(r, warp, W, M, sum, o);
+        __syncthreads();                           // the row before has been read
+        if (lane == 0) {
+            s_max[warp] = M;
+            s_sum[warp] = sum;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_out[warp][lane * E + e] = o[e];
+        __syncthreads();
+        if (warp == 0) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) most = fmaxf(most, s_max[w]);
+            sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f = s_max[w] == -INFINITY ? (s_sum[w] == 0.f ? 0.f : 1.f) : fast_exp2(s_max[w] - most);
+                sum = fmaf(f, s_sum[w], sum);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(f, s_out[w][lane * E + e], o[e]);
             }
-            const float inv = __fdiv_rn(1.f, sum);
-            const int row = row0 + r, token = row / p.group, head = kvh * p.group + row - token * p.group;
-            const size_t at = ((size_t)(q0 + token) * p.num_q_heads + head) * D + 4 * c;
-            store_pair(p, at, o.x * inv, o.y * inv);
-            store_pair(p, at + 2, o.z * inv, o.w * inv);
+            store(r, sum, o);
         }
     }
 }

@@ -96,6 +96,14 @@ bool is_scaled_type(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_INT8; }
 
 constexpr int kMaxScaledContext = 1 << 30;    // positions plus a partition stay in 32 bits
 
+// mul, shift: n / d = n * mul >> shift for 0 <= n < 2^31 (the product in 64 bits).
+void divide_by(int d, uint32_t& mul, int& shift) {
+    int log = 0;                              // 2^log >= d
+    while (1ll << log < d) ++log;
+    mul = (uint32_t)((1ull << (31 + log)) / d + 1);
+    shift = 31 + log;
+}
+
 struct ScaledPlan {
     int tile_rows, row_tiles;
     int workers;                              // warp-level MMAs
@@ -1285,11 +1293,10 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
         p.exp_sums = reinterpret_cast<float*>(w + l.exp_sums);
     }
     p.items = l.row_tiles * num_kv_heads;
-    int log = 0;                                  // 2^log >= block_size
-    while (1 << log < block_size) ++log;
-    p.block_mul = (uint32_t)((1ull << (31 + log)) / block_size + 1);
-    p.block_shift = 31 + log;
+    p.group = num_q_heads / num_kv_heads;
     p.workers = l.workers;
+    divide_by(block_size, p.block_mul, p.block_shift);
+    divide_by(p.group, p.group_mul, p.group_shift);
     p.status = dev_status;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
@@ -1298,7 +1305,6 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     p.max_queries = max_queries_per_seq;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
-    p.group = num_q_heads / num_kv_heads;
     p.block_size = block_size;
     p.max_context_len = max_context_len;
     p.partition_size = l.partition_size;

@@ -369,20 +369,19 @@ struct ScaledAttnParams {
     int workers;                  // warps that share the stages
     uint32_t block_mul;           // t / block_size = t * block_mul >> block_shift, t < 2^31
     int block_shift;
+    uint32_t group_mul;           // r / group, alike
+    int group_shift;
     float q_mul;                  // scale * log2(e)
     int bf16;                     // the query's and the output's type; else binary16
 };
 
-// Warps of a CTA that share the stages, and how many of those a worker takes: at least
-// kScaledLeast, as a piece costs a start and an end.
+// Warps of a CTA that share the stages, and the stages of a worker.
 constexpr int kScaledWarps = 4;
-constexpr int kScaledLeast = 4;
 #ifdef __CUDACC__
 __host__ __device__
 #endif
 inline int64_t scaled_piece(int64_t stages, int workers) {
-    const int64_t n = (stages + workers - 1) / workers;
-    return n < kScaledLeast ? kScaledLeast : n;
+    return stages <= workers ? 1 : (stages + workers - 1) / workers;
 }
 
 cudaError_t launch_scaled_attention_int8(const ScaledAttnParams& p, int head_size, cudaStream_t stream);

@@ -257,7 +257,8 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
         // the thread whose sequences hold a warp's first stage finds the sequence
         const int64_t before = upto - mine;
         for (int w = 0; w < W; ++w) {
-            const int64_t at = (blockIdx.x * W + w) * piece / p.items;
+            const int64_t from = (blockIdx.x * W + w) * piece;
+            const int64_t at = from < INT32_MAX ? (uint32_t)from / (uint32_t)p.items : from / p.items;
             if (at >= before && at < upto) {
                 int64_t b = before;
                 int s = s_lo;
@@ -443,7 +444,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) sc[nt][i >> 1][2 * (i & 1) + j] *= ka[i];
-        if (key0 + kScaledStage > all_see) {
+        if (__any_sync(0xffffffffu, key0 + kScaledStage > all_see)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -505,7 +506,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pb[nt][i >> 1][i & 1] = movmatrix_trans(Ops::pack(w[0][i], w[1][i]));
+            for (int k = 0; k < 4; ++k) pb[nt][k >> 1][k & 1] = movmatrix_trans(Ops::pack(w[0][k], w[1][k]));
         }
 
         // ---- O^T += C_V^T P^T: a chunk is 16 components of all 32 tokens; fragment
@@ -584,40 +585,68 @@ scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
     __shared__ float s_max[W], s_sum[W];
     __shared__ float s_out[W][D];
     const int s = blockIdx.y, item = blockIdx.x;
+    // all that says where the pieces lie, in one round of loads
     const int64_t before = p.stages_before[s], after = p.stages_before[s + 1], total = p.stages_before[p.num_seqs];
-    const int stages = (int)(after - before);
-    if (stages == 0) return;
-    const int64_t piece = scaled_piece(total * p.items, p.workers);
-    const int64_t first = before * p.items + (int64_t)item * stages;
-    const int64_t w0 = first / piece, w1 = (first + stages - 1) / piece;
-    if (w0 == w1) return;                          // whole, and written
     int L, q0, Q;
-    if (!scaled_sequence(p, s, false, L, q0, Q)) return;
+    const bool fine = scaled_sequence(p, s, false, L, q0, Q);
+    const int stages = (int)(after - before);
+    if (stages == 0 || !fine) return;
+    const int64_t line = total * p.items;
+    const int64_t piece = scaled_piece(line, p.workers);
+    const int64_t first = before * p.items + (int64_t)item * stages;
+    int64_t w0, w1;
+    if (line < INT32_MAX) {
+        w0 = (uint32_t)first / (uint32_t)piece;
+        w1 = (uint32_t)(first + stages - 1) / (uint32_t)piece;
+    } else {
+        w0 = first / piece;
+        w1 = (first + stages - 1) / piece;
+    }
+    if (w0 == w1) return;                          // whole, and written
     const int n = (int)(w1 - w0) + 1;
     const int kvh = item / p.row_tiles, row0 = (item - kvh * p.row_tiles) * ROWS;
     const int rows = min(ROWS, Q * p.group - row0);
     // the first piece of the item lies last among its warp's, the others first
     auto piece_of = [&](int i) { return p.parts + ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS * (D + 2); };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // pieces i0, i0 + step, ..: their maximum, and sums under it
+    // pieces i0, i0 + step, ..: their maximum, and sums under it; eight at a time, whose
+    // loads are in flight together
+    constexpr int kAtOnce = 8;
     auto gather = [&](int r, int i0, int step, float& M, float& sum, float (&o)[E]) {
         M = -INFINITY;
-        for (int i = i0 + lane * step; i < n; i += 32 * step) M = fmaxf(M, piece_of(i)[ROWS * D + r]);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
         sum = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 8
-        for (int i = i0; i < n; i += step) {
-            const float* part = piece_of(i);
-            const float m = part[ROWS * D + r], l = part[ROWS * (D + 1) + r];
-            float v[E];
-            RowLoader<float, E>::load(part + r * D + lane * E, v);
-            const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - M);
-            sum = fmaf(f, l, sum);
+        for (int i = i0; i < n; i += kAtOnce * step) {
+            float m[kAtOnce], l[kAtOnce], v[kAtOnce][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[e], o[e]);
+            for (int k = 0; k < kAtOnce; ++k) {
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+                if (i + k * step < n) {
+                    const float* part = piece_of(i + k * step);
+                    m[k] = part[ROWS * D + r];
+                    l[k] = part[ROWS * (D + 1) + r];
+                    RowLoader<float, E>::load(part + r * D + lane * E, v[k]);
+                }
+            }
+            float most = M;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) most = fmaxf(most, m[k]);
+            const float was = M == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : fast_exp2(M - most);
+            M = most;
+            sum *= was;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= was;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float f = m[k] == -INFINITY ? (l[k] == 0.f ? 0.f : 1.f) : fast_exp2(m[k] - M);
+                sum = fmaf(f, l[k], sum);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[k][e], o[e]);
+            }
         }
     };
     auto store = [&](int r, float sum, const float (&o)[E]) {

@@ -4,15 +4,20 @@
 // Work unit: (sequence, KV head, two tiles of 128 query rows, partition of the
 // context), one CTA on an SM. Rows are (query token, head of the group) pairs,
 // token-major, as in scaled_attention.cuh, whose definitions hold here. Key tiles of
-// 128. Roles:
-//   warps 0-3, 4-7   softmax of query tile 0, 1: a thread a row;
-//   warp 9           issues tcgen05.mma (one lane), tiles interleaved: S0, S1, then
-//                    PV0, S0', PV1, S1', ...
-//   warps 8, 10, 12  load K: codes from the cache's blocks into registers, a slice of
-//   and 11, 13, 15   32 keys ahead (V: the other three), widened to binary16 -- exactly,
-//                    as in scaled_attention.cuh -- into the swizzled tiles that the MMAs read.
+// 128. Two streams, each with scores, weights and an output of its own in TMEM, so
+// that the tensor cores work for one while the other's softmax runs: the two query
+// tiles over the same key tiles, or, where one tile holds all rows (drafts), the
+// even and the odd key tiles, joined at the end. Roles:
+//   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
+//   warp 9           issues tcgen05.mma (one lane): S0, S1, then PV0, S0', PV1, S1', ...
+//   warps 8, 10, 12  load K: codes from the cache's blocks into registers, 16 keys at a
+//   and 11, 13, 15   time and two such slices ahead (V: the other three), widened to
+//                    binary16 -- exactly, as in scaled_attention.cuh -- into the swizzled
+//                    tiles that the MMAs read.
 // The codes go through registers and not through shared memory: binary16 tiles and queries
-// take all of it, and the widening needs the registers anyway.
+// take all of it, and the widening needs the registers anyway. (A loader's own
+// fence between its stores and the MMAs' reads waited for its loads in flight: 541 us
+// for 8 chunks of 512, 510 with the fence in the MMA issuer, which waits for the tile.)
 //
 // The scales stay out of the tiles. Blocks are multiples of 16 tokens here, so a
 // group of 16 columns of S has one key scale a and one value scale b: with raw
@@ -34,8 +39,9 @@
 namespace pagedkv {
 
 constexpr int kSpLoaders = 3;                      // warps an operand
-constexpr int kSpSlice = 32;                       // keys a warp widens at a time
-constexpr int kSpRing = 4;                         // tiles whose scales are kept: K stages + 1 at least
+constexpr int kSpSlice = 16;                       // keys a warp widens at a time
+constexpr int kSpSlices = 128 / kSpSlice;
+constexpr int kSpRing = 8;                         // tiles whose scales are kept
 constexpr float kSpMoveLog2 = 8.f;                 // the running maximum moves when a score passes it by this
 
 template <int D>
@@ -58,10 +64,13 @@ struct SpShape {
     static constexpr int kTileCols = N + D;                            // S (then P), O
     static_assert(2 * kTileCols <= kTmemCols, "TMEM columns");
     static_assert(kAlloc <= kTcSmemLimit, "shared memory");
-    static_assert(kSpRing >= NSK + 1 && kSpRing >= NSV + 1, "scales live until both softmaxes have read them");
+    // Scales live until both softmaxes have read them: a loader writes those of tile j once it
+    // has passed the wait for tile j - 1's slot, so S of tile j - 1 - NSK (K) or P.V of tile
+    // j - 1 - NSV (V) is done. S of a tile comes after the weights of the tile two before it.
+    static_assert(kSpRing >= NSK + 3 && kSpRing >= NSV + 1, "scales");
 };
 
-// One loader warp's slices of an operand: slice n = 4 j + q is keys 32 q .. of tile j.
+// One loader warp's slices of an operand: slice n = 8 j + q is keys 16 q .. of tile j.
 template <typename CT, int D, int NS, bool kKeys>
 __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring, float2* scales, uint64_t* full,
                                         uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend, int ntiles,
@@ -70,62 +79,59 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring
     constexpr int CPR = D / 16;                    // 16-code chunks of a row
     constexpr int PER = kSpSlice * CPR / 32;       // of a lane's
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
-    const uint8_t* cache = kKeys ? p.k_cache : p.v_cache;
     const float* block_scales = kKeys ? p.k_scales : p.v_scales;
     const int B = p.block_size;
-    const int last = 4 * ntiles;
+    const int last = kSpSlices * ntiles;
     // eight lanes that store together hold two rows of one 64-column span, in all banks
     const int chunk = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
     const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
     constexpr int STEP = 32 / CPR;                 // rows of a pass
-    auto block_of = [&](int n) {
-        const int key = T0 + n * kSpSlice + lane;
-        return n < last && key < kend ? table[key / B] : -1;
+    const uint8_t* cache = (kKeys ? p.k_cache : p.v_cache) + chunk * 16;
+    // slices lie in one block each: blocks are multiples of 16 tokens
+    auto block_of = [&](int n, int& in) {
+        const int key = T0 + n * kSpSlice;
+        const int j = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
+        in = key - j * B;
+        return n < last && key < kend ? table[j] : -1;
     };
-    uint4 buf[PER];
-    float scale = 0.f;
-    auto fetch = [&](int n, int blk, uint4 (&w)[PER], float& sc) {
-        const int key = T0 + n * kSpSlice + lane;
-        bool there = n < last && key < kend;
-        if (there && (blk < 0 || blk >= p.num_blocks)) {
-            if (p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+    struct Slice {
+        uint4 w[PER];
+        float scale;
+    };
+    auto fetch = [&](int n, int blk, int in, Slice& to) {
+        const int key = T0 + n * kSpSlice;
+        const int rows = n < last ? min(kSpSlice, kend - key) : 0;
+        bool there = rows > 0;
+        if (there && (uint32_t)blk >= (uint32_t)p.num_blocks) {
+            if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
             there = false;
         }
-        const int64_t slab = there ? (int64_t)blk * p.num_kv_heads + kvh : 0;
-        const int64_t row = there ? slab * B + (key - key / B * B) : -1;
-        sc = there && (lane & 15) == 0 ? block_scales[slab] : 0.f;
+        const uint32_t slab = there ? (uint32_t)blk * p.num_kv_heads + kvh : 0u;
+        const uint8_t* from = cache + (size_t)(slab * B + in + row0) * D;
+        to.scale = there ? block_scales[slab] : 0.f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t r = __shfl_sync(0xffffffffu, row, i * STEP + row0);
-            w[i] = r >= 0 ? *reinterpret_cast<const uint4*>(cache + (size_t)r * D + chunk * 16) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int i = 0; i < PER; ++i)
+            to.w[i] = there && i * STEP + row0 < rows ? *reinterpret_cast<const uint4*>(from + i * STEP * D) : make_uint4(0u, 0u, 0u, 0u);
     };
-    int blk = block_of(which);
-    if (which < last) fetch(which, blk, buf, scale);
-    blk = block_of(which + kSpLoaders);
-    for (int n = which; n < last; n += kSpLoaders) {
-        uint4 ahead[PER];
-        float scale_ahead = 0.f;
-        const int j = n >> 2, q = n & 3;
-        if ((lane & 15) == 0) {
-            float* sp = reinterpret_cast<float*>(scales + (j % kSpRing) * 8 + q * 2 + (lane >> 4));
-            if (kKeys) sp[0] = scale;
-            else sp[1] = log2f(scale);
+    auto store = [&](int n, const Slice& from) -> bool {
+        const int j = n / kSpSlices, q = n % kSpSlices;
+        if (lane == 0) {
+            float* sp = reinterpret_cast<float*>(scales + (j % kSpRing) * kSpSlices + q);
+            if (kKeys) sp[0] = from.scale;
+            else sp[1] = log2f(from.scale);
+            mbar_arrive(&scale_bar[j % kSpRing]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&scale_bar[j % kSpRing]);
-        fetch(n + kSpLoaders, blk, ahead, scale_ahead);
-        blk = block_of(n + 2 * kSpLoaders);
         const int st = j % NS;
         if (j >= NS) {
             const bool ok = tc_wait(&empty[st], (uint32_t)((j / NS - 1) & 1), p.status, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) return;
+            if (!__all_sync(0xffffffffu, ok)) return false;
         }
         uint8_t* tile = ring + st * Sh::kTile;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int r = q * kSpSlice + i * STEP + row0;
-            const uint32_t in[4] = {buf[i].x, buf[i].y, buf[i].z, buf[i].w};
+            const uint32_t in[4] = {from.w[i].x, from.w[i].y, from.w[i].z, from.w[i].w};
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -139,10 +145,25 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);     // the MMA issuer, which waits for it, has the fence between the proxies
-#pragma unroll
-        for (int i = 0; i < PER; ++i) buf[i] = ahead[i];
-        scale = scale_ahead;
-    }
+        return true;
+    };
+    // two slices in flight while a third is widened; the blocks' ids one further ahead
+    Slice a, b, c;
+    int in, n = which;
+    int blk = block_of(n, in);
+    fetch(n, blk, in, a);
+    blk = block_of(n + kSpLoaders, in);
+    fetch(n + kSpLoaders, blk, in, b);
+    blk = block_of(n + 2 * kSpLoaders, in);
+    auto step = [&](const Slice& cur, Slice& next) -> bool {
+        if (n >= last) return false;
+        fetch(n + 2 * kSpLoaders, blk, in, next);
+        blk = block_of(n + 3 * kSpLoaders, in);
+        if (!store(n, cur)) return false;
+        n += kSpLoaders;
+        return true;
+    };
+    while (step(a, c) && step(b, a) && step(c, b)) {}
 }
 
 template <typename CT, int D, bool kTwoTerms>
@@ -176,24 +197,27 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     const int G = p.group;
     const int row0 = pair * 2 * kTcRows, rows = min(2 * kTcRows, Q * G - row0);
     if (rows <= 0) return;
-    const bool two = rows > kTcRows;
+    const bool two = rows > kTcRows;               // query tiles; else the streams take alternate key tiles
     const int first_pos = L - Q;
     const int seen = first_pos + (row0 + rows - 1) / G + 1;
     const int T0 = blockIdx.x * p.partition_size;
     if (T0 >= seen) return;                        // (an empty context has no query here)
     const int kend = min(T0 + p.partition_size, seen);
     const int ntiles = (kend - T0 + N - 1) / N;
+    // stream t's steps, and the key tile of step i
+    auto steps_of = [&](int t) { return two ? ntiles : (ntiles + 1 - t) / 2; };
+    auto tile_of = [&](int t, int i) { return two ? i : 2 * i + t; };
 
     if (tid == kTcKWarp * 32) {
         for (int i = 0; i < NSK; ++i) {
-            mbar_init(&k_full[i], N / kSpSlice);
+            mbar_init(&k_full[i], kSpSlices);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < NSV; ++i) {
-            mbar_init(&v_full[i], N / kSpSlice);
+            mbar_init(&v_full[i], kSpSlices);
             mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < kSpRing; ++i) mbar_init(&scale_bar[i], 2 * N / kSpSlice);
+        for (int i = 0; i < kSpRing; ++i) mbar_init(&scale_bar[i], 2 * kSpSlices);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], kTcRows);
@@ -224,15 +248,15 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         } else if (warp == kTcMmaWarp && lane == 0) {
             constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
             constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
-            const int last_t = two ? 1 : 0;
-            auto qk = [&](int t, int j) -> bool {
-                const int st = j % NSK;
-                if (t == 0) {
+            const int steps[2] = {steps_of(0), steps_of(1)};
+            auto qk = [&](int t, int i) -> bool {
+                const int j = tile_of(t, i), st = j % NSK;
+                if (t == 0 || !two) {
                     if (!tc_wait(&k_full[st], (uint32_t)((j / NSK) & 1), p.status, abort_flag)) return false;
                     fence_async_smem();
                     tc_fence_after();
                 }
-                const uint32_t qa = smem_u32(sm + t * Sh::kQBytes);
+                const uint32_t qa = smem_u32(sm + (two ? t : 0) * Sh::kQBytes);
                 const uint32_t ka = smem_u32(sm + Sh::kKOff + st * Sh::kTile);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -240,14 +264,14 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     tc_mma(tmem + t * Sh::kTileCols, tc_desc(qa + (kk >> 2) * (kTcRows * 128) + off, 16, 1024),
                            tc_desc(ka + (kk >> 2) * (N * 128) + off, 16, 1024), idS, kk > 0);
                 }
-                if (t == last_t) tc_commit(&k_empty[st]);
+                if (t == 1 || !two) tc_commit(&k_empty[st]);
                 tc_commit(&s_full[t]);
                 return true;
             };
-            auto pv = [&](int t, int j) -> bool {
-                const int st = j % NSV;
-                if (!tc_wait(&p_full[t], (uint32_t)(j & 1), p.status, abort_flag)) return false;
-                if (t == 0) {
+            auto pv = [&](int t, int i) -> bool {
+                const int j = tile_of(t, i), st = j % NSV;
+                if (!tc_wait(&p_full[t], (uint32_t)(i & 1), p.status, abort_flag)) return false;
+                if (t == 0 || !two) {
                     if (!tc_wait(&v_full[st], (uint32_t)((j / NSV) & 1), p.status, abort_flag)) return false;
                     fence_async_smem();
                 }
@@ -259,29 +283,28 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                     for (int kk = 0; kk < N / 16; ++kk)
                         tc_mma_ts(pt + N, pt + u * (N / 2) + kk * 8, tc_desc(va + kk * 2048, N * 128, 1024), idO,
-                                  j > 0 || u > 0 || kk > 0);
-                if (t == last_t) tc_commit(&v_empty[st]);
+                                  i > 0 || u > 0 || kk > 0);
+                if (t == 1 || !two) tc_commit(&v_empty[st]);
                 return true;
             };
             bool ok = tc_wait(q_ready, 0u, p.status, abort_flag);
             tc_fence_after();
             if (ok) ok = qk(0, 0);
-            if (ok && two) ok = qk(1, 0);
-            for (int j = 0; j < ntiles && ok; ++j) {
-                ok = pv(0, j);
-                if (ok && j + 1 < ntiles) ok = qk(0, j + 1);
-                if (ok && two) {
-                    ok = pv(1, j);
-                    if (ok && j + 1 < ntiles) ok = qk(1, j + 1);
-                }
-            }
+            if (ok && steps[1] > 0) ok = qk(1, 0);
+            for (int i = 0; i < steps[0] && ok; ++i)
+                for (int t = 0; t < 2 && ok; ++t)
+                    if (i < steps[t]) {
+                        ok = pv(t, i);
+                        if (ok && i + 1 < steps[t]) ok = qk(t, i + 1);
+                    }
             // everything issued ends before the epilogue reads O and before TMEM is freed
             tc_commit(drain);
             mbar_wait_bounded(drain, 0, p.status);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
-        const int qt = warp >> 2;
+        const int qt = warp >> 2;                                      // the stream
+        auto over_group = [&](int r) { return (int)((uint64_t)(uint32_t)r * p.group_mul >> p.group_shift); };
         const int r = tid & (kTcRows - 1);
         // ---- the query, under a power of two for each row: a group of lanes a row
         {
@@ -293,9 +316,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             for (int i = 0; i < 32 / RPW; ++i) {
                 const int rr = warp * 32 + i * RPW + lane / CPR, row = row0 + rr;
                 v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows)
+                if (rr < rows) {
+                    const int token = over_group(row);
                     v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
-                                                           ((size_t)(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D + c * 8);
+                                                           ((size_t)(q0 + token) * p.num_q_heads + kvh * G + row - token * G) * D + c * 8);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 32 / RPW; ++i) {
@@ -323,24 +348,32 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
+            if (!two) named_barrier(4, kTcSoftmaxThreads);             // both streams read the first tile's units
         }
-        if (qt == 0 || two) {
+        const int steps = steps_of(qt);
+        if (steps > 0) {
             const uint32_t sbuf = tmem + ((uint32_t)((warp & 3) * 32) << 16) + qt * Sh::kTileCols;
             const uint32_t obuf = sbuf + N;
-            const int rr = qt * kTcRows + r;
+            const int rr = (two ? qt * kTcRows : 0) + r;
             const bool valid = rr < rows;
+            const bool idle = (rr & ~31) >= rows;                      // a warp without rows: it keeps step
             const int row = row0 + min(rr, rows - 1);
-            const int token = row / G;
+            const int token = over_group(row);
             const int pos = first_pos + token;                         // the last key that the row sees
             const float hm = mul[rr];
             float m = -INFINITY, l = 0.f;
             float e_ref = -1e4f;                                       // value scales up to 2^e_ref fit the weights
             bool ok = true;
-            for (int j = 0; j < ntiles; ++j) {
+            for (int i = 0; i < steps; ++i) {
+                const int j = tile_of(qt, i);
                 ok = tc_wait(&scale_bar[j % kSpRing], (uint32_t)((j / kSpRing) & 1), p.status, abort_flag) &&
-                     tc_wait(&s_full[qt], (uint32_t)(j & 1), p.status, abort_flag);
+                     tc_wait(&s_full[qt], (uint32_t)(i & 1), p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if (idle) {
+                    mbar_arrive(&p_full[qt]);
+                    continue;
+                }
                 tc_fence_after();
                 uint32_t xr[N];
 #pragma unroll
@@ -356,7 +389,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                 for (int c = 0; c < N; ++c) x[c] = __uint_as_float(xr[c]);
                 const int key0 = T0 + j * N;
-                if (key0 + N - 1 > pos) {
+                if (__any_sync(0xffffffffu, key0 + N - 1 > pos)) {     // (a branch, not 128 selections)
 #pragma unroll
                     for (int c = 0; c < N; ++c)
                         if (key0 + c > pos) x[c] = -INFINITY;
@@ -417,7 +450,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     tc_st_n<16>(sbuf + h * 16, hi);
                     if constexpr (kTwoTerms) tc_st_n<16>(sbuf + N / 2 + h * 16, lo);
                 }
-                if (j > 0 && __any_sync(0xffffffffu, moved || wider)) {
+                if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
                     // O holds the tiles before this one: S of this tile came after their P.V
                     const float alpha = al * drop;
 #pragma unroll 1
@@ -438,10 +471,43 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 ok = tc_wait(drain, 0u, p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
             }
-            if (ok) {
+            float fall = fast_exp2(e_ref - 6.f) * (kFp8 ? 256.f : 1.f);
+            // two streams of one query tile: the second hands its rows to the first, in the
+            // queries' place (every MMA is done)
+            const bool join = !two && ntiles > 1;
+            float* other = reinterpret_cast<float*>(sm);               // [128][D], columns turned by the row
+            if (join && qt == 1) {
+                if (ok && !idle) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32(obuf + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) other[r * D + ((c + e + r) & (D - 1))] = __uint_as_float(o[e]) * fall;
+                    }
+                    mul[r] = m;
+                    mul[kTcRows + r] = l;
+                }
+                named_barrier(3, kTcSoftmaxThreads);
+                ok = false;
+            }
+            float from_other = 0.f;
+            if (join && qt == 0) {
+                named_barrier(3, kTcSoftmaxThreads);
+                const float m1 = mul[r], l1 = mul[kTcRows + r];
+                const float most = fmaxf(m, m1);
+                const float f0 = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - most);
+                from_other = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : fast_exp2(m1 - most);
+                l = l * f0 + l1 * from_other;
+                fall *= f0;
+                m = most;
+            }
+            if (ok && !idle) {
                 tc_fence_after();
                 const bool sees = valid && pos >= T0;                  // of this partition, anything
-                const float out_mul = fast_exp2(e_ref - 6.f) * (kFp8 ? 256.f : 1.f) / l;
+                const float inv = 1.f / l;
                 const size_t at = (size_t)(q0 + token) * p.num_q_heads + kvh * G + (row - token * G);
                 const size_t part = at * p.max_parts + blockIdx.x;
                 if (sees && p.max_parts > 1) {
@@ -455,7 +521,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     tc_wait_ld();
                     float f[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * out_mul;
+                    for (int e = 0; e < 32; ++e) {
+                        f[e] = __uint_as_float(o[e]) * fall;
+                        if (join) f[e] = fmaf(other[r * D + ((c + e + r) & (D - 1))], from_other, f[e]);
+                        f[e] *= inv;
+                    }
                     if (sees && p.max_parts > 1) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)

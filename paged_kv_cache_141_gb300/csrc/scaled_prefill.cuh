@@ -71,22 +71,25 @@ struct SpShape {
 };
 
 // One loader warp's slices of an operand: slice n = 8 j + q is keys 16 q .. of tile j.
-template <typename CT, int D, int NS, bool kKeys>
-__device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring, float2* scales, uint64_t* full,
-                                        uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend, int ntiles,
-                                        int which, int lane, volatile int* abort_flag) {
+// Keys and values run the same code: the roles of this kernel together
+// overflow the instruction cache otherwise, and every warp waits for instructions
+// (four stalls in ten, with code of their own and the issuer's calls inlined three times).
+template <typename CT, int D>
+__device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, uint8_t* ring, int stages, float* scales,
+                                        uint64_t* full, uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend,
+                                        int ntiles, int which, int lane, volatile int* abort_flag) {
     using Sh = SpShape<D>;
     constexpr int CPR = D / 16;                    // 16-code chunks of a row
     constexpr int PER = kSpSlice * CPR / 32;       // of a lane's
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
-    const float* block_scales = kKeys ? p.k_scales : p.v_scales;
+    const float* block_scales = keys ? p.k_scales : p.v_scales;
     const int B = p.block_size;
     const int last = kSpSlices * ntiles;
     // eight lanes that store together hold two rows of one 64-column span, in all banks
     const int chunk = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
     const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
     constexpr int STEP = 32 / CPR;                 // rows of a pass
-    const uint8_t* cache = (kKeys ? p.k_cache : p.v_cache) + chunk * 16;
+    const uint8_t* cache = (keys ? p.k_cache : p.v_cache) + chunk * 16;
     // slices lie in one block each: blocks are multiples of 16 tokens
     auto block_of = [&](int n, int& in) {
         const int key = T0 + n * kSpSlice;
@@ -99,8 +102,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring
         float scale;
     };
     auto fetch = [&](int n, int blk, int in, Slice& to) {
-        const int key = T0 + n * kSpSlice;
-        const int rows = n < last ? min(kSpSlice, kend - key) : 0;
+        const int rows = n < last ? min(kSpSlice, kend - T0 - n * kSpSlice) : 0;
         bool there = rows > 0;
         if (there && (uint32_t)blk >= (uint32_t)p.num_blocks) {
             if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
@@ -113,21 +115,27 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring
         for (int i = 0; i < PER; ++i)
             to.w[i] = there && i * STEP + row0 < rows ? *reinterpret_cast<const uint4*>(from + i * STEP * D) : make_uint4(0u, 0u, 0u, 0u);
     };
+    int tile = 0, st = 0;                          // of the slice to store, and its stage
+    uint32_t phase = 1;                            // of its stage's `empty`: the first round waits for nothing
     auto store = [&](int n, const Slice& from) -> bool {
-        const int j = n / kSpSlices, q = n % kSpSlices;
+        const int q = n % kSpSlices;
+        if (n / kSpSlices != tile) {
+            ++tile;
+            if (++st == stages) {
+                st = 0;
+                phase ^= 1u;
+            }
+        }
         if (lane == 0) {
-            float* sp = reinterpret_cast<float*>(scales + (j % kSpRing) * kSpSlices + q);
-            if (kKeys) sp[0] = from.scale;
-            else sp[1] = log2f(from.scale);
-            mbar_arrive(&scale_bar[j % kSpRing]);
+            scales[((tile % kSpRing) * kSpSlices + q) * 2 + (keys ? 0 : 1)] = keys ? from.scale : log2f(from.scale);
+            mbar_arrive(&scale_bar[tile % kSpRing]);
         }
         __syncwarp();
-        const int st = j % NS;
-        if (j >= NS) {
-            const bool ok = tc_wait(&empty[st], (uint32_t)((j / NS - 1) & 1), p.status, abort_flag);
+        if (tile >= stages) {
+            const bool ok = tc_wait(&empty[st], phase, p.status, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) return false;
         }
-        uint8_t* tile = ring + st * Sh::kTile;
+        uint8_t* to = ring + st * Sh::kTile;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int r = q * kSpSlice + i * STEP + row0;
@@ -141,29 +149,28 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, uint8_t* ring
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4*>(tile + sw128_chunk<Sh::N>(r, 2 * chunk + h)) = make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+                *reinterpret_cast<uint4*>(to + sw128_chunk<Sh::N>(r, 2 * chunk + h)) = make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);     // the MMA issuer, which waits for it, has the fence between the proxies
         return true;
     };
-    // two slices in flight while a third is widened; the blocks' ids one further ahead
-    Slice a, b, c;
+    // a slice in flight while another is widened; the blocks' ids one further ahead
+    Slice a, b;
     int in, n = which;
     int blk = block_of(n, in);
     fetch(n, blk, in, a);
     blk = block_of(n + kSpLoaders, in);
-    fetch(n + kSpLoaders, blk, in, b);
-    blk = block_of(n + 2 * kSpLoaders, in);
     auto step = [&](const Slice& cur, Slice& next) -> bool {
         if (n >= last) return false;
-        fetch(n + 2 * kSpLoaders, blk, in, next);
-        blk = block_of(n + 3 * kSpLoaders, in);
+        fetch(n + kSpLoaders, blk, in, next);
+        blk = block_of(n + 2 * kSpLoaders, in);
         if (!store(n, cur)) return false;
         n += kSpLoaders;
         return true;
     };
-    while (step(a, c) && step(b, a) && step(c, b)) {}
+#pragma unroll 1
+    while (step(a, b) && step(b, a)) {}
 }
 
 template <typename CT, int D, bool kTwoTerms>
@@ -239,16 +246,14 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 
     if (warp >= kTcSoftmaxThreads / 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcProducerRegs));
-        if (warp == 8 || warp == 10 || warp == 12) {
-            sp_load<CT, D, NSK, true>(p, sm + Sh::kKOff, scales, k_full, k_empty, scale_bar, s, kvh, T0, kend, ntiles,
-                                      (warp - 8) >> 1, lane, abort_flag);
-        } else if (warp == 11 || warp == 13 || warp == 15) {
-            sp_load<CT, D, NSV, false>(p, sm + Sh::kVOff, scales, v_full, v_empty, scale_bar, s, kvh, T0, kend, ntiles,
-                                       (warp - 11) >> 1, lane, abort_flag);
+        if (warp != kTcMmaWarp && warp != 14) {
+            const bool keys = warp < 13 && !(warp & 1);                // 8, 10, 12
+            sp_load<CT, D>(p, keys, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
+                           keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles,
+                           keys ? (warp - 8) >> 1 : (warp - 11) >> 1, lane, abort_flag);
         } else if (warp == kTcMmaWarp && lane == 0) {
             constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
             constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
-            const int steps[2] = {steps_of(0), steps_of(1)};
             auto qk = [&](int t, int i) -> bool {
                 const int j = tile_of(t, i), st = j % NSK;
                 if (t == 0 || !two) {
@@ -289,14 +294,13 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             };
             bool ok = tc_wait(q_ready, 0u, p.status, abort_flag);
             tc_fence_after();
-            if (ok) ok = qk(0, 0);
-            if (ok && steps[1] > 0) ok = qk(1, 0);
-            for (int i = 0; i < steps[0] && ok; ++i)
-                for (int t = 0; t < 2 && ok; ++t)
-                    if (i < steps[t]) {
-                        ok = pv(t, i);
-                        if (ok && i + 1 < steps[t]) ok = qk(t, i + 1);
-                    }
+#pragma unroll 1
+            for (int i = -1; i < steps_of(0) && ok; ++i)
+#pragma unroll 1
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (i >= 0 && i < steps_of(t)) ok = pv(t, i);
+                    if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
+                }
             // everything issued ends before the epilogue reads O and before TMEM is freed
             tc_commit(drain);
             mbar_wait_bounded(drain, 0, p.status);

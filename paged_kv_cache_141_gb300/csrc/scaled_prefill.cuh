@@ -70,6 +70,16 @@ struct SpShape {
     static_assert(kSpRing >= NSK + 3 && kSpRing >= NSV + 1, "scales");
 };
 
+// tcgen05.wait::ld, on which the loaded registers depend: no use moves above it.
+__device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+
 // One loader warp's slices of an operand: slice n = 8 j + q is keys 16 q .. of tile j.
 // Keys and values run the same code: the roles of this kernel together
 // overflow the instruction cache otherwise, and every warp waits for instructions
@@ -379,38 +389,46 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     continue;
                 }
                 tc_fence_after();
-                uint32_t xr[N];
-#pragma unroll
-                for (int c = 0; c < N; c += 32) tc_ld32(sbuf + c, *reinterpret_cast<uint32_t(*)[32]>(xr + c));
                 const float2* sp = scales + (j % kSpRing) * 8;         // broadcast reads
                 // the group's scale on the row's scores; zero must not meet a masked one
                 auto on_row = [&](float a) {
                     const float k = a * hm;
                     return k == 0.f ? 1.17549435e-38f : k;
                 };
-                tc_wait_ld();
-                float x[N];
+                // keys of this tile that the row sees (at or below 0: none)
+                const int sees = pos + 1 - (T0 + j * N);
+                const bool cut = __any_sync(0xffffffffu, sees < N);
+                auto mask = [&](uint32_t (&x)[32], int c0) {
+                    if (cut) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) x[c] = __uint_as_float(xr[c]);
-                const int key0 = T0 + j * N;
-                if (__any_sync(0xffffffffu, key0 + N - 1 > pos)) {     // (a branch, not 128 selections)
-#pragma unroll
-                    for (int c = 0; c < N; ++c)
-                        if (key0 + c > pos) x[c] = -INFINITY;
-                }
+                        for (int c = 0; c < 32; ++c)
+                            if (c0 + c >= sees) x[c] = 0xff800000u;    // -infinity
+                    }
+                };
+                // ---- the maximum
                 float m_cand = m, b_most = sp[0].y;
+                {
+                    uint32_t x[4][32];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    float y = fmax3(x[16 * g], x[16 * g + 1], x[16 * g + 2]);
-                    float z = fmax3(x[16 * g + 3], x[16 * g + 4], x[16 * g + 5]);
-                    y = fmax3(y, x[16 * g + 6], x[16 * g + 7]);
-                    z = fmax3(z, x[16 * g + 8], x[16 * g + 9]);
-                    y = fmax3(y, x[16 * g + 10], x[16 * g + 11]);
-                    z = fmax3(z, x[16 * g + 12], x[16 * g + 13]);
-                    y = fmax3(y, x[16 * g + 14], x[16 * g + 15]);
-                    const float2 ab = sp[g];
-                    m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
-                    b_most = fmaxf(b_most, ab.y);
+                    for (int h = 0; h < 4; ++h) tc_ld32(sbuf + 32 * h, x[h]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        tc_wait_ld32(x[h]);
+                        mask(x[h], 32 * h);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            auto at = [&](int c) { return __uint_as_float(x[h][16 * g + c]); };
+                            float y = fmax3(at(0), at(1), at(2)), z = fmax3(at(3), at(4), at(5));
+                            y = fmax3(y, at(6), at(7));
+                            z = fmax3(z, at(8), at(9));
+                            y = fmax3(y, at(10), at(11));
+                            z = fmax3(z, at(12), at(13));
+                            y = fmax3(y, at(14), at(15));
+                            const float2 ab = sp[2 * h + g];
+                            m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
+                            b_most = fmaxf(b_most, ab.y);
+                        }
+                    }
                 }
                 const bool wider = b_most > e_ref;                     // the same for every row
                 const bool moved = m_cand > m + kSpMoveLog2;
@@ -425,12 +443,16 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 l *= al;
                 const float m_sub = m_use == -INFINITY ? 0.f : m_use;
                 m = m_use;
+                // ---- the weights, 32 keys at a time, their scores read again: a loop of few
+                // instructions and registers, the next scores under way. Weights lie over scores already
+                // read: those of keys 32 h .. in columns 16 h .., their second terms in 64 + 16 h ..,
+                // stored once the scores there are in registers.
+                auto weigh = [&](uint32_t (&x)[32], int h, uint32_t (&lo)[16]) {
+                    uint32_t hi[16];
+                    mask(x, 32 * h);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int g = 2 * h; g < 2 * h + 2; ++g) {
-                        const float2 ab = sp[g];
+                    for (int g = 0; g < 2; ++g) {
+                        const float2 ab = sp[2 * h + g];
                         const float lift = (ab.y < e_ref - 60.f ? -60.f : ab.y - e_ref) + 6.f;
                         const float k1 = on_row(ab.x);
                         const float2 k2 = make_float2(k1, k1);
@@ -438,21 +460,39 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int c = 0; c < 16; c += 2) {
-                            const float2 t = __ffma2_rn(make_float2(x[16 * g + c], x[16 * g + c + 1]), k2, c2);
+                            const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[16 * g + c]), __uint_as_float(x[16 * g + c + 1])), k2, c2);
                             const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                             sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
                             const uint32_t w = pack2<__half>(e.x, e.y);
-                            hi[(16 * g + c - 32 * h) / 2] = w;
+                            hi[8 * g + c / 2] = w;
                             if constexpr (kTwoTerms) {
                                 const float2 rest = __ffma2_rn(unpack2<__half>(w), make_float2(-1.f, -1.f), e);
-                                lo[(16 * g + c - 32 * h) / 2] = pack2<__half>(rest.x, rest.y);
+                                lo[8 * g + c / 2] = pack2<__half>(rest.x, rest.y);
                             }
                         }
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         l = fmaf(sum[0].x + sum[0].y, fast_exp2(-lift), l);
                     }
-                    tc_st_n<16>(sbuf + h * 16, hi);
-                    if constexpr (kTwoTerms) tc_st_n<16>(sbuf + N / 2 + h * 16, lo);
+                    tc_st_n<16>(sbuf + 16 * h, hi);
+                };
+                uint32_t xa[32], xb[32], lo_a[16], lo_b[16];
+                tc_ld32(sbuf, xa);
+#pragma unroll 1
+                for (int h = 0; h < 4; h += 2) {
+                    tc_wait_ld32(xa);
+                    tc_ld32(sbuf + 32 * h + 32, xb);
+                    if (kTwoTerms && h > 0) {
+                        tc_st_n<16>(sbuf + N / 2, lo_a);
+                        tc_st_n<16>(sbuf + N / 2 + 16, lo_b);
+                    }
+                    weigh(xa, h, lo_a);
+                    tc_wait_ld32(xb);
+                    if (h == 0) tc_ld32(sbuf + 64, xa);
+                    weigh(xb, h + 1, lo_b);
+                }
+                if constexpr (kTwoTerms) {
+                    tc_st_n<16>(sbuf + N / 2 + 32, lo_a);
+                    tc_st_n<16>(sbuf + N / 2 + 48, lo_b);
                 }
                 if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
                     // O holds the tiles before this one: S of this tile came after their P.V
@@ -510,7 +550,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             }
             if (ok && !idle) {
                 tc_fence_after();
-                const bool sees = valid && pos >= T0;                  // of this partition, anything
+                const bool sees = valid && pos >= T0;                  // anything of this partition
                 const float inv = 1.f / l;
                 const size_t at = (size_t)(q0 + token) * p.num_q_heads + kvh * G + (row - token * G);
                 const size_t part = at * p.max_parts + blockIdx.x;

@@ -237,7 +237,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         for (int i = 0; i < kSpRing; ++i) mbar_init(&scale_bar[i], 2 * kSpSlices);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], kTcRows);
+            mbar_init(&p_full[t], kTcRows / 32);
         }
         mbar_init(drain, 1);
         mbar_init(q_ready, kTcSoftmaxThreads / 32);
@@ -264,6 +264,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         } else if (warp == kTcMmaWarp && lane == 0) {
             constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
             constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
+            // the operands' descriptors; an address adds to their low bits (in units of 16 bytes)
+            const uint64_t q_desc = tc_desc(smem_u32(sm), 16, 1024);
+            const uint64_t k_desc = tc_desc(smem_u32(sm + Sh::kKOff), 16, 1024);
+            const uint64_t v_desc = tc_desc(smem_u32(sm + Sh::kVOff), N * 128, 1024);
+            static_assert(kTcRows == N, "one column span of Q and of K");
             auto qk = [&](int t, int i) -> bool {
                 const int j = tile_of(t, i), st = j % NSK;
                 if (t == 0 || !two) {
@@ -271,13 +276,12 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     fence_async_smem();
                     tc_fence_after();
                 }
-                const uint32_t qa = smem_u32(sm + (two ? t : 0) * Sh::kQBytes);
-                const uint32_t ka = smem_u32(sm + Sh::kKOff + st * Sh::kTile);
+                const uint64_t qa = q_desc + (two && t ? Sh::kQBytes >> 4 : 0);
+                const uint64_t ka = k_desc + st * (Sh::kTile >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk & 3) * 32u;
-                    tc_mma(tmem + t * Sh::kTileCols, tc_desc(qa + (kk >> 2) * (kTcRows * 128) + off, 16, 1024),
-                           tc_desc(ka + (kk >> 2) * (N * 128) + off, 16, 1024), idS, kk > 0);
+                    const uint32_t off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
+                    tc_mma(tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
                 }
                 if (t == 1 || !two) tc_commit(&k_empty[st]);
                 tc_commit(&s_full[t]);
@@ -291,14 +295,13 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     fence_async_smem();
                 }
                 tc_fence_after();
-                const uint32_t va = smem_u32(sm + Sh::kVOff + st * Sh::kTile);
+                const uint64_t va = v_desc + st * (Sh::kTile >> 4);
                 const uint32_t pt = tmem + t * Sh::kTileCols;
 #pragma unroll
                 for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
 #pragma unroll
                     for (int kk = 0; kk < N / 16; ++kk)
-                        tc_mma_ts(pt + N, pt + u * (N / 2) + kk * 8, tc_desc(va + kk * 2048, N * 128, 1024), idO,
-                                  i > 0 || u > 0 || kk > 0);
+                        tc_mma_ts(pt + N, pt + u * (N / 2) + kk * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
                 if (t == 1 || !two) tc_commit(&v_empty[st]);
                 return true;
             };
@@ -385,7 +388,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (idle) {
-                    mbar_arrive(&p_full[qt]);
+                    if (lane == 0) mbar_arrive(&p_full[qt]);
                     continue;
                 }
                 tc_fence_after();
@@ -509,7 +512,8 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 }
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_full[qt]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[qt]);
             }
             if (ok) {
                 ok = tc_wait(drain, 0u, p.status, abort_flag);

@@ -9,7 +9,7 @@
 // tiles over the same key tiles, or, where one tile holds all rows (drafts), the
 // even and the odd key tiles, joined at the end. Roles:
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
-//   warp 9           issues tcgen05.mma (one lane): S0, S1, then PV0, S0', PV1, S1', ...
+//   warp 9           issues tcgen05.mma: S0, S1, then PV0, S0', PV1, S1', ...
 //   warps 8, 10, 12  load K: codes from the cache's blocks into registers, 16 keys at a
 //   and 11, 13, 15   time and two such slices ahead (V: the other three), widened to
 //                    binary16 -- exactly, as in scaled_attention.cuh -- into the swizzled
@@ -49,10 +49,12 @@ struct SpShape {
     static constexpr int N = 128;
     static constexpr int kQBytes = kTcRows * D * 2;                    // a query tile
     static constexpr int kTile = N * D * 2;                            // a K (V) stage
-    static constexpr int NSK = 2, NSV = 3;
+    static constexpr int NSK = 2, NSV = 2;
     static constexpr int kKOff = 2 * kQBytes;
     static constexpr int kVOff = kKOff + NSK * kTile;
-    static constexpr int kBarOff = kVOff + NSV * kTile;
+    static constexpr int kStagingOff = kVOff + NSV * kTile;            // two slices of codes and their scale for each loader
+    static constexpr int kSlot = kSpSlice * D + 16;
+    static constexpr int kBarOff = kStagingOff + 2 * kSpLoaders * 2 * kSlot;
     // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[2] drain q_ready
     static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 6;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;            // tmem base, abort flag
@@ -70,6 +72,39 @@ struct SpShape {
     static_assert(kSpRing >= NSK + 3 && kSpRing >= NSV + 1, "scales");
 };
 
+// tcgen05.mma and its commit from a whole warp, issued by the lane whose `leader` is set. The
+// warp stays together, so that descriptors and loop counts live in uniform registers, where the
+// instruction takes them from; a lone lane moves each of them there (100 cycles an instruction).
+__device__ __forceinline__ void sp_mma(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+}
+__device__ __forceinline__ void sp_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+}
+__device__ __forceinline__ void sp_commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"(leader) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // tcgen05.wait::ld, on which the loaded registers depend: no use moves above it.
 __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -85,7 +120,7 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
 // overflow the instruction cache otherwise, and every warp waits for instructions
 // (four stalls in ten, with code of their own and the issuer's calls inlined three times).
 template <typename CT, int D>
-__device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, uint8_t* ring, int stages, float* scales,
+__device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, const uint8_t* staging, uint8_t* ring, int stages, float* scales,
                                         uint64_t* full, uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend,
                                         int ntiles, int which, int lane, volatile int* abort_flag) {
     using Sh = SpShape<D>;
@@ -100,34 +135,68 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, ui
     const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
     constexpr int STEP = 32 / CPR;                 // rows of a pass
     const uint8_t* cache = (keys ? p.k_cache : p.v_cache) + chunk * 16;
-    // slices lie in one block each: blocks are multiples of 16 tokens
-    auto block_of = [&](int n, int& in) {
-        const int key = T0 + n * kSpSlice;
-        const int j = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
-        in = key - j * B;
-        return n < last && key < kend ? table[j] : -1;
-    };
-    struct Slice {
-        uint4 w[PER];
-        float scale;
-    };
-    auto fetch = [&](int n, int blk, int in, Slice& to) {
-        const int rows = n < last ? min(kSpSlice, kend - T0 - n * kSpSlice) : 0;
-        bool there = rows > 0;
-        if (there && (uint32_t)blk >= (uint32_t)p.num_blocks) {
-            if (lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
-            there = false;
+    // Slices lie in one block each: blocks are multiples of 16 tokens. Table entry and row of
+    // the block, of the slice whose id is read next; they move on without a division.
+    int entry, in;
+    {
+        const int key = T0 + which * kSpSlice;
+        entry = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
+        in = key - entry * B;
+    }
+    const int entry_step = kSpLoaders * kSpSlice / B, in_step = kSpLoaders * kSpSlice % B;
+    int left = kend - T0 - which * kSpSlice;       // keys from that slice on
+    int blk = 0, blk_in = 0, blk_left = 0;         // of the slice to copy next
+    auto look = [&] {
+        blk_in = in;
+        blk_left = left;
+        if (left > 0) blk = table[entry];
+        entry += entry_step;
+        in += in_step;
+        if (in >= B) {
+            in -= B;
+            ++entry;
         }
-        const uint32_t slab = there ? (uint32_t)blk * p.num_kv_heads + kvh : 0u;
-        const uint8_t* from = cache + (size_t)(slab * B + in + row0) * D;
-        to.scale = there ? block_scales[slab] : 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            to.w[i] = there && i * STEP + row0 < rows ? *reinterpret_cast<const uint4*>(from + i * STEP * D) : make_uint4(0u, 0u, 0u, 0u);
+        left -= kSpLoaders * kSpSlice;
     };
-    int tile = 0, st = 0;                          // of the slice to store, and its stage
-    uint32_t phase = 1;                            // of its stage's `empty`: the first round waits for nothing
-    auto store = [&](int n, const Slice& from) -> bool {
+    // a lane copies, and later widens, its own chunks: nothing of the staging slots is shared
+    const uint32_t mine = smem_u32(staging) + lane * 16;
+    auto fetch = [&](int slot) {
+        if (blk_left > 0) {
+            const uint32_t to = mine + slot * Sh::kSlot;
+            const bool there = (uint32_t)blk < (uint32_t)p.num_blocks;
+            if (there && blk_left >= kSpSlice) {
+                const uint32_t slab = (uint32_t)blk * p.num_kv_heads + kvh;
+                const uint8_t* from = cache + (size_t)(slab * B + blk_in + row0) * D;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, from + i * STEP * D);
+                if (lane == 0) cp_async4(to + PER * 512, block_scales + slab, true);
+            } else {                               // the context's end, or a bad block: zeros
+                if (!there && lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+                const uint32_t slab = there ? (uint32_t)blk * p.num_kv_heads + kvh : 0u;
+                const uint8_t* from = cache + (size_t)(slab * B + blk_in + row0) * D;
+                const int here = there ? blk_left - row0 : 0;          // of this lane's rows, STEP apart
+#pragma unroll 1
+                for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, i * STEP < here ? from + i * STEP * D : cache, i * STEP < here);
+                if (lane == 0) cp_async4(to + PER * 512, block_scales + slab, there);
+            }
+        } else {                                   // a tile's slices behind the last key
+            const uint32_t to = mine + slot * Sh::kSlot;
+#pragma unroll 1
+            for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, cache, false);
+            if (lane == 0) cp_async4(to + PER * 512, block_scales, false);
+        }
+        cp_async_commit();
+    };
+    // two slices under way; the blocks' ids one further ahead
+    look();
+    fetch(0);
+    look();
+    fetch(1);
+    look();
+    int tile = 0, st = 0, slot = 0;                // of the slice to widen: key tile, its stage, staging slot
+    uint32_t phase = 1;                            // of its stage's `empty`; the first round waits for nothing
+#pragma unroll 1
+    for (int n = which; n < last; n += kSpLoaders) {
         const int q = n % kSpSlices;
         if (n / kSpSlices != tile) {
             ++tile;
@@ -136,51 +205,42 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, ui
                 phase ^= 1u;
             }
         }
+        cp_async_wait<1>();
+        const uint32_t at = mine + slot * Sh::kSlot;
         if (lane == 0) {
-            scales[((tile % kSpRing) * kSpSlices + q) * 2 + (keys ? 0 : 1)] = keys ? from.scale : log2f(from.scale);
+            const float scale = ld_shared(at + PER * 512);
+            scales[((tile % kSpRing) * kSpSlices + q) * 2 + (keys ? 0 : 1)] = keys ? scale : log2f(scale);
             mbar_arrive(&scale_bar[tile % kSpRing]);
         }
         __syncwarp();
         if (tile >= stages) {
             const bool ok = tc_wait(&empty[st], phase, p.status, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) return false;
+            if (!__all_sync(0xffffffffu, ok)) break;
         }
-        uint8_t* to = ring + st * Sh::kTile;
-#pragma unroll
+        uint8_t* to = ring + st * Sh::kTile + q * kSpSlice * 128;
+#pragma unroll 2
         for (int i = 0; i < PER; ++i) {
-            const int r = q * kSpSlice + i * STEP + row0;
-            const uint32_t in[4] = {from.w[i].x, from.w[i].y, from.w[i].z, from.w[i].w};
+            const uint4 v = ld_shared4(at + i * 512);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t w = biased<CT>(in[k]);
-                o[2 * k] = widen2<CT>(w, 0x4140);
-                o[2 * k + 1] = widen2<CT>(w, 0x4342);
+                const uint32_t u = biased<CT>(w[k]);
+                o[2 * k] = widen2<CT>(u, 0x4140);
+                o[2 * k + 1] = widen2<CT>(u, 0x4342);
             }
+            const int r = i * STEP + row0;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(to + sw128_chunk<Sh::N>(r, 2 * chunk + h)) = make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);     // the MMA issuer, which waits for it, has the fence between the proxies
-        return true;
-    };
-    // a slice in flight while another is widened; the blocks' ids one further ahead
-    Slice a, b;
-    int in, n = which;
-    int blk = block_of(n, in);
-    fetch(n, blk, in, a);
-    blk = block_of(n + kSpLoaders, in);
-    auto step = [&](const Slice& cur, Slice& next) -> bool {
-        if (n >= last) return false;
-        fetch(n + kSpLoaders, blk, in, next);
-        blk = block_of(n + 2 * kSpLoaders, in);
-        if (!store(n, cur)) return false;
-        n += kSpLoaders;
-        return true;
-    };
-#pragma unroll 1
-    while (step(a, b) && step(b, a)) {}
+        fetch(slot);
+        look();
+        slot ^= 1;
+    }
+    cp_async_wait<0>();
 }
 
 template <typename CT, int D, bool kTwoTerms>
@@ -258,10 +318,15 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcProducerRegs));
         if (warp != kTcMmaWarp && warp != 14) {
             const bool keys = warp < 13 && !(warp & 1);                // 8, 10, 12
-            sp_load<CT, D>(p, keys, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
+            sp_load<CT, D>(p, keys, sm + Sh::kStagingOff + (keys ? (warp - 8) >> 1 : kSpLoaders + ((warp - 11) >> 1)) * 2 * Sh::kSlot,
+                           sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
                            keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles,
                            keys ? (warp - 8) >> 1 : (warp - 11) >> 1, lane, abort_flag);
-        } else if (warp == kTcMmaWarp && lane == 0) {
+        } else if (warp == kTcMmaWarp) {
+            const uint32_t leader = lane == 0;
+            auto wait = [&](uint64_t* bar, int parity) {
+                return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(parity & 1), p.status, abort_flag)) != 0;
+            };
             constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
             constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
             // the operands' descriptors; an address adds to their low bits (in units of 16 bytes)
@@ -272,7 +337,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             auto qk = [&](int t, int i) -> bool {
                 const int j = tile_of(t, i), st = j % NSK;
                 if (t == 0 || !two) {
-                    if (!tc_wait(&k_full[st], (uint32_t)((j / NSK) & 1), p.status, abort_flag)) return false;
+                    if (!wait(&k_full[st], j / NSK)) return false;
                     fence_async_smem();
                     tc_fence_after();
                 }
@@ -281,17 +346,17 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
-                    tc_mma(tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
+                    sp_mma(leader, tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
                 }
-                if (t == 1 || !two) tc_commit(&k_empty[st]);
-                tc_commit(&s_full[t]);
+                if (t == 1 || !two) sp_commit(leader, &k_empty[st]);
+                sp_commit(leader, &s_full[t]);
                 return true;
             };
             auto pv = [&](int t, int i) -> bool {
                 const int j = tile_of(t, i), st = j % NSV;
-                if (!tc_wait(&p_full[t], (uint32_t)(i & 1), p.status, abort_flag)) return false;
+                if (!wait(&p_full[t], i)) return false;
                 if (t == 0 || !two) {
-                    if (!tc_wait(&v_full[st], (uint32_t)((j / NSV) & 1), p.status, abort_flag)) return false;
+                    if (!wait(&v_full[st], j / NSV)) return false;
                     fence_async_smem();
                 }
                 tc_fence_after();
@@ -301,11 +366,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
 #pragma unroll
                     for (int kk = 0; kk < N / 16; ++kk)
-                        tc_mma_ts(pt + N, pt + u * (N / 2) + kk * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
-                if (t == 1 || !two) tc_commit(&v_empty[st]);
+                        sp_mma_ts(leader, pt + N, pt + u * (N / 2) + kk * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
+                if (t == 1 || !two) sp_commit(leader, &v_empty[st]);
                 return true;
             };
-            bool ok = tc_wait(q_ready, 0u, p.status, abort_flag);
+            bool ok = wait(q_ready, 0);
             tc_fence_after();
 #pragma unroll 1
             for (int i = -1; i < steps_of(0) && ok; ++i)
@@ -315,7 +380,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
                 }
             // everything issued ends before the epilogue reads O and before TMEM is freed
-            tc_commit(drain);
+            sp_commit(leader, drain);
             mbar_wait_bounded(drain, 0, p.status);
         }
     } else {
@@ -402,7 +467,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 const int sees = pos + 1 - (T0 + j * N);
                 const bool cut = __any_sync(0xffffffffu, sees < N);
                 auto mask = [&](uint32_t (&x)[32], int c0) {
-                    if (cut) {
+                    if (__builtin_expect(cut, 0)) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (c0 + c >= sees) x[c] = 0xff800000u;    // -infinity

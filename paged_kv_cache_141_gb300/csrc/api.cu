@@ -1314,8 +1314,14 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     p.q_mul = scale * 1.4426950408889634f;
     p.bf16 = q_dtype == PA_BF16;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return from_cuda(cache_dtype == PA_INT8 ? launch_scaled_attention_int8(p, head_size, cs)
-                                            : launch_scaled_attention_e4m3(p, head_size, cs));
+    const bool integer = cache_dtype == PA_INT8;
+    if (l.workers == 0)
+        return from_cuda(integer ? launch_scaled_prefill_int8(p, head_size, cs) : launch_scaled_prefill_e4m3(p, head_size, cs));
+    if (p.bf16)
+        return from_cuda(integer ? launch_scaled_attention_int8_bf16(p, head_size, cs)
+                                 : launch_scaled_attention_e4m3_bf16(p, head_size, cs));
+    return from_cuda(integer ? launch_scaled_attention_int8_f16(p, head_size, cs)
+                             : launch_scaled_attention_e4m3_f16(p, head_size, cs));
 }
 
 pa_status pa_verify_drafts(int64_t* out_tokens, int32_t* accepted, int32_t* rejected,

@@ -28,7 +28,8 @@
 // binary32. A weight p b is rounded to binary16 (2^-11, below half a step of the codes)
 // under a power of two shared by the stage's blocks, which follows the largest value
 // scale seen: 2^-14 of the largest weight before its bits thin out, 2^-25 of it before it
-// vanishes.
+// vanishes. A bfloat16 output's own rounding is eight times coarser; a binary16 output's
+// is no finer than the weights', and takes them in two terms (2^-22).
 //
 // An item within one warp's piece is written out by it. Pieces of others go to the
 // workspace, two of a warp's at most (the end of an item that began before its piece, the
@@ -207,7 +208,8 @@ struct ScaledPlace {
     }
 };
 
-template <typename CT, int D, int NT, int W>
+// kTwoTerms: weights as a binary16 number and the binary16 rest.
+template <typename CT, int D, int NT, int W, bool kTwoTerms>
 __global__ void __launch_bounds__(W * 32, NT == 1 && D < 256 ? 3 : (D < 256 ? 2 : 1))
 scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
@@ -491,7 +493,7 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
         const float lift = __uint_as_float((uint32_t)(127 + 6 - e_ref) << 23);
 #pragma unroll
         for (int i = 0; i < 4; ++i) vb[i] *= lift;
-        uint32_t pb[NT][2][2];                     // P^T fragments
+        uint32_t pb[NT][2][2], pl[kTwoTerms ? NT : 1][2][2];           // P^T fragments, and of the rests
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float w[2][4];
@@ -506,7 +508,14 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pb[nt][k >> 1][k & 1] = movmatrix_trans(Ops::pack(w[0][k], w[1][k]));
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t hi = Ops::pack(w[0][k], w[1][k]);
+                pb[nt][k >> 1][k & 1] = movmatrix_trans(hi);
+                if constexpr (kTwoTerms) {
+                    const float2 h = Ops::unpack(hi);
+                    pl[nt][k >> 1][k & 1] = movmatrix_trans(Ops::pack(w[0][k] - h.x, w[1][k] - h.y));
+                }
+            }
         }
 
         // ---- O^T += C_V^T P^T: a chunk is 16 components of all 32 tokens; fragment
@@ -524,7 +533,10 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                 a[2] = widen2<CT>(hi, 0x4240);
                 a[3] = widen2<CT>(hi, 0x4341);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Ops::mma(acc[nt][md], a, pb[nt][kt][0], pb[nt][kt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    Ops::mma(acc[nt][md], a, pb[nt][kt][0], pb[nt][kt][1]);
+                    if constexpr (kTwoTerms) Ops::mma(acc[nt][md], a, pl[nt][kt][0], pl[nt][kt][1]);
+                }
             }
         }
         slot = slot + 1 == NST ? 0 : slot + 1;
@@ -693,91 +705,11 @@ scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
     }
 }
 
-// The merge of a row's partitions (scaled_prefill.cuh), by the same threads.
-constexpr int kScaledMergeParts = 512;             // weights at a time
-
-template <int D>
-__global__ void __launch_bounds__(kScaledMergeThreads)
-scaled_merge_kernel(const __grid_constant__ ScaledAttnParams p) {
-    begin_overlapped();
-    constexpr int LANES = D / 4, SLICES = kScaledMergeThreads / LANES;
-    __shared__ float weight[kScaledMergeParts];
-    __shared__ float red[32];
-    __shared__ float4 part_sum[kScaledMergeThreads];
-    const int s = blockIdx.z, token = blockIdx.y, head = blockIdx.x;
-    int L, q0, Q;
-    if (!scaled_sequence(p, s, false, L, q0, Q) || token >= Q) return;
-    const int seen = L - Q + token + 1;
-    const int n = (seen + p.partition_size - 1) / p.partition_size;
-    const size_t at = (size_t)(q0 + token) * p.num_q_heads + head;
-    const float* ml = p.max_logits + at * p.max_parts;
-    const float* es = p.exp_sums + at * p.max_parts;
-    const float4* to = reinterpret_cast<const float4*>(p.tmp_out + at * p.max_parts * D);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float M = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kScaledMergeThreads) M = fmaxf(M, ml[i]);
-#pragma unroll
-    for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
-    M = red[0];
-#pragma unroll
-    for (int w = 1; w < kScaledMergeThreads / 32; ++w) M = fmaxf(M, red[w]);
-    const int slice = threadIdx.x / LANES, c = threadIdx.x % LANES;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int base = 0; base < n; base += kScaledMergeParts) {
-        const int count = min(kScaledMergeParts, n - base);
-        __syncthreads();
-        for (int i = threadIdx.x; i < count; i += kScaledMergeThreads) {
-            const float m = ml[base + i], l = es[base + i];
-            const float w = m == -INFINITY ? l : l * fast_exp2(m - M);
-            weight[i] = w;
-            sum += w;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int i = slice; i < count; i += SLICES) {
-            const float w = weight[i];
-            const float4 v = to[(size_t)(base + i) * LANES + c];
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
-        }
-    }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    part_sum[threadIdx.x] = o;
-    __syncthreads();
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    if (threadIdx.x >= LANES) return;
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kScaledMergeThreads / 32; ++w) sum += red[w];
-#pragma unroll
-    for (int i = 1; i < SLICES; ++i) {
-        const float4 v = part_sum[i * LANES + c];
-        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-    }
-    const float inv = n > 0 ? __fdiv_rn(1.f, sum) : 0.f;               // no token: zeros
-    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-    uint2 w;
-    if (p.bf16) w = make_uint2(MmaOps<__nv_bfloat16>::pack(o.x, o.y), MmaOps<__nv_bfloat16>::pack(o.z, o.w));
-    else w = make_uint2(MmaOps<__half>::pack(o.x, o.y), MmaOps<__half>::pack(o.z, o.w));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + 4 * c) = w;
-}
-
-// scaled_prefill.cuh, instantiated in files of its own.
-template <typename CT, int D>
-cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, cudaStream_t stream);
-
-template <typename CT, int D, int NT>
+template <typename CT, int D, int NT, bool kTwoTerms>
 cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     using S = ScaledShape<D, NT>;
     constexpr int W = kScaledWarps;
-    auto kernel = scaled_attention_kernel<CT, D, NT, W>;
+    auto kernel = scaled_attention_kernel<CT, D, NT, W, kTwoTerms>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), W * S::kWarpBytes);
     if (e != cudaSuccess) return e;
     e = launch_overlapped(kernel, p, dim3(p.workers / W), W * 32, W * S::kWarpBytes, stream);
@@ -787,25 +719,21 @@ cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     return launch_overlapped(scaled_join_kernel<D, NT>, p, dim3(p.items, p.num_seqs, rows), kScaledMergeThreads, 0, stream);
 }
 
-template <typename CT, int D>
-cudaError_t launch_scaled_head(const ScaledAttnParams& p, cudaStream_t stream) {
-    if (p.tile_rows == 8) return launch_scaled_rows<CT, D, 1>(p, stream);
-    if (p.tile_rows == 16) return launch_scaled_rows<CT, D, 2>(p, stream);
-    if constexpr (D < 256) {
-        if (p.tile_rows == 32) return launch_scaled_rows<CT, D, 4>(p, stream);
-        const cudaError_t e = launch_scaled_prefill<CT, D>(p, stream);
-        if (e != cudaSuccess || p.max_parts == 1) return e;
-        return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
-    }
-    return cudaErrorInvalidValue;
-}
-
-template <typename CT>
-cudaError_t launch_scaled(const ScaledAttnParams& p, int head_size, cudaStream_t stream) {
+// Up to 32 rows a tile; by the output's type (a file for each, scaled_attention_*.cu).
+template <typename CT, bool kTwoTerms>
+cudaError_t launch_scaled_warps(const ScaledAttnParams& p, int head_size, cudaStream_t stream) {
+    auto rows = [&](auto d) -> cudaError_t {
+        constexpr int D = decltype(d)::value;
+        if (p.tile_rows == 8) return launch_scaled_rows<CT, D, 1, kTwoTerms>(p, stream);
+        if (p.tile_rows == 16) return launch_scaled_rows<CT, D, 2, kTwoTerms>(p, stream);
+        if constexpr (D < 256)
+            if (p.tile_rows == 32) return launch_scaled_rows<CT, D, 4, kTwoTerms>(p, stream);
+        return cudaErrorInvalidValue;
+    };
     switch (head_size) {
-    case 64: return launch_scaled_head<CT, 64>(p, stream);
-    case 128: return launch_scaled_head<CT, 128>(p, stream);
-    case 256: return launch_scaled_head<CT, 256>(p, stream);
+    case 64: return rows(std::integral_constant<int, 64>{});
+    case 128: return rows(std::integral_constant<int, 128>{});
+    case 256: return rows(std::integral_constant<int, 256>{});
     }
     return cudaErrorInvalidValue;
 }

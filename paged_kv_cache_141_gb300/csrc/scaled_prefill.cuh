@@ -680,9 +680,97 @@ cudaError_t launch_scaled_prefill_terms(const ScaledAttnParams& p, cudaStream_t 
     return launch_overlapped(kernel, p, dim3(p.max_parts, p.num_kv_heads * p.row_tiles, p.num_seqs), kTcThreadsFp8, SpShape<D>::kAlloc, stream);
 }
 
+// The merge of a row's partitions: 16 or 32 threads hold four components each, and the others
+// of a (query token, head)'s CTA take partitions in turn.
+constexpr int kScaledMergeParts = 512;             // weights at a time
+
+template <int D>
+__global__ void __launch_bounds__(kScaledMergeThreads)
+scaled_merge_kernel(const __grid_constant__ ScaledAttnParams p) {
+    begin_overlapped();
+    constexpr int LANES = D / 4, SLICES = kScaledMergeThreads / LANES;
+    __shared__ float weight[kScaledMergeParts];
+    __shared__ float red[32];
+    __shared__ float4 part_sum[kScaledMergeThreads];
+    const int s = blockIdx.z, token = blockIdx.y, head = blockIdx.x;
+    int L, q0, Q;
+    if (!scaled_sequence(p, s, false, L, q0, Q) || token >= Q) return;
+    const int seen = L - Q + token + 1;
+    const int n = (seen + p.partition_size - 1) / p.partition_size;
+    const size_t at = (size_t)(q0 + token) * p.num_q_heads + head;
+    const float* ml = p.max_logits + at * p.max_parts;
+    const float* es = p.exp_sums + at * p.max_parts;
+    const float4* to = reinterpret_cast<const float4*>(p.tmp_out + at * p.max_parts * D);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float M = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += kScaledMergeThreads) M = fmaxf(M, ml[i]);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    M = red[0];
+#pragma unroll
+    for (int w = 1; w < kScaledMergeThreads / 32; ++w) M = fmaxf(M, red[w]);
+    const int slice = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int base = 0; base < n; base += kScaledMergeParts) {
+        const int count = min(kScaledMergeParts, n - base);
+        __syncthreads();
+        for (int i = threadIdx.x; i < count; i += kScaledMergeThreads) {
+            const float m = ml[base + i], l = es[base + i];
+            const float w = m == -INFINITY ? l : l * fast_exp2(m - M);
+            weight[i] = w;
+            sum += w;
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int i = slice; i < count; i += SLICES) {
+            const float w = weight[i];
+            const float4 v = to[(size_t)(base + i) * LANES + c];
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    part_sum[threadIdx.x] = o;
+    __syncthreads();
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x >= LANES) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kScaledMergeThreads / 32; ++w) sum += red[w];
+#pragma unroll
+    for (int i = 1; i < SLICES; ++i) {
+        const float4 v = part_sum[i * LANES + c];
+        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+    }
+    const float inv = n > 0 ? __fdiv_rn(1.f, sum) : 0.f;               // no token: zeros
+    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+    uint2 w;
+    if (p.bf16) w = make_uint2(MmaOps<__nv_bfloat16>::pack(o.x, o.y), MmaOps<__nv_bfloat16>::pack(o.z, o.w));
+    else w = make_uint2(MmaOps<__half>::pack(o.x, o.y), MmaOps<__half>::pack(o.z, o.w));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + 4 * c) = w;
+}
+
 template <typename CT, int D>
-cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, cudaStream_t stream) {
-    return p.bf16 ? launch_scaled_prefill_terms<CT, D, false>(p, stream) : launch_scaled_prefill_terms<CT, D, true>(p, stream);
+cudaError_t launch_scaled_prefill_head(const ScaledAttnParams& p, cudaStream_t stream) {
+    const cudaError_t e = p.bf16 ? launch_scaled_prefill_terms<CT, D, false>(p, stream) : launch_scaled_prefill_terms<CT, D, true>(p, stream);
+    if (e != cudaSuccess || p.max_parts == 1) return e;
+    return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
+}
+
+template <typename CT>
+cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, int head_size, cudaStream_t stream) {
+    switch (head_size) {
+    case 64: return launch_scaled_prefill_head<CT, 64>(p, stream);
+    case 128: return launch_scaled_prefill_head<CT, 128>(p, stream);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace pagedkv

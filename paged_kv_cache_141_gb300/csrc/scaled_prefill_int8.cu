@@ -4,7 +4,8 @@
 
 namespace pagedkv {
 
-template cudaError_t launch_scaled_prefill<int8_code_t, 64>(const ScaledAttnParams& p, cudaStream_t stream);
-template cudaError_t launch_scaled_prefill<int8_code_t, 128>(const ScaledAttnParams& p, cudaStream_t stream);
+cudaError_t launch_scaled_prefill_int8(const ScaledAttnParams& p, int head_size, cudaStream_t stream) {
+    return launch_scaled_prefill<int8_code_t>(p, head_size, stream);
+}
 
 }  // namespace pagedkv

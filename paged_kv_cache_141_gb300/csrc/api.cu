@@ -115,7 +115,7 @@ struct ScaledPlan {
 
 // How a call's work is cut. Up to 32 rows of a sequence and KV head: warp-level MMAs, the
 // smallest n-tiles that hold them, one wave of warps for all stages. More, at head size 64
-// or 128 and blocks of a multiple of 16 tokens: the tcgen05 kernel, 256 rows a CTA,
+// or 128 and blocks of a multiple of 8 tokens: the tcgen05 kernel, 256 rows a CTA,
 // one CTA on an SM, and partitions of the context where the sequences, heads and row
 // tiles alone leave SMs idle; else tiles of 32 rows (16 at head size 256, whose
 // accumulators fill the registers).
@@ -123,7 +123,7 @@ ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_k
                        int head_size, int block_size, int max_queries, int max_context_len) {
     ScaledPlan l{};
     const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
-    const bool tc = rows > 32 && head_size <= 128 && block_size % 16 == 0;
+    const bool tc = rows > 32 && head_size <= 128 && block_size % 8 == 0;
     l.tile_rows = tc ? 256 : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
     l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);
@@ -1314,14 +1314,12 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     p.q_mul = scale * 1.4426950408889634f;
     p.bf16 = q_dtype == PA_BF16;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool integer = cache_dtype == PA_INT8;
-    if (l.workers == 0)
-        return from_cuda(integer ? launch_scaled_prefill_int8(p, head_size, cs) : launch_scaled_prefill_e4m3(p, head_size, cs));
-    if (p.bf16)
-        return from_cuda(integer ? launch_scaled_attention_int8_bf16(p, head_size, cs)
-                                 : launch_scaled_attention_e4m3_bf16(p, head_size, cs));
-    return from_cuda(integer ? launch_scaled_attention_int8_f16(p, head_size, cs)
-                             : launch_scaled_attention_e4m3_f16(p, head_size, cs));
+    auto launch = l.workers > 0
+        ? (cache_dtype == PA_INT8 ? (p.bf16 ? launch_scaled_attention_int8_bf16 : launch_scaled_attention_int8_f16)
+                                  : (p.bf16 ? launch_scaled_attention_e4m3_bf16 : launch_scaled_attention_e4m3_f16))
+        : (cache_dtype == PA_INT8 ? (p.bf16 ? launch_scaled_prefill_int8_bf16 : launch_scaled_prefill_int8_f16)
+                                  : (p.bf16 ? launch_scaled_prefill_e4m3_bf16 : launch_scaled_prefill_e4m3_f16));
+    return from_cuda(launch(p, head_size, cs));
 }
 
 pa_status pa_verify_drafts(int64_t* out_tokens, int32_t* accepted, int32_t* rejected,

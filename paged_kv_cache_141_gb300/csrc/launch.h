@@ -389,8 +389,10 @@ cudaError_t launch_scaled_attention_int8_f16(const ScaledAttnParams& p, int head
 cudaError_t launch_scaled_attention_e4m3_bf16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
 cudaError_t launch_scaled_attention_e4m3_f16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
 // Many rows, on the tcgen05 tensor cores (scaled_prefill.cuh).
-cudaError_t launch_scaled_prefill_int8(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
-cudaError_t launch_scaled_prefill_e4m3(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_scaled_prefill_int8_bf16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_scaled_prefill_int8_f16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_scaled_prefill_e4m3_bf16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_scaled_prefill_e4m3_f16(const ScaledAttnParams& p, int head_size, cudaStream_t stream);
 
 // Draft verification (verify_drafts.cu).
 constexpr int kMaxVerifyVocab = 1 << 22;      // the tiles' sums in shared memory

@@ -19,8 +19,8 @@
 // fence between its stores and the MMAs' reads waited for its loads in flight: 541 us
 // for 8 chunks of 512, 510 with the fence in the MMA issuer, which waits for the tile.)
 //
-// The scales stay out of the tiles. Blocks are multiples of 16 tokens here, so a
-// group of 16 columns of S has one key scale a and one value scale b: with raw
+// The scales stay out of the tiles. Blocks are multiples of kG = 16 or 8 tokens here, so a
+// group of kG columns of S has one key scale a and one value scale b: with raw
 // scores s and the row's unit u (scale, log2 e and the query's power of two),
 //     weight = 2^(s (u a) + (log2 b - e + 6) - m),
 // one fused multiply-add and one exponential a score; the maximum is taken over raw
@@ -53,13 +53,13 @@ struct SpShape {
     static constexpr int kKOff = 2 * kQBytes;
     static constexpr int kVOff = kKOff + NSK * kTile;
     static constexpr int kStagingOff = kVOff + NSV * kTile;            // two slices of codes and their scale for each loader
-    static constexpr int kSlot = kSpSlice * D + 16;
+    static constexpr int kSlot = kSpSlice * D + 16;                    // (a scale for each group)
     static constexpr int kBarOff = kStagingOff + 2 * kSpLoaders * 2 * kSlot;
     // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[2] drain q_ready
     static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 6;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;            // tmem base, abort flag
-    static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;   // [kSpRing][8] pairs (a, log2 b)
-    static constexpr int kMulOff = kScaleOff + kSpRing * 8 * 8;        // [256] the rows' units
+    static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;   // [kSpRing][N / kG] pairs (a, log2 b)
+    static constexpr int kMulOff = kScaleOff + kSpRing * (N / 8) * 8;        // [256] the rows' units
     static constexpr int kBytes = kMulOff + 256 * 4;
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemCols = 512;
@@ -119,7 +119,7 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
 // Keys and values run the same code: the roles of this kernel together
 // overflow the instruction cache otherwise, and every warp waits for instructions
 // (four stalls in ten, with code of their own and the issuer's calls inlined three times).
-template <typename CT, int D>
+template <typename CT, int D, int kG>
 __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, const uint8_t* staging, uint8_t* ring, int stages, float* scales,
                                         uint64_t* full, uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend,
                                         int ntiles, int which, int lane, volatile int* abort_flag) {
@@ -135,55 +135,58 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
     const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
     constexpr int STEP = 32 / CPR;                 // rows of a pass
     const uint8_t* cache = (keys ? p.k_cache : p.v_cache) + chunk * 16;
-    // Slices lie in one block each: blocks are multiples of 16 tokens. Table entry and row of
-    // the block, of the slice whose id is read next; they move on without a division.
-    int entry, in;
-    {
-        const int key = T0 + which * kSpSlice;
-        entry = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
-        in = key - entry * B;
+    // A slice's parts of kG keys lie in one block each. Table entry and row of the block, of
+    // the slice whose ids are read next; they move on without a division.
+    constexpr int PARTS = kSpSlice / kG, PER_PART = PER / PARTS;
+    int entry[PARTS], in[PARTS];
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) {
+        const int key = T0 + which * kSpSlice + h * kG;
+        entry[h] = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
+        in[h] = key - entry[h] * B;
     }
     const int entry_step = kSpLoaders * kSpSlice / B, in_step = kSpLoaders * kSpSlice % B;
     int left = kend - T0 - which * kSpSlice;       // keys from that slice on
-    int blk = 0, blk_in = 0, blk_left = 0;         // of the slice to copy next
+    int blk[PARTS], blk_in[PARTS], blk_left = 0;   // of the slice to copy next
     auto look = [&] {
-        blk_in = in;
         blk_left = left;
-        if (left > 0) blk = table[entry];
-        entry += entry_step;
-        in += in_step;
-        if (in >= B) {
-            in -= B;
-            ++entry;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+            blk_in[h] = in[h];
+            blk[h] = left > h * kG ? table[entry[h]] : -1;
+            entry[h] += entry_step;
+            in[h] += in_step;
+            if (in[h] >= B) {
+                in[h] -= B;
+                ++entry[h];
+            }
         }
         left -= kSpLoaders * kSpSlice;
     };
     // a lane copies, and later widens, its own chunks: nothing of the staging slots is shared
-    const uint32_t mine = smem_u32(staging) + lane * 16;
+    const uint32_t mine = smem_u32(staging) + lane * 16, my_scale = smem_u32(staging) + kSpSlice * D + lane * 4;
     auto fetch = [&](int slot) {
-        if (blk_left > 0) {
-            const uint32_t to = mine + slot * Sh::kSlot;
-            const bool there = (uint32_t)blk < (uint32_t)p.num_blocks;
-            if (there && blk_left >= kSpSlice) {
-                const uint32_t slab = (uint32_t)blk * p.num_kv_heads + kvh;
-                const uint8_t* from = cache + (size_t)(slab * B + blk_in + row0) * D;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, from + i * STEP * D);
-                if (lane == 0) cp_async4(to + PER * 512, block_scales + slab, true);
+        for (int h = 0; h < PARTS; ++h) {
+            const uint32_t to = mine + slot * Sh::kSlot + h * PER_PART * 512;
+            const bool there = (uint32_t)blk[h] < (uint32_t)p.num_blocks;
+            if (there && blk_left >= (h + 1) * kG) {
+                const uint32_t slab = (uint32_t)blk[h] * p.num_kv_heads + kvh;
+                const uint8_t* from = cache + (size_t)(slab * B + blk_in[h] + row0) * D;
+#pragma unroll
+                for (int i = 0; i < PER_PART; ++i) cp_async16(to + i * 512, from + i * STEP * D);
+                if (lane == h) cp_async4(my_scale + slot * Sh::kSlot, block_scales + slab, true);
             } else {                               // the context's end, or a bad block: zeros
-                if (!there && lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
-                const uint32_t slab = there ? (uint32_t)blk * p.num_kv_heads + kvh : 0u;
-                const uint8_t* from = cache + (size_t)(slab * B + blk_in + row0) * D;
-                const int here = there ? blk_left - row0 : 0;          // of this lane's rows, STEP apart
+                const int keys_here = blk_left - h * kG;
+                if (!there && keys_here > 0 && lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+                const uint32_t slab = there ? (uint32_t)blk[h] * p.num_kv_heads + kvh : 0u;
+                const uint8_t* from = cache + (size_t)(slab * B + blk_in[h] + row0) * D;
+                const int here = there ? keys_here - row0 : 0;         // of this lane's rows, STEP apart
 #pragma unroll 1
-                for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, i * STEP < here ? from + i * STEP * D : cache, i * STEP < here);
-                if (lane == 0) cp_async4(to + PER * 512, block_scales + slab, there);
+                for (int i = 0; i < PER_PART; ++i)
+                    cp_async16(to + i * 512, i * STEP < here ? from + i * STEP * D : cache, i * STEP < here);
+                if (lane == h) cp_async4(my_scale + slot * Sh::kSlot, block_scales + slab, there);
             }
-        } else {                                   // a tile's slices behind the last key
-            const uint32_t to = mine + slot * Sh::kSlot;
-#pragma unroll 1
-            for (int i = 0; i < PER; ++i) cp_async16(to + i * 512, cache, false);
-            if (lane == 0) cp_async4(to + PER * 512, block_scales, false);
         }
         cp_async_commit();
     };
@@ -207,12 +210,12 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
         }
         cp_async_wait<1>();
         const uint32_t at = mine + slot * Sh::kSlot;
-        if (lane == 0) {
-            const float scale = ld_shared(at + PER * 512);
-            scales[((tile % kSpRing) * kSpSlices + q) * 2 + (keys ? 0 : 1)] = keys ? scale : log2f(scale);
-            mbar_arrive(&scale_bar[tile % kSpRing]);
+        if (lane < PARTS) {
+            const float scale = ld_shared(my_scale + slot * Sh::kSlot);
+            scales[((tile % kSpRing) * (Sh::N / kG) + q * PARTS + lane) * 2 + (keys ? 0 : 1)] = keys ? scale : log2f(scale);
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&scale_bar[tile % kSpRing]);
         if (tile >= stages) {
             const bool ok = tc_wait(&empty[st], phase, p.status, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -243,7 +246,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
     cp_async_wait<0>();
 }
 
-template <typename CT, int D, bool kTwoTerms>
+template <typename CT, int D, int kG, bool kTwoTerms>
 __global__ void __launch_bounds__(kTcThreadsFp8, 1)
 scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
@@ -318,7 +321,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcProducerRegs));
         if (warp != kTcMmaWarp && warp != 14) {
             const bool keys = warp < 13 && !(warp & 1);                // 8, 10, 12
-            sp_load<CT, D>(p, keys, sm + Sh::kStagingOff + (keys ? (warp - 8) >> 1 : kSpLoaders + ((warp - 11) >> 1)) * 2 * Sh::kSlot,
+            sp_load<CT, D, kG>(p, keys, sm + Sh::kStagingOff + (keys ? (warp - 8) >> 1 : kSpLoaders + ((warp - 11) >> 1)) * 2 * Sh::kSlot,
                            sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
                            keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles,
                            keys ? (warp - 8) >> 1 : (warp - 11) >> 1, lane, abort_flag);
@@ -457,7 +460,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     continue;
                 }
                 tc_fence_after();
-                const float2* sp = scales + (j % kSpRing) * 8;         // broadcast reads
+                const float2* sp = scales + (j % kSpRing) * (N / kG);         // broadcast reads
                 // the group's scale on the row's scores; zero must not meet a masked one
                 auto on_row = [&](float a) {
                     const float k = a * hm;
@@ -484,15 +487,17 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                         tc_wait_ld32(x[h]);
                         mask(x[h], 32 * h);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            auto at = [&](int c) { return __uint_as_float(x[h][16 * g + c]); };
+                        for (int g = 0; g < 32 / kG; ++g) {
+                            auto at = [&](int c) { return __uint_as_float(x[h][kG * g + c]); };
                             float y = fmax3(at(0), at(1), at(2)), z = fmax3(at(3), at(4), at(5));
                             y = fmax3(y, at(6), at(7));
-                            z = fmax3(z, at(8), at(9));
-                            y = fmax3(y, at(10), at(11));
-                            z = fmax3(z, at(12), at(13));
-                            y = fmax3(y, at(14), at(15));
-                            const float2 ab = sp[2 * h + g];
+                            if constexpr (kG == 16) {
+                                z = fmax3(z, at(8), at(9));
+                                y = fmax3(y, at(10), at(11));
+                                z = fmax3(z, at(12), at(13));
+                                y = fmax3(y, at(14), at(15));
+                            }
+                            const float2 ab = sp[32 / kG * h + g];
                             m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
                             b_most = fmaxf(b_most, ab.y);
                         }
@@ -519,23 +524,23 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     uint32_t hi[16];
                     mask(x, 32 * h);
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float2 ab = sp[2 * h + g];
+                    for (int g = 0; g < 32 / kG; ++g) {
+                        const float2 ab = sp[32 / kG * h + g];
                         const float lift = (ab.y < e_ref - 60.f ? -60.f : ab.y - e_ref) + 6.f;
                         const float k1 = on_row(ab.x);
                         const float2 k2 = make_float2(k1, k1);
                         const float2 c2 = make_float2(lift - m_sub, lift - m_sub);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[16 * g + c]), __uint_as_float(x[16 * g + c + 1])), k2, c2);
+                        for (int c = 0; c < kG; c += 2) {
+                            const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[kG * g + c]), __uint_as_float(x[kG * g + c + 1])), k2, c2);
                             const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                             sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
                             const uint32_t w = pack2<__half>(e.x, e.y);
-                            hi[8 * g + c / 2] = w;
+                            hi[kG / 2 * g + c / 2] = w;
                             if constexpr (kTwoTerms) {
                                 const float2 rest = __ffma2_rn(unpack2<__half>(w), make_float2(-1.f, -1.f), e);
-                                lo[8 * g + c / 2] = pack2<__half>(rest.x, rest.y);
+                                lo[kG / 2 * g + c / 2] = pack2<__half>(rest.x, rest.y);
                             }
                         }
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
@@ -672,9 +677,9 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     }
 }
 
-template <typename CT, int D, bool kTwoTerms>
+template <typename CT, int D, int kG, bool kTwoTerms>
 cudaError_t launch_scaled_prefill_terms(const ScaledAttnParams& p, cudaStream_t stream) {
-    auto kernel = scaled_prefill_kernel<CT, D, kTwoTerms>;
+    auto kernel = scaled_prefill_kernel<CT, D, kG, kTwoTerms>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), SpShape<D>::kAlloc);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kernel, p, dim3(p.max_parts, p.num_kv_heads * p.row_tiles, p.num_seqs), kTcThreadsFp8, SpShape<D>::kAlloc, stream);
@@ -757,18 +762,20 @@ scaled_merge_kernel(const __grid_constant__ ScaledAttnParams p) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + 4 * c) = w;
 }
 
-template <typename CT, int D>
+template <typename CT, int D, bool kTwoTerms>
 cudaError_t launch_scaled_prefill_head(const ScaledAttnParams& p, cudaStream_t stream) {
-    const cudaError_t e = p.bf16 ? launch_scaled_prefill_terms<CT, D, false>(p, stream) : launch_scaled_prefill_terms<CT, D, true>(p, stream);
+    const cudaError_t e = p.block_size % 16 == 0 ? launch_scaled_prefill_terms<CT, D, 16, kTwoTerms>(p, stream)
+                                                 : launch_scaled_prefill_terms<CT, D, 8, kTwoTerms>(p, stream);
     if (e != cudaSuccess || p.max_parts == 1) return e;
     return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
 }
 
-template <typename CT>
+// By the output's type, a file for each (scaled_prefill_*.cu).
+template <typename CT, bool kTwoTerms>
 cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, int head_size, cudaStream_t stream) {
     switch (head_size) {
-    case 64: return launch_scaled_prefill_head<CT, 64>(p, stream);
-    case 128: return launch_scaled_prefill_head<CT, 128>(p, stream);
+    case 64: return launch_scaled_prefill_head<CT, 64, kTwoTerms>(p, stream);
+    case 128: return launch_scaled_prefill_head<CT, 128, kTwoTerms>(p, stream);
     }
     return cudaErrorInvalidValue;
 }

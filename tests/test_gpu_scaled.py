@@ -247,6 +247,24 @@ def test_chunks(kind, heads):
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("B", [1, 4, 8, 16, 24, 40, 48, 128, 1024])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("f16", 128)])
+def test_many_rows_over_blocks(kind, B, dtype, D):
+    lens = [500, 45, 1300, 129, 9]
+    run_attention(kind, dtype, 8, 1, D, B, lens, [6, 45, 30, 1, 9], seed=B + D, tail=2)
+    run_attention(kind, dtype, 4, 2, D, B, lens, [200, 45, 150, 129, 0], seed=B + D)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_in_partitions(kind, D):
+    # few sequences, long contexts: the tcgen05 kernel's partitions, some of which a row does not see
+    run_attention(kind, "bf16", 8, 1, D, 16, [9000, 1025, 4096], [7, 6, 5], seed=D)
+    run_attention(kind, "f16", 8, 1, D, 8, [3000, 2048], [300, 1], seed=D)
+    run_attention(kind, "bf16", 8, 1, D, 32, [5000], [1100], seed=D)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_blocks_of_very_different_size(kind):
     # value scales over twenty octaves, an all-zero block, one with scale 0; keys alike, within the range of exp
     def prepare(kc, vc, ks, vs, table):
@@ -258,6 +276,8 @@ def test_blocks_of_very_different_size(kind):
         ks[ids[6:8]] *= 8
     for L in (500, 3000):
         run_attention(kind, "bf16", 8, 2, 128, 16, [L], [1], prepare=prepare)
+        run_attention(kind, "bf16", 8, 2, 128, 16, [L], [50], prepare=prepare)
+        run_attention(kind, "f16", 8, 2, 64, 8, [L], [90], prepare=prepare)
         run_attention(kind, "bf16", 8, 2, 128, 16, [L], [6], prepare=prepare)
 
 

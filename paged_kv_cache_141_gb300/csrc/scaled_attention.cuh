@@ -585,17 +585,19 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
 // Joins an item's pieces, a CTA for an item (or for some of its rows, where there are few
 // items). Few pieces: a warp a row. Many (a long context alone on the device): all warps a
 // row, and one of them joins their sums.
-constexpr int kScaledMergeThreads = 256;
+// (Its warps: one for each row of a batch's items, sixteen where few items have many pieces.)
+constexpr int kScaledJoinWarps = 16;
 constexpr int kScaledFewPieces = 16;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kScaledMergeThreads)
+__global__ void __launch_bounds__(kScaledJoinWarps * 32)
 scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
-    constexpr int ROWS = 8 * NT, W = kScaledMergeThreads / 32;
+    constexpr int ROWS = 8 * NT;
     constexpr int E = D / 32;                      // a lane's components, neighbours
-    __shared__ float s_max[W], s_sum[W];
-    __shared__ float s_out[W][D];
+    const int W = blockDim.x >> 5;
+    __shared__ float s_max[kScaledJoinWarps], s_sum[kScaledJoinWarps];
+    __shared__ float s_out[kScaledJoinWarps][D];
     const int s = blockIdx.y, item = blockIdx.x;
     // all that says where the pieces lie, in one round of loads
     const int64_t before = p.stages_before[s], after = p.stages_before[s + 1], total = p.stages_before[p.num_seqs];
@@ -688,12 +690,11 @@ scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
         __syncthreads();
         if (warp == 0) {
             float most = -INFINITY;
-#pragma unroll
             for (int w = 0; w < W; ++w) most = fmaxf(most, s_max[w]);
             sum = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll
+#pragma unroll 4
             for (int w = 0; w < W; ++w) {
                 const float f = s_max[w] == -INFINITY ? (s_sum[w] == 0.f ? 0.f : 1.f) : fast_exp2(s_max[w] - most);
                 sum = fmaf(f, s_sum[w], sum);
@@ -715,8 +716,10 @@ cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     e = launch_overlapped(kernel, p, dim3(p.workers / W), W * 32, W * S::kWarpBytes, stream);
     if (e != cudaSuccess) return e;
     const int64_t all = (int64_t)p.items * p.num_seqs;
-    const int rows = all >= 608 ? 1 : (int)(608 / all < 8 * NT ? 608 / all : 8 * NT);
-    return launch_overlapped(scaled_join_kernel<D, NT>, p, dim3(p.items, p.num_seqs, rows), kScaledMergeThreads, 0, stream);
+    const int64_t rows = (int64_t)p.max_queries * p.group < 8 * NT ? (int64_t)p.max_queries * p.group : 8 * NT;
+    const bool batch = all >= 152;
+    const int warps = batch ? (int)(rows < 8 ? rows : 8) : kScaledJoinWarps;
+    return launch_overlapped(scaled_join_kernel<D, NT>, p, dim3(p.items, p.num_seqs, batch ? 1 : (unsigned)rows), warps * 32, 0, stream);
 }
 
 // Up to 32 rows a tile; by the output's type (a file for each, scaled_attention_*.cu).

@@ -687,6 +687,7 @@ cudaError_t launch_scaled_prefill_terms(const ScaledAttnParams& p, cudaStream_t 
 
 // The merge of a row's partitions: 16 or 32 threads hold four components each, and the others
 // of a (query token, head)'s CTA take partitions in turn.
+constexpr int kScaledMergeThreads = 256;
 constexpr int kScaledMergeParts = 512;             // weights at a time
 
 template <int D>

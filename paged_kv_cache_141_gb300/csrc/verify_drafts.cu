@@ -29,8 +29,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 256;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyTile = 512;
 constexpr int kVerifyPer = kVerifyTile / 32;       // of a tile, a lane's values
 constexpr int kVerifyCluster = 8;
@@ -79,12 +77,14 @@ __device__ __forceinline__ Pair tile_sum(const float (&a)[kVerifyPer], const flo
     return x;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads)
+template <int T>
+__global__ void __launch_bounds__(T)
 verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     begin_overlapped();
+    constexpr int kWarps = T / 32;
     extern __shared__ Pair tile_sums[];
     __shared__ int s_accepted;
-    __shared__ Pair s_part[kVerifyWarps];
+    __shared__ Pair s_part[kWarps];
     __shared__ double s_totals[kVerifyCluster];
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -101,7 +101,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const bool bad = rows < 0 || rows > K + 1 || row0 < 0 || row0 + rows > p.num_rows;
     if (bad || rows == 0) {                        // every CTA of the cluster alike
         if (rank == 0) {
-            for (int i = threadIdx.x; i <= K; i += kVerifyThreads) out[i] = -1;
+            for (int i = threadIdx.x; i <= K; i += T) out[i] = -1;
             if (threadIdx.x == 0) {
                 p.accepted[s] = 0;
                 if (p.rejected) p.rejected[s] = 0;
@@ -150,7 +150,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const int first = min(tiles, rank * per), mine = min(tiles, first + per) - first;
     for (;;) {
         Pair sum{0.f, 0.f};
-        for (int t = warp; t < mine; t += kVerifyWarps) {
+        for (int t = warp; t < mine; t += kWarps) {
             float a[kVerifyPer], b[kVerifyPer];
             load_tile(w, (int64_t)(first + t) * kVerifyTile, V, lane, a, b);
             const Pair total = tile_sum(a, b);
@@ -164,7 +164,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
         if (threadIdx.x < ranks) {
             Pair c = s_part[0];
 #pragma unroll
-            for (int i = 1; i < kVerifyWarps; ++i) c = add(c, s_part[i]);
+            for (int i = 1; i < kWarps; ++i) c = add(c, s_part[i]);
             cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = value(c);
         }
         if (ranks > 1) cluster.sync();
@@ -254,15 +254,29 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
-    const int tiles = (int)((p.vocab + kVerifyTile - 1) / kVerifyTile);
-    int cluster = 1;
-    // (some four CTAs fit an SM)
-    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster <= 304 && tiles > cluster * kVerifyWarps) cluster *= 2;
+namespace {
+
+template <int T>
+cudaError_t launch_threads(const VerifyParams& p, int cluster, cudaStream_t stream) {
+    auto kernel = verify_drafts_kernel<T>;
+    const int tiles = (p.vocab + kVerifyTile - 1) / kVerifyTile;
     const int smem = (tiles + cluster - 1) / cluster * (int)sizeof(Pair);
-    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(verify_drafts_kernel), smem);
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(verify_drafts_kernel, p, dim3(p.num_seqs * cluster), kVerifyThreads, smem, stream, cluster);
+    return launch_overlapped(kernel, p, dim3(p.num_seqs * cluster), T, smem, stream, cluster);
+}
+
+}  // namespace
+
+// Few requests: as many warps as tiles, in clusters of up to eight CTAs. A batch: small CTAs
+// in one wave (some eight fit an SM), several to a request, so that the SMs' shares are even.
+cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
+    const int tiles = (p.vocab + kVerifyTile - 1) / kVerifyTile;
+    const bool batch = p.num_seqs > 76;
+    const int warps = batch ? 4 : 8;
+    int cluster = 1;
+    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster * 2 * warps <= 4864 && tiles > cluster * warps) cluster *= 2;
+    return batch ? launch_threads<128>(p, cluster, stream) : launch_threads<256>(p, cluster, stream);
 }
 
 }  // namespace pagedkv

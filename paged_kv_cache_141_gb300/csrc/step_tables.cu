@@ -298,21 +298,23 @@ trim_tables_kernel(const __grid_constant__ TablesParams p) {
         if (threadIdx.x == 0) *p.new_num_free = (int32_t)(fits ? F + given : F);
     }
     if (!fits) return;
-    const int threads = ranks * blockDim.x, top = top_step(S);
-    constexpr int kAtOnce = 4;                     // entries whose loads are in flight together
-    for (int k0 = rank * blockDim.x + threadIdx.x; k0 < (int)given; k0 += kAtOnce * threads) {
+    // a warp takes runs of neighbours, most often one request's: their first and last tell
+    constexpr int kAtOnce = 4, kRun = 32 * kAtOnce;                // entries whose loads are in flight together
+    const int lane = threadIdx.x & 31, warps = ranks * (int)(blockDim.x >> 5), top = top_step(S);
+    for (int k0 = (rank * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5)) * kRun; k0 < (int)given; k0 += warps * kRun) {
+        const int lo = owner_of(blk, S, top, k0), hi = owner_of(blk, S, top, min(k0 + kRun, (int)given) - 1);
         int32_t id[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int k = k0 + i * threads;
+            const int k = k0 + 32 * i + lane;
             if (k < (int)given) {
-                const int s = owner_of(blk, S, top, k);
+                const int s = lo == hi ? lo : lo + owner_of(blk + lo, hi - lo + 1, top_step(hi - lo + 1), k);
                 id[i] = p.block_tables[(size_t)s * p.max_blocks + from[s] + (k - blk[s])];
             }
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int k = k0 + i * threads;
+            const int k = k0 + 32 * i + lane;
             if (k < (int)given) p.stack[F + given - 1 - k] = id[i];
         }
     }

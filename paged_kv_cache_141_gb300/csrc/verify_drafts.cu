@@ -43,11 +43,24 @@ struct Weights {
 // This lane's values of the tile at `at`: elements 32 i + lane, i < 16; zeros past the row.
 __device__ __forceinline__ void load_tile(const Weights& w, int64_t at, int64_t V, int lane, float (&a)[kVerifyPer],
                                           float (&b)[kVerifyPer]) {
+    const float *p = w.p + at + lane, *q = w.q + at + lane;
+    if (at + kVerifyTile <= V && (w.without < at || w.without >= at + kVerifyTile)) {
+#pragma unroll
+        for (int i = 0; i < kVerifyPer; ++i) a[i] = p[32 * i];
+        if (w.q) {
+#pragma unroll
+            for (int i = 0; i < kVerifyPer; ++i) b[i] = q[32 * i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVerifyPer; ++i) b[i] = 0.f;
+        }
+        return;
+    }
+    const int left = (int)min((int64_t)kVerifyTile, V - at) - lane, not_this = (int)(w.without - at) - lane;
 #pragma unroll
     for (int i = 0; i < kVerifyPer; ++i) {
-        const int64_t j = at + 32 * i + lane;
-        a[i] = j < V && j != w.without ? w.p[j] : 0.f;
-        b[i] = w.q && j < V ? w.q[j] : 0.f;
+        a[i] = 32 * i < left && (w.without < 0 || 32 * i != not_this) ? p[32 * i] : 0.f;
+        b[i] = w.q && 32 * i < left ? q[32 * i] : 0.f;
     }
 }
 
@@ -224,27 +237,37 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
         // and the token: the first whose sum passes the goal, or the tile's last with any
         // weight. A lane takes 16 neighbours.
         const int64_t at = (int64_t)(first + tile) * kVerifyTile + lane * kVerifyPer;
-        double own[kVerifyPer], all = 0;
+        Pair own[kVerifyPer], all{0.f, 0.f};
         int last = -1;
+        float x[kVerifyPer], y[kVerifyPer];
 #pragma unroll
         for (int i = 0; i < kVerifyPer; ++i) {
-            const float x = at + i < V && at + i != w.without ? w.p[at + i] : 0.f;
-            const float y = w.q && at + i < V ? w.q[at + i] : 0.f;
-            if (x > y) last = i;
-            all += x > y ? (double)x - (double)y : 0;
+            x[i] = at + i < V && at + i != w.without ? w.p[at + i] : 0.f;
+            y[i] = w.q && at + i < V ? w.q[at + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kVerifyPer; ++i) {
+            if (x[i] > y[i]) {
+                const float d = x[i] - y[i];
+                all = add(all, {d, (x[i] - d) - y[i]});
+                last = i;
+            }
             own[i] = all;
         }
-        double up = all;
+        const double mine_all = value(all);
+        double up = mine_all;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const double o = __shfl_up_sync(0xffffffffu, up, m);
             if (lane >= m) up += o;
         }
-        const double start_of = base + (up - all);
+        // what is left of the goal at this lane's first value
+        const double rest = goal - (base + (up - mine_all));
+        const Pair r{(float)rest, (float)(rest - (double)(float)rest)};
         int here = kVerifyPer;
 #pragma unroll
         for (int i = kVerifyPer - 1; i >= 0; --i)
-            if (start_of + own[i] > goal && own[i] > (i ? own[i - 1] : 0)) here = i;
+            if (x[i] > y[i] && (own[i].hi - r.hi) + (own[i].lo - r.lo) > 0.f) here = i;
         const uint32_t past = __ballot_sync(0xffffffffu, here < kVerifyPer), any = __ballot_sync(0xffffffffu, last >= 0);
         const int who = past ? __ffs(past) - 1 : 31 - __clz(any);
         if (lane == who) out[a] = at + (past ? here : last);

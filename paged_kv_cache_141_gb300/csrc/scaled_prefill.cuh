@@ -9,15 +9,21 @@
 // tiles over the same key tiles, or, where one tile holds all rows (drafts), the
 // even and the odd key tiles, joined at the end. Roles:
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
-//   warp 9           issues tcgen05.mma: S0, S1, then PV0, S0', PV1, S1', ...
-//   warps 8, 10, 12  load K: codes from the cache's blocks into registers, 16 keys at a
-//   and 11, 13, 15   time and two such slices ahead (V: the other three), widened to
-//                    binary16 -- exactly, as in scaled_attention.cuh -- into the swizzled
-//                    tiles that the MMAs read.
-// The codes go through registers and not through shared memory: binary16 tiles and queries
-// take all of it, and the widening needs the registers anyway. (A loader's own
-// fence between its stores and the MMAs' reads waited for its loads in flight: 541 us
-// for 8 chunks of 512, 510 with the fence in the MMA issuer, which waits for the tile.)
+//   warps 8-11       load K (12-14: V): codes from the cache's blocks into staging slots of
+//                    a warp's own, 16 keys at a time by asynchronous copies, a second slice
+//                    under way; from there widened to binary16 -- exactly, as in
+//                    scaled_attention.cuh -- into the swizzled tiles that the MMAs read;
+//   warp 15          issues tcgen05.mma: S0, S1, then PV0, S0', PV1, S1', ...
+// Softmax warps without rows (40 rows of drafts leave two of four) load too: 64 contexts of
+// 2304 tokens with 5 drafted each 146 us, 167 with the same warps idle.
+// What bounds it is instructions: a warp gets one in some eight cycles, and the roles' loops
+// together have to fit the instruction cache. Loops of their own for K and V, unrolled over
+// register buffers, and an issuer inlined three times had four in ten warps waiting for
+// instructions: 482 us for 8 chunks of 512 that take 370 with one copy of each. A softmax holds
+// 64 scores at a time for the same reason, and so that 16 warps of 128 registers do without
+// a split of them by role (17 warps of 96 spill: 560 us).
+// (The fence between the loaders' stores and the MMAs' reads is the issuer's, which waits
+// for the tile: a loader's own waited for its loads in flight, 541 us for 510.)
 //
 // The scales stay out of the tiles. Blocks are multiples of kG = 16 or 8 tokens here, so a
 // group of kG columns of S has one key scale a and one value scale b: with raw
@@ -27,8 +33,8 @@
 // scores within a group (a >= 0) and the row's sum gets each group's weights divided by
 // 2^(log2 b - e + 6) again. e follows the largest value scale, with two octaves to spare:
 // weights reach the MMA below 2^15, rounded to binary16 (2^-11 of themselves; with a
-// binary16 output, whose own step is no larger, in two terms, 2^-22). A value scale more than 2^60 below the largest counts
-// as that: its weights vanish in binary16 either way.
+// binary16 output, whose own step is no larger, in two terms, 2^-22). A value scale more
+// than 2^60 below the largest counts as that: its weights vanish in binary16 either way.
 //
 // Every wait is bounded, as in prefill_tc.cuh.
 #pragma once
@@ -38,7 +44,9 @@
 
 namespace pagedkv {
 
-constexpr int kSpLoaders = 3;                      // warps an operand
+constexpr int kSpThreads = 16 * 32;
+constexpr int kSpMmaWarp = 15;
+constexpr int kSpLoaders = 4;                      // warps for K, one less for V; and up to three softmax warps without rows
 constexpr int kSpSlice = 16;                       // keys a warp widens at a time
 constexpr int kSpSlices = 128 / kSpSlice;
 constexpr int kSpRing = 8;                         // tiles whose scales are kept
@@ -54,17 +62,19 @@ struct SpShape {
     static constexpr int kVOff = kKOff + NSK * kTile;
     static constexpr int kStagingOff = kVOff + NSV * kTile;            // two slices of codes and their scale for each loader
     static constexpr int kSlot = kSpSlice * D + 16;                    // (a scale for each group)
-    static constexpr int kBarOff = kStagingOff + 2 * kSpLoaders * 2 * kSlot;
+    static constexpr int kBarOff = kStagingOff + (2 * kSpLoaders - 1) * 2 * kSlot;
     // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[2] drain q_ready
     static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 6;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;            // tmem base, abort flag
     static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;   // [kSpRing][N / kG] pairs (a, log2 b)
-    static constexpr int kMulOff = kScaleOff + kSpRing * (N / 8) * 8;        // [256] the rows' units
-    static constexpr int kBytes = kMulOff + 256 * 4;
+    static constexpr int kUnitOff = kScaleOff + kSpRing * (N / 8) * 8;     // [256] the rows' powers of two, biased exponents
+    static constexpr int kBytes = kUnitOff + 256;
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemCols = 512;
     static constexpr int kTileCols = N + D;                            // S (then P), O
     static_assert(2 * kTileCols <= kTmemCols, "TMEM columns");
+    static_assert(6 * 2 * kSlot <= kQBytes, "more loaders' slots fit the second query tile's place");
+    static_assert(2 * kTcRows * 4 <= kTile, "the streams trade maxima and sums in a K stage");
     static_assert(kAlloc <= kTcSmemLimit, "shared memory");
     // Scales live until both softmaxes have read them: a loader writes those of tile j once it
     // has passed the wait for tile j - 1's slot, so S of tile j - 1 - NSK (K) or P.V of tile
@@ -116,13 +126,13 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
 }
 
 // One loader warp's slices of an operand: slice n = 8 j + q is keys 16 q .. of tile j.
-// Keys and values run the same code: the roles of this kernel together
-// overflow the instruction cache otherwise, and every warp waits for instructions
-// (four stalls in ten, with code of their own and the issuer's calls inlined three times).
+// Keys and values, and every warp that loads, run the same code, inlined once.
+// At most 8 warps load an operand, so that each has a slice of every tile: waiting for a
+// stage's phase by parity needs that.
 template <typename CT, int D, int kG>
 __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, const uint8_t* staging, uint8_t* ring, int stages, float* scales,
                                         uint64_t* full, uint64_t* empty, uint64_t* scale_bar, int s, int kvh, int T0, int kend,
-                                        int ntiles, int which, int lane, volatile int* abort_flag) {
+                                        int ntiles, int which, int loaders, int lane, volatile int* abort_flag) {
     using Sh = SpShape<D>;
     constexpr int CPR = D / 16;                    // 16-code chunks of a row
     constexpr int PER = kSpSlice * CPR / 32;       // of a lane's
@@ -145,7 +155,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
         entry[h] = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
         in[h] = key - entry[h] * B;
     }
-    const int entry_step = kSpLoaders * kSpSlice / B, in_step = kSpLoaders * kSpSlice % B;
+    const int entry_step = loaders * kSpSlice / B, in_step = loaders * kSpSlice % B;
     int left = kend - T0 - which * kSpSlice;       // keys from that slice on
     int blk[PARTS], blk_in[PARTS], blk_left = 0;   // of the slice to copy next
     auto look = [&] {
@@ -161,11 +171,13 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
                 ++entry[h];
             }
         }
-        left -= kSpLoaders * kSpSlice;
+        left -= loaders * kSpSlice;
     };
     // a lane copies, and later widens, its own chunks: nothing of the staging slots is shared
     const uint32_t mine = smem_u32(staging) + lane * 16, my_scale = smem_u32(staging) + kSpSlice * D + lane * 4;
+    int to_copy = which;
     auto fetch = [&](int slot) {
+        if (to_copy < last)
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
             const uint32_t to = mine + slot * Sh::kSlot + h * PER_PART * 512;
@@ -189,6 +201,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
             }
         }
         cp_async_commit();
+        to_copy += loaders;
     };
     // two slices under way; the blocks' ids one further ahead
     look();
@@ -199,7 +212,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
     int tile = 0, st = 0, slot = 0;                // of the slice to widen: key tile, its stage, staging slot
     uint32_t phase = 1;                            // of its stage's `empty`; the first round waits for nothing
 #pragma unroll 1
-    for (int n = which; n < last; n += kSpLoaders) {
+    for (int n = which; n < last; n += loaders) {
         const int q = n % kSpSlices;
         if (n / kSpSlices != tile) {
             ++tile;
@@ -221,7 +234,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
             if (!__all_sync(0xffffffffu, ok)) break;
         }
         uint8_t* to = ring + st * Sh::kTile + q * kSpSlice * 128;
-#pragma unroll 2
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint4 v = ld_shared4(at + i * 512);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -247,7 +260,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
 }
 
 template <typename CT, int D, int kG, bool kTwoTerms>
-__global__ void __launch_bounds__(kTcThreadsFp8, 1)
+__global__ void __launch_bounds__(kSpThreads, 1)
 scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
     using Sh = SpShape<D>;
@@ -267,7 +280,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sh::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::kMiscOff + 4);
     float2* scales = reinterpret_cast<float2*>(sm + Sh::kScaleOff);
-    float* mul = reinterpret_cast<float*>(sm + Sh::kMulOff);
+    uint8_t* units = sm + Sh::kUnitOff;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = blockIdx.z;
@@ -287,8 +300,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     // stream t's steps, and the key tile of step i
     auto steps_of = [&](int t) { return two ? ntiles : (ntiles + 1 - t) / 2; };
     auto tile_of = [&](int t, int i) { return two ? i : 2 * i + t; };
+    // softmax warps with rows in stream t
+    auto warps_of = [&](int t) { return (min(kTcRows, two ? rows - t * kTcRows : rows) + 31) >> 5; };
+    const bool join = !two && ntiles > 1;          // the streams' results are one
 
-    if (tid == kTcKWarp * 32) {
+    if (tid == kSpMmaWarp * 32) {
         for (int i = 0; i < NSK; ++i) {
             mbar_init(&k_full[i], kSpSlices);
             mbar_init(&k_empty[i], 1);
@@ -300,14 +316,14 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         for (int i = 0; i < kSpRing; ++i) mbar_init(&scale_bar[i], 2 * kSpSlices);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], kTcRows / 32);
+            mbar_init(&p_full[t], max(1, warps_of(t)));
         }
         mbar_init(drain, 1);
         mbar_init(q_ready, kTcSoftmaxThreads / 32);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kTcMmaWarp) {
+    if (warp == kSpMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(tmem_slot)), "r"(Sh::kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -317,82 +333,72 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= kTcSoftmaxThreads / 32) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcProducerRegs));
-        if (warp != kTcMmaWarp && warp != 14) {
-            const bool keys = warp < 13 && !(warp & 1);                // 8, 10, 12
-            sp_load<CT, D, kG>(p, keys, sm + Sh::kStagingOff + (keys ? (warp - 8) >> 1 : kSpLoaders + ((warp - 11) >> 1)) * 2 * Sh::kSlot,
-                           sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
-                           keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles,
-                           keys ? (warp - 8) >> 1 : (warp - 11) >> 1, lane, abort_flag);
-        } else if (warp == kTcMmaWarp) {
-            const uint32_t leader = lane == 0;
-            auto wait = [&](uint64_t* bar, int parity) {
-                return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(parity & 1), p.status, abort_flag)) != 0;
-            };
-            constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
-            constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
-            // the operands' descriptors; an address adds to their low bits (in units of 16 bytes)
-            const uint64_t q_desc = tc_desc(smem_u32(sm), 16, 1024);
-            const uint64_t k_desc = tc_desc(smem_u32(sm + Sh::kKOff), 16, 1024);
-            const uint64_t v_desc = tc_desc(smem_u32(sm + Sh::kVOff), N * 128, 1024);
-            static_assert(kTcRows == N, "one column span of Q and of K");
-            auto qk = [&](int t, int i) -> bool {
-                const int j = tile_of(t, i), st = j % NSK;
-                if (t == 0 || !two) {
-                    if (!wait(&k_full[st], j / NSK)) return false;
-                    fence_async_smem();
-                    tc_fence_after();
-                }
-                const uint64_t qa = q_desc + (two && t ? Sh::kQBytes >> 4 : 0);
-                const uint64_t ka = k_desc + st * (Sh::kTile >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
-                    sp_mma(leader, tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
-                }
-                if (t == 1 || !two) sp_commit(leader, &k_empty[st]);
-                sp_commit(leader, &s_full[t]);
-                return true;
-            };
-            auto pv = [&](int t, int i) -> bool {
-                const int j = tile_of(t, i), st = j % NSV;
-                if (!wait(&p_full[t], i)) return false;
-                if (t == 0 || !two) {
-                    if (!wait(&v_full[st], j / NSV)) return false;
-                    fence_async_smem();
-                }
+    if (warp == kSpMmaWarp) {
+        const uint32_t leader = lane == 0;
+        auto wait = [&](uint64_t* bar, int parity) {
+            return __all_sync(0xffffffffu, tc_wait(bar, (uint32_t)(parity & 1), p.status, abort_flag)) != 0;
+        };
+        constexpr uint32_t idS = tc_idesc<__half>(kTcRows, N, 0);
+        constexpr uint32_t idO = tc_idesc<__half>(kTcRows, D, 1);
+        // the operands' descriptors; an address adds to their low bits (in units of 16 bytes)
+        const uint64_t q_desc = tc_desc(smem_u32(sm), 16, 1024);
+        const uint64_t k_desc = tc_desc(smem_u32(sm + Sh::kKOff), 16, 1024);
+        const uint64_t v_desc = tc_desc(smem_u32(sm + Sh::kVOff), N * 128, 1024);
+        static_assert(kTcRows == N, "one column span of Q and of K");
+        auto qk = [&](int t, int i) -> bool {
+            const int j = tile_of(t, i), st = j % NSK;
+            if (t == 0 || !two) {
+                if (!wait(&k_full[st], j / NSK)) return false;
+                fence_async_smem();
                 tc_fence_after();
-                const uint64_t va = v_desc + st * (Sh::kTile >> 4);
-                const uint32_t pt = tmem + t * Sh::kTileCols;
+            }
+            const uint64_t qa = q_desc + (two && t ? Sh::kQBytes >> 4 : 0);
+            const uint64_t ka = k_desc + st * (Sh::kTile >> 4);
 #pragma unroll
-                for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
-#pragma unroll
-                    for (int kk = 0; kk < N / 16; ++kk)
-                        sp_mma_ts(leader, pt + N, pt + u * (N / 2) + kk * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
-                if (t == 1 || !two) sp_commit(leader, &v_empty[st]);
-                return true;
-            };
-            bool ok = wait(q_ready, 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
+                sp_mma(leader, tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
+            }
+            if (t == 1 || !two) sp_commit(leader, &k_empty[st]);
+            sp_commit(leader, &s_full[t]);
+            return true;
+        };
+        auto pv = [&](int t, int i) -> bool {
+            const int j = tile_of(t, i), st = j % NSV;
+            if (!wait(&p_full[t], i)) return false;
+            if (t == 0 || !two) {
+                if (!wait(&v_full[st], j / NSV)) return false;
+                fence_async_smem();
+            }
             tc_fence_after();
+            const uint64_t va = v_desc + st * (Sh::kTile >> 4);
+            const uint32_t pt = tmem + t * Sh::kTileCols;
+#pragma unroll
+            for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    sp_mma_ts(leader, pt + N, pt + (kk >> 1) * 32 + u * 16 + (kk & 1) * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
+            if (t == 1 || !two) sp_commit(leader, &v_empty[st]);
+            return true;
+        };
+        bool ok = wait(q_ready, 0);
+        tc_fence_after();
 #pragma unroll 1
-            for (int i = -1; i < steps_of(0) && ok; ++i)
+        for (int i = -1; i < steps_of(0) && ok; ++i)
 #pragma unroll 1
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (i >= 0 && i < steps_of(t)) ok = pv(t, i);
-                    if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
-                }
-            // everything issued ends before the epilogue reads O and before TMEM is freed
-            sp_commit(leader, drain);
-            mbar_wait_bounded(drain, 0, p.status);
-        }
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (i >= 0 && i < steps_of(t)) ok = pv(t, i);
+                if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
+            }
+        // everything issued ends before the epilogue reads O and before TMEM is freed
+        sp_commit(leader, drain);
+        mbar_wait_bounded(drain, 0, p.status);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
         const int qt = warp >> 2;                                      // the stream
         auto over_group = [&](int r) { return (int)((uint64_t)(uint32_t)r * p.group_mul >> p.group_shift); };
         const int r = tid & (kTcRows - 1);
         // ---- the query, under a power of two for each row: a group of lanes a row
-        {
+        if (warp < kTcSoftmaxThreads / 32) {
             constexpr int CPR = D / 8;                                 // 16-byte chunks of a row
             constexpr int RPW = 32 / CPR;                              // rows at a time
             const int c = lane % CPR;
@@ -426,26 +432,39 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     const float2 f = p.bf16 ? unpack2<__nv_bfloat16>(w[k]) : unpack2<__half>(w[k]);
                     w[k] = pack2<__half>(f.x * inv, f.y * inv);
                 }
-                const int tr = rr & (kTcRows - 1);
-                *reinterpret_cast<uint4*>(sm + (rr >> 7) * Sh::kQBytes + sw128_chunk<kTcRows>(tr, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (c == 0) mul[rr] = p.q_mul * unit * (kFp8 ? 256.f : 1.f);
+                if (qt == 0 || two) {                                  // (else its place is the loaders')
+                    *reinterpret_cast<uint4*>(sm + qt * Sh::kQBytes + sw128_chunk<kTcRows>(rr & (kTcRows - 1), c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (c == 0) units[rr] = (uint8_t)(__float_as_uint(unit) >> 23);
+                }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
             if (!two) named_barrier(4, kTcSoftmaxThreads);             // both streams read the first tile's units
         }
-        const int steps = steps_of(qt);
-        if (steps > 0) {
+        // ---- loaders: warps 8-15, and the softmax warps without rows
+        const bool spare = warp < 8 && !two && (warp & 3) >= warps_of(qt);
+        const int steps = warp < 8 ? steps_of(qt) : 0;
+        if (warp >= 8 || spare) {
+            const bool keys = spare ? qt == 0 : warp < 12;
+            const int more = two ? 0 : 4 - warps_of(0);                // spare warps of either stream
+            const int more_which = (warp & 3) - warps_of(qt);
+            const int which = spare ? (qt ? kSpLoaders - 1 : kSpLoaders) + more_which : warp & 3;
+            const uint8_t* staging = spare ? sm + Sh::kQBytes + (qt * 3 + more_which) * 2 * Sh::kSlot
+                                           : sm + Sh::kStagingOff + (warp - 8) * 2 * Sh::kSlot;
+            sp_load<CT, D, kG>(p, keys, staging, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
+                               keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles, which,
+                               (keys ? kSpLoaders : kSpLoaders - 1) + more, lane, abort_flag);
+            if (spare && join) named_barrier(3, kTcSoftmaxThreads);
+        } else if (steps > 0 && (warp & 3) < warps_of(qt)) {
             const uint32_t sbuf = tmem + ((uint32_t)((warp & 3) * 32) << 16) + qt * Sh::kTileCols;
             const uint32_t obuf = sbuf + N;
             const int rr = (two ? qt * kTcRows : 0) + r;
             const bool valid = rr < rows;
-            const bool idle = (rr & ~31) >= rows;                      // a warp without rows: it keeps step
             const int row = row0 + min(rr, rows - 1);
             const int token = over_group(row);
             const int pos = first_pos + token;                         // the last key that the row sees
-            const float hm = mul[rr];
+            const float hm = p.q_mul * __uint_as_float((uint32_t)units[rr] << 23) * (kFp8 ? 256.f : 1.f);
             float m = -INFINITY, l = 0.f;
             float e_ref = -1e4f;                                       // value scales up to 2^e_ref fit the weights
             bool ok = true;
@@ -455,10 +474,6 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                      tc_wait(&s_full[qt], (uint32_t)(i & 1), p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (idle) {
-                    if (lane == 0) mbar_arrive(&p_full[qt]);
-                    continue;
-                }
                 tc_fence_after();
                 const float2* sp = scales + (j % kSpRing) * (N / kG);         // broadcast reads
                 // the group's scale on the row's scores; zero must not meet a masked one
@@ -478,30 +493,34 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 };
                 // ---- the maximum
                 float m_cand = m, b_most = sp[0].y;
-                {
-                    uint32_t x[4][32];
+                uint32_t xa[32], xb[32];
+                auto largest = [&](uint32_t (&x)[32], int h) {
+                    mask(x, 32 * h);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) tc_ld32(sbuf + 32 * h, x[h]);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        tc_wait_ld32(x[h]);
-                        mask(x[h], 32 * h);
-#pragma unroll
-                        for (int g = 0; g < 32 / kG; ++g) {
-                            auto at = [&](int c) { return __uint_as_float(x[h][kG * g + c]); };
-                            float y = fmax3(at(0), at(1), at(2)), z = fmax3(at(3), at(4), at(5));
-                            y = fmax3(y, at(6), at(7));
-                            if constexpr (kG == 16) {
-                                z = fmax3(z, at(8), at(9));
-                                y = fmax3(y, at(10), at(11));
-                                z = fmax3(z, at(12), at(13));
-                                y = fmax3(y, at(14), at(15));
-                            }
-                            const float2 ab = sp[32 / kG * h + g];
-                            m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
-                            b_most = fmaxf(b_most, ab.y);
+                    for (int g = 0; g < 32 / kG; ++g) {
+                        auto at = [&](int c) { return __uint_as_float(x[kG * g + c]); };
+                        float y = fmax3(at(0), at(1), at(2)), z = fmax3(at(3), at(4), at(5));
+                        y = fmax3(y, at(6), at(7));
+                        if constexpr (kG == 16) {
+                            z = fmax3(z, at(8), at(9));
+                            y = fmax3(y, at(10), at(11));
+                            z = fmax3(z, at(12), at(13));
+                            y = fmax3(y, at(14), at(15));
                         }
+                        const float2 ab = sp[32 / kG * h + g];
+                        m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
+                        b_most = fmaxf(b_most, ab.y);
                     }
+                };
+                tc_ld32(sbuf, xa);
+#pragma unroll 1
+                for (int h = 0; h < 4; h += 2) {
+                    tc_wait_ld32(xa);
+                    tc_ld32(sbuf + 32 * h + 32, xb);
+                    largest(xa, h);
+                    tc_wait_ld32(xb);
+                    tc_ld32(sbuf + (h == 0 ? 64 : 0), xa);             // (at last the first again, for the weights)
+                    largest(xb, h + 1);
                 }
                 const bool wider = b_most > e_ref;                     // the same for every row
                 const bool moved = m_cand > m + kSpMoveLog2;
@@ -517,11 +536,10 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 const float m_sub = m_use == -INFINITY ? 0.f : m_use;
                 m = m_use;
                 // ---- the weights, 32 keys at a time, their scores read again: a loop of few
-                // instructions and registers, the next scores under way. Weights lie over scores already
-                // read: those of keys 32 h .. in columns 16 h .., their second terms in 64 + 16 h ..,
-                // stored once the scores there are in registers.
-                auto weigh = [&](uint32_t (&x)[32], int h, uint32_t (&lo)[16]) {
-                    uint32_t hi[16];
+                // instructions and registers, the next scores under way. Weights lie over their
+                // scores: those of keys 32 h .. in columns 32 h .., their second terms in 32 h + 16 ..
+                auto weigh = [&](uint32_t (&x)[32], int h) {
+                    uint32_t hi[16], lo[16];
                     mask(x, 32 * h);
 #pragma unroll
                     for (int g = 0; g < 32 / kG; ++g) {
@@ -546,26 +564,17 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         l = fmaf(sum[0].x + sum[0].y, fast_exp2(-lift), l);
                     }
-                    tc_st_n<16>(sbuf + 16 * h, hi);
+                    tc_st_n<16>(sbuf + 32 * h, hi);
+                    if constexpr (kTwoTerms) tc_st_n<16>(sbuf + 32 * h + 16, lo);
                 };
-                uint32_t xa[32], xb[32], lo_a[16], lo_b[16];
-                tc_ld32(sbuf, xa);
 #pragma unroll 1
                 for (int h = 0; h < 4; h += 2) {
                     tc_wait_ld32(xa);
                     tc_ld32(sbuf + 32 * h + 32, xb);
-                    if (kTwoTerms && h > 0) {
-                        tc_st_n<16>(sbuf + N / 2, lo_a);
-                        tc_st_n<16>(sbuf + N / 2 + 16, lo_b);
-                    }
-                    weigh(xa, h, lo_a);
+                    weigh(xa, h);
                     tc_wait_ld32(xb);
                     if (h == 0) tc_ld32(sbuf + 64, xa);
-                    weigh(xb, h + 1, lo_b);
-                }
-                if constexpr (kTwoTerms) {
-                    tc_st_n<16>(sbuf + N / 2 + 32, lo_a);
-                    tc_st_n<16>(sbuf + N / 2 + 48, lo_b);
+                    weigh(xb, h + 1);
                 }
                 if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
                     // O holds the tiles before this one: S of this tile came after their P.V
@@ -591,11 +600,12 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             }
             float fall = fast_exp2(e_ref - 6.f) * (kFp8 ? 256.f : 1.f);
             // two streams of one query tile: the second hands its rows to the first, in the
-            // queries' place (every MMA is done)
-            const bool join = !two && ntiles > 1;
+            // queries' place (every MMA is done, and every slice widened)
             float* other = reinterpret_cast<float*>(sm);               // [128][D], columns turned by the row
+            float* other_m = reinterpret_cast<float*>(sm + Sh::kKOff);
+            float* other_l = other_m + kTcRows;
             if (join && qt == 1) {
-                if (ok && !idle) {
+                if (ok) {
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
@@ -605,8 +615,8 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) other[r * D + ((c + e + r) & (D - 1))] = __uint_as_float(o[e]) * fall;
                     }
-                    mul[r] = m;
-                    mul[kTcRows + r] = l;
+                    other_m[r] = m;
+                    other_l[r] = l;
                 }
                 named_barrier(3, kTcSoftmaxThreads);
                 ok = false;
@@ -614,7 +624,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             float from_other = 0.f;
             if (join && qt == 0) {
                 named_barrier(3, kTcSoftmaxThreads);
-                const float m1 = mul[r], l1 = mul[kTcRows + r];
+                const float m1 = other_m[r], l1 = other_l[r];
                 const float most = fmaxf(m, m1);
                 const float f0 = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - most);
                 from_other = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : fast_exp2(m1 - most);
@@ -622,7 +632,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 fall *= f0;
                 m = most;
             }
-            if (ok && !idle) {
+            if (ok) {
                 tc_fence_after();
                 const bool sees = valid && pos >= T0;                  // anything of this partition
                 const float inv = 1.f / l;
@@ -670,7 +680,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kTcMmaWarp) {
+    if (warp == kSpMmaWarp) {
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmemCols) : "memory");
@@ -682,7 +692,7 @@ cudaError_t launch_scaled_prefill_terms(const ScaledAttnParams& p, cudaStream_t 
     auto kernel = scaled_prefill_kernel<CT, D, kG, kTwoTerms>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), SpShape<D>::kAlloc);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, p, dim3(p.max_parts, p.num_kv_heads * p.row_tiles, p.num_seqs), kTcThreadsFp8, SpShape<D>::kAlloc, stream);
+    return launch_overlapped(kernel, p, dim3(p.max_parts, p.num_kv_heads * p.row_tiles, p.num_seqs), kSpThreads, SpShape<D>::kAlloc, stream);
 }
 
 // The merge of a row's partitions: 16 or 32 threads hold four components each, and the others

@@ -700,8 +700,9 @@ pa_status pa_trim_tables(const int32_t* block_tables, int max_blocks_per_seq,
  *    codes  = x / scale' to nearest even, in [-127, 127] or as E4M3; older codes c
  *             become c (scale / scale') to nearest even where the scale has grown.
  *  A NaN or an infinity makes the block's scale NaN, and with it whatever is read
- *  through it, until the block starts anew. Two sequences that write to one block
- *  race, as do the rows that pass num_tokens (PA_DEV_BAD_LEN, skipped).
+ *  through it, until the block starts anew. A sequence whose rows pass num_tokens or
+ *  max_new_tokens, or whose length its table does not hold, is skipped
+ *  (PA_DEV_BAD_LEN). Two sequences that write to one block race.
  *  Blocks copied by pa_copy_blocks need their scales copied too.
  */
 pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* value,
@@ -728,12 +729,15 @@ pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* valu
  *  workspace      256-byte aligned, pa_scaled_attention_workspace_bytes(...) of these
  *                 sizes (NULL where that is 0); nothing in it outlives the call's
  *                 kernels. Calls that overlap on the GPU need workspaces of their own.
+ *                 Fewer sequences are split further, so a workspace for several sizes
+ *                 has the largest of their byte counts, not that of the largest sizes.
  *  Codes past a context's end are not read. An E4M3 NaN code within it is read as
  *  +-480 (pa_scaled_append writes none but under a NaN scale).
  *  Scores, softmax statistics and sums are binary32. The query meets the codes exactly
  *  but for components more than 2^14 below a row's largest; a weight meets them to
- *  within 2^-11 of itself or 2^-25 of the largest. Block sizes up to 1024, head sizes
- *  64, 128 and 256, any group.
+ *  within 2^-11 of itself (2^-22 where the output is F16) or 2^-25 of the largest.
+ *  Block sizes up to 1024, head sizes 64, 128 and 256, any group; num_blocks *
+ *  num_kv_heads * block_size below 2^32.
  */
 size_t pa_scaled_attention_workspace_bytes(int num_seqs, int num_queries, int num_q_heads,
                                            int num_kv_heads, int head_size,

@@ -9,19 +9,23 @@
 // tiles over the same key tiles, or, where one tile holds all rows (drafts), the
 // even and the odd key tiles, joined at the end. Roles:
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
-//   warps 8-11       load K (12-14: V): codes from the cache's blocks into staging slots of
-//                    a warp's own, 16 keys at a time by asynchronous copies, a second slice
-//                    under way; from there widened to binary16 -- exactly, as in
-//                    scaled_attention.cuh -- into the swizzled tiles that the MMAs read;
+//   warps 8-11       load K (12-14: V): codes from the cache's blocks into two staging slots
+//                    of a warp's own by asynchronous copies, 32 keys at a time in two pieces,
+//                    the next slice's under way; from there widened to binary16 -- exactly, as
+//                    in scaled_attention.cuh -- into the swizzled tiles that the MMAs read;
 //   warp 15          issues tcgen05.mma: S0, S1, then PV0, S0', PV1, S1', ...
-// Softmax warps without rows (40 rows of drafts leave two of four) load too: 64 contexts of
-// 2304 tokens with 5 drafted each 146 us, 167 with the same warps idle.
-// What bounds it is instructions: a warp gets one in some eight cycles, and the roles' loops
-// together have to fit the instruction cache. Loops of their own for K and V, unrolled over
-// register buffers, and an issuer inlined three times had four in ten warps waiting for
-// instructions: 482 us for 8 chunks of 512 that take 370 with one copy of each. A softmax holds
-// 64 scores at a time for the same reason, and so that 16 warps of 128 registers do without
-// a split of them by role (17 warps of 96 spill: 560 us).
+// A softmax warp without rows (40 rows of drafts leave two of four) is a fourth for V.
+// What bounds it is a stream's chain of scores, softmax and P V -- a warp gets an instruction
+// in about eight cycles -- and the loaders' instructions beside it. Slices of 32 keys, whose
+// bookkeeping is done once and the blocks looked up by a lane each, took drafts (64 contexts of
+// 2304 tokens, 5 drafted each) from 147 us to 129 where 16 keys had taken 300 instructions; P V of
+// half of the keys while the others' weights are made, 133 to 128 (two terms: 167 to 158).
+// The roles' loops together have to fit the instruction cache: loops of their own for K and V,
+// unrolled over register buffers, and an issuer inlined three times had four in ten warps
+// waiting for instructions: 482 us for 8 chunks of 512 that take 366 with one copy of each. A
+// softmax holds 64 scores at a time for the same reason, and so that 16 warps of 128 registers
+// do without a split of them by role. 17 warps of 96 registers and 16 scores at a time: 420 us;
+// two threads a row (24 warps of 80): 387, though drafts in two terms gain 4 %.
 // (The fence between the loaders' stores and the MMAs' reads is the issuer's, which waits
 // for the tile: a loader's own waited for its loads in flight, 541 us for 510.)
 //
@@ -47,7 +51,8 @@ namespace pagedkv {
 constexpr int kSpThreads = 16 * 32;
 constexpr int kSpMmaWarp = 15;
 constexpr int kSpLoaders = 4;                      // warps for K, one less for V; and up to three softmax warps without rows
-constexpr int kSpSlice = 16;                       // keys a warp widens at a time
+constexpr int kSpSlice = 32;                       // keys of a loader at a time,
+constexpr int kSpPiece = 16;                       // copied and widened in two pieces
 constexpr int kSpSlices = 128 / kSpSlice;
 constexpr int kSpRing = 8;                         // tiles whose scales are kept
 constexpr float kSpMoveLog2 = 8.f;                 // the running maximum moves when a score passes it by this
@@ -61,10 +66,10 @@ struct SpShape {
     static constexpr int kKOff = 2 * kQBytes;
     static constexpr int kVOff = kKOff + NSK * kTile;
     static constexpr int kStagingOff = kVOff + NSV * kTile;            // two slices of codes and their scale for each loader
-    static constexpr int kSlot = kSpSlice * D + 16;                    // (a scale for each group)
+    static constexpr int kSlot = kSpPiece * D;
     static constexpr int kBarOff = kStagingOff + (2 * kSpLoaders - 1) * 2 * kSlot;
-    // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[2] drain q_ready
-    static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 6;
+    // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[4] drain q_ready
+    static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 8;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;            // tmem base, abort flag
     static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;   // [kSpRing][N / kG] pairs (a, log2 b)
     static constexpr int kUnitOff = kScaleOff + kSpRing * (N / 8) * 8;     // [256] the rows' powers of two, biased exponents
@@ -127,7 +132,7 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
 
 // One loader warp's slices of an operand: slice n = 8 j + q is keys 16 q .. of tile j.
 // Keys and values, and every warp that loads, run the same code, inlined once.
-// At most 8 warps load an operand, so that each has a slice of every tile: waiting for a
+// At most kSpSlices warps load an operand, so that each has a slice of every tile: waiting for a
 // stage's phase by parity needs that.
 template <typename CT, int D, int kG>
 __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, const uint8_t* staging, uint8_t* ring, int stages, float* scales,
@@ -135,7 +140,9 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
                                         int ntiles, int which, int loaders, int lane, volatile int* abort_flag) {
     using Sh = SpShape<D>;
     constexpr int CPR = D / 16;                    // 16-code chunks of a row
-    constexpr int PER = kSpSlice * CPR / 32;       // of a lane's
+    constexpr int PER = kSpPiece * CPR / 32;       // of a lane's, of a piece
+    constexpr int PARTS = kSpSlice / kG;           // runs of kG keys, in one block each
+    constexpr int PIECE_PARTS = kSpPiece / kG, PER_PART = PER / PIECE_PARTS;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
     const float* block_scales = keys ? p.k_scales : p.v_scales;
     const int B = p.block_size;
@@ -145,71 +152,75 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
     const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
     constexpr int STEP = 32 / CPR;                 // rows of a pass
     const uint8_t* cache = (keys ? p.k_cache : p.v_cache) + chunk * 16;
-    // A slice's parts of kG keys lie in one block each. Table entry and row of the block, of
-    // the slice whose ids are read next; they move on without a division.
-    constexpr int PARTS = kSpSlice / kG, PER_PART = PER / PARTS;
-    int entry[PARTS], in[PARTS];
-#pragma unroll
-    for (int h = 0; h < PARTS; ++h) {
-        const int key = T0 + which * kSpSlice + h * kG;
-        entry[h] = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
-        in[h] = key - entry[h] * B;
+    // Lane h, and those that repeat it, look up part h of the slices: table entry and row in
+    // the block, which move on without a division.
+    const int part = lane & (PARTS - 1);
+    int left = kend - T0 - which * kSpSlice;       // keys from the slice to look up on
+    int entry, in;
+    {
+        const int key = T0 + which * kSpSlice + part * kG;
+        entry = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
+        in = key - entry * B;
     }
     const int entry_step = loaders * kSpSlice / B, in_step = loaders * kSpSlice % B;
-    int left = kend - T0 - which * kSpSlice;       // keys from that slice on
-    int blk[PARTS], blk_in[PARTS], blk_left = 0;   // of the slice to copy next
+    int blk = -1, blk_in = 0, blk_left = 0;
     auto look = [&] {
         blk_left = left;
-#pragma unroll
-        for (int h = 0; h < PARTS; ++h) {
-            blk_in[h] = in[h];
-            blk[h] = left > h * kG ? table[entry[h]] : -1;
-            entry[h] += entry_step;
-            in[h] += in_step;
-            if (in[h] >= B) {
-                in[h] -= B;
-                ++entry[h];
-            }
+        blk_in = in;
+        blk = left > part * kG ? table[entry] : -1;
+        entry += entry_step;
+        in += in_step;
+        if (in >= B) {
+            in -= B;
+            ++entry;
         }
         left -= loaders * kSpSlice;
     };
-    // a lane copies, and later widens, its own chunks: nothing of the staging slots is shared
-    const uint32_t mine = smem_u32(staging) + lane * 16, my_scale = smem_u32(staging) + kSpSlice * D + lane * 4;
-    int to_copy = which;
-    auto fetch = [&](int slot) {
-        if (to_copy < last)
-#pragma unroll
-        for (int h = 0; h < PARTS; ++h) {
-            const uint32_t to = mine + slot * Sh::kSlot + h * PER_PART * 512;
-            const bool there = (uint32_t)blk[h] < (uint32_t)p.num_blocks;
-            if (there && blk_left >= (h + 1) * kG) {
-                const uint32_t slab = (uint32_t)blk[h] * p.num_kv_heads + kvh;
-                const uint8_t* from = cache + (size_t)(slab * B + blk_in[h] + row0) * D;
-#pragma unroll
-                for (int i = 0; i < PER_PART; ++i) cp_async16(to + i * 512, from + i * STEP * D);
-                if (lane == h) cp_async4(my_scale + slot * Sh::kSlot, block_scales + slab, true);
-            } else {                               // the context's end, or a bad block: zeros
-                const int keys_here = blk_left - h * kG;
-                if (!there && keys_here > 0 && lane == 0 && p.status) atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
-                const uint32_t slab = there ? (uint32_t)blk[h] * p.num_kv_heads + kvh : 0u;
-                const uint8_t* from = cache + (size_t)(slab * B + blk_in[h] + row0) * D;
-                const int here = there ? keys_here - row0 : 0;         // of this lane's rows, STEP apart
-#pragma unroll 1
-                for (int i = 0; i < PER_PART; ++i)
-                    cp_async16(to + i * 512, i * STEP < here ? from + i * STEP * D : cache, i * STEP < here);
-                if (lane == h) cp_async4(my_scale + slot * Sh::kSlot, block_scales + slab, there);
-            }
+    // of the slice to copy: the part's first row in the pool (~0: none), its scale, keys left
+    uint32_t row = ~0u;
+    float scale = 0.f;
+    int copy_left = 0;
+    auto place = [&] {
+        copy_left = blk_left;
+        row = ~0u;
+        scale = 0.f;
+        if ((uint32_t)blk < (uint32_t)p.num_blocks) {
+            const uint32_t slab = (uint32_t)blk * p.num_kv_heads + kvh;
+            row = slab * B + blk_in;
+            scale = block_scales[slab];
+        } else if (lane < PARTS && copy_left > part * kG && p.status) {
+            atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
         }
-        cp_async_commit();
-        to_copy += loaders;
     };
-    // two slices under way; the blocks' ids one further ahead
+    // a lane copies, and later widens, its own chunks: nothing of the staging slots is shared
+    const uint32_t mine = smem_u32(staging) + lane * 16;
+    auto fetch = [&](int piece, bool any) {
+        if (any)
+#pragma unroll
+            for (int h = 0; h < PIECE_PARTS; ++h) {
+                const uint32_t to = mine + piece * Sh::kSlot + h * PER_PART * 512;
+                const uint32_t at = __shfl_sync(0xffffffffu, row, piece * PIECE_PARTS + h);
+                const int here = copy_left - (piece * PIECE_PARTS + h) * kG;
+                if (at != ~0u && here >= kG) {
+                    const uint8_t* from = cache + (size_t)(at + row0) * D;
+#pragma unroll
+                    for (int i = 0; i < PER_PART; ++i) cp_async16(to + i * 512, from + i * STEP * D);
+                } else {                           // the context's end, or a bad block: zeros
+                    const int rows = at != ~0u ? here - row0 : 0;      // of this lane's, STEP apart
+                    const uint8_t* from = cache + ((size_t)at + row0) * D;
+#pragma unroll 1
+                    for (int i = 0; i < PER_PART; ++i)
+                        cp_async16(to + i * 512, i * STEP < rows ? from + i * STEP * D : cache, i * STEP < rows);
+                }
+            }
+        cp_async_commit();
+    };
     look();
-    fetch(0);
+    place();
     look();
-    fetch(1);
-    look();
-    int tile = 0, st = 0, slot = 0;                // of the slice to widen: key tile, its stage, staging slot
+    fetch(0, which < last);
+    fetch(1, which < last);
+    int tile = 0, st = 0;                          // of the slice to widen: key tile, its stage
     uint32_t phase = 1;                            // of its stage's `empty`; the first round waits for nothing
 #pragma unroll 1
     for (int n = which; n < last; n += loaders) {
@@ -221,11 +232,13 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
                 phase ^= 1u;
             }
         }
-        cp_async_wait<1>();
-        const uint32_t at = mine + slot * Sh::kSlot;
+        const float now = scale;
+        place();
+        look();
         if (lane < PARTS) {
-            const float scale = ld_shared(my_scale + slot * Sh::kSlot);
-            scales[((tile % kSpRing) * (Sh::N / kG) + q * PARTS + lane) * 2 + (keys ? 0 : 1)] = keys ? scale : log2f(scale);
+            float2* to = reinterpret_cast<float2*>(scales) + (tile % kSpRing) * (Sh::N / kG) + q * PARTS + lane;
+            if (keys) to->x = now;
+            else to->y = log2f(now);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&scale_bar[tile % kSpRing]);
@@ -234,29 +247,59 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
             if (!__all_sync(0xffffffffu, ok)) break;
         }
         uint8_t* to = ring + st * Sh::kTile + q * kSpSlice * 128;
+#pragma unroll 1
+        for (int piece = 0; piece < kSpSlice / kSpPiece; ++piece) {
+            cp_async_wait<1>();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint4 v = ld_shared4(at + i * 512);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[8];
+            for (int i = 0; i < PER; ++i) {
+                const uint4 v = ld_shared4(mine + piece * Sh::kSlot + i * 512);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t u = biased<CT>(w[k]);
-                o[2 * k] = widen2<CT>(u, 0x4140);
-                o[2 * k + 1] = widen2<CT>(u, 0x4342);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t u = biased<CT>(w[k]);
+                    o[2 * k] = widen2<CT>(u, 0x4140);
+                    o[2 * k + 1] = widen2<CT>(u, 0x4342);
+                }
+                const int r = i * STEP + row0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<uint4*>(to + piece * kSpPiece * 128 + sw128_chunk<Sh::N>(r, 2 * chunk + h)) =
+                        make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
-            const int r = i * STEP + row0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4*>(to + sw128_chunk<Sh::N>(r, 2 * chunk + h)) = make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+            fetch(piece, n + loaders < last);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);     // the MMA issuer, which waits for it, has the fence between the proxies
-        fetch(slot);
-        look();
-        slot ^= 1;
     }
     cp_async_wait<0>();
+}
+
+// The sequence of this CTA: the longest contexts' first, so that what is left when SMs run
+// out of work is short (64 contexts of 512-4096 tokens with 5 drafted: 121 us, 132 in their
+// order; 8 chunks of 512 in contexts of 512-8192: 320 us, 366). With more than kSpSorted sequences there are waves enough for it not to matter.
+constexpr int kSpSorted = 128;
+__device__ __forceinline__ int sp_sequence(const int32_t* context_lens, int num_seqs, int* lens) {
+    if (num_seqs == 1 || num_seqs > kSpSorted) return blockIdx.z;
+    __shared__ int mine;
+    const int t = threadIdx.x;
+    int len = 0;
+    if (t < kSpSorted) {
+        len = t < num_seqs ? context_lens[t] : INT_MIN;
+        lens[t] = len;
+    }
+    __syncthreads();
+    if (t < num_seqs) {
+        int longer = 0;
+        for (int u = 0; u < num_seqs; u += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(lens + u);
+            longer += (v.x > len || (v.x == len && u < t)) + (v.y > len || (v.y == len && u + 1 < t)) +
+                      (v.z > len || (v.z == len && u + 2 < t)) + (v.w > len || (v.w == len && u + 3 < t));
+        }
+        if (longer == (int)blockIdx.z) mine = t;
+    }
+    __syncthreads();
+    return mine;
 }
 
 template <typename CT, int D, int kG, bool kTwoTerms>
@@ -274,8 +317,8 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     uint64_t* v_empty = v_full + NSV;
     uint64_t* scale_bar = v_empty + NSV;           // [kSpRing]
     uint64_t* s_full = scale_bar + kSpRing;        // [2], by query tile
-    uint64_t* p_full = s_full + 2;                 // [2]
-    uint64_t* drain = p_full + 2;
+    uint64_t* p_full = s_full + 2;                 // [half of the keys][query tile]
+    uint64_t* drain = p_full + 4;
     uint64_t* q_ready = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sh::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::kMiscOff + 4);
@@ -283,7 +326,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     uint8_t* units = sm + Sh::kUnitOff;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int s = blockIdx.z;
+    const int s = sp_sequence(p.context_lens, p.num_seqs, reinterpret_cast<int*>(sm));
     const int pair = blockIdx.y / p.num_kv_heads, kvh = blockIdx.y - pair * p.num_kv_heads;
     int L, q0, Q;
     if (!scaled_sequence(p, s, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0, L, q0, Q)) return;
@@ -317,6 +360,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], max(1, warps_of(t)));
+            mbar_init(&p_full[2 + t], max(1, warps_of(t)));
         }
         mbar_init(drain, 1);
         mbar_init(q_ready, kTcSoftmaxThreads / 32);
@@ -365,19 +409,23 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         };
         auto pv = [&](int t, int i) -> bool {
             const int j = tile_of(t, i), st = j % NSV;
-            if (!wait(&p_full[t], i)) return false;
-            if (t == 0 || !two) {
-                if (!wait(&v_full[st], j / NSV)) return false;
-                fence_async_smem();
-            }
-            tc_fence_after();
             const uint64_t va = v_desc + st * (Sh::kTile >> 4);
             const uint32_t pt = tmem + t * Sh::kTileCols;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {                              // the first half while the second's weights are made
+                if (!wait(&p_full[2 * h + t], i)) return false;
+                if (h == 0 && (t == 0 || !two)) {
+                    if (!wait(&v_full[st], j / NSV)) return false;
+                    fence_async_smem();
+                }
+                tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
+                for (int kk = 0; kk < N / 32; ++kk)
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk)
-                    sp_mma_ts(leader, pt + N, pt + (kk >> 1) * 32 + u * 16 + (kk & 1) * 8, va + kk * (2048 >> 4), idO, i > 0 || u > 0 || kk > 0);
+                    for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
+                        sp_mma_ts(leader, pt + N, pt + h * (N / 2) + (kk >> 1) * 32 + u * 16 + (kk & 1) * 8,
+                                  va + (h * (N / 32) + kk) * (2048 >> 4), idO, i > 0 || h > 0 || u > 0 || kk > 0);
+            }
             if (t == 1 || !two) sp_commit(leader, &v_empty[st]);
             return true;
         };
@@ -447,14 +495,15 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         const int steps = warp < 8 ? steps_of(qt) : 0;
         if (warp >= 8 || spare) {
             const bool keys = spare ? qt == 0 : warp < 12;
-            const int more = two ? 0 : 4 - warps_of(0);                // spare warps of either stream
+            const int base = keys ? kSpLoaders : kSpLoaders - 1, more = two ? 0 : min(kSpSlices - base, 4 - warps_of(0));                // spare warps of either stream
             const int more_which = (warp & 3) - warps_of(qt);
-            const int which = spare ? (qt ? kSpLoaders - 1 : kSpLoaders) + more_which : warp & 3;
+            const int which = spare ? base + more_which : warp & 3;
             const uint8_t* staging = spare ? sm + Sh::kQBytes + (qt * 3 + more_which) * 2 * Sh::kSlot
                                            : sm + Sh::kStagingOff + (warp - 8) * 2 * Sh::kSlot;
-            sp_load<CT, D, kG>(p, keys, staging, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
+            if (!spare || more_which < more)
+                sp_load<CT, D, kG>(p, keys, staging, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
                                keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles, which,
-                               (keys ? kSpLoaders : kSpLoaders - 1) + more, lane, abort_flag);
+                               base + more, lane, abort_flag);
             if (spare && join) named_barrier(3, kTcSoftmaxThreads);
         } else if (steps > 0 && (warp & 3) < warps_of(qt)) {
             const uint32_t sbuf = tmem + ((uint32_t)((warp & 3) * 32) << 16) + qt * Sh::kTileCols;
@@ -535,6 +584,19 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 l *= al;
                 const float m_sub = m_use == -INFINITY ? 0.f : m_use;
                 m = m_use;
+                if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
+                    // O holds the tiles before this one: S of this tile came after their P.V
+                    const float alpha = al * drop;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32(obuf + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc_st32(obuf + c, o);
+                    }
+                }
                 // ---- the weights, 32 keys at a time, their scores read again: a loop of few
                 // instructions and registers, the next scores under way. Weights lie over their
                 // scores: those of keys 32 h .. in columns 32 h .., their second terms in 32 h + 16 ..
@@ -575,24 +637,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     tc_wait_ld32(xb);
                     if (h == 0) tc_ld32(sbuf + 64, xa);
                     weigh(xb, h + 1);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[h + qt]);
                 }
-                if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
-                    // O holds the tiles before this one: S of this tile came after their P.V
-                    const float alpha = al * drop;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc_ld32(obuf + c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tc_st32(obuf + c, o);
-                    }
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[qt]);
             }
             if (ok) {
                 ok = tc_wait(drain, 0u, p.status, abort_flag);

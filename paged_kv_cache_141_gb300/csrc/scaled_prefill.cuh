@@ -337,7 +337,14 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     const int first_pos = L - Q;
     const int seen = first_pos + (row0 + rows - 1) / G + 1;
     const int T0 = blockIdx.x * p.partition_size;
-    if (T0 >= seen) return;                        // (an empty context has no query here)
+    if (T0 >= seen) {
+        // a token with an empty context: zeros (with partitions, from their merge)
+        if (seen <= 0 && p.max_parts == 1) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)q0 * p.num_q_heads + kvh * G + row0) * D);
+            for (int i = tid; i < rows * (D / 8); i += kSpThreads) to[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
     const int kend = min(T0 + p.partition_size, seen);
     const int ntiles = (kend - T0 + N - 1) / N;
     // stream t's steps, and the key tile of step i

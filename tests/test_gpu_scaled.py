@@ -222,6 +222,21 @@ def test_empty_contexts():
     run_attention("e4m3", "f16", 8, 2, 64, 16, [0, 0], [1] * 2)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_empty_contexts_of_many_rows(D):
+    run_attention("int8", "bf16", 40, 1, D, 16, [0, 5, 0, 300], [1] * 4)
+    run_attention("e4m3", "f16", 600, 2, D, 16, [0, 0, 70], [1] * 3)
+    run_attention("e4m3", "f16", 40, 1, D, 16, [0, 5, 0, 300], [1] * 4, max_len=5000)      # partitions
+
+
+@pytest.mark.parametrize("S", [2, 127, 128, 129, 200])
+def test_many_sequences_of_many_rows(S):
+    # contexts of one length, of none, and in no order: each sequence is served once
+    lens = [(37 * s) % 61 if s % 3 else 40 for s in range(S)]
+    run_attention("int8", "bf16", 8, 1, 64, 8, lens, [min(L, (5 * s) % 7) for s, L in enumerate(lens)], seed=S)
+    run_attention("e4m3", "f16", 36, 1, 64, 16, lens, [1] * S, seed=S)
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("lens", [[5000], [4096, 255, 256, 257, 1, 2048], [1, 20001]])
 def test_decode_partitions(kind, lens):

@@ -156,7 +156,10 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     Weights w{p.target_probs + (row0 + a) * p.target_stride, nullptr, -1};
     if (a < n) {
         if (p.draft_probs) w.q = p.draft_probs + ((size_t)s * K + a) * p.draft_stride;
-        else w.without = p.draft_tokens[(size_t)s * K + a];
+        else {
+            const int64_t x = p.draft_tokens[(size_t)s * K + a];
+            if (x < V) w.without = x;              // (one that is no token takes nothing away)
+        }
     }
     auto started = cluster.barrier_arrive();       // every CTA of the cluster runs before its memory is written
     bool first_pass = true;

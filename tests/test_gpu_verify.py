@@ -144,3 +144,15 @@ def test_bad_data():
     odd[3:6] = 0.0
     out, acc, status = call(target=odd)
     assert status == pk().DEV_BAD_PROB and out[1] == [-1] * 3 and out[0][acc[0]] == -1 and out[2:] == fine[0][2:]
+
+
+@pytest.mark.parametrize("token", [2 ** 32 + 5, 2 ** 63 - 1, 100, -1, -2 ** 63])
+def test_a_token_outside_the_vocabulary_takes_nothing_away(token):
+    target = torch.zeros(2, 100, device="cuda")
+    target[:, 5:7] = 0.5
+    out = torch.empty(1, 2, dtype=torch.int64, device="cuda")
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    acc, status = t([77]), t([0])
+    pk().verify_drafts(out, acc, target, torch.tensor([[token]], device="cuda"), torch.tensor([[0.5, 0.25]], device="cuda"), t([0, 2]),
+                       dev_status=status)
+    assert out.tolist() == [[5, -1]] and acc.tolist() == [0] and int(status) == pk().DEV_BAD_TOKEN

@@ -123,14 +123,14 @@ ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_k
                        int head_size, int block_size, int max_queries, int max_context_len) {
     ScaledPlan l{};
     const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
-    const bool tc = rows > 32 && head_size <= 128 && block_size % 8 == 0;
-    l.tile_rows = tc ? 256 : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
+    const bool tc = rows > 32 && block_size % 8 == 0;
+    l.tile_rows = tc ? (head_size == 256 ? 128 : 256) : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
     l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);
     if (!tc) {
         // the CTAs that an SM holds, by their registers and rings
         const int ctas = head_size == 256 ? 1 : (l.tile_rows == 8 ? 3 : 2);
-        l.workers = 152 * ctas * kScaledWarps;
+        l.workers = 152 * ctas * scaled_warps(head_size, l.tile_rows);
         l.stages_before = align256((size_t)l.workers * 2 * l.tile_rows * (head_size + 2) * sizeof(float));
         l.total = l.stages_before + align256(((size_t)num_seqs + 1) * sizeof(int64_t));
         l.max_parts = 1;
@@ -1298,7 +1298,7 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
     divide_by(block_size, p.block_mul, p.block_shift);
     divide_by(p.group, p.group_mul, p.group_shift);
     p.status = dev_status;
-    p.num_blocks = num_blocks;
+    p.num_blocks = num_blocks < INT32_MAX ? num_blocks : INT32_MAX;      // (all that a table's entries can name)
     p.max_blocks = max_blocks_per_seq;
     p.num_seqs = num_seqs;
     p.num_queries = num_queries;

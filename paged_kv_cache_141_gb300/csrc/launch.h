@@ -375,8 +375,9 @@ struct ScaledAttnParams {
     int bf16;                     // the query's and the output's type; else binary16
 };
 
-// Warps of a CTA that share the stages, and the stages of a worker.
-constexpr int kScaledWarps = 4;
+// Warps of a CTA that share the stages, and the stages of a worker. At head size 256 a CTA has
+// an SM to itself and as many warps as rings fit its shared memory.
+constexpr int scaled_warps(int head_size, int tile_rows) { return head_size < 256 ? 4 : (tile_rows == 8 ? 6 : 5); }
 #ifdef __CUDACC__
 __host__ __device__
 #endif

@@ -712,7 +712,7 @@ scaled_join_kernel(const __grid_constant__ ScaledAttnParams p) {
 template <typename CT, int D, int NT, bool kTwoTerms>
 cudaError_t launch_scaled_rows(const ScaledAttnParams& p, cudaStream_t stream) {
     using S = ScaledShape<D, NT>;
-    constexpr int W = kScaledWarps;
+    constexpr int W = scaled_warps(D, 8 * NT);
     auto kernel = scaled_attention_kernel<CT, D, NT, W, kTwoTerms>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), W * S::kWarpBytes);
     if (e != cudaSuccess) return e;

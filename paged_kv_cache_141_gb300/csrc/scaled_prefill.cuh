@@ -7,7 +7,10 @@
 // 128. Two streams, each with scores, weights and an output of its own in TMEM, so
 // that the tensor cores work for one while the other's softmax runs: the two query
 // tiles over the same key tiles, or, where one tile holds all rows (drafts), the
-// even and the odd key tiles, joined at the end. Roles:
+// even and the odd key tiles, joined at the end. At head size 256 TMEM holds one output: one
+// stream of one query tile, key tiles of 64, and scores in two places by turns, so that the
+// next are on their way during a softmax (8 chunks of 512, 16/4 heads: 206 us, 668 TFLOP/s;
+// 1,287 on warp-level tiles of 16 rows). Roles:
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
 //   warps 8-11       load K (12-14: V): codes from the cache's blocks into two staging slots
 //                    of a warp's own by asynchronous copies, 32 keys at a time in two pieces,
@@ -51,23 +54,24 @@ namespace pagedkv {
 constexpr int kSpThreads = 16 * 32;
 constexpr int kSpMmaWarp = 15;
 constexpr int kSpLoaders = 4;                      // warps for K, one less for V; and up to three softmax warps without rows
-constexpr int kSpSlice = 32;                       // keys of a loader at a time,
-constexpr int kSpPiece = 16;                       // copied and widened in two pieces
-constexpr int kSpSlices = 128 / kSpSlice;
+constexpr int kSpSlices = 4;                       // of a key tile, each a loader's at a time
 constexpr int kSpRing = 8;                         // tiles whose scales are kept
 constexpr float kSpMoveLog2 = 8.f;                 // the running maximum moves when a score passes it by this
 
 template <int D>
 struct SpShape {
-    static constexpr int N = 128;
+    static constexpr bool kOne = D == 256;                             // one stream
+    static constexpr int N = kOne ? 64 : 128;                          // keys of a tile
+    static constexpr int kSlice = N / kSpSlices, kPiece = kSlice / 2;  // of a slice, of its pieces
+    static constexpr int kRows = kOne ? kTcRows : 2 * kTcRows;
     static constexpr int kQBytes = kTcRows * D * 2;                    // a query tile
     static constexpr int kTile = N * D * 2;                            // a K (V) stage
     static constexpr int NSK = 2, NSV = 2;
-    static constexpr int kKOff = 2 * kQBytes;
+    static constexpr int kKOff = kRows / kTcRows * kQBytes;
     static constexpr int kVOff = kKOff + NSK * kTile;
-    static constexpr int kStagingOff = kVOff + NSV * kTile;            // two slices of codes and their scale for each loader
-    static constexpr int kSlot = kSpPiece * D;
-    static constexpr int kBarOff = kStagingOff + (2 * kSpLoaders - 1) * 2 * kSlot;
+    static constexpr int kStagingOff = kVOff + NSV * kTile;            // two pieces of codes for each loader
+    static constexpr int kSlot = kPiece * D;
+    static constexpr int kBarOff = kStagingOff + (2 * kSpLoaders - !kOne) * 2 * kSlot;
     // k_full[NSK] k_empty[NSK] v_full[NSV] v_empty[NSV] scales[kSpRing] s_full[2] p_full[4] drain q_ready
     static constexpr int kNumBars = 2 * NSK + 2 * NSV + kSpRing + 8;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;            // tmem base, abort flag
@@ -76,9 +80,11 @@ struct SpShape {
     static constexpr int kBytes = kUnitOff + 256;
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemCols = 512;
-    static constexpr int kTileCols = N + D;                            // S (then P), O
-    static_assert(2 * kTileCols <= kTmemCols, "TMEM columns");
-    static_assert(6 * 2 * kSlot <= kQBytes, "more loaders' slots fit the second query tile's place");
+    // S (then P) and O of each stream; of one stream, S twice and O
+    static constexpr int kSCols = kOne ? N : N + D;                    // from one S to the other
+    static constexpr int kOCol = kOne ? 2 * N : N;
+    static_assert((kOne ? 2 * N + D : 2 * (N + D)) <= kTmemCols, "TMEM columns");
+    static_assert(kOne || 2 * kSlot <= kQBytes, "a loader more has its slots in the second query tile's place");
     static_assert(2 * kTcRows * 4 <= kTile, "the streams trade maxima and sums in a K stage");
     static_assert(kAlloc <= kTcSmemLimit, "shared memory");
     // Scales live until both softmaxes have read them: a loader writes those of tile j once it
@@ -120,7 +126,8 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
     return v;
 }
 
-// tcgen05.wait::ld, on which the loaded registers depend: no use moves above it.
+// tcgen05.wait::ld, on which the loaded registers depend: no use moves above it. (Nothing that
+// could move the registers themselves, a branch or a wait, stands between a load and this.)
 __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
@@ -140,29 +147,29 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
                                         int ntiles, int which, int loaders, int lane, volatile int* abort_flag) {
     using Sh = SpShape<D>;
     constexpr int CPR = D / 16;                    // 16-code chunks of a row
-    constexpr int PER = kSpPiece * CPR / 32;       // of a lane's, of a piece
-    constexpr int PARTS = kSpSlice / kG;           // runs of kG keys, in one block each
-    constexpr int PIECE_PARTS = kSpPiece / kG, PER_PART = PER / PIECE_PARTS;
+    constexpr int PER = Sh::kPiece * CPR / 32;       // of a lane's, of a piece
+    constexpr int PARTS = Sh::kSlice / kG;           // runs of kG keys, in one block each
+    constexpr int PIECE_PARTS = Sh::kPiece / kG, PER_PART = PER / PIECE_PARTS;
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks;
     const float* block_scales = keys ? p.k_scales : p.v_scales;
     const int B = p.block_size;
     const int last = kSpSlices * ntiles;
     // eight lanes that store together hold two rows of one 64-column span, in all banks
-    const int chunk = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3;
-    const int row0 = D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2;
+    const int chunk = D == 256 ? (lane & 3) + ((lane >> 3) << 2) : (D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3);
+    const int row0 = D == 256 ? (lane >> 2) & 1 : (D == 128 ? ((lane >> 2) & 1) + ((lane >> 4) << 1) : lane >> 2);
     constexpr int STEP = 32 / CPR;                 // rows of a pass
     const uint8_t* cache = (keys ? p.k_cache : p.v_cache) + chunk * 16;
     // Lane h, and those that repeat it, look up part h of the slices: table entry and row in
     // the block, which move on without a division.
     const int part = lane & (PARTS - 1);
-    int left = kend - T0 - which * kSpSlice;       // keys from the slice to look up on
+    int left = kend - T0 - which * Sh::kSlice;       // keys from the slice to look up on
     int entry, in;
     {
-        const int key = T0 + which * kSpSlice + part * kG;
+        const int key = T0 + which * Sh::kSlice + part * kG;
         entry = (int)((uint64_t)(uint32_t)key * p.block_mul >> p.block_shift);
         in = key - entry * B;
     }
-    const int entry_step = loaders * kSpSlice / B, in_step = loaders * kSpSlice % B;
+    const int entry_step = loaders * Sh::kSlice / B, in_step = loaders * Sh::kSlice % B;
     int blk = -1, blk_in = 0, blk_left = 0;
     auto look = [&] {
         blk_left = left;
@@ -174,7 +181,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
             in -= B;
             ++entry;
         }
-        left -= loaders * kSpSlice;
+        left -= loaders * Sh::kSlice;
     };
     // of the slice to copy: the part's first row in the pool (~0: none), its scale, keys left
     uint32_t row = ~0u;
@@ -246,9 +253,9 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
             const bool ok = tc_wait(&empty[st], phase, p.status, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
         }
-        uint8_t* to = ring + st * Sh::kTile + q * kSpSlice * 128;
+        uint8_t* to = ring + st * Sh::kTile + q * Sh::kSlice * 128;
 #pragma unroll 1
-        for (int piece = 0; piece < kSpSlice / kSpPiece; ++piece) {
+        for (int piece = 0; piece < Sh::kSlice / Sh::kPiece; ++piece) {
             cp_async_wait<1>();
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -264,7 +271,7 @@ __device__ __forceinline__ void sp_load(const ScaledAttnParams& p, bool keys, co
                 const int r = i * STEP + row0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<uint4*>(to + piece * kSpPiece * 128 + sw128_chunk<Sh::N>(r, 2 * chunk + h)) =
+                    *reinterpret_cast<uint4*>(to + piece * Sh::kPiece * 128 + sw128_chunk<Sh::N>(r, 2 * chunk + h)) =
                         make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
             fetch(piece, n + loaders < last);
@@ -308,6 +315,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     begin_overlapped();
     using Sh = SpShape<D>;
     constexpr bool kFp8 = std::is_same<CT, e4m3_t>::value;
+    constexpr bool kOne = Sh::kOne;
     constexpr int N = Sh::N, NSK = Sh::NSK, NSV = Sh::NSV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -331,7 +339,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     int L, q0, Q;
     if (!scaled_sequence(p, s, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0, L, q0, Q)) return;
     const int G = p.group;
-    const int row0 = pair * 2 * kTcRows, rows = min(2 * kTcRows, Q * G - row0);
+    const int row0 = pair * Sh::kRows, rows = min(Sh::kRows, Q * G - row0);
     if (rows <= 0) return;
     const bool two = rows > kTcRows;               // query tiles; else the streams take alternate key tiles
     const int first_pos = L - Q;
@@ -348,11 +356,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
     const int kend = min(T0 + p.partition_size, seen);
     const int ntiles = (kend - T0 + N - 1) / N;
     // stream t's steps, and the key tile of step i
-    auto steps_of = [&](int t) { return two ? ntiles : (ntiles + 1 - t) / 2; };
-    auto tile_of = [&](int t, int i) { return two ? i : 2 * i + t; };
+    auto steps_of = [&](int t) { return kOne ? (t ? 0 : ntiles) : (two ? ntiles : (ntiles + 1 - t) / 2); };
+    auto tile_of = [&](int t, int i) { return two || kOne ? i : 2 * i + t; };
     // softmax warps with rows in stream t
     auto warps_of = [&](int t) { return (min(kTcRows, two ? rows - t * kTcRows : rows) + 31) >> 5; };
-    const bool join = !two && ntiles > 1;          // the streams' results are one
+    const bool join = !kOne && !two && ntiles > 1;          // the streams' results are one
 
     if (tid == kSpMmaWarp * 32) {
         for (int i = 0; i < NSK; ++i) {
@@ -395,7 +403,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         const uint64_t q_desc = tc_desc(smem_u32(sm), 16, 1024);
         const uint64_t k_desc = tc_desc(smem_u32(sm + Sh::kKOff), 16, 1024);
         const uint64_t v_desc = tc_desc(smem_u32(sm + Sh::kVOff), N * 128, 1024);
-        static_assert(kTcRows == N, "one column span of Q and of K");
+        // S of stream t's step i; of one stream, S into place t
         auto qk = [&](int t, int i) -> bool {
             const int j = tile_of(t, i), st = j % NSK;
             if (t == 0 || !two) {
@@ -407,8 +415,9 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             const uint64_t ka = k_desc + st * (Sh::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
-                sp_mma(leader, tmem + t * Sh::kTileCols, qa + off, ka + off, idS, kk > 0);
+                const uint32_t q_off = ((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4;
+                const uint32_t k_off = ((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4;
+                sp_mma(leader, tmem + t * Sh::kSCols, qa + q_off, ka + k_off, idS, kk > 0);
             }
             if (t == 1 || !two) sp_commit(leader, &k_empty[st]);
             sp_commit(leader, &s_full[t]);
@@ -417,34 +426,44 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
         auto pv = [&](int t, int i) -> bool {
             const int j = tile_of(t, i), st = j % NSV;
             const uint64_t va = v_desc + st * (Sh::kTile >> 4);
-            const uint32_t pt = tmem + t * Sh::kTileCols;
+            const uint32_t pt = tmem + t * Sh::kSCols, ot = tmem + (kOne ? 0 : t * Sh::kSCols) + Sh::kOCol;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {                              // the first half while the second's weights are made
-                if (!wait(&p_full[2 * h + t], i)) return false;
+            for (int h = 0; h < N / 64; ++h) {                         // the first half while the second's weights are made
+                if (!wait(&p_full[2 * h + t], kOne ? i >> 1 : i)) return false;
                 if (h == 0 && (t == 0 || !two)) {
                     if (!wait(&v_full[st], j / NSV)) return false;
                     fence_async_smem();
                 }
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < N / 32; ++kk)
+                for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                     for (int u = 0; u < (kTwoTerms ? 2 : 1); ++u)
-                        sp_mma_ts(leader, pt + N, pt + h * (N / 2) + (kk >> 1) * 32 + u * 16 + (kk & 1) * 8,
-                                  va + (h * (N / 32) + kk) * (2048 >> 4), idO, i > 0 || h > 0 || u > 0 || kk > 0);
+                        sp_mma_ts(leader, ot, pt + h * 64 + (kk >> 1) * 32 + u * 16 + (kk & 1) * 8,
+                                  va + (h * 4 + kk) * (2048 >> 4), idO, i > 0 || h > 0 || u > 0 || kk > 0);
             }
             if (t == 1 || !two) sp_commit(leader, &v_empty[st]);
             return true;
         };
         bool ok = wait(q_ready, 0);
         tc_fence_after();
+        if constexpr (kOne) {
+            // the next scores are on their way while a softmax runs
+            ok = ok && qk(0, 0);
 #pragma unroll 1
-        for (int i = -1; i < steps_of(0) && ok; ++i)
-#pragma unroll 1
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (i >= 0 && i < steps_of(t)) ok = pv(t, i);
-                if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
+            for (int i = 0; i < ntiles && ok; ++i) {
+                if (i + 1 < ntiles) ok = qk((i + 1) & 1, i + 1);
+                if (ok) ok = pv(i & 1, i);
             }
+        } else {
+#pragma unroll 1
+            for (int i = -1; i < steps_of(0) && ok; ++i)
+#pragma unroll 1
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (i >= 0 && i < steps_of(t)) ok = pv(t, i);
+                    if (ok && i + 1 < steps_of(t)) ok = qk(t, i + 1);
+                }
+        }
         // everything issued ends before the epilogue reads O and before TMEM is freed
         sp_commit(leader, drain);
         mbar_wait_bounded(drain, 0, p.status);
@@ -457,10 +476,11 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             constexpr int CPR = D / 8;                                 // 16-byte chunks of a row
             constexpr int RPW = 32 / CPR;                              // rows at a time
             const int c = lane % CPR;
-            uint4 v[32 / RPW];
+            constexpr int ROWS = Sh::kRows / 8;                        // of a warp
+            uint4 v[ROWS / RPW];
 #pragma unroll
-            for (int i = 0; i < 32 / RPW; ++i) {
-                const int rr = warp * 32 + i * RPW + lane / CPR, row = row0 + rr;
+            for (int i = 0; i < ROWS / RPW; ++i) {
+                const int rr = warp * ROWS + i * RPW + lane / CPR, row = row0 + rr;
                 v[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (rr < rows) {
                     const int token = over_group(row);
@@ -469,8 +489,8 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 32 / RPW; ++i) {
-                const int rr = warp * 32 + i * RPW + lane / CPR;
+            for (int i = 0; i < ROWS / RPW; ++i) {
+                const int rr = warp * ROWS + i * RPW + lane / CPR;
                 uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                 uint32_t m2 = 0u;                                      // magnitudes order as integers
 #pragma unroll
@@ -487,8 +507,8 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     const float2 f = p.bf16 ? unpack2<__nv_bfloat16>(w[k]) : unpack2<__half>(w[k]);
                     w[k] = pack2<__half>(f.x * inv, f.y * inv);
                 }
-                if (qt == 0 || two) {                                  // (else its place is the loaders')
-                    *reinterpret_cast<uint4*>(sm + qt * Sh::kQBytes + sw128_chunk<kTcRows>(rr & (kTcRows - 1), c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (rr < kTcRows || two) {                             // (else its place is a loader's)
+                    *reinterpret_cast<uint4*>(sm + (rr >> 7) * Sh::kQBytes + sw128_chunk<kTcRows>(rr & (kTcRows - 1), c)) = make_uint4(w[0], w[1], w[2], w[3]);
                     if (c == 0) units[rr] = (uint8_t)(__float_as_uint(unit) >> 23);
                 }
             }
@@ -497,24 +517,22 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             if (lane == 0) mbar_arrive(q_ready);
             if (!two) named_barrier(4, kTcSoftmaxThreads);             // both streams read the first tile's units
         }
-        // ---- loaders: warps 8-15, and the softmax warps without rows
-        const bool spare = warp < 8 && !two && (warp & 3) >= warps_of(qt);
+        // ---- loaders: warps 8-14, and a softmax warp without rows
+        const bool spare = kOne ? warp == 4 : warp < 8 && !two && (warp & 3) >= warps_of(qt);
         const int steps = warp < 8 ? steps_of(qt) : 0;
         if (warp >= 8 || spare) {
-            const bool keys = spare ? qt == 0 : warp < 12;
-            const int base = keys ? kSpLoaders : kSpLoaders - 1, more = two ? 0 : min(kSpSlices - base, 4 - warps_of(0));                // spare warps of either stream
-            const int more_which = (warp & 3) - warps_of(qt);
-            const int which = spare ? base + more_which : warp & 3;
-            const uint8_t* staging = spare ? sm + Sh::kQBytes + (qt * 3 + more_which) * 2 * Sh::kSlot
-                                           : sm + Sh::kStagingOff + (warp - 8) * 2 * Sh::kSlot;
-            if (!spare || more_which < more)
-                sp_load<CT, D, kG>(p, keys, staging, sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
-                               keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles, which,
-                               base + more, lane, abort_flag);
+            const bool keys = !spare && warp < 8 + kSpLoaders;
+            const bool more = kOne || (!two && warps_of(1) < 4);       // a fourth for V: the first such warp of stream 1
+            if (!spare || warp == 4 + (kOne ? 0 : warps_of(1)))
+                sp_load<CT, D, kG>(p, keys, !spare ? sm + Sh::kStagingOff + (warp - 8) * 2 * Sh::kSlot
+                                                   : (kOne ? sm + Sh::kStagingOff + 7 * 2 * Sh::kSlot : sm + Sh::kQBytes),
+                                   sm + (keys ? Sh::kKOff : Sh::kVOff), keys ? NSK : NSV, reinterpret_cast<float*>(scales),
+                                   keys ? k_full : v_full, keys ? k_empty : v_empty, scale_bar, s, kvh, T0, kend, ntiles,
+                                   spare ? 3 : warp & 3, keys || more ? kSpLoaders : kSpLoaders - 1, lane, abort_flag);
             if (spare && join) named_barrier(3, kTcSoftmaxThreads);
         } else if (steps > 0 && (warp & 3) < warps_of(qt)) {
-            const uint32_t sbuf = tmem + ((uint32_t)((warp & 3) * 32) << 16) + qt * Sh::kTileCols;
-            const uint32_t obuf = sbuf + N;
+            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + qt * Sh::kSCols;
+            const uint32_t obuf = lanes + Sh::kOCol;
             const int rr = (two ? qt * kTcRows : 0) + r;
             const bool valid = rr < rows;
             const int row = row0 + min(rr, rows - 1);
@@ -526,8 +544,9 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             bool ok = true;
             for (int i = 0; i < steps; ++i) {
                 const int j = tile_of(qt, i);
+                const uint32_t sbuf = lanes + (kOne ? (i & 1) * N : 0);
                 ok = tc_wait(&scale_bar[j % kSpRing], (uint32_t)((j / kSpRing) & 1), p.status, abort_flag) &&
-                     tc_wait(&s_full[qt], (uint32_t)(i & 1), p.status, abort_flag);
+                     tc_wait(&s_full[kOne ? i & 1 : qt], (uint32_t)((kOne ? i >> 1 : i) & 1), p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -570,12 +589,12 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 };
                 tc_ld32(sbuf, xa);
 #pragma unroll 1
-                for (int h = 0; h < 4; h += 2) {
+                for (int h = 0; h < N / 32; h += 2) {
                     tc_wait_ld32(xa);
                     tc_ld32(sbuf + 32 * h + 32, xb);
                     largest(xa, h);
                     tc_wait_ld32(xb);
-                    tc_ld32(sbuf + (h == 0 ? 64 : 0), xa);             // (at last the first again, for the weights)
+                    if (h + 2 < N / 32) tc_ld32(sbuf + 32 * h + 64, xa);
                     largest(xb, h + 1);
                 }
                 const bool wider = b_most > e_ref;                     // the same for every row
@@ -592,13 +611,19 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 const float m_sub = m_use == -INFINITY ? 0.f : m_use;
                 m = m_use;
                 if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
-                    // O holds the tiles before this one: S of this tile came after their P.V
+                    // O holds the tiles before this one: S of this tile came after their P.V, of
+                    // one stream after all but the last
+                    if constexpr (kOne) {
+                        ok = __all_sync(0xffffffffu, tc_wait(&v_empty[(i - 1) % NSV], (uint32_t)((i - 1) / NSV & 1), p.status, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                     const float alpha = al * drop;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tc_ld32(obuf + c, o);
-                        tc_wait_ld();
+                        tc_wait_ld32(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                         tc_st32(obuf + c, o);
@@ -636,18 +661,20 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     tc_st_n<16>(sbuf + 32 * h, hi);
                     if constexpr (kTwoTerms) tc_st_n<16>(sbuf + 32 * h + 16, lo);
                 };
+                tc_ld32(sbuf, xa);
 #pragma unroll 1
-                for (int h = 0; h < 4; h += 2) {
+                for (int h = 0; h < N / 32; h += 2) {
                     tc_wait_ld32(xa);
                     tc_ld32(sbuf + 32 * h + 32, xb);
                     weigh(xa, h);
                     tc_wait_ld32(xb);
-                    if (h == 0) tc_ld32(sbuf + 64, xa);
+                    if (h + 2 < N / 32) tc_ld32(sbuf + 64, xa);
                     weigh(xb, h + 1);
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[h + qt]);
+                    // (of one stream by turns: a warp may be a tile ahead of another)
+                    if (lane == 0) mbar_arrive(&p_full[h + (kOne ? i & 1 : qt)]);
                 }
             }
             if (ok) {
@@ -667,7 +694,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tc_ld32(obuf + c, o);
-                        tc_wait_ld();
+                        tc_wait_ld32(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) other[r * D + ((c + e + r) & (D - 1))] = __uint_as_float(o[e]) * fall;
                     }
@@ -702,7 +729,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tc_ld32(obuf + c, o);
-                    tc_wait_ld();
+                    tc_wait_ld32(o);
                     float f[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -831,7 +858,7 @@ scaled_merge_kernel(const __grid_constant__ ScaledAttnParams p) {
 
 template <typename CT, int D, bool kTwoTerms>
 cudaError_t launch_scaled_prefill_head(const ScaledAttnParams& p, cudaStream_t stream) {
-    const cudaError_t e = p.block_size % 16 == 0 ? launch_scaled_prefill_terms<CT, D, 16, kTwoTerms>(p, stream)
+    const cudaError_t e = D < 256 && p.block_size % 16 == 0 ? launch_scaled_prefill_terms<CT, D, D < 256 ? 16 : 8, kTwoTerms>(p, stream)
                                                  : launch_scaled_prefill_terms<CT, D, 8, kTwoTerms>(p, stream);
     if (e != cudaSuccess || p.max_parts == 1) return e;
     return launch_overlapped(scaled_merge_kernel<D>, p, dim3(p.num_q_heads, p.max_queries, p.num_seqs), kScaledMergeThreads, 0, stream);
@@ -843,6 +870,7 @@ cudaError_t launch_scaled_prefill(const ScaledAttnParams& p, int head_size, cuda
     switch (head_size) {
     case 64: return launch_scaled_prefill_head<CT, 64, kTwoTerms>(p, stream);
     case 128: return launch_scaled_prefill_head<CT, 128, kTwoTerms>(p, stream);
+    case 256: return launch_scaled_prefill_head<CT, 256, kTwoTerms>(p, stream);
     }
     return cudaErrorInvalidValue;
 }

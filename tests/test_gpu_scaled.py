@@ -222,7 +222,7 @@ def test_empty_contexts():
     run_attention("e4m3", "f16", 8, 2, 64, 16, [0, 0], [1] * 2)
 
 
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_empty_contexts_of_many_rows(D):
     run_attention("int8", "bf16", 40, 1, D, 16, [0, 5, 0, 300], [1] * 4)
     run_attention("e4m3", "f16", 600, 2, D, 16, [0, 0, 70], [1] * 3)
@@ -235,6 +235,7 @@ def test_many_sequences_of_many_rows(S):
     lens = [(37 * s) % 61 if s % 3 else 40 for s in range(S)]
     run_attention("int8", "bf16", 8, 1, 64, 8, lens, [min(L, (5 * s) % 7) for s, L in enumerate(lens)], seed=S)
     run_attention("e4m3", "f16", 36, 1, 64, 16, lens, [1] * S, seed=S)
+    run_attention("e4m3", "bf16", 36, 1, 256, 16, lens, [1] * S, seed=S)
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
@@ -263,7 +264,7 @@ def test_chunks(kind, heads):
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("B", [1, 4, 8, 16, 24, 40, 48, 128, 1024])
-@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("f16", 128)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("f16", 128), ("bf16", 256), ("f16", 256)])
 def test_many_rows_over_blocks(kind, B, dtype, D):
     lens = [500, 45, 1300, 129, 9]
     run_attention(kind, dtype, 8, 1, D, B, lens, [6, 45, 30, 1, 9], seed=B + D, tail=2)
@@ -271,10 +272,11 @@ def test_many_rows_over_blocks(kind, B, dtype, D):
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_many_rows_in_partitions(kind, D):
     # few sequences, long contexts: the tcgen05 kernel's partitions, some of which a row does not see
-    run_attention(kind, "bf16", 8, 1, D, 16, [9000, 1025, 4096], [7, 6, 5], seed=D)
+    for _ in range(5):                                                       # (warps run ahead of each other by turns)
+        run_attention(kind, "bf16", 8, 1, D, 16, [9000, 1025, 4096], [7, 6, 5], seed=D)
     run_attention(kind, "f16", 8, 1, D, 8, [3000, 2048], [300, 1], seed=D)
     run_attention(kind, "bf16", 8, 1, D, 32, [5000], [1100], seed=D)
 

@@ -113,17 +113,19 @@ struct ScaledPlan {
     size_t total;                             // bytes; the first region starts at 0
 };
 
-// How a call's work is cut. Up to 32 rows of a sequence and KV head: warp-level MMAs, the
-// smallest n-tiles that hold them, one wave of warps for all stages. More, at head size 64
-// or 128 and blocks of a multiple of 8 tokens: the tcgen05 kernel, 256 rows a CTA,
-// one CTA on an SM, and partitions of the context where the sequences, heads and row
-// tiles alone leave SMs idle; else tiles of 32 rows (16 at head size 256, whose
-// accumulators fill the registers).
+// How a call's work is cut. Up to 32 rows of a sequence and KV head (16 at head size 256, where
+// accumulators of more fill the registers): warp-level MMAs, the smallest n-tiles that hold them,
+// one wave of warps for all stages. More, in blocks of a multiple of 8 tokens: the tcgen05
+// kernel, 256 (128) rows a CTA, one CTA on an SM, and partitions of the context where the
+// sequences, heads and row tiles alone leave SMs idle; else several such small tiles.
 ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_kv_heads,
                        int head_size, int block_size, int max_queries, int max_context_len) {
     ScaledPlan l{};
     const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
-    const bool tc = rows > 32 && block_size % 8 == 0;
+    // The tcgen05 kernel from where the warp-level tiles end: 64 contexts of 512-4096 tokens, 32/8
+    // heads of 128, 5 (8) tokens each, 20 (32) rows, take 107 (113) us on one tile of 32 rows and
+    // 119 (119) there; at head size 256, where a tile has 16 rows, 20 rows take 180 us and 97.
+    const bool tc = rows > (head_size == 256 ? 16 : 32) && block_size % 8 == 0;
     l.tile_rows = tc ? (head_size == 256 ? 128 : 256) : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;
     l.row_tiles = (int)(tiles < INT32_MAX ? tiles : INT32_MAX);

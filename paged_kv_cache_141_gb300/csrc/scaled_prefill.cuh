@@ -9,8 +9,8 @@
 // tiles over the same key tiles, or, where one tile holds all rows (drafts), the
 // even and the odd key tiles, joined at the end. At head size 256 TMEM holds one output: one
 // stream of one query tile, key tiles of 64, and scores in two places by turns, so that the
-// next are on their way during a softmax (8 chunks of 512, 16/4 heads: 206 us, 668 TFLOP/s;
-// 1,287 on warp-level tiles of 16 rows). Roles:
+// next are on their way during a softmax (8 chunks of 512, 16/4 heads: 180-206 us by card, 668
+// TFLOP/s at 206; 1,287 on warp-level tiles of 16 rows). Roles:
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread a row;
 //   warps 8-11       load K (12-14: V): codes from the cache's blocks into two staging slots
 //                    of a warp's own by asynchronous copies, 32 keys at a time in two pieces,
@@ -22,7 +22,8 @@
 // in about eight cycles -- and the loaders' instructions beside it. Slices of 32 keys, whose
 // bookkeeping is done once and the blocks looked up by a lane each, took drafts (64 contexts of
 // 2304 tokens, 5 drafted each) from 147 us to 129 where 16 keys had taken 300 instructions; P V of
-// half of the keys while the others' weights are made, 133 to 128 (two terms: 167 to 158).
+// half of the keys while the others' weights are made, 133 to 128 (two terms: 167 to 158; 155 with
+// both terms in one store).
 // The roles' loops together have to fit the instruction cache: loops of their own for K and V,
 // unrolled over register buffers, and an issuer inlined three times had four in ten warps
 // waiting for instructions: 482 us for 8 chunks of 512 that take 366 with one copy of each. A
@@ -633,7 +634,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 // instructions and registers, the next scores under way. Weights lie over their
                 // scores: those of keys 32 h .. in columns 32 h .., their second terms in 32 h + 16 ..
                 auto weigh = [&](uint32_t (&x)[32], int h) {
-                    uint32_t hi[16], lo[16];
+                    uint32_t w2[kTwoTerms ? 32 : 16];                  // first terms, second terms
                     mask(x, 32 * h);
 #pragma unroll
                     for (int g = 0; g < 32 / kG; ++g) {
@@ -649,17 +650,16 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                             const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                             sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
                             const uint32_t w = pack2<__half>(e.x, e.y);
-                            hi[kG / 2 * g + c / 2] = w;
+                            w2[kG / 2 * g + c / 2] = w;
                             if constexpr (kTwoTerms) {
                                 const float2 rest = __ffma2_rn(unpack2<__half>(w), make_float2(-1.f, -1.f), e);
-                                lo[kG / 2 * g + c / 2] = pack2<__half>(rest.x, rest.y);
+                                w2[16 + kG / 2 * g + c / 2] = pack2<__half>(rest.x, rest.y);
                             }
                         }
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         l = fmaf(sum[0].x + sum[0].y, fast_exp2(-lift), l);
                     }
-                    tc_st_n<16>(sbuf + 32 * h, hi);
-                    if constexpr (kTwoTerms) tc_st_n<16>(sbuf + 32 * h + 16, lo);
+                    tc_st_n<kTwoTerms ? 32 : 16>(sbuf + 32 * h, w2);
                 };
                 tc_ld32(sbuf, xa);
 #pragma unroll 1

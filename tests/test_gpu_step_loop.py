@@ -194,16 +194,17 @@ def test_two_streams_of_steps():
         assert dev.out[:n].equal(other.out[:n])
 
 
+@pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("queries", [1, 5, 40])
-def test_repeated_and_replayed_calls_are_bit_identical(queries):
+def test_repeated_and_replayed_calls_are_bit_identical(queries, D):
     lens = [700, 64, 2500]
     table, nb = sc.table_of(3, 160, 1)
-    (kc, ks), (vc, vs) = (sc.pool(nb, 2, 16, 128, "e4m3", i) for i in range(2))
+    (kc, ks), (vc, vs) = (sc.pool(nb, 2, 16, D, "e4m3", i) for i in range(2))
     t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     args = [x.cuda() for x in (kc, vc, ks, vs)] + [table.cuda(), t(lens)]
-    q = torch.randn(3 * queries, 8, 128, device="cuda").bfloat16()
+    q = torch.randn(3 * queries, 8, D, device="cuda").bfloat16()
     qs = t([0, queries, 2 * queries, 3 * queries])
-    ws = pk().alloc_scaled_workspace(3, 3 * queries, 8, 2, 128, queries, 2560)
+    ws = pk().alloc_scaled_workspace(3, 3 * queries, 8, 2, D, queries, 2560)
     outs = [torch.empty_like(q) for _ in range(2)]
     call = lambda out: pk().scaled_attention(out, q, *args, 2560, 0.09, ws, query_start=qs, max_queries_per_seq=queries)  # noqa: E731
     call(outs[0])
@@ -218,6 +219,34 @@ def test_repeated_and_replayed_calls_are_bit_identical(queries):
     g.replay()
     torch.cuda.synchronize()
     assert outs[0].equal(outs[1]) and outs[0].equal(replayed)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_replays_follow_lengths_that_change(D):
+    # many rows: which context is the longest, who has how many tokens and who none, change between replays
+    table, nb = sc.table_of(4, 100, 3)
+    (kc, ks), (vc, vs) = (sc.pool(nb, 1, 16, D, "int8", i) for i in range(2))
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, starts, status = t([50] * 4), t([0, 9, 18, 27, 36]), t([0])
+    query = torch.randn(36, 8, D).half()
+    out = torch.empty_like(query).cuda()
+    ws = pk().alloc_scaled_workspace(4, 36, 8, 1, D, 20, 1600)
+    args = [query.cuda(), *(x.cuda() for x in (kc, vc, ks, vs, table)), lens, 1600, D ** -0.5, ws]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        pk().scaled_attention(out, *args, query_start=starts, max_queries_per_seq=20, dev_status=status)
+    for L, n in (([1600, 9, 300, 77], [9, 9, 9, 9]), ([20, 1600, 0, 1100], [16, 20, 0, 0]), ([5, 6, 1599, 1], [5, 6, 20, 1])):
+        at = [0]
+        for k in n:
+            at.append(at[-1] + k)
+        lens.copy_(t(L))
+        starts.copy_(t(at))
+        out.fill_(7.0)
+        g.replay()
+        want, tol = sc.attention(query, kc, vc, ks, vs, table, L, at, D ** -0.5, query.dtype)
+        sc.assert_close(out, want, tol)
+        assert int(status) == 0 and bool((out[at[-1]:] == 7.0).all())
 
 
 def test_copied_blocks_keep_their_codes():

@@ -257,8 +257,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // Host: raise a kernel's dynamic shared-memory limit once per device.
-// `key` identifies the kernel (its address); the table is small and
-// append-only, and a race only repeats the (idempotent) attribute call.
+// `key` identifies the kernel (its address); `bytes` is the most that any launch
+// of it takes, as only a kernel's first call here sets the limit. The table is
+// small and append-only, and a race only repeats the (idempotent) attribute call.
 inline cudaError_t ensure_smem_attribute(const void* key, int bytes) {
     if (bytes <= 48 * 1024) return cudaSuccess;
     int dev = 0;

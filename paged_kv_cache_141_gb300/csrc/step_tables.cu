@@ -333,7 +333,7 @@ cudaError_t launch_tables(const TablesParams& tables, bool extend, cudaStream_t 
     const int cluster = work <= kTablesThreads ? 1 : kTablesCluster;
     auto kernel = extend ? extend_tables_kernel : trim_tables_kernel;
     const int smem = 12 * p.num_seqs;
-    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), smem);
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), 12 * kMaxTableSeqs);
     if (e != cudaSuccess) return e;
     e = launch_overlapped(kernel, p, dim3(cluster), threads, smem, stream, cluster);
     if (e != cudaSuccess || !p.slots_apart) return e;

@@ -289,7 +289,7 @@ cudaError_t launch_threads(const VerifyParams& p, int cluster, cudaStream_t stre
     auto kernel = verify_drafts_kernel<T>;
     const int tiles = (p.vocab + kVerifyTile - 1) / kVerifyTile;
     const int smem = (tiles + cluster - 1) / cluster * (int)sizeof(Pair);
-    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), smem);
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), kMaxVerifyVocab / kVerifyTile * (int)sizeof(Pair));
     if (e != cudaSuccess) return e;
     return launch_overlapped(kernel, p, dim3(p.num_seqs * cluster), T, smem, stream, cluster);
 }

@@ -62,3 +62,30 @@ def test_trim_of_many_requests(S, shared):
     stack[5:5 + len(back)] = back[::-1]
     assert st.d_stack.tolist() == stack and int(st.d_free) == 5 + len(back)
     assert st.d_lens.tolist() == [L - d for L, d in zip(lens, drop)] and int(st.status) == 0
+
+
+def test_as_many_blocks_as_a_stack_holds():
+    """2^31 - 1 blocks of one token, taken by one call and given back by another."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("takes 34 GB")
+    S, most, N, part = 16384, 131072, 2 ** 31 - 1, 2 ** 27
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.full((S, most), -1, dtype=torch.int32, device="cuda")
+    stack = torch.arange(N, dtype=torch.int32, device="cuda")
+    slots = torch.full((N,), -2, dtype=torch.int64, device="cuda")
+    lens, new, free, status, starts = t([0] * S), t([most] * (S - 1) + [most - 1]), t([N]), t([0]), t([0] * (S + 1))
+    pk().extend_tables(table, lens, new, stack, free, slots, starts, 1, dev_status=status)
+    assert int(status) == 0 and int(free) == 0 and lens.equal(new) and int(starts[S]) == N
+    flat = table.view(-1)
+    for a in range(0, N, part):
+        b = min(N, a + part)
+        want = torch.arange(N - 1 - a, N - 1 - b, -1, dtype=torch.int32, device="cuda")
+        assert flat[a:b].equal(want) and slots[a:b].equal(want.long())
+    assert int(flat[N]) == -1
+    del slots
+    stack.fill_(-3)
+    pk().trim_tables(table, lens, new, stack, free, 1, dev_status=status)
+    assert int(status) == 0 and int(free) == N and int(lens.count_nonzero()) == 0
+    for a in range(0, N, part):
+        b = min(N, a + part)
+        assert stack[a:b].equal(torch.arange(a, b, dtype=torch.int32, device="cuda"))

@@ -509,6 +509,10 @@ const float* prob_rows(PyObject* o, int dev, const char* name, int64_t& rows, in
     const int64_t d = t.dim();
     vocab = t.size(d - 1);
     rows = t.numel() == 0 ? 0 : t.numel() / vocab;
+    if (rows == 0 && d <= 3) {                     // a step without drafts: nothing is spaced
+        stride = vocab;
+        return t.const_data_ptr<float>();
+    }
     stride = t.size(d - 2) > 1 ? t.stride(d - 2) : (d == 3 && t.size(0) > 1 ? t.stride(0) : vocab);
     if ((vocab > 1 && t.stride(d - 1) != 1) || (d == 3 && t.size(0) > 1 && t.stride(0) != t.size(1) * stride) || d > 3)
         bad(std::string(name) + ": rows must be contiguous and evenly spaced");

@@ -174,10 +174,11 @@ extend_tables_kernel(const __grid_constant__ TablesParams p) {
     }
     const int me = rank * blockDim.x + threadIdx.x, threads = ranks * blockDim.x;
     const int top = top_step(S);
-    for (int64_t k = me; k < taken; k += threads) {         // (the step beyond the last may pass 32 bits)
+    // (`left` counts down: the step beyond the last may pass 2^31)
+    for (int k = me, left = (int)taken - me; left > 0; left -= threads, k += left > 0 ? threads : 0) {
         // several requests may share a first block where all but the last need none
-        const int s = owner_of(blk, S, top, (int)k);
-        p.block_tables[(size_t)s * p.max_blocks + (len[s] + B - 1) / B + ((int)k - blk[s])] = p.free_blocks[F - 1 - k];
+        const int s = owner_of(blk, S, top, k);
+        p.block_tables[(size_t)s * p.max_blocks + (len[s] + B - 1) / B + (k - blk[s])] = p.free_blocks[F - 1 - k];
     }
     if (p.slots_apart) return;
     for (int64_t t = me; t < T; t += threads) {
@@ -302,25 +303,22 @@ trim_tables_kernel(const __grid_constant__ TablesParams p) {
     // a warp takes runs of neighbours, most often one request's: their first and last tell
     constexpr int kAtOnce = 4, kRun = 32 * kAtOnce;                // entries whose loads are in flight together
     const int lane = threadIdx.x & 31, warps = ranks * (int)(blockDim.x >> 5), top = top_step(S);
-    // (unsigned: the run beyond the last may pass 31 bits)
-    const uint32_t count = (uint32_t)given;
-    for (uint32_t k0 = (rank * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kRun; k0 < count; k0 += warps * kRun) {
-        const int lo = owner_of(blk, S, top, (int)k0), hi = owner_of(blk, S, top, (int)(min(k0 + kRun, count) - 1));
+    // (unsigned: the run beyond the last may pass 2^31)
+    for (uint32_t k0 = (rank * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kRun; k0 < (uint32_t)given; k0 += warps * kRun) {
+        const int left = (int)given - (int)k0;
+        const int lo = owner_of(blk, S, top, (int)k0), hi = owner_of(blk, S, top, (int)k0 + min(kRun, left) - 1);
         int32_t id[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const uint32_t run = k0 + 32 * i + lane;
-            if (run < count) {
-                const int k = (int)run;
+            if (32 * i + lane < left) {
+                const int k = (int)k0 + 32 * i + lane;
                 const int s = lo == hi ? lo : lo + owner_of(blk + lo, hi - lo + 1, top_step(hi - lo + 1), k);
                 id[i] = p.block_tables[(size_t)s * p.max_blocks + from[s] + (k - blk[s])];
             }
         }
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const uint32_t k = k0 + 32 * i + lane;
-            if (k < count) p.stack[F + given - 1 - k] = id[i];
-        }
+        for (int i = 0; i < kAtOnce; ++i)
+            if (32 * i + lane < left) p.stack[F + given - 1 - (int)k0 - (32 * i + lane)] = id[i];
     }
 }
 

@@ -734,8 +734,9 @@ pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* valu
  *  Codes past a context's end are not read. An E4M3 NaN code within it is read as
  *  +-480 (pa_scaled_append writes none but under a NaN scale).
  *  Scores, softmax statistics and sums are binary32. The query meets the codes exactly
- *  but for components more than 2^14 below a row's largest; a weight meets them to
- *  within 2^-11 of itself (2^-22 where the output is F16) or 2^-25 of the largest.
+ *  but for components more than 2^14 below a row's largest; a weight (softmax times
+ *  value scale) meets them to within 2^-11 of itself (2^-22 where the output is F16) or
+ *  2^-30 of the row's largest among the tokens that it sees.
  *  Block sizes up to 1024, head sizes 64, 128 and 256, any group; num_blocks *
  *  num_kv_heads * block_size below 2^32.
  */

@@ -22,17 +22,21 @@
 //   S (16 tokens x 8 rows) = C_K Q^T on binary16 warp-level MMAs, the codes widened in
 //     registers, exactly: integers by the bits of 1024 + (c + 128), less 1152; E4M3 by
 //     moving the exponent field (values times 2^-8);
-//   softmax against a reference that moves only when a logit passes it by 2^8;
+//   softmax against a reference that moves only when a logit passes it by 2^8 (both rows of a
+//     lane at a time, in two-wide binary32 instructions);
 //   O^T += C_V^T P^T, with the value scales in the weights.
 //
 // Precision. The query meets the codes in binary16 under a power of two for each row
 // that brings its largest component into [1, 2): exact for bfloat16 and binary16 but for
 // components more than 2^14 below the row's largest. Scores, statistics and sums are
 // binary32. A weight p b is rounded to binary16 (2^-11, below half a step of the codes)
-// under a power of two shared by the stage's blocks, which follows the largest value
-// scale seen: 2^-14 of the largest weight before its bits thin out, 2^-25 of it before it
-// vanishes. A bfloat16 output's own rounding is eight times coarser; a binary16 output's
-// is no finer than the weights', and takes them in two terms (2^-22).
+// under a power of two of the row's own, which follows the largest weight among the tokens
+// that it sees: the largest stands between 2^5 and 2^15, so that 2^-19 of it keeps all its
+// bits and 2^-30 of it vanishes. (One unit for all rows, by the largest value scale among
+// the blocks read, would cost no more, but a block of large values that a row hardly attends
+// to, or does not see, would take the bits from all others.) A bfloat16 output's own
+// rounding is eight times coarser; a binary16 output's is no finer than the weights', and
+// takes them in two terms (2^-22).
 //
 // An item within one warp's piece is written out by it. Pieces of others go to the
 // workspace, two of a warp's at most (the end of an item that began before its piece, the
@@ -187,6 +191,14 @@ __device__ __forceinline__ void store_pair(const ScaledAttnParams& p, size_t at,
     else w = MmaOps<__half>::pack(x, y);
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = w;
 }
+
+// The unit of a row's weights, 2^(6 - d), as kWeightBias - d: a number whose lowest bits are
+// the unit's exponent, so that a shift makes it. d: of the row's largest weight p b, from
+// above, for p relative to the row's reference.
+constexpr float kWeightBias = 12582912.f + 133.f;  // 1.5 * 2^23, and 127 + 6
+constexpr float kLeastWeight = -110.f, kMostWeight = 128.f;
+__device__ __forceinline__ float weight_unit(float w_ref) { return __uint_as_float(__float_as_uint(w_ref) << 23); }
+__device__ __forceinline__ float weight_fall(float w_ref) { return __uint_as_float((254u << 23) - (__float_as_uint(w_ref) << 23)); }
 
 // Stages of a sequence's context; 0 where the call has nothing to do for it.
 __device__ __forceinline__ int scaled_stages(const ScaledAttnParams& p, int s, bool report, int& L, int& q0, int& Q) {
@@ -364,10 +376,15 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
 
     uint2 qr[S::kQReg ? NT * KS : 1];
     float hm[NT][2], m_ref[NT][2], l_run[NT][2];
-    int lim[NT][2];                                // tokens that the row sees
+    float w_ref[NT][2];                            // kWeightBias - d; weights are p b 2^(6 - d)
     float acc[NT][KS][4];
-    int e_ref = 0, all_see = 0, kvh = 0, row0 = 0, rows = 0;
+    int all_see = 0, kvh = 0, row0 = 0, rows = 0;
     bool whole = false;                            // from the item's first stage on
+    // tokens that row r sees (worked out where a stage is cut, as few are: in registers they
+    // would spill in the widest tiles)
+    auto sees = [&](int r) {
+        return r < rows ? now.L - now.Q + (int)((uint64_t)(uint32_t)(row0 + r) * p.group_mul >> p.group_shift) + 1 : 0;
+    };
     int slot = 0;
     for (int i = 0; i < count; ++i) {
         if (i == 0 || now.k == 0) {
@@ -377,18 +394,15 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             rows = max(0, min(S::kRows, now.Q * G - row0));
             whole = now.k == 0;
             scaled_query<CT, D, NT>(p, now.q0, kvh, row0, rows, lane, qr, qf, hm);
-            const int first_pos = now.L - now.Q;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int r = 8 * nt + 2 * t4 + j;
-                    lim[nt][j] = r < rows ? first_pos + (row0 + r) / G + 1 : 0;
                     m_ref[nt][j] = -INFINITY;
                     l_run[nt][j] = 0.f;
+                    w_ref[nt][j] = kWeightBias - kLeastWeight;
                 }
-            all_see = first_pos + row0 / G + 1;    // tokens below it are seen by every row
-            e_ref = -120;                          // value scales below 2^(e_ref + 1) fit the weights' range
+            all_see = now.L - now.Q + row0 / G + 1;    // tokens below it are seen by every row
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -442,33 +456,41 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             vb[i] = scales[kScaledStage + g + 8 * i];
         }
         const int vexp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(scales[kScaledStage + lane]) << 1 >> 24)) - 127;
-        bool move = vexp > e_ref;
+        const float v_room = kWeightBias + 8.f - (float)vexp;
+        bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) sc[nt][i >> 1][2 * (i & 1) + j] *= ka[i];
+            for (int i = 0; i < 4; ++i) {
+                float* x = &sc[nt][i >> 1][2 * (i & 1)];           // both rows
+                const float2 y = __fmul2_rn(make_float2(x[0], x[1]), make_float2(ka[i], ka[i]));
+                x[0] = y.x;
+                x[1] = y.y;
+            }
         if (__any_sync(0xffffffffu, key0 + kScaledStage > all_see)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 2; ++j) {
+                    const int lim = sees(8 * nt + 2 * t4 + j);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (key0 + g + 8 * i >= lim[nt][j]) sc[nt][i >> 1][2 * (i & 1) + j] = -INFINITY;
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + g + 8 * i >= lim) sc[nt][i >> 1][2 * (i & 1) + j] = -INFINITY;
+                }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float mx = fmaxf(fmaxf(sc[nt][0][j], sc[nt][0][2 + j]), fmaxf(sc[nt][1][j], sc[nt][1][2 + j]));
-                move |= mx * hm[nt][j] > m_ref[nt][j] + 8.f;
+                // no logit more than 2^8 above the reference, and no weight of 2^15, were
+                // the largest logit's value scale the stage's largest
+                move |= fmaf(mx, hm[nt][j], -m_ref[nt][j]) > fminf(8.f, v_room - w_ref[nt][j]);
             }
         if (__any_sync(0xffffffffu, move)) {
-            const int e_new = max(e_ref, vexp > e_ref ? vexp + 2 : e_ref);
-            const float drop = fast_exp2((float)(e_ref - e_new));
-            e_ref = e_new;
+            float bx[4];                           // the value scales' exponents
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bx[i] = (float)((int)(__float_as_uint(vb[i]) << 1 >> 24) - 127);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float alpha[2];
@@ -478,47 +500,56 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float m_new = fmaxf(m_ref[nt][j], mx * hm[nt][j]);
-                    const float al = m_new == -INFINITY || m_ref[nt][j] == -INFINITY ? 1.f : fast_exp2(m_ref[nt][j] - m_new);
+                    // whole numbers, as d: what moves from one to the other is not rounded
+                    const float m_new = fmaxf(m_ref[nt][j], ceilf(mx * hm[nt][j]));
+                    // the largest weight, to an octave (masked ones are none: -infinity or NaN here)
+                    float t = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaf(sc[nt][i >> 1][2 * (i & 1) + j], hm[nt][j], -m_new) + bx[i]);
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    const float fell = m_ref[nt][j] - m_new;       // (NaN where the row has seen nothing)
+                    const float d = kWeightBias - w_ref[nt][j], d_new = fminf(fmaxf(fmaxf(d + fell, ceilf(t)), kLeastWeight), kMostWeight);
+                    const bool none = m_new == -INFINITY || m_ref[nt][j] == -INFINITY;
                     m_ref[nt][j] = m_new;
-                    l_run[nt][j] *= al;
-                    alpha[j] = al * drop;
+                    w_ref[nt][j] = kWeightBias - d_new;
+                    l_run[nt][j] *= none ? 1.f : fast_exp2(fell);
+                    alpha[j] = none ? 1.f : fast_exp2(fell + (d - d_new));
                 }
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    acc[nt][i][0] *= alpha[0];
-                    acc[nt][i][1] *= alpha[1];
-                    acc[nt][i][2] *= alpha[0];
-                    acc[nt][i][3] *= alpha[1];
-                }
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 y = __fmul2_rn(make_float2(acc[nt][i][e], acc[nt][i][e + 1]), make_float2(alpha[0], alpha[1]));
+                        acc[nt][i][e] = y.x;
+                        acc[nt][i][e + 1] = y.y;
+                    }
             }
         }
-        const float lift = __uint_as_float((uint32_t)(127 + 6 - e_ref) << 23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vb[i] *= lift;
         uint32_t pb[NT][2][2], pl[kTwoTerms ? NT : 1][2][2];           // P^T fragments, and of the rests
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float w[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float m = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = fast_exp2(fmaf(sc[nt][i >> 1][2 * (i & 1) + j], hm[nt][j], -m));
-                    l_run[nt][j] += e;
-                    w[j][i] = e * vb[i];
-                }
-            }
+            // both rows at a time
+            const float2 less = make_float2(m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0], m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1]);
+            const float2 unit = make_float2(weight_unit(w_ref[nt][0]), weight_unit(w_ref[nt][1]));
+            float2 sum = make_float2(l_run[nt][0], l_run[nt][1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t hi = Ops::pack(w[0][k], w[1][k]);
+                const float2 t = __ffma2_rn(make_float2(sc[nt][k >> 1][2 * (k & 1)], sc[nt][k >> 1][2 * (k & 1) + 1]),
+                                            make_float2(hm[nt][0], hm[nt][1]), less);
+                const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                sum = __fadd2_rn(sum, e);
+                const float2 w = __fmul2_rn(__fmul2_rn(e, unit), make_float2(vb[k], vb[k]));
+                const uint32_t hi = Ops::pack(w.x, w.y);
                 pb[nt][k >> 1][k & 1] = movmatrix_trans(hi);
                 if constexpr (kTwoTerms) {
                     const float2 h = Ops::unpack(hi);
-                    pl[nt][k >> 1][k & 1] = movmatrix_trans(Ops::pack(w[0][k] - h.x, w[1][k] - h.y));
+                    pl[nt][k >> 1][k & 1] = movmatrix_trans(Ops::pack(w.x - h.x, w.y - h.y));
                 }
             }
+            l_run[nt][0] = sum.x;
+            l_run[nt][1] = sum.y;
         }
 
         // ---- O^T += C_V^T P^T: a chunk is 16 components of all 32 tokens; fragment
@@ -548,7 +579,6 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
         if (ends || i + 1 == count) {
             // ---- the item ends, or the piece does
             const bool done = whole && ends;
-            const float fall = __uint_as_float((uint32_t)(127 + e_ref - 6) << 23) * (kFp8 ? 256.f : 1.f);
             // where it began in this piece it is the piece's last, else its first
             float* part = p.parts + ((size_t)(blockIdx.x * W + warp) * 2 + (whole ? 1 : 0)) * S::kRows * (D + 2);
 #pragma unroll
@@ -561,17 +591,19 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
                     const int r = 8 * nt + 2 * t4 + j;
                     if (r >= rows) continue;
+                    const float fall = weight_fall(w_ref[nt][j]);
+                    constexpr float kBack = kFp8 ? 256.f : 1.f;                // (apart: their product may pass the largest number)
                     if (done) {
                         const int row = row0 + r, token = row / G;
                         const size_t at = ((size_t)(now.q0 + token) * p.num_q_heads + kvh * G + row - token * G) * D;
                         const float inv = __fdiv_rn(fall, l);
 #pragma unroll
                         for (int md = 0; md < KS; ++md)
-                            store_pair(p, at + 16 * md + 2 * g, acc[nt][md][j] * inv, acc[nt][md][2 + j] * inv);
+                            store_pair(p, at + 16 * md + 2 * g, acc[nt][md][j] * kBack * inv, acc[nt][md][2 + j] * kBack * inv);
                     } else {
 #pragma unroll
                         for (int md = 0; md < KS; ++md)
-                            *reinterpret_cast<float2*>(part + r * D + 16 * md + 2 * g) = make_float2(acc[nt][md][j] * fall, acc[nt][md][2 + j] * fall);
+                            *reinterpret_cast<float2*>(part + r * D + 16 * md + 2 * g) = make_float2(acc[nt][md][j] * kBack * fall, acc[nt][md][2 + j] * kBack * fall);
                         if (g == 0) {
                             part[S::kRows * D + r] = m_ref[nt][j];
                             part[S::kRows * (D + 1) + r] = l;

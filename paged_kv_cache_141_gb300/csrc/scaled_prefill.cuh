@@ -36,13 +36,16 @@
 // The scales stay out of the tiles. Blocks are multiples of kG = 16 or 8 tokens here, so a
 // group of kG columns of S has one key scale a and one value scale b: with raw
 // scores s and the row's unit u (scale, log2 e and the query's power of two),
-//     weight = 2^(s (u a) + (log2 b - e + 6) - m),
+//     weight = 2^(s (u a) + (log2 b - d + 6) - m),
 // one fused multiply-add and one exponential a score; the maximum is taken over raw
 // scores within a group (a >= 0) and the row's sum gets each group's weights divided by
-// 2^(log2 b - e + 6) again. e follows the largest value scale, with two octaves to spare:
-// weights reach the MMA below 2^15, rounded to binary16 (2^-11 of themselves; with a
-// binary16 output, whose own step is no larger, in two terms, 2^-22). A value scale more
-// than 2^60 below the largest counts as that: its weights vanish in binary16 either way.
+// 2^(log2 b - d + 6) again. d follows the largest of s (u a) + log2 b - m among the keys
+// that the row sees (one addition a group and row more than a unit for all rows by the
+// largest value scale, 1 % of the chunks' time; but that one gave the bits of all weights
+// to a block of large values that a row hardly attends to or does not see): the row's
+// largest weight reaches the MMA between 2^5 and 2^14, rounded to binary16 (2^-11 of
+// itself; with a binary16 output, whose own step is no larger, in two terms, 2^-22). A
+// value scale below 2^(d - 60) counts as that: its weights vanish in binary16 either way.
 //
 // Every wait is bounded, as in prefill_tc.cuh.
 #pragma once
@@ -57,7 +60,8 @@ constexpr int kSpMmaWarp = 15;
 constexpr int kSpLoaders = 4;                      // warps for K, one less for V; and up to three softmax warps without rows
 constexpr int kSpSlices = 4;                       // of a key tile, each a loader's at a time
 constexpr int kSpRing = 8;                         // tiles whose scales are kept
-constexpr float kSpMoveLog2 = 8.f;                 // the running maximum moves when a score passes it by this
+constexpr float kSpMoveLog2 = 8.f;                 // a row's references move when a score, a weight, passes them by this
+constexpr float kSpNoWeight = -1e4f;
 
 template <int D>
 struct SpShape {
@@ -541,7 +545,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
             const int pos = first_pos + token;                         // the last key that the row sees
             const float hm = p.q_mul * __uint_as_float((uint32_t)units[rr] << 23) * (kFp8 ? 256.f : 1.f);
             float m = -INFINITY, l = 0.f;
-            float e_ref = -1e4f;                                       // value scales up to 2^e_ref fit the weights
+            float d = kSpNoWeight;                                     // weights are p b 2^(6 - d), p relative to m
             bool ok = true;
             for (int i = 0; i < steps; ++i) {
                 const int j = tile_of(qt, i);
@@ -568,7 +572,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     }
                 };
                 // ---- the maximum
-                float m_cand = m, b_most = sp[0].y;
+                float m_cand = m, w_cand = -INFINITY;                  // of the logits, and of logit + log2 b
                 uint32_t xa[32], xb[32];
                 auto largest = [&](uint32_t (&x)[32], int h) {
                     mask(x, 32 * h);
@@ -584,8 +588,9 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                             y = fmax3(y, at(14), at(15));
                         }
                         const float2 ab = sp[32 / kG * h + g];
-                        m_cand = fmaxf(m_cand, fmaxf(y, z) * on_row(ab.x));
-                        b_most = fmaxf(b_most, ab.y);
+                        y = fmaxf(y, z) * on_row(ab.x);
+                        m_cand = fmaxf(m_cand, y);
+                        w_cand = fmaxf(w_cand, y + ab.y);
                     }
                 };
                 tc_ld32(sbuf, xa);
@@ -598,18 +603,18 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                     if (h + 2 < N / 32) tc_ld32(sbuf + 32 * h + 64, xa);
                     largest(xb, h + 1);
                 }
-                const bool wider = b_most > e_ref;                     // the same for every row
                 const bool moved = m_cand > m + kSpMoveLog2;
                 const float m_use = moved ? m_cand : m;
-                const float al = m == -INFINITY ? 1.f : fast_exp2(m - m_use);
-                float drop = 1.f;
-                if (wider) {
-                    const float e_new = ceilf(b_most) + 2.f;
-                    drop = fast_exp2(e_ref - e_new);
-                    e_ref = e_new;
-                }
-                l *= al;
                 const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+                const float fell = m == -INFINITY ? 0.f : m - m_use;
+                // d falls by what m rises, and rises to the row's largest weight
+                float d_use = fmaxf(d + fell, kSpNoWeight);
+                const float w_most = w_cand - m_sub;
+                const bool wider = w_most > d_use + kSpMoveLog2;
+                if (wider) d_use = ceilf(w_most);
+                l *= fast_exp2(fell);
+                const float alpha = fast_exp2(fell + (d - d_use));
+                d = d_use;
                 m = m_use;
                 if (i > 0 && __any_sync(0xffffffffu, moved || wider)) {
                     // O holds the tiles before this one: S of this tile came after their P.V, of
@@ -619,7 +624,6 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    const float alpha = al * drop;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
@@ -639,7 +643,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                     for (int g = 0; g < 32 / kG; ++g) {
                         const float2 ab = sp[32 / kG * h + g];
-                        const float lift = (ab.y < e_ref - 60.f ? -60.f : ab.y - e_ref) + 6.f;
+                        const float lift = (ab.y < d - 60.f ? -60.f : ab.y - d) + 6.f;
                         const float k1 = on_row(ab.x);
                         const float2 k2 = make_float2(k1, k1);
                         const float2 c2 = make_float2(lift - m_sub, lift - m_sub);
@@ -681,7 +685,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 ok = tc_wait(drain, 0u, p.status, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
             }
-            float fall = fast_exp2(e_ref - 6.f) * (kFp8 ? 256.f : 1.f);
+            float fall = fast_exp2(d - (kFp8 ? -2.f : 6.f));
             // two streams of one query tile: the second hands its rows to the first, in the
             // queries' place (every MMA is done, and every slice widened)
             float* other = reinterpret_cast<float*>(sm);               // [128][D], columns turned by the row

@@ -723,7 +723,8 @@ pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* valu
  *  out, query     [num_queries][num_q_heads][head_size], F16 or BF16; rows behind
  *                 the last sequence's are left as they are.
  *  k_cache, v_cache, k_scales, v_scales  as pa_scaled_append leaves them; any finite
- *                 scale >= 0 is read as it is.
+ *                 scale >= 0 is read as it is. A scale of NaN makes NaN of the rows that
+ *                 see a token of its block, and of no other.
  *  max_queries_per_seq  an upper bound of Q_s; 0 <= Q_s <= it and Q_s <=
  *                 context_lens[s] (else PA_DEV_BAD_LEN and the sequence is skipped).
  *  workspace      256-byte aligned, pa_scaled_attention_workspace_bytes(...) of these

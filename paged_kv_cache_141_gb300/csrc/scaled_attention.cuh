@@ -456,6 +456,16 @@ scaled_attention_kernel(const __grid_constant__ ScaledAttnParams p) {
             vb[i] = scales[kScaledStage + g + 8 * i];
         }
         const int vexp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(scales[kScaledStage + lane]) << 1 >> 24)) - 127;
+        if (vexp == 128) {
+            // a value scale that is no number goes with the key's: the rows that see the token get
+            // its NaN by their scores, and the weights of others, which are zero, stay so
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!(vb[i] < INFINITY)) {
+                    ka[i] = NAN;
+                    vb[i] = 0.f;
+                }
+        }
         const float v_room = kWeightBias + 8.f - (float)vexp;
         bool move = false;
 #pragma unroll

@@ -557,9 +557,9 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                 tc_fence_after();
                 const float2* sp = scales + (j % kSpRing) * (N / kG);         // broadcast reads
                 // the group's scale on the row's scores; zero must not meet a masked one
-                auto on_row = [&](float a) {
+                auto on_row = [&](float a, bool past) {
                     const float k = a * hm;
-                    return k == 0.f ? 1.17549435e-38f : k;
+                    return past | (k == 0.f) ? 1.17549435e-38f : k;
                 };
                 // keys of this tile that the row sees (at or below 0: none)
                 const int sees = pos + 1 - (T0 + j * N);
@@ -588,7 +588,7 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
                             y = fmax3(y, at(14), at(15));
                         }
                         const float2 ab = sp[32 / kG * h + g];
-                        y = fmaxf(y, z) * on_row(ab.x);
+                        y = fmaxf(y, z) * on_row(ab.x, false);
                         m_cand = fmaxf(m_cand, y);
                         w_cand = fmaxf(w_cand, y + ab.y);
                     }
@@ -643,8 +643,10 @@ scaled_prefill_kernel(const __grid_constant__ ScaledAttnParams p) {
 #pragma unroll
                     for (int g = 0; g < 32 / kG; ++g) {
                         const float2 ab = sp[32 / kG * h + g];
-                        const float lift = (ab.y < d - 60.f ? -60.f : ab.y - d) + 6.f;
-                        const float k1 = on_row(ab.x);
+                        // (of a group that the row does not see the scales may be no numbers)
+                        const bool past = 32 * h + kG * g >= sees;
+                        const float lift = (past | (ab.y < d - 60.f) ? -60.f : ab.y - d) + 6.f;
+                        const float k1 = on_row(ab.x, past);
                         const float2 k2 = make_float2(k1, k1);
                         const float2 c2 = make_float2(lift - m_sub, lift - m_sub);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

@@ -157,6 +157,48 @@ def test_value_scales_that_grow_and_shrink(kind, shape):
             c.check(cap)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("of", ["keys", "values", "both"])
+def test_what_is_not_a_number_stays_where_it_is_seen(kind, dtype, shape, of):
+    # scales of NaN in the newest block, where tokens before it are queries too, and in one of two sequences' last
+    c = Case(kind, dtype, shape, [shape[3] // 2 + 192, shape[3] + 120])
+    bad = c.table[0, (c.lens[0] - c.Q // 2) // c.B:-(-c.lens[0] // c.B)].long()
+    for x in {"keys": [c.ks], "values": [c.vs], "both": [c.ks, c.vs]}[of]:
+        x[bad, -1] = math.nan
+    want = c.check()
+    rows = want[:c.Q].isnan().any(-1)
+    assert bool(rows.any()) == (len(bad) > 0) and not bool(rows[0].any() and c.Q > 1) and not bool(want[c.Q:].isnan().any())
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (8, 1)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_draft_leaves_the_tokens_before_it(heads, bad):
+    """Through the append: the last of six new tokens is not finite, and begins a block."""
+    Hq, H = heads
+    D, B, L = 128, 16, 161
+    g = torch.Generator().manual_seed(3)
+    table, nb = sc.table_of(1, 11, 1)
+    k, v = (torch.randn(L, H, D, generator=g).bfloat16() for _ in range(2))
+    query = torch.randn(6, Hq, D, generator=g).bfloat16().cuda()
+    outs = []
+    for x in (None, k, v):
+        put = [t.clone().cuda() for t in (k, v)]
+        if x is not None:
+            put[0 if x is k else 1][-1, :, 3] = bad
+        kc, vc = (torch.zeros(nb, H, B, D, dtype=torch.int8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(nb, H, device="cuda") for _ in range(2))
+        t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        pk().scaled_append(*put, kc, vc, ks, vs, table.cuda(), t([L]), L, t([0, L]))
+        out = torch.empty_like(query)
+        ws = pk().alloc_scaled_workspace(1, 6, Hq, H, D, 6, L)
+        pk().scaled_attention(out, query, kc, vc, ks, vs, table.cuda(), t([L]), L, D ** -0.5, ws, query_start=t([0, 6]), max_queries_per_seq=6)
+        outs.append(out)
+    for out in outs[1:]:
+        assert out[:5].equal(outs[0][:5]) and bool(out[5].isnan().all())
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 def test_calls_repeat_bit_for_bit(shape):
     c = Case("int8", "bf16", shape, [2100, 350, 64])

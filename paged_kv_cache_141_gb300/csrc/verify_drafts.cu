@@ -14,12 +14,14 @@
 // cluster of CTAs takes a request, each CTA a contiguous section of the row in
 // tiles of 512, a warp a tile, whose sum stays in shared memory. The CTAs trade their
 // totals, the one whose section holds u W finds the tile among its sums, and one warp
-// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-44, as pairs of
-// binary32 numbers (binary64 units would take five times as long as the reads; binary64
-// across the lanes alone took 85 us where pairs took 63, and whole tiles without a test for
-// each value now take 50, 5.3 TB/s, for 256 requests of 128,256 tokens; one request of 32,000
-// takes 9.2: launch, three cluster barriers and the loads between them). With 100,000 borders between
-// tokens, sums to 2^-30 alone would draw another token in one request of 5,000.
+// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-41 of themselves
+// whatever the vocabulary: a tile's as a tree of pairs of binary32 numbers, a warp's tiles in
+// binary64 (pairs added tile after tile lose up to 2^-31 over a vocabulary of 2^22).
+// Binary64 units would take five times as long as the reads; binary64 across a tile's lanes
+// alone took 85 us where pairs took 63, and whole tiles without a test for each value now take
+// 51, 5.2 TB/s, for 256 requests of 128,256 tokens (0.8 of it the tiles' sums); one request of
+// 32,000 takes 9.3: launch, three cluster barriers and the loads between them. With 100,000
+// borders between tokens, sums to 2^-30 alone would draw another token in one request of 5,000.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -75,18 +77,29 @@ __device__ __forceinline__ Pair add(Pair x, Pair y) {
     return {s, (x.lo + y.lo) + ((x.hi - (s - t)) + (y.hi - t))};
 }
 __device__ __forceinline__ double value(Pair x) { return (double)x.hi + (double)x.lo; }
+// The same sum, |lo| <= 2^-24 |hi| again.
+__device__ __forceinline__ Pair normal(Pair x) {
+    const float s = x.hi + x.lo;
+    return {s, x.lo - (s - x.hi)};
+}
 
-// The sum of max(a - b, 0) over the warp's values; the differences keep their rounding
-// errors, as the sums do. A NaN stays.
+// The sum of max(a - b, 0) over the warp's values, as a tree; the differences keep their
+// rounding errors, as the sums do. A NaN stays. After k additions in a row lo is at most
+// (k + 1) 2^-24 of the sum, and the two roundings of the next one's lo 2^-24 of that: 9
+// levels, 108 2^-48 of the sum, less than 2^-41.
 __device__ __forceinline__ Pair tile_sum(const float (&a)[kVerifyPer], const float (&b)[kVerifyPer]) {
-    Pair x{0.f, 0.f};
+    Pair l[kVerifyPer];
 #pragma unroll
     for (int i = 0; i < kVerifyPer; ++i) {
-        float d = a[i] - b[i];
-        float e = (a[i] - d) - b[i];                               // exact for a >= b >= 0
-        if (d <= 0.f) d = e = 0.f;
-        x = add(x, {d, e});
+        l[i].hi = a[i] - b[i];
+        l[i].lo = (a[i] - l[i].hi) - b[i];                         // exact for a >= b >= 0
+        if (l[i].hi <= 0.f) l[i].hi = l[i].lo = 0.f;
     }
+#pragma unroll
+    for (int m = kVerifyPer / 2; m; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < m; ++i) l[i] = add(l[i], l[i + m]);
+    Pair x = l[0];
 #pragma unroll
     for (int m = 16; m; m >>= 1) x = add(x, {__shfl_xor_sync(0xffffffffu, x.hi, m), __shfl_xor_sync(0xffffffffu, x.lo, m)});
     return x;
@@ -167,23 +180,34 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const int per = (tiles + ranks - 1) / ranks;
     const int first = min(tiles, rank * per), mine = min(tiles, first + per) - first;
     for (;;) {
-        Pair sum{0.f, 0.f};
+        Pair part{0.f, 0.f};
         for (int t = warp; t < mine; t += kWarps) {
             float a[kVerifyPer], b[kVerifyPer];
             load_tile(w, (int64_t)(first + t) * kVerifyTile, V, lane, a, b);
-            const Pair total = tile_sum(a, b);
-            if (lane == 0) tile_sums[t] = total;
-            sum = add(sum, total);
+            part = tile_sum(a, b);
+            if (lane == 0) tile_sums[t] = part;
         }
-        if (lane == 0) s_part[warp] = sum;
+        if (mine > kWarps) {
+            // the warp's tiles in binary64: however many they are, nothing more is lost
+            __syncwarp();
+            double sum = 0;
+            for (int t = warp + lane * kWarps; t < mine; t += 32 * kWarps) sum += value(tile_sums[t]);
+            for (int m = 1; m < 32 && m * kWarps < mine; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);    // (lanes that have any)
+            part = {(float)sum, (float)(sum - (double)(float)sum)};
+        }
+        if (lane == 0) s_part[warp] = part;
         if (first_pass) cluster.barrier_wait(std::move(started));
         first_pass = false;
         __syncthreads();
         if (threadIdx.x < ranks) {
-            Pair c = s_part[0];
+            Pair c[kWarps];
 #pragma unroll
-            for (int i = 1; i < kWarps; ++i) c = add(c, s_part[i]);
-            cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = value(c);
+            for (int i = 0; i < kWarps; ++i) c[i] = s_part[i];
+#pragma unroll
+            for (int m = kWarps / 2; m; m >>= 1)
+#pragma unroll
+                for (int i = 0; i < m; ++i) c[i] = add(c[i], c[i + m]);
+            cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = value(c[0]);
         }
         if (ranks > 1) cluster.sync();
         else __syncthreads();
@@ -257,6 +281,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
                 all = add(all, {d, (x[i] - d) - y[i]});
                 last = i;
             }
+            if ((i & 3) == 3) all = normal(all);                   // sixteen additions in a row would be too many
             own[i] = all;
         }
         const double mine_all = value(all);

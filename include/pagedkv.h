@@ -775,7 +775,7 @@ pa_status pa_scaled_attention(void* out, const void* query, const void* k_cache,
  *                 are not read.
  *  uniforms       [num_seqs][max_drafts + 1] float32 in [0, 1): u_i of the drafts, and
  *                 last in the row the one that draws.
- *  Rows need not sum to 1. Sums are kept to 2^-41 of themselves. More
+ *  Rows need not sum to 1. Sums are kept to 2^-39 of themselves. More
  *  rows than max_drafts + 1, or outside [0, num_rows): PA_DEV_BAD_LEN, as without
  *  rows. vocab up to 2^22.
  */

@@ -14,14 +14,16 @@
 // cluster of CTAs takes a request, each CTA a contiguous section of the row in
 // tiles of 512, a warp a tile, whose sum stays in shared memory. The CTAs trade their
 // totals, the one whose section holds u W finds the tile among its sums, and one warp
-// reads that tile again (from L1 or L2) for the token. Sums are kept to 2^-41 of themselves
-// whatever the vocabulary: a tile's as a tree of pairs of binary32 numbers, a warp's tiles in
-// binary64 (pairs added tile after tile lose up to 2^-31 over a vocabulary of 2^22).
-// Binary64 units would take five times as long as the reads; binary64 across a tile's lanes
-// alone took 85 us where pairs took 63, and whole tiles without a test for each value now take
-// 51, 5.2 TB/s, for 256 requests of 128,256 tokens (0.8 of it the tiles' sums); one request of
-// 32,000 takes 9.3: launch, three cluster barriers and the loads between them. With 100,000
-// borders between tokens, sums to 2^-30 alone would draw another token in one request of 5,000.
+// reads that tile again (from L1 or L2) for the token. Sums are pairs of binary32 numbers, a
+// tile's as a tree, a warp's tiles dealt to its lanes: with 64 tiles a lane, of 2^22 tokens,
+// (99 + 3 64 + 3 8) 2^-48 of the sum at most, less than 2^-39 (added tile after tile in one
+// pair that is not brought back to |lo| <= 2^-24 |hi|, they lost up to 2^-31). Binary64
+// units would take five times as long as the reads; binary64 across the lanes alone took 85 us
+// where pairs took 63, across a warp's tiles alone 30.5 where this takes 28 (64 requests), and
+// whole tiles without a test for each value now take 50, 5.2 TB/s, for 256 requests of 128,256
+// tokens; one request of 32,000 takes 9.5: launch, three cluster barriers and the loads between them.
+// With 100,000 borders between tokens, sums to 2^-30 alone would draw another token in one
+// request of 5,000.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -36,6 +38,8 @@ namespace cg = cooperative_groups;
 constexpr int kVerifyTile = 512;
 constexpr int kVerifyPer = kVerifyTile / 32;       // of a tile, a lane's values
 constexpr int kVerifyCluster = 8;
+// Warps that run at once, 32 an SM.
+constexpr int kVerifyWave = 4864;
 
 // Row weights: p alone, p beyond q, or p without one token.
 struct Weights {
@@ -84,9 +88,9 @@ __device__ __forceinline__ Pair normal(Pair x) {
 }
 
 // The sum of max(a - b, 0) over the warp's values, as a tree; the differences keep their
-// rounding errors, as the sums do. A NaN stays. After k additions in a row lo is at most
-// (k + 1) 2^-24 of the sum, and the two roundings of the next one's lo 2^-24 of that: 9
-// levels, 108 2^-48 of the sum, less than 2^-41.
+// rounding errors, as the sums do. A NaN stays. At level k of the tree lo is at most
+// (k + 1) 2^-24 of the sum, and its two roundings (2 k + 1) 2^-48: 99 2^-48 after 9 levels.
+// (A sum of normal pairs is good to 3 2^-48.)
 __device__ __forceinline__ Pair tile_sum(const float (&a)[kVerifyPer], const float (&b)[kVerifyPer]) {
     Pair l[kVerifyPer];
 #pragma unroll
@@ -106,7 +110,7 @@ __device__ __forceinline__ Pair tile_sum(const float (&a)[kVerifyPer], const flo
 }
 
 template <int T>
-__global__ void __launch_bounds__(T)
+__global__ void __launch_bounds__(T, 1024 / T)
 verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     begin_overlapped();
     constexpr int kWarps = T / 32;
@@ -180,21 +184,19 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     const int per = (tiles + ranks - 1) / ranks;
     const int first = min(tiles, rank * per), mine = min(tiles, first + per) - first;
     for (;;) {
-        Pair part{0.f, 0.f};
+        Pair part{0.f, 0.f};                       // the warp's tiles, dealt to its lanes
+        int turn = lane;
         for (int t = warp; t < mine; t += kWarps) {
             float a[kVerifyPer], b[kVerifyPer];
             load_tile(w, (int64_t)(first + t) * kVerifyTile, V, lane, a, b);
-            part = tile_sum(a, b);
-            if (lane == 0) tile_sums[t] = part;
+            const Pair total = tile_sum(a, b);
+            if (lane == 0) tile_sums[t] = total;
+            const Pair next = normal(add(part, total));
+            if (turn == 0) part = next;
+            turn = (turn + 31) & 31;
         }
-        if (mine > kWarps) {
-            // the warp's tiles in binary64: however many they are, nothing more is lost
-            __syncwarp();
-            double sum = 0;
-            for (int t = warp + lane * kWarps; t < mine; t += 32 * kWarps) sum += value(tile_sums[t]);
-            for (int m = 1; m < 32 && m * kWarps < mine; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);    // (lanes that have any)
-            part = {(float)sum, (float)(sum - (double)(float)sum)};
-        }
+        for (int m = 1; m < 32 && m * kWarps < mine; m <<= 1)      // (over the lanes that were dealt any)
+            part = normal(add(part, {__shfl_xor_sync(0xffffffffu, part.hi, m), __shfl_xor_sync(0xffffffffu, part.lo, m)}));
         if (lane == 0) s_part[warp] = part;
         if (first_pass) cluster.barrier_wait(std::move(started));
         first_pass = false;
@@ -206,7 +208,7 @@ verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
 #pragma unroll
             for (int m = kWarps / 2; m; m >>= 1)
 #pragma unroll
-                for (int i = 0; i < m; ++i) c[i] = add(c[i], c[i + m]);
+                for (int i = 0; i < m; ++i) c[i] = normal(add(c[i], c[i + m]));
             cluster.map_shared_rank(s_totals, threadIdx.x)[rank] = value(c[0]);
         }
         if (ranks > 1) cluster.sync();
@@ -328,7 +330,7 @@ cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
     const bool batch = p.num_seqs > 76;
     const int warps = batch ? 4 : 8;
     int cluster = 1;
-    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster * 2 * warps <= 4864 && tiles > cluster * warps) cluster *= 2;
+    while (cluster < kVerifyCluster && (long long)p.num_seqs * cluster * 2 * warps <= kVerifyWave && tiles > cluster * warps) cluster *= 2;
     return batch ? launch_threads<128>(p, cluster, stream) : launch_threads<256>(p, cluster, stream);
 }
 

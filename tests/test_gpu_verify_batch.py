@@ -104,9 +104,10 @@ VALUES = ["0x1.2bb564p-44", "0x1.6be390p-28", "0x1.2a0f90p-34", "0x1.6fd12cp-29"
 
 @pytest.mark.parametrize("S,V", [(1, 2 ** 22), (609, 2 ** 18)])
 def test_sums_over_many_tiles(S, V):
-    """Every tile the same, 128 of them a warp; u = 1/16, and so much more in the last value that the goal
-    lies 2^-39.9 of itself above the border behind a sixteenth of the tiles: more than twice the 2^-41
-    to which goal and border are kept."""
+    """Every tile the same, 128 of them a warp, four a lane; u = 1/16, and so much more in the last value that
+    the goal lies 2^-39.9 of itself above the border behind a sixteenth of the tiles. The goal is kept to
+    (99 + 3 4 + 3 8) 2^-48 of itself (a tile's tree; four tiles; the trees over lanes and warps), the border
+    to 99 2^-48: 2^-40.1 in all."""
     values = [float.fromhex(x) for x in VALUES]
     tile, tiles = sum(Fraction(x) for x in values) * 32, V // 512
     last = torch.tensor(values[-1] + 1.0e-12 * float(tile * tiles), dtype=torch.float32).item()

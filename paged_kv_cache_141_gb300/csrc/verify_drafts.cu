@@ -38,8 +38,9 @@ namespace cg = cooperative_groups;
 constexpr int kVerifyTile = 512;
 constexpr int kVerifyPer = kVerifyTile / 32;       // of a tile, a lane's values
 constexpr int kVerifyCluster = 8;
-// Warps that run at once, 32 an SM.
-constexpr int kVerifyWave = 4864;
+// Warps that run at once: 32 an SM, and in clusters of eight CTAs 1184 of four warps or 592 of
+// eight (as the occupancy calculator says; four SMs' worth fit no whole cluster).
+constexpr int kVerifyWave = 4736;
 
 // Row weights: p alone, p beyond q, or p without one token.
 struct Weights {
@@ -323,8 +324,12 @@ cudaError_t launch_threads(const VerifyParams& p, int cluster, cudaStream_t stre
 
 }  // namespace
 
-// Few requests: as many warps as tiles, in clusters of up to eight CTAs. A batch: small CTAs
-// in one wave (some eight fit an SM), several to a request, so that the SMs' shares are even.
+// Few requests: as many warps as tiles, in clusters of up to eight CTAs. A batch: small CTAs,
+// several to a request, so that the SMs' shares are even. Clusters grow only as far as they all
+// run at once (75 requests of 128,256 tokens in clusters of eight, one of which waits: 34.5 us,
+// in clusters of four 27; 150: 44.6, 41.3). Small CTAs against large ones: 256 requests 50 us
+// and 59; 96 of them 36 and 31, 64 of them 23 and 28, 16 of them 14 and 15.5, so the border in
+// between is a rough one.
 cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
     const int tiles = (p.vocab + kVerifyTile - 1) / kVerifyTile;
     const bool batch = p.num_seqs > 76;

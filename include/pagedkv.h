@@ -668,7 +668,9 @@ pa_status pa_extend_tables(int32_t* block_tables, int max_blocks_per_seq,
  *                 go to the stack (a prefix that other requests hold too).
  *  A count outside [0, context_lens[s]] drops nothing (PA_DEV_BAD_LEN). If the stack
  *  cannot hold all blocks, nothing is dropped (PA_DEV_BAD_BLOCK_ID). The tables keep
- *  their entries. Other arguments as above.
+ *  their entries. Lengths and blocks alone move: what a dropped token has done to the
+ *  scale of a block that stays (see pa_scaled_append) is not undone. Other arguments as
+ *  above.
  */
 pa_status pa_trim_tables(const int32_t* block_tables, int max_blocks_per_seq,
                          const int32_t* context_lens, const int32_t* drop_tokens, int num_seqs,
@@ -700,7 +702,10 @@ pa_status pa_trim_tables(const int32_t* block_tables, int max_blocks_per_seq,
  *    codes  = x / scale' to nearest even, in [-127, 127] or as E4M3; older codes c
  *             become c (scale / scale') to nearest even where the scale has grown.
  *  A NaN or an infinity makes the block's scale NaN, and with it whatever is read
- *  through it, until the block starts anew. A sequence whose rows pass num_tokens or
+ *  through it, until the block starts anew. A token that is taken out again (a rejected
+ *  draft) leaves the scale as large as it made it, and the older codes rounded to that
+ *  (PA_INT8: a bit lost for each doubling; PA_FP8_E4M3: only what became subnormal), until
+ *  the block starts anew. A sequence whose rows pass num_tokens or
  *  max_new_tokens, or whose length its table does not hold, is skipped
  *  (PA_DEV_BAD_LEN). Two sequences that write to one block race.
  *  Blocks copied by pa_copy_blocks need their scales copied too.
@@ -734,7 +739,8 @@ pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* valu
  *                 has the largest of their byte counts, not that of the largest sizes.
  *  Codes past a context's end are not read. An E4M3 NaN code within it is read as
  *  +-480 (pa_scaled_append writes none but under a NaN scale).
- *  Scores, softmax statistics and sums are binary32. The query meets the codes exactly
+ *  Scores, softmax statistics and sums are binary32 (sums of codes under a key scale past
+ *  2^110 overflow). The query meets the codes exactly
  *  but for components more than 2^14 below a row's largest; a weight (softmax times
  *  value scale) meets them to within 2^-11 of itself (2^-22 where the output is F16) or
  *  2^-30 of the row's largest among the tokens that it sees.

@@ -123,8 +123,9 @@ ScaledPlan scaled_plan(int num_seqs, int num_queries, int num_q_heads, int num_k
     ScaledPlan l{};
     const int64_t rows = (int64_t)max_queries * (num_q_heads / num_kv_heads);
     // The tcgen05 kernel from where the warp-level tiles end: 64 contexts of 512-4096 tokens, 32/8
-    // heads of 128, 5 (8) tokens each, 20 (32) rows, take 107 (113) us on one tile of 32 rows and
-    // 119 (119) there; at head size 256, where a tile has 16 rows, 20 rows take 180 us and 97.
+    // heads of 128, 5 (8) tokens each, 20 (32) rows, take 103 (110) us on one tile of 32 rows and
+    // 118 (119) there; 64/8 heads of 128 and 5 tokens, 40 rows, 194 and 124; at head size 256, where
+    // a tile has 16 rows, 20 rows take 169 us and 91.
     const bool tc = rows > (head_size == 256 ? 16 : 32) && block_size % 8 == 0;
     l.tile_rows = tc ? (head_size == 256 ? 128 : 256) : (rows <= 8 ? 8 : (rows <= 16 || head_size == 256 ? 16 : 32));
     const int64_t tiles = (rows + l.tile_rows - 1) / l.tile_rows;

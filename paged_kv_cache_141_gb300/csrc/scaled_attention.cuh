@@ -17,7 +17,7 @@
 // 32/8 heads of 128: 96 us, 117 with CTAs of four warps for partitions of 1024-4096 tokens;
 // one of 131072: 53, 64. That is 6.0 and 5.0 TB/s; without the join 91 and 47 us, 0.93 and
 // 0.85 of what the bytes take at 6.78 TB/s. What is left is the last pieces' end, the join's
-// launch, and issue slots: 770 instructions a stage, 973 at first.)
+// launch, and issue slots: 758 instructions a stage, 973 at first.)
 // Per stage:
 //   S (16 tokens x 8 rows) = C_K Q^T on binary16 warp-level MMAs, the codes widened in
 //     registers, exactly: integers by the bits of 1024 + (c + 128), less 1152; E4M3 by

@@ -18,8 +18,8 @@
 // launch latency and two or three dependent loads; sums in a kernel of their own
 // would cost a launch more. A prompt step's slots are too many for one cluster's
 // eight SMs (some 130,000 of them took 23 us): from kSlotsApart on a second kernel
-// fills the whole device with them, from the first one's outputs (9.3 us). 4 requests of a
-// token each take 3.4 us, 512 of five 5.3, 512 trimmed 7.9 (each CTA sums all requests first).
+// fills the whole device with them, from the first one's outputs (9.4 us). 4 requests of a
+// token each take 3.4 us, 512 of five 5.4, 512 trimmed 8 (each CTA sums all requests first).
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"

@@ -327,8 +327,8 @@ cudaError_t launch_threads(const VerifyParams& p, int cluster, cudaStream_t stre
 // Few requests: as many warps as tiles, in clusters of up to eight CTAs. A batch: small CTAs,
 // several to a request, so that the SMs' shares are even. Clusters grow only as far as they all
 // run at once (75 requests of 128,256 tokens in clusters of eight, one of which waits: 34.5 us,
-// in clusters of four 27; 150: 44.6, 41.3). Small CTAs against large ones: 256 requests 50 us
-// and 59; 96 of them 36 and 31, 64 of them 23 and 28, 16 of them 14 and 15.5, so the border in
+// in clusters of four 27; 150: 44.6, 41.3). Small CTAs against large ones: 256 requests 51 us
+// and 52; 96 of them 34 and 31, 64 of them 23 and 28, 16 of them 14 and 15, so the border in
 // between is a rough one.
 cudaError_t launch_verify_drafts(const VerifyParams& p, cudaStream_t stream) {
     const int tiles = (p.vocab + kVerifyTile - 1) / kVerifyTile;

@@ -743,7 +743,8 @@ pa_status pa_scaled_append(const void* key, int64_t key_stride, const void* valu
  *  2^110 overflow). The query meets the codes exactly
  *  but for components more than 2^14 below a row's largest; a weight (softmax times
  *  value scale) meets them to within 2^-11 of itself (2^-22 where the output is F16) or
- *  2^-30 of the row's largest among the tokens that it sees.
+ *  2^-30 of the row's largest among the tokens that it sees (weights below 2^-120 may
+ *  count as none).
  *  Block sizes up to 1024, head sizes 64, 128 and 256, any group; num_blocks *
  *  num_kv_heads * block_size below 2^32.
  */
